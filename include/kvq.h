@@ -275,6 +275,73 @@ KVQ_API kv_status_t kv_decode_attn_groups(kv_pool_t* const* pools, int32_t n_poo
                                           const int32_t* req_ids, int32_t batch, int32_t num_q_heads,
                                           float softmax_scale, float* out, void* stream);
 
+/* Attention of several new tokens per request over the request's cache and
+ * over each other: drafts to be verified (in a line or as a tree) before the
+ * accepted ones are appended, and a further chunk of a prompt (HyQuant,
+ * Algorithm 3, with more than one query token; TriAxialKV key design 4, whose
+ * decode is the case of one).  New token t of a request, q head h:
+ *     out = sum_x p_x v_x / sum_x p_x,   p_x = exp(softmax_scale * q . k_x - max)
+ * over the live slots of the request's pages (evicted slots and slots excluded
+ * for the kv head have weight zero), its full-precision list, and those of its
+ * own new tokens j that t may see: j <= t, or bit j of tree[t].  A row that sees
+ * nothing is zero.
+ *   q        device, bf16 [N][num_q_heads][128], N = sum of n_new
+ *   k, v     device, bf16 [N][num_kv_heads][128], the new tokens' own rows (not
+ *            appended by this call); both NULL: the rows see the cache only.
+ *            Checked as in kv_append_quant: NaN, Inf or |x| > 65504 is used as 0
+ *            and makes kv_pool_sync() return KV_ERR_RANGE.
+ *   tree     device, uint64 [N], or NULL (causal); at most 64 new tokens of a
+ *            request with it.  Bits at or past the request's n_new are ignored.
+ *   req_ids  host, int32 [n_req]: open requests; the tokens of req_ids[b] follow
+ *            those of req_ids[b - 1].  A request may be listed twice.
+ *   n_new    host, int32 [n_req], each in [0, 2^20]
+ *   out      device, bf16 [N][num_q_heads][128]
+ * q, k, v and out need 2-byte alignment only.  num_q_heads as in
+ * kv_decode_attn; n_req x num_kv_heads <= 65535.  K, V and the softmax weights
+ * pass through binary16 (logits, sums and outputs are accumulated in fp32 and
+ * rounded to bf16 once); with KV_DECODE_SIMT everything is fp32.  The call
+ * plans on the host: on a stream that is being captured it is KV_ERR_STATE. */
+KVQ_API kv_status_t kv_attend(kv_pool_t* pool, const void* q, const void* k, const void* v, const uint64_t* tree,
+                              const int32_t* req_ids, const int32_t* n_new, int32_t n_req, int32_t num_q_heads,
+                              float softmax_scale, void* out, void* stream);
+
+/* kv_decode_attn that also accumulates attention weight per cached token, the
+ * ranking of eviction policies that keep heavy hitters.  For batch row b, kv
+ * head h and every slot of the request that is live for h, with p_jt the
+ * softmax weight of q head j for it:
+ *     scores[b][h][pos] = decay * scores[b][h][pos] + sum over h's q heads j of p_jt
+ * pos the token's position (appended tokens count from 0).  Other entries are
+ * left as they are; full-precision list tokens take part in the softmax and
+ * have no score.
+ *   scores   device, fp32 [batch][num_kv_heads][score_stride], read and written;
+ *            score_stride >= the positions of every request of the batch
+ *   decay    finite; 1 sums all steps
+ * The other arguments, out and the rules are kv_decode_attn's (a request may
+ * be listed twice: its rows of scores are separate); always the tensor-core
+ * scan, batch x num_kv_heads <= 65535.  A workspace of 128 bytes per q head and
+ * page grows with cudaMalloc; the first call also puts the slots' positions on
+ * the device (128 bytes per page of the pool).  On a stream that is being
+ * captured it is KV_ERR_STATE.  kv_decode_timing does not cover it. */
+KVQ_API kv_status_t kv_decode_attn_scored(kv_pool_t* pool, const void* q, const int32_t* req_ids, int32_t batch,
+                                          int32_t num_q_heads, float softmax_scale, float decay, float* scores,
+                                          int64_t score_stride, float* out, void* stream);
+
+/* The cached tokens of least score, to be evicted (kv_evict_slots,
+ * kv_evict_slots_head).  For each listed request (per_head: and kv head): among
+ * the positions in [0, positions - protect) whose slot is live (per_head: for
+ * that head; else for any head), the n_select[b] of least score (per_head: the
+ * head's own; else the kv heads' sum, taken in fp64 and rounded to fp32), ties
+ * to the lower position, -0 equal to +0, NaN last.
+ *   scores   device, fp32 [n_req][num_kv_heads][score_stride], as above
+ *   n_select host, int32 [n_req], each in [0, out_stride]
+ *   out      device, int32 [n_req][per_head ? num_kv_heads : 1][out_stride]:
+ *            the chosen positions in ascending order, then -1
+ * Fewer eligible positions than n_select: all of them.  At most 65535
+ * requests.  On a stream that is being captured it is KV_ERR_STATE. */
+KVQ_API kv_status_t kv_select_lowest(kv_pool_t* pool, const float* scores, int64_t score_stride, const int32_t* req_ids,
+                                     const int32_t* n_select, int32_t n_req, int64_t protect, int32_t per_head,
+                                     int32_t* out, int64_t out_stride, void* stream);
+
 /* Testing aid for the device-timeout path (off by default).  Every copy wait
  * in the scans is bounded; first_wait_spins >= 0 makes the first copy wait of
  * every warp of the tensor-core page scan and of the full-precision list scan

@@ -28,7 +28,7 @@ EXPORTED = ["kv_pool_create", "kv_pool_destroy", "kv_request_open", "kv_request_
             "kv_request_info", "kv_export_request", "kv_last_decode_stats", "kv_pool_launch_count", "kv_alloc_bits",
             "kv_last_error", "kv_decode_attn_noalloc", "kv_decode_timing", "kv_evict_slots_head", "kv_fp_configure",
             "kv_fp_append", "kv_fp_drop", "kv_fp_count", "kv_set_wait_limit", "kv_drop_dead_pages",
-            "kv_decode_attn_groups", "kv_alloc_bits3"]
+            "kv_decode_attn_groups", "kv_alloc_bits3", "kv_attend", "kv_decode_attn_scored", "kv_select_lowest"]
 
 _P = ctypes.c_void_p
 _I32, _I64 = ctypes.c_int32, ctypes.c_int64
@@ -75,6 +75,9 @@ def load_library(path: str = LIB_PATH):
             "kv_fp_count": [_P, _I32, _P],
             "kv_decode_attn": [_P, _P, _P, _I32, _I32, ctypes.c_float, _P, _P],
             "kv_decode_attn_noalloc": [_P, _P, _P, _I32, _I32, ctypes.c_float, _P, _P],
+            "kv_attend": [_P, _P, _P, _P, _P, _P, _P, _I32, _I32, ctypes.c_float, _P, _P],
+            "kv_decode_attn_scored": [_P, _P, _P, _I32, _I32, ctypes.c_float, ctypes.c_float, _P, _I64, _P, _P],
+            "kv_select_lowest": [_P, _P, _I64, _P, _P, _I32, _I64, _I32, _P, _I64, _P],
             "kv_set_decode_impl": [_P, _I32],
             "kv_set_wait_limit": [_P, _I64],
             "kv_pool_sync": [_P],
@@ -345,6 +348,116 @@ class KVPool:
                                                     ctypes.c_void_p(out.data_ptr()), _stream(stream, dev)),
                "kv_decode_attn_groups")
         return out
+
+    def attend(self, q, req_ids, n_new, softmax_scale, k=None, v=None, tree=None, out=None, stream=None):
+        """kv_attend: n_new[b] new tokens of each request attend to the request's cache and to
+        each other (causally, or as tree says).  q: torch bf16 CUDA [N][Hq][128], N = sum(n_new);
+        k, v: the new tokens' own rows, bf16 [N][Hkv][128] (None: the cache only); tree: int64
+        (or uint64) CUDA [N], bit j = may see new token j of its request -> out bf16 like q."""
+        torch = _torch_mod()
+        req_ids = _np(req_ids, np.int32)
+        n_new = _np(n_new, np.int32)
+        if req_ids.ndim != 1 or n_new.shape != req_ids.shape:
+            raise ValueError("req_ids and n_new must be sequences of one length")
+        n = int(n_new.sum(dtype=np.int64))
+        if q.dim() != 3 or q.shape[0] != n or q.shape[2] != HEAD_DIM or q.dtype is not torch.bfloat16 or \
+                not self._on_pool_device(q) or not q.is_contiguous():
+            raise ValueError("q must be a contiguous bf16 tensor [sum(n_new)][Hq][128] on the pool's device")
+        if (k is None) != (v is None):
+            raise ValueError("k and v come together")
+        if k is not None:
+            self._check_kv(k, n)
+            self._check_kv(v, n)
+        if tree is not None and (tree.dtype not in (torch.int64, torch.uint64) or tuple(tree.shape) != (n,) or
+                                 not self._on_pool_device(tree) or not tree.is_contiguous()):
+            raise ValueError("tree must be a contiguous int64 tensor [sum(n_new)] on the pool's device")
+        if out is None:
+            out = torch.empty_like(q)
+        elif out.dtype is not torch.bfloat16 or out.shape != q.shape or not self._on_pool_device(out) or \
+                not out.is_contiguous():
+            raise ValueError("out must be a contiguous bf16 tensor shaped like q on the pool's device")
+        rc = self._L.kv_attend(self._h, q.data_ptr(), k.data_ptr() if k is not None else None,
+                               v.data_ptr() if v is not None else None, tree.data_ptr() if tree is not None else None,
+                               req_ids.ctypes.data, n_new.ctypes.data, req_ids.size, q.shape[1], softmax_scale,
+                               out.data_ptr(), _stream(stream, self.device))
+        if rc:
+            _check(rc, "kv_attend")
+        return out
+
+    def _check_scores(self, scores, n):
+        torch = _torch_mod()
+        if scores.dtype is not torch.float32 or scores.dim() != 3 or \
+                tuple(scores.shape[:2]) != (n, self.num_kv_heads) or not self._on_pool_device(scores) or \
+                not scores.is_contiguous():
+            raise ValueError(f"scores must be a contiguous fp32 tensor [{n}][{self.num_kv_heads}][positions] on the "
+                             f"pool's device")
+
+    def decode_scored(self, q, req_ids, softmax_scale, scores, decay=1.0, out=None, stream=None):
+        """kv_decode_attn_scored: decode() that also adds every live slot's attention weight,
+        summed over its kv head's q heads, to decay * scores (fp32 CUDA [B][Hkv][positions],
+        indexed by token position; updated in place)."""
+        torch = _torch_mod()
+        req_ids = _np(req_ids, np.int32)
+        if q.dim() != 3 or q.dtype is not torch.bfloat16 or not self._on_pool_device(q) or \
+                q.shape[2] != HEAD_DIM or q.shape[0] != req_ids.size or not q.is_contiguous():
+            raise ValueError("q must be a contiguous bf16 tensor [B][Hq][128] on the pool's device with "
+                             "B == len(req_ids)")
+        self._check_scores(scores, req_ids.size)
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        elif out.dtype is not torch.float32 or out.shape != q.shape or not self._on_pool_device(out) or \
+                not out.is_contiguous():
+            raise ValueError("out must be a contiguous fp32 tensor shaped like q on the pool's device")
+        rc = self._L.kv_decode_attn_scored(self._h, q.data_ptr(), req_ids.ctypes.data, req_ids.size, q.shape[1],
+                                           softmax_scale, decay, scores.data_ptr(), scores.shape[2], out.data_ptr(),
+                                           _stream(stream, self.device))
+        if rc:
+            _check(rc, "kv_decode_attn_scored")
+        return out
+
+    def select_lowest(self, scores, req_ids, n_select, protect=0, per_head=False, out=None, stream=None):
+        """kv_select_lowest: per request (per_head: and kv head) the positions of the n_select[b]
+        live tokens of least score (all kv heads' sum, or the head's own) that are not among the
+        `protect` newest -> int32 CUDA [B][max(n_select)] (per_head: [B][Hkv][...]), ascending,
+        then -1.  n_select: an int or a host sequence [B]."""
+        torch = _torch_mod()
+        req_ids = _np(req_ids, np.int32)
+        n_select = np.full(req_ids.size, int(n_select), np.int32) if np.ndim(n_select) == 0 else _np(n_select, np.int32)
+        if req_ids.ndim != 1 or n_select.shape != req_ids.shape:
+            raise ValueError("req_ids and n_select must be sequences of one length")
+        self._check_scores(scores, req_ids.size)
+        if req_ids.size and int(n_select.min()) < 0:
+            raise ValueError("n_select must not be negative")
+        most = int(n_select.max()) if req_ids.size else 0
+        shape = (req_ids.size, self.num_kv_heads, most) if per_head else (req_ids.size, most)
+        if out is None:
+            out = torch.empty(shape, dtype=torch.int32, device=scores.device)
+        elif out.dtype is not torch.int32 or tuple(out.shape) != shape or not self._on_pool_device(out) or \
+                not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous int32 tensor {list(shape)} on the pool's device")
+        rc = self._L.kv_select_lowest(self._h, scores.data_ptr(), scores.shape[2], req_ids.ctypes.data,
+                                      n_select.ctypes.data, req_ids.size, int(protect), int(bool(per_head)),
+                                      out.data_ptr(), most, _stream(stream, self.device))
+        if rc:
+            _check(rc, "kv_select_lowest")
+        return out
+
+    def evict_lowest(self, scores, req_ids, n_select, protect=0, per_head=False, stream=None):
+        """select_lowest(), then evict() the chosen positions (per_head: evict_head(), each head
+        its own).  Returns the positions on the host, shaped as select_lowest() gives them."""
+        torch = _torch_mod()
+        req_ids = _np(req_ids, np.int32)
+        if np.unique(req_ids).size != req_ids.size:
+            raise ValueError("a request is listed twice")
+        pos = self.select_lowest(scores, req_ids, n_select, protect, per_head, stream=stream)
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
+            pos = pos.cpu().numpy()
+        at = np.nonzero(pos >= 0)
+        if per_head:
+            self.evict_head(req_ids[at[0]], pos[at], at[1], stream=stream)
+        else:
+            self.evict(req_ids[at[0]], pos[at], stream=stream)
+        return pos
 
     def set_wait_limit(self, first_wait_spins):
         """kv_set_wait_limit: bound of the scans' first copy wait (testing the timeout

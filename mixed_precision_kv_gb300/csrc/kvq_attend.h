@@ -1,0 +1,65 @@
+// Attention of new tokens over the cache (kv_attend): what its host side hands
+// to its kernels.
+#pragma once
+#include "kvq_internal.h"
+
+namespace kvq {
+
+constexpr int kMaxNewTokens = 1 << 20;   // new tokens of one request in a call
+
+// One (request of the call, kv head): T new tokens of g q heads each.  Row i
+// of a unit is (new token i / g, q head kvh * g + i % g).
+struct AttUnit {
+  int32_t req, kvh;
+  int32_t T;          // new tokens
+  int32_t n_pages;    // table entries
+  int32_t n_fp;       // full-precision list tokens
+  int32_t pad;
+  int64_t tok0;       // the request's first row in q, k, v and out
+};
+
+// Everything a kernel needs besides its plan.
+struct AttArgs {
+  const uint8_t* pool;
+  size_t int4_off, int3_off, fp4_off;
+  int64_t n2, n3b, nfb;          // first INT4, INT3 and FP4 page id
+  const Entry* table;
+  const uint32_t* hdead;         // null: no slot is excluded for a kv head
+  const uint16_t *fpk, *fpv;     // full-precision lists [request][kv head][fp_cap][128], see att_list_at
+  const uint16_t *q, *k, *v;     // new tokens, bf16; k and v null: the rows see the cache only
+  const uint64_t* tree;          // null: causal
+  uint16_t* out;                 // bf16
+  uint32_t* status;
+  float scale_log2;
+  int32_t max_pages, hkv, hq, fp_cap;
+};
+
+// A page's width class and block address.
+enum : int { kClsInt2 = 0, kClsInt4 = 1, kClsInt3 = 2, kClsFp4 = 3 };
+#ifdef __CUDACC__
+__device__ __forceinline__ int att_page(const AttArgs& A, int32_t id, int32_t kvh, const uint8_t*& blk) {
+  if (id < A.n2) {
+    blk = A.pool + ((size_t)id * A.hkv + kvh) * kInt2Block;
+    return kClsInt2;
+  }
+  if (id < A.n3b) {
+    blk = A.pool + A.int4_off + ((size_t)(id - A.n2) * A.hkv + kvh) * kInt4Block;
+    return kClsInt4;
+  }
+  if (id < A.nfb) {
+    blk = A.pool + A.int3_off + ((size_t)(id - A.n3b) * A.hkv + kvh) * kInt3Block;
+    return kClsInt3;
+  }
+  blk = A.pool + A.fp4_off + ((size_t)(id - A.nfb) * A.hkv + kvh) * kFp4Block;
+  return kClsFp4;
+}
+// Offset of channel c in list row t: the 8-channel pieces of a row are stored
+// in the order piece ^ (t & 7).
+__device__ __forceinline__ int att_list_at(int t, int c) { return (((c >> 3) ^ (t & 7)) << 3) | (c & 7); }
+#endif
+
+// CUDA-core kernel (kvq_attend_simt.cu): every unit's rows in blocks of 32.
+cudaError_t launch_attend_simt(kv_pool* P, const AttArgs& A, const AttUnit* d_units, int n_units, int max_rows,
+                               cudaStream_t s);
+
+}  // namespace kvq

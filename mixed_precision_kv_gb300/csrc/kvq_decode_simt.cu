@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(
 // dependent load rounds at two.
 template <int G>
 __global__ void __launch_bounds__(256) merge_kernel(const Unit* __restrict__ units, const float* __restrict__ part,
-                                                    int hq, float* __restrict__ out) {
+                                                    int hq, float* __restrict__ out, float2* __restrict__ ml) {
   constexpr int kW = 8;
   __shared__ float mpart[kW], lpart[kW];
   __shared__ float4 apart[kW][32];
@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const Unit* __restrict__ uni
       Lt = fmaf(lpart[k], g, Lt);
     }
     const float inv = Lt > 0.0f ? 1.0f / Lt : 0.0f;
+    if (ml && lane == 0) ml[blockIdx.x] = make_float2(M, inv);   // base-2 maximum and 1 / sum of the row
     float* o = out + ((size_t)u.b * hq + (size_t)u.kvh * G + h) * kHeadDim + 4 * lane;
     *reinterpret_cast<float4*>(o) = make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv);
   }
@@ -342,7 +343,7 @@ cudaError_t launch_g(kv_pool* P, const void* q, int32_t hq, float scale_log2, co
 }  // namespace
 
 cudaError_t launch_merge(kv_pool* P, int g, const Unit* d_units, int n_units, const float* d_part, int hq, float* out,
-                         cudaStream_t s) {
+                         cudaStream_t s, float2* ml) {
   ++P->launches;
   // Programmatic dependent launch: the merge grid is set up while the scan
   // grid drains; its griddepcontrol.wait orders it after the scan's results.
@@ -357,14 +358,14 @@ cudaError_t launch_merge(kv_pool* P, int g, const Unit* d_units, int n_units, co
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   switch (g) {
-    case 1: return cudaLaunchKernelEx(&cfg, merge_kernel<1>, d_units, d_part, hq, out);
-    case 2: return cudaLaunchKernelEx(&cfg, merge_kernel<2>, d_units, d_part, hq, out);
-    case 3: return cudaLaunchKernelEx(&cfg, merge_kernel<3>, d_units, d_part, hq, out);
-    case 4: return cudaLaunchKernelEx(&cfg, merge_kernel<4>, d_units, d_part, hq, out);
-    case 5: return cudaLaunchKernelEx(&cfg, merge_kernel<5>, d_units, d_part, hq, out);
-    case 6: return cudaLaunchKernelEx(&cfg, merge_kernel<6>, d_units, d_part, hq, out);
-    case 7: return cudaLaunchKernelEx(&cfg, merge_kernel<7>, d_units, d_part, hq, out);
-    case 8: return cudaLaunchKernelEx(&cfg, merge_kernel<8>, d_units, d_part, hq, out);
+    case 1: return cudaLaunchKernelEx(&cfg, merge_kernel<1>, d_units, d_part, hq, out, ml);
+    case 2: return cudaLaunchKernelEx(&cfg, merge_kernel<2>, d_units, d_part, hq, out, ml);
+    case 3: return cudaLaunchKernelEx(&cfg, merge_kernel<3>, d_units, d_part, hq, out, ml);
+    case 4: return cudaLaunchKernelEx(&cfg, merge_kernel<4>, d_units, d_part, hq, out, ml);
+    case 5: return cudaLaunchKernelEx(&cfg, merge_kernel<5>, d_units, d_part, hq, out, ml);
+    case 6: return cudaLaunchKernelEx(&cfg, merge_kernel<6>, d_units, d_part, hq, out, ml);
+    case 7: return cudaLaunchKernelEx(&cfg, merge_kernel<7>, d_units, d_part, hq, out, ml);
+    case 8: return cudaLaunchKernelEx(&cfg, merge_kernel<8>, d_units, d_part, hq, out, ml);
     default: return cudaErrorInvalidValue;
   }
 }

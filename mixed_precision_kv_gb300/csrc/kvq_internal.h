@@ -76,7 +76,7 @@ struct Unit {
   int32_t n_splits;     // number of splits (0 = no tokens)
   int32_t fp_begin;     // first full-precision split of this unit
   int32_t n_fp_splits;  // number of full-precision splits
-  int32_t pad;
+  int32_t pad;          // grouped decode: the pool; else the unit's first row of logits (scored decode)
 };
 
 // Full-precision splits: a Split whose page_begin / page_end are token
@@ -97,7 +97,7 @@ struct Split {
   int32_t req;          // request id of the unit
   int32_t n_pos;        // the unit's table length when planned
   int32_t n_lead;       // leading table entries spread evenly through the scan order (0: table order)
-  int32_t pad[2];
+  int32_t pad[2];       // [0]: the unit's first row of logits (scored decode); both: see GroupPool (grouped decode)
 };
 
 // One pool of a grouped decode (kv_decode_attn_groups): its splits carry the
@@ -307,6 +307,13 @@ struct kv_pool {
   kvq::DevBuf plan;                   // decode plan (units, splits)
   kvq::DevBuf partials;               // decode split partials
   kvq::DevBuf frags;                  // per-unit q operands of the tensor-core scan
+  kvq::DevBuf logits;                 // scored decode: logits of the batch's pages, then each row's (maximum, 1 / sum)
+  kvq::DevBuf select;                 // lowest-score selection: lengths, eligibility bits, keys, counts
+  kvq::DevBuf attend;                 // attention of new tokens: plan, then partials
+  // token position of every slot, on the device ([page id][32]; allocated by
+  // the first call that needs it, then refreshed for the pages in pos_dirty)
+  int32_t* d_pos = nullptr;
+  std::vector<int32_t> pos_dirty;
   // per-head exclusion (allocated by the first kv_evict_slots_head): per page
   // id x kv head, the slots that read as dead for that head only
   uint32_t* d_hdead = nullptr;
@@ -341,6 +348,7 @@ struct kv_pool {
   kvq::FpLaunch fp_pending;           // launched by the next launch_decode_* between scan and merge
   int32_t n_fpw = 0;
   size_t plan_units_off = 0, plan_splits_off = 0, plan_cta_off = 0;
+  int64_t plan_rows = 0;              // rows of logits that the plan's units reserve (table lengths and their slack)
   int32_t n_ctas = 0;
   std::vector<int32_t> stat_req;      // request ids of the last decode (for kv_last_decode_stats)
   int32_t stat_hq = 0;
@@ -357,6 +365,7 @@ struct kv_pool {
   size_t gplan_units_off = 0, gplan_splits_off = 0, gplan_wsplit_off = 0, gplan_pools_off = 0;
   int32_t decode_impl = KV_DECODE_AUTO;
   cudaStream_t last_stream = nullptr;
+  bool used = false;                  // some work was put on last_stream
   int64_t launches = 0;               // kernels launched by this pool
   bool timing = false;                // record events around the decode kernels
   int32_t timing_every = 1;           // record every timing_every-th decode call
@@ -457,8 +466,15 @@ cudaError_t launch_decode_mma(kv_pool* P, const void* q, int32_t hq, float scale
 int decode_mma_workers_per_sm(int g);
 constexpr int kMmaWarpsPerCta = 16;
 size_t decode_mma_frag_bytes();
+// The same scan, keeping every page's logits (base 2): logits[row][head][slot], row = Split::pad[0] + table
+// index; ml (device, [units][g]): each row's maximum and 1 / sum (kvq_decode_score.cu).
+cudaError_t launch_decode_mma_scored(kv_pool* P, const void* q, int32_t hq, float scale_log2, const Unit* d_units,
+                                     int n_units, const Split* d_splits, const int32_t* d_wsplit, int n_workers,
+                                     void* d_frags, float* d_part, float* out, float* logits, float2* ml,
+                                     cudaStream_t s);
 // Split merge: out[b][h][:] = sum_s acc_s 2^(m_s - M) / sum_s l_s 2^(m_s - M) over the unit's splits.
+// ml (may be null): device float2 [units][g], (M, 1 / sum_s l_s 2^(m_s - M)), the second 0 for an empty row.
 cudaError_t launch_merge(kv_pool* P, int g, const Unit* d_units, int n_units, const float* d_part, int hq, float* out,
-                         cudaStream_t s);
+                         cudaStream_t s, float2* ml = nullptr);
 
 }  // namespace kvq

@@ -17,6 +17,7 @@
 #include <utility>
 #include <vector>
 
+#include "kvq_host.h"
 #include "kvq_internal.h"
 
 using namespace kvq;
@@ -24,40 +25,6 @@ using namespace kvq;
 namespace {
 
 thread_local std::string g_err;
-
-kv_status_t fail(kv_status_t st, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_err = buf;
-  return st;
-}
-
-#define KV_CUDA(call)                                                                       \
-  do {                                                                                      \
-    cudaError_t e_ = (call);                                                                \
-    if (e_ != cudaSuccess) return fail(KV_ERR_CUDA, "%s: %s", #call, cudaGetErrorString(e_)); \
-  } while (0)
-
-// Makes the pool's device current for the duration of a call.
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    if (prev != dev) ok = cudaSetDevice(dev) == cudaSuccess;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-  }
-};
-
-bool req_ok(const kv_pool* P, int32_t r) {
-  return r >= 0 && r < P->cfg.max_requests && P->reqs[r].open;
-}
 
 bool is_int2(const kv_pool* P, int32_t id) { return id < P->cfg.n_int2_pages; }
 // INT3 ids follow the INT2 and INT4 ids, FP4 ids the INT3 ids
@@ -105,80 +72,6 @@ void hdead_final(const kv_pool* P, std::vector<TableUpd>& hu) {
 }
 
 
-// Grow a device buffer to at least `bytes` (contents are not kept).
-kv_status_t ensure(DevBuf& b, size_t bytes) {
-  if (b.cap >= bytes) return KV_OK;
-  size_t cap = std::max<size_t>(bytes, b.cap * 2);
-  cap = (cap + 255) & ~size_t(255);
-  if (b.ptr) {
-    KV_CUDA(cudaDeviceSynchronize());
-    KV_CUDA(cudaFree(b.ptr));
-    b.ptr = nullptr;
-    b.cap = 0;
-  }
-  KV_CUDA(cudaMalloc(&b.ptr, cap));
-  b.cap = cap;
-  return KV_OK;
-}
-
-// Several host arrays laid out for one upload (one H2D copy per call); the
-// arrays are copied straight into the pinned staging buffer by h2d (they must
-// stay alive until then).
-struct Upload {
-  struct Piece {
-    const void* p;
-    size_t n, off;
-  };
-  static constexpr int kMaxPieces = 8;
-  Piece pieces[kMaxPieces];
-  int n_pieces = 0;
-  size_t size = 0;
-  size_t add(const void* p, size_t n) {   // byte offset of the array in the upload
-    const size_t off = (size + 255) & ~size_t(255);
-    pieces[n_pieces++] = Piece{p, n, off};
-    size = off + n;
-    return off;
-  }
-};
-
-// Host-to-device copy through a pinned staging slot.  A copy from pageable
-// memory first waits for the stream to drain, which would stall the queue of
-// calls the host keeps ahead of the GPU; from pinned memory it is queued like
-// a kernel.  A slot is reused after its previous copy has run (normally long
-// before: the ring has kPinnedSlots slots).
-kv_status_t h2d(kv_pool* P, void* dst, const Upload& u, cudaStream_t s) {
-  const size_t n = u.size;
-  if (n == 0) return KV_OK;
-  kv_pool::PinnedSlot& sl = P->pinned[P->pinned_next];
-  P->pinned_next = (P->pinned_next + 1) % kv_pool::kPinnedSlots;
-  if (sl.pending) {
-    KV_CUDA(cudaEventSynchronize(sl.ev));
-    sl.pending = false;
-  }
-  if (sl.cap < n) {
-    if (sl.ptr) KV_CUDA(cudaFreeHost(sl.ptr));
-    sl.ptr = nullptr;
-    sl.cap = 0;
-    const size_t cap = std::max(n + n / 2, size_t(1) << 16);
-    KV_CUDA(cudaMallocHost(&sl.ptr, cap));
-    sl.cap = cap;
-  }
-  if (!sl.ev) KV_CUDA(cudaEventCreateWithFlags(&sl.ev, cudaEventDisableTiming));
-  for (int i = 0; i < u.n_pieces; ++i)
-    if (u.pieces[i].n) std::memcpy((uint8_t*)sl.ptr + u.pieces[i].off, u.pieces[i].p, u.pieces[i].n);
-  KV_CUDA(cudaMemcpyAsync(dst, sl.ptr, n, cudaMemcpyHostToDevice, s));
-  KV_CUDA(cudaEventRecord(sl.ev, s));
-  sl.pending = true;
-  return KV_OK;
-}
-
-kv_status_t upload(kv_pool* P, const Upload& u, cudaStream_t s) {
-  if (u.size == 0) return KV_OK;
-  kv_status_t st = ensure(P->upload, u.size);
-  if (st != KV_OK) return st;
-  return h2d(P, P->upload.ptr, u, s);
-}
-
 // Device table rows to rewrite after a call: per request, every entry from
 // `from` to the end plus individually listed entries below it.
 struct Dirty {
@@ -213,9 +106,77 @@ void emit_updates(const kv_pool* P, const Dirty& d, std::vector<TableUpd>& out) 
   }
 }
 
+}  // namespace
+
+void kvq::set_last_error(const char* msg) { g_err = msg; }
+
+kv_status_t kvq::fail(kv_status_t st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  g_err = buf;
+  return st;
+}
+
+// Grow a device buffer to at least `bytes` (contents are not kept).
+kv_status_t kvq::ensure(DevBuf& b, size_t bytes) {
+  if (b.cap >= bytes) return KV_OK;
+  size_t cap = std::max<size_t>(bytes, b.cap * 2);
+  cap = (cap + 255) & ~size_t(255);
+  if (b.ptr) {
+    KV_CUDA(cudaDeviceSynchronize());
+    KV_CUDA(cudaFree(b.ptr));
+    b.ptr = nullptr;
+    b.cap = 0;
+  }
+  KV_CUDA(cudaMalloc(&b.ptr, cap));
+  b.cap = cap;
+  return KV_OK;
+}
+
+// Host-to-device copy through a pinned staging slot.  A copy from pageable
+// memory first waits for the stream to drain, which would stall the queue of
+// calls the host keeps ahead of the GPU; from pinned memory it is queued like
+// a kernel.  A slot is reused after its previous copy has run (normally long
+// before: the ring has kPinnedSlots slots).
+kv_status_t kvq::h2d(kv_pool* P, void* dst, const Upload& u, cudaStream_t s) {
+  const size_t n = u.size;
+  if (n == 0) return KV_OK;
+  kv_pool::PinnedSlot& sl = P->pinned[P->pinned_next];
+  P->pinned_next = (P->pinned_next + 1) % kv_pool::kPinnedSlots;
+  if (sl.pending) {
+    KV_CUDA(cudaEventSynchronize(sl.ev));
+    sl.pending = false;
+  }
+  if (sl.cap < n) {
+    if (sl.ptr) KV_CUDA(cudaFreeHost(sl.ptr));
+    sl.ptr = nullptr;
+    sl.cap = 0;
+    const size_t cap = std::max(n + n / 2, size_t(1) << 16);
+    KV_CUDA(cudaMallocHost(&sl.ptr, cap));
+    sl.cap = cap;
+  }
+  if (!sl.ev) KV_CUDA(cudaEventCreateWithFlags(&sl.ev, cudaEventDisableTiming));
+  for (int i = 0; i < u.n_pieces; ++i)
+    if (u.pieces[i].n) std::memcpy((uint8_t*)sl.ptr + u.pieces[i].off, u.pieces[i].p, u.pieces[i].n);
+  KV_CUDA(cudaMemcpyAsync(dst, sl.ptr, n, cudaMemcpyHostToDevice, s));
+  KV_CUDA(cudaEventRecord(sl.ev, s));
+  sl.pending = true;
+  return KV_OK;
+}
+
+kv_status_t kvq::upload(kv_pool* P, const Upload& u, cudaStream_t s) {
+  if (u.size == 0) return KV_OK;
+  kv_status_t st = ensure(P->upload, u.size);
+  if (st != KV_OK) return st;
+  return h2d(P, P->upload.ptr, u, s);
+}
+
 // Order this call after the pool's previous work when the stream changes.
-kv_status_t order_after_previous(kv_pool* P, cudaStream_t s) {
-  if (P->last_stream != s && P->last_stream != nullptr) {
+kv_status_t kvq::order_after_previous(kv_pool* P, cudaStream_t s) {
+  if (P->last_stream != s && P->used) {
     cudaEvent_t ev;
     KV_CUDA(cudaEventCreateWithFlags(&ev, cudaEventDisableTiming));
     KV_CUDA(cudaEventRecord(ev, P->last_stream));
@@ -223,12 +184,10 @@ kv_status_t order_after_previous(kv_pool* P, cudaStream_t s) {
     KV_CUDA(cudaEventDestroy(ev));
   }
   P->last_stream = s;
+  P->used = true;
   return KV_OK;
 }
 
-}  // namespace
-
-void kvq::set_last_error(const char* msg) { g_err = msg; }
 
 void kvq::plan_decode(const kv_pool* P, const int32_t* req_ids, int32_t batch, int64_t n_ctas, int64_t min_pages,
                        PageCost pc, bool spread, HostPlan& out) {
@@ -531,6 +490,10 @@ kv_status_t kv_pool_destroy(kv_pool_t* P) {
   cudaFree(P->d_fpv);
   cudaFree(P->d_nfp);
   cudaFree(P->fp_scratch.ptr);
+  cudaFree(P->logits.ptr);
+  cudaFree(P->select.ptr);
+  cudaFree(P->attend.ptr);
+  cudaFree(P->d_pos);
   for (cudaEvent_t e : P->tev)
     if (e) cudaEventDestroy(e);
   for (auto& sl : P->pinned) {
@@ -1047,6 +1010,11 @@ kv_status_t kv_append_quant(kv_pool_t* P, const void* k, const void* v, const in
   }
   }   // per-token path
   const int64_t off = bulk ? bulk_job_toks : (int64_t)toks.size();
+  if (P->d_pos) {   // the pages whose slots got other positions
+    for (const auto& j : jobs) P->pos_dirty.push_back(j.page);
+    for (const auto& j : repacks) P->pos_dirty.push_back(j.dst);
+    for (const auto& j : directs) P->pos_dirty.push_back(j.dst);
+  }
   for (int32_t id : deferred) {
     P->fill[id] = 0;
     P->live[id] = 0;
@@ -1561,8 +1529,6 @@ kv_status_t kv_export_request(kv_pool_t* P, int32_t r, int32_t* ids, uint8_t* is
 
 }  // extern "C"
 
-namespace {
-
 // Split planner (Tangram, ahead-of-time load balancing: the CTA count comes
 // from the occupancy API and work is partitioned before the launch).  All
 // (batch row, kv head) units' pages, in order, are cut into n_ctas contiguous
@@ -1570,7 +1536,7 @@ namespace {
 // split per unit.  A page costs what the chosen scan kernel spends on a page
 // of its precision (PageCost), so INT2 and INT4 pages are weighed fairly.
 
-kv_status_t build_plan(kv_pool* P, const int32_t* req_ids, int32_t batch, int32_t hq, int32_t impl,
+kv_status_t kvq::build_plan(kv_pool* P, const int32_t* req_ids, int32_t batch, int32_t hq, int32_t impl,
                        cudaStream_t s) {
   const int hkv = P->cfg.num_kv_heads, g = hq / hkv;
   // A plan stays valid while the batch is the same and no table has shrunk:
@@ -1598,6 +1564,17 @@ kv_status_t build_plan(kv_pool* P, const int32_t* req_ids, int32_t batch, int32_
   HostPlan hp;
   plan_decode(P, req_ids, batch, (int64_t)P->sm_count * per_sm, mma ? kMinPagesPerWarp : kMinPagesPerCta,
               mma ? mma_page_cost(g) : kSimtPageCost, mma, hp);
+  int64_t total_pages = 0;
+  for (int32_t b = 0; b < batch; ++b) total_pages += (int64_t)P->reqs[req_ids[b]].table.size() * hkv;
+  // growth a tail worker absorbs before the plan is rebuilt: 5% of a worker's share
+  P->plan_slack = (int32_t)std::max<int64_t>(1, total_pages / std::max<int64_t>(1, hp.n_ctas()) / 20);
+  // rows of logits (scored decode): each unit reserves its table and the growth the plan allows
+  P->plan_rows = 0;
+  for (Unit& u : hp.units) {
+    u.pad = (int32_t)P->plan_rows;
+    P->plan_rows += (int64_t)P->reqs[u.req].table.size() + P->plan_slack;
+  }
+  for (int32_t x = 0; x < hp.n_page_splits; ++x) hp.splits[(size_t)x].pad[0] = hp.units[(size_t)hp.splits[(size_t)x].unit].pad;
   Upload up;
   const size_t ou = up.add(hp.units.data(), hp.units.size() * sizeof(Unit));
   const size_t os = up.add(hp.splits.data(), hp.splits.size() * sizeof(Split));
@@ -1621,19 +1598,11 @@ kv_status_t build_plan(kv_pool* P, const int32_t* req_ids, int32_t batch, int32_
   P->plan_ver.resize(batch);
   for (int32_t b = 0; b < batch; ++b) P->plan_ver[b] = P->reqs[req_ids[b]].shape;
   for (int32_t b = 0; b < batch; ++b) P->plan_nfp[b] = P->n_fp.empty() ? 0 : P->n_fp[req_ids[b]];
-  int64_t total_pages = 0;
-  for (int32_t b = 0; b < batch; ++b) {
-    P->plan_len[b] = (int32_t)P->reqs[req_ids[b]].table.size();
-    total_pages += (int64_t)P->plan_len[b] * hkv;
-  }
-  // growth a tail worker absorbs before the plan is rebuilt: 5% of a worker's share
-  P->plan_slack = (int32_t)std::max<int64_t>(1, total_pages / std::max<int64_t>(1, P->n_ctas) / 20);
+  for (int32_t b = 0; b < batch; ++b) P->plan_len[b] = (int32_t)P->reqs[req_ids[b]].table.size();
   P->plan_hq = hq;
   P->plan_impl = impl;
   return KV_OK;
 }
-
-}  // namespace
 
 extern "C" {
 
