@@ -1,5 +1,6 @@
 // Host side of kv_attend: checks, the units of the call and the choice of the
 // kernel.
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -9,6 +10,152 @@
 
 #include "kvq_attend.h"
 #include "kvq_host.h"
+
+namespace kvq {
+namespace {
+
+// ---- merge of partials -----------------------------------------------------
+// out = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M); a CTA of four warps per
+// row (warp w takes parts w, w + 4, ...; a lane four channels).  Bound by the
+// partials' bytes, which are still in L2.
+__global__ void __launch_bounds__(128) attend_merge_kernel(AttArgs A, const AttUnit* __restrict__ units,
+                                                           const AttMerge* __restrict__ merges,
+                                                           const float* __restrict__ part, int part_rows) {
+  __shared__ float4 acc[4][32];
+  __shared__ float2 ml[4];
+  const AttMerge D = merges[blockIdx.y];
+  const int i = blockIdx.x;
+  if (i >= D.rows) return;
+  const AttUnit u = units[D.unit];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int p = w; p < D.n_parts; p += 4) {
+    const float* pp = part + ((size_t)(D.part0 + p * D.stride) * part_rows + i) * kAttPart;
+    const float2 x = *reinterpret_cast<const float2*>(pp + kHeadDim);
+    const float4 a = *reinterpret_cast<const float4*>(pp + 4 * lane);
+    if (x.x == -INFINITY && x.y == 0.0f) continue;   // nothing seen in this part
+    const float mn = fmaxf(m, x.x);
+    const float c = m == -INFINITY ? 0.0f : exp2f(m - mn), f = x.x == -INFINITY ? 1.0f : exp2f(x.x - mn);
+    o.x = fmaf(o.x, c, a.x * f); o.y = fmaf(o.y, c, a.y * f); o.z = fmaf(o.z, c, a.z * f); o.w = fmaf(o.w, c, a.w * f);
+    l = fmaf(l, c, x.y * f);
+    m = mn;
+  }
+  acc[w][lane] = o;
+  if (lane == 0) ml[w] = make_float2(m, l);
+  __syncthreads();
+  if (w) return;
+  const float M = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+  float L = 0.0f;
+  o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float f = ml[k].x == -INFINITY ? (ml[k].y == 0.0f ? 0.0f : 1.0f) : exp2f(ml[k].x - M);
+    const float4 a = acc[k][lane];
+    o.x = fmaf(a.x, f, o.x); o.y = fmaf(a.y, f, o.y); o.z = fmaf(a.z, f, o.z); o.w = fmaf(a.w, f, o.w);
+    L = fmaf(ml[k].y, f, L);
+  }
+  const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
+  const float r[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+  bool bad = false;
+  const int g = A.hq / A.hkv, row = D.row0 + i;
+  uint16_t* op = A.out + ((size_t)(u.tok0 + row / g) * A.hq + (size_t)u.kvh * g + row % g) * kHeadDim + 4 * lane;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (!(fabsf(r[k]) < INFINITY)) bad = true;
+    op[k] = __bfloat16_as_ushort(__float2bfloat16_rn(r[k]));
+  }
+  if (bad) atomicOr(A.status, kStatusRange);
+}
+
+cudaError_t launch_attend_merge(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const AttMerge* d_merges,
+                                int n_merges, int max_rows, const float* d_part, int part_rows, cudaStream_t s) {
+  for (int a = 0; a < n_merges; a += 65535) {
+    ++P->launches;
+    attend_merge_kernel<<<dim3((unsigned)max_rows, (unsigned)std::min(65535, n_merges - a)), 128, 0, s>>>(
+        A, d_units, d_merges + a, d_part, part_rows);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+// ---- work plan ---------------------------------------------------------
+struct AttPlan {
+  std::vector<AttItem> items;
+  std::vector<int32_t> cta_item{0};
+  std::vector<AttMerge> merges;
+  int64_t n_parts = 0;
+  int merge_rows = 0;
+};
+
+// Key tiles of the block of rows [row0, row0 + rows) of a unit.
+int block_tiles(const AttUnit& u, int g, int row0, int rows, bool kv, bool tree) {
+  const int t_last = (row0 + rows - 1) / g;
+  return (u.n_pages + 3) / 4 + (u.n_fp + 127) / 128 + (kv ? (tree ? u.T - 1 : t_last) / 128 + 1 : 0);
+}
+
+// Blocks of kWideRows rows, their tiles in one line of cost, cut into equal
+// runs, one per CTA (a run may end inside a block: its pieces are merged).  A
+// tile of a block of more than 128 rows costs 2, else 1 (the MMAs' time); an
+// item 1 more for its first and last steps.
+constexpr int kWideRows = 256;
+void plan_wide(const std::vector<AttUnit>& units, int g, bool kv, bool tree, int ctas, AttPlan& out) {
+  struct Block {
+    int unit, row0, rows, tiles, cost;
+  };
+  std::vector<Block> blocks;
+  int64_t total = 0;
+  for (int x = 0; x < (int)units.size(); ++x) {
+    const int rows = units[(size_t)x].T * g;
+    for (int r = 0; r < rows; r += kWideRows) {
+      const int n = std::min(kWideRows, rows - r);
+      const Block b{x, r, n, block_tiles(units[(size_t)x], g, r, n, kv, tree), n > 128 ? 2 : 1};
+      blocks.push_back(b);
+      total += (int64_t)b.tiles * b.cost + 1;
+    }
+  }
+  const double share = (double)total / ctas;
+  double done = 0.0;
+  int cta = 0;
+  for (const Block& b : blocks) {
+    const size_t first = out.items.size();
+    int t = 0;
+    do {
+      int take = b.tiles - t;
+      if (cta < ctas - 1) {
+        const double room = (cta + 1) * share - done;
+        const int fit = (int)((room - 0.5) / b.cost + 0.5);
+        if (fit < std::min(2, take)) {   // nothing worth starting fits: the next CTA
+          out.cta_item.push_back((int32_t)out.items.size());
+          ++cta;
+          continue;
+        }
+        if (fit + 1 < take) take = fit;
+      }
+      out.items.push_back(AttItem{b.unit, b.row0, t, t + take, -1, {0, 0, 0}});
+      done += (double)take * b.cost + 1.0;
+      t += take;
+      if (t >= b.tiles) break;
+    } while (true);
+    const int n = (int)(out.items.size() - first);
+    if (n == 1 && b.rows > 128) continue;
+    const int32_t p0 = (int32_t)out.n_parts;
+    for (int y = 0; y < n; ++y) out.items[first + (size_t)y].part = p0 + 2 * y;
+    out.n_parts += 2 * n;
+    if (b.rows > 128) {
+      out.merges.push_back(AttMerge{b.unit, b.row0, 128, p0, n, 2});
+      out.merges.push_back(AttMerge{b.unit, b.row0 + 128, b.rows - 128, p0 + 1, n, 2});
+    } else {
+      out.merges.push_back(AttMerge{b.unit, b.row0, b.rows, p0, 2 * n, 1});
+    }
+    out.merge_rows = std::max(out.merge_rows, std::min(128, b.rows));
+  }
+  out.cta_item.push_back((int32_t)out.items.size());
+}
+
+}  // namespace
+}  // namespace kvq
 
 using namespace kvq;
 
@@ -77,11 +224,30 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
         units.push_back(AttUnit{r, h, n_new[b], (int32_t)P->reqs[r].table.size(), P->n_fp.empty() ? 0 : P->n_fp[r], 0, tok0});
     tok0 += n_new[b];
   }
+  if (P->decode_impl == KV_DECODE_SIMT) {
+    Upload u;
+    u.add(units.data(), units.size() * sizeof(AttUnit));
+    if ((st = ensure(P->attend, u.size)) != KV_OK) return st;
+    if ((st = h2d(P, P->attend.ptr, u, s)) != KV_OK) return st;
+    KV_CUDA(launch_attend_simt(P, A, (const AttUnit*)P->attend.ptr, (int)units.size(), max_new * g, s));
+    return KV_OK;
+  }
+  AttPlan pl;
+  plan_wide(units, g, k != nullptr, tree != nullptr, P->sm_count, pl);
   Upload u;
   const size_t ou = u.add(units.data(), units.size() * sizeof(AttUnit));
-  if ((st = ensure(P->attend, u.size)) != KV_OK) return st;
+  const size_t oi = u.add(pl.items.data(), pl.items.size() * sizeof(AttItem));
+  const size_t oc = u.add(pl.cta_item.data(), pl.cta_item.size() * sizeof(int32_t));
+  const size_t om = u.add(pl.merges.data(), pl.merges.size() * sizeof(AttMerge));
+  const size_t op = (u.size + 255) & ~size_t(255);
+  if ((st = ensure(P->attend, op + (size_t)pl.n_parts * 128 * kAttPart * sizeof(float))) != KV_OK) return st;
   if ((st = h2d(P, P->attend.ptr, u, s)) != KV_OK) return st;
-  const AttUnit* du = (const AttUnit*)((const uint8_t*)P->attend.ptr + ou);
-  KV_CUDA(launch_attend_simt(P, A, du, (int)units.size(), max_new * g, s));
+  const uint8_t* base = (const uint8_t*)P->attend.ptr;
+  const AttUnit* du = (const AttUnit*)(base + ou);
+  float* d_part = (float*)((uint8_t*)P->attend.ptr + op);
+  KV_CUDA(launch_attend_wide(P, A, du, (const AttItem*)(base + oi), (const int32_t*)(base + oc),
+                             (int)pl.cta_item.size() - 1, d_part, s));
+  if (!pl.merges.empty())
+    KV_CUDA(launch_attend_merge(P, A, du, (const AttMerge*)(base + om), (int)pl.merges.size(), pl.merge_rows, d_part, 128, s));
   return KV_OK;
 }

@@ -18,6 +18,21 @@ struct AttUnit {
   int64_t tok0;       // the request's first row in q, k, v and out
 };
 
+// A block of a unit's rows over a run of its key tiles, done by one CTA.
+struct AttItem {
+  int32_t unit, row0;
+  int32_t tile0, tile1;   // tiles of 128 keys: pages by fours, then the list's rows, then the new tokens
+  int32_t part;           // first partial (see each kernel), or -1: the block is done here
+  int32_t pad[3];
+};
+
+// Rows whose partials are to be merged: parts part0, part0 + stride, ...
+struct AttMerge {
+  int32_t unit, row0, rows;
+  int32_t part0, n_parts, stride;
+};
+constexpr int kAttPart = kHeadDim + 4;   // floats per row of a partial: O, then m and l
+
 // Everything a kernel needs besides its plan.
 struct AttArgs {
   const uint8_t* pool;
@@ -61,5 +76,11 @@ __device__ __forceinline__ int att_list_at(int t, int c) { return (((c >> 3) ^ (
 // CUDA-core kernel (kvq_attend_simt.cu): every unit's rows in blocks of 32.
 cudaError_t launch_attend_simt(kv_pool* P, const AttArgs& A, const AttUnit* d_units, int n_units, int max_rows,
                                cudaStream_t s);
+
+// Tensor-core kernel for many rows per unit (kvq_attend_wide.cu): blocks of 256
+// rows, partials of 128 rows, two per item (rows 0..127 and 128..255; for a
+// block of at most 128 rows, the same rows over even and over odd tiles).
+cudaError_t launch_attend_wide(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const AttItem* d_items,
+                               const int32_t* d_cta_item, int n_ctas, float* d_part, cudaStream_t s);
 
 }  // namespace kvq

@@ -1,0 +1,654 @@
+// kv_attend for many rows per unit (chunks of a prompt, wide trees): tcgen05
+// attention with the cache dequantized on the way into shared memory.
+//
+// A CTA takes an item: a block of up to 256 rows of one (request, kv head) unit
+// and a run of its key tiles (128 keys: four pages, or bf16 rows).  Per tile
+//     S_x = Q_x K^T          (x = 0, 1: 128 rows each; 128 x 128 x 128)
+//     P_x = 2^(S_x rf - m)   (rf: softmax scale, log2 e and the row's power of two)
+//     O_x += P_x V           (P_x read from TMEM)
+// with the running maximum m and sum of each row; O_x stays in TMEM over the
+// item and is rescaled only when a row's maximum has grown by more than 2^8
+// (the sums are fp32 and P is binary16 with 2^7 of headroom below 65504, so a
+// stale maximum loses nothing).
+//
+// Roles (18 warps): two warpgroups hold one row per thread of S_0 / S_1; eight
+// warps dequantize (a page's K or V each); one thread issues every MMA; one
+// warp streams page blocks with bulk copies through a ring of six pages.
+// While one warpgroup works on its S, the tensor cores work for the other.  A
+// block of at most 128 rows uses the two warpgroups for even and odd tiles
+// instead (the same rows, two partial states).
+//
+// What bounds it: per tile and 256 rows the tensor cores need 2048 cycles, the
+// operand reads and writes of shared memory about as many, exponentials
+// 32768 / (SM rate); the CTA's shared memory (Q, two K and two V tiles) leaves
+// one CTA per SM.
+#include <algorithm>
+#include <atomic>
+
+#include "kvq_attend_mma.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kRing = 6;                        // pages in flight
+constexpr int kWarps = 18;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTileBytes = 128 * 128 * 2;
+constexpr int kMaskRing = 8;                    // tiles whose live words are kept
+constexpr float kHead = 7.0f;                   // P = 2^(x - m + 7)
+constexpr float kGrow = 8.0f;                   // a maximum may be stale by this much (base 2)
+
+struct alignas(1024) WideSmem {
+  uint8_t q[2][kTileBytes], k[2][kTileBytes], v[2][kTileBytes];
+  alignas(128) uint8_t raw[kRing][kInt4Block];
+  uint32_t live[kMaskRing][4];
+  int32_t cls[kRing];
+  uint64_t raw_full[kRing], raw_empty[kRing];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t q_full, s_full[2], p_full[2], o_full, drain;
+  uint32_t tmem, gave_up;
+};
+static_assert(sizeof(WideSmem) <= 232448, "one CTA's shared memory");
+
+struct Tiles {   // an item's tiles: [0, pages), [pages, lists), [lists, all) by kind
+  int pages, lists, all, t_last, rows;
+};
+__device__ __forceinline__ Tiles tiles_of(const AttArgs& A, const AttUnit& u, int row0, int block) {
+  Tiles t;
+  const int g = A.hq / A.hkv;
+  t.rows = min(block, u.T * g - row0);
+  t.t_last = (row0 + t.rows - 1) / g;
+  t.pages = (u.n_pages + 3) >> 2;
+  t.lists = t.pages + ((u.n_fp + 127) >> 7);
+  t.all = t.lists + (!A.k ? 0 : (((A.tree ? u.T - 1 : t.t_last) >> 7) + 1));
+  return t;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
+    AttArgs A, const AttUnit* __restrict__ units, const AttItem* __restrict__ items, const int32_t* __restrict__ cta_item,
+    float* __restrict__ part, uint32_t first_spins) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  WideSmem& S = *reinterpret_cast<WideSmem*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int i0 = cta_item[blockIdx.x], i1 = cta_item[blockIdx.x + 1];
+  volatile uint32_t* gave_up = &S.gave_up;
+  if (tid == 0) {
+    for (int x = 0; x < kRing; ++x) {
+      mb_init(&S.raw_full[x], 1);
+      mb_init(&S.raw_empty[x], 2);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mb_init(&S.k_full[x], 4);
+      mb_init(&S.k_empty[x], 1);
+      mb_init(&S.v_full[x], 4);
+      mb_init(&S.v_empty[x], 1);
+      mb_init(&S.s_full[x], 1);
+      mb_init(&S.p_full[x], 4);
+    }
+    mb_init(&S.q_full, 8);
+    mb_init(&S.o_full, 1);
+    mb_init(&S.drain, 1);
+    S.gave_up = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 16) tm_alloc(&S.tmem, 512);
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tmem = S.tmem;
+  const int g = A.hq / A.hkv;
+
+  if (warp < 8) {
+    // ---------------------------------------------------------------- softmax
+    const int x = warp >> 2;                               // S / P / O of this warpgroup
+    const int rt = tid & 127;
+    const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);   // the warp's 32 TMEM lanes
+    const uint32_t ts = tl + 128u * x, to = tl + 256u + 128u * x;
+    uint32_t page_tiles = 0, s_phase = 0, o_phase = 0, bad = 0u;
+    bool ok = true;
+    const bool qal = ((uintptr_t)A.q & 15) == 0;
+    for (int it = i0; it < i1 && ok; ++it) {
+      const AttItem I = items[it];
+      const AttUnit u = units[I.unit];
+      const Tiles T = tiles_of(A, u, I.row0, 256);
+      const bool one = T.rows <= 128;                      // both warpgroups: the same rows
+      const int rl = one ? rt : 128 * x + rt;              // row in the block
+      const bool valid = rl < T.rows;
+      const int row = I.row0 + (valid ? rl : 0), t = row / g;
+      const size_t at = ((size_t)(u.tok0 + t) * A.hq + (size_t)u.kvh * g + (row - t * g)) * kHeadDim;
+      // ---- Q row: scaled by a power of two so that its largest element is in [2^7, 2^8)
+      float rf = 0.0f;
+      {
+        float mx = 0.0f;
+        if (valid)
+          for (int c = 0; c < 16; ++c) {
+            const uint4 w = load8(A.q + at + 8 * c, qal);
+            const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mx = fmaxf(mx, fmaxf(fabsf(bf_f(wd[k] & 0xFFFFu)), fabsf(__uint_as_float(wd[k] & 0xFFFF0000u))));
+          }
+        const int e = mx > 0.0f && mx < INFINITY ? max(-100, min(100, 7 - ilogbf(mx))) : 0;
+        const float mul = copysignf(__int_as_float((e + 127) << 23), A.scale_log2);
+        rf = fabsf(A.scale_log2) * __int_as_float((127 - e) << 23);
+        if (!one || x == 0) {
+          uint8_t* qb = S.q[x];
+          for (int c = 0; c < 16; ++c) {
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (valid) w = load8(A.q + at + 8 * c, qal);
+            const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              f[2 * k] = bf_f(wd[k] & 0xFFFFu) * mul;
+              f[2 * k + 1] = __uint_as_float(wd[k] & 0xFFFF0000u) * mul;
+            }
+            *reinterpret_cast<uint4*>(qb + tile_off(128, rt, c)) =
+                make_uint4(f16x2(f[0], f[4]), f16x2(f[1], f[5]), f16x2(f[2], f[6]), f16x2(f[3], f[7]));
+          }
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      tm_fence_before();   // the previous item's O has been read
+      __syncwarp();
+      if (lane == 0) mb_arrive(&S.q_full);
+      const uint64_t tm = A.tree ? A.tree[u.tok0 + t] : 0ull;
+
+      float m = -INFINITY, l = 0.0f;
+      bool any = false;                                    // O_x has been written in this item
+      for (int tile = I.tile0; tile < I.tile1; ++tile) {
+        const bool page = tile < T.pages;
+        const uint32_t pt = page_tiles;
+        page_tiles += page ? 1u : 0u;
+        if (one && ((tile - I.tile0) & 1) != x) continue;
+        // ---- keys this row sees, 128 bits in the tiles' order
+        uint32_t mk[4];
+        ok = __all_sync(0xFFFFFFFFu, mb_wait(&S.s_full[x], s_phase, gave_up));
+        if (!ok) break;
+        s_phase ^= 1u;
+        tm_fence_after();
+        if (page) {
+          const volatile uint32_t* lv = S.live[pt & (kMaskRing - 1)];
+          mk[0] = lv[0]; mk[1] = lv[1]; mk[2] = lv[2]; mk[3] = lv[3];
+        } else {
+          const bool list = tile < T.lists;
+          const int base = 128 * (tile - (list ? T.pages : T.lists));
+          // keys [base, base + n) are seen (with a tree, those of its bits)
+          const int n = (list ? u.n_fp : (A.tree ? u.T : t + 1)) - base;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int nw = n - 32 * w;
+            uint32_t b = nw >= 32 ? 0xFFFFFFFFu : (nw <= 0 ? 0u : (1u << nw) - 1u);
+            if (!list && A.tree) b &= w == 0 ? (uint32_t)tm : (w == 1 ? (uint32_t)(tm >> 32) : 0u);
+            mk[w] = order_bits(b);
+          }
+        }
+        const bool full = (mk[0] & mk[1] & mk[2] & mk[3]) == 0xFFFFFFFFu;
+        const bool warp_full = __all_sync(0xFFFFFFFFu, full);
+        // ---- maximum
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t s[32];
+          tm_ld<32>(s, ts + 32u * c);
+          tm_wait_ld();
+          if (warp_full) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 1])));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, ((mk[c] >> j) & 1u) ? __uint_as_float(s[j]) : -INFINITY);
+          }
+        }
+        mx = mx == -INFINITY ? mx : mx * rf;               // rf may be 0
+        const bool grow = mx > m + kGrow || (m == -INFINITY && mx > -INFINITY);
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+          const float corr = grow ? ex2f(m - mx) : 1.0f;   // m = -inf: 0
+          if (grow) m = mx;
+          l *= corr;
+          if (any) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tm_ld<32>(o, to + 32u * c);
+              tm_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
+              tm_st<32>(to + 32u * c, o);
+            }
+          }
+        }
+        any = true;
+        // ---- weights
+        const float nm = kHead - m;
+        float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t s[32], p[16];
+          tm_ld<32>(s, ts + 32u * c);
+          tm_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float a, b;
+            fma2(a, b, __uint_as_float(s[j]), __uint_as_float(s[j + 1]), rf, rf, nm, nm);
+            a = ex2f(a);
+            b = ex2f(b);
+            if (!warp_full) {
+              a = ((mk[c] >> j) & 1u) ? a : 0.0f;
+              b = ((mk[c] >> (j + 1)) & 1u) ? b : 0.0f;
+            }
+            add2f(l0, l1, a, b);
+            p[j >> 1] = f16x2(a, b);
+          }
+          tm_st<16>(ts + 16u * c, p);
+        }
+        l += l0 + l1;
+        tm_wait_st();
+        tm_fence_before();
+        __syncwarp();
+        if (lane == 0) mb_arrive(&S.p_full[x]);
+      }
+      if (!ok) break;
+      // ---- result of the item
+      if (I.tile1 > I.tile0) {
+        ok = __all_sync(0xFFFFFFFFu, mb_wait(&S.o_full, o_phase, gave_up));
+        if (!ok) break;
+        o_phase ^= 1u;
+        tm_fence_after();
+      }
+      const bool whole = I.part < 0;
+      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // a NaN stays
+      // an infinite sum or a NaN: a value of the cache past binary16 (or of q)
+      if (valid && !(l < INFINITY)) bad = 1u;
+      float* pp = part + (size_t)(whole ? 0 : I.part + x) * 128 * kAttPart + (size_t)rt * kAttPart;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        if (any) {
+          tm_ld<32>(o, to + 32u * c);
+          tm_wait_ld();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0u;
+        }
+        if (valid && whole) {
+          if (qal && ((uintptr_t)A.out & 15) == 0) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float a = __uint_as_float(o[j + 2 * k]) * inv, b = __uint_as_float(o[j + 2 * k + 1]) * inv;
+                if (!(fabsf(a) < INFINITY) || !(fabsf(b) < INFINITY)) bad = 1u;
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(b), "f"(a));
+              }
+              *reinterpret_cast<uint4*>(A.out + at + 32 * c + j) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float a = __uint_as_float(o[j]) * inv;
+              if (!(fabsf(a) < INFINITY)) bad = 1u;
+              A.out[at + 32 * c + j] = __bfloat16_as_ushort(__float2bfloat16_rn(a));
+            }
+          }
+        } else if (valid) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(pp + 32 * c + j) = make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
+                                                                      __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
+        }
+        __syncwarp();
+      }
+      if (!whole && valid) *reinterpret_cast<float2*>(pp + kHeadDim) = make_float2(m, l);
+    }
+    if (bad) atomicOr(A.status, kStatusRange);
+  } else if (warp < 16) {
+    // ----------------------------------------------------------- dequantize
+    const bool is_k = warp < 12;
+    const int p = warp & 3;                                // page (or 32 rows) of the tile
+    // slots r, channels' / slots' run i of this lane: 8 lanes of a shared-memory
+    // phase read 128 different bytes and write 8 different chunk positions
+    const int qd = lane >> 3, hf = (lane >> 2) & 1, i = lane & 3;
+    const int rk = ((qd & 1) | ((qd & 2) << 1)) ^ (3 * hf), rv = qd ^ (5 * hf);
+    uint32_t page_tiles = 0, tc = 0, bad = 0u;
+    const bool kal = (((uintptr_t)A.k | (uintptr_t)A.v) & 15) == 0;
+    const bool val = (((uintptr_t)A.k | (uintptr_t)A.v) & 3) == 0;
+    bool ok = true;
+    uint64_t* full = is_k ? S.k_full : S.v_full;
+    uint64_t* empty = is_k ? S.k_empty : S.v_empty;
+    for (int it = i0; it < i1 && ok; ++it) {
+      const AttItem I = items[it];
+      const AttUnit u = units[I.unit];
+      const Tiles T = tiles_of(A, u, I.row0, 256);
+      for (int tile = I.tile0; tile < I.tile1; ++tile, ++tc) {
+        const uint32_t st = tc & 1u;
+        uint8_t* dst = is_k ? S.k[st] : S.v[st];
+        ok = __all_sync(0xFFFFFFFFu, mb_wait(&empty[st], ((tc >> 1) & 1u) ^ 1u, gave_up));
+        if (!ok) break;
+        if (tile < T.pages) {
+          const uint32_t c = 4u * page_tiles + p, slot = c % kRing;
+          ++page_tiles;
+          ok = mb_wait(&S.raw_full[slot], (c / kRing) & 1u, gave_up, c < 4u ? first_spins : kAttSpin);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          const uint8_t* blk = S.raw[slot];
+          const int cls = *(volatile int32_t*)&S.cls[slot];
+          if (is_k) {
+            auto put = [&](int t, const uint32_t (&w)[4][4]) {
+              const int n = 32 * p + (t & ~7) + order8(t & 7);
+#pragma unroll
+              for (int gr = 0; gr < 4; ++gr)
+                *reinterpret_cast<uint4*>(dst + tile_off(128, n, 4 * gr + i)) =
+                    make_uint4(w[gr][0], w[gr][1], w[gr][2], w[gr][3]);
+            };
+            uint32_t w[4][4];
+            if (cls == kClsInt2) {
+              KScales2 sc;
+              k_scales2(blk, i, sc);
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                k_slot2(blk, 8 * b + rk, i, sc, w);
+                put(8 * b + rk, w);
+              }
+            } else if (cls == kClsInt4) {
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                k_slot4(blk, 8 * b + rk, i, w);
+                put(8 * b + rk, w);
+              }
+            } else {
+              for (int b = 0; b < 4; ++b) {
+                if (cls == kClsInt3) {
+                  k_slot3(blk, 8 * b + rk, i, w);
+                } else if (cls == kClsFp4) {
+                  k_slotf(blk, 8 * b + rk, i, w);
+                } else {
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) w[x >> 2][x & 3] = 0u;
+                }
+                put(8 * b + rk, w);
+              }
+            }
+          } else {
+            auto put = [&](int gr, const uint32_t (&w)[4][4]) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<uint4*>(dst + tile_off(128, 32 * gr + 8 * x + rv, 4 * p + i)) =
+                    make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
+            };
+            uint32_t w[4][4];
+            if (cls == kClsInt2) {
+#pragma unroll
+              for (int gr = 0; gr < 4; ++gr) {
+                v_group2(blk, gr, rv, i, w);
+                put(gr, w);
+              }
+            } else if (cls == kClsInt4) {
+#pragma unroll
+              for (int gr = 0; gr < 4; ++gr) {
+                v_group4(blk, gr, rv, i, w);
+                put(gr, w);
+              }
+            } else {
+              for (int gr = 0; gr < 4; ++gr) {
+                if (cls == kClsInt3) {
+                  v_group3(blk, gr, rv, i, w);
+                } else if (cls == kClsFp4) {
+                  v_groupf(blk, gr, rv, i, w);
+                } else {
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) w[x >> 2][x & 3] = 0u;
+                }
+                put(gr, w);
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mb_arrive(&S.raw_empty[slot]);
+        } else {
+          // ---- 32 bf16 rows: list tokens or new tokens
+          const bool list = tile < T.lists;
+          const int j0 = 128 * (tile - (list ? T.pages : T.lists)) + 32 * p;   // first row of this warp
+          const int n = list ? u.n_fp : u.T;
+          const size_t stride = list ? kHeadDim : (size_t)A.hkv * kHeadDim;
+          const uint16_t* src =
+              list ? (is_k ? A.fpk : A.fpv) + ((size_t)u.req * A.hkv + u.kvh) * (size_t)A.fp_cap * kHeadDim
+                   : (is_k ? A.k : A.v) + ((size_t)u.tok0 * A.hkv + u.kvh) * kHeadDim;
+          if (is_k) {
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+              const int t = 8 * b + rk, j = j0 + t, nn = 32 * p + 8 * b + order8(rk);
+#pragma unroll
+              for (int gr = 0; gr < 4; ++gr) {
+                uint32_t w[4] = {0u, 0u, 0u, 0u};
+                if (j < n) {
+                  const int ch = 4 * gr + i;
+                  const uint4 y = load8(src + (size_t)j * stride + 8 * (list ? ch ^ (j & 7) : ch), list || kal);
+                  order8_f16(y, 1.0f, w, bad);
+                }
+                *reinterpret_cast<uint4*>(dst + tile_off(128, nn, 4 * gr + i)) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          } else {
+            // a lane takes channels (2 cp, 2 cp + 1) of 8 rows at a time
+#pragma unroll 1
+            for (int y = 0; y < 8; ++y) {
+              const int cp = lane + 32 * (y & 1), b = y >> 1;
+              float lo[8], hi[8];
+#pragma unroll
+              for (int s = 0; s < 8; ++s) {
+                const int j = j0 + 8 * b + s;
+                uint32_t w = 0u;
+                if (j < n) {
+                  const uint16_t* q = src + (size_t)j * stride + (list ? att_list_at(j, 2 * cp) : 2 * cp);
+                  w = list || val ? __ldg(reinterpret_cast<const uint32_t*>(q))
+                                  : (uint32_t)__ldg(q) | ((uint32_t)__ldg(q + 1) << 16);
+                }
+                lo[s] = in_range(bf_f(w & 0xFFFFu), bad);
+                hi[s] = in_range(__uint_as_float(w & 0xFFFF0000u), bad);
+              }
+              *reinterpret_cast<uint4*>(dst + tile_off(128, 2 * cp, 4 * p + b)) =
+                  make_uint4(f16x2(lo[0], lo[4]), f16x2(lo[1], lo[5]), f16x2(lo[2], lo[6]), f16x2(lo[3], lo[7]));
+              *reinterpret_cast<uint4*>(dst + tile_off(128, 2 * cp + 1, 4 * p + b)) =
+                  make_uint4(f16x2(hi[0], hi[4]), f16x2(hi[1], hi[5]), f16x2(hi[2], hi[6]), f16x2(hi[3], hi[7]));
+            }
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMAs read what was written
+        __syncwarp();
+        if (lane == 0) mb_arrive(&full[st]);
+      }
+    }
+    if (bad) atomicOr(A.status, kStatusRange);
+  } else if (warp == 16) {
+    // ------------------------------------------------------------------ MMA
+    if (lane == 0) {
+      constexpr uint32_t idesc = mma_idesc(128, 128);
+      const uint32_t qa[2] = {sm32(S.q[0]), sm32(S.q[1])};
+      uint32_t tc0 = 0;            // tiles before this item
+      uint32_t p_phase = 0;        // bit x: phase of p_full[x]
+      bool ok = true;
+      // S_x = Q K^T of tile number tc; block-major operands: 4 K steps of 16 per 64-channel block
+      auto qk = [&](int x, int qx, uint32_t tc) {
+        const uint32_t kb = sm32(S.k[tc & 1u]);
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          const uint32_t off = (uint32_t)(s >> 2) * 16384u + (uint32_t)(s & 3) * 32u;
+          mma_ss(tmem + 128u * x, sw128_desc(qa[qx] + off), sw128_desc(kb + off), idesc, s > 0);
+        }
+      };
+      auto pv = [&](int x, uint32_t tc, bool first) {
+        const uint32_t vb = sm32(S.v[tc & 1u]);
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          const uint32_t off = (uint32_t)(s >> 2) * 16384u + (uint32_t)(s & 3) * 32u;
+          mma_ts(tmem + 256u + 128u * x, tmem + 128u * x + 8u * s, sw128_desc(vb + off), idesc, !first || s > 0);
+        }
+      };
+      auto k_ready = [&](uint32_t tc) { return mb_wait(&S.k_full[tc & 1u], (tc >> 1) & 1u, gave_up); };
+      auto v_ready = [&](uint32_t tc) { return mb_wait(&S.v_full[tc & 1u], (tc >> 1) & 1u, gave_up); };
+      auto p_ready = [&](int x) {
+        const bool r = mb_wait(&S.p_full[x], (p_phase >> x) & 1u, gave_up);
+        p_phase ^= 1u << x;
+        return r;
+      };
+      for (int it = i0; it < i1 && ok; ++it) {
+        const AttItem I = items[it];
+        const AttUnit u = units[I.unit];
+        const Tiles T = tiles_of(A, u, I.row0, 256);
+        const bool one = T.rows <= 128;
+        const int n = I.tile1 - I.tile0;
+        ok = mb_wait(&S.q_full, (uint32_t)(it - i0) & 1u, gave_up);
+        if (!ok || n == 0) continue;
+        tm_fence_after();
+        if (!one) {
+          ok = k_ready(tc0);
+          if (!ok) break;
+          tm_fence_after();
+          for (int x = 0; x < 2; ++x) {
+            qk(x, x, tc0);
+            tm_commit(&S.s_full[x]);
+          }
+          tm_commit(&S.k_empty[tc0 & 1u]);
+          for (int t = 0; t < n && ok; ++t) {
+            const uint32_t tc = tc0 + t;
+            for (int x = 0; x < 2 && ok; ++x) {
+              ok = p_ready(x) && (x || v_ready(tc));
+              if (!ok) break;
+              tm_fence_after();
+              pv(x, tc, t == 0);
+              if (x) tm_commit(&S.v_empty[tc & 1u]);
+              if (t + 1 < n) {
+                ok = x || k_ready(tc + 1);
+                if (!ok) break;
+                tm_fence_after();
+                qk(x, x, tc + 1);
+                tm_commit(&S.s_full[x]);
+                if (x) tm_commit(&S.k_empty[(tc + 1) & 1u]);
+              }
+            }
+          }
+        } else {
+          for (int t = 0; t < 2 && t < n && ok; ++t) {
+            ok = k_ready(tc0 + t);
+            if (!ok) break;
+            tm_fence_after();
+            qk(t, 0, tc0 + t);
+            tm_commit(&S.s_full[t]);
+            tm_commit(&S.k_empty[(tc0 + t) & 1u]);
+          }
+          for (int t = 0; t < n && ok; ++t) {
+            const uint32_t tc = tc0 + t;
+            const int x = t & 1;
+            ok = p_ready(x) && v_ready(tc);
+            if (!ok) break;
+            tm_fence_after();
+            pv(x, tc, t < 2);
+            tm_commit(&S.v_empty[tc & 1u]);
+            if (t + 2 < n) {
+              ok = k_ready(tc + 2);
+              if (!ok) break;
+              tm_fence_after();
+              qk(x, 0, tc + 2);
+              tm_commit(&S.s_full[x]);
+              tm_commit(&S.k_empty[tc & 1u]);
+            }
+          }
+        }
+        if (ok) tm_commit(&S.o_full);
+        tc0 += (uint32_t)n;
+      }
+      if (!ok) {   // let the MMAs that were issued finish before TMEM is given back
+        volatile uint32_t never = 0u;
+        tm_commit(&S.drain);
+        mb_wait(&S.drain, 0u, &never);
+      }
+    }
+    __syncwarp();
+  } else {
+    // --------------------------------------------------------------- loader
+    uint32_t page_tiles = 0, issued = 0;   // issued: pages of this lane
+    bool ok = true;
+    for (int it = i0; it < i1 && ok; ++it) {
+      const AttItem I = items[it];
+      const AttUnit u = units[I.unit];
+      const Tiles T = tiles_of(A, u, I.row0, 256);
+      const Entry* tab = A.table + (size_t)u.req * A.max_pages;
+      const int end = min(I.tile1, T.pages);
+      for (int tile = I.tile0; tile < end; ++tile, ++page_tiles) {
+        if (lane < 4) {
+          const uint32_t c = 4u * page_tiles + lane, slot = c % kRing;
+          const int pi = 4 * tile + lane;
+          Entry e{-1, 0u};
+          int cls = -1;
+          const uint8_t* blk = nullptr;
+          if (pi < u.n_pages) {
+            e = tab[pi];
+            if (A.hdead) e.live &= ~A.hdead[(size_t)e.id * A.hkv + u.kvh];
+            if (e.live) cls = att_page(A, e.id, u.kvh, blk);
+          }
+          ok = mb_wait(&S.raw_empty[slot], ((c / kRing) & 1u) ^ 1u, gave_up);
+          if (ok) {
+            *(volatile int32_t*)&S.cls[slot] = cls;
+            *(volatile uint32_t*)&S.live[page_tiles & (kMaskRing - 1)][lane] = order_bits(e.live);
+            ++issued;
+            if (cls < 0)
+              mb_arrive(&S.raw_full[slot]);
+            else
+              bulk_to_smem(S.raw[slot], blk,
+                           cls == kClsInt2 ? kInt2Block : (cls == kClsInt4 ? kInt4Block : (cls == kClsInt3 ? kInt3Block : kFp4Block)),
+                           &S.raw_full[slot]);
+          }
+        }
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+      }
+    }
+    // every copy has landed before the CTA leaves: the last one of each slot
+    uint32_t n[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) n[j] = __shfl_sync(0xFFFFFFFFu, issued, j);
+    if (lane < kRing) {
+      volatile uint32_t never = 0u;
+      const uint32_t most = max(max(n[0], n[1]), max(n[2], n[3]));
+      for (uint32_t c = 4u * most, back = 0; c > 0 && back < 4u + kRing; ++back) {
+        --c;
+        if (c % kRing == (uint32_t)lane && (c >> 2) < n[c & 3u]) {
+          mb_wait(&S.raw_full[lane], (c / kRing) & 1u, &never);
+          break;
+        }
+      }
+    }
+    __syncwarp();
+  }
+  tm_fence_before();
+  __syncthreads();
+  if (tid == 0 && *gave_up) atomicOr(A.status, kStatusTimeout);
+  if (warp == 16) {
+    tm_fence_after();
+    tm_free(tmem, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attend_wide(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const AttItem* d_items,
+                               const int32_t* d_cta_item, int n_ctas, float* d_part, cudaStream_t s) {
+  if (n_ctas <= 0) return cudaSuccess;
+  static std::atomic<uint64_t> attr_set{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!(attr_set.load() >> dev & 1u)) {
+    const cudaError_t e = cudaFuncSetAttribute(attend_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)sizeof(WideSmem));
+    if (e != cudaSuccess) return e;
+    attr_set.fetch_or(uint64_t(1) << dev);
+  }
+  ++P->launches;
+  attend_wide_kernel<<<(unsigned)n_ctas, kThreads, sizeof(WideSmem), s>>>(
+      A, d_units, d_items, d_cta_item, d_part, P->first_wait_spins < 0 ? kAttSpin : (uint32_t)P->first_wait_spins);
+  return cudaGetLastError();
+}
+
+}  // namespace kvq
