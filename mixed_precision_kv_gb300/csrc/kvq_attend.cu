@@ -115,7 +115,7 @@ void plan_wide(const std::vector<AttUnit>& units, int g, bool kv, bool tree, int
       total += (int64_t)b.tiles * b.cost + 1;
     }
   }
-  const double share = (double)total / ctas;
+  const double share = (double)(total + ctas) / ctas;   // every CTA ends inside a block once
   double done = 0.0;
   int cta = 0;
   for (const Block& b : blocks) {

@@ -53,6 +53,15 @@ __device__ __forceinline__ bool mb_wait(uint64_t* b, uint32_t parity, volatile u
   *gave_up = 1u;
   return false;
 }
+// Wait until a ring slot's number is `c` (bounded as mb_wait).
+__device__ __forceinline__ bool slot_is(volatile uint32_t* seq, uint32_t c, volatile uint32_t* gave_up) {
+  for (uint32_t it = 0; it < kAttSpin; ++it) {
+    if (*seq == c) return true;
+    if (*gave_up) return false;
+  }
+  *gave_up = 1u;
+  return false;
+}
 __device__ __forceinline__ void bulk_to_smem(void* dst, const void* src, uint32_t bytes, uint64_t* b) {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the slot was read generically
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(sm32(b)), "r"(bytes) : "memory");
@@ -117,6 +126,12 @@ __device__ __forceinline__ void tm_ld<32>(uint32_t (&r)[32], uint32_t addr) {
                  "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
                  "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
                  "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(addr));
+}
+template <>
+__device__ __forceinline__ void tm_ld<64>(uint32_t (&r)[64], uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
                : "r"(addr));
 }
 template <int N>
@@ -359,12 +374,14 @@ __device__ __forceinline__ float in_range(float f, uint32_t& bad) {
   return 0.0f;
 }
 // 8 bf16 values at p (2-byte aligned; one 16-byte load where the caller knows p to be 16-byte aligned)
-__device__ __forceinline__ uint4 load8(const uint16_t* p, bool aligned) {
-  if (aligned) return __ldg(reinterpret_cast<const uint4*>(p));
+__device__ __noinline__ uint4 load8_unaligned(const uint16_t* p) {
   uint32_t x[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) x[k] = (uint32_t)__ldg(p + 2 * k) | ((uint32_t)__ldg(p + 2 * k + 1) << 16);
   return make_uint4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ uint4 load8(const uint16_t* p, bool aligned) {
+  return aligned ? __ldg(reinterpret_cast<const uint4*>(p)) : load8_unaligned(p);
 }
 // 8 values in order8, scaled by 2^e exactly (mul), as binary16
 __device__ __forceinline__ void order8_f16(const uint4& x, float mul, uint32_t (&out)[4], uint32_t& bad) {

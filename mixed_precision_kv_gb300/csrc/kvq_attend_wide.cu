@@ -37,12 +37,14 @@ constexpr int kTileBytes = 128 * 128 * 2;
 constexpr int kMaskRing = 8;                    // tiles whose live words are kept
 constexpr float kHead = 7.0f;                   // P = 2^(x - m + 7)
 constexpr float kGrow = 8.0f;                   // a maximum may be stale by this much (base 2)
+constexpr float kNever = -3.0e38f;              // S of a key that is not seen
 
 struct alignas(1024) WideSmem {
   uint8_t q[2][kTileBytes], k[2][kTileBytes], v[2][kTileBytes];
   alignas(128) uint8_t raw[kRing][kInt4Block];
   uint32_t live[kMaskRing][4];
   int32_t cls[kRing];
+  uint32_t seq[kRing];                          // the page number a slot was last filled for
   uint64_t raw_full[kRing], raw_empty[kRing];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t q_full, s_full[2], p_full[2], o_full, drain;
@@ -76,6 +78,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
     for (int x = 0; x < kRing; ++x) {
       mb_init(&S.raw_full[x], 1);
       mb_init(&S.raw_empty[x], 2);
+      S.seq[x] = 0xFFFFFFFFu;
     }
     for (int x = 0; x < 2; ++x) {
       mb_init(&S.k_full[x], 4);
@@ -121,6 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
       {
         float mx = 0.0f;
         if (valid)
+#pragma unroll 1
           for (int c = 0; c < 16; ++c) {
             const uint4 w = load8(A.q + at + 8 * c, qal);
             const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
@@ -130,9 +134,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
           }
         const int e = mx > 0.0f && mx < INFINITY ? max(-100, min(100, 7 - ilogbf(mx))) : 0;
         const float mul = copysignf(__int_as_float((e + 127) << 23), A.scale_log2);
-        rf = fabsf(A.scale_log2) * __int_as_float((127 - e) << 23);
+        // (a factor below 1e-30 makes every logit 0, as 1e-30 does; kNever times it must stay far below 0)
+        rf = fmaxf(fabsf(A.scale_log2) * __int_as_float((127 - e) << 23), 1e-30f);
         if (!one || x == 0) {
           uint8_t* qb = S.q[x];
+#pragma unroll 1
           for (int c = 0; c < 16; ++c) {
             uint4 w = make_uint4(0u, 0u, 0u, 0u);
             if (valid) w = load8(A.q + at + 8 * c, qal);
@@ -151,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       tm_fence_before();   // the previous item's O has been read
       __syncwarp();
-      if (lane == 0) mb_arrive(&S.q_full);
+      if (lane == 0 && I.tile1 > I.tile0) mb_arrive(&S.q_full);   // an item without tiles has no MMAs
       const uint64_t tm = A.tree ? A.tree[u.tok0 + t] : 0ull;
 
       float m = -INFINITY, l = 0.0f;
@@ -183,46 +189,54 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
             mk[w] = order_bits(b);
           }
         }
-        const bool full = (mk[0] & mk[1] & mk[2] & mk[3]) == 0xFFFFFFFFu;
-        const bool warp_full = __all_sync(0xFFFFFFFFu, full);
-        // ---- maximum
-        float mx = -INFINITY;
+        // Keys that are not seen become kNever in S, so that the code below needs no masks (the hot code
+        // has to stay small: every warp of an SM runs its own part of it, and fetching it was the limit).
+        if (!__all_sync(0xFFFFFFFFu, (mk[0] & mk[1] & mk[2] & mk[3]) == 0xFFFFFFFFu)) {
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t s[16];
+            tm_ld<16>(s, ts + 16u * c);
+            tm_wait_ld();
+            const uint32_t mc = (c < 4 ? (c < 2 ? mk[0] : mk[1]) : (c < 6 ? mk[2] : mk[3])) >> (16 * (c & 1));
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t s[32];
-          tm_ld<32>(s, ts + 32u * c);
-          tm_wait_ld();
-          if (warp_full) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 1])));
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, ((mk[c] >> j) & 1u) ? __uint_as_float(s[j]) : -INFINITY);
+            for (int j = 0; j < 16; ++j) s[j] = ((mc >> j) & 1u) ? s[j] : __float_as_uint(kNever);
+            tm_st<16>(ts + 16u * c, s);
           }
+          tm_wait_st();
         }
-        mx = mx == -INFINITY ? mx : mx * rf;               // rf may be 0
+        // ---- maximum
+        float mx = kNever;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t s[64];
+          tm_ld<64>(s, ts + 64u * c);
+          tm_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 64; j += 2) mx = fmaxf(fmaxf(mx, __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
+        }
+        mx = mx > 0.9f * kNever ? mx * rf : -INFINITY;
         const bool grow = mx > m + kGrow || (m == -INFINITY && mx > -INFINITY);
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float corr = grow ? ex2f(m - mx) : 1.0f;   // m = -inf: 0
           if (grow) m = mx;
           l *= corr;
           if (any) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tm_ld<32>(o, to + 32u * c);
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              tm_ld<16>(o, to + 16u * c);
               tm_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
-              tm_st<32>(to + 32u * c, o);
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
+              tm_st<16>(to + 16u * c, o);
             }
           }
         }
         any = true;
-        // ---- weights
-        const float nm = kHead - m;
+        // ---- weights (a row that has seen nothing: every weight is 2^(kNever rf) = 0)
+        const float nm = m == -INFINITY ? 0.0f : kHead - m;
         float l0 = 0.0f, l1 = 0.0f;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t s[32], p[16];
           tm_ld<32>(s, ts + 32u * c);
@@ -233,14 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
             fma2(a, b, __uint_as_float(s[j]), __uint_as_float(s[j + 1]), rf, rf, nm, nm);
             a = ex2f(a);
             b = ex2f(b);
-            if (!warp_full) {
-              a = ((mk[c] >> j) & 1u) ? a : 0.0f;
-              b = ((mk[c] >> (j + 1)) & 1u) ? b : 0.0f;
-            }
             add2f(l0, l1, a, b);
             p[j >> 1] = f16x2(a, b);
           }
-          tm_st<16>(ts + 16u * c, p);
+          tm_st<16>(ts + 16u * c, p);   // over columns that have been read
         }
         l += l0 + l1;
         tm_wait_st();
@@ -260,21 +270,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // a NaN stays
       // an infinite sum or a NaN: a value of the cache past binary16 (or of q)
       if (valid && !(l < INFINITY)) bad = 1u;
-      float* pp = part + (size_t)(whole ? 0 : I.part + x) * 128 * kAttPart + (size_t)rt * kAttPart;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
+      float* const pp = part + (size_t)(whole ? 0 : I.part + x) * 128 * kAttPart + (size_t)rt * kAttPart;
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t o[16];
         if (any) {
-          tm_ld<32>(o, to + 32u * c);
+          tm_ld<16>(o, to + 16u * c);
           tm_wait_ld();
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0u;
+          for (int j = 0; j < 16; ++j) o[j] = 0u;
         }
         if (valid && whole) {
           if (qal && ((uintptr_t)A.out & 15) == 0) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
+            for (int j = 0; j < 16; j += 8) {
               uint32_t w[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -282,20 +292,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
                 if (!(fabsf(a) < INFINITY) || !(fabsf(b) < INFINITY)) bad = 1u;
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(b), "f"(a));
               }
-              *reinterpret_cast<uint4*>(A.out + at + 32 * c + j) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(A.out + at + 16 * c + j) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
+            for (int j = 0; j < 16; ++j) {
               const float a = __uint_as_float(o[j]) * inv;
               if (!(fabsf(a) < INFINITY)) bad = 1u;
-              A.out[at + 32 * c + j] = __bfloat16_as_ushort(__float2bfloat16_rn(a));
+              A.out[at + 16 * c + j] = __bfloat16_as_ushort(__float2bfloat16_rn(a));
             }
           }
         } else if (valid) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4*>(pp + 32 * c + j) = make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
+          for (int j = 0; j < 16; j += 4)
+            *reinterpret_cast<float4*>(pp + 16 * c + j) = make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
                                                                       __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
         }
         __syncwarp();
@@ -329,7 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
         if (tile < T.pages) {
           const uint32_t c = 4u * page_tiles + p, slot = c % kRing;
           ++page_tiles;
-          ok = mb_wait(&S.raw_full[slot], (c / kRing) & 1u, gave_up, c < 4u ? first_spins : kAttSpin);
+          // A slot serves different warps in turn, so a parity alone does not say
+          // which fill it means: the slot must be this page's first.
+          ok = slot_is(&S.seq[slot], c, gave_up) &&
+               mb_wait(&S.raw_full[slot], (c / kRing) & 1u, gave_up, c < 4u ? first_spins : kAttSpin);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           const uint8_t* blk = S.raw[slot];
@@ -346,18 +359,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
             if (cls == kClsInt2) {
               KScales2 sc;
               k_scales2(blk, i, sc);
-#pragma unroll
+#pragma unroll 1
               for (int b = 0; b < 4; ++b) {
                 k_slot2(blk, 8 * b + rk, i, sc, w);
                 put(8 * b + rk, w);
               }
             } else if (cls == kClsInt4) {
-#pragma unroll
+#pragma unroll 1
               for (int b = 0; b < 4; ++b) {
                 k_slot4(blk, 8 * b + rk, i, w);
                 put(8 * b + rk, w);
               }
             } else {
+#pragma unroll 1
               for (int b = 0; b < 4; ++b) {
                 if (cls == kClsInt3) {
                   k_slot3(blk, 8 * b + rk, i, w);
@@ -379,18 +393,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
             };
             uint32_t w[4][4];
             if (cls == kClsInt2) {
-#pragma unroll
+#pragma unroll 1
               for (int gr = 0; gr < 4; ++gr) {
                 v_group2(blk, gr, rv, i, w);
                 put(gr, w);
               }
             } else if (cls == kClsInt4) {
-#pragma unroll
+#pragma unroll 1
               for (int gr = 0; gr < 4; ++gr) {
                 v_group4(blk, gr, rv, i, w);
                 put(gr, w);
               }
             } else {
+#pragma unroll 1
               for (int gr = 0; gr < 4; ++gr) {
                 if (cls == kClsInt3) {
                   v_group3(blk, gr, rv, i, w);
@@ -415,43 +430,54 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
           const uint16_t* src =
               list ? (is_k ? A.fpk : A.fpv) + ((size_t)u.req * A.hkv + u.kvh) * (size_t)A.fp_cap * kHeadDim
                    : (is_k ? A.k : A.v) + ((size_t)u.tok0 * A.hkv + u.kvh) * kHeadDim;
+          // rows past the end: the last row is loaded and used as 0 (loads without branches stay in flight together)
           if (is_k) {
 #pragma unroll 1
             for (int b = 0; b < 4; ++b) {
-              const int t = 8 * b + rk, j = j0 + t, nn = 32 * p + 8 * b + order8(rk);
+              const int j = j0 + 8 * b + rk, jc = min(j, n - 1), nn = 32 * p + 8 * b + order8(rk);
+              uint4 y[4];
 #pragma unroll
               for (int gr = 0; gr < 4; ++gr) {
-                uint32_t w[4] = {0u, 0u, 0u, 0u};
-                if (j < n) {
-                  const int ch = 4 * gr + i;
-                  const uint4 y = load8(src + (size_t)j * stride + 8 * (list ? ch ^ (j & 7) : ch), list || kal);
-                  order8_f16(y, 1.0f, w, bad);
-                }
+                const int ch = 4 * gr + i;
+                y[gr] = load8(src + (size_t)jc * stride + 8 * (list ? ch ^ (jc & 7) : ch), list || kal);
+              }
+#pragma unroll
+              for (int gr = 0; gr < 4; ++gr) {
+                uint32_t w[4];
+                if (j >= n) y[gr] = make_uint4(0u, 0u, 0u, 0u);
+                order8_f16(y[gr], 1.0f, w, bad);
                 *reinterpret_cast<uint4*>(dst + tile_off(128, nn, 4 * gr + i)) = make_uint4(w[0], w[1], w[2], w[3]);
               }
             }
           } else {
             // a lane takes channels (2 cp, 2 cp + 1) of 8 rows at a time
 #pragma unroll 1
-            for (int y = 0; y < 8; ++y) {
-              const int cp = lane + 32 * (y & 1), b = y >> 1;
-              float lo[8], hi[8];
+            for (int b = 0; b < 4; ++b) {
+              uint32_t y[2][8];
 #pragma unroll
-              for (int s = 0; s < 8; ++s) {
-                const int j = j0 + 8 * b + s;
-                uint32_t w = 0u;
-                if (j < n) {
-                  const uint16_t* q = src + (size_t)j * stride + (list ? att_list_at(j, 2 * cp) : 2 * cp);
-                  w = list || val ? __ldg(reinterpret_cast<const uint32_t*>(q))
-                                  : (uint32_t)__ldg(q) | ((uint32_t)__ldg(q + 1) << 16);
+              for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                  const int jc = min(j0 + 8 * b + s, n - 1), c = 2 * (lane + 32 * x);
+                  const uint16_t* q = src + (size_t)jc * stride + (list ? att_list_at(jc, c) : c);
+                  y[x][s] = list || val ? __ldg(reinterpret_cast<const uint32_t*>(q))
+                                        : (uint32_t)__ldg(q) | ((uint32_t)__ldg(q + 1) << 16);
                 }
-                lo[s] = in_range(bf_f(w & 0xFFFFu), bad);
-                hi[s] = in_range(__uint_as_float(w & 0xFFFF0000u), bad);
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const int c = 2 * (lane + 32 * x);
+                float lo[8], hi[8];
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                  const uint32_t w = j0 + 8 * b + s < n ? y[x][s] : 0u;
+                  lo[s] = in_range(bf_f(w & 0xFFFFu), bad);
+                  hi[s] = in_range(__uint_as_float(w & 0xFFFF0000u), bad);
+                }
+                *reinterpret_cast<uint4*>(dst + tile_off(128, c, 4 * p + b)) =
+                    make_uint4(f16x2(lo[0], lo[4]), f16x2(lo[1], lo[5]), f16x2(lo[2], lo[6]), f16x2(lo[3], lo[7]));
+                *reinterpret_cast<uint4*>(dst + tile_off(128, c + 1, 4 * p + b)) =
+                    make_uint4(f16x2(hi[0], hi[4]), f16x2(hi[1], hi[5]), f16x2(hi[2], hi[6]), f16x2(hi[3], hi[7]));
               }
-              *reinterpret_cast<uint4*>(dst + tile_off(128, 2 * cp, 4 * p + b)) =
-                  make_uint4(f16x2(lo[0], lo[4]), f16x2(lo[1], lo[5]), f16x2(lo[2], lo[6]), f16x2(lo[3], lo[7]));
-              *reinterpret_cast<uint4*>(dst + tile_off(128, 2 * cp + 1, 4 * p + b)) =
-                  make_uint4(f16x2(hi[0], hi[4]), f16x2(hi[1], hi[5]), f16x2(hi[2], hi[6]), f16x2(hi[3], hi[7]));
             }
           }
         }
@@ -465,26 +491,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
     // ------------------------------------------------------------------ MMA
     if (lane == 0) {
       constexpr uint32_t idesc = mma_idesc(128, 128);
-      const uint32_t qa[2] = {sm32(S.q[0]), sm32(S.q[1])};
+      // descriptors of the tiles; a K step of 16 is 32 bytes, a 64-element block 16384 (in units of 16 bytes)
+      const uint64_t qd0 = sw128_desc(sm32(S.q[0])), kd0 = sw128_desc(sm32(S.k[0])), vd0 = sw128_desc(sm32(S.v[0]));
+      constexpr uint32_t kTile16 = kTileBytes >> 4;
       uint32_t tc0 = 0;            // tiles before this item
+      uint32_t q_phase = 0;
       uint32_t p_phase = 0;        // bit x: phase of p_full[x]
       bool ok = true;
-      // S_x = Q K^T of tile number tc; block-major operands: 4 K steps of 16 per 64-channel block
+      // S_x = Q K^T of tile number tc
       auto qk = [&](int x, int qx, uint32_t tc) {
-        const uint32_t kb = sm32(S.k[tc & 1u]);
+        const uint64_t a = qd0 + (uint32_t)qx * kTile16, b = kd0 + (tc & 1u) * kTile16;
+        const uint32_t d = tmem + 128u * x;
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          const uint32_t off = (uint32_t)(s >> 2) * 16384u + (uint32_t)(s & 3) * 32u;
-          mma_ss(tmem + 128u * x, sw128_desc(qa[qx] + off), sw128_desc(kb + off), idesc, s > 0);
-        }
+        for (int s = 0; s < 8; ++s) mma_ss(d, a + ((s >> 2) * 1024 + (s & 3) * 2), b + ((s >> 2) * 1024 + (s & 3) * 2), idesc, s > 0);
       };
       auto pv = [&](int x, uint32_t tc, bool first) {
-        const uint32_t vb = sm32(S.v[tc & 1u]);
+        const uint64_t b = vd0 + (tc & 1u) * kTile16;
+        const uint32_t d = tmem + 256u + 128u * x, a = tmem + 128u * x;
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          const uint32_t off = (uint32_t)(s >> 2) * 16384u + (uint32_t)(s & 3) * 32u;
-          mma_ts(tmem + 256u + 128u * x, tmem + 128u * x + 8u * s, sw128_desc(vb + off), idesc, !first || s > 0);
-        }
+        for (int s = 0; s < 8; ++s) mma_ts(d, a + 8u * s, b + ((s >> 2) * 1024 + (s & 3) * 2), idesc, !first || s > 0);
       };
       auto k_ready = [&](uint32_t tc) { return mb_wait(&S.k_full[tc & 1u], (tc >> 1) & 1u, gave_up); };
       auto v_ready = [&](uint32_t tc) { return mb_wait(&S.v_full[tc & 1u], (tc >> 1) & 1u, gave_up); };
@@ -499,61 +524,33 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
         const Tiles T = tiles_of(A, u, I.row0, 256);
         const bool one = T.rows <= 128;
         const int n = I.tile1 - I.tile0;
-        ok = mb_wait(&S.q_full, (uint32_t)(it - i0) & 1u, gave_up);
-        if (!ok || n == 0) continue;
+        if (n == 0) continue;
+        ok = mb_wait(&S.q_full, q_phase, gave_up);
+        if (!ok) break;
+        q_phase ^= 1u;
         tm_fence_after();
-        if (!one) {
-          ok = k_ready(tc0);
-          if (!ok) break;
-          tm_fence_after();
-          for (int x = 0; x < 2; ++x) {
-            qk(x, x, tc0);
+        // Steps: two per tile (x = 0, 1), or one per tile with x = its parity (one).  Step y does P V of
+        // its S and then issues the next Q K^T into the same S, two steps ahead of it.
+        const int per = one ? 1 : 2, steps = n * per;
+#pragma unroll 1
+        for (int y = -2; y < steps && ok; ++y) {
+          const int x = y & 1;
+          if (y >= 0) {
+            const uint32_t tc = tc0 + (uint32_t)(one ? y : y >> 1);
+            ok = p_ready(x) && ((!one && x) || v_ready(tc));
+            if (!ok) break;
+            tm_fence_after();
+            pv(x, tc, y < 2);
+            if (one || x) tm_commit(&S.v_empty[tc & 1u]);
+          }
+          if (y + 2 < steps) {
+            const uint32_t tc = tc0 + (uint32_t)(one ? y + 2 : (y + 2) >> 1);
+            ok = (!one && x) || k_ready(tc);
+            if (!ok) break;
+            tm_fence_after();
+            qk(x, one ? 0 : x, tc);
             tm_commit(&S.s_full[x]);
-          }
-          tm_commit(&S.k_empty[tc0 & 1u]);
-          for (int t = 0; t < n && ok; ++t) {
-            const uint32_t tc = tc0 + t;
-            for (int x = 0; x < 2 && ok; ++x) {
-              ok = p_ready(x) && (x || v_ready(tc));
-              if (!ok) break;
-              tm_fence_after();
-              pv(x, tc, t == 0);
-              if (x) tm_commit(&S.v_empty[tc & 1u]);
-              if (t + 1 < n) {
-                ok = x || k_ready(tc + 1);
-                if (!ok) break;
-                tm_fence_after();
-                qk(x, x, tc + 1);
-                tm_commit(&S.s_full[x]);
-                if (x) tm_commit(&S.k_empty[(tc + 1) & 1u]);
-              }
-            }
-          }
-        } else {
-          for (int t = 0; t < 2 && t < n && ok; ++t) {
-            ok = k_ready(tc0 + t);
-            if (!ok) break;
-            tm_fence_after();
-            qk(t, 0, tc0 + t);
-            tm_commit(&S.s_full[t]);
-            tm_commit(&S.k_empty[(tc0 + t) & 1u]);
-          }
-          for (int t = 0; t < n && ok; ++t) {
-            const uint32_t tc = tc0 + t;
-            const int x = t & 1;
-            ok = p_ready(x) && v_ready(tc);
-            if (!ok) break;
-            tm_fence_after();
-            pv(x, tc, t < 2);
-            tm_commit(&S.v_empty[tc & 1u]);
-            if (t + 2 < n) {
-              ok = k_ready(tc + 2);
-              if (!ok) break;
-              tm_fence_after();
-              qk(x, 0, tc + 2);
-              tm_commit(&S.s_full[x]);
-              tm_commit(&S.k_empty[tc & 1u]);
-            }
+            if (one || x) tm_commit(&S.k_empty[tc & 1u]);
           }
         }
         if (ok) tm_commit(&S.o_full);
@@ -591,6 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
           ok = mb_wait(&S.raw_empty[slot], ((c / kRing) & 1u) ^ 1u, gave_up);
           if (ok) {
             *(volatile int32_t*)&S.cls[slot] = cls;
+            *(volatile uint32_t*)&S.seq[slot] = c;
             *(volatile uint32_t*)&S.live[page_tiles & (kMaskRing - 1)][lane] = order_bits(e.live);
             ++issued;
             if (cls < 0)
