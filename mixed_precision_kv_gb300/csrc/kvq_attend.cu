@@ -83,7 +83,7 @@ cudaError_t launch_attend_merge(kv_pool* P, const AttArgs& A, const AttUnit* d_u
 // ---- work plan ---------------------------------------------------------
 struct AttPlan {
   std::vector<AttItem> items;
-  std::vector<int32_t> cta_item{0};
+  std::vector<int32_t> cta_item;   // per group of units: first item of every CTA, and the end
   std::vector<AttMerge> merges;
   int64_t n_parts = 0;
   int merge_rows = 0;
@@ -95,18 +95,18 @@ int block_tiles(const AttUnit& u, int g, int row0, int rows, bool kv, bool tree)
   return (u.n_pages + 3) / 4 + (u.n_fp + 127) / 128 + (kv ? (tree ? u.T - 1 : t_last) / 128 + 1 : 0);
 }
 
-// Blocks of kWideRows rows, their tiles in one line of cost, cut into equal
-// runs, one per CTA (a run may end inside a block: its pieces are merged).  A
-// tile of a block of more than 128 rows costs 2, else 1 (the MMAs' time); an
-// item 1 more for its first and last steps.
+// Blocks of kWideRows rows of units [u0, u1), their tiles in one line of cost,
+// cut into equal runs, one per CTA (a run may end inside a block: its pieces are
+// merged).  A tile of a block of more than 128 rows costs 2, else 1 (the MMAs'
+// time); an item 1 more for its first and last steps.
 constexpr int kWideRows = 256;
-void plan_wide(const std::vector<AttUnit>& units, int g, bool kv, bool tree, int ctas, AttPlan& out) {
+void plan_wide(const std::vector<AttUnit>& units, int u0, int u1, int g, bool kv, bool tree, int ctas, AttPlan& out) {
   struct Block {
     int unit, row0, rows, tiles, cost;
   };
   std::vector<Block> blocks;
   int64_t total = 0;
-  for (int x = 0; x < (int)units.size(); ++x) {
+  for (int x = u0; x < u1; ++x) {
     const int rows = units[(size_t)x].T * g;
     for (int r = 0; r < rows; r += kWideRows) {
       const int n = std::min(kWideRows, rows - r);
@@ -118,6 +118,7 @@ void plan_wide(const std::vector<AttUnit>& units, int g, bool kv, bool tree, int
   const double share = (double)(total + ctas) / ctas;   // every CTA ends inside a block once
   double done = 0.0;
   int cta = 0;
+  out.cta_item.push_back((int32_t)out.items.size());
   for (const Block& b : blocks) {
     const size_t first = out.items.size();
     int t = 0;
@@ -153,6 +154,10 @@ void plan_wide(const std::vector<AttUnit>& units, int g, bool kv, bool tree, int
   }
   out.cta_item.push_back((int32_t)out.items.size());
 }
+
+// Units taken together: their operand tiles stay in L2 (126 MB, shared with
+// the rows of q and out) while every block of rows reads them.
+constexpr int64_t kTilesInL2 = 1100;   // 72 MB
 
 }  // namespace
 }  // namespace kvq
@@ -233,7 +238,27 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
     return KV_OK;
   }
   AttPlan pl;
-  plan_wide(units, g, k != nullptr, tree != nullptr, P->sm_count, pl);
+  struct Group {
+    int u0, u1, max_tiles, cta0, ctas;
+  };
+  std::vector<Group> groups;
+  int64_t most = 0;
+  for (int u0 = 0; u0 < (int)units.size();) {
+    int u1 = u0, max_tiles = 0;
+    int64_t n = 0;
+    for (; u1 < (int)units.size(); ++u1) {
+      const int t = block_tiles(units[(size_t)u1], g, 0, units[(size_t)u1].T * g, k != nullptr, tree != nullptr);
+      if (u1 > u0 && n + t > kTilesInL2) break;
+      units[(size_t)u1].tile_base = (int32_t)n;
+      n += t;
+      max_tiles = std::max(max_tiles, t);
+    }
+    const int cta0 = (int)pl.cta_item.size();
+    plan_wide(units, u0, u1, g, k != nullptr, tree != nullptr, P->sm_count, pl);
+    groups.push_back(Group{u0, u1, max_tiles, cta0, (int)pl.cta_item.size() - cta0 - 1});
+    most = std::max(most, n);
+    u0 = u1;
+  }
   Upload u;
   const size_t ou = u.add(units.data(), units.size() * sizeof(AttUnit));
   const size_t oi = u.add(pl.items.data(), pl.items.size() * sizeof(AttItem));
@@ -241,12 +266,17 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
   const size_t om = u.add(pl.merges.data(), pl.merges.size() * sizeof(AttMerge));
   const size_t op = (u.size + 255) & ~size_t(255);
   if ((st = ensure(P->attend, op + (size_t)pl.n_parts * 128 * kAttPart * sizeof(float))) != KV_OK) return st;
+  if ((st = ensure(P->attend_tiles, (size_t)most * (kAttTileBytes + 16))) != KV_OK) return st;
   if ((st = h2d(P, P->attend.ptr, u, s)) != KV_OK) return st;
   const uint8_t* base = (const uint8_t*)P->attend.ptr;
   const AttUnit* du = (const AttUnit*)(base + ou);
   float* d_part = (float*)((uint8_t*)P->attend.ptr + op);
-  KV_CUDA(launch_attend_wide(P, A, du, (const AttItem*)(base + oi), (const int32_t*)(base + oc),
-                             (int)pl.cta_item.size() - 1, d_part, s));
+  uint32_t* d_live = (uint32_t*)((uint8_t*)P->attend_tiles.ptr + (size_t)most * kAttTileBytes);
+  for (const Group& G : groups) {
+    KV_CUDA(launch_attend_tiles(P, A, du + G.u0, G.u1 - G.u0, G.max_tiles, P->attend_tiles.ptr, d_live, s));
+    KV_CUDA(launch_attend_wide(P, A, du, (const AttItem*)(base + oi), (const int32_t*)(base + oc) + G.cta0, G.ctas,
+                               P->attend_tiles.ptr, d_live, d_part, s));
+  }
   if (!pl.merges.empty())
     KV_CUDA(launch_attend_merge(P, A, du, (const AttMerge*)(base + om), (int)pl.merges.size(), pl.merge_rows, d_part, 128, s));
   return KV_OK;

@@ -14,7 +14,7 @@ struct AttUnit {
   int32_t T;          // new tokens
   int32_t n_pages;    // table entries
   int32_t n_fp;       // full-precision list tokens
-  int32_t pad;
+  int32_t tile_base;  // wide kernel: the unit's first operand tile pair
   int64_t tok0;       // the request's first row in q, k, v and out
 };
 
@@ -77,10 +77,15 @@ __device__ __forceinline__ int att_list_at(int t, int c) { return (((c >> 3) ^ (
 cudaError_t launch_attend_simt(kv_pool* P, const AttArgs& A, const AttUnit* d_units, int n_units, int max_rows,
                                cudaStream_t s);
 
-// Tensor-core kernel for many rows per unit (kvq_attend_wide.cu): blocks of 256
-// rows, partials of 128 rows, two per item (rows 0..127 and 128..255; for a
-// block of at most 128 rows, the same rows over even and over odd tiles).
+// Tensor-core kernels for many rows per unit (kvq_attend_wide.cu): the units' keys
+// as operand tiles (64 KB and four live words per 128 keys), then blocks of 256
+// rows over them.  Partials of 128 rows, two per item (rows 0..127 and 128..255;
+// for a block of at most 128 rows, the same rows over even and over odd tiles).
+constexpr size_t kAttTileBytes = 65536;
+cudaError_t launch_attend_tiles(kv_pool* P, const AttArgs& A, const AttUnit* d_units, int n_units, int max_tiles,
+                                void* d_tiles, uint32_t* d_live, cudaStream_t s);
 cudaError_t launch_attend_wide(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const AttItem* d_items,
-                               const int32_t* d_cta_item, int n_ctas, float* d_part, cudaStream_t s);
+                               const int32_t* d_cta_item, int n_ctas, const void* d_tiles, const uint32_t* d_live,
+                               float* d_part, cudaStream_t s);
 
 }  // namespace kvq

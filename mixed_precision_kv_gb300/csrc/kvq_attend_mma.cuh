@@ -69,6 +69,12 @@ __device__ __forceinline__ void bulk_to_smem(void* dst, const void* src, uint32_
                ::"r"(sm32(dst)), "l"(src), "r"(bytes), "r"(sm32(b)) : "memory");
 }
 
+// ---- registers of a warpgroup (all its warps) ------------------------------
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // ---- tcgen05 ---------------------------------------------------------------
 __device__ __forceinline__ void tm_alloc(uint32_t* slot, uint32_t cols) {   // one warp
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm32(slot)), "r"(cols) : "memory");
@@ -128,10 +134,11 @@ __device__ __forceinline__ void tm_ld<32>(uint32_t (&r)[32], uint32_t addr) {
                  "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
                : "r"(addr));
 }
-template <>
-__device__ __forceinline__ void tm_ld<64>(uint32_t (&r)[64], uint32_t addr) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+// 32 columns into r[kAt ..] of a longer array
+template <int kAt, int N>
+__device__ __forceinline__ void tm_ld32_at(uint32_t (&r)[N], uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=r"(r[kAt+0]), "=r"(r[kAt+1]), "=r"(r[kAt+2]), "=r"(r[kAt+3]), "=r"(r[kAt+4]), "=r"(r[kAt+5]), "=r"(r[kAt+6]), "=r"(r[kAt+7]), "=r"(r[kAt+8]), "=r"(r[kAt+9]), "=r"(r[kAt+10]), "=r"(r[kAt+11]), "=r"(r[kAt+12]), "=r"(r[kAt+13]), "=r"(r[kAt+14]), "=r"(r[kAt+15]), "=r"(r[kAt+16]), "=r"(r[kAt+17]), "=r"(r[kAt+18]), "=r"(r[kAt+19]), "=r"(r[kAt+20]), "=r"(r[kAt+21]), "=r"(r[kAt+22]), "=r"(r[kAt+23]), "=r"(r[kAt+24]), "=r"(r[kAt+25]), "=r"(r[kAt+26]), "=r"(r[kAt+27]), "=r"(r[kAt+28]), "=r"(r[kAt+29]), "=r"(r[kAt+30]), "=r"(r[kAt+31])
                : "r"(addr));
 }
 template <int N>
@@ -233,34 +240,27 @@ __device__ __forceinline__ uint32_t order_bits(uint32_t m) {
 
 // ---- K of a page: slot t, channels 32 gr + 8 i .. + 7 for gr = 0..3 --------
 // out[gr][k] = channels (k, k + 4) of that run.
-struct KScales2 {   // INT2: scale and zero pairs of the lane's channels (the same for every slot)
-  uint32_t s[4][4], z[4][4];
-};
-__device__ __forceinline__ void k_scales2(const uint8_t* blk, int i, KScales2& S) {
+// INT2: the scale and zero pairs of run (gr, i) are the same for every slot.
+__device__ __forceinline__ void k_scales2(const uint8_t* blk, int gr, int i, uint32_t (&sc)[4], uint32_t (&z)[4]) {
   const uint32_t sel = (i & 1) ? 0x7632u : 0x5410u, sel0 = (i & 1) ? 0x7610u : 0x5432u;   // pair 0 is stored swapped
-#pragma unroll
-  for (int gr = 0; gr < 4; ++gr) {
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const uint4* p = reinterpret_cast<const uint4*>(blk + kI2KMeta + 256 * x + 4 * ((gr * 2 + (i >> 1)) * 8));
-      const uint4 a = p[0], b = p[1];
-      uint32_t* d = x ? S.z[gr] : S.s[gr];
-      d[0] = __byte_perm(a.x, b.x, sel0);
-      d[1] = __byte_perm(a.y, b.y, sel);
-      d[2] = __byte_perm(a.z, b.z, sel);
-      d[3] = __byte_perm(a.w, b.w, sel);
-    }
-  }
+  const uint4* p = reinterpret_cast<const uint4*>(blk + kI2KMeta + 4 * ((gr * 2 + (i >> 1)) * 8));
+  const uint4 a = p[0], b = p[1], c = p[16], d = p[17];   // zeros 256 bytes on
+  sc[0] = __byte_perm(a.x, b.x, sel0);
+  sc[1] = __byte_perm(a.y, b.y, sel);
+  sc[2] = __byte_perm(a.z, b.z, sel);
+  sc[3] = __byte_perm(a.w, b.w, sel);
+  z[0] = __byte_perm(c.x, d.x, sel0);
+  z[1] = __byte_perm(c.y, d.y, sel);
+  z[2] = __byte_perm(c.z, d.z, sel);
+  z[3] = __byte_perm(c.w, d.w, sel);
 }
-__device__ __forceinline__ void k_slot2(const uint8_t* blk, int t, int i, const KScales2& S, uint32_t (&out)[4][4]) {
+__device__ __forceinline__ void k_run2(const uint8_t* blk, int t, int gr, int i, const uint32_t (&sc)[4],
+                                       const uint32_t (&z)[4], uint32_t (&out)[4]) {
+  const uint32_t h = *reinterpret_cast<const uint16_t*>(blk + kI2KCodes + 32 * t + 8 * gr + 2 * i);
+  uint32_t c[4];
+  crumbs(__byte_perm(h, 0u, 0x4140u), c);
 #pragma unroll
-  for (int gr = 0; gr < 4; ++gr) {
-    const uint32_t h = *reinterpret_cast<const uint16_t*>(blk + kI2KCodes + 32 * t + 8 * gr + 2 * i);
-    uint32_t c[4];
-    crumbs(__byte_perm(h, 0u, 0x4140u), c);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) out[gr][k] = hfma2u(c[k], S.s[gr][k], S.z[gr][k]);
-  }
+  for (int k = 0; k < 4; ++k) out[k] = hfma2u(c[k], sc[k], z[k]);
 }
 __device__ __forceinline__ void k_slot4(const uint8_t* blk, int t, int i, uint32_t (&out)[4][4]) {
   const uint4 w = *reinterpret_cast<const uint4*>(blk + kI4KCodes + 64 * t + 16 * i);

@@ -1,8 +1,18 @@
-// kv_attend for many rows per unit (chunks of a prompt, wide trees): tcgen05
-// attention with the cache dequantized on the way into shared memory.
+// kv_attend for many rows per unit (chunks of a prompt): the cache is
+// dequantized once per call into operand tiles, then tcgen05 attention runs over
+// the tiles.
 //
-// A CTA takes an item: a block of up to 256 rows of one (request, kv head) unit
-// and a run of its key tiles (128 keys: four pages, or bf16 rows).  Per tile
+// attend_tiles_kernel turns every 128 keys of a (request, kv head) unit (four
+// pages, or bf16 rows of the list or of the new tokens) into one K and one V
+// operand tile, 32 KB each, in the very layout that the MMAs read from shared
+// memory (V transposed), and the keys' live bits into four words.  Every block of
+// 256 rows reads the tiles again (from L2: the units of a call are taken in
+// groups whose tiles fit there), so this costs one pass over the pages for any
+// number of blocks.  Dequantizing inside the attention kernel instead cost eight
+// warps' issue slots per block: 2.72 ms against the present figure below.
+//
+// attend_wide_kernel: a CTA takes an item: a block of up to 256 rows of a unit
+// and a run of its tiles.  Per tile
 //     S_x = Q_x K^T          (x = 0, 1: 128 rows each; 128 x 128 x 128)
 //     P_x = 2^(S_x rf - m)   (rf: softmax scale, log2 e and the row's power of two)
 //     O_x += P_x V           (P_x read from TMEM)
@@ -11,17 +21,16 @@
 // (the sums are fp32 and P is binary16 with 2^7 of headroom below 65504, so a
 // stale maximum loses nothing).
 //
-// Roles (18 warps): two warpgroups hold one row per thread of S_0 / S_1; eight
-// warps dequantize (a page's K or V each); one thread issues every MMA; one
-// warp streams page blocks with bulk copies through a ring of six pages.
-// While one warpgroup works on its S, the tensor cores work for the other.  A
-// block of at most 128 rows uses the two warpgroups for even and odd tiles
-// instead (the same rows, two partial states).
+// Roles: two warpgroups hold one row per thread of S_0 / S_1; one thread per x
+// issues the MMAs of S_x and O_x; one thread streams tiles through a ring of
+// five.  While one warpgroup works on its S, the tensor cores work for the other;
+// two issuing threads, because the waits and commits between runs of MMAs cost one
+// thread 600 of every 1650 cycles.  A block of at most 128 rows uses the two
+// warpgroups for even and odd tiles instead (the same rows, two partial states).
 //
-// What bounds it: per tile and 256 rows the tensor cores need 2048 cycles, the
-// operand reads and writes of shared memory about as many, exponentials
-// 32768 / (SM rate); the CTA's shared memory (Q, two K and two V tiles) leaves
-// one CTA per SM.
+// What bounds it: per tile and 256 rows the tensor cores need 2048 cycles, their
+// operand reads of shared memory 1536; the exponentials 1024; the CTA's shared
+// memory (Q and five tiles) leaves one CTA per SM.
 #include <algorithm>
 #include <atomic>
 
@@ -30,45 +39,210 @@
 namespace kvq {
 namespace {
 
-constexpr int kRing = 6;                        // pages in flight
-constexpr int kWarps = 18;
+constexpr int kRing = 5;                        // K and V tiles in flight
+constexpr int kWarps = 12;                      // the last one idle
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTileBytes = 128 * 128 * 2;
-constexpr int kMaskRing = 8;                    // tiles whose live words are kept
 constexpr float kHead = 7.0f;                   // P = 2^(x - m + 7)
 constexpr float kGrow = 8.0f;                   // a maximum may be stale by this much (base 2)
 constexpr float kNever = -3.0e38f;              // S of a key that is not seen
 
 struct alignas(1024) WideSmem {
-  uint8_t q[2][kTileBytes], k[2][kTileBytes], v[2][kTileBytes];
-  alignas(128) uint8_t raw[kRing][kInt4Block];
-  uint32_t live[kMaskRing][4];
-  int32_t cls[kRing];
-  uint32_t seq[kRing];                          // the page number a slot was last filled for
-  uint64_t raw_full[kRing], raw_empty[kRing];
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t q_full, s_full[2], p_full[2], o_full, drain;
+  uint8_t q[2][kTileBytes], kv[kRing][kTileBytes];
+  uint64_t full[kRing], empty[kRing];
+  uint64_t q_full, s_full[2], p_full[2], o_full, drain[2];
   uint32_t tmem, gave_up;
 };
 static_assert(sizeof(WideSmem) <= 232448, "one CTA's shared memory");
 
 struct Tiles {   // an item's tiles: [0, pages), [pages, lists), [lists, all) by kind
-  int pages, lists, all, t_last, rows;
+  int pages, lists, all, rows;
 };
-__device__ __forceinline__ Tiles tiles_of(const AttArgs& A, const AttUnit& u, int row0, int block) {
+__device__ __forceinline__ Tiles tiles_of(const AttArgs& A, const AttUnit& u, int row0, int rows) {
   Tiles t;
   const int g = A.hq / A.hkv;
-  t.rows = min(block, u.T * g - row0);
-  t.t_last = (row0 + t.rows - 1) / g;
+  t.rows = min(rows, u.T * g - row0);
   t.pages = (u.n_pages + 3) >> 2;
   t.lists = t.pages + ((u.n_fp + 127) >> 7);
-  t.all = t.lists + (!A.k ? 0 : (((A.tree ? u.T - 1 : t.t_last) >> 7) + 1));
+  t.all = t.lists + (!A.k ? 0 : (((A.tree ? u.T - 1 : (row0 + t.rows - 1) / g) >> 7) + 1));
   return t;
+}
+
+// One CTA of eight warps per tile: warp p takes page (or 32 rows) p of K, warp
+// 4 + p of V.  Bound by memory: 64 KB written per 12 to 20 KB read.
+__global__ void __launch_bounds__(256) attend_tiles_kernel(AttArgs A, const AttUnit* __restrict__ units,
+                                                           uint8_t* __restrict__ tiles, uint32_t* __restrict__ live) {
+  const AttUnit u = units[blockIdx.y];
+  const Tiles T = tiles_of(A, u, 0, 1 << 30);
+  const int tile = blockIdx.x;
+  if (tile >= T.all) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool is_k = warp < 4;
+  const int p = warp & 3;
+  uint8_t* const dst = tiles + ((size_t)(u.tile_base + tile) * 2 + (is_k ? 0 : 1)) * kTileBytes;
+  uint32_t bad = 0u;
+  const int rk = lane >> 2, rv = rk, i = lane & 3;   // slots r of runs i
+  if (tile < T.pages) {
+    const int pi = 4 * tile + p;
+    Entry e{-1, 0u};
+    int cls = -1;
+    const uint8_t* blk = nullptr;
+    if (pi < u.n_pages) {
+      e = A.table[(size_t)u.req * A.max_pages + pi];
+      if (A.hdead) e.live &= ~A.hdead[(size_t)e.id * A.hkv + u.kvh];
+      if (e.live) cls = att_page(A, e.id, u.kvh, blk);
+    }
+    if (is_k && lane == 0) live[(size_t)(u.tile_base + tile) * 4 + p] = order_bits(e.live);
+    {
+          if (is_k) {
+            auto put = [&](int t, const uint32_t (&w)[4][4]) {
+              const int n = 32 * p + (t & ~7) + order8(t & 7);
+#pragma unroll
+              for (int gr = 0; gr < 4; ++gr)
+                *reinterpret_cast<uint4*>(dst + tile_off(128, n, 4 * gr + i)) =
+                    make_uint4(w[gr][0], w[gr][1], w[gr][2], w[gr][3]);
+            };
+            uint32_t w[4][4];
+            if (cls == kClsInt2) {
+#pragma unroll 1
+              for (int gr = 0; gr < 4; ++gr) {
+                uint32_t sc[4], z[4];
+                k_scales2(blk, gr, i, sc, z);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                  uint32_t y[4];
+                  k_run2(blk, 8 * b + rk, gr, i, sc, z, y);
+                  *reinterpret_cast<uint4*>(dst + tile_off(128, 32 * p + 8 * b + order8(rk), 4 * gr + i)) =
+                      make_uint4(y[0], y[1], y[2], y[3]);
+                }
+              }
+            } else if (cls == kClsInt4) {
+#pragma unroll 1
+              for (int b = 0; b < 4; ++b) {
+                k_slot4(blk, 8 * b + rk, i, w);
+                put(8 * b + rk, w);
+              }
+            } else {
+#pragma unroll 1
+              for (int b = 0; b < 4; ++b) {
+                if (cls == kClsInt3) {
+                  k_slot3(blk, 8 * b + rk, i, w);
+                } else if (cls == kClsFp4) {
+                  k_slotf(blk, 8 * b + rk, i, w);
+                } else {
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) w[x >> 2][x & 3] = 0u;
+                }
+                put(8 * b + rk, w);
+              }
+            }
+          } else {
+            auto put = [&](int gr, const uint32_t (&w)[4][4]) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<uint4*>(dst + tile_off(128, 32 * gr + 8 * x + rv, 4 * p + i)) =
+                    make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
+            };
+            uint32_t w[4][4];
+            if (cls == kClsInt2) {
+#pragma unroll 1
+              for (int gr = 0; gr < 4; ++gr) {
+                v_group2(blk, gr, rv, i, w);
+                put(gr, w);
+              }
+            } else if (cls == kClsInt4) {
+#pragma unroll 1
+              for (int gr = 0; gr < 4; ++gr) {
+                v_group4(blk, gr, rv, i, w);
+                put(gr, w);
+              }
+            } else {
+#pragma unroll 1
+              for (int gr = 0; gr < 4; ++gr) {
+                if (cls == kClsInt3) {
+                  v_group3(blk, gr, rv, i, w);
+                } else if (cls == kClsFp4) {
+                  v_groupf(blk, gr, rv, i, w);
+                } else {
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) w[x >> 2][x & 3] = 0u;
+                }
+                put(gr, w);
+              }
+            }
+          }
+    }
+  } else {
+    const bool kal = (((uintptr_t)A.k | (uintptr_t)A.v) & 15) == 0;
+    const bool val = (((uintptr_t)A.k | (uintptr_t)A.v) & 3) == 0;
+    {
+          // ---- 32 bf16 rows: list tokens or new tokens
+          const bool list = tile < T.lists;
+          const int j0 = 128 * (tile - (list ? T.pages : T.lists)) + 32 * p;   // first row of this warp
+          const int n = list ? u.n_fp : u.T;
+          const size_t stride = list ? kHeadDim : (size_t)A.hkv * kHeadDim;
+          const uint16_t* src =
+              list ? (is_k ? A.fpk : A.fpv) + ((size_t)u.req * A.hkv + u.kvh) * (size_t)A.fp_cap * kHeadDim
+                   : (is_k ? A.k : A.v) + ((size_t)u.tok0 * A.hkv + u.kvh) * kHeadDim;
+          // rows past the end: the last row is loaded and used as 0 (loads without branches stay in flight together)
+          if (is_k) {
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+              const int j = j0 + 8 * b + rk, jc = min(j, n - 1), nn = 32 * p + 8 * b + order8(rk);
+              uint4 y[4];
+#pragma unroll
+              for (int gr = 0; gr < 4; ++gr) {
+                const int ch = 4 * gr + i;
+                y[gr] = load8(src + (size_t)jc * stride + 8 * (list ? ch ^ (jc & 7) : ch), list || kal);
+              }
+#pragma unroll
+              for (int gr = 0; gr < 4; ++gr) {
+                uint32_t w[4];
+                if (j >= n) y[gr] = make_uint4(0u, 0u, 0u, 0u);
+                order8_f16(y[gr], 1.0f, w, bad);
+                *reinterpret_cast<uint4*>(dst + tile_off(128, nn, 4 * gr + i)) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          } else {
+            // a lane takes channels (2 cp, 2 cp + 1) of 8 rows at a time
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+              uint32_t y[2][8];
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                  const int jc = min(j0 + 8 * b + s, n - 1), c = 2 * (lane + 32 * x);
+                  const uint16_t* q = src + (size_t)jc * stride + (list ? att_list_at(jc, c) : c);
+                  y[x][s] = list || val ? __ldg(reinterpret_cast<const uint32_t*>(q))
+                                        : (uint32_t)__ldg(q) | ((uint32_t)__ldg(q + 1) << 16);
+                }
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const int c = 2 * (lane + 32 * x);
+                float lo[8], hi[8];
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                  const uint32_t w = j0 + 8 * b + s < n ? y[x][s] : 0u;
+                  lo[s] = in_range(bf_f(w & 0xFFFFu), bad);
+                  hi[s] = in_range(__uint_as_float(w & 0xFFFF0000u), bad);
+                }
+                *reinterpret_cast<uint4*>(dst + tile_off(128, c, 4 * p + b)) =
+                    make_uint4(f16x2(lo[0], lo[4]), f16x2(lo[1], lo[5]), f16x2(lo[2], lo[6]), f16x2(lo[3], lo[7]));
+                *reinterpret_cast<uint4*>(dst + tile_off(128, c + 1, 4 * p + b)) =
+                    make_uint4(f16x2(hi[0], hi[4]), f16x2(hi[1], hi[5]), f16x2(hi[2], hi[6]), f16x2(hi[3], hi[7]));
+              }
+            }
+          }
+    }
+  }
+  if (bad) atomicOr(A.status, kStatusRange);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
     AttArgs A, const AttUnit* __restrict__ units, const AttItem* __restrict__ items, const int32_t* __restrict__ cta_item,
-    float* __restrict__ part, uint32_t first_spins) {
+    const uint8_t* __restrict__ tiles, const uint32_t* __restrict__ live, float* __restrict__ part,
+    uint32_t first_spins) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   WideSmem& S = *reinterpret_cast<WideSmem*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -76,25 +250,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
   volatile uint32_t* gave_up = &S.gave_up;
   if (tid == 0) {
     for (int x = 0; x < kRing; ++x) {
-      mb_init(&S.raw_full[x], 1);
-      mb_init(&S.raw_empty[x], 2);
-      S.seq[x] = 0xFFFFFFFFu;
+      mb_init(&S.full[x], 1);
+      mb_init(&S.empty[x], 2);
     }
     for (int x = 0; x < 2; ++x) {
-      mb_init(&S.k_full[x], 4);
-      mb_init(&S.k_empty[x], 1);
-      mb_init(&S.v_full[x], 4);
-      mb_init(&S.v_empty[x], 1);
       mb_init(&S.s_full[x], 1);
       mb_init(&S.p_full[x], 4);
+      mb_init(&S.drain[x], 1);
     }
     mb_init(&S.q_full, 8);
-    mb_init(&S.o_full, 1);
-    mb_init(&S.drain, 1);
+    mb_init(&S.o_full, 2);
     S.gave_up = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 16) tm_alloc(&S.tmem, 512);
+  if (warp == 8) tm_alloc(&S.tmem, 512);
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
@@ -107,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
     const int rt = tid & 127;
     const uint32_t tl = tmem + ((uint32_t)(warp & 3) << 21);   // the warp's 32 TMEM lanes
     const uint32_t ts = tl + 128u * x, to = tl + 256u + 128u * x;
-    uint32_t page_tiles = 0, s_phase = 0, o_phase = 0, bad = 0u;
+    uint32_t s_phase = 0, o_phase = 0, bad = 0u;
     bool ok = true;
     const bool qal = ((uintptr_t)A.q & 15) == 0;
     for (int it = i0; it < i1 && ok; ++it) {
@@ -164,19 +333,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
       bool any = false;                                    // O_x has been written in this item
       for (int tile = I.tile0; tile < I.tile1; ++tile) {
         const bool page = tile < T.pages;
-        const uint32_t pt = page_tiles;
-        page_tiles += page ? 1u : 0u;
         if (one && ((tile - I.tile0) & 1) != x) continue;
         // ---- keys this row sees, 128 bits in the tiles' order
         uint32_t mk[4];
+        if (page) {
+          const uint4 lv = __ldg(reinterpret_cast<const uint4*>(live) + u.tile_base + tile);   // before the wait below
+          mk[0] = lv.x; mk[1] = lv.y; mk[2] = lv.z; mk[3] = lv.w;
+        }
         ok = __all_sync(0xFFFFFFFFu, mb_wait(&S.s_full[x], s_phase, gave_up));
         if (!ok) break;
         s_phase ^= 1u;
         tm_fence_after();
-        if (page) {
-          const volatile uint32_t* lv = S.live[pt & (kMaskRing - 1)];
-          mk[0] = lv[0]; mk[1] = lv[1]; mk[2] = lv[2]; mk[3] = lv[3];
-        } else {
+        if (!page) {
           const bool list = tile < T.lists;
           const int base = 128 * (tile - (list ? T.pages : T.lists));
           // keys [base, base + n) are seen (with a tree, those of its bits)
@@ -189,8 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
             mk[w] = order_bits(b);
           }
         }
-        // Keys that are not seen become kNever in S, so that the code below needs no masks (the hot code
-        // has to stay small: every warp of an SM runs its own part of it, and fetching it was the limit).
+        // Keys that are not seen become kNever in S, so that the code below needs no masks.
         if (!__all_sync(0xFFFFFFFFu, (mk[0] & mk[1] & mk[2] & mk[3]) == 0xFFFFFFFFu)) {
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
@@ -205,15 +372,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
           tm_wait_st();
         }
         // ---- maximum
-        float mx = kNever;
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          uint32_t s[64];
-          tm_ld<64>(s, ts + 64u * c);
-          tm_wait_ld();
+        uint32_t sv[128];
+        tm_ld32_at<0>(sv, ts);
+        tm_ld32_at<32>(sv, ts + 32u);
+        tm_ld32_at<64>(sv, ts + 64u);
+        tm_ld32_at<96>(sv, ts + 96u);
+        tm_wait_ld();
+        float mq[4] = {kNever, kNever, kNever, kNever};
 #pragma unroll
-          for (int j = 0; j < 64; j += 2) mx = fmaxf(fmaxf(mx, __uint_as_float(s[j])), __uint_as_float(s[j + 1]));
-        }
+        for (int j = 0; j < 128; j += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            mq[y] = fmaxf(fmaxf(mq[y], __uint_as_float(sv[j + 2 * y])), __uint_as_float(sv[j + 2 * y + 1]));
+        float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
         mx = mx > 0.9f * kNever ? mx * rf : -INFINITY;
         const bool grow = mx > m + kGrow || (m == -INFINITY && mx > -INFINITY);
         if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -235,24 +406,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
         any = true;
         // ---- weights (a row that has seen nothing: every weight is 2^(kNever rf) = 0)
         const float nm = m == -INFINITY ? 0.0f : kHead - m;
-        float l0 = 0.0f, l1 = 0.0f;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t s[32], p[16];
-          tm_ld<32>(s, ts + 32u * c);
-          tm_wait_ld();
+        float l0 = 0.0f, l1 = 0.0f, l2 = 0.0f, l3 = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            float a, b;
-            fma2(a, b, __uint_as_float(s[j]), __uint_as_float(s[j + 1]), rf, rf, nm, nm);
-            a = ex2f(a);
-            b = ex2f(b);
-            add2f(l0, l1, a, b);
-            p[j >> 1] = f16x2(a, b);
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            float a[4];
+#pragma unroll
+            for (int y = 0; y < 4; y += 2) {
+              fma2(a[y], a[y + 1], __uint_as_float(sv[32 * c + j + y]), __uint_as_float(sv[32 * c + j + y + 1]), rf, rf, nm, nm);
+              a[y] = ex2f(a[y]);
+              a[y + 1] = ex2f(a[y + 1]);
+              p[(j + y) >> 1] = f16x2(a[y], a[y + 1]);
+            }
+            add2f(l0, l1, a[0], a[1]);
+            add2f(l2, l3, a[2], a[3]);
           }
           tm_st<16>(ts + 16u * c, p);   // over columns that have been read
         }
-        l += l0 + l1;
+        l += (l0 + l1) + (l2 + l3);
         tm_wait_st();
         tm_fence_before();
         __syncwarp();
@@ -313,244 +486,74 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
       if (!whole && valid) *reinterpret_cast<float2*>(pp + kHeadDim) = make_float2(m, l);
     }
     if (bad) atomicOr(A.status, kStatusRange);
-  } else if (warp < 16) {
-    // ----------------------------------------------------------- dequantize
-    const bool is_k = warp < 12;
-    const int p = warp & 3;                                // page (or 32 rows) of the tile
-    // slots r, channels' / slots' run i of this lane: 8 lanes of a shared-memory
-    // phase read 128 different bytes and write 8 different chunk positions
-    const int qd = lane >> 3, hf = (lane >> 2) & 1, i = lane & 3;
-    const int rk = ((qd & 1) | ((qd & 2) << 1)) ^ (3 * hf), rv = qd ^ (5 * hf);
-    uint32_t page_tiles = 0, tc = 0, bad = 0u;
-    const bool kal = (((uintptr_t)A.k | (uintptr_t)A.v) & 15) == 0;
-    const bool val = (((uintptr_t)A.k | (uintptr_t)A.v) & 3) == 0;
-    bool ok = true;
-    uint64_t* full = is_k ? S.k_full : S.v_full;
-    uint64_t* empty = is_k ? S.k_empty : S.v_empty;
-    for (int it = i0; it < i1 && ok; ++it) {
-      const AttItem I = items[it];
-      const AttUnit u = units[I.unit];
-      const Tiles T = tiles_of(A, u, I.row0, 256);
-      for (int tile = I.tile0; tile < I.tile1; ++tile, ++tc) {
-        const uint32_t st = tc & 1u;
-        uint8_t* dst = is_k ? S.k[st] : S.v[st];
-        ok = __all_sync(0xFFFFFFFFu, mb_wait(&empty[st], ((tc >> 1) & 1u) ^ 1u, gave_up));
-        if (!ok) break;
-        if (tile < T.pages) {
-          const uint32_t c = 4u * page_tiles + p, slot = c % kRing;
-          ++page_tiles;
-          // A slot serves different warps in turn, so a parity alone does not say
-          // which fill it means: the slot must be this page's first.
-          ok = slot_is(&S.seq[slot], c, gave_up) &&
-               mb_wait(&S.raw_full[slot], (c / kRing) & 1u, gave_up, c < 4u ? first_spins : kAttSpin);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          const uint8_t* blk = S.raw[slot];
-          const int cls = *(volatile int32_t*)&S.cls[slot];
-          if (is_k) {
-            auto put = [&](int t, const uint32_t (&w)[4][4]) {
-              const int n = 32 * p + (t & ~7) + order8(t & 7);
-#pragma unroll
-              for (int gr = 0; gr < 4; ++gr)
-                *reinterpret_cast<uint4*>(dst + tile_off(128, n, 4 * gr + i)) =
-                    make_uint4(w[gr][0], w[gr][1], w[gr][2], w[gr][3]);
-            };
-            uint32_t w[4][4];
-            if (cls == kClsInt2) {
-              KScales2 sc;
-              k_scales2(blk, i, sc);
-#pragma unroll 1
-              for (int b = 0; b < 4; ++b) {
-                k_slot2(blk, 8 * b + rk, i, sc, w);
-                put(8 * b + rk, w);
-              }
-            } else if (cls == kClsInt4) {
-#pragma unroll 1
-              for (int b = 0; b < 4; ++b) {
-                k_slot4(blk, 8 * b + rk, i, w);
-                put(8 * b + rk, w);
-              }
-            } else {
-#pragma unroll 1
-              for (int b = 0; b < 4; ++b) {
-                if (cls == kClsInt3) {
-                  k_slot3(blk, 8 * b + rk, i, w);
-                } else if (cls == kClsFp4) {
-                  k_slotf(blk, 8 * b + rk, i, w);
-                } else {
-#pragma unroll
-                  for (int x = 0; x < 16; ++x) w[x >> 2][x & 3] = 0u;
-                }
-                put(8 * b + rk, w);
-              }
-            }
-          } else {
-            auto put = [&](int gr, const uint32_t (&w)[4][4]) {
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                *reinterpret_cast<uint4*>(dst + tile_off(128, 32 * gr + 8 * x + rv, 4 * p + i)) =
-                    make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
-            };
-            uint32_t w[4][4];
-            if (cls == kClsInt2) {
-#pragma unroll 1
-              for (int gr = 0; gr < 4; ++gr) {
-                v_group2(blk, gr, rv, i, w);
-                put(gr, w);
-              }
-            } else if (cls == kClsInt4) {
-#pragma unroll 1
-              for (int gr = 0; gr < 4; ++gr) {
-                v_group4(blk, gr, rv, i, w);
-                put(gr, w);
-              }
-            } else {
-#pragma unroll 1
-              for (int gr = 0; gr < 4; ++gr) {
-                if (cls == kClsInt3) {
-                  v_group3(blk, gr, rv, i, w);
-                } else if (cls == kClsFp4) {
-                  v_groupf(blk, gr, rv, i, w);
-                } else {
-#pragma unroll
-                  for (int x = 0; x < 16; ++x) w[x >> 2][x & 3] = 0u;
-                }
-                put(gr, w);
-              }
-            }
-          }
-          __syncwarp();
-          if (lane == 0) mb_arrive(&S.raw_empty[slot]);
-        } else {
-          // ---- 32 bf16 rows: list tokens or new tokens
-          const bool list = tile < T.lists;
-          const int j0 = 128 * (tile - (list ? T.pages : T.lists)) + 32 * p;   // first row of this warp
-          const int n = list ? u.n_fp : u.T;
-          const size_t stride = list ? kHeadDim : (size_t)A.hkv * kHeadDim;
-          const uint16_t* src =
-              list ? (is_k ? A.fpk : A.fpv) + ((size_t)u.req * A.hkv + u.kvh) * (size_t)A.fp_cap * kHeadDim
-                   : (is_k ? A.k : A.v) + ((size_t)u.tok0 * A.hkv + u.kvh) * kHeadDim;
-          // rows past the end: the last row is loaded and used as 0 (loads without branches stay in flight together)
-          if (is_k) {
-#pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-              const int j = j0 + 8 * b + rk, jc = min(j, n - 1), nn = 32 * p + 8 * b + order8(rk);
-              uint4 y[4];
-#pragma unroll
-              for (int gr = 0; gr < 4; ++gr) {
-                const int ch = 4 * gr + i;
-                y[gr] = load8(src + (size_t)jc * stride + 8 * (list ? ch ^ (jc & 7) : ch), list || kal);
-              }
-#pragma unroll
-              for (int gr = 0; gr < 4; ++gr) {
-                uint32_t w[4];
-                if (j >= n) y[gr] = make_uint4(0u, 0u, 0u, 0u);
-                order8_f16(y[gr], 1.0f, w, bad);
-                *reinterpret_cast<uint4*>(dst + tile_off(128, nn, 4 * gr + i)) = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            }
-          } else {
-            // a lane takes channels (2 cp, 2 cp + 1) of 8 rows at a time
-#pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-              uint32_t y[2][8];
-#pragma unroll
-              for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                  const int jc = min(j0 + 8 * b + s, n - 1), c = 2 * (lane + 32 * x);
-                  const uint16_t* q = src + (size_t)jc * stride + (list ? att_list_at(jc, c) : c);
-                  y[x][s] = list || val ? __ldg(reinterpret_cast<const uint32_t*>(q))
-                                        : (uint32_t)__ldg(q) | ((uint32_t)__ldg(q + 1) << 16);
-                }
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const int c = 2 * (lane + 32 * x);
-                float lo[8], hi[8];
-#pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                  const uint32_t w = j0 + 8 * b + s < n ? y[x][s] : 0u;
-                  lo[s] = in_range(bf_f(w & 0xFFFFu), bad);
-                  hi[s] = in_range(__uint_as_float(w & 0xFFFF0000u), bad);
-                }
-                *reinterpret_cast<uint4*>(dst + tile_off(128, c, 4 * p + b)) =
-                    make_uint4(f16x2(lo[0], lo[4]), f16x2(lo[1], lo[5]), f16x2(lo[2], lo[6]), f16x2(lo[3], lo[7]));
-                *reinterpret_cast<uint4*>(dst + tile_off(128, c + 1, 4 * p + b)) =
-                    make_uint4(f16x2(hi[0], hi[4]), f16x2(hi[1], hi[5]), f16x2(hi[2], hi[6]), f16x2(hi[3], hi[7]));
-              }
-            }
-          }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMAs read what was written
-        __syncwarp();
-        if (lane == 0) mb_arrive(&full[st]);
-      }
-    }
-    if (bad) atomicOr(A.status, kStatusRange);
-  } else if (warp == 16) {
-    // ------------------------------------------------------------------ MMA
+  } else if (warp < 10) {
+    // ------------------------------------------------- MMA: warp 8 + x issues those of S_x, P_x and O_x
     if (lane == 0) {
+      const int x = warp & 1;
       constexpr uint32_t idesc = mma_idesc(128, 128);
       // descriptors of the tiles; a K step of 16 is 32 bytes, a 64-element block 16384 (in units of 16 bytes)
-      const uint64_t qd0 = sw128_desc(sm32(S.q[0])), kd0 = sw128_desc(sm32(S.k[0])), vd0 = sw128_desc(sm32(S.v[0]));
       constexpr uint32_t kTile16 = kTileBytes >> 4;
-      uint32_t tc0 = 0;            // tiles before this item
-      uint32_t q_phase = 0;
-      uint32_t p_phase = 0;        // bit x: phase of p_full[x]
+      const uint64_t qd0 = sw128_desc(sm32(S.q[0])), td0 = sw128_desc(sm32(S.kv[0]));
+      const uint32_t ds = tmem + 128u * x, dout = tmem + 256u + 128u * x;
+      uint32_t tc0 = 0, q_phase = 0, p_phase = 0;   // tc0: tiles before this item
       bool ok = true;
-      // S_x = Q K^T of tile number tc
-      auto qk = [&](int x, int qx, uint32_t tc) {
-        const uint64_t a = qd0 + (uint32_t)qx * kTile16, b = kd0 + (tc & 1u) * kTile16;
-        const uint32_t d = tmem + 128u * x;
-#pragma unroll
-        for (int s = 0; s < 8; ++s) mma_ss(d, a + ((s >> 2) * 1024 + (s & 3) * 2), b + ((s >> 2) * 1024 + (s & 3) * 2), idesc, s > 0);
-      };
-      auto pv = [&](int x, uint32_t tc, bool first) {
-        const uint64_t b = vd0 + (tc & 1u) * kTile16;
-        const uint32_t d = tmem + 256u + 128u * x, a = tmem + 128u * x;
-#pragma unroll
-        for (int s = 0; s < 8; ++s) mma_ts(d, a + 8u * s, b + ((s >> 2) * 1024 + (s & 3) * 2), idesc, !first || s > 0);
-      };
-      auto k_ready = [&](uint32_t tc) { return mb_wait(&S.k_full[tc & 1u], (tc >> 1) & 1u, gave_up); };
-      auto v_ready = [&](uint32_t tc) { return mb_wait(&S.v_full[tc & 1u], (tc >> 1) & 1u, gave_up); };
-      auto p_ready = [&](int x) {
-        const bool r = mb_wait(&S.p_full[x], (p_phase >> x) & 1u, gave_up);
-        p_phase ^= 1u << x;
-        return r;
+      // tile t of the CTA's stream: K is ring entry 2 t, V entry 2 t + 1
+      auto ready = [&](uint32_t e) {
+        return mb_wait(&S.full[e % kRing], (e / kRing) & 1u, gave_up, e ? kAttSpin : first_spins);
       };
       for (int it = i0; it < i1 && ok; ++it) {
         const AttItem I = items[it];
         const AttUnit u = units[I.unit];
-        const Tiles T = tiles_of(A, u, I.row0, 256);
-        const bool one = T.rows <= 128;
+        const bool one = tiles_of(A, u, I.row0, 256).rows <= 128;
         const int n = I.tile1 - I.tile0;
         if (n == 0) continue;
         ok = mb_wait(&S.q_full, q_phase, gave_up);
         if (!ok) break;
         q_phase ^= 1u;
-        tm_fence_after();
-        // Steps: two per tile (x = 0, 1), or one per tile with x = its parity (one).  Step y does P V of
-        // its S and then issues the next Q K^T into the same S, two steps ahead of it.
-        const int per = one ? 1 : 2, steps = n * per;
+        const uint64_t qd = qd0 + (one ? 0u : (uint32_t)x * kTile16);
+        // A step: P V of tile t - 1 (of this x), then Q K^T of tile t into the same S, issued together
+        // so that the tensor cores see one run of 16; the other warp's run fills the time that the
+        // softmax of this one takes.  With `one`, tiles of the other parity are only counted: every entry
+        // is waited for in order (a parity does not tell one fill of a slot from the next but one).
+        uint32_t pend = 0u;       // entry of the V tile whose P is due
+        bool due = false, first = true;
 #pragma unroll 1
-        for (int y = -2; y < steps && ok; ++y) {
-          const int x = y & 1;
-          if (y >= 0) {
-            const uint32_t tc = tc0 + (uint32_t)(one ? y : y >> 1);
-            ok = p_ready(x) && ((!one && x) || v_ready(tc));
-            if (!ok) break;
-            tm_fence_after();
-            pv(x, tc, y < 2);
-            if (one || x) tm_commit(&S.v_empty[tc & 1u]);
+        for (int t = 0; t <= n; ++t) {
+          const uint32_t ke = 2u * (tc0 + (uint32_t)t), pv = pend;
+          const bool mine = t < n && (!one || (t & 1) == x), skip = t < n && !mine;
+          const bool did = due && (mine || t == n);
+          if (t < n) ok = ready(ke);
+          if (ok && did) {
+            ok = mb_wait(&S.p_full[x], p_phase, gave_up);
+            p_phase ^= 1u;
           }
-          if (y + 2 < steps) {
-            const uint32_t tc = tc0 + (uint32_t)(one ? y + 2 : (y + 2) >> 1);
-            ok = (!one && x) || k_ready(tc);
-            if (!ok) break;
-            tm_fence_after();
-            qk(x, one ? 0 : x, tc);
+          if (!ok) break;
+          tm_fence_after();
+          if (did) {
+            const uint64_t b = td0 + (pv % kRing) * kTile16;
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              mma_ts(dout, ds + 8u * s, b + ((s >> 2) * 1024 + (s & 3) * 2), idesc, !first || s > 0);
+            first = due = false;
+          }
+          if (mine) {
+            const uint64_t b = td0 + (ke % kRing) * kTile16;
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              mma_ss(ds, qd + ((s >> 2) * 1024 + (s & 3) * 2), b + ((s >> 2) * 1024 + (s & 3) * 2), idesc, s > 0);
             tm_commit(&S.s_full[x]);
-            if (one || x) tm_commit(&S.k_empty[tc & 1u]);
+            tm_commit(&S.empty[ke % kRing]);
+          }
+          if (did) tm_commit(&S.empty[pv % kRing]);
+          if (t == n) break;
+          ok = ready(ke + 1u);   // this tile's V
+          if (!ok) break;
+          if (skip) {
+            mb_arrive(&S.empty[ke % kRing]);
+            mb_arrive(&S.empty[(ke + 1u) % kRing]);
+          } else {
+            pend = ke + 1u;
+            due = true;
           }
         }
         if (ok) tm_commit(&S.o_full);
@@ -558,72 +561,35 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
       }
       if (!ok) {   // let the MMAs that were issued finish before TMEM is given back
         volatile uint32_t never = 0u;
-        tm_commit(&S.drain);
-        mb_wait(&S.drain, 0u, &never);
+        tm_commit(&S.drain[x]);
+        mb_wait(&S.drain[x], 0u, &never);
       }
     }
     __syncwarp();
-  } else {
+  } else if (warp == 10) {
     // --------------------------------------------------------------- loader
-    uint32_t page_tiles = 0, issued = 0;   // issued: pages of this lane
-    bool ok = true;
-    for (int it = i0; it < i1 && ok; ++it) {
-      const AttItem I = items[it];
-      const AttUnit u = units[I.unit];
-      const Tiles T = tiles_of(A, u, I.row0, 256);
-      const Entry* tab = A.table + (size_t)u.req * A.max_pages;
-      const int end = min(I.tile1, T.pages);
-      for (int tile = I.tile0; tile < end; ++tile, ++page_tiles) {
-        if (lane < 4) {
-          const uint32_t c = 4u * page_tiles + lane, slot = c % kRing;
-          const int pi = 4 * tile + lane;
-          Entry e{-1, 0u};
-          int cls = -1;
-          const uint8_t* blk = nullptr;
-          if (pi < u.n_pages) {
-            e = tab[pi];
-            if (A.hdead) e.live &= ~A.hdead[(size_t)e.id * A.hkv + u.kvh];
-            if (e.live) cls = att_page(A, e.id, u.kvh, blk);
-          }
-          ok = mb_wait(&S.raw_empty[slot], ((c / kRing) & 1u) ^ 1u, gave_up);
-          if (ok) {
-            *(volatile int32_t*)&S.cls[slot] = cls;
-            *(volatile uint32_t*)&S.seq[slot] = c;
-            *(volatile uint32_t*)&S.live[page_tiles & (kMaskRing - 1)][lane] = order_bits(e.live);
-            ++issued;
-            if (cls < 0)
-              mb_arrive(&S.raw_full[slot]);
-            else
-              bulk_to_smem(S.raw[slot], blk,
-                           cls == kClsInt2 ? kInt2Block : (cls == kClsInt4 ? kInt4Block : (cls == kClsInt3 ? kInt3Block : kFp4Block)),
-                           &S.raw_full[slot]);
-          }
+    if (lane == 0) {
+      uint32_t e = 0;   // ring entries issued
+      bool ok = true;
+      for (int it = i0; it < i1 && ok; ++it) {
+        const AttItem I = items[it];
+        const uint8_t* src = tiles + (size_t)(units[I.unit].tile_base + I.tile0) * 2 * kTileBytes;
+        for (int y = 0; y < 2 * (I.tile1 - I.tile0); ++y, ++e, src += kTileBytes) {
+          ok = mb_wait(&S.empty[e % kRing], ((e / kRing) & 1u) ^ 1u, gave_up);
+          if (!ok) break;
+          bulk_to_smem(S.kv[e % kRing], src, kTileBytes, &S.full[e % kRing]);
         }
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
       }
-    }
-    // every copy has landed before the CTA leaves: the last one of each slot
-    uint32_t n[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) n[j] = __shfl_sync(0xFFFFFFFFu, issued, j);
-    if (lane < kRing) {
+      // every copy has landed before the CTA leaves
       volatile uint32_t never = 0u;
-      const uint32_t most = max(max(n[0], n[1]), max(n[2], n[3]));
-      for (uint32_t c = 4u * most, back = 0; c > 0 && back < 4u + kRing; ++back) {
-        --c;
-        if (c % kRing == (uint32_t)lane && (c >> 2) < n[c & 3u]) {
-          mb_wait(&S.raw_full[lane], (c / kRing) & 1u, &never);
-          break;
-        }
-      }
+      for (uint32_t y = e > kRing ? e - kRing : 0u; y < e; ++y) mb_wait(&S.full[y % kRing], (y / kRing) & 1u, &never);
     }
     __syncwarp();
   }
   tm_fence_before();
   __syncthreads();
   if (tid == 0 && *gave_up) atomicOr(A.status, kStatusTimeout);
-  if (warp == 16) {
+  if (warp == 8) {
     tm_fence_after();
     tm_free(tmem, 512);
   }
@@ -631,8 +597,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
 
 }  // namespace
 
+cudaError_t launch_attend_tiles(kv_pool* P, const AttArgs& A, const AttUnit* d_units, int n_units, int max_tiles,
+                                void* d_tiles, uint32_t* d_live, cudaStream_t s) {
+  if (n_units <= 0 || max_tiles <= 0) return cudaSuccess;
+  ++P->launches;
+  attend_tiles_kernel<<<dim3((unsigned)max_tiles, (unsigned)n_units), 256, 0, s>>>(A, d_units, (uint8_t*)d_tiles, d_live);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_attend_wide(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const AttItem* d_items,
-                               const int32_t* d_cta_item, int n_ctas, float* d_part, cudaStream_t s) {
+                               const int32_t* d_cta_item, int n_ctas, const void* d_tiles, const uint32_t* d_live,
+                               float* d_part, cudaStream_t s) {
   if (n_ctas <= 0) return cudaSuccess;
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
@@ -645,7 +620,8 @@ cudaError_t launch_attend_wide(kv_pool* P, const AttArgs& A, const AttUnit* d_un
   }
   ++P->launches;
   attend_wide_kernel<<<(unsigned)n_ctas, kThreads, sizeof(WideSmem), s>>>(
-      A, d_units, d_items, d_cta_item, d_part, P->first_wait_spins < 0 ? kAttSpin : (uint32_t)P->first_wait_spins);
+      A, d_units, d_items, d_cta_item, (const uint8_t*)d_tiles, d_live, d_part,
+      P->first_wait_spins < 0 ? kAttSpin : (uint32_t)P->first_wait_spins);
   return cudaGetLastError();
 }
 

@@ -310,6 +310,7 @@ struct kv_pool {
   kvq::DevBuf logits;                 // scored decode: logits of the batch's pages, then each row's (maximum, 1 / sum)
   kvq::DevBuf select;                 // lowest-score selection: lengths, eligibility bits, keys, counts
   kvq::DevBuf attend;                 // attention of new tokens: plan, then partials
+  kvq::DevBuf attend_tiles;           // ... many rows per unit: operand tiles, then their live words
   // token position of every slot, on the device ([page id][32]; allocated by
   // the first call that needs it, then refreshed for the pages in pos_dirty)
   int32_t* d_pos = nullptr;

@@ -493,6 +493,7 @@ kv_status_t kv_pool_destroy(kv_pool_t* P) {
   cudaFree(P->logits.ptr);
   cudaFree(P->select.ptr);
   cudaFree(P->attend.ptr);
+  cudaFree(P->attend_tiles.ptr);
   cudaFree(P->d_pos);
   for (cudaEvent_t e : P->tev)
     if (e) cudaEventDestroy(e);
