@@ -15,46 +15,51 @@ namespace kvq {
 namespace {
 
 // ---- merge of partials -----------------------------------------------------
-// out = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M); a CTA of four warps per
-// row (warp w takes parts w, w + 4, ...; a lane four channels).  Bound by the
-// partials' bytes, which are still in L2.
-__global__ void __launch_bounds__(128) attend_merge_kernel(AttArgs A, const AttUnit* __restrict__ units,
-                                                           const AttMerge* __restrict__ merges,
-                                                           const float* __restrict__ part, int part_rows) {
-  __shared__ float4 acc[4][32];
-  __shared__ float2 ml[4];
+// out = sum_p O_p 2^(m_p - M) / sum_p l_p 2^(m_p - M); a warp per row (a lane four
+// channels): the parts' m and l at once, a part per lane, then their O by eights.
+// Bound by the partials' bytes, which are still in L2.
+constexpr int kMergeRows = 8;
+__global__ void __launch_bounds__(32 * kMergeRows) attend_merge_kernel(AttArgs A, const AttUnit* __restrict__ units,
+                                                                       const AttMerge* __restrict__ merges,
+                                                                       const float* __restrict__ part, int part_rows) {
   const AttMerge D = merges[blockIdx.y];
-  const int i = blockIdx.x;
+  const int i = blockIdx.x * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (i >= D.rows) return;
   const AttUnit u = units[D.unit];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float m = -INFINITY, l = 0.0f;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int p = w; p < D.n_parts; p += 4) {
-    const float* pp = part + ((size_t)(D.part0 + p * D.stride) * part_rows + i) * kAttPart;
-    const float2 x = *reinterpret_cast<const float2*>(pp + kHeadDim);
-    const float4 a = *reinterpret_cast<const float4*>(pp + 4 * lane);
-    if (x.x == -INFINITY && x.y == 0.0f) continue;   // nothing seen in this part
-    const float mn = fmaxf(m, x.x);
-    const float c = m == -INFINITY ? 0.0f : exp2f(m - mn), f = x.x == -INFINITY ? 1.0f : exp2f(x.x - mn);
-    o.x = fmaf(o.x, c, a.x * f); o.y = fmaf(o.y, c, a.y * f); o.z = fmaf(o.z, c, a.z * f); o.w = fmaf(o.w, c, a.w * f);
-    l = fmaf(l, c, x.y * f);
-    m = mn;
-  }
-  acc[w][lane] = o;
-  if (lane == 0) ml[w] = make_float2(m, l);
-  __syncthreads();
-  if (w) return;
-  const float M = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
-  float L = 0.0f;
-  o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const size_t step = (size_t)D.stride * part_rows * kAttPart;
+  const float* base = part + ((size_t)D.part0 * part_rows + i) * kAttPart;
+  float M = -INFINITY;
+  for (int p0 = 0; p0 < D.n_parts; p0 += 32)
+    if (p0 + lane < D.n_parts) M = fmaxf(M, base[(size_t)(p0 + lane) * step + kHeadDim]);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float f = ml[k].x == -INFINITY ? (ml[k].y == 0.0f ? 0.0f : 1.0f) : exp2f(ml[k].x - M);
-    const float4 a = acc[k][lane];
-    o.x = fmaf(a.x, f, o.x); o.y = fmaf(a.y, f, o.y); o.z = fmaf(a.z, f, o.z); o.w = fmaf(a.w, f, o.w);
-    L = fmaf(ml[k].y, f, L);
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  float L = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int p0 = 0; p0 < D.n_parts; p0 += 32) {
+    float f = 0.0f;
+    if (p0 + lane < D.n_parts) {
+      const float2 ml = *reinterpret_cast<const float2*>(base + (size_t)(p0 + lane) * step + kHeadDim);
+      // a part that saw nothing (m = -inf, l = 0) adds nothing; one with a NaN sum keeps it
+      f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2f(ml.x - M);
+      L = fmaf(ml.y, f, L);
+    }
+    const int n = min(32, D.n_parts - p0);
+    for (int p = 0; p < n; p += 8) {
+      float4 a[8];
+#pragma unroll
+      for (int y = 0; y < 8; ++y)
+        a[y] = *reinterpret_cast<const float4*>(base + (size_t)(p0 + min(p + y, n - 1)) * step + 4 * lane);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const float w = __shfl_sync(0xFFFFFFFFu, f, (p + y) & 31);
+        if (p + y < n && w != 0.0f) {
+          o.x = fmaf(a[y].x, w, o.x); o.y = fmaf(a[y].y, w, o.y); o.z = fmaf(a[y].z, w, o.z); o.w = fmaf(a[y].w, w, o.w);
+        }
+      }
+    }
   }
+#pragma unroll
+  for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, x);
   const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
   const float r[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
   bool bad = false;
@@ -72,7 +77,8 @@ cudaError_t launch_attend_merge(kv_pool* P, const AttArgs& A, const AttUnit* d_u
                                 int n_merges, int max_rows, const float* d_part, int part_rows, cudaStream_t s) {
   for (int a = 0; a < n_merges; a += 65535) {
     ++P->launches;
-    attend_merge_kernel<<<dim3((unsigned)max_rows, (unsigned)std::min(65535, n_merges - a)), 128, 0, s>>>(
+    attend_merge_kernel<<<dim3((unsigned)((max_rows + kMergeRows - 1) / kMergeRows), (unsigned)std::min(65535, n_merges - a)),
+                          32 * kMergeRows, 0, s>>>(
         A, d_units, d_merges + a, d_part, part_rows);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -83,7 +89,7 @@ cudaError_t launch_attend_merge(kv_pool* P, const AttArgs& A, const AttUnit* d_u
 // ---- work plan ---------------------------------------------------------
 struct AttPlan {
   std::vector<AttItem> items;
-  std::vector<int32_t> cta_item;   // per group of units: first item of every CTA, and the end
+  std::vector<int32_t> cta_item;   // per pass: first item of every CTA, and the end
   std::vector<AttMerge> merges;
   int64_t n_parts = 0;
   int merge_rows = 0;
@@ -98,9 +104,10 @@ int block_tiles(const AttUnit& u, int g, int row0, int rows, bool kv, bool tree)
 // Blocks of kWideRows rows of units [u0, u1), their tiles in one line of cost,
 // cut into equal runs, one per CTA (a run may end inside a block: its pieces are
 // merged).  A tile of a block of more than 128 rows costs 2, else 1 (the MMAs'
-// time); an item 1 more for its first and last steps.
+// time); an item 1 more for its first and last steps.  by_cta[c] gets run c.
 constexpr int kWideRows = 256;
-void plan_wide(const std::vector<AttUnit>& units, int u0, int u1, int g, bool kv, bool tree, int ctas, AttPlan& out) {
+void plan_wide(const std::vector<AttUnit>& units, int u0, int u1, int g, bool kv, bool tree, int ctas,
+               std::vector<std::vector<AttItem>>& by_cta, AttPlan& out) {
   struct Block {
     int unit, row0, rows, tiles, cost;
   };
@@ -118,9 +125,9 @@ void plan_wide(const std::vector<AttUnit>& units, int u0, int u1, int g, bool kv
   const double share = (double)(total + ctas) / ctas;   // every CTA ends inside a block once
   double done = 0.0;
   int cta = 0;
-  out.cta_item.push_back((int32_t)out.items.size());
+  std::vector<std::pair<int, size_t>> pieces;   // (CTA, index) of a block's items
   for (const Block& b : blocks) {
-    const size_t first = out.items.size();
+    pieces.clear();
     int t = 0;
     do {
       int take = b.tiles - t;
@@ -128,21 +135,20 @@ void plan_wide(const std::vector<AttUnit>& units, int u0, int u1, int g, bool kv
         const double room = (cta + 1) * share - done;
         const int fit = (int)((room - 0.5) / b.cost + 0.5);
         if (fit < std::min(2, take)) {   // nothing worth starting fits: the next CTA
-          out.cta_item.push_back((int32_t)out.items.size());
           ++cta;
           continue;
         }
         if (fit + 1 < take) take = fit;
       }
-      out.items.push_back(AttItem{b.unit, b.row0, t, t + take, -1, {0, 0, 0}});
+      pieces.emplace_back(cta, by_cta[(size_t)cta].size());
+      by_cta[(size_t)cta].push_back(AttItem{b.unit, b.row0, t, t + take, -1, {0, 0, 0}});
       done += (double)take * b.cost + 1.0;
       t += take;
-      if (t >= b.tiles) break;
-    } while (true);
-    const int n = (int)(out.items.size() - first);
+    } while (t < b.tiles);
+    const int n = (int)pieces.size();
     if (n == 1 && b.rows > 128) continue;
     const int32_t p0 = (int32_t)out.n_parts;
-    for (int y = 0; y < n; ++y) out.items[first + (size_t)y].part = p0 + 2 * y;
+    for (int y = 0; y < n; ++y) by_cta[(size_t)pieces[(size_t)y].first][pieces[(size_t)y].second].part = p0 + 2 * y;
     out.n_parts += 2 * n;
     if (b.rows > 128) {
       out.merges.push_back(AttMerge{b.unit, b.row0, 128, p0, n, 2});
@@ -152,12 +158,14 @@ void plan_wide(const std::vector<AttUnit>& units, int u0, int u1, int g, bool kv
     }
     out.merge_rows = std::max(out.merge_rows, std::min(128, b.rows));
   }
-  out.cta_item.push_back((int32_t)out.items.size());
 }
 
-// Units taken together: their operand tiles stay in L2 (126 MB, shared with
-// the rows of q and out) while every block of rows reads them.
-constexpr int64_t kTilesInL2 = 1100;   // 72 MB
+// The units are taken in groups whose operand tiles stay in L2 (126 MB, shared
+// with the rows of q and out) while every block of rows reads them: each CTA has
+// a run of every group, in order, so all CTAs are at the same group at about the
+// same time.  A pass holds the tiles of several groups.
+constexpr int64_t kTilesInL2 = 1400;      // 92 MB
+constexpr int64_t kTilesPerPass = 1 << 16;   // 4.3 GB
 
 }  // namespace
 }  // namespace kvq
@@ -238,27 +246,45 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
     return KV_OK;
   }
   AttPlan pl;
-  struct Group {
-    int u0, u1, max_tiles, cta0, ctas;
+  struct Pass {
+    int u0, u1, max_tiles, cta0;
   };
-  std::vector<Group> groups;
-  int64_t most = 0;
-  for (int u0 = 0; u0 < (int)units.size();) {
-    int u1 = u0, max_tiles = 0;
-    int64_t n = 0;
-    for (; u1 < (int)units.size(); ++u1) {
-      const int t = block_tiles(units[(size_t)u1], g, 0, units[(size_t)u1].T * g, k != nullptr, tree != nullptr);
-      if (u1 > u0 && n + t > kTilesInL2) break;
-      units[(size_t)u1].tile_base = (int32_t)n;
-      n += t;
-      max_tiles = std::max(max_tiles, t);
+  std::vector<Pass> passes;
+  std::vector<std::vector<AttItem>> by_cta((size_t)P->sm_count);
+  int64_t most = 0, n = 0, group = 0;
+  int u0 = 0, g0 = 0, max_tiles = 0;
+  auto end_group = [&](int x) {
+    plan_wide(units, g0, x, g, k != nullptr, tree != nullptr, P->sm_count, by_cta, pl);
+    g0 = x;
+    group = 0;
+  };
+  auto end_pass = [&](int x) {
+    passes.push_back(Pass{u0, x, max_tiles, (int)pl.cta_item.size()});
+    for (auto& c : by_cta) {
+      pl.cta_item.push_back((int32_t)pl.items.size());
+      pl.items.insert(pl.items.end(), c.begin(), c.end());
+      c.clear();
     }
-    const int cta0 = (int)pl.cta_item.size();
-    plan_wide(units, u0, u1, g, k != nullptr, tree != nullptr, P->sm_count, pl);
-    groups.push_back(Group{u0, u1, max_tiles, cta0, (int)pl.cta_item.size() - cta0 - 1});
+    pl.cta_item.push_back((int32_t)pl.items.size());
     most = std::max(most, n);
-    u0 = u1;
+    u0 = x;
+    n = 0;
+    max_tiles = 0;
+  };
+  for (int x = 0; x < (int)units.size(); ++x) {
+    const int t = block_tiles(units[(size_t)x], g, 0, units[(size_t)x].T * g, k != nullptr, tree != nullptr);
+    if (x > g0 && group + t > kTilesInL2) end_group(x);
+    if (x > u0 && n + t > kTilesPerPass) {
+      if (x > g0) end_group(x);
+      end_pass(x);
+    }
+    units[(size_t)x].tile_base = (int32_t)n;
+    n += t;
+    group += t;
+    max_tiles = std::max(max_tiles, t);
   }
+  end_group((int)units.size());
+  end_pass((int)units.size());
   Upload u;
   const size_t ou = u.add(units.data(), units.size() * sizeof(AttUnit));
   const size_t oi = u.add(pl.items.data(), pl.items.size() * sizeof(AttItem));
@@ -272,9 +298,9 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
   const AttUnit* du = (const AttUnit*)(base + ou);
   float* d_part = (float*)((uint8_t*)P->attend.ptr + op);
   uint32_t* d_live = (uint32_t*)((uint8_t*)P->attend_tiles.ptr + (size_t)most * kAttTileBytes);
-  for (const Group& G : groups) {
+  for (const Pass& G : passes) {
     KV_CUDA(launch_attend_tiles(P, A, du + G.u0, G.u1 - G.u0, G.max_tiles, P->attend_tiles.ptr, d_live, s));
-    KV_CUDA(launch_attend_wide(P, A, du, (const AttItem*)(base + oi), (const int32_t*)(base + oc) + G.cta0, G.ctas,
+    KV_CUDA(launch_attend_wide(P, A, du, (const AttItem*)(base + oi), (const int32_t*)(base + oc) + G.cta0, P->sm_count,
                                P->attend_tiles.ptr, d_live, d_part, s));
   }
   if (!pl.merges.empty())

@@ -62,6 +62,20 @@ __device__ __forceinline__ bool slot_is(volatile uint32_t* seq, uint32_t c, vola
   *gave_up = 1u;
   return false;
 }
+// The same without suspending the thread: for waits on the critical path, where
+// the wake-up of a suspended thread costs a few hundred cycles.
+__device__ __forceinline__ bool mb_spin(uint64_t* b, uint32_t parity, volatile uint32_t* gave_up) {
+  for (uint32_t it = 0; it < 16 * kAttSpin; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok) : "r"(sm32(b)), "r"(parity) : "memory");
+    if (ok) return true;
+    if ((it & 63u) == 63u && *gave_up) return false;
+  }
+  *gave_up = 1u;
+  return false;
+}
 __device__ __forceinline__ void bulk_to_smem(void* dst, const void* src, uint32_t bytes, uint64_t* b) {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the slot was read generically
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(sm32(b)), "r"(bytes) : "memory");

@@ -50,7 +50,7 @@ constexpr float kNever = -3.0e38f;              // S of a key that is not seen
 struct alignas(1024) WideSmem {
   uint8_t q[2][kTileBytes], kv[kRing][kTileBytes];
   uint64_t full[kRing], empty[kRing];
-  uint64_t q_full, s_full[2], p_full[2], o_full, drain[2];
+  uint64_t q_full, s_full[2], p_full[2], o_full, turn[2], drain[2];
   uint32_t tmem, gave_up;
 };
 static_assert(sizeof(WideSmem) <= 232448, "one CTA's shared memory");
@@ -68,10 +68,12 @@ __device__ __forceinline__ Tiles tiles_of(const AttArgs& A, const AttUnit& u, in
   return t;
 }
 
-// One CTA of eight warps per tile: warp p takes page (or 32 rows) p of K, warp
-// 4 + p of V.  Bound by memory: 64 KB written per 12 to 20 KB read.
+// One CTA of eight warps per tile: the four page blocks go to shared memory in
+// 16-byte pieces, then warp p dequantizes K of page (or 32 rows) p and warp 4 + p
+// its V.  Bound by memory: 64 KB written per 12 to 20 KB read.
 __global__ void __launch_bounds__(256) attend_tiles_kernel(AttArgs A, const AttUnit* __restrict__ units,
                                                            uint8_t* __restrict__ tiles, uint32_t* __restrict__ live) {
+  __shared__ __align__(16) uint8_t raw[4][kInt4Block];
   const AttUnit u = units[blockIdx.y];
   const Tiles T = tiles_of(A, u, 0, 1 << 30);
   const int tile = blockIdx.x;
@@ -92,6 +94,22 @@ __global__ void __launch_bounds__(256) attend_tiles_kernel(AttArgs A, const AttU
       if (A.hdead) e.live &= ~A.hdead[(size_t)e.id * A.hkv + u.kvh];
       if (e.live) cls = att_page(A, e.id, u.kvh, blk);
     }
+    if (cls >= 0) {   // the two warps of a page copy half of it each
+      const int n16 = (cls == kClsInt2 ? kInt2Block : (cls == kClsInt4 ? kInt4Block : (cls == kClsInt3 ? kInt3Block : kFp4Block))) / 16;
+      uint4 w[5];
+#pragma unroll
+      for (int y = 0; y < 5; ++y) {
+        const int c = 64 * y + 32 * (is_k ? 0 : 1) + lane;
+        if (c < n16) w[y] = __ldcs(reinterpret_cast<const uint4*>(blk) + c);
+      }
+#pragma unroll
+      for (int y = 0; y < 5; ++y) {
+        const int c = 64 * y + 32 * (is_k ? 0 : 1) + lane;
+        if (c < n16) reinterpret_cast<uint4*>(raw[p])[c] = w[y];
+      }
+      blk = raw[p];
+    }
+    __syncthreads();
     if (is_k && lane == 0) live[(size_t)(u.tile_base + tile) * 4 + p] = order_bits(e.live);
     {
           if (is_k) {
@@ -257,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
       mb_init(&S.s_full[x], 1);
       mb_init(&S.p_full[x], 4);
       mb_init(&S.drain[x], 1);
+      mb_init(&S.turn[x], 1);
     }
     mb_init(&S.q_full, 8);
     mb_init(&S.o_full, 2);
@@ -287,39 +306,46 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
       const int rl = one ? rt : 128 * x + rt;              // row in the block
       const bool valid = rl < T.rows;
       const int row = I.row0 + (valid ? rl : 0), t = row / g;
-      const size_t at = ((size_t)(u.tok0 + t) * A.hq + (size_t)u.kvh * g + (row - t * g)) * kHeadDim;
-      // ---- Q row: scaled by a power of two so that its largest element is in [2^7, 2^8)
+      auto row_at = [&](int r) {
+        return ((size_t)(u.tok0 + r / g) * A.hq + (size_t)u.kvh * g + r % g) * kHeadDim;
+      };
+      const size_t at = row_at(row);
+      // ---- Q: every row scaled by a power of two so that its largest element is in [2^7, 2^8).  A warp
+      // loads its 32 rows two at a time (16 lanes each), 16 rows in flight.
       float rf = 0.0f;
       {
-        float mx = 0.0f;
-        if (valid)
+        const int c = lane & 15, half = lane >> 4, w32 = rl - lane;   // first row of the warp in the block
 #pragma unroll 1
-          for (int c = 0; c < 16; ++c) {
-            const uint4 w = load8(A.q + at + 8 * c, qal);
-            const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+        for (int y0 = 0; y0 < 16; y0 += 8) {
+          uint4 w[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mx = fmaxf(mx, fmaxf(fabsf(bf_f(wd[k] & 0xFFFFu)), fabsf(__uint_as_float(wd[k] & 0xFFFF0000u))));
+          for (int y = 0; y < 8; ++y) {
+            const int r = min(w32 + 2 * (y0 + y) + half, T.rows - 1);
+            w[y] = load8(A.q + row_at(I.row0 + r) + 8 * c, qal);
           }
-        const int e = mx > 0.0f && mx < INFINITY ? max(-100, min(100, 7 - ilogbf(mx))) : 0;
-        const float mul = copysignf(__int_as_float((e + 127) << 23), A.scale_log2);
-        // (a factor below 1e-30 makes every logit 0, as 1e-30 does; kNever times it must stay far below 0)
-        rf = fmaxf(fabsf(A.scale_log2) * __int_as_float((127 - e) << 23), 1e-30f);
-        if (!one || x == 0) {
-          uint8_t* qb = S.q[x];
-#pragma unroll 1
-          for (int c = 0; c < 16; ++c) {
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (valid) w = load8(A.q + at + 8 * c, qal);
-            const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
-            float f[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const uint32_t wd[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+            float f[8], mx = 0.0f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              f[2 * k] = bf_f(wd[k] & 0xFFFFu) * mul;
-              f[2 * k + 1] = __uint_as_float(wd[k] & 0xFFFF0000u) * mul;
+              f[2 * k] = bf_f(wd[k] & 0xFFFFu);
+              f[2 * k + 1] = __uint_as_float(wd[k] & 0xFFFF0000u);
+              mx = fmaxf(mx, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
             }
-            *reinterpret_cast<uint4*>(qb + tile_off(128, rt, c)) =
-                make_uint4(f16x2(f[0], f[4]), f16x2(f[1], f[5]), f16x2(f[2], f[6]), f16x2(f[3], f[7]));
+#pragma unroll
+            for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+            const int e = mx > 0.0f && mx < INFINITY ? max(-100, min(100, 7 - ilogbf(mx))) : 0;
+            const float mul = copysignf(__int_as_float((e + 127) << 23), A.scale_log2);
+            // (a factor below 1e-30 makes every logit 0, as 1e-30 does; kNever times it must stay far below 0)
+            const float rr = fmaxf(fabsf(A.scale_log2) * __int_as_float((127 - e) << 23), 1e-30f);
+            const float mine = __shfl_sync(0xFFFFFFFFu, rr, (lane & 1) << 4);
+            if ((lane >> 1) == y0 + y) rf = mine;   // the thread's own row
+            const int rr0 = (rt & ~31) + 2 * (y0 + y) + half;
+            if (!one || x == 0)
+              *reinterpret_cast<uint4*>(S.q[x] + tile_off(128, rr0, c)) =
+                  make_uint4(f16x2(f[0] * mul, f[4] * mul), f16x2(f[1] * mul, f[5] * mul), f16x2(f[2] * mul, f[6] * mul),
+                             f16x2(f[3] * mul, f[7] * mul));
           }
         }
       }
@@ -495,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
       constexpr uint32_t kTile16 = kTileBytes >> 4;
       const uint64_t qd0 = sw128_desc(sm32(S.q[0])), td0 = sw128_desc(sm32(S.kv[0]));
       const uint32_t ds = tmem + 128u * x, dout = tmem + 256u + 128u * x;
-      uint32_t tc0 = 0, q_phase = 0, p_phase = 0;   // tc0: tiles before this item
+      uint32_t tc0 = 0, q_phase = 0, p_phase = 0, turns = 0;   // tc0: tiles before this item
       bool ok = true;
       // tile t of the CTA's stream: K is ring entry 2 t, V entry 2 t + 1
       auto ready = [&](uint32_t e) {
@@ -523,8 +549,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
           const bool mine = t < n && (!one || (t & 1) == x), skip = t < n && !mine;
           const bool did = due && (mine || t == n);
           if (t < n) ok = ready(ke);
+          // Runs of the two halves take turns: issued at will they would fall into step, both halves'
+          // MMAs at one time and both softmaxes at the next (4100 cycles per tile instead of 3200).
+          if (ok && !one && (x || turns)) ok = mb_wait(&S.turn[x], (x ? turns : turns - 1u) & 1u, gave_up);
+          if (!one) ++turns;
           if (ok && did) {
-            ok = mb_wait(&S.p_full[x], p_phase, gave_up);
+            ok = mb_spin(&S.p_full[x], p_phase, gave_up);
             p_phase ^= 1u;
           }
           if (!ok) break;
@@ -544,6 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
             tm_commit(&S.s_full[x]);
             tm_commit(&S.empty[ke % kRing]);
           }
+          if (!one) mb_arrive(&S.turn[x ^ 1]);
           if (did) tm_commit(&S.empty[pv % kRing]);
           if (t == n) break;
           ok = ready(ke + 1u);   // this tile's V
