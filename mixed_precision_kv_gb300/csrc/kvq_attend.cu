@@ -160,6 +160,55 @@ void plan_wide(const std::vector<AttUnit>& units, int u0, int u1, int g, bool kv
   }
 }
 
+// Few rows per unit: blocks of R rows, all key tiles of all blocks in one line, cut
+// into equal runs.  A tile costs 1 (its unpacking, whatever R), an item 1.5 more.
+constexpr int kFewRows = 256;   // units of up to this many rows
+void plan_few(const std::vector<AttUnit>& units, int g, int R, bool kv, bool tree, int sms, AttPlan& out) {
+  double total = 0.0;
+  int64_t tiles = 0;
+  for (const AttUnit& u : units)
+    for (int r = 0; r < u.T * g; r += R) {
+      const int t = block_tiles(u, g, r, std::min(R, u.T * g - r), kv, tree);
+      tiles += t;
+      total += t + 1.5;
+    }
+  const int ctas = (int)std::max<int64_t>(1, std::min<int64_t>(sms, tiles));
+  const double share = (total + 1.5 * (ctas - 1)) / ctas;
+  double done = 0.0;
+  int cta = 0;
+  out.cta_item.push_back(0);
+  for (int x = 0; x < (int)units.size(); ++x) {
+    const AttUnit& u = units[(size_t)x];
+    for (int r = 0; r < u.T * g; r += R) {
+      const int rows = std::min(R, u.T * g - r), n = block_tiles(u, g, r, rows, kv, tree);
+      const size_t first = out.items.size();
+      int t = 0;
+      do {
+        int take = n - t;
+        if (cta < ctas - 1) {
+          const int fit = (int)((cta + 1) * share - done - 1.0);
+          if (fit < std::min(1, take)) {
+            out.cta_item.push_back((int32_t)out.items.size());
+            ++cta;
+            continue;
+          }
+          take = std::min(take, fit);
+        }
+        out.items.push_back(AttItem{x, r, t, t + take, -1, {0, 0, 0}});
+        done += take + 1.5;
+        t += take;
+      } while (t < n);
+      const int pieces = (int)(out.items.size() - first);
+      if (pieces == 1) continue;
+      for (int y = 0; y < pieces; ++y) out.items[first + (size_t)y].part = (int32_t)out.n_parts + y;
+      out.merges.push_back(AttMerge{x, r, rows, (int32_t)out.n_parts, pieces, 1});
+      out.n_parts += pieces;
+      out.merge_rows = std::max(out.merge_rows, rows);
+    }
+  }
+  out.cta_item.push_back((int32_t)out.items.size());
+}
+
 // The units are taken in groups whose operand tiles stay in L2 (126 MB, shared
 // with the rows of q and out) while every block of rows reads them: each CTA has
 // a run of every group, in order, so all CTAs are at the same group at about the
@@ -227,17 +276,20 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
   A.hq = hq;
   A.fp_cap = P->fp_cap;
 
-  std::vector<AttUnit> units;
-  units.reserve((size_t)n_req * hkv);
+  const bool simt = P->decode_impl == KV_DECODE_SIMT;
+  std::vector<AttUnit> units, few;   // many rows (or all, on the CUDA cores) and few rows per unit
+  int few_rows = 0;
   int64_t tok0 = 0;
   for (int32_t b = 0; b < n_req; ++b) {
     const int32_t r = req_ids[b];
     if (n_new[b] > 0)
       for (int h = 0; h < hkv; ++h)
-        units.push_back(AttUnit{r, h, n_new[b], (int32_t)P->reqs[r].table.size(), P->n_fp.empty() ? 0 : P->n_fp[r], 0, tok0});
+        (!simt && n_new[b] * g <= kFewRows ? few : units)
+            .push_back(AttUnit{r, h, n_new[b], (int32_t)P->reqs[r].table.size(), P->n_fp.empty() ? 0 : P->n_fp[r], 0, tok0});
+    if (n_new[b] * g <= kFewRows) few_rows = std::max(few_rows, n_new[b] * g);
     tok0 += n_new[b];
   }
-  if (P->decode_impl == KV_DECODE_SIMT) {
+  if (simt) {
     Upload u;
     u.add(units.data(), units.size() * sizeof(AttUnit));
     if ((st = ensure(P->attend, u.size)) != KV_OK) return st;
@@ -245,7 +297,10 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
     KV_CUDA(launch_attend_simt(P, A, (const AttUnit*)P->attend.ptr, (int)units.size(), max_new * g, s));
     return KV_OK;
   }
-  AttPlan pl;
+  const bool kv = k != nullptr, tr = tree != nullptr;
+  AttPlan pf, pl;
+  const int R = few_rows <= 16 ? 16 : (few_rows <= 32 ? 32 : 64);
+  if (!few.empty()) plan_few(few, g, R, kv, tr, P->sm_count, pf);
   struct Pass {
     int u0, u1, max_tiles, cta0;
   };
@@ -254,7 +309,7 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
   int64_t most = 0, n = 0, group = 0;
   int u0 = 0, g0 = 0, max_tiles = 0;
   auto end_group = [&](int x) {
-    plan_wide(units, g0, x, g, k != nullptr, tree != nullptr, P->sm_count, by_cta, pl);
+    plan_wide(units, g0, x, g, kv, tr, P->sm_count, by_cta, pl);
     g0 = x;
     group = 0;
   };
@@ -271,39 +326,58 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
     n = 0;
     max_tiles = 0;
   };
-  for (int x = 0; x < (int)units.size(); ++x) {
-    const int t = block_tiles(units[(size_t)x], g, 0, units[(size_t)x].T * g, k != nullptr, tree != nullptr);
-    if (x > g0 && group + t > kTilesInL2) end_group(x);
-    if (x > u0 && n + t > kTilesPerPass) {
-      if (x > g0) end_group(x);
-      end_pass(x);
+  if (!units.empty()) {
+    for (int x = 0; x < (int)units.size(); ++x) {
+      const int t = block_tiles(units[(size_t)x], g, 0, units[(size_t)x].T * g, kv, tr);
+      if (x > g0 && group + t > kTilesInL2) end_group(x);
+      if (x > u0 && n + t > kTilesPerPass) {
+        if (x > g0) end_group(x);
+        end_pass(x);
+      }
+      units[(size_t)x].tile_base = (int32_t)n;
+      n += t;
+      group += t;
+      max_tiles = std::max(max_tiles, t);
     }
-    units[(size_t)x].tile_base = (int32_t)n;
-    n += t;
-    group += t;
-    max_tiles = std::max(max_tiles, t);
+    end_group((int)units.size());
+    end_pass((int)units.size());
   }
-  end_group((int)units.size());
-  end_pass((int)units.size());
+  struct Placed {   // a plan's arrays in the upload, its partials behind
+    size_t units, items, ctas, merges, parts;
+  };
   Upload u;
-  const size_t ou = u.add(units.data(), units.size() * sizeof(AttUnit));
-  const size_t oi = u.add(pl.items.data(), pl.items.size() * sizeof(AttItem));
-  const size_t oc = u.add(pl.cta_item.data(), pl.cta_item.size() * sizeof(int32_t));
-  const size_t om = u.add(pl.merges.data(), pl.merges.size() * sizeof(AttMerge));
-  const size_t op = (u.size + 255) & ~size_t(255);
-  if ((st = ensure(P->attend, op + (size_t)pl.n_parts * 128 * kAttPart * sizeof(float))) != KV_OK) return st;
+  auto place = [&](const std::vector<AttUnit>& un, const AttPlan& p) {
+    Placed x;
+    x.units = u.add(un.data(), un.size() * sizeof(AttUnit));
+    x.items = u.add(p.items.data(), p.items.size() * sizeof(AttItem));
+    x.ctas = u.add(p.cta_item.data(), p.cta_item.size() * sizeof(int32_t));
+    x.merges = u.add(p.merges.data(), p.merges.size() * sizeof(AttMerge));
+    return x;
+  };
+  Placed xf = place(few, pf), xl = place(units, pl);
+  xf.parts = (u.size + 255) & ~size_t(255);
+  xl.parts = xf.parts + (size_t)pf.n_parts * R * kAttPart * sizeof(float);
+  if ((st = ensure(P->attend, xl.parts + (size_t)pl.n_parts * 128 * kAttPart * sizeof(float))) != KV_OK) return st;
   if ((st = ensure(P->attend_tiles, (size_t)most * (kAttTileBytes + 16))) != KV_OK) return st;
   if ((st = h2d(P, P->attend.ptr, u, s)) != KV_OK) return st;
-  const uint8_t* base = (const uint8_t*)P->attend.ptr;
-  const AttUnit* du = (const AttUnit*)(base + ou);
-  float* d_part = (float*)((uint8_t*)P->attend.ptr + op);
+  uint8_t* base = (uint8_t*)P->attend.ptr;
+  auto merge = [&](const Placed& x, const AttPlan& p, int part_rows) -> cudaError_t {
+    if (p.merges.empty()) return cudaSuccess;
+    return launch_attend_merge(P, A, (const AttUnit*)(base + x.units), (const AttMerge*)(base + x.merges),
+                               (int)p.merges.size(), p.merge_rows, (const float*)(base + x.parts), part_rows, s);
+  };
+  if (!few.empty()) {
+    KV_CUDA(launch_attend_few(P, R, A, (const AttUnit*)(base + xf.units), (const AttItem*)(base + xf.items),
+                              (const int32_t*)(base + xf.ctas), (int)pf.cta_item.size() - 1, (float*)(base + xf.parts), s));
+    KV_CUDA(merge(xf, pf, R));
+  }
+  const AttUnit* du = (const AttUnit*)(base + xl.units);
   uint32_t* d_live = (uint32_t*)((uint8_t*)P->attend_tiles.ptr + (size_t)most * kAttTileBytes);
   for (const Pass& G : passes) {
     KV_CUDA(launch_attend_tiles(P, A, du + G.u0, G.u1 - G.u0, G.max_tiles, P->attend_tiles.ptr, d_live, s));
-    KV_CUDA(launch_attend_wide(P, A, du, (const AttItem*)(base + oi), (const int32_t*)(base + oc) + G.cta0, P->sm_count,
-                               P->attend_tiles.ptr, d_live, d_part, s));
+    KV_CUDA(launch_attend_wide(P, A, du, (const AttItem*)(base + xl.items), (const int32_t*)(base + xl.ctas) + G.cta0,
+                               P->sm_count, P->attend_tiles.ptr, d_live, (float*)(base + xl.parts), s));
   }
-  if (!pl.merges.empty())
-    KV_CUDA(launch_attend_merge(P, A, du, (const AttMerge*)(base + om), (int)pl.merges.size(), pl.merge_rows, d_part, 128, s));
+  KV_CUDA(merge(xl, pl, 128));
   return KV_OK;
 }

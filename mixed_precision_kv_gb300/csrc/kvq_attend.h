@@ -77,6 +77,11 @@ __device__ __forceinline__ int att_list_at(int t, int c) { return (((c >> 3) ^ (
 cudaError_t launch_attend_simt(kv_pool* P, const AttArgs& A, const AttUnit* d_units, int n_units, int max_rows,
                                cudaStream_t s);
 
+// Tensor-core kernel for few rows per unit (kvq_attend_few.cu): blocks of `rows`
+// (16, 32 or 64) rows, one partial of that many rows per item.
+cudaError_t launch_attend_few(kv_pool* P, int rows, const AttArgs& A, const AttUnit* d_units, const AttItem* d_items,
+                              const int32_t* d_cta_item, int n_ctas, float* d_part, cudaStream_t s);
+
 // Tensor-core kernels for many rows per unit (kvq_attend_wide.cu): the units' keys
 // as operand tiles (64 KB and four live words per 128 keys), then blocks of 256
 // rows over them.  Partials of 128 rows, two per item (rows 0..127 and 128..255;

@@ -1,0 +1,680 @@
+// kv_attend for few rows per unit (drafts to be verified, single tokens): tcgen05
+// attention bound by the cache's bytes.
+//
+// With R <= 64 rows the products are taken transposed, so that the 128 rows of an
+// MMA are always full:
+//     S^T = K Q^T   (128 keys x R),      O^T += V^T P^T   (128 channels x R).
+// The A operands, K (a key per TMEM lane) and V^T (a channel per lane), are
+// dequantized from the page blocks straight into TMEM: the code words of the
+// pages are laid out by mma fragments, and tcgen05.st's 16x256b shape has the same
+// ownership (lane 4 r + i: rows r and r + 8, columns 2 i and 2 i + 1 of every 8), so a
+// word goes from shared memory through registers to its place with no exchange.
+// Through shared memory instead, each tile would cost 64 KB written and 64 KB read
+// again, 1000 cycles of its 128 bytes a cycle; TMEM has its own ports.
+//
+// A CTA takes an item: a block of R rows of one (request, kv head) unit and a run
+// of its tiles of 128 keys (four pages, or bf16 rows).  Roles (14 warps): one
+// warpgroup for the softmax (a key per thread), four warps for K (a page each),
+// four for V (32 channels each), one thread for the MMAs, one warp streaming
+// pages with bulk copies, seven tiles deep.  The running maximum of a row is kept
+// while no key exceeds it by more than 2^8 (P is binary16 with 2^7 of headroom);
+// otherwise the warpgroup takes the maxima of all columns and rescales O^T.
+//
+// What bounds it: unpacking, about 2 instructions per element (32768 per tile),
+// against 520 (INT2) to 870 (INT4) cycles that a tile's bytes take from HBM.
+#include <algorithm>
+#include <atomic>
+
+#include "kvq_attend_mma.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kStages = 7;                      // raw tiles in flight
+constexpr int kWarps = 14;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaskRing = 16;                   // tiles whose live words are kept
+constexpr float kHead = 7.0f;                   // P = 2^(x - m + 7)
+constexpr float kGrow = 8.0f;                   // a maximum may be stale by this much (base 2)
+constexpr float kNever = -3.0e38f;              // S of a key that is not seen
+constexpr float kUnseen = -1.0e30f;             // kHead - m of a row that has seen nothing: its weights are 0
+// TMEM columns
+constexpr uint32_t kColK = 0, kColV = 128, kColS = 256, kColO = 384;
+
+template <int R>
+struct alignas(1024) FewSmem {
+  uint8_t q[R * 256], p[2][R * 256];            // operand rows of 128 elements, 128-byte swizzled
+  alignas(128) uint8_t raw[kStages][4][kInt4Block];
+  float2 rfnm[R];                               // per row: factor of S, kHead - m
+  float m[R], fac[R], wmax[4][R];
+  unsigned long long tree[R];
+  uint32_t live[kMaskRing][4];
+  int32_t cls[kStages][4];
+  uint32_t grow[2][4];
+  uint64_t raw_full[kStages], raw_empty[kStages];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2], q_full, drain;
+  uint32_t tmem, gave_up, unseen;
+};
+static_assert(sizeof(FewSmem<64>) <= 232448, "one CTA's shared memory");
+
+struct Tiles {   // an item's tiles: [0, pages), [pages, lists), [lists, ..) by kind
+  int pages, lists, rows;
+};
+template <int R>
+__device__ __forceinline__ Tiles tiles_of(const AttArgs& A, const AttUnit& u, int row0) {
+  Tiles t;
+  t.rows = min(R, u.T * (A.hq / A.hkv) - row0);
+  t.pages = (u.n_pages + 3) >> 2;
+  t.lists = t.pages + ((u.n_fp + 127) >> 7);
+  return t;
+}
+
+// tcgen05.st of fragments: 16 lanes x (8 N) columns, lane 4 r + i holds rows r and
+// r + 8, columns 8 x + 2 i and + 1 (registers 4 x .. 4 x + 3)
+__device__ __forceinline__ void tm_st_frag64(uint32_t addr, const uint32_t (&a)[4][4], const uint32_t (&b)[4][4]) {
+  // word w = 2 x + c of row r is a[w >> 2][w & 3], of row r + 8 b[w >> 2][w & 3]
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(a[0][0]), "r"(a[0][1]), "r"(b[0][0]), "r"(b[0][1]), "r"(a[0][2]), "r"(a[0][3]), "r"(b[0][2]), "r"(b[0][3]),
+      "r"(a[1][0]), "r"(a[1][1]), "r"(b[1][0]), "r"(b[1][1]), "r"(a[1][2]), "r"(a[1][3]), "r"(b[1][2]), "r"(b[1][3]),
+      "r"(a[2][0]), "r"(a[2][1]), "r"(b[2][0]), "r"(b[2][1]), "r"(a[2][2]), "r"(a[2][3]), "r"(b[2][2]), "r"(b[2][3]),
+      "r"(a[3][0]), "r"(a[3][1]), "r"(b[3][0]), "r"(b[3][1]), "r"(a[3][2]), "r"(a[3][3]), "r"(b[3][2]), "r"(b[3][3])
+      : "memory");
+}
+__device__ __forceinline__ void tm_st_frag16(uint32_t addr, const uint32_t (&a)[4], const uint32_t (&b)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(a[0]), "r"(a[1]),
+               "r"(b[0]), "r"(b[1]), "r"(a[2]), "r"(a[3]), "r"(b[2]), "r"(b[3]) : "memory");
+}
+// Place of element n (0..7) of run (gr, i) in a row of the K contraction, and of
+// slot 8 i + n of page gr in one of the V contraction (see tm_st_frag*).
+__device__ __forceinline__ int frag_pos(int gr, int i, int n) {
+  return 32 * gr + 16 * ((n & 3) >> 1) + 4 * i + 2 * (n & 1) + (n >> 2);
+}
+__device__ __forceinline__ float warp_max_f(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Barrier of the softmax warpgroup; true if any thread gives `stop` (every thread
+// gets the same answer, so all leave together).
+__device__ __forceinline__ bool group_stop(bool stop) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, 1, 128, a;\n selp.u32 %0, 1, 0, b;\n}"
+               : "=r"(r) : "r"((uint32_t)stop) : "memory");
+  return r != 0;
+}
+
+template <int R>
+__global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
+    AttArgs A, const AttUnit* __restrict__ units, const AttItem* __restrict__ items, const int32_t* __restrict__ cta_item,
+    float* __restrict__ part, uint32_t first_spins) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  FewSmem<R>& S = *reinterpret_cast<FewSmem<R>*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int i0 = cta_item[blockIdx.x], i1 = cta_item[blockIdx.x + 1];
+  volatile uint32_t* gave_up = &S.gave_up;
+  if (tid == 0) {
+    for (int x = 0; x < kStages; ++x) {
+      mb_init(&S.raw_full[x], 4);
+      mb_init(&S.raw_empty[x], 8);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mb_init(&S.k_full[x], 4);
+      mb_init(&S.k_empty[x], 1);
+      mb_init(&S.v_full[x], 4);
+      mb_init(&S.v_empty[x], 1);
+      mb_init(&S.s_full[x], 1);
+      mb_init(&S.p_full[x], 4);
+      mb_init(&S.pv_done[x], 1);
+    }
+    mb_init(&S.q_full, 4);
+    mb_init(&S.drain, 1);
+    S.gave_up = 0u;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 12) tm_alloc(&S.tmem, 512);
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tmem = S.tmem;
+  const int g = A.hq / A.hkv;
+
+  if (warp < 4) {
+    // ---------------------------------------------------------------- softmax
+    const uint32_t tl = tmem + ((uint32_t)warp << 21);
+    // this thread's key in a row of P: its chunk and byte
+    const int kp = frag_pos(warp, lane >> 3, lane & 7);
+    const uint32_t p_blk = (uint32_t)(kp >> 6) * R * 128, p_chunk = (uint32_t)((kp & 63) >> 3), p_byte = 2u * (kp & 7);
+    uint32_t page_tiles = 0, tc = 0, bad = 0u;   // tc: tiles of this CTA so far
+    bool ok = true;
+    const bool qal = ((uintptr_t)A.q & 15) == 0;
+    for (int it = i0; it < i1; ++it) {
+      const AttItem I = items[it];
+      const AttUnit u = units[I.unit];
+      const Tiles T = tiles_of<R>(A, u, I.row0);
+      auto row_at = [&](int r) {
+        return ((size_t)(u.tok0 + r / g) * A.hq + (size_t)u.kvh * g + r % g) * kHeadDim;
+      };
+      // ---- Q: 128 / R threads per row; scaled by a power of two so that its largest element is in [2^7, 2^8)
+      {
+        constexpr int kPer = 128 / R, kRuns = 16 / kPer;
+        const int n = tid / kPer, sub = tid % kPer;
+        const bool valid = n < T.rows;
+        const uint16_t* qr = A.q + row_at(I.row0 + (valid ? n : 0));
+        uint4 w[kRuns];
+#pragma unroll
+        for (int y = 0; y < kRuns; ++y) w[y] = load8(qr + 8 * (sub + kPer * y), qal);
+        float mx = 0.0f;
+#pragma unroll
+        for (int y = 0; y < kRuns; ++y) {
+          if (!valid) w[y] = make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t wd[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx = fmaxf(mx, fmaxf(fabsf(bf_f(wd[k] & 0xFFFFu)), fabsf(__uint_as_float(wd[k] & 0xFFFF0000u))));
+        }
+#pragma unroll
+        for (int o = kPer / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+        const int e = mx > 0.0f && mx < INFINITY ? max(-100, min(100, 7 - ilogbf(mx))) : 0;
+        const float mul = copysignf(__int_as_float((e + 127) << 23), A.scale_log2);
+#pragma unroll
+        for (int y = 0; y < kRuns; ++y) {
+          const int run = sub + kPer * y, gr = run >> 2, i = run & 3;
+          const uint32_t wd[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            f[2 * k] = bf_f(wd[k] & 0xFFFFu) * mul;
+            f[2 * k + 1] = __uint_as_float(wd[k] & 0xFFFF0000u) * mul;
+          }
+          // elements 0, 4, 1, 5 at frag_pos(gr, i, 0), elements 2, 6, 3, 7 sixteen places on
+          const int e0 = 32 * gr + 4 * i;
+          uint8_t* base = S.q + (e0 >> 6) * R * 128 + n * 128 + 8 * (i & 1);
+          const int c = (e0 & 63) >> 3;
+          *reinterpret_cast<uint2*>(base + ((c ^ (n & 7)) << 4)) = make_uint2(f16x2(f[0], f[4]), f16x2(f[1], f[5]));
+          *reinterpret_cast<uint2*>(base + (((c + 2) ^ (n & 7)) << 4)) = make_uint2(f16x2(f[2], f[6]), f16x2(f[3], f[7]));
+        }
+        if (sub == 0) {
+          // (a factor below 1e-30 makes every logit 0, as 1e-30 does; kNever times it must stay far below 0)
+          S.rfnm[n] = make_float2(fmaxf(fabsf(A.scale_log2) * __int_as_float((127 - e) << 23), 1e-30f), kUnseen);
+          S.m[n] = -INFINITY;
+          S.tree[n] = A.tree && valid ? A.tree[u.tok0 + (I.row0 + n) / g] : 0ull;
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      tm_fence_before();   // the previous item's O has been read
+      if (group_stop(false)) break;   // rows' factors are in place
+      if (lane == 0 && I.tile1 > I.tile0) mb_arrive(&S.q_full);
+
+      float l[R];
+#pragma unroll
+      for (int n = 0; n < R; ++n) l[n] = 0.0f;
+      bool unseen = true;   // some row has seen no key yet
+      bool stop = false;
+      for (int tile = I.tile0; tile < I.tile1; ++tile, ++tc) {
+        const uint32_t b = tc & 1u, ts = tl + kColS + 64u * b;
+        ok = __all_sync(0xFFFFFFFFu, mb_spin(&S.s_full[b], (tc >> 1) & 1u, gave_up));
+        // the P buffer of two tiles ago has been used
+        if (ok && tile >= I.tile0 + 2)
+          ok = __all_sync(0xFFFFFFFFu, mb_wait(&S.pv_done[b], ((tc >> 1) & 1u) ^ 1u, gave_up));
+        tm_fence_after();
+        // ---- rows n >= from see this thread's key (with a tree: those whose bit is set)
+        int from = R;
+        bool by_tree = false;
+        unsigned long long bit = 0ull;
+        if (tile < T.pages) {
+          const uint32_t lv = *(volatile uint32_t*)&S.live[page_tiles & (kMaskRing - 1)][warp];
+          if ((lv >> lane) & 1u) from = 0;
+          ++page_tiles;
+        } else if (tile < T.lists) {
+          if (128 * (tile - T.pages) + tid < u.n_fp) from = 0;
+        } else {
+          const int j = 128 * (tile - T.lists) + tid;
+          if (j < u.T) {
+            if (A.tree) {
+              by_tree = true;
+              bit = 1ull << j;   // u.T <= 64
+            } else {
+              const int64_t f = (int64_t)j * g - I.row0;
+              from = f > R ? R : (f < 0 ? 0 : (int)f);
+            }
+          }
+        }
+        const bool all_seen = __all_sync(0xFFFFFFFFu, from == 0);
+        constexpr int kC = R < 32 ? R : 32;   // columns at a time
+        uint32_t s[kC];
+        auto load = [&](int c) {
+          if constexpr (kC == 16) tm_ld<16>(s, ts + (uint32_t)c);
+          else tm_ld<32>(s, ts + (uint32_t)c);
+          tm_wait_ld();
+          if (!all_seen) {
+#pragma unroll
+            for (int n = 0; n < kC; ++n) {
+              const bool see = by_tree ? (S.tree[c + n] & bit) != 0ull : c + n >= from;
+              s[n] = see ? s[n] : __float_as_uint(kNever);
+            }
+          }
+        };
+        // ---- does a key exceed its row's maximum by too much?
+        float top = 0.0f;
+        if (ok && !unseen) {
+#pragma unroll
+          for (int c = 0; c < R; c += kC) {
+            load(c);
+#pragma unroll
+            for (int n = 0; n < kC; n += 2) {
+              const float4 f = *reinterpret_cast<const float4*>(&S.rfnm[c + n]);
+              float x, y;
+              fma2(x, y, __uint_as_float(s[n]), __uint_as_float(s[n + 1]), f.x, f.z, f.y, f.w);
+              top = fmaxf(fmaxf(top, x), y);
+            }
+          }
+        }
+        const bool mine = __any_sync(0xFFFFFFFFu, unseen || top > kHead + kGrow);
+        if (lane == 0) *(volatile uint32_t*)&S.grow[b][warp] = mine;
+        if (group_stop(!ok)) {
+          stop = true;
+          break;
+        }
+        const volatile uint32_t* gw = S.grow[b];
+        if (gw[0] | gw[1] | gw[2] | gw[3]) {
+          // ---- new maxima of all rows
+#pragma unroll
+          for (int c = 0; c < R; c += kC) {
+            load(c);
+            float keep = kNever;
+#pragma unroll
+            for (int n = 0; n < kC; ++n) {
+              const float v = __uint_as_float(s[n]);
+              const float w = warp_max_f(v == kNever ? kNever : fmaxf(v * S.rfnm[c + n].x, 0.9f * kNever));
+              if (lane == n) keep = w;
+            }
+            if (lane < kC) S.wmax[warp][c + lane] = keep;
+          }
+          if (tid == 0) S.unseen = 0u;
+          if (tile > I.tile0) ok = mb_wait(&S.pv_done[b ^ 1u], ((tc - 1u) >> 1) & 1u, gave_up);   // O is at rest
+          if (group_stop(!ok)) {
+            stop = true;
+            break;
+          }
+          if (tid < R) {
+            const float w = fmaxf(fmaxf(S.wmax[0][tid], S.wmax[1][tid]), fmaxf(S.wmax[2][tid], S.wmax[3][tid]));
+            const float mo = S.m[tid], mn = w > 0.95f * kNever ? fmaxf(mo, w) : mo;
+            S.m[tid] = mn;
+            S.fac[tid] = mo == -INFINITY ? 1.0f : ex2f(mo - mn);
+            S.rfnm[tid].y = mn == -INFINITY ? kUnseen : kHead - mn;
+            if (mn == -INFINITY && tid < T.rows) S.unseen = 1u;
+          }
+          group_stop(false);
+          unseen = *(volatile uint32_t*)&S.unseen != 0u;
+#pragma unroll
+          for (int n = 0; n < R; ++n) l[n] *= S.fac[n];
+          if (tile > I.tile0) {
+            tm_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < R; c += 16) {
+              uint32_t o[16];
+              tm_ld<16>(o, tl + kColO + (uint32_t)c);
+              tm_wait_ld();
+#pragma unroll
+              for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * S.fac[c + n]);
+              tm_st<16>(tl + kColO + (uint32_t)c, o);
+            }
+            tm_wait_st();
+          }
+        }
+        // ---- weights
+        uint8_t* pb = S.p[b] + p_blk + p_byte;
+#pragma unroll
+        for (int c = 0; c < R; c += kC) {
+          load(c);
+#pragma unroll
+          for (int n = 0; n < kC; n += 2) {
+            const float4 f = *reinterpret_cast<const float4*>(&S.rfnm[c + n]);
+            float x, y;
+            fma2(x, y, __uint_as_float(s[n]), __uint_as_float(s[n + 1]), f.x, f.z, f.y, f.w);
+            x = ex2f(x);
+            y = ex2f(y);
+            l[c + n] += x;
+            l[c + n + 1] += y;
+            const uint32_t h = f16x2(x, y);
+            *reinterpret_cast<uint16_t*>(pb + (c + n) * 128 + ((p_chunk ^ ((c + n) & 7)) << 4)) = (uint16_t)h;
+            *reinterpret_cast<uint16_t*>(pb + (c + n + 1) * 128 + ((p_chunk ^ ((c + n + 1) & 7)) << 4)) = (uint16_t)(h >> 16);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMAs read P
+        tm_fence_before();
+        __syncwarp();
+        if (lane == 0) mb_arrive(&S.p_full[b]);
+      }
+      if (stop) break;
+      // ---- result of the item: sums over the keys, then O
+      const bool some = I.tile1 > I.tile0;
+      if (some) ok = mb_wait(&S.pv_done[(tc - 1u) & 1u], ((tc - 1u) >> 1) & 1u, gave_up);
+#pragma unroll
+      for (int n = 0; n < R; ++n) {
+        float v = l[n];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+        if (lane == (n & 31)) S.wmax[warp][n] = v;
+      }
+      if (group_stop(!ok)) break;
+      tm_fence_after();
+      const bool whole = I.part < 0;
+      float* pp = part + (size_t)(whole ? 0 : I.part) * R * kAttPart;
+#pragma unroll 1
+      for (int c = 0; c < R; c += 16) {
+        uint32_t o[16];
+        if (some) {
+          tm_ld<16>(o, tl + kColO + (uint32_t)c);
+          tm_wait_ld();
+        } else {
+#pragma unroll
+          for (int n = 0; n < 16; ++n) o[n] = 0u;
+        }
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          if (c + n >= T.rows) break;
+          const float L = (S.wmax[0][c + n] + S.wmax[1][c + n]) + (S.wmax[2][c + n] + S.wmax[3][c + n]);
+          if (whole) {
+            const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);   // a NaN stays
+            const float v = __uint_as_float(o[n]) * inv;
+            if (!(fabsf(v) < INFINITY) || !(L < INFINITY)) bad = 1u;
+            A.out[row_at(I.row0 + c + n) + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+          } else {
+            pp[(size_t)(c + n) * kAttPart + tid] = __uint_as_float(o[n]);
+            if (!(L < INFINITY)) bad = 1u;
+            if (tid == 0) *reinterpret_cast<float2*>(pp + (size_t)(c + n) * kAttPart + kHeadDim) = make_float2(S.m[c + n], L);
+          }
+        }
+        __syncwarp();
+      }
+      if (group_stop(false)) break;   // the sums and maxima have been read
+    }
+    if (bad) atomicOr(A.status, kStatusRange);
+  } else if (warp < 12) {
+    // ----------------------------------------------------------- dequantize
+    const bool is_k = warp < 8;
+    const int w4 = warp & 3;                               // K: page; V: channel group
+    const int r = lane >> 2, i = lane & 3;
+    const uint32_t tl = tmem + ((uint32_t)w4 << 21);
+    uint32_t page_tiles = 0, tc = 0, bad = 0u;
+    const bool kal = (((uintptr_t)A.k | (uintptr_t)A.v) & 15) == 0;
+    bool ok = true;
+    uint64_t* full = is_k ? S.k_full : S.v_full;
+    uint64_t* empty = is_k ? S.k_empty : S.v_empty;
+    for (int it = i0; it < i1 && ok; ++it) {
+      const AttItem I = items[it];
+      const AttUnit u = units[I.unit];
+      const Tiles T = tiles_of<R>(A, u, I.row0);
+      for (int tile = I.tile0; tile < I.tile1; ++tile, ++tc) {
+        const uint32_t st = tc & 1u;
+        const uint32_t dst = tl + (is_k ? kColK : kColV) + 64u * st;
+        ok = mb_wait(&empty[st], ((tc >> 1) & 1u) ^ 1u, gave_up);
+        if (tile < T.pages) {
+          const uint32_t sg = page_tiles % kStages;
+          if (ok) ok = mb_wait(&S.raw_full[sg], (page_tiles / kStages) & 1u, gave_up, page_tiles ? kAttSpin : first_spins);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          ++page_tiles;
+          tm_fence_after();
+          if (is_k) {
+            const uint8_t* blk = S.raw[sg][w4];
+            const int cls = *(volatile int32_t*)&S.cls[sg][w4];
+#pragma unroll 1
+            for (int m = 0; m < 2; ++m) {                  // slots 16 m + r and 16 m + r + 8
+              const int t0 = 16 * m + r;
+              uint32_t a[4][4], b[4][4];
+              if (cls == kClsInt2) {
+#pragma unroll
+                for (int gr = 0; gr < 4; ++gr) {
+                  uint32_t sc[4], z[4];
+                  k_scales2(blk, gr, i, sc, z);
+                  k_run2(blk, t0, gr, i, sc, z, a[gr]);
+                  k_run2(blk, t0 + 8, gr, i, sc, z, b[gr]);
+                }
+              } else if (cls == kClsInt4) {
+                k_slot4(blk, t0, i, a);
+                k_slot4(blk, t0 + 8, i, b);
+              } else if (cls == kClsInt3) {
+                k_slot3(blk, t0, i, a);
+                k_slot3(blk, t0 + 8, i, b);
+              } else if (cls == kClsFp4) {
+                k_slotf(blk, t0, i, a);
+                k_slotf(blk, t0 + 8, i, b);
+              } else {
+#pragma unroll
+                for (int x = 0; x < 16; ++x) a[x >> 2][x & 3] = b[x >> 2][x & 3] = 0u;
+              }
+              tm_st_frag64(dst + ((uint32_t)(16 * m) << 16), a, b);
+            }
+          } else {
+#pragma unroll 1
+            for (int p = 0; p < 4; ++p) {
+              const uint8_t* blk = S.raw[sg][p];
+              const int cls = *(volatile int32_t*)&S.cls[sg][p];
+              uint32_t v[4][4];
+              if (cls == kClsInt2) {
+                v_group2(blk, w4, r, i, v);
+              } else if (cls == kClsInt4) {
+                v_group4(blk, w4, r, i, v);
+              } else if (cls == kClsInt3) {
+                v_group3(blk, w4, r, i, v);
+              } else if (cls == kClsFp4) {
+                v_groupf(blk, w4, r, i, v);
+              } else {
+#pragma unroll
+                for (int x = 0; x < 16; ++x) v[x >> 2][x & 3] = 0u;
+              }
+              tm_st_frag16(dst + 16u * p, v[0], v[1]);
+              tm_st_frag16(dst + 16u * p + (16u << 16), v[2], v[3]);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mb_arrive(&S.raw_empty[sg]);
+        } else {
+          // ---- bf16 rows: list tokens or new tokens (rows past the end: the last one is loaded and used as 0)
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          tm_fence_after();
+          const bool list = tile < T.lists;
+          const int j0 = 128 * (tile - (list ? T.pages : T.lists));
+          const int n = list ? u.n_fp : u.T;
+          const size_t stride = list ? kHeadDim : (size_t)A.hkv * kHeadDim;
+          const uint16_t* src =
+              list ? (is_k ? A.fpk : A.fpv) + ((size_t)u.req * A.hkv + u.kvh) * (size_t)A.fp_cap * kHeadDim
+                   : (is_k ? A.k : A.v) + ((size_t)u.tok0 * A.hkv + u.kvh) * kHeadDim;
+          if (is_k) {
+#pragma unroll 1
+            for (int m = 0; m < 2; ++m) {
+              uint32_t a[4][4], b[4][4];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int j = j0 + 32 * w4 + 16 * m + 8 * e + r, jc = min(j, n - 1);
+                uint4 y[4];
+#pragma unroll
+                for (int gr = 0; gr < 4; ++gr) {
+                  const int ch = 4 * gr + i;
+                  y[gr] = load8(src + (size_t)jc * stride + 8 * (list ? ch ^ (jc & 7) : ch), list || kal);
+                }
+#pragma unroll
+                for (int gr = 0; gr < 4; ++gr) {
+                  if (j >= n) y[gr] = make_uint4(0u, 0u, 0u, 0u);
+                  order8_f16(y[gr], 1.0f, e ? b[gr] : a[gr], bad);
+                }
+              }
+              tm_st_frag64(dst + ((uint32_t)(16 * m) << 16), a, b);
+            }
+          } else {
+#pragma unroll 1
+            for (int p = 0; p < 4; ++p) {
+              uint32_t v[4][4];
+              uint16_t y[4][8];
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const int jc = min(j0 + 32 * p + 8 * i + e, n - 1), c = 32 * w4 + 8 * x + r;
+                  y[x][e] = __ldg(src + (size_t)jc * stride + (list ? att_list_at(jc, c) : c));
+                }
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  f[e] = j0 + 32 * p + 8 * i + e < n ? in_range(bf_f(y[x][e]), bad) : 0.0f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[x][k] = f16x2(f[k], f[k + 4]);
+              }
+              tm_st_frag16(dst + 16u * p, v[0], v[1]);
+              tm_st_frag16(dst + 16u * p + (16u << 16), v[2], v[3]);
+            }
+          }
+        }
+        tm_wait_st();
+        tm_fence_before();
+        __syncwarp();
+        if (lane == 0) mb_arrive(&full[st]);
+      }
+    }
+    if (bad) atomicOr(A.status, kStatusRange);
+  } else if (warp == 12) {
+    // ------------------------------------------------------------------ MMA
+    if (lane == 0) {
+      constexpr uint32_t idesc = mma_idesc(128, R);
+      const uint64_t qd = sw128_desc(sm32(S.q)), pd0 = sw128_desc(sm32(S.p[0])), pd1 = sw128_desc(sm32(S.p[1]));
+      uint32_t tc0 = 0, q_phase = 0;
+      bool ok = true;
+      for (int it = i0; it < i1 && ok; ++it) {
+        const AttItem I = items[it];
+        const uint32_t n = (uint32_t)(I.tile1 - I.tile0);
+        if (n == 0) continue;
+        ok = mb_wait(&S.q_full, q_phase, gave_up);
+        q_phase ^= 1u;
+        // a step: Q K^T of tile t, then P V of tile t - 1
+#pragma unroll 1
+        for (uint32_t t = 0; t <= n && ok; ++t) {
+          const uint32_t tc = tc0 + t, b = tc & 1u;
+          if (t < n) {
+            ok = mb_wait(&S.k_full[b], (tc >> 1) & 1u, gave_up);
+            if (!ok) break;
+            tm_fence_after();
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              mma_ts(tmem + kColS + 64u * b, tmem + kColK + 64u * b + 8u * s, qd + ((s >> 2) * (R * 8) + (s & 3) * 2), idesc, s > 0);
+            tm_commit(&S.s_full[b]);
+            tm_commit(&S.k_empty[b]);
+          }
+          if (t > 0) {
+            const uint32_t pc = tc - 1u, pb = pc & 1u;
+            ok = mb_wait(&S.v_full[pb], (pc >> 1) & 1u, gave_up) && mb_spin(&S.p_full[pb], (pc >> 1) & 1u, gave_up);
+            if (!ok) break;
+            tm_fence_after();
+            const uint64_t pd = pb ? pd1 : pd0;
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              mma_ts(tmem + kColO, tmem + kColV + 64u * pb + 8u * s, pd + ((s >> 2) * (R * 8) + (s & 3) * 2), idesc, t > 1 || s > 0);
+            tm_commit(&S.v_empty[pb]);
+            tm_commit(&S.pv_done[pb]);
+          }
+        }
+        tc0 += n;
+      }
+      if (!ok) {   // let the MMAs that were issued finish before TMEM is given back
+        volatile uint32_t never = 0u;
+        tm_commit(&S.drain);
+        mb_wait(&S.drain, 0u, &never);
+      }
+    }
+    __syncwarp();
+  } else {
+    // --------------------------------------------------------------- loader
+    uint32_t page_tiles = 0, issued = 0;   // issued: tiles whose page this lane has issued
+    bool ok = true;
+    for (int it = i0; it < i1 && ok; ++it) {
+      const AttItem I = items[it];
+      const AttUnit u = units[I.unit];
+      const Tiles T = tiles_of<R>(A, u, I.row0);
+      const Entry* tab = A.table + (size_t)u.req * A.max_pages;
+      const int end = min(I.tile1, T.pages);
+      for (int tile = I.tile0; tile < end; ++tile, ++page_tiles) {
+        if (lane < 4) {
+          const uint32_t sg = page_tiles % kStages;
+          const int pi = 4 * tile + lane;
+          Entry e{-1, 0u};
+          int cls = -1;
+          const uint8_t* blk = nullptr;
+          if (pi < u.n_pages) {
+            e = tab[pi];
+            if (A.hdead) e.live &= ~A.hdead[(size_t)e.id * A.hkv + u.kvh];
+            if (e.live) cls = att_page(A, e.id, u.kvh, blk);
+          }
+          ok = mb_wait(&S.raw_empty[sg], ((page_tiles / kStages) & 1u) ^ 1u, gave_up);
+          if (ok) {
+            *(volatile int32_t*)&S.cls[sg][lane] = cls;
+            *(volatile uint32_t*)&S.live[page_tiles & (kMaskRing - 1)][lane] = e.live;
+            ++issued;
+            if (cls < 0)
+              mb_arrive(&S.raw_full[sg]);
+            else
+              bulk_to_smem(S.raw[sg][lane], blk,
+                           cls == kClsInt2 ? kInt2Block : (cls == kClsInt4 ? kInt4Block : (cls == kClsInt3 ? kInt3Block : kFp4Block)),
+                           &S.raw_full[sg]);
+          }
+        }
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+      }
+    }
+    // Every copy has landed before the CTA leaves.  A tile of which only some lanes got to issue never
+    // completes its barrier; those lanes' copies are waited for by time (the bound of the wait).
+    const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, issued);
+    if (lane == 0) {
+      volatile uint32_t never = 0u;
+      for (uint32_t y = most > kStages ? most - kStages : 0u; y < most; ++y)
+        mb_wait(&S.raw_full[y % kStages], (y / kStages) & 1u, &never);
+    }
+    __syncwarp();
+  }
+  tm_fence_before();
+  __syncthreads();
+  if (tid == 0 && *gave_up) atomicOr(A.status, kStatusTimeout);
+  if (warp == 12) {
+    tm_fence_after();
+    tm_free(tmem, 512);
+  }
+}
+
+template <int R>
+cudaError_t launch_r(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const AttItem* d_items,
+                     const int32_t* d_cta_item, int n_ctas, float* d_part, cudaStream_t s) {
+  static std::atomic<uint64_t> attr_set{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!(attr_set.load() >> dev & 1u)) {
+    const cudaError_t e = cudaFuncSetAttribute(attend_few_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)sizeof(FewSmem<R>));
+    if (e != cudaSuccess) return e;
+    attr_set.fetch_or(uint64_t(1) << dev);
+  }
+  ++P->launches;
+  attend_few_kernel<R><<<(unsigned)n_ctas, kThreads, sizeof(FewSmem<R>), s>>>(
+      A, d_units, d_items, d_cta_item, d_part, P->first_wait_spins < 0 ? kAttSpin : (uint32_t)P->first_wait_spins);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attend_few(kv_pool* P, int rows, const AttArgs& A, const AttUnit* d_units, const AttItem* d_items,
+                              const int32_t* d_cta_item, int n_ctas, float* d_part, cudaStream_t s) {
+  if (n_ctas <= 0) return cudaSuccess;
+  switch (rows) {
+    case 16: return launch_r<16>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s);
+    case 32: return launch_r<32>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s);
+    case 64: return launch_r<64>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace kvq
