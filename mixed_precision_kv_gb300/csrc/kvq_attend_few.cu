@@ -30,29 +30,30 @@
 namespace kvq {
 namespace {
 
-constexpr int kStages = 7;                      // raw tiles in flight
-constexpr int kWarps = 14;
+constexpr int kStages = 6;                      // raw tiles in flight
+constexpr int kWarps = 19;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaskRing = 16;                   // tiles whose live words are kept
 constexpr float kHead = 7.0f;                   // P = 2^(x - m + 7)
 constexpr float kGrow = 8.0f;                   // a maximum may be stale by this much (base 2)
 constexpr float kNever = -3.0e38f;              // S of a key that is not seen
 constexpr float kUnseen = -1.0e30f;             // kHead - m of a row that has seen nothing: its weights are 0
-// TMEM columns
-constexpr uint32_t kColK = 0, kColV = 128, kColS = 256, kColO = 384;
+// TMEM columns (two stages of K, V and S; kColOne: the ones of the sums, for R <= 32)
+constexpr uint32_t kColK = 0, kColV = 128, kColS = 256, kColO = 384, kColL = 448, kColOne = 480;
 
 template <int R>
 struct alignas(1024) FewSmem {
   uint8_t q[R * 256], p[2][R * 256];            // operand rows of 128 elements, 128-byte swizzled
+  uint8_t one[R == 64 ? 16384 : 16];            // ones (R = 64: TMEM has no columns left for them)
   alignas(128) uint8_t raw[kStages][4][kInt4Block];
   float2 rfnm[R];                               // per row: factor of S, kHead - m
   float m[R], fac[R], wmax[4][R];
   unsigned long long tree[R];
   uint32_t live[kMaskRing][4];
   int32_t cls[kStages][4];
-  uint32_t grow[2][4];
+  uint32_t grow[2][8];
   uint64_t raw_full[kStages], raw_empty[kStages];
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2], q_full, drain;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2], q_full, drain[2];
   uint32_t tmem, gave_up, unseen;
 };
 static_assert(sizeof(FewSmem<64>) <= 232448, "one CTA's shared memory");
@@ -96,12 +97,18 @@ __device__ __forceinline__ float warp_max_f(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(y) : "f"(x));
   return y;
 }
-// Barrier of the softmax warpgroup; true if any thread gives `stop` (every thread
+// Barrier of the softmax warps; true if any thread gives `stop` (every thread
 // gets the same answer, so all leave together).
 __device__ __forceinline__ bool group_stop(bool stop) {
   uint32_t r;
-  asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, 1, 128, a;\n selp.u32 %0, 1, 0, b;\n}"
+  asm volatile("{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n barrier.cta.red.or.pred b, 1, 256, a;\n selp.u32 %0, 1, 0, b;\n}"
                : "=r"(r) : "r"((uint32_t)stop) : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
   return r != 0;
 }
 
@@ -125,30 +132,43 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
       mb_init(&S.v_full[x], 4);
       mb_init(&S.v_empty[x], 1);
       mb_init(&S.s_full[x], 1);
-      mb_init(&S.p_full[x], 4);
+      mb_init(&S.p_full[x], 8);
       mb_init(&S.pv_done[x], 1);
     }
-    mb_init(&S.q_full, 4);
-    mb_init(&S.drain, 1);
+    mb_init(&S.q_full, 8);
+    mb_init(&S.drain[0], 1);
+    mb_init(&S.drain[1], 1);
     S.gave_up = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 12) tm_alloc(&S.tmem, 512);
+  if (warp == 16) tm_alloc(&S.tmem, 512);
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
   const uint32_t tmem = S.tmem;
   const int g = A.hq / A.hkv;
 
-  if (warp < 4) {
+  if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    const uint32_t tl = tmem + ((uint32_t)warp << 21);
+    // hf: the half of the columns (rows of the block) of this warp; its 32 keys are those of page warp & 3
+    constexpr int kC = R / 2;
+    const int hf = warp >> 2, c0 = hf * kC, wq = warp & 3, key = tid & 127;
+    const uint32_t tl = tmem + ((uint32_t)wq << 21);
     // this thread's key in a row of P: its chunk and byte
-    const int kp = frag_pos(warp, lane >> 3, lane & 7);
-    const uint32_t p_blk = (uint32_t)(kp >> 6) * R * 128, p_chunk = (uint32_t)((kp & 63) >> 3), p_byte = 2u * (kp & 7);
+    const int kp = frag_pos(wq, lane >> 3, lane & 7);
+    const uint32_t p_off = (uint32_t)(kp >> 6) * R * 128 + (uint32_t)c0 * 128 + 2u * (kp & 7), p_chunk = (uint32_t)((kp & 63) >> 3);
     uint32_t page_tiles = 0, tc = 0, bad = 0u;   // tc: tiles of this CTA so far
     bool ok = true;
     const bool qal = ((uintptr_t)A.q & 15) == 0;
+    if constexpr (R == 64) {
+      for (int x = tid; x < 1024; x += 256) reinterpret_cast<uint4*>(S.one)[x] = make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u);
+    } else if (hf == 0) {
+      uint32_t w[16];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) w[x] = 0x3C003C00u;
+      tm_st<16>(tl + kColOne, w);
+      tm_wait_st();
+    }
     for (int it = i0; it < i1; ++it) {
       const AttItem I = items[it];
       const AttUnit u = units[I.unit];
@@ -156,9 +176,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
       auto row_at = [&](int r) {
         return ((size_t)(u.tok0 + r / g) * A.hq + (size_t)u.kvh * g + r % g) * kHeadDim;
       };
-      // ---- Q: 128 / R threads per row; scaled by a power of two so that its largest element is in [2^7, 2^8)
+      // ---- Q: 256 / R threads per row; scaled by a power of two so that its largest element is in [2^7, 2^8)
       {
-        constexpr int kPer = 128 / R, kRuns = 16 / kPer;
+        constexpr int kPer = R == 16 ? 16 : 256 / R, kRuns = 16 / kPer;
         const int n = tid / kPer, sub = tid % kPer;
         const bool valid = n < T.rows;
         const uint16_t* qr = A.q + row_at(I.row0 + (valid ? n : 0));
@@ -207,91 +227,75 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
       if (group_stop(false)) break;   // rows' factors are in place
       if (lane == 0 && I.tile1 > I.tile0) mb_arrive(&S.q_full);
 
-      float l[R];
-#pragma unroll
-      for (int n = 0; n < R; ++n) l[n] = 0.0f;
       bool unseen = true;   // some row has seen no key yet
       bool stop = false;
+#pragma unroll 1
       for (int tile = I.tile0; tile < I.tile1; ++tile, ++tc) {
-        const uint32_t b = tc & 1u, ts = tl + kColS + 64u * b;
-        ok = __all_sync(0xFFFFFFFFu, mb_spin(&S.s_full[b], (tc >> 1) & 1u, gave_up));
-        // the P buffer of two tiles ago has been used
-        if (ok && tile >= I.tile0 + 2)
-          ok = __all_sync(0xFFFFFFFFu, mb_wait(&S.pv_done[b], ((tc >> 1) & 1u) ^ 1u, gave_up));
-        tm_fence_after();
-        // ---- rows n >= from see this thread's key (with a tree: those whose bit is set)
-        int from = R;
-        bool by_tree = false;
-        unsigned long long bit = 0ull;
+        const uint32_t b = tc & 1u, ts = tl + kColS + 64u * b + (uint32_t)c0;
+        // ---- rows of this half that see this thread's key, as bits
+        uint32_t vis = 0u;
+        bool live_ring = false;
         if (tile < T.pages) {
-          const uint32_t lv = *(volatile uint32_t*)&S.live[page_tiles & (kMaskRing - 1)][warp];
-          if ((lv >> lane) & 1u) from = 0;
-          ++page_tiles;
+          live_ring = true;
         } else if (tile < T.lists) {
-          if (128 * (tile - T.pages) + tid < u.n_fp) from = 0;
+          if (128 * (tile - T.pages) + key < u.n_fp) vis = 0xFFFFFFFFu;
         } else {
-          const int j = 128 * (tile - T.lists) + tid;
+          const int j = 128 * (tile - T.lists) + key;
           if (j < u.T) {
-            if (A.tree) {
-              by_tree = true;
-              bit = 1ull << j;   // u.T <= 64
+            if (A.tree) {   // u.T <= 64
+#pragma unroll 1
+              for (int n = 0; n < kC; ++n) vis |= ((S.tree[c0 + n] >> j) & 1ull) ? 1u << n : 0u;
             } else {
-              const int64_t f = (int64_t)j * g - I.row0;
-              from = f > R ? R : (f < 0 ? 0 : (int)f);
+              const int64_t f = (int64_t)j * g - I.row0 - c0;   // rows from f on
+              vis = f >= 32 ? 0u : (f <= 0 ? 0xFFFFFFFFu : 0xFFFFFFFFu << f);
             }
           }
         }
-        const bool all_seen = __all_sync(0xFFFFFFFFu, from == 0);
-        constexpr int kC = R < 32 ? R : 32;   // columns at a time
+        ok = __all_sync(0xFFFFFFFFu, mb_spin(&S.s_full[b], (tc >> 1) & 1u, gave_up));
+        tm_fence_after();
+        if (live_ring) {
+          const uint32_t lv = *(volatile uint32_t*)&S.live[page_tiles & (kMaskRing - 1)][wq];
+          vis = ((lv >> lane) & 1u) ? 0xFFFFFFFFu : 0u;
+          ++page_tiles;
+        }
         uint32_t s[kC];
-        auto load = [&](int c) {
-          if constexpr (kC == 16) tm_ld<16>(s, ts + (uint32_t)c);
-          else tm_ld<32>(s, ts + (uint32_t)c);
-          tm_wait_ld();
-          if (!all_seen) {
+        if constexpr (kC == 8) tm_ld<8>(s, ts);
+        else if constexpr (kC == 16) tm_ld<16>(s, ts);
+        else tm_ld<32>(s, ts);
+        tm_wait_ld();
+        if (!__all_sync(0xFFFFFFFFu, vis == 0xFFFFFFFFu)) {
 #pragma unroll
-            for (int n = 0; n < kC; ++n) {
-              const bool see = by_tree ? (S.tree[c + n] & bit) != 0ull : c + n >= from;
-              s[n] = see ? s[n] : __float_as_uint(kNever);
-            }
-          }
-        };
-        // ---- does a key exceed its row's maximum by too much?
-        float top = 0.0f;
-        if (ok && !unseen) {
+          for (int n = 0; n < kC; ++n) s[n] = ((vis >> n) & 1u) ? s[n] : __float_as_uint(kNever);
+        }
+        // ---- x = S rf + 7 - m; does a key exceed its row's maximum by too much?
+        const float4* fr = reinterpret_cast<const float4*>(&S.rfnm[c0]);
+        float x[kC], top = 0.0f;
 #pragma unroll
-          for (int c = 0; c < R; c += kC) {
-            load(c);
-#pragma unroll
-            for (int n = 0; n < kC; n += 2) {
-              const float4 f = *reinterpret_cast<const float4*>(&S.rfnm[c + n]);
-              float x, y;
-              fma2(x, y, __uint_as_float(s[n]), __uint_as_float(s[n + 1]), f.x, f.z, f.y, f.w);
-              top = fmaxf(fmaxf(top, x), y);
-            }
-          }
+        for (int n = 0; n < kC; n += 2) {
+          const float4 f = fr[n >> 1];
+          fma2(x[n], x[n + 1], __uint_as_float(s[n]), __uint_as_float(s[n + 1]), f.x, f.z, f.y, f.w);
+          top = fmaxf(fmaxf(top, x[n]), x[n + 1]);
         }
         const bool mine = __any_sync(0xFFFFFFFFu, unseen || top > kHead + kGrow);
         if (lane == 0) *(volatile uint32_t*)&S.grow[b][warp] = mine;
+        // the P buffer of two tiles ago has been used
+        if (ok && tile >= I.tile0 + 2)
+          ok = __all_sync(0xFFFFFFFFu, mb_wait(&S.pv_done[b], ((tc >> 1) & 1u) ^ 1u, gave_up));
         if (group_stop(!ok)) {
           stop = true;
           break;
         }
-        const volatile uint32_t* gw = S.grow[b];
-        if (gw[0] | gw[1] | gw[2] | gw[3]) {
+        const uint4 g0 = *reinterpret_cast<const uint4*>(&S.grow[b][0]), g1 = *reinterpret_cast<const uint4*>(&S.grow[b][4]);
+        if (g0.x | g0.y | g0.z | g0.w | g1.x | g1.y | g1.z | g1.w) {
           // ---- new maxima of all rows
+          float keep = kNever;
 #pragma unroll
-          for (int c = 0; c < R; c += kC) {
-            load(c);
-            float keep = kNever;
-#pragma unroll
-            for (int n = 0; n < kC; ++n) {
-              const float v = __uint_as_float(s[n]);
-              const float w = warp_max_f(v == kNever ? kNever : fmaxf(v * S.rfnm[c + n].x, 0.9f * kNever));
-              if (lane == n) keep = w;
-            }
-            if (lane < kC) S.wmax[warp][c + lane] = keep;
+          for (int n = 0; n < kC; ++n) {
+            const float v = __uint_as_float(s[n]);
+            const float w = warp_max_f(v == kNever ? kNever : fmaxf(v * S.rfnm[c0 + n].x, 0.9f * kNever));
+            if (lane == n) keep = w;
           }
+          if (lane < kC) S.wmax[wq][c0 + lane] = keep;
           if (tid == 0) S.unseen = 0u;
           if (tile > I.tile0) ok = mb_wait(&S.pv_done[b ^ 1u], ((tc - 1u) >> 1) & 1u, gave_up);   // O is at rest
           if (group_stop(!ok)) {
@@ -309,39 +313,35 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
           group_stop(false);
           unseen = *(volatile uint32_t*)&S.unseen != 0u;
 #pragma unroll
-          for (int n = 0; n < R; ++n) l[n] *= S.fac[n];
-          if (tile > I.tile0) {
+          for (int n = 0; n < kC; n += 2) {
+            const float4 f = fr[n >> 1];
+            fma2(x[n], x[n + 1], __uint_as_float(s[n]), __uint_as_float(s[n + 1]), f.x, f.z, f.y, f.w);
+          }
+          if (tile > I.tile0) {   // O and the sums
             tm_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < R; c += 16) {
-              uint32_t o[16];
-              tm_ld<16>(o, tl + kColO + (uint32_t)c);
-              tm_wait_ld();
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t at = tl + (y ? kColL : kColO) + (uint32_t)c0;
+#pragma unroll 1
+              for (int c = 0; c < kC; c += 8) {
+                uint32_t o[8];
+                tm_ld<8>(o, at + (uint32_t)c);
+                tm_wait_ld();
 #pragma unroll
-              for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * S.fac[c + n]);
-              tm_st<16>(tl + kColO + (uint32_t)c, o);
+                for (int n = 0; n < 8; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * S.fac[c0 + c + n]);
+                tm_st<8>(at + (uint32_t)c, o);
+              }
             }
             tm_wait_st();
           }
         }
         // ---- weights
-        uint8_t* pb = S.p[b] + p_blk + p_byte;
+        uint8_t* pb = S.p[b] + p_off;
 #pragma unroll
-        for (int c = 0; c < R; c += kC) {
-          load(c);
-#pragma unroll
-          for (int n = 0; n < kC; n += 2) {
-            const float4 f = *reinterpret_cast<const float4*>(&S.rfnm[c + n]);
-            float x, y;
-            fma2(x, y, __uint_as_float(s[n]), __uint_as_float(s[n + 1]), f.x, f.z, f.y, f.w);
-            x = ex2f(x);
-            y = ex2f(y);
-            l[c + n] += x;
-            l[c + n + 1] += y;
-            const uint32_t h = f16x2(x, y);
-            *reinterpret_cast<uint16_t*>(pb + (c + n) * 128 + ((p_chunk ^ ((c + n) & 7)) << 4)) = (uint16_t)h;
-            *reinterpret_cast<uint16_t*>(pb + (c + n + 1) * 128 + ((p_chunk ^ ((c + n + 1) & 7)) << 4)) = (uint16_t)(h >> 16);
-          }
+        for (int n = 0; n < kC; n += 2) {
+          const uint32_t h = f16x2(ex2f(x[n]), ex2f(x[n + 1]));
+          *reinterpret_cast<uint16_t*>(pb + n * 128 + ((p_chunk ^ (n & 7)) << 4)) = (uint16_t)h;
+          *reinterpret_cast<uint16_t*>(pb + (n + 1) * 128 + ((p_chunk ^ ((n + 1) & 7)) << 4)) = (uint16_t)(h >> 16);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMAs read P
         tm_fence_before();
@@ -349,53 +349,47 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
         if (lane == 0) mb_arrive(&S.p_full[b]);
       }
       if (stop) break;
-      // ---- result of the item: sums over the keys, then O
+      // ---- result of the item: O and the sums (every lane holds them)
       const bool some = I.tile1 > I.tile0;
       if (some) ok = mb_wait(&S.pv_done[(tc - 1u) & 1u], ((tc - 1u) >> 1) & 1u, gave_up);
-#pragma unroll
-      for (int n = 0; n < R; ++n) {
-        float v = l[n];
-#pragma unroll
-        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        if (lane == (n & 31)) S.wmax[warp][n] = v;
-      }
       if (group_stop(!ok)) break;
       tm_fence_after();
       const bool whole = I.part < 0;
       float* pp = part + (size_t)(whole ? 0 : I.part) * R * kAttPart;
 #pragma unroll 1
-      for (int c = 0; c < R; c += 16) {
-        uint32_t o[16];
+      for (int c = c0; c < c0 + kC; c += 8) {
+        uint32_t o[8], ls[8];
         if (some) {
-          tm_ld<16>(o, tl + kColO + (uint32_t)c);
+          tm_ld<8>(o, tl + kColO + (uint32_t)c);
+          tm_ld<8>(ls, tl + kColL + (uint32_t)c);
           tm_wait_ld();
         } else {
 #pragma unroll
-          for (int n = 0; n < 16; ++n) o[n] = 0u;
+          for (int n = 0; n < 8; ++n) o[n] = ls[n] = 0u;
         }
 #pragma unroll
-        for (int n = 0; n < 16; ++n) {
+        for (int n = 0; n < 8; ++n) {
           if (c + n >= T.rows) break;
-          const float L = (S.wmax[0][c + n] + S.wmax[1][c + n]) + (S.wmax[2][c + n] + S.wmax[3][c + n]);
+          const float L = __uint_as_float(ls[n]);
+          if (!(L < INFINITY)) bad = 1u;
           if (whole) {
             const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);   // a NaN stays
             const float v = __uint_as_float(o[n]) * inv;
-            if (!(fabsf(v) < INFINITY) || !(L < INFINITY)) bad = 1u;
-            A.out[row_at(I.row0 + c + n) + tid] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            if (!(fabsf(v) < INFINITY)) bad = 1u;
+            A.out[row_at(I.row0 + c + n) + key] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
           } else {
-            pp[(size_t)(c + n) * kAttPart + tid] = __uint_as_float(o[n]);
-            if (!(L < INFINITY)) bad = 1u;
-            if (tid == 0) *reinterpret_cast<float2*>(pp + (size_t)(c + n) * kAttPart + kHeadDim) = make_float2(S.m[c + n], L);
+            pp[(size_t)(c + n) * kAttPart + key] = __uint_as_float(o[n]);
+            if (key == 0) *reinterpret_cast<float2*>(pp + (size_t)(c + n) * kAttPart + kHeadDim) = make_float2(S.m[c + n], L);
           }
         }
         __syncwarp();
       }
-      if (group_stop(false)) break;   // the sums and maxima have been read
+      if (group_stop(false)) break;   // the maxima have been read
     }
     if (bad) atomicOr(A.status, kStatusRange);
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     // ----------------------------------------------------------- dequantize
-    const bool is_k = warp < 8;
+    const bool is_k = warp < 12;
     const int w4 = warp & 3;                               // K: page; V: channel group
     const int r = lane >> 2, i = lane & 3;
     const uint32_t tl = tmem + ((uint32_t)w4 << 21);
@@ -422,32 +416,37 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
           if (is_k) {
             const uint8_t* blk = S.raw[sg][w4];
             const int cls = *(volatile int32_t*)&S.cls[sg][w4];
+            if (cls == kClsInt2) {
+              // a run of 8 channels at a time: its scales serve the lane's four slots
 #pragma unroll 1
-            for (int m = 0; m < 2; ++m) {                  // slots 16 m + r and 16 m + r + 8
-              const int t0 = 16 * m + r;
-              uint32_t a[4][4], b[4][4];
-              if (cls == kClsInt2) {
+              for (int gr = 0; gr < 4; ++gr) {
+                uint32_t sc[4], z[4], a[4][4];
+                k_scales2(blk, gr, i, sc, z);
 #pragma unroll
-                for (int gr = 0; gr < 4; ++gr) {
-                  uint32_t sc[4], z[4];
-                  k_scales2(blk, gr, i, sc, z);
-                  k_run2(blk, t0, gr, i, sc, z, a[gr]);
-                  k_run2(blk, t0 + 8, gr, i, sc, z, b[gr]);
-                }
-              } else if (cls == kClsInt4) {
-                k_slot4(blk, t0, i, a);
-                k_slot4(blk, t0 + 8, i, b);
-              } else if (cls == kClsInt3) {
-                k_slot3(blk, t0, i, a);
-                k_slot3(blk, t0 + 8, i, b);
-              } else if (cls == kClsFp4) {
-                k_slotf(blk, t0, i, a);
-                k_slotf(blk, t0 + 8, i, b);
-              } else {
-#pragma unroll
-                for (int x = 0; x < 16; ++x) a[x >> 2][x & 3] = b[x >> 2][x & 3] = 0u;
+                for (int x = 0; x < 4; ++x) k_run2(blk, 8 * x + r, gr, i, sc, z, a[x]);
+                tm_st_frag16(dst + 16u * gr, a[0], a[1]);
+                tm_st_frag16(dst + 16u * gr + (16u << 16), a[2], a[3]);
               }
-              tm_st_frag64(dst + ((uint32_t)(16 * m) << 16), a, b);
+            } else {
+#pragma unroll 1
+              for (int m = 0; m < 2; ++m) {                // slots 16 m + r and 16 m + r + 8
+                const int t0 = 16 * m + r;
+                uint32_t a[4][4], b[4][4];
+                if (cls == kClsInt4) {
+                  k_slot4(blk, t0, i, a);
+                  k_slot4(blk, t0 + 8, i, b);
+                } else if (cls == kClsInt3) {
+                  k_slot3(blk, t0, i, a);
+                  k_slot3(blk, t0 + 8, i, b);
+                } else if (cls == kClsFp4) {
+                  k_slotf(blk, t0, i, a);
+                  k_slotf(blk, t0 + 8, i, b);
+                } else {
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) a[x >> 2][x & 3] = b[x >> 2][x & 3] = 0u;
+                }
+                tm_st_frag64(dst + ((uint32_t)(16 * m) << 16), a, b);
+              }
             }
           } else {
 #pragma unroll 1
@@ -539,53 +538,64 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
       }
     }
     if (bad) atomicOr(A.status, kStatusRange);
-  } else if (warp == 12) {
-    // ------------------------------------------------------------------ MMA
-    if (lane == 0) {
-      constexpr uint32_t idesc = mma_idesc(128, R);
-      const uint64_t qd = sw128_desc(sm32(S.q)), pd0 = sw128_desc(sm32(S.p[0])), pd1 = sw128_desc(sm32(S.p[1]));
-      uint32_t tc0 = 0, q_phase = 0;
-      bool ok = true;
-      for (int it = i0; it < i1 && ok; ++it) {
-        const AttItem I = items[it];
-        const uint32_t n = (uint32_t)(I.tile1 - I.tile0);
-        if (n == 0) continue;
-        ok = mb_wait(&S.q_full, q_phase, gave_up);
-        q_phase ^= 1u;
-        // a step: Q K^T of tile t, then P V of tile t - 1
+  } else if (warp < 18) {
+    // ------------------------------------------- MMA: warp 16 Q K^T, warp 17 P V and the sums of P
+    // The whole warp runs the loop and one elected lane issues: with operands that the compiler knows to
+    // be the same in all lanes an MMA of N = 32 issues every 21 cycles, from a branch on the lane every 47.
+    constexpr uint32_t idesc = mma_idesc(128, R);
+    const bool is_qk = warp == 16;
+    const uint64_t qd = sw128_desc(sm32(S.q)), pd0 = sw128_desc(sm32(S.p[0])), od = sw128_desc(sm32(S.one));
+    constexpr uint32_t kP16 = R * 16;   // one P buffer, in units of 16 bytes
+    uint32_t tc = 0, q_phase = 0;
+    bool ok = true;
+    for (int it = i0; it < i1 && ok; ++it) {
+      const AttItem I = items[it];
+      const int n = I.tile1 - I.tile0;
+      if (n == 0) continue;
+      ok = mb_wait(&S.q_full, q_phase, gave_up);
+      q_phase ^= 1u;
 #pragma unroll 1
-        for (uint32_t t = 0; t <= n && ok; ++t) {
-          const uint32_t tc = tc0 + t, b = tc & 1u;
-          if (t < n) {
-            ok = mb_wait(&S.k_full[b], (tc >> 1) & 1u, gave_up);
-            if (!ok) break;
-            tm_fence_after();
+      for (int t = 0; t < n; ++t, ++tc) {
+        const uint32_t b = tc & 1u, ph = (tc >> 1) & 1u;
+        if (is_qk) {
+          ok = ok && mb_wait(&S.k_full[b], ph, gave_up);
+          if (ok && tc >= 2u) ok = mb_wait(&S.p_full[b], ph ^ 1u, gave_up);   // S of two tiles ago has been read
+        } else {
+          ok = ok && mb_wait(&S.v_full[b], ph, gave_up) && mb_spin(&S.p_full[b], ph, gave_up);
+        }
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tm_fence_after();
+        if (is_qk) {
+          if (elect_one()) {
 #pragma unroll
             for (int s = 0; s < 8; ++s)
               mma_ts(tmem + kColS + 64u * b, tmem + kColK + 64u * b + 8u * s, qd + ((s >> 2) * (R * 8) + (s & 3) * 2), idesc, s > 0);
             tm_commit(&S.s_full[b]);
             tm_commit(&S.k_empty[b]);
           }
-          if (t > 0) {
-            const uint32_t pc = tc - 1u, pb = pc & 1u;
-            ok = mb_wait(&S.v_full[pb], (pc >> 1) & 1u, gave_up) && mb_spin(&S.p_full[pb], (pc >> 1) & 1u, gave_up);
-            if (!ok) break;
-            tm_fence_after();
-            const uint64_t pd = pb ? pd1 : pd0;
+        } else {
+          const uint64_t pd = pd0 + b * kP16;
+          if (elect_one()) {
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
-              mma_ts(tmem + kColO, tmem + kColV + 64u * pb + 8u * s, pd + ((s >> 2) * (R * 8) + (s & 3) * 2), idesc, t > 1 || s > 0);
-            tm_commit(&S.v_empty[pb]);
-            tm_commit(&S.pv_done[pb]);
+            for (int s = 0; s < 8; ++s) {
+              const uint64_t at = pd + ((s >> 2) * (R * 8) + (s & 3) * 2);
+              mma_ts(tmem + kColO, tmem + kColV + 64u * b + 8u * s, at, idesc, t > 0 || s > 0);
+              if constexpr (R == 64) mma_ss(tmem + kColL, od, at, idesc, t > 0 || s > 0);
+              else mma_ts(tmem + kColL, tmem + kColOne, at, idesc, t > 0 || s > 0);
+            }
+            tm_commit(&S.v_empty[b]);
+            tm_commit(&S.pv_done[b]);
           }
         }
-        tc0 += n;
+        __syncwarp();
       }
-      if (!ok) {   // let the MMAs that were issued finish before TMEM is given back
-        volatile uint32_t never = 0u;
-        tm_commit(&S.drain);
-        mb_wait(&S.drain, 0u, &never);
-      }
+    }
+    if (!ok) {   // let the MMAs that were issued finish before TMEM is given back
+      volatile uint32_t never = 0u;
+      if (elect_one()) tm_commit(&S.drain[is_qk ? 0 : 1]);
+      __syncwarp();
+      mb_wait(&S.drain[is_qk ? 0 : 1], 0u, &never);
     }
     __syncwarp();
   } else {
@@ -640,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
   tm_fence_before();
   __syncthreads();
   if (tid == 0 && *gave_up) atomicOr(A.status, kStatusTimeout);
-  if (warp == 12) {
+  if (warp == 16) {
     tm_fence_after();
     tm_free(tmem, 512);
   }

@@ -132,6 +132,11 @@ __device__ __forceinline__ uint32_t tile_off(int rows, int r, int c) {
 template <int N>
 __device__ __forceinline__ void tm_ld(uint32_t (&r)[N], uint32_t addr);   // 32 lanes x N columns, lane = thread
 template <>
+__device__ __forceinline__ void tm_ld<8>(uint32_t (&r)[8], uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(addr));
+}
+template <>
 __device__ __forceinline__ void tm_ld<16>(uint32_t (&r)[16], uint32_t addr) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
@@ -157,6 +162,11 @@ __device__ __forceinline__ void tm_ld32_at(uint32_t (&r)[N], uint32_t addr) {
 }
 template <int N>
 __device__ __forceinline__ void tm_st(uint32_t addr, const uint32_t (&r)[N]);
+template <>
+__device__ __forceinline__ void tm_st<8>(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
 template <>
 __device__ __forceinline__ void tm_st<16>(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
