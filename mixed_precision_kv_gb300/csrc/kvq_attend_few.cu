@@ -31,7 +31,7 @@ namespace kvq {
 namespace {
 
 constexpr int kStages = 6;                      // raw tiles in flight
-constexpr int kWarps = 19;
+constexpr int kWarps = 27;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaskRing = 16;                   // tiles whose live words are kept
 constexpr float kHead = 7.0f;                   // P = 2^(x - m + 7)
@@ -46,7 +46,7 @@ struct alignas(1024) FewSmem {
   uint8_t q[R * 256], p[2][R * 256];            // operand rows of 128 elements, 128-byte swizzled
   uint8_t one[R == 64 ? 16384 : 16];            // ones (R = 64: TMEM has no columns left for them)
   alignas(128) uint8_t raw[kStages][4][kInt4Block];
-  float2 rfnm[R];                               // per row: factor of S, kHead - m
+  float rf[R], nm[R];                           // per row: factor of S, kHead - m
   float m[R], fac[R], wmax[4][R];
   unsigned long long tree[R];
   uint32_t live[kMaskRing][4];
@@ -72,15 +72,12 @@ __device__ __forceinline__ Tiles tiles_of(const AttArgs& A, const AttUnit& u, in
 
 // tcgen05.st of fragments: 16 lanes x (8 N) columns, lane 4 r + i holds rows r and
 // r + 8, columns 8 x + 2 i and + 1 (registers 4 x .. 4 x + 3)
-__device__ __forceinline__ void tm_st_frag64(uint32_t addr, const uint32_t (&a)[4][4], const uint32_t (&b)[4][4]) {
+__device__ __forceinline__ void tm_st_frag32(uint32_t addr, const uint32_t (&a)[2][4], const uint32_t (&b)[2][4]) {
   // word w = 2 x + c of row r is a[w >> 2][w & 3], of row r + 8 b[w >> 2][w & 3]
   asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
       "r"(a[0][0]), "r"(a[0][1]), "r"(b[0][0]), "r"(b[0][1]), "r"(a[0][2]), "r"(a[0][3]), "r"(b[0][2]), "r"(b[0][3]),
-      "r"(a[1][0]), "r"(a[1][1]), "r"(b[1][0]), "r"(b[1][1]), "r"(a[1][2]), "r"(a[1][3]), "r"(b[1][2]), "r"(b[1][3]),
-      "r"(a[2][0]), "r"(a[2][1]), "r"(b[2][0]), "r"(b[2][1]), "r"(a[2][2]), "r"(a[2][3]), "r"(b[2][2]), "r"(b[2][3]),
-      "r"(a[3][0]), "r"(a[3][1]), "r"(b[3][0]), "r"(b[3][1]), "r"(a[3][2]), "r"(a[3][3]), "r"(b[3][2]), "r"(b[3][3])
+      "r"(a[1][0]), "r"(a[1][1]), "r"(b[1][0]), "r"(b[1][1]), "r"(a[1][2]), "r"(a[1][3]), "r"(b[1][2]), "r"(b[1][3])
       : "memory");
 }
 __device__ __forceinline__ void tm_st_frag16(uint32_t addr, const uint32_t (&a)[4], const uint32_t (&b)[4]) {
@@ -106,6 +103,18 @@ __device__ __forceinline__ bool group_stop(bool stop) {
   return r != 0;
 }
 
+// P of this thread's key, rows kN ..: row n is 128 n bytes on, its chunks exchanged
+// by n & 7 (an exclusive or on the address).
+template <int kN, int kC>
+__device__ __forceinline__ void store_weights(uint32_t addr, const float (&x)[kC]) {
+  if constexpr (kN < kC) {
+    const uint32_t h = f16x2(ex2f(x[kN]), ex2f(x[kN + 1]));
+    asm volatile("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %4;\n st.shared.b16 [%0 + %2], l;\n st.shared.b16 [%1 + %3], h;\n}"
+                 ::"r"(addr ^ ((kN & 7) << 4)), "r"(addr ^ (((kN + 1) & 7) << 4)), "n"(kN * 128), "n"((kN + 1) * 128), "r"(h)
+                 : "memory");
+    store_weights<kN + 2>(addr, x);
+  }
+}
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
@@ -124,12 +133,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
   if (tid == 0) {
     for (int x = 0; x < kStages; ++x) {
       mb_init(&S.raw_full[x], 4);
-      mb_init(&S.raw_empty[x], 8);
+      mb_init(&S.raw_empty[x], 16);
     }
     for (int x = 0; x < 2; ++x) {
-      mb_init(&S.k_full[x], 4);
+      mb_init(&S.k_full[x], 8);
       mb_init(&S.k_empty[x], 1);
-      mb_init(&S.v_full[x], 4);
+      mb_init(&S.v_full[x], 8);
       mb_init(&S.v_empty[x], 1);
       mb_init(&S.s_full[x], 1);
       mb_init(&S.p_full[x], 8);
@@ -141,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
     S.gave_up = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 16) tm_alloc(&S.tmem, 512);
+  if (warp == 24) tm_alloc(&S.tmem, 512);
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
@@ -156,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
     const uint32_t tl = tmem + ((uint32_t)wq << 21);
     // this thread's key in a row of P: its chunk and byte
     const int kp = frag_pos(wq, lane >> 3, lane & 7);
-    const uint32_t p_off = (uint32_t)(kp >> 6) * R * 128 + (uint32_t)c0 * 128 + 2u * (kp & 7), p_chunk = (uint32_t)((kp & 63) >> 3);
+    const uint32_t p_addr = sm32(S.p[0]) + (uint32_t)(kp >> 6) * R * 128 + (uint32_t)c0 * 128 + 2u * (kp & 63);
     uint32_t page_tiles = 0, tc = 0, bad = 0u;   // tc: tiles of this CTA so far
     bool ok = true;
     const bool qal = ((uintptr_t)A.q & 15) == 0;
@@ -217,7 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
         }
         if (sub == 0) {
           // (a factor below 1e-30 makes every logit 0, as 1e-30 does; kNever times it must stay far below 0)
-          S.rfnm[n] = make_float2(fmaxf(fabsf(A.scale_log2) * __int_as_float((127 - e) << 23), 1e-30f), kUnseen);
+          S.rf[n] = fmaxf(fabsf(A.scale_log2) * __int_as_float((127 - e) << 23), 1e-30f);
+          S.nm[n] = kUnseen;
           S.m[n] = -INFINITY;
           S.tree[n] = A.tree && valid ? A.tree[u.tok0 + (I.row0 + n) / g] : 0ull;
         }
@@ -251,32 +261,44 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
             }
           }
         }
-        ok = __all_sync(0xFFFFFFFFu, mb_spin(&S.s_full[b], (tc >> 1) & 1u, gave_up));
+        ok = __all_sync(0xFFFFFFFFu, mb_wait(&S.s_full[b], (tc >> 1) & 1u, gave_up));
         tm_fence_after();
         if (live_ring) {
           const uint32_t lv = *(volatile uint32_t*)&S.live[page_tiles & (kMaskRing - 1)][wq];
           vis = ((lv >> lane) & 1u) ? 0xFFFFFFFFu : 0u;
           ++page_tiles;
         }
+        const bool all_seen = __all_sync(0xFFFFFFFFu, vis == 0xFFFFFFFFu);
         uint32_t s[kC];
-        if constexpr (kC == 8) tm_ld<8>(s, ts);
-        else if constexpr (kC == 16) tm_ld<16>(s, ts);
-        else tm_ld<32>(s, ts);
-        tm_wait_ld();
-        if (!__all_sync(0xFFFFFFFFu, vis == 0xFFFFFFFFu)) {
+        auto load = [&]() {
+          if constexpr (kC == 8) tm_ld<8>(s, ts);
+          else if constexpr (kC == 16) tm_ld<16>(s, ts);
+          else tm_ld<32>(s, ts);
+          tm_wait_ld();
+          if (!all_seen) {
 #pragma unroll
-          for (int n = 0; n < kC; ++n) s[n] = ((vis >> n) & 1u) ? s[n] : __float_as_uint(kNever);
-        }
+            for (int n = 0; n < kC; ++n) s[n] = ((vis >> n) & 1u) ? s[n] : __float_as_uint(kNever);
+          }
+        };
+        load();
         // ---- x = S rf + 7 - m; does a key exceed its row's maximum by too much?
-        const float4* fr = reinterpret_cast<const float4*>(&S.rfnm[c0]);
-        float x[kC], top = 0.0f;
+        float x[kC];
+        auto weights_of = [&]() {
 #pragma unroll
-        for (int n = 0; n < kC; n += 2) {
-          const float4 f = fr[n >> 1];
-          fma2(x[n], x[n + 1], __uint_as_float(s[n]), __uint_as_float(s[n + 1]), f.x, f.z, f.y, f.w);
+          for (int n = 0; n < kC; n += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(&S.rf[c0 + n]), d = *reinterpret_cast<const float4*>(&S.nm[c0 + n]);
+            fma2(x[n], x[n + 1], __uint_as_float(s[n]), __uint_as_float(s[n + 1]), f.x, f.y, d.x, d.y);
+            fma2(x[n + 2], x[n + 3], __uint_as_float(s[n + 2]), __uint_as_float(s[n + 3]), f.z, f.w, d.z, d.w);
+          }
+        };
+        weights_of();
+        float top = 0.0f, top1 = 0.0f;
+#pragma unroll
+        for (int n = 0; n < kC; n += 4) {
           top = fmaxf(fmaxf(top, x[n]), x[n + 1]);
+          top1 = fmaxf(fmaxf(top1, x[n + 2]), x[n + 3]);
         }
-        const bool mine = __any_sync(0xFFFFFFFFu, unseen || top > kHead + kGrow);
+        const bool mine = __any_sync(0xFFFFFFFFu, unseen || fmaxf(top, top1) > kHead + kGrow);
         if (lane == 0) *(volatile uint32_t*)&S.grow[b][warp] = mine;
         // the P buffer of two tiles ago has been used
         if (ok && tile >= I.tile0 + 2)
@@ -288,11 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
         const uint4 g0 = *reinterpret_cast<const uint4*>(&S.grow[b][0]), g1 = *reinterpret_cast<const uint4*>(&S.grow[b][4]);
         if (g0.x | g0.y | g0.z | g0.w | g1.x | g1.y | g1.z | g1.w) {
           // ---- new maxima of all rows
+          load();
           float keep = kNever;
 #pragma unroll
           for (int n = 0; n < kC; ++n) {
             const float v = __uint_as_float(s[n]);
-            const float w = warp_max_f(v == kNever ? kNever : fmaxf(v * S.rfnm[c0 + n].x, 0.9f * kNever));
+            const float w = warp_max_f(v == kNever ? kNever : fmaxf(v * S.rf[c0 + n], 0.9f * kNever));
             if (lane == n) keep = w;
           }
           if (lane < kC) S.wmax[wq][c0 + lane] = keep;
@@ -307,16 +330,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
             const float mo = S.m[tid], mn = w > 0.95f * kNever ? fmaxf(mo, w) : mo;
             S.m[tid] = mn;
             S.fac[tid] = mo == -INFINITY ? 1.0f : ex2f(mo - mn);
-            S.rfnm[tid].y = mn == -INFINITY ? kUnseen : kHead - mn;
+            S.nm[tid] = mn == -INFINITY ? kUnseen : kHead - mn;
             if (mn == -INFINITY && tid < T.rows) S.unseen = 1u;
           }
           group_stop(false);
           unseen = *(volatile uint32_t*)&S.unseen != 0u;
-#pragma unroll
-          for (int n = 0; n < kC; n += 2) {
-            const float4 f = fr[n >> 1];
-            fma2(x[n], x[n + 1], __uint_as_float(s[n]), __uint_as_float(s[n + 1]), f.x, f.z, f.y, f.w);
-          }
+          weights_of();
           if (tile > I.tile0) {   // O and the sums
             tm_fence_after();
 #pragma unroll 1
@@ -336,13 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
           }
         }
         // ---- weights
-        uint8_t* pb = S.p[b] + p_off;
-#pragma unroll
-        for (int n = 0; n < kC; n += 2) {
-          const uint32_t h = f16x2(ex2f(x[n]), ex2f(x[n + 1]));
-          *reinterpret_cast<uint16_t*>(pb + n * 128 + ((p_chunk ^ (n & 7)) << 4)) = (uint16_t)h;
-          *reinterpret_cast<uint16_t*>(pb + (n + 1) * 128 + ((p_chunk ^ ((n + 1) & 7)) << 4)) = (uint16_t)(h >> 16);
-        }
+        store_weights<0>(p_addr + b * (R * 256), x);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the MMAs read P
         tm_fence_before();
         __syncwarp();
@@ -387,10 +400,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
       if (group_stop(false)) break;   // the maxima have been read
     }
     if (bad) atomicOr(A.status, kStatusRange);
-  } else if (warp < 16) {
+  } else if (warp < 24) {
     // ----------------------------------------------------------- dequantize
-    const bool is_k = warp < 12;
-    const int w4 = warp & 3;                               // K: page; V: channel group
+    const bool is_k = warp < 16;
+    const int w4 = warp & 3, half = (warp >> 2) & 1;       // K: page, two of its channel groups; V: group, two of the pages
     const int r = lane >> 2, i = lane & 3;
     const uint32_t tl = tmem + ((uint32_t)w4 << 21);
     uint32_t page_tiles = 0, tc = 0, bad = 0u;
@@ -419,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
             if (cls == kClsInt2) {
               // a run of 8 channels at a time: its scales serve the lane's four slots
 #pragma unroll 1
-              for (int gr = 0; gr < 4; ++gr) {
+              for (int gr = 2 * half; gr < 2 * half + 2; ++gr) {
                 uint32_t sc[4], z[4], a[4][4];
                 k_scales2(blk, gr, i, sc, z);
 #pragma unroll
@@ -431,26 +444,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
 #pragma unroll 1
               for (int m = 0; m < 2; ++m) {                // slots 16 m + r and 16 m + r + 8
                 const int t0 = 16 * m + r;
-                uint32_t a[4][4], b[4][4];
+                uint32_t a[2][4], b[2][4];
                 if (cls == kClsInt4) {
-                  k_slot4(blk, t0, i, a);
-                  k_slot4(blk, t0 + 8, i, b);
+                  k_slot4(blk, t0, i, half, a);
+                  k_slot4(blk, t0 + 8, i, half, b);
                 } else if (cls == kClsInt3) {
-                  k_slot3(blk, t0, i, a);
-                  k_slot3(blk, t0 + 8, i, b);
+                  k_slot3(blk, t0, i, half, a);
+                  k_slot3(blk, t0 + 8, i, half, b);
                 } else if (cls == kClsFp4) {
-                  k_slotf(blk, t0, i, a);
-                  k_slotf(blk, t0 + 8, i, b);
+                  k_slotf(blk, t0, i, half, a);
+                  k_slotf(blk, t0 + 8, i, half, b);
                 } else {
 #pragma unroll
-                  for (int x = 0; x < 16; ++x) a[x >> 2][x & 3] = b[x >> 2][x & 3] = 0u;
+                  for (int x = 0; x < 8; ++x) a[x >> 2][x & 3] = b[x >> 2][x & 3] = 0u;
                 }
-                tm_st_frag64(dst + ((uint32_t)(16 * m) << 16), a, b);
+                tm_st_frag32(dst + 32u * half + ((uint32_t)(16 * m) << 16), a, b);
               }
             }
           } else {
 #pragma unroll 1
-            for (int p = 0; p < 4; ++p) {
+            for (int p = 2 * half; p < 2 * half + 2; ++p) {
               const uint8_t* blk = S.raw[sg][p];
               const int cls = *(volatile int32_t*)&S.cls[sg][p];
               uint32_t v[4][4];
@@ -487,27 +500,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
           if (is_k) {
 #pragma unroll 1
             for (int m = 0; m < 2; ++m) {
-              uint32_t a[4][4], b[4][4];
+              uint32_t a[2][4], b[2][4];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int j = j0 + 32 * w4 + 16 * m + 8 * e + r, jc = min(j, n - 1);
-                uint4 y[4];
+                uint4 y[2];
 #pragma unroll
-                for (int gr = 0; gr < 4; ++gr) {
-                  const int ch = 4 * gr + i;
-                  y[gr] = load8(src + (size_t)jc * stride + 8 * (list ? ch ^ (jc & 7) : ch), list || kal);
+                for (int x = 0; x < 2; ++x) {
+                  const int ch = 4 * (2 * half + x) + i;
+                  y[x] = load8(src + (size_t)jc * stride + 8 * (list ? ch ^ (jc & 7) : ch), list || kal);
                 }
 #pragma unroll
-                for (int gr = 0; gr < 4; ++gr) {
-                  if (j >= n) y[gr] = make_uint4(0u, 0u, 0u, 0u);
-                  order8_f16(y[gr], 1.0f, e ? b[gr] : a[gr], bad);
+                for (int x = 0; x < 2; ++x) {
+                  if (j >= n) y[x] = make_uint4(0u, 0u, 0u, 0u);
+                  order8_f16(y[x], 1.0f, e ? b[x] : a[x], bad);
                 }
               }
-              tm_st_frag64(dst + ((uint32_t)(16 * m) << 16), a, b);
+              tm_st_frag32(dst + 32u * half + ((uint32_t)(16 * m) << 16), a, b);
             }
           } else {
 #pragma unroll 1
-            for (int p = 0; p < 4; ++p) {
+            for (int p = 2 * half; p < 2 * half + 2; ++p) {
               uint32_t v[4][4];
               uint16_t y[4][8];
 #pragma unroll
@@ -538,12 +551,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
       }
     }
     if (bad) atomicOr(A.status, kStatusRange);
-  } else if (warp < 18) {
-    // ------------------------------------------- MMA: warp 16 Q K^T, warp 17 P V and the sums of P
+  } else if (warp < 26) {
+    // ------------------------------------------- MMA: warp 24 Q K^T, warp 25 P V and the sums of P
     // The whole warp runs the loop and one elected lane issues: with operands that the compiler knows to
     // be the same in all lanes an MMA of N = 32 issues every 21 cycles, from a branch on the lane every 47.
     constexpr uint32_t idesc = mma_idesc(128, R);
-    const bool is_qk = warp == 16;
+    const bool is_qk = warp == 24;
     const uint64_t qd = sw128_desc(sm32(S.q)), pd0 = sw128_desc(sm32(S.p[0])), od = sw128_desc(sm32(S.one));
     constexpr uint32_t kP16 = R * 16;   // one P buffer, in units of 16 bytes
     uint32_t tc = 0, q_phase = 0;
@@ -561,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
           ok = ok && mb_wait(&S.k_full[b], ph, gave_up);
           if (ok && tc >= 2u) ok = mb_wait(&S.p_full[b], ph ^ 1u, gave_up);   // S of two tiles ago has been read
         } else {
-          ok = ok && mb_wait(&S.v_full[b], ph, gave_up) && mb_spin(&S.p_full[b], ph, gave_up);
+          ok = ok && mb_wait(&S.v_full[b], ph, gave_up) && mb_wait(&S.p_full[b], ph, gave_up);
         }
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
@@ -650,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
   tm_fence_before();
   __syncthreads();
   if (tid == 0 && *gave_up) atomicOr(A.status, kStatusTimeout);
-  if (warp == 16) {
+  if (warp == 24) {
     tm_fence_after();
     tm_free(tmem, 512);
   }

@@ -262,8 +262,8 @@ __device__ __forceinline__ uint32_t order_bits(uint32_t m) {
   return d;
 }
 
-// ---- K of a page: slot t, channels 32 gr + 8 i .. + 7 for gr = 0..3 --------
-// out[gr][k] = channels (k, k + 4) of that run.
+// ---- K of a page: slot t, channels 32 gr + 8 i .. + 7 (run (gr, i)) ---------
+// out[..][k] = channels (k, k + 4) of a run.
 // INT2: the scale and zero pairs of run (gr, i) are the same for every slot.
 __device__ __forceinline__ void k_scales2(const uint8_t* blk, int gr, int i, uint32_t (&sc)[4], uint32_t (&z)[4]) {
   const uint32_t sel = (i & 1) ? 0x7632u : 0x5410u, sel0 = (i & 1) ? 0x7610u : 0x5432u;   // pair 0 is stored swapped
@@ -286,44 +286,43 @@ __device__ __forceinline__ void k_run2(const uint8_t* blk, int t, int gr, int i,
 #pragma unroll
   for (int k = 0; k < 4; ++k) out[k] = hfma2u(c[k], sc[k], z[k]);
 }
-__device__ __forceinline__ void k_slot4(const uint8_t* blk, int t, int i, uint32_t (&out)[4][4]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(blk + kI4KCodes + 64 * t + 16 * i);
-  const uint4 m = *reinterpret_cast<const uint4*>(blk + kI4KMeta + 16 * t);
-  const uint32_t wd[4] = {w.x, w.y, w.z, w.w}, md[4] = {m.x, m.y, m.z, m.w};
+// The other widths: groups 2 half and 2 half + 1 of slot t.
+__device__ __forceinline__ void k_slot4(const uint8_t* blk, int t, int i, int half, uint32_t (&out)[2][4]) {
+  const uint2 w = *reinterpret_cast<const uint2*>(blk + kI4KCodes + 64 * t + 16 * i + 8 * half);
+  const uint2 m = *reinterpret_cast<const uint2*>(blk + kI4KMeta + 16 * t + 8 * half);
 #pragma unroll
-  for (int gr = 0; gr < 4; ++gr) {
-    const uint32_t s = __byte_perm(md[gr], 0u, 0x1010u), z = __byte_perm(md[gr], 0u, 0x3232u);
+  for (int x = 0; x < 2; ++x) {
+    const uint32_t md = x ? m.y : m.x;
+    const uint32_t s = __byte_perm(md, 0u, 0x1010u), z = __byte_perm(md, 0u, 0x3232u);
     uint32_t c[4];
-    nibbles(wd[gr], c);
+    nibbles(x ? w.y : w.x, c);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) out[gr][k] = hfma2u(c[k], s, z);
+    for (int k = 0; k < 4; ++k) out[x][k] = hfma2u(c[k], s, z);
   }
 }
-__device__ __forceinline__ void k_slot3(const uint8_t* blk, int t, int i, uint32_t (&out)[4][4]) {
-  const uint2 lo = *reinterpret_cast<const uint2*>(blk + kI3KCodes + 48 * t + 8 * i);
-  const uint32_t hi = *reinterpret_cast<const uint32_t*>(blk + kI3KCodes + 48 * t + 32 + 4 * i);
-  const uint4 m = *reinterpret_cast<const uint4*>(blk + kI3KMeta + 16 * t);
-  const uint32_t md[4] = {m.x, m.y, m.z, m.w};
+__device__ __forceinline__ void k_slot3(const uint8_t* blk, int t, int i, int half, uint32_t (&out)[2][4]) {
+  const uint32_t lo = *reinterpret_cast<const uint32_t*>(blk + kI3KCodes + 48 * t + 8 * i + 4 * half);
+  const uint32_t hi = *reinterpret_cast<const uint32_t*>(blk + kI3KCodes + 48 * t + 32 + 4 * i) >> (8 * half);
+  const uint2 m = *reinterpret_cast<const uint2*>(blk + kI3KMeta + 16 * t + 8 * half);
 #pragma unroll
-  for (int gr = 0; gr < 4; ++gr) {
-    const uint32_t s = __byte_perm(md[gr], 0u, 0x1010u), z = __byte_perm(md[gr], 0u, 0x3232u);
-    const uint32_t l = (gr < 2 ? lo.x : lo.y) >> (8 * (gr & 1));
+  for (int x = 0; x < 2; ++x) {
+    const uint32_t md = x ? m.y : m.x;
+    const uint32_t s = __byte_perm(md, 0u, 0x1010u), z = __byte_perm(md, 0u, 0x3232u);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint32_t c = ((l >> (2 * k)) & 0x00030003u) | (((hi >> (4 * gr + k)) & 0x00010001u) << 2);
-      out[gr][k] = hfma2u(codes0(c | 0x64006400u), s, z);
+      const uint32_t c = ((lo >> (8 * x + 2 * k)) & 0x00030003u) | (((hi >> (4 * x + k)) & 0x00010001u) << 2);
+      out[x][k] = hfma2u(codes0(c | 0x64006400u), s, z);
     }
   }
 }
-__device__ __forceinline__ void k_slotf(const uint8_t* blk, int t, int i, uint32_t (&out)[4][4]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(blk + kF4KCodes + 64 * t + 16 * i);
-  const uint2 m = *reinterpret_cast<const uint2*>(blk + kF4KScale + 8 * t);
-  const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ void k_slotf(const uint8_t* blk, int t, int i, int half, uint32_t (&out)[2][4]) {
+  const uint2 w = *reinterpret_cast<const uint2*>(blk + kF4KCodes + 64 * t + 16 * i + 8 * half);
+  const uint32_t m = *reinterpret_cast<const uint32_t*>(blk + kF4KScale + 8 * t + 4 * half);
 #pragma unroll
-  for (int gr = 0; gr < 4; ++gr) {
-    const uint32_t s = __byte_perm(gr < 2 ? m.x : m.y, 0u, (gr & 1) ? 0x3232u : 0x1010u);
+  for (int x = 0; x < 2; ++x) {
+    const uint32_t s = __byte_perm(m, 0u, x ? 0x3232u : 0x1010u);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) out[gr][k] = hmul2u(e2m1x2(wd[gr] >> (8 * k)), s);
+    for (int k = 0; k < 4; ++k) out[x][k] = hmul2u(e2m1x2((x ? w.y : w.x) >> (8 * k)), s);
   }
 }
 

@@ -113,14 +113,6 @@ __global__ void __launch_bounds__(256) attend_tiles_kernel(AttArgs A, const AttU
     if (is_k && lane == 0) live[(size_t)(u.tile_base + tile) * 4 + p] = order_bits(e.live);
     {
           if (is_k) {
-            auto put = [&](int t, const uint32_t (&w)[4][4]) {
-              const int n = 32 * p + (t & ~7) + order8(t & 7);
-#pragma unroll
-              for (int gr = 0; gr < 4; ++gr)
-                *reinterpret_cast<uint4*>(dst + tile_off(128, n, 4 * gr + i)) =
-                    make_uint4(w[gr][0], w[gr][1], w[gr][2], w[gr][3]);
-            };
-            uint32_t w[4][4];
             if (cls == kClsInt2) {
 #pragma unroll 1
               for (int gr = 0; gr < 4; ++gr) {
@@ -134,24 +126,25 @@ __global__ void __launch_bounds__(256) attend_tiles_kernel(AttArgs A, const AttU
                       make_uint4(y[0], y[1], y[2], y[3]);
                 }
               }
-            } else if (cls == kClsInt4) {
-#pragma unroll 1
-              for (int b = 0; b < 4; ++b) {
-                k_slot4(blk, 8 * b + rk, i, w);
-                put(8 * b + rk, w);
-              }
             } else {
-#pragma unroll 1
-              for (int b = 0; b < 4; ++b) {
-                if (cls == kClsInt3) {
-                  k_slot3(blk, 8 * b + rk, i, w);
+#pragma unroll 2
+              for (int y = 0; y < 8; ++y) {
+                const int t = 8 * (y >> 1) + rk, half = y & 1;
+                uint32_t w[2][4];
+                if (cls == kClsInt4) {
+                  k_slot4(blk, t, i, half, w);
+                } else if (cls == kClsInt3) {
+                  k_slot3(blk, t, i, half, w);
                 } else if (cls == kClsFp4) {
-                  k_slotf(blk, 8 * b + rk, i, w);
+                  k_slotf(blk, t, i, half, w);
                 } else {
 #pragma unroll
-                  for (int x = 0; x < 16; ++x) w[x >> 2][x & 3] = 0u;
+                  for (int x = 0; x < 8; ++x) w[x >> 2][x & 3] = 0u;
                 }
-                put(8 * b + rk, w);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                  *reinterpret_cast<uint4*>(dst + tile_off(128, 32 * p + (t & ~7) + order8(rk), 4 * (2 * half + x) + i)) =
+                      make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
               }
             }
           } else {
