@@ -161,7 +161,8 @@ void plan_wide(const std::vector<AttUnit>& units, int u0, int u1, int g, bool kv
 }
 
 // Few rows per unit: blocks of R rows, all key tiles of all blocks in one line, cut
-// into equal runs.  A tile costs 1 (its unpacking, whatever R), an item 1.5 more.
+// into equal runs.  A tile costs 1 (its unpacking, whatever R), an item 3 more (its
+// rows, the first and last steps).
 constexpr int kFewRows = 256;   // units of up to this many rows
 void plan_few(const std::vector<AttUnit>& units, int g, int R, bool kv, bool tree, int sms, AttPlan& out) {
   double total = 0.0;
@@ -170,10 +171,10 @@ void plan_few(const std::vector<AttUnit>& units, int g, int R, bool kv, bool tre
     for (int r = 0; r < u.T * g; r += R) {
       const int t = block_tiles(u, g, r, std::min(R, u.T * g - r), kv, tree);
       tiles += t;
-      total += t + 1.5;
+      total += t + 3.0;
     }
   const int ctas = (int)std::max<int64_t>(1, std::min<int64_t>(sms, tiles));
-  const double share = (total + 1.5 * (ctas - 1)) / ctas;
+  const double share = (total + 3.0 * (ctas - 1)) / ctas;
   double done = 0.0;
   int cta = 0;
   out.cta_item.push_back(0);
@@ -186,7 +187,7 @@ void plan_few(const std::vector<AttUnit>& units, int g, int R, bool kv, bool tre
       do {
         int take = n - t;
         if (cta < ctas - 1) {
-          const int fit = (int)((cta + 1) * share - done - 1.0);
+          const int fit = (int)((cta + 1) * share - done - 2.5);
           if (fit < std::min(1, take)) {
             out.cta_item.push_back((int32_t)out.items.size());
             ++cta;
@@ -195,7 +196,7 @@ void plan_few(const std::vector<AttUnit>& units, int g, int R, bool kv, bool tre
           take = std::min(take, fit);
         }
         out.items.push_back(AttItem{x, r, t, t + take, -1, {0, 0, 0}});
-        done += take + 1.5;
+        done += take + 3.0;
         t += take;
       } while (t < n);
       const int pieces = (int)(out.items.size() - first);

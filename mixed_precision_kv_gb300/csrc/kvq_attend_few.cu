@@ -31,8 +31,14 @@ namespace kvq {
 namespace {
 
 constexpr int kStages = 6;                      // raw tiles in flight
-constexpr int kWarps = 27;
-constexpr int kThreads = 32 * kWarps;
+// Warps each for K and for V: with R = 64 the softmax code needs the registers (72 per thread with 27
+// warps): 420 us for 31-token trees x 8 over 32K with 4, 478 with 8; ragged drafts (R = 32) 440 and 358.
+template <int R>
+constexpr int kSide = R == 64 ? 4 : 8;
+template <int R>
+constexpr int kMma = 8 + 2 * kSide<R>;          // first MMA warp
+template <int R>
+constexpr int kThreads = 32 * (kMma<R> + 3);
 constexpr int kMaskRing = 16;                   // tiles whose live words are kept
 constexpr float kHead = 7.0f;                   // P = 2^(x - m + 7)
 constexpr float kGrow = 8.0f;                   // a maximum may be stale by this much (base 2)
@@ -122,7 +128,7 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 template <int R>
-__global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
+__global__ void __launch_bounds__(kThreads<R>, 1) attend_few_kernel(
     AttArgs A, const AttUnit* __restrict__ units, const AttItem* __restrict__ items, const int32_t* __restrict__ cta_item,
     float* __restrict__ part, uint32_t first_spins) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -133,12 +139,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
   if (tid == 0) {
     for (int x = 0; x < kStages; ++x) {
       mb_init(&S.raw_full[x], 4);
-      mb_init(&S.raw_empty[x], 16);
+      mb_init(&S.raw_empty[x], 2 * kSide<R>);
     }
     for (int x = 0; x < 2; ++x) {
-      mb_init(&S.k_full[x], 8);
+      mb_init(&S.k_full[x], kSide<R>);
       mb_init(&S.k_empty[x], 1);
-      mb_init(&S.v_full[x], 8);
+      mb_init(&S.v_full[x], kSide<R>);
       mb_init(&S.v_empty[x], 1);
       mb_init(&S.s_full[x], 1);
       mb_init(&S.p_full[x], 8);
@@ -150,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
     S.gave_up = 0u;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 24) tm_alloc(&S.tmem, 512);
+  if (warp == kMma<R>) tm_alloc(&S.tmem, 512);
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
@@ -400,10 +406,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
       if (group_stop(false)) break;   // the maxima have been read
     }
     if (bad) atomicOr(A.status, kStatusRange);
-  } else if (warp < 24) {
+  } else if (warp < kMma<R>) {
     // ----------------------------------------------------------- dequantize
-    const bool is_k = warp < 16;
-    const int w4 = warp & 3, half = (warp >> 2) & 1;       // K: page, two of its channel groups; V: group, two of the pages
+    const bool is_k = warp < 8 + kSide<R>;
+    // K: a page, channel groups 2 half and 2 half + 1; V: a group, pages 2 half and 2 half + 1 (4 warps a side: both halves)
+    const int w4 = warp & 3, h0 = kSide<R> == 8 ? (warp >> 2) & 1 : 0, h1 = kSide<R> == 8 ? h0 + 1 : 2;
     const int r = lane >> 2, i = lane & 3;
     const uint32_t tl = tmem + ((uint32_t)w4 << 21);
     uint32_t page_tiles = 0, tc = 0, bad = 0u;
@@ -432,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
             if (cls == kClsInt2) {
               // a run of 8 channels at a time: its scales serve the lane's four slots
 #pragma unroll 1
-              for (int gr = 2 * half; gr < 2 * half + 2; ++gr) {
+              for (int gr = 2 * h0; gr < 2 * h1; ++gr) {
                 uint32_t sc[4], z[4], a[4][4];
                 k_scales2(blk, gr, i, sc, z);
 #pragma unroll
@@ -442,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
               }
             } else {
 #pragma unroll 1
-              for (int m = 0; m < 2; ++m) {                // slots 16 m + r and 16 m + r + 8
-                const int t0 = 16 * m + r;
+              for (int y = 2 * h0; y < 2 * h1; ++y) {      // slots 16 m + r and 16 m + r + 8
+                const int m = y & 1, half = y >> 1, t0 = 16 * m + r;
                 uint32_t a[2][4], b[2][4];
                 if (cls == kClsInt4) {
                   k_slot4(blk, t0, i, half, a);
@@ -463,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
             }
           } else {
 #pragma unroll 1
-            for (int p = 2 * half; p < 2 * half + 2; ++p) {
+            for (int p = 2 * h0; p < 2 * h1; ++p) {
               const uint8_t* blk = S.raw[sg][p];
               const int cls = *(volatile int32_t*)&S.cls[sg][p];
               uint32_t v[4][4];
@@ -499,7 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
                    : (is_k ? A.k : A.v) + ((size_t)u.tok0 * A.hkv + u.kvh) * kHeadDim;
           if (is_k) {
 #pragma unroll 1
-            for (int m = 0; m < 2; ++m) {
+            for (int yy = 2 * h0; yy < 2 * h1; ++yy) {
+              const int m = yy & 1, half = yy >> 1;
               uint32_t a[2][4], b[2][4];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
@@ -520,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
             }
           } else {
 #pragma unroll 1
-            for (int p = 2 * half; p < 2 * half + 2; ++p) {
+            for (int p = 2 * h0; p < 2 * h1; ++p) {
               uint32_t v[4][4];
               uint16_t y[4][8];
 #pragma unroll
@@ -551,12 +559,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
       }
     }
     if (bad) atomicOr(A.status, kStatusRange);
-  } else if (warp < 26) {
-    // ------------------------------------------- MMA: warp 24 Q K^T, warp 25 P V and the sums of P
+  } else if (warp < kMma<R> + 2) {
+    // ---------------------------------------------- MMA: one warp Q K^T, one P V and the sums of P
     // The whole warp runs the loop and one elected lane issues: with operands that the compiler knows to
     // be the same in all lanes an MMA of N = 32 issues every 21 cycles, from a branch on the lane every 47.
     constexpr uint32_t idesc = mma_idesc(128, R);
-    const bool is_qk = warp == 24;
+    const bool is_qk = warp == kMma<R>;
     const uint64_t qd = sw128_desc(sm32(S.q)), pd0 = sw128_desc(sm32(S.p[0])), od = sw128_desc(sm32(S.one));
     constexpr uint32_t kP16 = R * 16;   // one P buffer, in units of 16 bytes
     uint32_t tc = 0, q_phase = 0;
@@ -663,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_few_kernel(
   tm_fence_before();
   __syncthreads();
   if (tid == 0 && *gave_up) atomicOr(A.status, kStatusTimeout);
-  if (warp == 24) {
+  if (warp == kMma<R>) {
     tm_fence_after();
     tm_free(tmem, 512);
   }
@@ -682,7 +690,7 @@ cudaError_t launch_r(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const
     attr_set.fetch_or(uint64_t(1) << dev);
   }
   ++P->launches;
-  attend_few_kernel<R><<<(unsigned)n_ctas, kThreads, sizeof(FewSmem<R>), s>>>(
+  attend_few_kernel<R><<<(unsigned)n_ctas, kThreads<R>, sizeof(FewSmem<R>), s>>>(
       A, d_units, d_items, d_cta_item, d_part, P->first_wait_spins < 0 ? kAttSpin : (uint32_t)P->first_wait_spins);
   return cudaGetLastError();
 }

@@ -23,7 +23,7 @@
 namespace kvq {
 namespace {
 
-constexpr uint32_t kAttSpin = 1u << 22;   // bound of every wait
+constexpr uint32_t kAttSpin = 1u << 22;   // bound of every wait, in polls
 
 __device__ __forceinline__ uint32_t sm32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -45,18 +45,8 @@ __device__ __forceinline__ bool mb_try(uint64_t* b, uint32_t parity) {
 // another role gave up (then every role leaves its loop).
 __device__ __forceinline__ bool mb_wait(uint64_t* b, uint32_t parity, volatile uint32_t* gave_up,
                                         uint32_t limit = kAttSpin) {
-  if (limit && mb_try(b, parity)) return true;
   for (uint32_t it = 0; it < limit; ++it) {
     if (mb_try(b, parity)) return true;
-    if (*gave_up) return false;
-  }
-  *gave_up = 1u;
-  return false;
-}
-// Wait until a ring slot's number is `c` (bounded as mb_wait).
-__device__ __forceinline__ bool slot_is(volatile uint32_t* seq, uint32_t c, volatile uint32_t* gave_up) {
-  for (uint32_t it = 0; it < kAttSpin; ++it) {
-    if (*seq == c) return true;
     if (*gave_up) return false;
   }
   *gave_up = 1u;
@@ -65,7 +55,7 @@ __device__ __forceinline__ bool slot_is(volatile uint32_t* seq, uint32_t c, vola
 // The same without suspending the thread: for waits on the critical path, where
 // the wake-up of a suspended thread costs a few hundred cycles.
 __device__ __forceinline__ bool mb_spin(uint64_t* b, uint32_t parity, volatile uint32_t* gave_up) {
-  for (uint32_t it = 0; it < 16 * kAttSpin; ++it) {
+  for (uint32_t it = 0; it < (1u << 26); ++it) {
     uint32_t ok;
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
