@@ -337,7 +337,8 @@ KVQ_API kv_status_t kv_decode_attn_scored(kv_pool_t* pool, const void* q, const 
  *   out      device, int32 [n_req][per_head ? num_kv_heads : 1][out_stride]:
  *            the chosen positions in ascending order, then -1
  * Fewer eligible positions than n_select: all of them.  At most 65535
- * requests.  On a stream that is being captured it is KV_ERR_STATE. */
+ * requests, and 12,582,912 positions below the protected ones in any of them.
+ * On a stream that is being captured it is KV_ERR_STATE. */
 KVQ_API kv_status_t kv_select_lowest(kv_pool_t* pool, const float* scores, int64_t score_stride, const int32_t* req_ids,
                                      const int32_t* n_select, int32_t n_req, int64_t protect, int32_t per_head,
                                      int32_t* out, int64_t out_stride, void* stream);

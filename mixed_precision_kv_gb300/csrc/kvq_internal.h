@@ -308,7 +308,7 @@ struct kv_pool {
   kvq::DevBuf partials;               // decode split partials
   kvq::DevBuf frags;                  // per-unit q operands of the tensor-core scan
   kvq::DevBuf logits;                 // scored decode: logits of the batch's pages, then each row's (maximum, 1 / sum)
-  kvq::DevBuf select;                 // lowest-score selection: lengths, eligibility bits, keys, counts
+  kvq::DevBuf select;                 // lowest-score selection: the rows of a call of many requests
   kvq::DevBuf attend;                 // attention of new tokens: plan, then partials
   kvq::DevBuf attend_tiles;           // ... many rows per unit: operand tiles, then their live words
   // token position of every slot, on the device ([page id][32]; allocated by

@@ -7,9 +7,11 @@
 // the lower position; listed in ascending order.  Keys are the scores' bits
 // mapped to unsigned integers of the same order (-0 as +0, NaN last), so the
 // choice is exact whatever the order of the work.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <vector>
 
@@ -17,6 +19,8 @@
 
 namespace kvq {
 namespace {
+
+namespace cg = cooperative_groups;
 
 // ---- positions -------------------------------------------------------------
 struct PosRow {
@@ -40,127 +44,258 @@ struct SelRow {
 };
 
 __device__ __forceinline__ uint32_t order_key(float x) {
-  if (x != x) return 0xFFFFFFFFu;
+  if (x != x) return 0xFFFFFFFEu;   // 0xFFFFFFFF marks a position that may not be chosen
   const uint32_t u = __float_as_uint(x + 0.0f);   // -0 -> +0
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Eligible positions as bits, one row of words per request (rows_per = 1) or
-// per request and kv head (rows_per = hkv).  Warp = a page, lane = slot.
-__global__ void __launch_bounds__(256) eligible_kernel(const SelRow* __restrict__ rows, const Entry* __restrict__ table,
-                                                       int max_pages, const int32_t* __restrict__ ntab,
-                                                       const uint32_t* __restrict__ hdead,
-                                                       const int32_t* __restrict__ pos, int hkv, int rows_per,
-                                                       int words, uint32_t* __restrict__ bits) {
-  const SelRow r = rows[blockIdx.y];
-  const int lane = threadIdx.x & 31;
-  const int p = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (p >= ntab[r.req]) return;
-  const Entry e = table[(size_t)r.req * max_pages + p];
-  const int32_t at = pos[(size_t)e.id * kPage + lane];
-  for (int h = 0; h < rows_per; ++h) {
-    uint32_t live = e.live;
-    if (hdead) {
-      if (rows_per > 1) {
-        live &= ~hdead[(size_t)e.id * hkv + h];
-      } else {   // all heads together: a slot that some head still reads
-        uint32_t any = 0u;
-        for (int x = 0; x < hkv; ++x) any |= ~hdead[(size_t)e.id * hkv + x];
-        live &= any;
+// The rows of a call, by value while they fit the parameters.
+constexpr int kRowsByValue = 128;
+struct SelRows {
+  SelRow r[kRowsByValue];
+};
+
+// Which of a page's slots may be chosen (bits): live, for the row's head or for any.
+__device__ __forceinline__ uint32_t eligible_slots(const Entry& e, const uint32_t* hdead, int hkv, int h, bool per_head) {
+  uint32_t live = e.live;
+  if (hdead) {
+    if (per_head) {
+      live &= ~hdead[(size_t)e.id * hkv + h];
+    } else {   // all heads together: a slot that some head still reads
+      uint32_t any = 0u;
+      for (int x = 0; x < hkv; ++x) any |= ~hdead[(size_t)e.id * hkv + x];
+      live &= any;
+    }
+  }
+  return live;
+}
+// Key of a position: the head's score, or the heads' sum as if taken in 64 bits and
+// rounded once.  fp64 runs at 1/64 of the fp32 rate here, so the sum is carried as an
+// unevaluated pair of fp32 (48 bits); values so large that the pair could overflow, and
+// what is not finite, take the fp64 path.
+__device__ __noinline__ float sum_wide(const float* sc, int64_t stride, int hkv, int x) {
+  double sum = 0.0;
+  for (int y = 0; y < hkv; ++y) sum += (double)__ldg(sc + (size_t)y * stride + x);
+  return (float)sum;
+}
+__device__ __forceinline__ uint32_t key_of(const float* sc, int64_t stride, int hkv, int h, bool per_head, int x) {
+  if (per_head) return order_key(__ldg(sc + (size_t)h * stride + x));
+  float hi = 0.0f, lo = 0.0f, top = 0.0f;
+  bool odd = false;
+  for (int y = 0; y < hkv; y += 8) {
+    float f[8];
+#pragma unroll
+    for (int z = 0; z < 8; ++z) f[z] = y + z < hkv ? __ldg(sc + (size_t)(y + z) * stride + x) : 0.0f;
+#pragma unroll
+    for (int z = 0; z < 8; ++z) {
+      odd |= f[z] != f[z];
+      top = fmaxf(top, fabsf(f[z]));
+      const float t = __fadd_rn(hi, f[z]), b = __fsub_rn(t, hi);   // hi + f = t + e exactly
+      const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(f[z], b));
+      hi = t;
+      lo = __fadd_rn(lo, e);
+    }
+  }
+  if (odd || !(top < 1.0e36f)) return order_key(sum_wide(sc, stride, hkv, x));
+  return order_key(__fadd_rn(hi, lo));
+}
+// Inclusive sum over the block's 1024 threads; `total` is the whole sum.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, uint32_t& total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  uint32_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sum[w] = x;
+  __syncthreads();
+  uint32_t t = warp_sum[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, t, o);
+    if (lane >= o) t += y;
+  }
+  total = __shfl_sync(0xFFFFFFFFu, t, 31);
+  const uint32_t before = w ? __shfl_sync(0xFFFFFFFFu, t, w - 1) : 0u;
+  __syncthreads();
+  return before + x;
+}
+
+// A cluster of CTAs per row; CTA c holds the keys of positions [c per, (c + 1) per)
+// in shared memory, so the scores are read once and the rest stays on the SMs:
+//   the table's pages, a share per CTA, set the eligible positions' bits where they
+//   belong (a page's slots are one or two runs of positions, so a warp sends one or
+//   two words); keys; radix selection by digits of 11 bits, the CTAs' histograms
+//   added up through distributed shared memory; an ordered listing.
+// Bound by the scores' bytes for long rows, by a dozen barriers for short ones.
+// 16 x 100K positions, 8 heads summed: 380 us with one CTA per row reading its keys
+// once per digit, 36 us so.
+constexpr int kSelThreads = 1024;
+constexpr int kSelStored = 48 * 1024;      // positions per CTA whose keys fit its shared memory
+constexpr int kSelMost = 3 * 512 * 1024;   // ... whose bits do
+constexpr int sel_smem(int per) { return (per <= kSelStored ? per * 4 : 0) + per / 8; }
+constexpr int kBins = 2048;                // digits of 11, 11 and 10 bits
+struct SelShared {
+  uint32_t hist[3][kBins], warp_sum[32];
+  uint32_t below, ties;      // of this CTA
+  uint32_t digit, left;
+};
+template <bool kStored>
+__global__ void __launch_bounds__(kSelThreads) select_kernel(
+    SelRows by_value, const SelRow* __restrict__ rows, const Entry* __restrict__ table, int max_pages,
+    const int32_t* __restrict__ ntab, const uint32_t* __restrict__ hdead, const int32_t* __restrict__ pos, int hkv,
+    int per_head, const float* __restrict__ scores, int64_t stride, int per, int32_t* __restrict__ out,
+    int64_t out_stride) {
+  extern __shared__ __align__(16) uint32_t keys[];   // kStored: per keys; then per / 32 words of bits
+  __shared__ SelShared S;
+  cg::cluster_group cl = cg::this_cluster();
+  const int n_cta = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const int rows_per = per_head ? hkv : 1;
+  const int idx = (int)(blockIdx.x / n_cta), row = idx / rows_per, h = idx - row * rows_per;
+  const SelRow r = rows ? rows[row] : by_value.r[row];
+  const float* sc = scores + (size_t)r.b * hkv * stride;
+  int32_t* o = out + (size_t)idx * out_stride;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  uint32_t* bits = keys + (kStored ? per : 0);
+  const int words = per >> 5;
+  const int n_pages = ntab[r.req];
+  for (int x = tid; x < words; x += kSelThreads) bits[x] = 0u;
+  for (int x = tid; x < 3 * kBins; x += kSelThreads) (&S.hist[0][0])[x] = 0u;
+  if (tid == 0) S.below = S.ties = 0u;
+  cl.sync();
+  // ---- eligible positions, four pages of a warp in flight
+  const Entry* tab = table + (size_t)r.req * max_pages;
+  for (int p0 = (rank * 32 + w) * 4; p0 < n_pages; p0 += n_cta * 128) {
+    Entry e[4];
+    int32_t at[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) e[y] = p0 + y < n_pages ? tab[p0 + y] : Entry{-1, 0u};
+#pragma unroll
+    for (int y = 0; y < 4; ++y) at[y] = e[y].id >= 0 ? pos[(size_t)e[y].id * kPage + lane] : 0;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      if (e[y].id < 0) continue;   // the same for the whole warp
+      const bool can = ((eligible_slots(e[y], hdead, hkv, h, per_head) >> lane) & 1u) && at[y] < r.limit;
+      const int word = can ? at[y] >> 5 : -1;
+      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, word);
+      if (can) {
+        const uint32_t m = __reduce_or_sync(peers, 1u << (at[y] & 31));
+        if (lane == __ffs(peers) - 1) atomicOr(cl.map_shared_rank(bits, word / words) + word % words, m);
       }
     }
-    const bool can = ((live >> lane) & 1u) && at < r.limit;
-    if (can) atomicOr(&bits[((size_t)blockIdx.y * rows_per + h) * words + (at >> 5)], 1u << (at & 31));
   }
-}
-
-// Keys of the rows that sum their kv heads: the sum in 64 bits, rounded once.
-__global__ void __launch_bounds__(256) sum_key_kernel(const SelRow* __restrict__ rows, const float* __restrict__ scores,
-                                                      int64_t stride, int hkv, int max_len, uint32_t* __restrict__ keys) {
-  const SelRow r = rows[blockIdx.y];
-  const int x = blockIdx.x * 256 + threadIdx.x;
-  if (x >= r.limit) return;
-  double sum = 0.0;
-  for (int h = 0; h < hkv; ++h) sum += (double)scores[((size_t)r.b * hkv + h) * stride + x];
-  keys[(size_t)blockIdx.y * max_len + x] = order_key((float)sum);
-}
-
-// One CTA per row: radix selection by 8-bit digits, then an ordered listing.
-__global__ void __launch_bounds__(1024) select_kernel(const SelRow* __restrict__ rows, const uint32_t* __restrict__ bits,
-                                                      int bit_rows_per, int words, const float* __restrict__ scores,
-                                                      int64_t stride, int hkv, const uint32_t* __restrict__ keys,
-                                                      int max_len, int rows_per, int32_t* __restrict__ out,
-                                                      int64_t out_stride) {
-  __shared__ uint32_t hist[256], warp_n[32], warp_t[32];
-  __shared__ uint32_t s_prefix, s_left;
-  const int row = blockIdx.x / rows_per, h = blockIdx.x - row * rows_per;
-  const SelRow r = rows[row];
-  const uint32_t* bw = bits + ((size_t)row * bit_rows_per + (bit_rows_per > 1 ? h : 0)) * words;
-  const float* sc = scores + ((size_t)r.b * hkv + h) * stride;
-  const uint32_t* ky = keys ? keys + (size_t)row * max_len : nullptr;
-  int32_t* o = out + ((size_t)r.b * rows_per + h) * out_stride;
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  auto key_at = [&](int x) { return ky ? ky[x] : order_key(sc[x]); };
-  auto can = [&](int x) { return x < r.limit && ((bw[x >> 5] >> (x & 31)) & 1u); };
+  cl.sync();
+  // ---- keys of this CTA's positions
+  const int x0 = rank * per, mine = max(0, min(per, r.limit - x0));
+  auto fresh = [&](int x) {
+    return (bits[x >> 5] >> (x & 31)) & 1u ? key_of(sc, stride, hkv, h, per_head, x0 + x) : 0xFFFFFFFFu;
+  };
+  if constexpr (kStored) {
+#pragma unroll 4
+    for (int x = tid; x < mine; x += kSelThreads) keys[x] = fresh(x);
+    __syncthreads();
+  }
+  auto key = [&](int x) { return kStored ? keys[x] : fresh(x); };
+  // ---- the n-th least key, digit by digit
   uint32_t prefix = 0u, left = (uint32_t)r.want;
   bool all = false;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0u;
-    __syncthreads();
-    for (int x = tid; x < r.limit; x += 1024)
-      if (can(x)) {
-        const uint32_t k = key_at(x);
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+#pragma unroll 1
+  for (int d = 0; d < 3; ++d) {
+    const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0);
+    const uint32_t mask = d == 2 ? 1023u : 2047u;
+    const uint32_t high = d == 0 ? 0u : (d == 1 ? 0xFFE00000u : 0xFFFFFC00u);   // the bits settled so far
+    for (int x = tid; x < ((mine + 31) & ~31); x += kSelThreads) {
+      const uint32_t k = x < mine ? key(x) : 0xFFFFFFFFu;
+      const bool in = k != 0xFFFFFFFFu && ((k ^ prefix) & high) == 0u;
+      const uint32_t b = in ? (k >> shift) & mask : 0xFFFFFFFFu;
+      int same;
+      __match_all_sync(0xFFFFFFFFu, b, &same);   // scores crowd into few digits, often into one
+      if (same) {
+        if (in && lane == 0) atomicAdd(&S.hist[d][b], 32u);
+      } else if (in) {
+        atomicAdd(&S.hist[d][b], 1u);
       }
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t n = left;
-      int d = 0;
-      while (d < 256 && hist[d] < n) n -= hist[d++];
-      s_prefix = d < 256 ? (prefix | ((uint32_t)d << shift)) : 0xFFFFFFFFu;
-      s_left = d < 256 ? n : 0xFFFFFFFFu;   // fewer eligible positions than wanted: all of them
+    }
+    if (tid == 0) S.digit = 0xFFFFFFFFu;
+    cl.sync();
+    {
+      // bins 2 tid and 2 tid + 1 over all CTAs, then the first whose running sum reaches `left`
+      uint2 v = make_uint2(0u, 0u);
+#pragma unroll 8
+      for (int y = 0; y < n_cta; ++y) {
+        const uint2 q = reinterpret_cast<const uint2*>(cl.map_shared_rank(&S.hist[d][0], y))[tid];
+        v.x += q.x;
+        v.y += q.y;
+      }
+      uint32_t total;
+      const uint32_t s1 = block_scan(v.x + v.y, S.warp_sum, total), s0 = s1 - v.y;
+      if (s0 >= left && s0 - v.x < left) {   // one thread at most, none if there are too few (or left is 0)
+        S.digit = 2u * tid;
+        S.left = left - (s0 - v.x);
+      } else if (s1 >= left && s0 < left) {
+        S.digit = 2u * tid + 1u;
+        S.left = left - s0;
+      }
     }
     __syncthreads();
-    if (s_left == 0xFFFFFFFFu) {
-      all = true;
+    if (S.digit == 0xFFFFFFFFu) {   // fewer eligible positions than wanted: all of them (or none wanted)
+      all = left > 0u;
       break;
     }
-    prefix = s_prefix;
-    left = s_left;
+    prefix |= S.digit << shift;
+    left = S.left;
     __syncthreads();
   }
-  // take keys below prefix and the first `left` that equal it
-  uint32_t base = 0u, ties = 0u;
-  for (int x0 = 0; x0 < r.limit; x0 += 1024) {
-    const int x = x0 + tid;
-    const bool c = can(x);
-    const uint32_t k = c ? key_at(x) : 0u;
-    const bool below = c && (all || k < prefix), tie = c && !all && k == prefix;
-    const uint32_t tb = __ballot_sync(0xFFFFFFFFu, tie);
-    if (lane == 0) warp_t[w] = __popc(tb);
-    __syncthreads();
-    uint32_t before = ties, total_t = 0u;
-    for (int y = 0; y < 32; ++y) {
-      if (y < w) before += warp_t[y];
-      total_t += warp_t[y];
-    }
-    before += __popc(tb & ((1u << lane) - 1u));
-    const bool take = below || (tie && before < left);
-    const uint32_t nb = __ballot_sync(0xFFFFFFFFu, take);
-    if (lane == 0) warp_n[w] = __popc(nb);
-    __syncthreads();
-    uint32_t at = base, total = 0u;
-    for (int y = 0; y < 32; ++y) {
-      if (y < w) at += warp_n[y];
-      total += warp_n[y];
-    }
-    at += __popc(nb & ((1u << lane) - 1u));
-    if (take) o[at] = x;
-    base += total;
-    ties += total_t;
-    __syncthreads();
+  const bool none = r.want == 0;
+  // ---- counts per CTA, then the listing: a thread takes a run of positions (an odd number of them)
+  const int run = ((per + kSelThreads - 1) / kSelThreads) | 1;
+  const int a = min(mine, tid * run), e = min(mine, a + run);
+  uint32_t nb = 0u, nt = 0u;
+  for (int x = a; x < e; ++x) {
+    const uint32_t k = key(x);
+    if (k == 0xFFFFFFFFu) continue;
+    nb += (all || k < prefix) ? 1u : 0u;
+    nt += (!all && k == prefix) ? 1u : 0u;
   }
-  for (int64_t x = base + tid; x < out_stride; x += 1024) o[x] = -1;
+  if (none) nb = nt = 0u;
+  uint32_t tb, tt;
+  const uint32_t sb = block_scan(nb, S.warp_sum, tb), st = block_scan(nt, S.warp_sum, tt);
+  if (tid == 0) {
+    S.below = tb;
+    S.ties = tt;
+  }
+  cl.sync();
+  // every CTA's counts, one per lane
+  uint32_t yb = 0u, yt = 0u;
+  if (lane < n_cta) {
+    const SelShared* q = cl.map_shared_rank(&S, lane);
+    yb = q->below;
+    yt = q->ties;
+  }
+  uint32_t off = 0u, ties_before = 0u, count = 0u, tie_all = 0u;
+  for (int y = 0; y < n_cta; ++y) {
+    const uint32_t cb = __shfl_sync(0xFFFFFFFFu, yb, y), ct = __shfl_sync(0xFFFFFFFFu, yt, y);
+    const uint32_t took = cb + min(ct, left - min(left, tie_all));
+    if (y < rank) {
+      off += took;
+      ties_before += ct;
+    }
+    count += took;
+    tie_all += ct;
+  }
+  uint32_t t = ties_before + st - nt;   // ties before this thread's run; those before `left` are taken
+  off += sb - nb + (min(t, max(left, ties_before)) - ties_before);
+  if (!none)
+    for (int x = a; x < e; ++x) {
+      const uint32_t k = key(x);
+      if (k == 0xFFFFFFFFu) continue;
+      bool take = all || k < prefix;
+      if (!all && k == prefix) take = t++ < left;
+      if (take) o[off++] = x0 + x;
+    }
+  for (int64_t x = count + (int64_t)rank * kSelThreads + tid; x < out_stride; x += (int64_t)n_cta * kSelThreads) o[x] = -1;
+  cl.sync();   // the shared memory of every CTA is still read above
 }
 
 }  // namespace
@@ -221,7 +356,7 @@ extern "C" kv_status_t kv_select_lowest(kv_pool_t* P, const float* scores, int64
   const int hkv = P->cfg.num_kv_heads, rows_per = per_head ? hkv : 1;
   if (n_req > 65535) return fail(KV_ERR_INVALID_ARG, "kv_select_lowest: at most 65535 requests");
   std::vector<SelRow> rows((size_t)n_req);
-  int32_t max_len = 0, max_pages = 0;
+  int32_t max_len = 0;
   for (int32_t b = 0; b < n_req; ++b) {
     if (!req_ok(P, req_ids[b])) return fail(KV_ERR_INVALID_ARG, "kv_select_lowest: request %d not open", req_ids[b]);
     const Request& R = P->reqs[req_ids[b]];
@@ -233,7 +368,6 @@ extern "C" kv_status_t kv_select_lowest(kv_pool_t* P, const float* scores, int64
       return fail(KV_ERR_INVALID_ARG, "kv_select_lowest: n_select[%d] = %d is not in [0, out_stride]", b, n_select[b]);
     rows[(size_t)b] = SelRow{b, req_ids[b], (int32_t)std::max<int64_t>(0, n - protect), n_select[b]};
     max_len = std::max(max_len, rows[(size_t)b].limit);
-    max_pages = std::max(max_pages, (int32_t)R.table.size());
   }
   if (out_stride == 0) return KV_OK;
   DeviceGuard dg(P->cfg.device);
@@ -243,37 +377,48 @@ extern "C" kv_status_t kv_select_lowest(kv_pool_t* P, const float* scores, int64
   if ((st = order_after_previous(P, s)) != KV_OK) return st;
   if ((st = sync_positions(P, s)) != KV_OK) return st;
   const bool hd = !P->hdead.empty();
-  const int bit_rows_per = per_head && hd ? hkv : 1;
-  const int words = std::max(1, (max_len + 31) / 32);
-  const size_t bit_bytes = (size_t)n_req * bit_rows_per * words * sizeof(uint32_t);
-  const size_t rows_off = (bit_bytes + 255) & ~size_t(255);
-  const size_t key_off = (rows_off + (size_t)n_req * sizeof(SelRow) + 255) & ~size_t(255);
-  const size_t key_bytes = per_head ? 0 : (size_t)n_req * std::max(1, max_len) * sizeof(uint32_t);
-  if ((st = ensure(P->select, key_off + key_bytes)) != KV_OK) return st;
-  uint8_t* base = (uint8_t*)P->select.ptr;
-  uint32_t* bits = (uint32_t*)base;
-  const SelRow* d_rows = (const SelRow*)(base + rows_off);
-  uint32_t* keys = per_head ? nullptr : (uint32_t*)(base + key_off);
-  Upload u;
-  u.add(rows.data(), rows.size() * sizeof(SelRow));
-  if ((st = h2d(P, base + rows_off, u, s)) != KV_OK) return st;
-  KV_CUDA(cudaMemsetAsync(bits, 0, bit_bytes, s));
-  if (max_pages > 0 && max_len > 0) {
-    ++P->launches;
-    eligible_kernel<<<dim3((unsigned)((max_pages + 7) / 8), (unsigned)n_req), 256, 0, s>>>(
-        d_rows, P->d_table, P->cfg.max_pages_per_request, P->d_ntab, hd ? P->d_hdead : nullptr, P->d_pos, hkv,
-        bit_rows_per, words, bits);
-    KV_CUDA(cudaGetLastError());
-    if (!per_head) {
-      ++P->launches;
-      sum_key_kernel<<<dim3((unsigned)((max_len + 255) / 256), (unsigned)n_req), 256, 0, s>>>(
-          d_rows, scores, score_stride, hkv, max_len, keys);
-      KV_CUDA(cudaGetLastError());
-    }
+  // CTAs per row: 2,048 positions or more each, about two per SM over all rows, and as many as the
+  // row's keys need
+  const int n_rows = n_req * rows_per;
+  int n_cta = 1;
+  while (n_cta < 8 && (max_len > 2048 * n_cta) && (int64_t)n_rows * n_cta * 2 <= 2 * P->sm_count) n_cta *= 2;
+  while (n_cta < 8 && max_len > kSelStored * n_cta) n_cta *= 2;
+  if (max_len > kSelMost * n_cta)
+    return fail(KV_ERR_INVALID_ARG, "kv_select_lowest: a request holds more than %d positions", 8 * kSelMost);
+  const int per = std::max(32, ((max_len + n_cta - 1) / n_cta + 31) & ~31);
+  auto* kernel = per <= kSelStored ? select_kernel<true> : select_kernel<false>;   // longer rows read their keys again
+  static std::atomic<uint64_t> attr_set{0};
+  if (!(attr_set.load() >> (P->cfg.device & 63) & 1u)) {
+    KV_CUDA(cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, sel_smem(kSelStored)));
+    KV_CUDA(cudaFuncSetAttribute(select_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, sel_smem(kSelMost)));
+    attr_set.fetch_or(uint64_t(1) << (P->cfg.device & 63));
   }
+  SelRows by_value;
+  const SelRow* d_rows = nullptr;
+  if (n_req <= kRowsByValue) {
+    std::copy(rows.begin(), rows.end(), by_value.r);
+  } else {
+    Upload u;
+    u.add(rows.data(), rows.size() * sizeof(SelRow));
+    if ((st = ensure(P->select, u.size)) != KV_OK) return st;
+    if ((st = h2d(P, P->select.ptr, u, s)) != KV_OK) return st;
+    d_rows = (const SelRow*)P->select.ptr;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)n_cta;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(n_rows * n_cta));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = (size_t)sel_smem(per);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   ++P->launches;
-  select_kernel<<<(unsigned)(n_req * rows_per), 1024, 0, s>>>(d_rows, bits, bit_rows_per, words, scores, score_stride,
-                                                             hkv, keys, max_len, rows_per, out, out_stride);
-  KV_CUDA(cudaGetLastError());
+  KV_CUDA(cudaLaunchKernelEx(&cfg, kernel, by_value, d_rows, (const Entry*)P->d_table,
+                             (int)P->cfg.max_pages_per_request, (const int32_t*)P->d_ntab,
+                             (const uint32_t*)(hd ? P->d_hdead : nullptr), (const int32_t*)P->d_pos, hkv,
+                             (int)(per_head ? 1 : 0), scores, score_stride, per, out, out_stride));
   return KV_OK;
 }
