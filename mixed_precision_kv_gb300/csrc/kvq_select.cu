@@ -71,8 +71,8 @@ __device__ __forceinline__ uint32_t eligible_slots(const Entry& e, const uint32_
 }
 // Key of a position: the head's score, or the heads' sum as if taken in 64 bits and
 // rounded once.  fp64 runs at 1/64 of the fp32 rate here, so the sum is carried as an
-// unevaluated pair of fp32 (48 bits); values so large that the pair could overflow, and
-// what is not finite, take the fp64 path.
+// unevaluated pair of fp32 (48 bits); a sum that overflows on the way, or is not
+// finite, takes the fp64 path.
 __device__ __noinline__ float sum_wide(const float* sc, int64_t stride, int hkv, int x) {
   double sum = 0.0;
   for (int y = 0; y < hkv; ++y) sum += (double)__ldg(sc + (size_t)y * stride + x);
@@ -80,26 +80,27 @@ __device__ __noinline__ float sum_wide(const float* sc, int64_t stride, int hkv,
 }
 __device__ __forceinline__ uint32_t key_of(const float* sc, int64_t stride, int hkv, int h, bool per_head, int x) {
   if (per_head) return order_key(__ldg(sc + (size_t)h * stride + x));
-  float hi = 0.0f, lo = 0.0f, top = 0.0f;
-  bool odd = false;
-  for (int y = 0; y < hkv; y += 8) {
+  float hi = 0.0f, lo = 0.0f;
+  auto add = [&](float f) {
+    const float t = __fadd_rn(hi, f), b = __fsub_rn(t, hi);   // hi + f = t + e exactly
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(f, b)));
+    hi = t;
+  };
+  const float* p = sc + x;
+  int y = 0;
+  for (; y + 8 <= hkv; y += 8, p += 8 * stride) {
     float f[8];
 #pragma unroll
-    for (int z = 0; z < 8; ++z) f[z] = y + z < hkv ? __ldg(sc + (size_t)(y + z) * stride + x) : 0.0f;
+    for (int z = 0; z < 8; ++z) f[z] = __ldg(p + z * stride);
 #pragma unroll
-    for (int z = 0; z < 8; ++z) {
-      odd |= f[z] != f[z];
-      top = fmaxf(top, fabsf(f[z]));
-      const float t = __fadd_rn(hi, f[z]), b = __fsub_rn(t, hi);   // hi + f = t + e exactly
-      const float e = __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(f[z], b));
-      hi = t;
-      lo = __fadd_rn(lo, e);
-    }
+    for (int z = 0; z < 8; ++z) add(f[z]);
   }
-  if (odd || !(top < 1.0e36f)) return order_key(sum_wide(sc, stride, hkv, x));
-  return order_key(__fadd_rn(hi, lo));
+  for (; y < hkv; ++y, p += stride) add(__ldg(p));
+  const float sum = __fadd_rn(hi, lo);
+  // an overflow on the way leaves an infinity or a NaN behind
+  return order_key(fabsf(sum) < INFINITY ? sum : sum_wide(sc, stride, hkv, x));
 }
-// Inclusive sum over the block's 1024 threads; `total` is the whole sum.
+// Inclusive sum over the block's 512 threads; `total` is the whole sum.
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, uint32_t& total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   uint32_t x = v;
@@ -110,13 +111,13 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, u
   }
   if (lane == 31) warp_sum[w] = x;
   __syncthreads();
-  uint32_t t = warp_sum[lane];
+  uint32_t t = warp_sum[lane & 15];   // lanes 16 .. 31: the same, not read below
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+  for (int o = 1; o < 16; o <<= 1) {
     const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, t, o);
     if (lane >= o) t += y;
   }
-  total = __shfl_sync(0xFFFFFFFFu, t, 31);
+  total = __shfl_sync(0xFFFFFFFFu, t, 15);
   const uint32_t before = w ? __shfl_sync(0xFFFFFFFFu, t, w - 1) : 0u;
   __syncthreads();
   return before + x;
@@ -131,13 +132,15 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, u
 // Bound by the scores' bytes for long rows, by a dozen barriers for short ones.
 // 16 x 100K positions, 8 heads summed: 380 us with one CTA per row reading its keys
 // once per digit, 36 us so.
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;            // two CTAs per SM: clusters of eight fit four SMs
 constexpr int kSelStored = 48 * 1024;      // positions per CTA whose keys fit its shared memory
 constexpr int kSelMost = 3 * 512 * 1024;   // ... whose bits do
 constexpr int sel_smem(int per) { return (per <= kSelStored ? per * 4 : 0) + per / 8; }
 constexpr int kBins = 2048;                // digits of 11, 11 and 10 bits
+static_assert(kBins == 4 * kSelThreads, "four bins per thread");
 struct SelShared {
-  uint32_t hist[3][kBins], warp_sum[32];
+  alignas(16) uint32_t hist[3][kBins];
+  uint32_t warp_sum[32];
   uint32_t below, ties;      // of this CTA
   uint32_t digit, left;
 };
@@ -166,7 +169,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(
   cl.sync();
   // ---- eligible positions, four pages of a warp in flight
   const Entry* tab = table + (size_t)r.req * max_pages;
-  for (int p0 = (rank * 32 + w) * 4; p0 < n_pages; p0 += n_cta * 128) {
+  constexpr int kWarps = kSelThreads / 32;
+  for (int p0 = (rank * kWarps + w) * 4; p0 < n_pages; p0 += n_cta * kWarps * 4) {
     Entry e[4];
     int32_t at[4];
 #pragma unroll
@@ -220,22 +224,22 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(
     if (tid == 0) S.digit = 0xFFFFFFFFu;
     cl.sync();
     {
-      // bins 2 tid and 2 tid + 1 over all CTAs, then the first whose running sum reaches `left`
-      uint2 v = make_uint2(0u, 0u);
+      // bins 4 tid .. 4 tid + 3 over all CTAs, then the first whose running sum reaches `left`
+      uint32_t v[4] = {0u, 0u, 0u, 0u};
 #pragma unroll 8
       for (int y = 0; y < n_cta; ++y) {
-        const uint2 q = reinterpret_cast<const uint2*>(cl.map_shared_rank(&S.hist[d][0], y))[tid];
-        v.x += q.x;
-        v.y += q.y;
+        const uint4 q = reinterpret_cast<const uint4*>(cl.map_shared_rank(&S.hist[d][0], y))[tid];
+        v[0] += q.x; v[1] += q.y; v[2] += q.z; v[3] += q.w;
       }
       uint32_t total;
-      const uint32_t s1 = block_scan(v.x + v.y, S.warp_sum, total), s0 = s1 - v.y;
-      if (s0 >= left && s0 - v.x < left) {   // one thread at most, none if there are too few (or left is 0)
-        S.digit = 2u * tid;
-        S.left = left - (s0 - v.x);
-      } else if (s1 >= left && s0 < left) {
-        S.digit = 2u * tid + 1u;
-        S.left = left - s0;
+      uint32_t run = block_scan(v[0] + v[1] + v[2] + v[3], S.warp_sum, total) - (v[0] + v[1] + v[2] + v[3]);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        if (run < left && run + v[y] >= left) {   // one bin at most, none if there are too few (or left is 0)
+          S.digit = 4u * tid + y;
+          S.left = left - run;
+        }
+        run += v[y];
       }
     }
     __syncthreads();
@@ -377,11 +381,12 @@ extern "C" kv_status_t kv_select_lowest(kv_pool_t* P, const float* scores, int64
   if ((st = order_after_previous(P, s)) != KV_OK) return st;
   if ((st = sync_positions(P, s)) != KV_OK) return st;
   const bool hd = !P->hdead.empty();
-  // CTAs per row: 2,048 positions or more each, about two per SM over all rows, and as many as the
-  // row's keys need
+  // CTAs per row: at most two per SM over all rows (more would wait for a place: 64 rows of 20-32K
+  // positions took 52 us with 256 CTAs and 72 us with 512), 2,048 positions or more each, and as many
+  // as the row's keys need; clusters of 16 were slower than of 8 (16 rows of 100K: 117 and 62 us).
   const int n_rows = n_req * rows_per;
   int n_cta = 1;
-  while (n_cta < 8 && (max_len > 2048 * n_cta) && (int64_t)n_rows * n_cta * 2 <= 2 * P->sm_count) n_cta *= 2;
+  while (n_cta < 8 && max_len > 2048 * n_cta && (int64_t)n_rows * n_cta * 2 <= 2 * P->sm_count) n_cta *= 2;
   while (n_cta < 8 && max_len > kSelStored * n_cta) n_cta *= 2;
   if (max_len > kSelMost * n_cta)
     return fail(KV_ERR_INVALID_ARG, "kv_select_lowest: a request holds more than %d positions", 8 * kSelMost);
