@@ -19,6 +19,9 @@ namespace {
 // channels): the parts' m and l at once, a part per lane, then their O by eights.
 // Bound by the partials' bytes, which are still in L2.
 constexpr int kMergeRows = 8;
+// kWide: a part holds 128 rows as [channels / 4][row][4], then (m, l) [row] (as the
+// wide kernel's threads, a row each, write them in whole lines); else [row][kAttPart].
+template <bool kWide>
 __global__ void __launch_bounds__(32 * kMergeRows) attend_merge_kernel(AttArgs A, const AttUnit* __restrict__ units,
                                                                        const AttMerge* __restrict__ merges,
                                                                        const float* __restrict__ part, int part_rows) {
@@ -27,10 +30,12 @@ __global__ void __launch_bounds__(32 * kMergeRows) attend_merge_kernel(AttArgs A
   if (i >= D.rows) return;
   const AttUnit u = units[D.unit];
   const size_t step = (size_t)D.stride * part_rows * kAttPart;
-  const float* base = part + ((size_t)D.part0 * part_rows + i) * kAttPart;
+  const float* base = part + (size_t)D.part0 * part_rows * kAttPart;
+  const float* bml = base + (kWide ? (size_t)part_rows * kHeadDim + 2 * i : (size_t)i * kAttPart + kHeadDim);
+  base += kWide ? ((size_t)lane * part_rows + i) * 4 : (size_t)i * kAttPart + 4 * lane;
   float M = -INFINITY;
   for (int p0 = 0; p0 < D.n_parts; p0 += 32)
-    if (p0 + lane < D.n_parts) M = fmaxf(M, base[(size_t)(p0 + lane) * step + kHeadDim]);
+    if (p0 + lane < D.n_parts) M = fmaxf(M, bml[(size_t)(p0 + lane) * step]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
   float L = 0.0f;
@@ -38,7 +43,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) attend_merge_kernel(AttArgs A
   for (int p0 = 0; p0 < D.n_parts; p0 += 32) {
     float f = 0.0f;
     if (p0 + lane < D.n_parts) {
-      const float2 ml = *reinterpret_cast<const float2*>(base + (size_t)(p0 + lane) * step + kHeadDim);
+      const float2 ml = *reinterpret_cast<const float2*>(bml + (size_t)(p0 + lane) * step);
       // a part that saw nothing (m = -inf, l = 0) adds nothing; one with a NaN sum keeps it
       f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2f(ml.x - M);
       L = fmaf(ml.y, f, L);
@@ -48,7 +53,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) attend_merge_kernel(AttArgs A
       float4 a[8];
 #pragma unroll
       for (int y = 0; y < 8; ++y)
-        a[y] = *reinterpret_cast<const float4*>(base + (size_t)(p0 + min(p + y, n - 1)) * step + 4 * lane);
+        a[y] = *reinterpret_cast<const float4*>(base + (size_t)(p0 + min(p + y, n - 1)) * step);
 #pragma unroll
       for (int y = 0; y < 8; ++y) {
         const float w = __shfl_sync(0xFFFFFFFFu, f, (p + y) & 31);
@@ -74,11 +79,13 @@ __global__ void __launch_bounds__(32 * kMergeRows) attend_merge_kernel(AttArgs A
 }
 
 cudaError_t launch_attend_merge(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const AttMerge* d_merges,
-                                int n_merges, int max_rows, const float* d_part, int part_rows, cudaStream_t s) {
+                                int n_merges, int max_rows, const float* d_part, int part_rows, bool wide,
+                                cudaStream_t s) {
+  auto* kernel = wide ? attend_merge_kernel<true> : attend_merge_kernel<false>;
   for (int a = 0; a < n_merges; a += 65535) {
     ++P->launches;
-    attend_merge_kernel<<<dim3((unsigned)((max_rows + kMergeRows - 1) / kMergeRows), (unsigned)std::min(65535, n_merges - a)),
-                          32 * kMergeRows, 0, s>>>(
+    kernel<<<dim3((unsigned)((max_rows + kMergeRows - 1) / kMergeRows), (unsigned)std::min(65535, n_merges - a)),
+             32 * kMergeRows, 0, s>>>(
         A, d_units, d_merges + a, d_part, part_rows);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -365,7 +372,7 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
   auto merge = [&](const Placed& x, const AttPlan& p, int part_rows) -> cudaError_t {
     if (p.merges.empty()) return cudaSuccess;
     return launch_attend_merge(P, A, (const AttUnit*)(base + x.units), (const AttMerge*)(base + x.merges),
-                               (int)p.merges.size(), p.merge_rows, (const float*)(base + x.parts), part_rows, s);
+                               (int)p.merges.size(), p.merge_rows, (const float*)(base + x.parts), part_rows, part_rows == 128, s);
   };
   if (!few.empty()) {
     KV_CUDA(launch_attend_few(P, R, A, (const AttUnit*)(base + xf.units), (const AttItem*)(base + xf.items),

@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(kThreads<R>, 1) attend_few_kernel(
     uint32_t page_tiles = 0, tc = 0, bad = 0u;   // tc: tiles of this CTA so far
     bool ok = true;
     const bool qal = ((uintptr_t)A.q & 15) == 0;
+    const RowMap rows(g);
     if constexpr (R == 64) {
       for (int x = tid; x < 1024; x += 256) reinterpret_cast<uint4*>(S.one)[x] = make_uint4(0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u);
     } else if (hf == 0) {
@@ -188,15 +189,12 @@ __global__ void __launch_bounds__(kThreads<R>, 1) attend_few_kernel(
       const AttItem I = items[it];
       const AttUnit u = units[I.unit];
       const Tiles T = tiles_of<R>(A, u, I.row0);
-      auto row_at = [&](int r) {
-        return ((size_t)(u.tok0 + r / g) * A.hq + (size_t)u.kvh * g + r % g) * kHeadDim;
-      };
       // ---- Q: 256 / R threads per row; scaled by a power of two so that its largest element is in [2^7, 2^8)
       {
         constexpr int kPer = R == 16 ? 16 : 256 / R, kRuns = 16 / kPer;
         const int n = tid / kPer, sub = tid % kPer;
         const bool valid = n < T.rows;
-        const uint16_t* qr = A.q + row_at(I.row0 + (valid ? n : 0));
+        const uint16_t* qr = A.q + rows.at(A, u, I.row0 + (valid ? n : 0));
         uint4 w[kRuns];
 #pragma unroll
         for (int y = 0; y < kRuns; ++y) w[y] = load8(qr + 8 * (sub + kPer * y), qal);
@@ -211,8 +209,8 @@ __global__ void __launch_bounds__(kThreads<R>, 1) attend_few_kernel(
         }
 #pragma unroll
         for (int o = kPer / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-        const int e = mx > 0.0f && mx < INFINITY ? max(-100, min(100, 7 - ilogbf(mx))) : 0;
-        const float mul = copysignf(__int_as_float((e + 127) << 23), A.scale_log2);
+        const int e = q_exponent(mx);
+        const float mul = copysignf(pow2f(e), A.scale_log2);
 #pragma unroll
         for (int y = 0; y < kRuns; ++y) {
           const int run = sub + kPer * y, gr = run >> 2, i = run & 3;
@@ -232,10 +230,10 @@ __global__ void __launch_bounds__(kThreads<R>, 1) attend_few_kernel(
         }
         if (sub == 0) {
           // (a factor below 1e-30 makes every logit 0, as 1e-30 does; kNever times it must stay far below 0)
-          S.rf[n] = fmaxf(fabsf(A.scale_log2) * __int_as_float((127 - e) << 23), 1e-30f);
+          S.rf[n] = fmaxf(fabsf(A.scale_log2) * pow2f(-e), 1e-30f);
           S.nm[n] = kUnseen;
           S.m[n] = -INFINITY;
-          S.tree[n] = A.tree && valid ? A.tree[u.tok0 + (I.row0 + n) / g] : 0ull;
+          S.tree[n] = A.tree && valid ? A.tree[u.tok0 + rows.token(I.row0 + n)] : 0ull;
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -395,7 +393,7 @@ __global__ void __launch_bounds__(kThreads<R>, 1) attend_few_kernel(
             const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);   // a NaN stays
             const float v = __uint_as_float(o[n]) * inv;
             if (!(fabsf(v) < INFINITY)) bad = 1u;
-            A.out[row_at(I.row0 + c + n) + key] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            A.out[rows.at(A, u, I.row0 + c + n) + key] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
           } else {
             pp[(size_t)(c + n) * kAttPart + key] = __uint_as_float(o[n]);
             if (key == 0) *reinterpret_cast<float2*>(pp + (size_t)(c + n) * kAttPart + kHeadDim) = make_float2(S.m[c + n], L);

@@ -396,6 +396,24 @@ __device__ __noinline__ uint4 load8_unaligned(const uint16_t* p) {
 __device__ __forceinline__ uint4 load8(const uint16_t* p, bool aligned) {
   return aligned ? __ldg(reinterpret_cast<const uint4*>(p)) : load8_unaligned(p);
 }
+// Power-of-two scale of a row of q: exponent e so that mx 2^e lies in [2^7, 2^8)
+// (0 for a row that is zero or not finite).
+__device__ __forceinline__ int q_exponent(float mx) {
+  return mx > 0.0f && mx < INFINITY ? max(-100, min(100, 134 - (int)(__float_as_uint(mx) >> 23))) : 0;
+}
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// Rows of a unit: row / g and the row's offset in q and out.  g <= 8, so the high
+// word of row * ceil(2^32 / g) is the quotient for every row below 2^29.
+struct RowMap {
+  uint32_t magic;
+  int g;
+  __device__ __forceinline__ explicit RowMap(int g_) : magic(0xFFFFFFFFu / (uint32_t)g_ + 1u), g(g_) {}
+  __device__ __forceinline__ int token(int row) const { return g == 1 ? row : (int)__umulhi((uint32_t)row, magic); }
+  __device__ __forceinline__ size_t at(const AttArgs& A, const AttUnit& u, int row) const {
+    const int t = token(row);
+    return ((size_t)(u.tok0 + t) * A.hq + (size_t)(u.kvh * g + row - t * g)) * kHeadDim;
+  }
+};
 // 8 values in order8, scaled by 2^e exactly (mul), as binary16
 __device__ __forceinline__ void order8_f16(const uint4& x, float mul, uint32_t (&out)[4], uint32_t& bad) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};

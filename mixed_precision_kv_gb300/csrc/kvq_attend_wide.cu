@@ -290,7 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
     const uint32_t ts = tl + 128u * x, to = tl + 256u + 128u * x;
     uint32_t s_phase = 0, o_phase = 0, bad = 0u;
     bool ok = true;
-    const bool qal = ((uintptr_t)A.q & 15) == 0;
+    const bool qal = ((uintptr_t)A.q & 15) == 0, oal = ((uintptr_t)A.out & 15) == 0;
+    const RowMap rows(g);
     for (int it = i0; it < i1 && ok; ++it) {
       const AttItem I = items[it];
       const AttUnit u = units[I.unit];
@@ -298,11 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
       const bool one = T.rows <= 128;                      // both warpgroups: the same rows
       const int rl = one ? rt : 128 * x + rt;              // row in the block
       const bool valid = rl < T.rows;
-      const int row = I.row0 + (valid ? rl : 0), t = row / g;
-      auto row_at = [&](int r) {
-        return ((size_t)(u.tok0 + r / g) * A.hq + (size_t)u.kvh * g + r % g) * kHeadDim;
-      };
-      const size_t at = row_at(row);
+      const int t = rows.token(I.row0 + (valid ? rl : 0));
       // ---- Q: every row scaled by a power of two so that its largest element is in [2^7, 2^8).  A warp
       // loads its 32 rows two at a time (16 lanes each), 16 rows in flight.
       float rf = 0.0f;
@@ -312,10 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
         for (int y0 = 0; y0 < 16; y0 += 8) {
           uint4 w[8];
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const int r = min(w32 + 2 * (y0 + y) + half, T.rows - 1);
-            w[y] = load8(A.q + row_at(I.row0 + r) + 8 * c, qal);
-          }
+          for (int y = 0; y < 8; ++y)
+            w[y] = load8(A.q + rows.at(A, u, I.row0 + min(w32 + 2 * (y0 + y) + half, T.rows - 1)) + 8 * c, qal);
 #pragma unroll
           for (int y = 0; y < 8; ++y) {
             const uint32_t wd[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
@@ -324,19 +319,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
             for (int k = 0; k < 4; ++k) {
               f[2 * k] = bf_f(wd[k] & 0xFFFFu);
               f[2 * k + 1] = __uint_as_float(wd[k] & 0xFFFF0000u);
-              mx = fmaxf(mx, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
+              mx = fmaxf(fmaxf(mx, fabsf(f[2 * k])), fabsf(f[2 * k + 1]));
             }
 #pragma unroll
             for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-            const int e = mx > 0.0f && mx < INFINITY ? max(-100, min(100, 7 - ilogbf(mx))) : 0;
-            const float mul = copysignf(__int_as_float((e + 127) << 23), A.scale_log2);
+            const int e = q_exponent(mx);
+            const float mul = copysignf(pow2f(e), A.scale_log2);
             // (a factor below 1e-30 makes every logit 0, as 1e-30 does; kNever times it must stay far below 0)
-            const float rr = fmaxf(fabsf(A.scale_log2) * __int_as_float((127 - e) << 23), 1e-30f);
+            const float rr = fmaxf(fabsf(A.scale_log2) * pow2f(-e), 1e-30f);
             const float mine = __shfl_sync(0xFFFFFFFFu, rr, (lane & 1) << 4);
             if ((lane >> 1) == y0 + y) rf = mine;   // the thread's own row
-            const int rr0 = (rt & ~31) + 2 * (y0 + y) + half;
             if (!one || x == 0)
-              *reinterpret_cast<uint4*>(S.q[x] + tile_off(128, rr0, c)) =
+              *reinterpret_cast<uint4*>(S.q[x] + tile_off(128, (rt & ~31) + 2 * (y0 + y) + half, c)) =
                   make_uint4(f16x2(f[0] * mul, f[4] * mul), f16x2(f[1] * mul, f[5] * mul), f16x2(f[2] * mul, f[6] * mul),
                              f16x2(f[3] * mul, f[7] * mul));
           }
@@ -462,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // a NaN stays
       // an infinite sum or a NaN: a value of the cache past binary16 (or of q)
       if (valid && !(l < INFINITY)) bad = 1u;
-      float* const pp = part + (size_t)(whole ? 0 : I.part + x) * 128 * kAttPart + (size_t)rt * kAttPart;
+      float4* const pp = reinterpret_cast<float4*>(part + (size_t)(whole ? 0 : I.part + x) * 128 * kAttPart) + rt;
+      float check = 0.0f;   // becomes a NaN if any element is not finite
 #pragma unroll 1
       for (int c = 0; c < 8; ++c) {
         uint32_t o[16];
@@ -473,36 +468,51 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
 #pragma unroll
           for (int j = 0; j < 16; ++j) o[j] = 0u;
         }
-        if (valid && whole) {
-          if (qal && ((uintptr_t)A.out & 15) == 0) {
+        if (whole) {
+          // rows go through the warp's own rows of Q, which every MMA has read, to be written whole
+          uint32_t w[8];
 #pragma unroll
-            for (int j = 0; j < 16; j += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float a = __uint_as_float(o[j + 2 * k]) * inv, b = __uint_as_float(o[j + 2 * k + 1]) * inv;
-                if (!(fabsf(a) < INFINITY) || !(fabsf(b) < INFINITY)) bad = 1u;
-                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(b), "f"(a));
-              }
-              *reinterpret_cast<uint4*>(A.out + at + 16 * c + j) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float a = __uint_as_float(o[j]) * inv;
-              if (!(fabsf(a) < INFINITY)) bad = 1u;
-              A.out[at + 16 * c + j] = __bfloat16_as_ushort(__float2bfloat16_rn(a));
-            }
+          for (int k = 0; k < 8; ++k) {
+            const float a = __uint_as_float(o[2 * k]) * inv, b = __uint_as_float(o[2 * k + 1]) * inv;
+            check = fmaf(a, 0.0f, fmaf(b, 0.0f, check));
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(b), "f"(a));
           }
+          *reinterpret_cast<uint4*>(S.q[x] + tile_off(128, rt, 2 * c)) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(S.q[x] + tile_off(128, rt, 2 * c + 1)) = make_uint4(w[4], w[5], w[6], w[7]);
         } else if (valid) {
+          // partial: four channels of 128 rows at a time
 #pragma unroll
           for (int j = 0; j < 16; j += 4)
-            *reinterpret_cast<float4*>(pp + 16 * c + j) = make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
-                                                                      __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
+            pp[(4 * c + (j >> 2)) * 128] = make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
+                                                       __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
         }
         __syncwarp();
       }
-      if (!whole && valid) *reinterpret_cast<float2*>(pp + kHeadDim) = make_float2(m, l);
+      if (whole) {
+        if (valid && check != 0.0f) bad = 1u;
+        const int c = lane & 15, half = lane >> 4, w32 = rl - lane;
+#pragma unroll 4
+        for (int y = 0; y < 16; ++y) {
+          const int r = 2 * y + half;
+          if (w32 + r < T.rows) {
+            const uint4 w = *reinterpret_cast<const uint4*>(S.q[x] + tile_off(128, (rt & ~31) + r, c));
+            uint16_t* op = A.out + rows.at(A, u, I.row0 + w32 + r) + 8 * c;
+            if (oal) {
+              *reinterpret_cast<uint4*>(op) = w;
+            } else {
+              const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                op[2 * k] = (uint16_t)wd[k];
+                op[2 * k + 1] = (uint16_t)(wd[k] >> 16);
+              }
+            }
+          }
+        }
+        __syncwarp();   // the rows are Q again in the next item
+      } else if (valid) {
+        reinterpret_cast<float2*>(part + (size_t)(I.part + x) * 128 * kAttPart + 128 * kHeadDim)[rt] = make_float2(m, l);
+      }
     }
     if (bad) atomicOr(A.status, kStatusRange);
   } else if (warp < 10) {
