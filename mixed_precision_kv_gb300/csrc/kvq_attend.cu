@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <functional>
+#include <queue>
 #include <climits>
 #include <cmath>
 #include <vector>
@@ -19,9 +21,6 @@ namespace {
 // channels): the parts' m and l at once, a part per lane, then their O by eights.
 // Bound by the partials' bytes, which are still in L2.
 constexpr int kMergeRows = 8;
-// kWide: a part holds 128 rows as [channels / 4][row][4], then (m, l) [row] (as the
-// wide kernel's threads, a row each, write them in whole lines); else [row][kAttPart].
-template <bool kWide>
 __global__ void __launch_bounds__(32 * kMergeRows) attend_merge_kernel(AttArgs A, const AttUnit* __restrict__ units,
                                                                        const AttMerge* __restrict__ merges,
                                                                        const float* __restrict__ part, int part_rows) {
@@ -30,12 +29,10 @@ __global__ void __launch_bounds__(32 * kMergeRows) attend_merge_kernel(AttArgs A
   if (i >= D.rows) return;
   const AttUnit u = units[D.unit];
   const size_t step = (size_t)D.stride * part_rows * kAttPart;
-  const float* base = part + (size_t)D.part0 * part_rows * kAttPart;
-  const float* bml = base + (kWide ? (size_t)part_rows * kHeadDim + 2 * i : (size_t)i * kAttPart + kHeadDim);
-  base += kWide ? ((size_t)lane * part_rows + i) * 4 : (size_t)i * kAttPart + 4 * lane;
+  const float* base = part + ((size_t)D.part0 * part_rows + i) * kAttPart;
   float M = -INFINITY;
   for (int p0 = 0; p0 < D.n_parts; p0 += 32)
-    if (p0 + lane < D.n_parts) M = fmaxf(M, bml[(size_t)(p0 + lane) * step]);
+    if (p0 + lane < D.n_parts) M = fmaxf(M, base[(size_t)(p0 + lane) * step + kHeadDim]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
   float L = 0.0f;
@@ -43,7 +40,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) attend_merge_kernel(AttArgs A
   for (int p0 = 0; p0 < D.n_parts; p0 += 32) {
     float f = 0.0f;
     if (p0 + lane < D.n_parts) {
-      const float2 ml = *reinterpret_cast<const float2*>(bml + (size_t)(p0 + lane) * step);
+      const float2 ml = *reinterpret_cast<const float2*>(base + (size_t)(p0 + lane) * step + kHeadDim);
       // a part that saw nothing (m = -inf, l = 0) adds nothing; one with a NaN sum keeps it
       f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2f(ml.x - M);
       L = fmaf(ml.y, f, L);
@@ -53,7 +50,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) attend_merge_kernel(AttArgs A
       float4 a[8];
 #pragma unroll
       for (int y = 0; y < 8; ++y)
-        a[y] = *reinterpret_cast<const float4*>(base + (size_t)(p0 + min(p + y, n - 1)) * step);
+        a[y] = *reinterpret_cast<const float4*>(base + (size_t)(p0 + min(p + y, n - 1)) * step + 4 * lane);
 #pragma unroll
       for (int y = 0; y < 8; ++y) {
         const float w = __shfl_sync(0xFFFFFFFFu, f, (p + y) & 31);
@@ -78,15 +75,88 @@ __global__ void __launch_bounds__(32 * kMergeRows) attend_merge_kernel(AttArgs A
   if (bad) atomicOr(A.status, kStatusRange);
 }
 
+// The same for parts of many rows, which hold 128 rows as [channels / 4][row][4] and
+// then (m, l) [row]: a row per lane, four channels per warp, so that loads are whole
+// lines; 32 results of 128 channels then cross over through shared memory.
+constexpr int kTallRows = 128, kTallWarps = kHeadDim / 4;
+__global__ void __launch_bounds__(32 * kTallWarps) attend_merge_tall_kernel(AttArgs A, const AttUnit* __restrict__ units,
+                                                                            const AttMerge* __restrict__ merges,
+                                                                            const float* __restrict__ part) {
+  __shared__ uint2 done[32][kTallWarps + 1];
+  const AttMerge D = merges[blockIdx.y];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r0 = 32 * (int)blockIdx.x;
+  if (r0 >= D.rows) return;
+  const size_t step = (size_t)D.stride * kTallRows * kAttPart;
+  const int i = min(r0 + lane, D.rows - 1);   // rows past the end repeat the last one
+  const float* base = part + (size_t)D.part0 * kTallRows * kAttPart;
+  const float2* ml = reinterpret_cast<const float2*>(base + kTallRows * kHeadDim) + i;
+  const float4* ov = reinterpret_cast<const float4*>(base) + (size_t)warp * kTallRows + i;
+  constexpr int kAhead = 8;
+  float M = -INFINITY, L = 0.0f;
+  for (int p = 0; p < D.n_parts; p += kAhead)
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y)
+      if (p + y < D.n_parts) M = fmaxf(M, ml[(size_t)(p + y) * (step / 2)].x);
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int p = 0; p < D.n_parts; p += kAhead) {
+    float4 a[kAhead];
+    float2 b[kAhead];
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y)
+      if (p + y < D.n_parts) {
+        a[y] = ov[(size_t)(p + y) * (step / 4)];
+        b[y] = ml[(size_t)(p + y) * (step / 2)];
+      }
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y)
+      if (p + y < D.n_parts) {
+        // a part that saw nothing (m = -inf, l = 0) adds nothing; one with a NaN sum keeps it
+        const float f = b[y].x == -INFINITY ? (b[y].y == 0.0f ? 0.0f : 1.0f) : exp2f(b[y].x - M);
+        L = fmaf(b[y].y, f, L);
+        if (f != 0.0f) {
+          o.x = fmaf(a[y].x, f, o.x); o.y = fmaf(a[y].y, f, o.y); o.z = fmaf(a[y].z, f, o.z); o.w = fmaf(a[y].w, f, o.w);
+        }
+      }
+  }
+  const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
+  const float r[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+  bool bad = false;
+  uint32_t h[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (!(fabsf(r[k]) < INFINITY)) bad = true;
+    h[k] = __bfloat16_as_ushort(__float2bfloat16_rn(r[k]));
+  }
+  done[lane][warp] = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  if (bad) atomicOr(A.status, kStatusRange);
+  __syncthreads();
+  if (r0 + warp < D.rows) {
+    const AttUnit u = units[D.unit];
+    const int g = A.hq / A.hkv, row = D.row0 + r0 + warp;
+    uint16_t* op = A.out + ((size_t)(u.tok0 + row / g) * A.hq + (size_t)u.kvh * g + row % g) * kHeadDim + 4 * lane;
+    const uint2 w = done[warp][lane];
+    if (((uintptr_t)A.out & 7) == 0) {
+      *reinterpret_cast<uint2*>(op) = w;
+    } else {
+      op[0] = (uint16_t)w.x;
+      op[1] = (uint16_t)(w.x >> 16);
+      op[2] = (uint16_t)w.y;
+      op[3] = (uint16_t)(w.y >> 16);
+    }
+  }
+}
+
 cudaError_t launch_attend_merge(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const AttMerge* d_merges,
-                                int n_merges, int max_rows, const float* d_part, int part_rows, bool wide,
-                                cudaStream_t s) {
-  auto* kernel = wide ? attend_merge_kernel<true> : attend_merge_kernel<false>;
+                                int n_merges, int max_rows, const float* d_part, int part_rows, cudaStream_t s) {
+  const bool tall = part_rows == kTallRows;
+  const int per = tall ? 32 : kMergeRows;
   for (int a = 0; a < n_merges; a += 65535) {
     ++P->launches;
-    kernel<<<dim3((unsigned)((max_rows + kMergeRows - 1) / kMergeRows), (unsigned)std::min(65535, n_merges - a)),
-             32 * kMergeRows, 0, s>>>(
-        A, d_units, d_merges + a, d_part, part_rows);
+    const dim3 grid((unsigned)((max_rows + per - 1) / per), (unsigned)std::min(65535, n_merges - a));
+    if (tall)
+      attend_merge_tall_kernel<<<grid, 32 * kTallWarps, 0, s>>>(A, d_units, d_merges + a, d_part);
+    else
+      attend_merge_kernel<<<grid, 32 * kMergeRows, 0, s>>>(A, d_units, d_merges + a, d_part, part_rows);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -108,62 +178,89 @@ int block_tiles(const AttUnit& u, int g, int row0, int rows, bool kv, bool tree)
   return (u.n_pages + 3) / 4 + (u.n_fp + 127) / 128 + (kv ? (tree ? u.T - 1 : t_last) / 128 + 1 : 0);
 }
 
-// Blocks of kWideRows rows of units [u0, u1), their tiles in one line of cost,
-// cut into equal runs, one per CTA (a run may end inside a block: its pieces are
-// merged).  A tile of a block of more than 128 rows costs 2, else 1 (the MMAs'
-// time); an item 1 more for its first and last steps.  by_cta[c] gets run c.
+// Blocks of kWideRows rows of units [u0, u1).  An item costs its tiles (3700 cycles
+// each) and kWideItem more (20,000 for its rows, the first and last steps).  Whole blocks go to the least loaded CTA while they fit into an
+// equal share, units with the most tiles first; the blocks that are left are cut to
+// fill up the shares, and their pieces merged.  So most items are whole blocks, and
+// the blocks of a unit, which start together, read each tile at about the same time:
+// it comes from L2 once it has been read.  (One line of blocks cut into equal runs
+// took 1006 us for four chunks of 300 to 512 tokens over 15K to 32K, 850 us with
+// every tile in L2.)  by_cta[c] gets the items of CTA c.
 constexpr int kWideRows = 256;
+constexpr double kWideItem = 5.4;
 void plan_wide(const std::vector<AttUnit>& units, int u0, int u1, int g, bool kv, bool tree, int ctas,
                std::vector<std::vector<AttItem>>& by_cta, AttPlan& out) {
   struct Block {
-    int unit, row0, rows, tiles, cost;
+    int unit, row0, rows, tiles;
   };
-  std::vector<Block> blocks;
-  int64_t total = 0;
-  for (int x = u0; x < u1; ++x) {
+  std::vector<int> order;
+  std::vector<Block> blocks, rest;
+  double total = kWideItem * ctas;   // about one cut per CTA
+  for (int x = u0; x < u1; ++x) order.push_back(x);
+  auto tiles_of = [&](int x) { return block_tiles(units[(size_t)x], g, 0, units[(size_t)x].T * g, kv, tree); };
+  std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return tiles_of(a) > tiles_of(b); });
+  for (int x : order) {
     const int rows = units[(size_t)x].T * g;
     for (int r = 0; r < rows; r += kWideRows) {
       const int n = std::min(kWideRows, rows - r);
-      const Block b{x, r, n, block_tiles(units[(size_t)x], g, r, n, kv, tree), n > 128 ? 2 : 1};
+      const Block b{x, r, n, block_tiles(units[(size_t)x], g, r, n, kv, tree)};
       blocks.push_back(b);
-      total += (int64_t)b.tiles * b.cost + 1;
+      total += b.tiles + kWideItem;
     }
   }
-  const double share = (double)(total + ctas) / ctas;   // every CTA ends inside a block once
-  double done = 0.0;
-  int cta = 0;
+  const double share = total / ctas;
+  std::vector<double> load((size_t)ctas, 0.0);
   std::vector<std::pair<int, size_t>> pieces;   // (CTA, index) of a block's items
+  auto give = [&](int cta, const Block& b, int t0, int t1) {
+    pieces.emplace_back(cta, by_cta[(size_t)cta].size());
+    by_cta[(size_t)cta].push_back(AttItem{b.unit, b.row0, t0, t1, -1, {0, 0, 0}});
+  };
+  auto join = [&](const Block& b) {   // partials of a block, if it needs any
+    const int n = (int)pieces.size();
+    if (n == 1) return;
+    const int32_t p0 = (int32_t)out.n_parts;
+    for (int y = 0; y < n; ++y) by_cta[(size_t)pieces[(size_t)y].first][pieces[(size_t)y].second].part = p0 + 2 * y;
+    out.n_parts += 2 * n;
+    out.merges.push_back(AttMerge{b.unit, b.row0, std::min(128, b.rows), p0, n, 2});
+    if (b.rows > 128) out.merges.push_back(AttMerge{b.unit, b.row0 + 128, b.rows - 128, p0 + 1, n, 2});
+    out.merge_rows = std::max(out.merge_rows, std::min(128, b.rows));
+  };
+  std::priority_queue<std::pair<double, int>, std::vector<std::pair<double, int>>, std::greater<>> least;
+  for (int c = 0; c < ctas; ++c) least.emplace(0.0, c);
   for (const Block& b : blocks) {
+    const double cost = b.tiles + kWideItem;
+    const auto [l, c] = least.top();
+    if (l + cost > share) {
+      rest.push_back(b);
+      continue;
+    }
+    least.pop();
+    least.emplace(load[(size_t)c] = l + cost, c);
+    pieces.clear();
+    give(c, b, 0, b.tiles);
+    join(b);
+  }
+  int cta = 0;
+  double room = share - load[0];   // of the CTAs up to this one
+  for (const Block& b : rest) {
     pieces.clear();
     int t = 0;
     do {
       int take = b.tiles - t;
       if (cta < ctas - 1) {
-        const double room = (cta + 1) * share - done;
-        const int fit = (int)((room - 0.5) / b.cost + 0.5);
+        const int fit = (int)(room - kWideItem + 0.5);
         if (fit < std::min(2, take)) {   // nothing worth starting fits: the next CTA
           ++cta;
+          room += share - load[(size_t)cta];
           continue;
         }
         if (fit + 1 < take) take = fit;
       }
-      pieces.emplace_back(cta, by_cta[(size_t)cta].size());
-      by_cta[(size_t)cta].push_back(AttItem{b.unit, b.row0, t, t + take, -1, {0, 0, 0}});
-      done += (double)take * b.cost + 1.0;
+      give(cta, b, t, t + take);
+      room -= take + kWideItem;
       t += take;
     } while (t < b.tiles);
-    const int n = (int)pieces.size();
-    if (n == 1 && b.rows > 128) continue;
-    const int32_t p0 = (int32_t)out.n_parts;
-    for (int y = 0; y < n; ++y) by_cta[(size_t)pieces[(size_t)y].first][pieces[(size_t)y].second].part = p0 + 2 * y;
-    out.n_parts += 2 * n;
-    if (b.rows > 128) {
-      out.merges.push_back(AttMerge{b.unit, b.row0, 128, p0, n, 2});
-      out.merges.push_back(AttMerge{b.unit, b.row0 + 128, b.rows - 128, p0 + 1, n, 2});
-    } else {
-      out.merges.push_back(AttMerge{b.unit, b.row0, b.rows, p0, 2 * n, 1});
-    }
-    out.merge_rows = std::max(out.merge_rows, std::min(128, b.rows));
+    join(b);
   }
 }
 
@@ -217,11 +314,7 @@ void plan_few(const std::vector<AttUnit>& units, int g, int R, bool kv, bool tre
   out.cta_item.push_back((int32_t)out.items.size());
 }
 
-// The units are taken in groups whose operand tiles stay in L2 (126 MB, shared
-// with the rows of q and out) while every block of rows reads them: each CTA has
-// a run of every group, in order, so all CTAs are at the same group at about the
-// same time.  A pass holds the tiles of several groups.
-constexpr int64_t kTilesInL2 = 1400;      // 92 MB
+// A pass holds the operand tiles of as many units as fit into this many.
 constexpr int64_t kTilesPerPass = 1 << 16;   // 4.3 GB
 
 }  // namespace
@@ -314,15 +407,11 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
   };
   std::vector<Pass> passes;
   std::vector<std::vector<AttItem>> by_cta((size_t)P->sm_count);
-  int64_t most = 0, n = 0, group = 0;
-  int u0 = 0, g0 = 0, max_tiles = 0;
-  auto end_group = [&](int x) {
-    plan_wide(units, g0, x, g, kv, tr, P->sm_count, by_cta, pl);
-    g0 = x;
-    group = 0;
-  };
+  int64_t most = 0, n = 0;
+  int u0 = 0, max_tiles = 0;
   auto end_pass = [&](int x) {
     passes.push_back(Pass{u0, x, max_tiles, (int)pl.cta_item.size()});
+    plan_wide(units, u0, x, g, kv, tr, P->sm_count, by_cta, pl);
     for (auto& c : by_cta) {
       pl.cta_item.push_back((int32_t)pl.items.size());
       pl.items.insert(pl.items.end(), c.begin(), c.end());
@@ -337,17 +426,11 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
   if (!units.empty()) {
     for (int x = 0; x < (int)units.size(); ++x) {
       const int t = block_tiles(units[(size_t)x], g, 0, units[(size_t)x].T * g, kv, tr);
-      if (x > g0 && group + t > kTilesInL2) end_group(x);
-      if (x > u0 && n + t > kTilesPerPass) {
-        if (x > g0) end_group(x);
-        end_pass(x);
-      }
+      if (x > u0 && n + t > kTilesPerPass) end_pass(x);
       units[(size_t)x].tile_base = (int32_t)n;
       n += t;
-      group += t;
       max_tiles = std::max(max_tiles, t);
     }
-    end_group((int)units.size());
     end_pass((int)units.size());
   }
   struct Placed {   // a plan's arrays in the upload, its partials behind
@@ -372,7 +455,7 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
   auto merge = [&](const Placed& x, const AttPlan& p, int part_rows) -> cudaError_t {
     if (p.merges.empty()) return cudaSuccess;
     return launch_attend_merge(P, A, (const AttUnit*)(base + x.units), (const AttMerge*)(base + x.merges),
-                               (int)p.merges.size(), p.merge_rows, (const float*)(base + x.parts), part_rows, part_rows == 128, s);
+                               (int)p.merges.size(), p.merge_rows, (const float*)(base + x.parts), part_rows, s);
   };
   if (!few.empty()) {
     KV_CUDA(launch_attend_few(P, R, A, (const AttUnit*)(base + xf.units), (const AttItem*)(base + xf.items),

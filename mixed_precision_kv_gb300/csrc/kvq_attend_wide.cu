@@ -6,10 +6,10 @@
 // pages, or bf16 rows of the list or of the new tokens) into one K and one V
 // operand tile, 32 KB each, in the very layout that the MMAs read from shared
 // memory (V transposed), and the keys' live bits into four words.  Every block of
-// 256 rows reads the tiles again (from L2: the units of a call are taken in
-// groups whose tiles fit there), so this costs one pass over the pages for any
-// number of blocks.  Dequantizing inside the attention kernel instead cost eight
-// warps' issue slots per block: 2.72 ms against the present figure below.
+// 256 rows reads the tiles again, most of them from L2 (the plan starts a unit's
+// blocks together), so this costs one pass over the pages for any number of blocks.
+// Dequantizing inside the attention kernel instead cost eight warps' issue slots per
+// block: 2.72 ms for 2048 tokens of 64 heads over 32K, 1.77 ms so.
 //
 // attend_wide_kernel: a CTA takes an item: a block of up to 256 rows of a unit
 // and a run of its tiles.  Per tile
@@ -25,8 +25,8 @@
 // issues the MMAs of S_x and O_x; one thread streams tiles through a ring of
 // five.  While one warpgroup works on its S, the tensor cores work for the other;
 // two issuing threads, because the waits and commits between runs of MMAs cost one
-// thread 600 of every 1650 cycles.  A block of at most 128 rows uses the two
-// warpgroups for even and odd tiles instead (the same rows, two partial states).
+// thread 600 of every 1650 cycles.  (Even and odd tiles of a last block of at most 128
+// rows given to the two warpgroups took 3350 cycles per tile, as they are 3700.)
 //
 // What bounds it: per tile and 256 rows the tensor cores need 2048 cycles, their
 // operand reads of shared memory 1536; the exponentials 1024; the CTA's shared
@@ -296,8 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
       const AttItem I = items[it];
       const AttUnit u = units[I.unit];
       const Tiles T = tiles_of(A, u, I.row0, 256);
-      const bool one = T.rows <= 128;                      // both warpgroups: the same rows
-      const int rl = one ? rt : 128 * x + rt;              // row in the block
+      const int rl = 128 * x + rt;                         // row in the block
       const bool valid = rl < T.rows;
       const int t = rows.token(I.row0 + (valid ? rl : 0));
       // ---- Q: every row scaled by a power of two so that its largest element is in [2^7, 2^8).  A warp
@@ -329,10 +328,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
             const float rr = fmaxf(fabsf(A.scale_log2) * pow2f(-e), 1e-30f);
             const float mine = __shfl_sync(0xFFFFFFFFu, rr, (lane & 1) << 4);
             if ((lane >> 1) == y0 + y) rf = mine;   // the thread's own row
-            if (!one || x == 0)
-              *reinterpret_cast<uint4*>(S.q[x] + tile_off(128, (rt & ~31) + 2 * (y0 + y) + half, c)) =
-                  make_uint4(f16x2(f[0] * mul, f[4] * mul), f16x2(f[1] * mul, f[5] * mul), f16x2(f[2] * mul, f[6] * mul),
-                             f16x2(f[3] * mul, f[7] * mul));
+            *reinterpret_cast<uint4*>(S.q[x] + tile_off(128, (rt & ~31) + 2 * (y0 + y) + half, c)) =
+                make_uint4(f16x2(f[0] * mul, f[4] * mul), f16x2(f[1] * mul, f[5] * mul), f16x2(f[2] * mul, f[6] * mul),
+                           f16x2(f[3] * mul, f[7] * mul));
           }
         }
       }
@@ -346,7 +344,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
       bool any = false;                                    // O_x has been written in this item
       for (int tile = I.tile0; tile < I.tile1; ++tile) {
         const bool page = tile < T.pages;
-        if (one && ((tile - I.tile0) & 1) != x) continue;
         // ---- keys this row sees, 128 bits in the tiles' order
         uint32_t mk[4];
         if (page) {
@@ -531,45 +528,36 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
         return mb_wait(&S.full[e % kRing], (e / kRing) & 1u, gave_up, e ? kAttSpin : first_spins);
       };
       for (int it = i0; it < i1 && ok; ++it) {
-        const AttItem I = items[it];
-        const AttUnit u = units[I.unit];
-        const bool one = tiles_of(A, u, I.row0, 256).rows <= 128;
-        const int n = I.tile1 - I.tile0;
+        const int n = items[it].tile1 - items[it].tile0;
         if (n == 0) continue;
         ok = mb_wait(&S.q_full, q_phase, gave_up);
         if (!ok) break;
         q_phase ^= 1u;
-        const uint64_t qd = qd0 + (one ? 0u : (uint32_t)x * kTile16);
-        // A step: P V of tile t - 1 (of this x), then Q K^T of tile t into the same S, issued together
-        // so that the tensor cores see one run of 16; the other warp's run fills the time that the
-        // softmax of this one takes.  With `one`, tiles of the other parity are only counted: every entry
-        // is waited for in order (a parity does not tell one fill of a slot from the next but one).
-        uint32_t pend = 0u;       // entry of the V tile whose P is due
-        bool due = false, first = true;
+        const uint64_t qd = qd0 + (uint32_t)x * kTile16;
+        // A step: P V of tile t - 1, then Q K^T of tile t into the same S, issued together so that the
+        // tensor cores see one run of 16; the other warp's run fills the time that the softmax of this
+        // one takes.
 #pragma unroll 1
         for (int t = 0; t <= n; ++t) {
-          const uint32_t ke = 2u * (tc0 + (uint32_t)t), pv = pend;
-          const bool mine = t < n && (!one || (t & 1) == x), skip = t < n && !mine;
-          const bool did = due && (mine || t == n);
+          const uint32_t ke = 2u * (tc0 + (uint32_t)t), pv = ke - 1u;
           if (t < n) ok = ready(ke);
           // Runs of the two halves take turns: issued at will they would fall into step, both halves'
-          // MMAs at one time and both softmaxes at the next (4100 cycles per tile instead of 3200).
-          if (ok && !one && (x || turns)) ok = mb_wait(&S.turn[x], (x ? turns : turns - 1u) & 1u, gave_up);
-          if (!one) ++turns;
-          if (ok && did) {
+          // MMAs at one time and both softmaxes at the next (4100 cycles per tile instead of 3700).
+          if (ok && (x || turns)) ok = mb_wait(&S.turn[x], (x ? turns : turns - 1u) & 1u, gave_up);
+          ++turns;
+          if (ok && t) {
             ok = mb_spin(&S.p_full[x], p_phase, gave_up);
             p_phase ^= 1u;
           }
           if (!ok) break;
           tm_fence_after();
-          if (did) {
+          if (t) {
             const uint64_t b = td0 + (pv % kRing) * kTile16;
 #pragma unroll
             for (int s = 0; s < 8; ++s)
-              mma_ts(dout, ds + 8u * s, b + ((s >> 2) * 1024 + (s & 3) * 2), idesc, !first || s > 0);
-            first = due = false;
+              mma_ts(dout, ds + 8u * s, b + ((s >> 2) * 1024 + (s & 3) * 2), idesc, t > 1 || s > 0);
           }
-          if (mine) {
+          if (t < n) {
             const uint64_t b = td0 + (ke % kRing) * kTile16;
 #pragma unroll
             for (int s = 0; s < 8; ++s)
@@ -577,18 +565,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
             tm_commit(&S.s_full[x]);
             tm_commit(&S.empty[ke % kRing]);
           }
-          if (!one) mb_arrive(&S.turn[x ^ 1]);
-          if (did) tm_commit(&S.empty[pv % kRing]);
+          mb_arrive(&S.turn[x ^ 1]);
+          if (t) tm_commit(&S.empty[pv % kRing]);
           if (t == n) break;
           ok = ready(ke + 1u);   // this tile's V
           if (!ok) break;
-          if (skip) {
-            mb_arrive(&S.empty[ke % kRing]);
-            mb_arrive(&S.empty[(ke + 1u) % kRing]);
-          } else {
-            pend = ke + 1u;
-            due = true;
-          }
         }
         if (ok) tm_commit(&S.o_full);
         tc0 += (uint32_t)n;
