@@ -264,10 +264,22 @@ void plan_wide(const std::vector<AttUnit>& units, int u0, int u1, int g, bool kv
   }
 }
 
+// Which kernel.  Per key tile (cycles of a CTA) the few-row kernel unpacks for every
+// block of up to 64 rows, the other once and then works through blocks of 256; that one
+// also costs a launch more and a longer first and last step.  Up to kFewRows rows the
+// first is faster whatever the size (128 rows of 8 requests x 8 kv heads over 16K: 212 us
+// against 259), above kFewMost the second (512 rows: 783 against 390); between them the
+// call's tiles decide (256 rows: 405 against 271, but 42 against 58 for one request
+// over 4K).
+constexpr int kFewRows = 128, kFewMost = 384;
+constexpr int64_t kFewBlock = 3400, kWideTile = 3900, kWideBlock = 3900, kWideStart = 38000;
+int64_t wide_gain(int rows, int64_t tiles) {
+  return tiles * (kFewBlock * ((rows + 63) / 64) - kWideTile - kWideBlock * ((rows + 255) / 256));
+}
+
 // Few rows per unit: blocks of R rows, all key tiles of all blocks in one line, cut
 // into equal runs.  A tile costs 1 (its unpacking, whatever R), an item 3 more (its
 // rows, the first and last steps).
-constexpr int kFewRows = 256;   // units of up to this many rows
 void plan_few(const std::vector<AttUnit>& units, int g, int R, bool kv, bool tree, int sms, AttPlan& out) {
   double total = 0.0;
   int64_t tiles = 0;
@@ -379,15 +391,26 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
 
   const bool simt = P->decode_impl == KV_DECODE_SIMT;
   std::vector<AttUnit> units, few;   // many rows (or all, on the CUDA cores) and few rows per unit
+  const bool kv = k != nullptr, tr = tree != nullptr;
+  auto unit = [&](int32_t b, int h, int64_t tok0) {
+    const int32_t r = req_ids[b];
+    return AttUnit{r, h, n_new[b], (int32_t)P->reqs[r].table.size(), P->n_fp.empty() ? 0 : P->n_fp[r], 0, tok0};
+  };
+  int few_most = kFewMost;   // rows of a unit that the few-row kernel takes
+  int64_t gain = -kWideStart * P->sm_count;
+  for (int32_t b = 0; b < n_req; ++b) {
+    const int rows = n_new[b] * g;
+    if (rows > kFewMost) gain += kWideStart * P->sm_count;   // the other kernel runs anyway
+    if (rows > kFewRows && rows <= kFewMost) gain += hkv * wide_gain(rows, block_tiles(unit(b, 0, 0), g, 0, rows, kv, tr));
+  }
+  if (gain > 0) few_most = kFewRows;
   int few_rows = 0;
   int64_t tok0 = 0;
   for (int32_t b = 0; b < n_req; ++b) {
-    const int32_t r = req_ids[b];
+    const bool is_few = !simt && n_new[b] * g <= few_most;
     if (n_new[b] > 0)
-      for (int h = 0; h < hkv; ++h)
-        (!simt && n_new[b] * g <= kFewRows ? few : units)
-            .push_back(AttUnit{r, h, n_new[b], (int32_t)P->reqs[r].table.size(), P->n_fp.empty() ? 0 : P->n_fp[r], 0, tok0});
-    if (n_new[b] * g <= kFewRows) few_rows = std::max(few_rows, n_new[b] * g);
+      for (int h = 0; h < hkv; ++h) (is_few ? few : units).push_back(unit(b, h, tok0));
+    if (is_few) few_rows = std::max(few_rows, n_new[b] * g);
     tok0 += n_new[b];
   }
   if (simt) {
@@ -398,7 +421,6 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
     KV_CUDA(launch_attend_simt(P, A, (const AttUnit*)P->attend.ptr, (int)units.size(), max_new * g, s));
     return KV_OK;
   }
-  const bool kv = k != nullptr, tr = tree != nullptr;
   AttPlan pf, pl;
   const int R = few_rows <= 16 ? 16 : (few_rows <= 32 ? 32 : 64);
   if (!few.empty()) plan_few(few, g, R, kv, tr, P->sm_count, pf);

@@ -20,14 +20,16 @@
 namespace kvq {
 namespace {
 
-constexpr int kScoreWarps = 8;
+constexpr int kScoreWarps = 4;
 constexpr int kScorePages = 4;   // pages in flight per warp
 
 // Warp = a run of kScorePages table entries of one unit, lane = slot.  Bound
 // by memory: 128 g bytes of logits, 128 bytes of positions (shared by the kv
-// heads, so mostly from L2) and 256 bytes of scores per page and kv head; all
-// loads of a warp's pages are issued before the first is used.  Slots of a
-// page hold tokens in order of arrival, so the scattered scores of a page
+// heads, so mostly from L2) and 256 bytes of scores per page and kv head.  The
+// logits' loads come first: they need no table entry, and the chain entry ->
+// position -> score runs behind them (80 us for 16 requests of 100K slots and 8
+// kv heads of 8 q heads, 6.5 TB/s; 110 us with them behind the entries).  Slots
+// of a page hold tokens in order of arrival, so the scattered scores of a page
 // fall into one or two runs.
 template <int G>
 __global__ void __launch_bounds__(32 * kScoreWarps) score_add_kernel(
@@ -53,18 +55,19 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_add_kernel(
   int32_t at[kScorePages];
   float lg[kScorePages][G], old[kScorePages];
 #pragma unroll
+  for (int x = 0; x < kScorePages; ++x) {   // (past the end: the last page's again, not used)
+    const float* lp = logits + ((size_t)(uint32_t)u.pad + min(p0 + x, n - 1)) * (G * kPage) + lane;
+#pragma unroll
+    for (int h = 0; h < G; ++h) lg[x][h] = __ldcs(lp + h * kPage);
+  }
+#pragma unroll
   for (int x = 0; x < kScorePages; ++x) {
     live[x] = false;
     if (p0 + x < n) {
       const Entry e = tab[p0 + x];
       const uint32_t m = hdead ? e.live & ~hdead[(size_t)e.id * hkv + u.kvh] : e.live;
       live[x] = (m >> lane) & 1u;
-      if (live[x]) {
-        at[x] = pos[(size_t)e.id * kPage + lane];
-        const float* lp = logits + ((size_t)(uint32_t)u.pad + p0 + x) * (G * kPage) + lane;
-#pragma unroll
-        for (int h = 0; h < G; ++h) lg[x][h] = __ldcs(lp + h * kPage);
-      }
+      if (live[x]) at[x] = pos[(size_t)e.id * kPage + lane];
     }
   }
 #pragma unroll

@@ -381,3 +381,30 @@ def test_refusals(kvq):
             status.append(err.status)
     assert status == [kvq.KV_ERR_STATE]
     check(P, MMA, [0], [3], 8)
+
+
+@pytest.mark.parametrize("n_new", [[64, 20, 48, 3, 16], [33, 17, 32, 0, 1], [0, 0, 48, 47, 0]])
+def test_middle_sizes(kvq, n_new):
+    """Units of 136 to 384 rows: next to larger ones, and alone."""
+    P = Pool(kvq, 2, [mixed(n, n) for n in (300, 129, 77, 500, 0)], seed=21)
+    check(P, MMA, range(5), n_new, 16, rows=[0, 15, 16, 31, 32, 47])
+
+
+@pytest.mark.parametrize("n_new", [[2, 1], [70, 2], [100, 300]])
+def test_expired_wait_reports_timeout_once(kvq, n_new):
+    """The first wait for a copy gives up at once: a status at the next sync, and the pool goes on."""
+    P = Pool(kvq, 2, [mixed(600, 1), mixed(200, 2)], seed=22)
+    q, k, v = (rand((sum(n_new), h, 128), P.gen) for h in (8, 2, 2))
+    P.pool.set_decode_impl(MMA)
+    good = P.pool.attend(q, P.ids, n_new, SCALE, k, v)
+    P.pool.sync()
+    P.pool.set_wait_limit(0)
+    P.pool.attend(q, P.ids, n_new, SCALE, k, v)
+    with pytest.raises(kvq.KVError) as e:
+        P.pool.sync()
+    assert e.value.status == kvq.KV_ERR_DEVICE_TIMEOUT
+    P.pool.sync()
+    P.pool.set_wait_limit(-1)
+    again = P.pool.attend(q, P.ids, n_new, SCALE, k, v)
+    P.pool.sync()
+    assert torch.equal(again, good)
