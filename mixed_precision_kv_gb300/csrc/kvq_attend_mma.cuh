@@ -73,12 +73,6 @@ __device__ __forceinline__ void bulk_to_smem(void* dst, const void* src, uint32_
                ::"r"(sm32(dst)), "l"(src), "r"(bytes), "r"(sm32(b)) : "memory");
 }
 
-// ---- registers of a warpgroup (all its warps) ------------------------------
-template <int N>
-__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
 // ---- tcgen05 ---------------------------------------------------------------
 __device__ __forceinline__ void tm_alloc(uint32_t* slot, uint32_t cols) {   // one warp
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sm32(slot)), "r"(cols) : "memory");

