@@ -299,8 +299,14 @@ KVQ_API kv_status_t kv_decode_attn_groups(kv_pool_t* const* pools, int32_t n_poo
  * q, k, v and out need 2-byte alignment only.  num_q_heads as in
  * kv_decode_attn; n_req x num_kv_heads <= 65535.  K, V and the softmax weights
  * pass through binary16 (logits, sums and outputs are accumulated in fp32 and
- * rounded to bf16 once); with KV_DECODE_SIMT everything is fp32.  The call
- * plans on the host: on a stream that is being captured it is KV_ERR_STATE. */
+ * rounded to bf16 once); with KV_DECODE_SIMT everything is fp32.  A list token
+ * past binary16's range counts as above; a row of q that is not finite, or whose
+ * sums are not, gives a row that is not finite, and KV_ERR_RANGE.  Workspace:
+ * 64 KB per 128 keys and kv head of requests with more than 128 rows (n_new x q
+ * heads per kv head), up to 4.3 GB or one kv head of the longest request, and
+ * the rows' partial sums; it grows with cudaMalloc.  At most 2^31 rows of q.
+ * The call plans on the host: on a stream that is being captured it is
+ * KV_ERR_STATE. */
 KVQ_API kv_status_t kv_attend(kv_pool_t* pool, const void* q, const void* k, const void* v, const uint64_t* tree,
                               const int32_t* req_ids, const int32_t* n_new, int32_t n_req, int32_t num_q_heads,
                               float softmax_scale, void* out, void* stream);

@@ -8,6 +8,7 @@
 #include <queue>
 #include <climits>
 #include <cmath>
+#include <new>
 #include <vector>
 
 #include "kvq_attend.h"
@@ -336,7 +337,7 @@ using namespace kvq;
 
 extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, const void* v, const uint64_t* tree,
                                  const int32_t* req_ids, const int32_t* n_new, int32_t n_req, int32_t hq,
-                                 float softmax_scale, void* out, void* stream) {
+                                 float softmax_scale, void* out, void* stream) try {
   if (!P) return fail(KV_ERR_INVALID_ARG, "kv_attend: null pool");
   if (!req_ids || !n_new || n_req < 1) return fail(KV_ERR_INVALID_ARG, "kv_attend: null pointer or n_req < 1");
   if ((k == nullptr) != (v == nullptr)) return fail(KV_ERR_INVALID_ARG, "kv_attend: k and v come together");
@@ -358,6 +359,8 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
     max_new = std::max(max_new, n_new[b]);
   }
   if (total == 0) return KV_OK;
+  if (total > kMaxRows / hq)
+    return fail(KV_ERR_INVALID_ARG, "kv_attend: more than %lld rows (tokens x num_q_heads)", (long long)kMaxRows);
   if (!q || !out) return fail(KV_ERR_INVALID_ARG, "kv_attend: null pointer");
   DeviceGuard dg(P->cfg.device);
   cudaStream_t s = (cudaStream_t)stream;
@@ -493,4 +496,6 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
   }
   KV_CUDA(merge(xl, pl, 128));
   return KV_OK;
+} catch (const std::bad_alloc&) {
+  return fail(KV_ERR_OOM, "kv_attend: host allocation failed");
 }

@@ -6,6 +6,7 @@
 namespace kvq {
 
 constexpr int kMaxNewTokens = 1 << 20;   // new tokens of one request in a call
+constexpr int64_t kMaxRows = int64_t(1) << 31;   // rows of q of a call (512 GB)
 
 // One (request of the call, kv head): T new tokens of g q heads each.  Row i
 // of a unit is (new token i / g, q head kvh * g + i % g).
@@ -84,8 +85,8 @@ cudaError_t launch_attend_few(kv_pool* P, int rows, const AttArgs& A, const AttU
 
 // Tensor-core kernels for many rows per unit (kvq_attend_wide.cu): the units' keys
 // as operand tiles (64 KB and four live words per 128 keys), then blocks of 256
-// rows over them.  Partials of 128 rows, two per item (rows 0..127 and 128..255;
-// for a block of at most 128 rows, the same rows over even and over odd tiles).
+// rows over them.  Partials of 128 rows, two per item (rows 0..127 and 128..255):
+// [channels / 4][row][4], then (m, l) [row].
 constexpr size_t kAttTileBytes = 65536;
 cudaError_t launch_attend_tiles(kv_pool* P, const AttArgs& A, const AttUnit* d_units, int n_units, int max_tiles,
                                 void* d_tiles, uint32_t* d_live, cudaStream_t s);

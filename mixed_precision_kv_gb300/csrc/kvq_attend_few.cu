@@ -13,15 +13,22 @@
 // again, 1000 cycles of its 128 bytes a cycle; TMEM has its own ports.
 //
 // A CTA takes an item: a block of R rows of one (request, kv head) unit and a run
-// of its tiles of 128 keys (four pages, or bf16 rows).  Roles (14 warps): one
-// warpgroup for the softmax (a key per thread), four warps for K (a page each),
-// four for V (32 channels each), one thread for the MMAs, one warp streaming
-// pages with bulk copies, seven tiles deep.  The running maximum of a row is kept
-// while no key exceeds it by more than 2^8 (P is binary16 with 2^7 of headroom);
-// otherwise the warpgroup takes the maxima of all columns and rescales O^T.
+// of its tiles of 128 keys (four pages, or bf16 rows).  Roles: eight warps for the
+// softmax (a key per thread, the rows in two halves), eight (R = 64: four) each for K
+// and V (a page, or 32 channels, each or in pairs), one to issue the MMAs of S^T and
+// one those of O^T, one that streams pages with bulk copies, six tiles deep.  The
+// running maximum of a row is kept while no key exceeds it by more than 2^8 (P is
+// binary16 with 2^7 of headroom); otherwise the warps take the maxima of all columns
+// and rescale O^T.  The sums of P come from the tensor cores (ones times P).
 //
-// What bounds it: unpacking, about 2 instructions per element (32768 per tile),
-// against 520 (INT2) to 870 (INT4) cycles that a tile's bytes take from HBM.
+// What bounds it: 3400 cycles per tile whatever R is, against 520 (INT2) to 870 (INT4)
+// that a tile's bytes take from HBM and about 600 (R = 64) of MMAs.  Unpacking takes
+// some 2500 warp instructions, the softmax 300 to 1200; the warps issue in a quarter
+// of the cycles and wait for instructions, shared memory and one another (two stages
+// of K and V, all that TMEM holds beside S and O).  24 requests with 1 to 7 new tokens
+// over 1K to 32K, 32 q on 8 kv heads: 283 us, 1.4 TB/s; a tree of 31 for 8 requests
+// over 32K: 381 us.  Both sides by the same sixteen warps in turn, so that one code
+// path is in use at a time, was slower (394 and 426 us).
 #include <algorithm>
 #include <atomic>
 

@@ -28,9 +28,13 @@
 // thread 600 of every 1650 cycles.  (Even and odd tiles of a last block of at most 128
 // rows given to the two warpgroups took 3350 cycles per tile, as they are 3700.)
 //
-// What bounds it: per tile and 256 rows the tensor cores need 2048 cycles, their
-// operand reads of shared memory 1536; the exponentials 1024; the CTA's shared
-// memory (Q and five tiles) leaves one CTA per SM.
+// What bounds it: 3700 cycles per tile of 256 rows, of which the tensor cores work
+// 2048 (their operand reads of shared memory 1536, the exponentials 1024): a half's
+// MMAs wait for its softmax (TMEM to registers, maximum, exponentials, back), about
+// 2700 cycles, and the other half's fill only part of that; S, P and O of both halves
+// are all of TMEM, and Q and five tiles all of shared memory.  An item costs 20,000
+// cycles more.  2048 tokens of 64 q on 8 kv heads over 32K: 1.77 ms, 1.28 PFLOP/s.
+// Slower: P V in two halves as P arrives (1.88 ms), 16 softmax warps (2.06 ms).
 #include <algorithm>
 #include <atomic>
 

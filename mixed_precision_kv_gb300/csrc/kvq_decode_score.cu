@@ -13,6 +13,7 @@
 // scan's own bound.
 #include <algorithm>
 #include <cmath>
+#include <new>
 
 #include "kvq_host.h"
 #include "kvq_scan_mma.cuh"
@@ -170,7 +171,7 @@ using namespace kvq;
 
 extern "C" kv_status_t kv_decode_attn_scored(kv_pool_t* P, const void* q, const int32_t* req_ids, int32_t batch,
                                              int32_t hq, float softmax_scale, float decay, float* scores,
-                                             int64_t score_stride, float* out, void* stream) {
+                                             int64_t score_stride, float* out, void* stream) try {
   if (!P) return fail(KV_ERR_INVALID_ARG, "kv_decode_attn_scored: null pool");
   if (!q || !out || !req_ids || !scores || batch < 1)
     return fail(KV_ERR_INVALID_ARG, "kv_decode_attn_scored: null pointer or batch < 1");
@@ -222,4 +223,6 @@ extern "C" kv_status_t kv_decode_attn_scored(kv_pool_t* P, const void* q, const 
   P->stat_hq = hq;
   P->stat_skip_dead = false;
   return KV_OK;
+} catch (const std::bad_alloc&) {
+  return fail(KV_ERR_OOM, "kv_decode_attn_scored: host allocation failed");
 }

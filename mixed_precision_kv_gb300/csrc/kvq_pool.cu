@@ -1015,6 +1015,10 @@ kv_status_t kv_append_quant(kv_pool_t* P, const void* k, const void* v, const in
     for (const auto& j : jobs) P->pos_dirty.push_back(j.page);
     for (const auto& j : repacks) P->pos_dirty.push_back(j.dst);
     for (const auto& j : directs) P->pos_dirty.push_back(j.dst);
+    if (P->pos_dirty.size() > 2 * P->fill.size() + 4096) {   // no reader for long: each page once
+      std::sort(P->pos_dirty.begin(), P->pos_dirty.end());
+      P->pos_dirty.erase(std::unique(P->pos_dirty.begin(), P->pos_dirty.end()), P->pos_dirty.end());
+    }
   }
   for (int32_t id : deferred) {
     P->fill[id] = 0;

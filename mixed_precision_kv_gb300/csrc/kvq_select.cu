@@ -13,6 +13,7 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <new>
 #include <vector>
 
 #include "kvq_host.h"
@@ -130,9 +131,9 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, u
 //   two words); keys; radix selection by digits of 11 bits, the CTAs' histograms
 //   added up through distributed shared memory; an ordered listing.
 // Bound by the scores' bytes for long rows, by a dozen barriers for short ones.
-// 16 x 100K positions, 8 heads summed: 380 us with one CTA per row reading its keys
-// once per digit, 36 us so.
-constexpr int kSelThreads = 512;            // two CTAs per SM: clusters of eight fit four SMs
+// 16 x 100K positions, 8 heads summed: 72 us; 380 with one CTA per row that reads its
+// keys once per digit.
+constexpr int kSelThreads = 512;            // (1024, and no limit of two CTAs per SM below: 64 rows of 20K to 32K 73 us, 38 so)
 constexpr int kSelStored = 48 * 1024;      // positions per CTA whose keys fit its shared memory
 constexpr int kSelMost = 3 * 512 * 1024;   // ... whose bits do
 constexpr int sel_smem(int per) { return (per <= kSelStored ? per * 4 : 0) + per / 8; }
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
       if (e[y].id < 0) continue;   // the same for the whole warp
-      const bool can = ((eligible_slots(e[y], hdead, hkv, h, per_head) >> lane) & 1u) && at[y] < r.limit;
+      const bool can = ((eligible_slots(e[y], hdead, hkv, h, per_head) >> lane) & 1u) && (uint32_t)at[y] < (uint32_t)r.limit;
       const int word = can ? at[y] >> 5 : -1;
       const uint32_t peers = __match_any_sync(0xFFFFFFFFu, word);
       if (can) {
@@ -315,14 +316,14 @@ kv_status_t refuse_capture(const char* what, cudaStream_t s) {
 kv_status_t sync_positions(kv_pool* P, cudaStream_t s) {
   std::vector<int32_t>& ids = P->pos_dirty;
   if (!P->d_pos) {
+    ids.clear();
+    for (const Request& R : P->reqs) ids.insert(ids.end(), R.table.begin(), R.table.end());
     const size_t n = P->fill.size() * (size_t)kPage;
     if (cudaMalloc(&P->d_pos, n * sizeof(int32_t)) != cudaSuccess) {
       cudaGetLastError();
       P->d_pos = nullptr;
       return fail(KV_ERR_OOM, "cannot allocate the positions of %zu slots", n);
     }
-    ids.clear();
-    for (const Request& R : P->reqs) ids.insert(ids.end(), R.table.begin(), R.table.end());
   }
   if (ids.empty()) return KV_OK;
   std::sort(ids.begin(), ids.end());
@@ -353,7 +354,7 @@ using namespace kvq;
 
 extern "C" kv_status_t kv_select_lowest(kv_pool_t* P, const float* scores, int64_t score_stride, const int32_t* req_ids,
                                         const int32_t* n_select, int32_t n_req, int64_t protect, int32_t per_head,
-                                        int32_t* out, int64_t out_stride, void* stream) {
+                                        int32_t* out, int64_t out_stride, void* stream) try {
   if (!P) return fail(KV_ERR_INVALID_ARG, "kv_select_lowest: null pool");
   if (!scores || !req_ids || !n_select || n_req < 1 || protect < 0 || out_stride < 0 || (out_stride > 0 && !out))
     return fail(KV_ERR_INVALID_ARG, "kv_select_lowest: bad arguments");
@@ -426,4 +427,6 @@ extern "C" kv_status_t kv_select_lowest(kv_pool_t* P, const float* scores, int64
                              (const uint32_t*)(hd ? P->d_hdead : nullptr), (const int32_t*)P->d_pos, hkv,
                              (int)(per_head ? 1 : 0), scores, score_stride, per, out, out_stride));
   return KV_OK;
+} catch (const std::bad_alloc&) {
+  return fail(KV_ERR_OOM, "kv_select_lowest: host allocation failed");
 }

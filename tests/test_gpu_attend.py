@@ -408,3 +408,23 @@ def test_expired_wait_reports_timeout_once(kvq, n_new):
     again = P.pool.attend(q, P.ids, n_new, SCALE, k, v)
     P.pool.sync()
     assert torch.equal(again, good)
+
+
+def test_more_keys_than_a_pass(kvq):
+    """Operand tiles past one pass's workspace (65536 tiles of 128 keys, 4.3 GB): the same request nine
+    times, so that every copy of a row has one answer, and the answer of a call that lists it once."""
+    n, T, hkv, hq = 131072, 49, 8, 64
+    pages = 2 * (n // 32 + 64)
+    pool = kvq.KVPool(hkv, pages, pages, 1, n // 32 + 64)
+    rid = pool.open()
+    gen = torch.Generator("cuda").manual_seed(23)
+    for a in range(0, n, 16384):
+        pool.append(rand((16384, hkv, 128), gen), rand((16384, hkv, 128), gen), np.full(16384, rid, np.int32),
+                    np.full(16384, 2, np.uint8))
+    q, k, v = (rand((T, h, 128), gen) for h in (hq, hkv, hkv))
+    one = pool.attend(q, [rid], [T], SCALE, k, v).double()
+    many = pool.attend(q.repeat(9, 1, 1), [rid] * 9, [T] * 9, SCALE, k.repeat(9, 1, 1), v.repeat(9, 1, 1)).double()
+    pool.sync()
+    # both are rounded to bf16 (2^-8 each at most) from sums taken in other pieces (far below)
+    for x in many.view(9, T, hq, 128):
+        assert float((x - one).norm() / one.norm()) <= 2 * 2.0 ** -8
