@@ -21,14 +21,14 @@
 // binary16 with 2^7 of headroom); otherwise the warps take the maxima of all columns
 // and rescale O^T.  The sums of P come from the tensor cores (ones times P).
 //
-// What bounds it: 3400 cycles per tile whatever R is, against 520 (INT2) to 870 (INT4)
-// that a tile's bytes take from HBM and about 600 (R = 64) of MMAs.  Unpacking takes
-// some 2500 warp instructions, the softmax 300 to 1200; the warps issue in a quarter
-// of the cycles and wait for instructions, shared memory and one another (two stages
-// of K and V, all that TMEM holds beside S and O).  24 requests with 1 to 7 new tokens
-// over 1K to 32K, 32 q on 8 kv heads: 283 us, 1.4 TB/s; a tree of 31 for 8 requests
-// over 32K: 381 us.  Both sides by the same sixteen warps in turn, so that one code
-// path is in use at a time, was slower (394 and 426 us).
+// What bounds it: the instructions of unpacking and softmax and their waits.  A tile
+// takes 2750 (R = 32) to 3300 cycles (R = 64): about 7000 warp instructions, in 67 and
+// 52 % of the issue slots, against 520 (INT2) to 870 cycles (INT4) that its bytes take
+// from HBM and 600 of MMAs at R = 64; two stages of K and V are all that TMEM holds
+// beside S and O.  24 requests with 1 to 7 new tokens over 1K to 32K, 32 q on 8 kv
+// heads: 283 us, 1.4 TB/s; a tree of 31 for 8 requests over 32K: 381 us.  Slower: K
+// and V by the same sixteen warps in turn, one code path at a time (drafts + 10 %);
+// softmax warps that skip a half without rows (+ 4 %).
 #include <algorithm>
 #include <atomic>
 
