@@ -27,7 +27,7 @@ namespace cg = cooperative_groups;
 struct PosRow {
   int32_t pos[kPage];
 };
-constexpr size_t kPosChunk = 1 << 16;   // page rows per upload
+constexpr size_t kPosChunk = 1 << 11;   // page rows per upload: one copy runs while the next is gathered
 
 __global__ void pos_scatter_kernel(const int32_t* __restrict__ ids, const PosRow* __restrict__ rows, int n,
                                    int32_t* __restrict__ d_pos) {
@@ -315,7 +315,8 @@ kv_status_t refuse_capture(const char* what, cudaStream_t s) {
 
 kv_status_t sync_positions(kv_pool* P, cudaStream_t s) {
   std::vector<int32_t>& ids = P->pos_dirty;
-  if (!P->d_pos) {
+  const bool first = !P->d_pos;
+  if (first) {
     ids.clear();
     for (const Request& R : P->reqs) ids.insert(ids.end(), R.table.begin(), R.table.end());
     const size_t n = P->fill.size() * (size_t)kPage;
@@ -326,8 +327,10 @@ kv_status_t sync_positions(kv_pool* P, cudaStream_t s) {
     }
   }
   if (ids.empty()) return KV_OK;
-  std::sort(ids.begin(), ids.end());
-  ids.erase(std::unique(ids.begin(), ids.end()), ids.end());
+  if (!first) {   // (a page is in one table, once)
+    std::sort(ids.begin(), ids.end());
+    ids.erase(std::unique(ids.begin(), ids.end()), ids.end());
+  }
   std::vector<PosRow> rows;
   for (size_t a = 0; a < ids.size(); a += kPosChunk) {
     const size_t n = std::min(kPosChunk, ids.size() - a);
