@@ -460,8 +460,8 @@ class KVPool:
         return pos
 
     def set_wait_limit(self, first_wait_spins):
-        """kv_set_wait_limit: bound of the scans' first copy wait (testing the timeout
-        path); -1 restores the normal bound."""
+        """kv_set_wait_limit: bound of the scans' and attend's first copy wait (testing the
+        timeout path); -1 restores the normal bound."""
         _check(load_library().kv_set_wait_limit(self._h, int(first_wait_spins)), "kv_set_wait_limit")
 
     def set_decode_impl(self, impl):
