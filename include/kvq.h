@@ -352,14 +352,14 @@ KVQ_API kv_status_t kv_select_lowest(kv_pool_t* pool, const float* scores, int64
 /* Testing aid for the device-timeout path (off by default).  Every copy wait
  * in the scans and every wait in kv_attend is bounded; first_wait_spins >= 0
  * makes the first copy wait of every warp of the tensor-core page scan and of
- * the full-precision list scan, and the first wait for cached keys in kv_attend,
- * give up after that many polls (0: at once) instead of the normal bound;
- * -1 restores the normal bound.  A warp whose wait gives up records
+ * the full-precision list scan, and the first wait for cached keys in
+ * kv_attend, give up after that many polls (0: at once) instead of the normal
+ * bound; -1 restores the normal bound.  A warp whose wait gives up records
  * KV_ERR_DEVICE_TIMEOUT in the pool's status, still waits (with the normal
  * bound) for every copy it issued, writes empty partials and exits, so the
  * device stays usable: kv_pool_sync() then returns KV_ERR_DEVICE_TIMEOUT once
- * and the call's output (scored decode: and its scores) is unspecified.  Values outside [-1, 2^32) are
- * KV_ERR_INVALID_ARG. */
+ * and the call's output (scored decode: and its scores) is unspecified.
+ * Values outside [-1, 2^32) are KV_ERR_INVALID_ARG. */
 KVQ_API kv_status_t kv_set_wait_limit(kv_pool_t* pool, int64_t first_wait_spins);
 
 /* Choose the decode implementation (kv_decode_impl_t). */
