@@ -180,13 +180,14 @@ int block_tiles(const AttUnit& u, int g, int row0, int rows, bool kv, bool tree)
 }
 
 // Blocks of kWideRows rows of units [u0, u1).  An item costs its tiles (3700 cycles
-// each) and kWideItem more (20,000 for its rows, the first and last steps).  Whole blocks go to the least loaded CTA while they fit into an
-// equal share, units with the most tiles first; the blocks that are left are cut to
-// fill up the shares, and their pieces merged.  So most items are whole blocks, and
-// the blocks of a unit, which start together, read each tile at about the same time:
-// it comes from L2 once it has been read.  (One line of blocks cut into equal runs
-// took 1006 us for four chunks of 300 to 512 tokens over 15K to 32K, 850 us with
-// every tile in L2.)  by_cta[c] gets the items of CTA c.
+// each) and kWideItem more (20,000 for its rows, the first and last steps).  Whole
+// blocks, those with the most tiles first, go to the least loaded CTA while they fit
+// into an equal share; the blocks that are left are cut to fill up the shares, and
+// their pieces merged.  So most items are whole blocks, and the blocks of a unit, which
+// start together, read each tile at about the same time: it comes from L2 once it has
+// been read.  (One line of blocks cut into equal runs took 1006 us for four chunks of
+// 300 to 512 tokens over 15K to 32K, 850 us with every tile in L2; 761 us so.)
+// by_cta[c] gets the items of CTA c.
 constexpr int kWideRows = 256;
 constexpr double kWideItem = 5.4;
 void plan_wide(const std::vector<AttUnit>& units, int u0, int u1, int g, bool kv, bool tree, int ctas,
@@ -194,13 +195,9 @@ void plan_wide(const std::vector<AttUnit>& units, int u0, int u1, int g, bool kv
   struct Block {
     int unit, row0, rows, tiles;
   };
-  std::vector<int> order;
   std::vector<Block> blocks, rest;
   double total = kWideItem * ctas;   // about one cut per CTA
-  for (int x = u0; x < u1; ++x) order.push_back(x);
-  auto tiles_of = [&](int x) { return block_tiles(units[(size_t)x], g, 0, units[(size_t)x].T * g, kv, tree); };
-  std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return tiles_of(a) > tiles_of(b); });
-  for (int x : order) {
+  for (int x = u0; x < u1; ++x) {
     const int rows = units[(size_t)x].T * g;
     for (int r = 0; r < rows; r += kWideRows) {
       const int n = std::min(kWideRows, rows - r);
@@ -209,6 +206,7 @@ void plan_wide(const std::vector<AttUnit>& units, int u0, int u1, int g, bool kv
       total += b.tiles + kWideItem;
     }
   }
+  std::stable_sort(blocks.begin(), blocks.end(), [](const Block& a, const Block& b) { return a.tiles > b.tiles; });
   const double share = total / ctas;
   std::vector<double> load((size_t)ctas, 0.0);
   std::vector<std::pair<int, size_t>> pieces;   // (CTA, index) of a block's items
