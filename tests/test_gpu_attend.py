@@ -428,3 +428,37 @@ def test_more_keys_than_a_pass(kvq):
     # both are rounded to bf16 (2^-8 each at most) from sums taken in other pieces (far below)
     for x in many.view(9, T, hq, 128):
         assert float((x - one).norm() / one.norm()) <= 2 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("impl", IMPLS)
+@pytest.mark.parametrize("size", [1e20, 1e-20])
+def test_queries_far_from_one(kvq, impl, size):
+    P = Pool(kvq, 1, [mixed(200, 2)], seed=24)
+    check(P, impl, [0], [5], 8, scale=SCALE / size, q_mult=size)
+    check(P, impl, [0], [100], 8, scale=SCALE / size, q_mult=size, rows=[0, 60, 99])
+
+
+@pytest.mark.parametrize("n_new", [[3, 2], [70, 50]])
+def test_two_pools_from_two_threads(kvq, n_new):
+    """Calls on two pools at once, each on its own stream: what one call alone gives."""
+    import threading
+    pools = [Pool(kvq, 2, [mixed(700, s), mixed(90, s + 1)], seed=s) for s in (31, 33)]
+    q, k, v = (rand((sum(n_new), h, 128), pools[0].gen) for h in (8, 2, 2))
+    alone = [P.pool.attend(q, P.ids, n_new, SCALE, k, v) for P in pools]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(P, want):
+        s = torch.cuda.Stream()
+        out = torch.empty_like(want)
+        for _ in range(20):
+            P.pool.attend(q, P.ids, n_new, SCALE, k, v, out=out, stream=s)
+        s.synchronize()
+        P.pool.sync()
+        if not torch.equal(out, want):
+            wrong.append(P)
+
+    t = [threading.Thread(target=work, args=x) for x in zip(pools, alone)]
+    [x.start() for x in t]
+    [x.join() for x in t]
+    assert not wrong
