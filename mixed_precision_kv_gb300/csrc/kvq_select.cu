@@ -124,6 +124,14 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, u
   return before + x;
 }
 
+// *p |= v in CTA `rank` of the cluster, without waiting for the old value (a call alone
+// on 16 rows of 100K: 83.5 us, 87.7 with an atomicOr through the mapped pointer).
+__device__ __forceinline__ void or_in_cluster(uint32_t* p, uint32_t rank, uint32_t v) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
 // A cluster of CTAs per row; CTA c holds the keys of positions [c per, (c + 1) per)
 // in shared memory, so the scores are read once and the rest stays on the SMs:
 //   the table's pages, a share per CTA, set the eligible positions' bits where they
@@ -131,8 +139,8 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, u
 //   two words); keys; radix selection by digits of 11 bits, the CTAs' histograms
 //   added up through distributed shared memory; an ordered listing.
 // Bound by the scores' bytes for long rows, by a dozen barriers for short ones.
-// 16 x 100K positions, 8 heads summed: 72 us; 380 with one CTA per row that reads its
-// keys once per digit.
+// 16 x 100K positions, 8 heads summed: 68 us, of which the eligible positions and the
+// keys take a third each; 380 with one CTA per row that reads its keys once per digit.
 constexpr int kSelThreads = 512;            // (1024, and no limit of two CTAs per SM below: 64 rows of 20K to 32K 73 us, 38 so)
 constexpr int kSelStored = 48 * 1024;      // positions per CTA whose keys fit its shared memory
 constexpr int kSelMost = 3 * 512 * 1024;   // ... whose bits do
@@ -168,25 +176,42 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(
   for (int x = tid; x < 3 * kBins; x += kSelThreads) (&S.hist[0][0])[x] = 0u;
   if (tid == 0) S.below = S.ties = 0u;
   cl.sync();
-  // ---- eligible positions, four pages of a warp in flight
+  // ---- eligible positions: a warp takes up to 32 pages, their entries at once, their positions by eights
   const Entry* tab = table + (size_t)r.req * max_pages;
   constexpr int kWarps = kSelThreads / 32;
-  for (int p0 = (rank * kWarps + w) * 4; p0 < n_pages; p0 += n_cta * kWarps * 4) {
-    Entry e[4];
-    int32_t at[4];
+  const float inv_words = 1.0f / (float)words;
+  const int warps = n_cta * kWarps, share = min(32, max(1, (n_pages + warps - 1) / warps));
+  for (int p0 = (rank * kWarps + w) * share; p0 < n_pages; p0 += warps * share) {
+    const int n = min(share, n_pages - p0);
+    Entry e{-1, 0u};
+    uint32_t can = 0u;
+    if (lane < n) {
+      e = tab[p0 + lane];
+      if (e.id >= 0) can = eligible_slots(e, hdead, hkv, h, per_head);
+    }
+    for (int y0 = 0; y0 < n; y0 += 8) {
+      uint32_t m[8];
+      int32_t at[8];
 #pragma unroll
-    for (int y = 0; y < 4; ++y) e[y] = p0 + y < n_pages ? tab[p0 + y] : Entry{-1, 0u};
+      for (int y = 0; y < 8; ++y) {   // y0 + y <= 31; lanes from n on have no slots
+        m[y] = __shfl_sync(0xFFFFFFFFu, can, y0 + y);
+        const int32_t id = __shfl_sync(0xFFFFFFFFu, e.id, y0 + y);
+        at[y] = m[y] ? pos[(size_t)id * kPage + lane] : 0;
+      }
 #pragma unroll
-    for (int y = 0; y < 4; ++y) at[y] = e[y].id >= 0 ? pos[(size_t)e[y].id * kPage + lane] : 0;
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      if (e[y].id < 0) continue;   // the same for the whole warp
-      const bool can = ((eligible_slots(e[y], hdead, hkv, h, per_head) >> lane) & 1u) && (uint32_t)at[y] < (uint32_t)r.limit;
-      const int word = can ? at[y] >> 5 : -1;
-      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, word);
-      if (can) {
-        const uint32_t m = __reduce_or_sync(peers, 1u << (at[y] & 31));
-        if (lane == __ffs(peers) - 1) atomicOr(cl.map_shared_rank(bits, word / words) + word % words, m);
+      for (int y = 0; y < 8; ++y) {
+        if (m[y] == 0u) continue;   // the same for the whole warp
+        const bool take = ((m[y] >> lane) & 1u) && (uint32_t)at[y] < (uint32_t)r.limit;
+        const int word = take ? at[y] >> 5 : -1;
+        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, word);
+        if (take) {
+          const uint32_t set = __reduce_or_sync(peers, 1u << (at[y] & 31));
+          if (lane == __ffs(peers) - 1) {
+            // word / words: exact, as (word + 1/2) / words is at least 1 / (2 words) > 8 2^-22 from an integer
+            const int cta = (int)(((float)word + 0.5f) * inv_words);
+            or_in_cluster(bits + (word - cta * words), (uint32_t)cta, set);
+          }
+        }
       }
     }
   }
@@ -210,16 +235,25 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(
     const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0);
     const uint32_t mask = d == 2 ? 1023u : 2047u;
     const uint32_t high = d == 0 ? 0u : (d == 1 ? 0xFFE00000u : 0xFFFFFC00u);   // the bits settled so far
-    for (int x = tid; x < ((mine + 31) & ~31); x += kSelThreads) {
-      const uint32_t k = x < mine ? key(x) : 0xFFFFFFFFu;
-      const bool in = k != 0xFFFFFFFFu && ((k ^ prefix) & high) == 0u;
-      const uint32_t b = in ? (k >> shift) & mask : 0xFFFFFFFFu;
-      int same;
-      __match_all_sync(0xFFFFFFFFu, b, &same);   // scores crowd into few digits, often into one
-      if (same) {
-        if (in && lane == 0) atomicAdd(&S.hist[d][b], 32u);
-      } else if (in) {
-        atomicAdd(&S.hist[d][b], 1u);
+    for (int y = tid; y < ((mine + 127) >> 7) << 5; y += kSelThreads) {   // whole warps, four positions a thread
+      uint32_t b[4];
+      if constexpr (kStored) {
+        const uint4 k = 4 * y < per ? reinterpret_cast<const uint4*>(keys)[y] : make_uint4(0u, 0u, 0u, 0u);
+        b[0] = k.x; b[1] = k.y; b[2] = k.z; b[3] = k.w;
+      }
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const int x = 4 * y + z;
+        const uint32_t k = x >= mine ? 0xFFFFFFFFu : (kStored ? b[z] : fresh(x));
+        b[z] = k != 0xFFFFFFFFu && ((k ^ prefix) & high) == 0u ? (k >> shift) & mask : 0xFFFFFFFFu;
+      }
+      const uint32_t f = __shfl_sync(0xFFFFFFFFu, b[0], 0);
+      if (__all_sync(0xFFFFFFFFu, b[0] == f && b[1] == f && b[2] == f && b[3] == f)) {   // scores crowd into few digits
+        if (f != 0xFFFFFFFFu && lane == 0) atomicAdd(&S.hist[d][f], 128u);
+      } else {
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          if (b[z] != 0xFFFFFFFFu) atomicAdd(&S.hist[d][b[z]], 1u);
       }
     }
     if (tid == 0) S.digit = 0xFFFFFFFFu;
