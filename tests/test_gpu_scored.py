@@ -247,3 +247,24 @@ def test_refusals(kvq):
     with pytest.raises(ValueError):
         pool.evict_lowest(sc.expand(2, 2, 64).contiguous(), [r, r], 1)
     assert pool.select_lowest(sc, [r], 0).shape == (1, 0)
+
+
+@pytest.mark.parametrize("rows,n", [(160, 40000), (1, 40000), (3, 110000)])
+def test_select_long_and_many(kvq, rows, n):
+    """One CTA per row with more pages than its warps hold at once, and clusters; a request listed
+    as often as there are rows, every third token evicted in a stretch."""
+    pool = kvq.KVPool(1, n // 32 + 16, n // 32 + 16, 1, n // 32 + 32)
+    rid = pool.open()
+    gen = torch.Generator("cuda").manual_seed(n + rows)
+    w = mixed(n, 3)
+    for a in range(0, n, 10000):
+        pool.append(rand((10000, 1, 128), gen), rand((10000, 1, 128), gen), np.full(10000, rid, np.int32), w[a:a + 10000])
+    dead = np.arange(5000, 20000, 3)
+    pool.evict(np.full(dead.size, rid, np.int32), dead)
+    x = torch.rand(rows, 1, n + 5, device="cuda", generator=gen)
+    x = torch.where(x < 0.3, torch.zeros_like(x), x)   # many ties
+    got = pool.select_lowest(x, [rid] * rows, 17000, protect=100).cpu().numpy()
+    pool.sync()
+    live = np.setdiff1d(np.arange(n - 100), dead)
+    for b, key in enumerate(x[:, 0].cpu().numpy()):
+        assert np.array_equal(got[b], np.sort(live[np.argsort(key[live], kind="stable")[:17000]])), b
