@@ -39,6 +39,10 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_add_kernel(
     const uint32_t* __restrict__ hdead, const int32_t* __restrict__ pos, int hkv, float decay,
     float* __restrict__ scores, int64_t stride) {
   const Unit u = units[blockIdx.y];
+  // A unit without page splits had an empty table when it was planned, and still has one (a table that gains
+  // its first page is planned again).  ntab and table are written by appends only: under a request id that
+  // was closed and opened again they hold the earlier request's until then.
+  if (u.n_splits == 0) return;
   const int lane = threadIdx.x & 31;
   const int n = ntab[u.req];
   const int p0 = (blockIdx.x * kScoreWarps + (threadIdx.x >> 5)) * kScorePages;

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   uint32_t* bits = keys + (kStored ? per : 0);
   const int words = per >> 5;
-  const int n_pages = ntab[r.req];
+  const int n_pages = r.limit > 0 ? ntab[r.req] : 0;   // (a request that was never appended to has no length there)
   for (int x = tid; x < words; x += kSelThreads) bits[x] = 0u;
   for (int x = tid; x < 3 * kBins; x += kSelThreads) (&S.hist[0][0])[x] = 0u;
   if (tid == 0) S.below = S.ties = 0u;
