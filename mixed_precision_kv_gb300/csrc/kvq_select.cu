@@ -70,10 +70,20 @@ __device__ __forceinline__ uint32_t eligible_slots(const Entry& e, const uint32_
   }
   return live;
 }
-// Key of a position: the head's score, or the heads' sum as if taken in 64 bits and
-// rounded once.  fp64 runs at 1/64 of the fp32 rate here, so the sum is carried as an
-// unevaluated pair of fp32 (48 bits); a sum that overflows on the way, or is not
-// finite, takes the fp64 path.
+// Key of a position: the head's score, or the heads' sum taken in fp64, head after head,
+// and rounded once.  fp64 runs at 1/64 of the fp32 rate here, so the sum is carried as an
+// unevaluated pair of fp32 first:
+//   hi + f = t + e exactly (e: the two-sum's error), hi <- t, lo <- fl(lo + e).
+// With u = 2^-24, n heads and m >= sum |f|, every |e| <= u m, so |lo| <= n u m.
+//   - Every f is a multiple of q = ulp(least |f| above 0) > u least |f|.  Where n u m <= least
+//     |f|, lo and the fp64 sums are multiples of q below 2^24 q and 2^53 q: both sums are
+//     exact, and hi + lo rounds once.  So it is for scores of one scale (0 of 10^6 sums of 2
+//     to 16 lognormal scores, of sigma 2, fail this).
+//   - Else lo's n roundings add up to n^2 u^2 m at most, and the fp64 sum is within n 2^-53 m of
+//     the exact one, so it lies within 2^-47 n^2 m of hi + lo; where both ends of that range
+//     round to the same fp32, so does it.
+//   - Else (next to the middle of two fp32 values, where terms cancel, or not finite) it is
+//     taken again in fp64.
 __device__ __noinline__ float sum_wide(const float* sc, int64_t stride, int hkv, int x) {
   double sum = 0.0;
   for (int y = 0; y < hkv; ++y) sum += (double)__ldg(sc + (size_t)y * stride + x);
@@ -81,11 +91,14 @@ __device__ __noinline__ float sum_wide(const float* sc, int64_t stride, int hkv,
 }
 __device__ __forceinline__ uint32_t key_of(const float* sc, int64_t stride, int hkv, int h, bool per_head, int x) {
   if (per_head) return order_key(__ldg(sc + (size_t)h * stride + x));
-  float hi = 0.0f, lo = 0.0f;
+  float hi = 0.0f, lo = 0.0f, m = 0.0f;
+  uint32_t least = 0xFFFFFFFFu;   // 2 |f|'s bits - 1: a zero is no least
   auto add = [&](float f) {
-    const float t = __fadd_rn(hi, f), b = __fsub_rn(t, hi);   // hi + f = t + e exactly
+    const float t = __fadd_rn(hi, f), b = __fsub_rn(t, hi);
     lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(f, b)));
     hi = t;
+    m = __fadd_ru(m, fabsf(f));
+    least = min(least, (__float_as_uint(f) << 1) - 1u);
   };
   const float* p = sc + x;
   int y = 0;
@@ -98,8 +111,14 @@ __device__ __forceinline__ uint32_t key_of(const float* sc, int64_t stride, int 
   }
   for (; y < hkv; ++y, p += stride) add(__ldg(p));
   const float sum = __fadd_rn(hi, lo);
-  // an overflow on the way leaves an infinity or a NaN behind
-  return order_key(fabsf(sum) < INFINITY ? sum : sum_wide(sc, stride, hkv, x));
+  bool sure = __fmul_ru(m, (float)hkv * 0x1p-24f) <= __uint_as_float((least + 1u) >> 1);
+  if (!sure) {
+    const float b = __fsub_rn(sum, hi), rest = __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, b)), __fsub_rn(lo, b));   // hi + lo = sum + rest
+    const float most = __fmul_ru(m, (float)(hkv * hkv) * 0x1p-47f);
+    sure = __fadd_rn(sum, __fadd_ru(rest, most)) == sum && __fadd_rn(sum, __fadd_rd(rest, -most)) == sum;
+  }
+  sure = sure && fabsf(sum) < INFINITY;   // an overflow on the way leaves an infinity or a NaN behind
+  return order_key(sure ? sum : sum_wide(sc, stride, hkv, x));
 }
 // Inclusive sum over the block's 512 threads; `total` is the whole sum.
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, uint32_t& total) {

@@ -45,3 +45,56 @@ def test_a_request_id_used_again_without_pages(kvq, lists, first):
     P.widths[r] = list(map(int, w))
     step(P, 8, scores, 1.0, fp=fp)
     check_select(P, scores, 30, 3, False)
+
+
+def summed_keys(scores):
+    """The kv heads' sum in fp64, head after head, rounded to fp32; [H][positions]."""
+    s = np.zeros(scores.shape[1])
+    for row in scores.astype(np.float64):
+        s = s + row
+    return s.astype(np.float32)
+
+
+def hard_sums(hkv, n, seed, signs):
+    """Scores of many magnitudes, sums at and next to the middle of two fp32 values, cancellation."""
+    rng = np.random.default_rng(seed)
+    x = np.ldexp(rng.uniform(1, 2, (hkv, n)), rng.integers(-60, 1, (hkv, n)))
+    x[:, n // 4:n // 2] = np.ldexp(1.0, rng.integers(-55, 1, (hkv, n // 2 - n // 4)))          # powers of two
+    x[:, n // 2:3 * n // 4] = rng.integers(0, 5, (hkv, 3 * n // 4 - n // 2)) / 8.0                # ties and zeros
+    # one, half a unit of it, and something far below that decides (or not, where it is zero)
+    near = np.arange(3 * n // 4, n)
+    x[:, near] = 0.0
+    x[0, near] = rng.integers(1, 4, near.size)
+    x[1, near] = np.ldexp(x[0, near], -24) * rng.integers(0, 3, near.size)
+    if hkv > 2:
+        x[2, near] = np.ldexp(rng.integers(-1 if signs else 0, 2, near.size).astype(np.float64), rng.integers(-52, -40, near.size))
+    if signs:
+        x[:, :near[0]] *= rng.choice([-1.0, 1.0], (hkv, near[0]))
+    for col in x.T:
+        rng.shuffle(col)
+    return x.astype(np.float32)
+
+
+@pytest.mark.parametrize("signs", [False, True])
+@pytest.mark.parametrize("hkv", [2, 3, 7, 8, 9, 17])
+def test_selection_by_the_sum_of_many_heads(kvq, hkv, signs):
+    n = 4000
+    P = Pool(kvq, hkv, [mixed(n, 1)], seed=hkv, chunk=1000, slack=256)
+    sc = hard_sums(hkv, n, 10 * hkv + signs, signs)
+    key = summed_keys(sc)
+    x = torch.from_numpy(sc[None].copy()).cuda()
+    order = np.argsort(key + np.float32(0), kind="stable")
+    for m in list(range(1, 60)) + [100, 500, 999, 1000, 1001, 1777, 2000, 2500, 3000, 3100, 3500, 3999]:
+        got = P.pool.select_lowest(x, P.ids, m).cpu().numpy()[0]
+        assert np.array_equal(got, np.sort(order[:m])), m
+
+
+def test_selection_where_the_third_head_decides(kvq):
+    """1 + 2^-24 + 2^-50 rounds up, 1 + 2^-24 does not."""
+    P = Pool(kvq, 3, [mixed(40, 1)], seed=1)
+    x = torch.full((1, 3, 40), 2.0, device="cuda")
+    x[0, :, 0] = torch.tensor([1.0, 2.0 ** -24, 2.0 ** -50])
+    x[0, :, 1] = torch.tensor([1.0, 0.0, 0.0])
+    x[0, :, 2] = torch.tensor([1.0, 2.0 ** -24, 0.0])
+    assert P.pool.select_lowest(x, P.ids, 1).cpu().tolist() == [[1]]
+    assert P.pool.select_lowest(x, P.ids, 2).cpu().tolist() == [[1, 2]]
