@@ -92,7 +92,11 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttArgs A, const AttUn
         const float4 qv = *reinterpret_cast<const float4*>(&qr[c]);
         s = fmaf(qv.x, kv.x, s); s = fmaf(qv.y, kv.y, s); s = fmaf(qv.z, kv.z, s); s = fmaf(qv.w, kv.w, s);
       }
-      s = may(y) ? s * A.scale_log2 : -INFINITY;
+      s *= A.scale_log2;
+      const bool see = may(y), odd = see && !(fabsf(s) < INFINITY);
+      // a logit that is not finite makes the row's sum, and so the row, not a number
+      if (__any_sync(0xFFFFFFFFu, odd)) l[y] = __int_as_float(0x7FFFFFFF);
+      s = see && !odd ? s : -INFINITY;
       float mx = s;
 #pragma unroll
       for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
@@ -165,6 +169,7 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttArgs A, const AttUn
       return A.tree ? ((A.tree[u.tok0 + t] >> j) & 1ull) != 0ull : j <= t;
     });
   }
+  bool bad = false;
 #pragma unroll
   for (int y = 0; y < kPer; ++y) {
     const int i = r0 + kPer * w + y;
@@ -172,8 +177,13 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttArgs A, const AttUn
     const float inv = l[y] > 0.0f ? 1.0f / l[y] : (l[y] == 0.0f ? 0.0f : l[y]);   // a NaN sum stays NaN
     uint16_t* op = A.out + row_at(i) + 4 * lane;
 #pragma unroll
-    for (int a = 0; a < 4; ++a) op[a] = __bfloat16_as_ushort(__float2bfloat16_rn(o[y][a] * inv));
+    for (int a = 0; a < 4; ++a) {
+      const float v = o[y][a] * inv;
+      if (!(fabsf(v) < INFINITY)) bad = true;
+      op[a] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    }
   }
+  if (bad) atomicOr(A.status, kStatusRange);
 }
 
 }  // namespace
