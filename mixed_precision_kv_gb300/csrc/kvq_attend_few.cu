@@ -50,6 +50,7 @@ constexpr int kMaskRing = 16;                   // tiles whose live words are ke
 constexpr float kHead = 7.0f;                   // P = 2^(x - m + 7)
 constexpr float kGrow = 8.0f;                   // a maximum may be stale by this much (base 2)
 constexpr float kNever = -3.0e38f;              // S of a key that is not seen
+constexpr float kLowest = 0.9f * kNever;        // logits below it count as it
 constexpr float kUnseen = -1.0e30f;             // kHead - m of a row that has seen nothing: its weights are 0
 // TMEM columns (two stages of K, V and S; kColOne: the ones of the sums, for R <= 32)
 constexpr uint32_t kColK = 0, kColV = 128, kColS = 256, kColO = 384, kColL = 448, kColOne = 480;
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kThreads<R>, 1) attend_few_kernel(
 #pragma unroll
         for (int o = kPer / 2; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
         const int e = q_exponent(mx);
-        const float mul = copysignf(pow2f(e), A.scale_log2);
+        const float mul = q_factor(mx, e, A.scale_log2);
 #pragma unroll
         for (int y = 0; y < kRuns; ++y) {
           const int run = sub + kPer * y, gr = run >> 2, i = run & 3;
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kThreads<R>, 1) attend_few_kernel(
 #pragma unroll
           for (int n = 0; n < kC; ++n) {
             const float v = __uint_as_float(s[n]);
-            const float w = warp_max_f(v == kNever ? kNever : fmaxf(v * S.rf[c0 + n], 0.9f * kNever));
+            const float w = warp_max_f(v == kNever ? kNever : fmaxf(v * S.rf[c0 + n], kLowest));
             if (lane == n) keep = w;
           }
           if (lane < kC) S.wmax[wq][c0 + lane] = keep;
@@ -341,7 +342,9 @@ __global__ void __launch_bounds__(kThreads<R>, 1) attend_few_kernel(
             const float mo = S.m[tid], mn = w > 0.95f * kNever ? fmaxf(mo, w) : mo;
             S.m[tid] = mn;
             S.fac[tid] = mo == -INFINITY ? 1.0f : ex2f(mo - mn);
-            S.nm[tid] = mn == -INFINITY ? kUnseen : kHead - mn;
+            // a logit above fp32's range, or all below it so far: the row's weights are not a number
+            const bool past = mn == INFINITY || mn == kLowest;
+            S.nm[tid] = mn == -INFINITY ? kUnseen : (past ? __int_as_float(0x7FFFFFFF) : kHead - mn);
             if (mn == -INFINITY && tid < T.rows) S.unseen = 1u;
           }
           group_stop(false);

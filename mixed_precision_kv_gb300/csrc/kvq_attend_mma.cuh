@@ -388,6 +388,12 @@ __device__ __forceinline__ int q_exponent(float mx) {
   return mx > 0.0f && mx < INFINITY ? max(-100, min(100, 134 - (int)(__float_as_uint(mx) >> 23))) : 0;
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// The factor of a row of q: 2^e with the scale's sign.  A row with an infinity (mx; a NaN is
+// none) becomes NaN throughout: its logits of keys of one sign could all be -inf otherwise,
+// and a row without weight is 0.
+__device__ __forceinline__ float q_factor(float mx, int e, float scale) {
+  return mx < INFINITY ? copysignf(pow2f(e), scale) : __int_as_float(0x7FFFFFFF);
+}
 // Rows of a unit: row / g and the row's offset in q and out.  g <= 8, so the high
 // word of row * ceil(2^32 / g) is the quotient for every row below 2^29.
 struct RowMap {

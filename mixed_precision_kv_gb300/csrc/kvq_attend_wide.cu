@@ -50,6 +50,7 @@ constexpr int kTileBytes = 128 * 128 * 2;
 constexpr float kHead = 7.0f;                   // P = 2^(x - m + 7)
 constexpr float kGrow = 8.0f;                   // a maximum may be stale by this much (base 2)
 constexpr float kNever = -3.0e38f;              // S of a key that is not seen
+constexpr float kLowest = 0.9f * kNever;        // logits below it count as it
 
 struct alignas(1024) WideSmem {
   uint8_t q[2][kTileBytes], kv[kRing][kTileBytes];
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
 #pragma unroll
             for (int o = 8; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
             const int e = q_exponent(mx);
-            const float mul = copysignf(pow2f(e), A.scale_log2);
+            const float mul = q_factor(mx, e, A.scale_log2);
             // (a factor below 1e-30 makes every logit 0, as 1e-30 does; kNever times it must stay far below 0)
             const float rr = fmaxf(fabsf(A.scale_log2) * pow2f(-e), 1e-30f);
             const float mine = __shfl_sync(0xFFFFFFFFu, rr, (lane & 1) << 4);
@@ -391,12 +392,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
           for (int y = 0; y < 4; ++y)
             mq[y] = fmaxf(fmaxf(mq[y], __uint_as_float(sv[j + 2 * y])), __uint_as_float(sv[j + 2 * y + 1]));
         float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-        mx = mx > 0.9f * kNever ? mx * rf : -INFINITY;
+        mx = mx > kLowest ? fmaxf(mx * rf, kLowest) : -INFINITY;
         const bool grow = mx > m + kGrow || (m == -INFINITY && mx > -INFINITY);
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float corr = grow ? ex2f(m - mx) : 1.0f;   // m = -inf: 0
           if (grow) m = mx;
           l *= corr;
+          // a logit above fp32's range, or all below it so far: the row's sum is not a number
+          if (m == INFINITY || m == kLowest) l = __int_as_float(0x7FFFFFFF);
           if (any) {
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 from attend_ref import SCALE, attend_row
-from test_gpu_attend import MMA, ROUND, SIMT, Pool, check, kvq, mixed, rand  # noqa: F401
+from test_gpu_attend import IMPLS, MMA, ROUND, Pool, check, kvq, mixed, rand  # noqa: F401
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -18,7 +18,7 @@ def range_error(kvq, pool):
     pool.sync()   # reported once
 
 
-@pytest.mark.parametrize("impl", [SIMT])
+@pytest.mark.parametrize("impl", IMPLS)
 @pytest.mark.parametrize("n,T", [(70, 3), (6000, 3), (70, 130), (6000, 130)])
 def test_rows_of_q_that_are_not_finite(kvq, impl, n, T):
     """They give rows that are not finite and KV_ERR_RANGE, and leave the other rows alone; blocks
@@ -45,7 +45,7 @@ def test_rows_of_q_that_are_not_finite(kvq, impl, n, T):
                 assert (np.abs(got[t, j] - o) <= tol).all(), (t, j)
 
 
-@pytest.mark.parametrize("impl", [SIMT])
+@pytest.mark.parametrize("impl", IMPLS)
 @pytest.mark.parametrize("T", [1, 130])
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 def test_one_infinite_element_and_keys_of_one_sign(kvq, impl, T, sign):
@@ -62,7 +62,7 @@ def test_one_infinite_element_and_keys_of_one_sign(kvq, impl, T, sign):
     assert torch.isfinite(out.float()).all()
 
 
-@pytest.mark.parametrize("impl", [SIMT])
+@pytest.mark.parametrize("impl", IMPLS)
 @pytest.mark.parametrize("T", [1, 130])
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 def test_logits_past_fp32(kvq, impl, T, sign):
