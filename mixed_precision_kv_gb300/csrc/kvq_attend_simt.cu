@@ -26,7 +26,7 @@ constexpr int kKs = kHeadDim + 4;    // K row stride in floats: 16-byte reads of
 
 __device__ __forceinline__ float half_at(const uint8_t* p) { return __half2float(*reinterpret_cast<const __half*>(p)); }
 __device__ __forceinline__ float bf(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
-// a new token's value as the cache takes it: NaN, Inf and |x| > 65504 are reported and used as 0
+// a new or list token's value: NaN, Inf and |x| > 65504 are reported and used as 0
 __device__ __forceinline__ float new_value(uint16_t x, uint32_t* status) {
   const float f = bf(x);
   if (fabsf(f) <= 65504.0f) return f;
@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttArgs A, const AttUn
     for (int x = tid; x < kPage * kHeadDim; x += 256) {
       const int t = x / kHeadDim, c = x % kHeadDim;
       const bool on = j0 + t < u.n_fp;
-      ks[t][c] = on ? bf(A.fpk[fp0 + (size_t)(j0 + t) * kHeadDim + att_list_at(j0 + t, c)]) : 0.0f;
-      vs[t][c] = on ? bf(A.fpv[fp0 + (size_t)(j0 + t) * kHeadDim + att_list_at(j0 + t, c)]) : 0.0f;
+      ks[t][c] = on ? new_value(A.fpk[fp0 + (size_t)(j0 + t) * kHeadDim + att_list_at(j0 + t, c)], A.status) : 0.0f;
+      vs[t][c] = on ? new_value(A.fpv[fp0 + (size_t)(j0 + t) * kHeadDim + att_list_at(j0 + t, c)], A.status) : 0.0f;
     }
     __syncthreads();
     keys([&](int) { return j0 + lane < u.n_fp; });

@@ -78,3 +78,27 @@ def test_logits_past_fp32(kvq, impl, T, sign):
     assert not torch.isfinite(out[0, 1].float()).any()
     out[0, 1] = 1.0
     assert (out == 1.0).all()
+
+
+@pytest.mark.parametrize("impl", IMPLS)
+@pytest.mark.parametrize("T", [2, 130])
+def test_list_tokens_out_of_range(kvq, impl, T):
+    """A list token past binary16's range (or not a number) is used as 0 there and reported."""
+    P = Pool(kvq, 1, [mixed(50, 1), mixed(50, 1)], seed=9)
+    P.pool.fp_configure(40)
+    k, v = rand((33, 1, 128), P.gen), rand((33, 1, 128), P.gen)
+    bad = [(3, 7, float("nan")), (20, 100, 1e38), (32, 0, float("-inf"))]
+    k0, v0 = k.clone(), v.clone()
+    for t, c, x in bad:
+        k[t, 0, c], v[t, 0, (c + 5) % 128] = x, x
+        k0[t, 0, c], v0[t, 0, (c + 5) % 128] = 0, 0
+    P.pool.fp_append(P.ids[0], k, v)
+    q, kn, vn = (rand((T, h, 128), P.gen) for h in (4, 1, 1))
+    P.pool.set_decode_impl(impl)
+    out = P.pool.attend(q, [P.ids[0]], [T], SCALE, kn, vn)
+    range_error(kvq, P.pool)
+    P.pool.fp_drop(P.ids[0], 0, 33)
+    P.pool.fp_append(P.ids[0], k0, v0)
+    ref = P.pool.attend(q, [P.ids[0]], [T], SCALE, kn, vn)
+    P.pool.sync()
+    assert torch.isfinite(out.float()).all() and torch.equal(out, ref)
