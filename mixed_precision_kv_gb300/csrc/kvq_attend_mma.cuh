@@ -383,9 +383,10 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p, bool aligned) {
   return aligned ? __ldg(reinterpret_cast<const uint4*>(p)) : load8_unaligned(p);
 }
 // Power-of-two scale of a row of q: exponent e so that mx 2^e lies in [2^7, 2^8)
-// (0 for a row that is zero or not finite).
+// (0 for a row that is zero or not finite; at most 126, so that 2^-e is a normal
+// number: rows below 2^-119 end below 2^7).
 __device__ __forceinline__ int q_exponent(float mx) {
-  return mx > 0.0f && mx < INFINITY ? max(-100, min(100, 134 - (int)(__float_as_uint(mx) >> 23))) : 0;
+  return mx > 0.0f && mx < INFINITY ? min(126, 134 - (int)(__float_as_uint(mx) >> 23)) : 0;
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 // The factor of a row of q: 2^e with the scale's sign.  A row with an infinity (mx; a NaN is

@@ -102,3 +102,32 @@ def test_list_tokens_out_of_range(kvq, impl, T):
     ref = P.pool.attend(q, [P.ids[0]], [T], SCALE, kn, vn)
     P.pool.sync()
     assert torch.isfinite(out.float()).all() and torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("impl", IMPLS)
+@pytest.mark.parametrize("size", [1e36, 1e-36])
+def test_queries_near_the_ends_of_bf16(kvq, impl, size):
+    P = Pool(kvq, 1, [mixed(200, 2)], seed=24)
+    check(P, impl, [0], [5], 8, scale=SCALE / size, q_mult=size)
+    check(P, impl, [0], [100], 8, scale=SCALE / size, q_mult=size, rows=[0, 60, 99])
+
+
+@pytest.mark.parametrize("T", [3, 100])
+def test_queries_at_the_ends_of_bf16(kvq, T):
+    """The greatest and the least normal elements (the CUDA cores' fp32 sums do not hold the greatest).
+    The scale of the greatest is below 2^-126, so fp32 holds it, and its product with log2 e, to 2^-20
+    each: logits move by 2^-19 of themselves, which is within the hundredth that the tolerance of
+    attend_row() adds to the 2^-11 of rounding K."""
+    P = Pool(kvq, 1, [mixed(200, 2)], seed=25)
+    P.pool.set_decode_impl(MMA)
+    q = rand((T, 8, 128), P.gen).clamp(-3.9, 3.9)
+    C = P.content(0)
+    for e in (126, -118):
+        qe = (q.float() * 2.0 ** e).bfloat16()
+        got = P.pool.attend(qe, P.ids, [T], SCALE * 2.0 ** -e).double().cpu().numpy()
+        P.pool.sync()
+        qh = qe.double().cpu().numpy() * 2.0 ** -e
+        for t in {0, T // 2, T - 1}:
+            for j in range(8):
+                o, tol = attend_row(qh[t, j], C.K[0], C.V[0], SCALE, ROUND[MMA])
+                assert (np.abs(got[t, j] - o) <= tol).all(), (e, t, j)
