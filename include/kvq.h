@@ -213,7 +213,11 @@ KVQ_API kv_status_t kv_fp_count(kv_pool_t* pool, int32_t req_id, int64_t* n_tok)
  *   out      device, fp32 [batch][num_q_heads][128]
  * q head h uses kv head h / (num_q_heads / num_kv_heads); num_q_heads must be
  * a multiple of num_kv_heads with a ratio <= 8.  A request with no tokens
- * yields zeros.  Logits are softmax_scale * q.k^ in fp32 accumulation. */
+ * yields zeros.  Logits are softmax_scale * q.k^ in fp32 accumulation.
+ * On a stream that is being captured into a graph the call does not wait for
+ * the pool's work on other streams; the caller orders the graph's launches.
+ * Such a graph is of kernels alone where the plan of the decode before stands
+ * (the same batch, no page added since), and good until the pool plans again. */
 KVQ_API kv_status_t kv_decode_attn(kv_pool_t* pool, const void* q, const int32_t* req_ids, int32_t batch,
                            int32_t num_q_heads, float softmax_scale, float* out, void* stream);
 

@@ -177,6 +177,11 @@ kv_status_t kvq::upload(kv_pool* P, const Upload& u, cudaStream_t s) {
 // Order this call after the pool's previous work when the stream changes.
 kv_status_t kvq::order_after_previous(kv_pool* P, cudaStream_t s) {
   if (P->last_stream != s && P->used) {
+    // A capture may not wait for work outside it, and puts nothing on the stream: when the
+    // graph runs is the caller's to order.
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    KV_CUDA(cudaStreamIsCapturing(s, &cs));
+    if (cs != cudaStreamCaptureStatusNone) return KV_OK;
     cudaEvent_t ev;
     KV_CUDA(cudaEventCreateWithFlags(&ev, cudaEventDisableTiming));
     KV_CUDA(cudaEventRecord(ev, P->last_stream));

@@ -98,3 +98,26 @@ def test_selection_where_the_third_head_decides(kvq):
     x[0, :, 2] = torch.tensor([1.0, 2.0 ** -24, 0.0])
     assert P.pool.select_lowest(x, P.ids, 1).cpu().tolist() == [[1]]
     assert P.pool.select_lowest(x, P.ids, 2).cpu().tolist() == [[1, 2]]
+
+
+@pytest.mark.parametrize("before", ["default", "other"])
+def test_a_decode_is_captured_after_work_on_another_stream(kvq, before):
+    """With a standing plan a decode only launches kernels: a graph of it gives what the call gives."""
+    P = Pool(kvq, 2, [mixed(900, 1), mixed(333, 2)], seed=4)
+    q, out = rand((2, 8, 128), P.gen), torch.empty(2, 8, 128, device="cuda")
+    s, o = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(o if before == "other" else torch.cuda.current_stream()):
+        want = P.pool.decode(q, P.ids, SCALE).clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        P.pool.decode(q, P.ids, SCALE, out=out)
+    for _ in range(2):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want)
+    q.neg_()
+    g.replay()
+    assert torch.equal(out, P.pool.decode(q, P.ids, SCALE))
+    P.pool.sync()
