@@ -308,7 +308,8 @@ KVQ_API kv_status_t kv_decode_attn_groups(kv_pool_t* const* pools, int32_t n_poo
  * sums are not, gives a row that is not finite, and KV_ERR_RANGE.  Workspace:
  * 64 KB per 128 keys and kv head of requests with more than 128 rows (n_new x q
  * heads per kv head), up to 4.3 GB or one kv head of the longest request, and
- * the rows' partial sums; it grows with cudaMalloc.  At most 2^31 rows of q.
+ * the rows' partial sums; it grows with cudaMalloc, and without memory for it
+ * the call is KV_ERR_OOM with nothing changed.  At most 2^31 rows of q.
  * The call plans on the host: on a stream that is being captured it is
  * KV_ERR_STATE. */
 KVQ_API kv_status_t kv_attend(kv_pool_t* pool, const void* q, const void* k, const void* v, const uint64_t* tree,
@@ -329,7 +330,8 @@ KVQ_API kv_status_t kv_attend(kv_pool_t* pool, const void* q, const void* k, con
  * The other arguments, out and the rules are kv_decode_attn's (a request may
  * be listed twice: its rows of scores are separate); always the tensor-core
  * scan, batch x num_kv_heads <= 65535.  A workspace of 128 bytes per q head and
- * page grows with cudaMalloc; the first call also puts the slots' positions on
+ * page grows with cudaMalloc, by doubling (KV_ERR_OOM without memory for it,
+ * nothing changed); the first call also puts the slots' positions on
  * the device (128 bytes per page of the pool).  On a stream that is being
  * captured it is KV_ERR_STATE.  kv_decode_timing does not cover it. */
 KVQ_API kv_status_t kv_decode_attn_scored(kv_pool_t* pool, const void* q, const int32_t* req_ids, int32_t batch,

@@ -11,7 +11,7 @@ ROOT = os.path.dirname(HERE)
 SO = os.path.join(HERE, "libkvq.so")
 SOURCES = ["kvq_pool.cu", "kvq_quant.cu", "kvq_decode_simt.cu", "kvq_decode_mma.cu", "kvq_noalloc.cu", "kvq_fp.cu",
            "kvq_decode_score.cu", "kvq_select.cu", "kvq_attend.cu", "kvq_attend_simt.cu", "kvq_attend_wide.cu", "kvq_attend_few.cu"]
-HEADERS = ["kvq_internal.h", "kvq_host.h", "kvq_layout.cuh", "kvq_scan_mma.cuh", "kvq_attend.h",
+HEADERS = ["kvq_internal.h", "kvq_host.h", "kvq_grow.h", "kvq_layout.cuh", "kvq_scan_mma.cuh", "kvq_attend.h",
            "kvq_attend_mma.cuh"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]

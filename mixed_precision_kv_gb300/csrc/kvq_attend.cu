@@ -472,7 +472,9 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
   xf.parts = (u.size + 255) & ~size_t(255);
   xl.parts = xf.parts + (size_t)pf.n_parts * R * kAttPart * sizeof(float);
   if ((st = ensure(P->attend, xl.parts + (size_t)pl.n_parts * 128 * kAttPart * sizeof(float))) != KV_OK) return st;
-  if ((st = ensure(P->attend_tiles, (size_t)most * (kAttTileBytes + 16))) != KV_OK) return st;
+  if ((st = ensure(P->attend_tiles, (size_t)most * (kAttTileBytes + 16), (size_t)kTilesPerPass * (kAttTileBytes + 16))) !=
+      KV_OK)
+    return st;
   if ((st = h2d(P, P->attend.ptr, u, s)) != KV_OK) return st;
   uint8_t* base = (uint8_t*)P->attend.ptr;
   auto merge = [&](const Placed& x, const AttPlan& p, int part_rows) -> cudaError_t {

@@ -33,8 +33,9 @@ struct DeviceGuard {
 
 inline bool req_ok(const kv_pool* P, int32_t r) { return r >= 0 && r < P->cfg.max_requests && P->reqs[r].open; }
 
-// Grow a device buffer to at least `bytes` (contents are not kept).
-kv_status_t ensure(DevBuf& b, size_t bytes);
+// Grow a device buffer to at least `bytes` (contents are not kept), as grow() in
+// kvq_grow.h says.  KV_ERR_OOM if there is no memory for it; the buffer is then empty.
+kv_status_t ensure(DevBuf& b, size_t bytes, size_t most = SIZE_MAX);
 
 // Several host arrays laid out for one upload (one H2D copy per call); the
 // arrays are copied straight into the pinned staging buffer by h2d (they must

@@ -17,6 +17,7 @@
 #include <utility>
 #include <vector>
 
+#include "kvq_grow.h"
 #include "kvq_host.h"
 #include "kvq_internal.h"
 
@@ -120,20 +121,27 @@ kv_status_t kvq::fail(kv_status_t st, const char* fmt, ...) {
   return st;
 }
 
-// Grow a device buffer to at least `bytes` (contents are not kept).
-kv_status_t kvq::ensure(DevBuf& b, size_t bytes) {
+kv_status_t kvq::ensure(DevBuf& b, size_t bytes, size_t most) {
   if (b.cap >= bytes) return KV_OK;
-  size_t cap = std::max<size_t>(bytes, b.cap * 2);
-  cap = (cap + 255) & ~size_t(255);
+  const size_t have = b.cap;
   if (b.ptr) {
     KV_CUDA(cudaDeviceSynchronize());
     KV_CUDA(cudaFree(b.ptr));
     b.ptr = nullptr;
     b.cap = 0;
   }
-  KV_CUDA(cudaMalloc(&b.ptr, cap));
-  b.cap = cap;
-  return KV_OK;
+  cudaError_t e = cudaSuccess;
+  b.cap = grow(have, bytes, most, [&](size_t n) {
+    e = cudaMalloc(&b.ptr, n);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      b.ptr = nullptr;
+    }
+    return e == cudaSuccess;
+  });
+  if (b.cap) return KV_OK;
+  return fail(e == cudaErrorMemoryAllocation ? KV_ERR_OOM : KV_ERR_CUDA, "cannot allocate a workspace of %zu bytes: %s",
+              bytes, cudaGetErrorString(e));
 }
 
 // Host-to-device copy through a pinned staging slot.  A copy from pageable
@@ -170,7 +178,7 @@ kv_status_t kvq::h2d(kv_pool* P, void* dst, const Upload& u, cudaStream_t s) {
 kv_status_t kvq::upload(kv_pool* P, const Upload& u, cudaStream_t s) {
   if (u.size == 0) return KV_OK;
   kv_status_t st = ensure(P->upload, u.size);
-  if (st != KV_OK) return st;
+  if (st != KV_OK) return KV_ERR_CUDA;   // not KV_ERR_OOM: the caller's tables may have changed
   return h2d(P, P->upload.ptr, u, s);
 }
 

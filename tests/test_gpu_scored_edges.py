@@ -121,3 +121,57 @@ def test_a_decode_is_captured_after_work_on_another_stream(kvq, before):
     g.replay()
     assert torch.equal(out, P.pool.decode(q, P.ids, SCALE))
     P.pool.sync()
+
+
+def test_operand_tiles_stay_within_their_bound(kvq):
+    """kv_attend's workspace grows to what a call needs and at most to 4.3 GB where that is enough."""
+    n, T, hkv, hq = 131072, 49, 8, 64
+    pages = 2 * (n // 32 + 64)
+    pool = kvq.KVPool(hkv, pages, pages, 1, n // 32 + 64)
+    rid = pool.open()
+    gen = torch.Generator("cuda").manual_seed(23)
+    for a in range(0, n, 16384):
+        pool.append(rand((16384, hkv, 128), gen), rand((16384, hkv, 128), gen), np.full(16384, rid, np.int32),
+                    np.full(16384, 2, np.uint8))
+    q, k, v = (rand((6 * T, h, 128), gen) for h in (hq, hkv, hkv))
+    out = torch.empty_like(q)
+    pool.sync()
+    free = torch.cuda.mem_get_info()[0]
+    for times in (5, 6):   # 2.7 and 3.2 GB of tiles
+        m = times * T
+        pool.attend(q[:m], [rid] * times, [T] * times, SCALE, k[:m], v[:m], out=out[:m])
+        pool.sync()
+    grown = free - torch.cuda.mem_get_info()[0]
+    assert 3.2e9 < grown < 4.8e9, grown   # tiles, and 0.1 GB or so of plan and partial sums
+
+
+def test_a_workspace_without_memory_for_it(kvq):
+    """The logits of one request listed 8191 times (314 GB) are KV_ERR_OOM; scores stay, and the pool
+    goes on with what it was."""
+    n, hkv, hq, times = 150000, 8, 64, 8191
+    pages = 2 * (n // 32 + 64)
+    pool = kvq.KVPool(hkv, pages, pages, 1, n // 32 + 64)
+    rid = pool.open()
+    gen = torch.Generator("cuda").manual_seed(23)
+    for a in range(0, n, 15000):
+        pool.append(rand((15000, hkv, 128), gen), rand((15000, hkv, 128), gen), np.full(15000, rid, np.int32),
+                    np.full(15000, 2, np.uint8))
+    q = rand((times, hq, 128), gen)
+    pool.set_decode_impl(MMA)
+    want = pool.decode(q[:2], [rid, rid], SCALE)
+    scores = torch.empty(times, hkv, n, device="cuda")   # 39 GB
+    out = torch.empty(times, hq, 128, device="cuda")
+    scores[:2] = 0
+    with pytest.raises(kvq.KVError) as e:
+        pool.decode_scored(q, [rid] * times, SCALE, scores, out=out)
+    assert e.value.status == kvq.KV_ERR_OOM and "workspace" in str(e.value)
+    pool.sync()
+    assert (scores[:2] == 0).all()
+    got = pool.decode_scored(q[:2], [rid, rid], SCALE, scores[:2], out=out[:2])
+    assert torch.equal(got, want) and torch.equal(pool.decode(q[:2], [rid, rid], SCALE), want)
+    # 8 weights' sums of 1: a logit is off by 136 roundings of at most 10 (128 products of normal values,
+    # scaled), which moves a weight by twice that, 1.6e-4 of itself; the sum's own error is far below
+    assert torch.allclose(scores[:2].sum(2), torch.full((2, hkv), 8.0, device="cuda"), rtol=0.0, atol=2e-3)
+    pool.sync()
+    del scores
+    torch.cuda.empty_cache()
