@@ -1598,6 +1598,7 @@ kv_status_t kvq::build_plan(kv_pool* P, const int32_t* req_ids, int32_t batch, i
   const size_t os = up.add(hp.splits.data(), hp.splits.size() * sizeof(Split));
   const size_t oc = up.add(hp.cta_split.data(), hp.cta_split.size() * sizeof(int32_t));
   const size_t of = up.add(hp.fp_wsplit.data(), hp.fp_wsplit.size() * sizeof(int32_t));
+  P->plan_impl = -1;   // no plan stands until the new one is on the device
   kv_status_t st = ensure(P->plan, up.size);
   if (st != KV_OK) return st;
   if ((st = h2d(P, P->plan.ptr, up, s)) != KV_OK) return st;
@@ -1893,6 +1894,7 @@ kv_status_t build_group_plan(kv_pool* const* pools, int n_pools, const int32_t* 
   const size_t os = up.add(hp.splits.data(), hp.splits.size() * sizeof(Split));
   const size_t ow = up.add(hp.wsplit.data(), hp.wsplit.size() * sizeof(int32_t));
   const size_t og = up.add(gp.data(), gp.size() * sizeof(GroupPool));
+  P->gplan_hq = 0;   // no plan stands until the new one is on the device
   kv_status_t st = ensure(P->gplan, up.size);
   if (st != KV_OK) return st;
   if ((st = h2d(P, P->gplan.ptr, up, s)) != KV_OK) return st;
