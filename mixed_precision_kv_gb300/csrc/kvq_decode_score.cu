@@ -225,7 +225,7 @@ extern "C" kv_status_t kv_decode_attn_scored(kv_pool_t* P, const void* q, const 
     KV_CUDA(launch_score_add_any(g, P, du, P->n_units, max_len, ml, logits, decay, scores, score_stride, s));
   P->stat_req.assign(req_ids, req_ids + batch);
   P->stat_hq = hq;
-  P->stat_skip_dead = false;
+  P->stat_skip_dead = true;   // as the scan does
   return KV_OK;
 } catch (const std::bad_alloc&) {
   return fail(KV_ERR_OOM, "kv_decode_attn_scored: host allocation failed");

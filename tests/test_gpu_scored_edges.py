@@ -175,3 +175,18 @@ def test_a_workspace_without_memory_for_it(kvq):
     pool.sync()
     del scores
     torch.cuda.empty_cache()
+
+
+def test_statistics_after_a_scored_decode(kvq):
+    """Pages without a live slot are not read by the scored decode, and not counted."""
+    P = Pool(kvq, 2, [mixed(320, 1, (4,))], seed=2, dead=[np.arange(64)])
+    q, sc = rand((1, 8, 128), P.gen), torch.zeros(1, 2, 320, device="cuda")
+    P.pool.set_decode_impl(MMA)
+    P.pool.decode(q, P.ids, SCALE)
+    plain = P.pool.last_decode_stats()
+    P.pool.decode_scored(q, P.ids, SCALE, sc)
+    scored = P.pool.last_decode_stats()
+    P.pool.decode(q, P.ids, SCALE)
+    assert P.pool.last_decode_stats() == plain
+    page = 32 * 160 * 2   # an INT4 page of two kv heads
+    assert plain["kv_bytes"] - scored["kv_bytes"] == 2 * page
