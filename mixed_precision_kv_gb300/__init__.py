@@ -138,6 +138,19 @@ def _stream(stream, device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """A call's output: a block of the stream that the call runs on.  One of the current stream
+    could still be in use by work queued there, and would be handed out again before the call on
+    `stream` is done; the current stream is taken to read the output."""
+    torch = _torch_mod()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(torch.cuda.current_stream(device))
+    return out
+
+
 def alloc_bits(N, D2, D4, budget):
     """Greedy INT2/INT4 bit allocation (host); budget = (num, den) average bits."""
     N = _np(N, np.int64)
@@ -291,7 +304,7 @@ class KVPool:
             raise ValueError("q must be a contiguous bf16 tensor [B][Hq][128] on the pool's device with "
                              "B == len(req_ids)")
         if out is None:
-            out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+            out = _empty((B, Hq, D), torch.float32, q.device, stream)
         elif out.dtype is not torch.float32 or out.shape != q.shape or not self._on_pool_device(out) or \
                 not out.is_contiguous():
             raise ValueError("out must be a contiguous fp32 tensor shaped like q on the pool's device")
@@ -338,7 +351,7 @@ class KVPool:
                 not q.is_contiguous():
             raise ValueError("q must be a contiguous bf16 tensor [B][Hq][128] on the pools' device")
         if out is None:
-            out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+            out = _empty((B, Hq, D), torch.float32, q.device, stream)
         elif out.dtype is not torch.float32 or out.shape != q.shape or not pools[0]._on_pool_device(out) or \
                 not out.is_contiguous():
             raise ValueError("out must be a contiguous fp32 tensor shaped like q on the pools' device")
@@ -372,7 +385,7 @@ class KVPool:
                                  not self._on_pool_device(tree) or not tree.is_contiguous()):
             raise ValueError("tree must be a contiguous int64 tensor [sum(n_new)] on the pool's device")
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty(q.shape, q.dtype, q.device, stream)
         elif out.dtype is not torch.bfloat16 or out.shape != q.shape or not self._on_pool_device(out) or \
                 not out.is_contiguous():
             raise ValueError("out must be a contiguous bf16 tensor shaped like q on the pool's device")
@@ -404,7 +417,7 @@ class KVPool:
                              "B == len(req_ids)")
         self._check_scores(scores, req_ids.size)
         if out is None:
-            out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+            out = _empty(q.shape, torch.float32, q.device, stream)
         elif out.dtype is not torch.float32 or out.shape != q.shape or not self._on_pool_device(out) or \
                 not out.is_contiguous():
             raise ValueError("out must be a contiguous fp32 tensor shaped like q on the pool's device")
@@ -431,7 +444,7 @@ class KVPool:
         most = int(n_select.max()) if req_ids.size else 0
         shape = (req_ids.size, self.num_kv_heads, most) if per_head else (req_ids.size, most)
         if out is None:
-            out = torch.empty(shape, dtype=torch.int32, device=scores.device)
+            out = _empty(shape, torch.int32, scores.device, stream)
         elif out.dtype is not torch.int32 or tuple(out.shape) != shape or not self._on_pool_device(out) or \
                 not out.is_contiguous():
             raise ValueError(f"out must be a contiguous int32 tensor {list(shape)} on the pool's device")

@@ -190,3 +190,28 @@ def test_statistics_after_a_scored_decode(kvq):
     assert P.pool.last_decode_stats() == plain
     page = 32 * 160 * 2   # an INT4 page of two kv heads
     assert plain["kv_bytes"] - scored["kv_bytes"] == 2 * page
+
+
+def test_outputs_are_blocks_of_the_stream_of_the_call(kvq):
+    """Work queued on the current stream may still use a block that it gave back: an output on another
+    stream is none of those, and its own block is not given out while the current stream may read it."""
+    P = Pool(kvq, 2, [mixed(300, 1), mixed(65, 2)], seed=6)
+    pool, ids, s = P.pool, P.ids, torch.cuda.Stream()
+    q, k, v = (rand((2, h, 128), P.gen) for h in (8, 2, 2))
+    scores = torch.rand(2, 2, 300, device="cuda", generator=P.gen)
+    calls = [(lambda **kw: pool.decode(q, ids, SCALE, **kw), (2, 8, 128), torch.float32),
+             (lambda **kw: kvq.KVPool.decode_groups([pool], q, [ids], SCALE, **kw), (2, 8, 128), torch.float32),
+             (lambda **kw: pool.attend(q, ids, [1, 1], SCALE, k, v, **kw), (2, 8, 128), torch.bfloat16),
+             (lambda **kw: pool.decode_scored(q, ids, SCALE, scores, decay=1.0, **kw), (2, 8, 128), torch.float32),
+             (lambda **kw: pool.select_lowest(scores, ids, 40, **kw), (2, 40), torch.int32)]
+    for call, shape, dtype in calls:
+        want = call()
+        given = set()
+        for _ in range(20):   # blocks of the current stream, given back
+            given |= {x.data_ptr() for x in [torch.empty(shape, dtype=dtype, device="cuda") for _ in range(4)]}
+            s.wait_stream(torch.cuda.current_stream())
+            out = call(stream=s)
+            assert out.data_ptr() not in given and out.shape == shape and out.dtype == dtype
+        s.synchronize()
+        assert torch.equal(out, want)
+    pool.sync()
