@@ -131,3 +131,120 @@ def test_queries_at_the_ends_of_bf16(kvq, T):
             for j in range(8):
                 o, tol = attend_row(qh[t, j], C.K[0], C.V[0], SCALE, ROUND[MMA])
                 assert (np.abs(got[t, j] - o) <= tol).all(), (e, t, j)
+
+
+# ---- units above 384 rows on the tensor cores ------------------------------
+@pytest.mark.parametrize("T", [100, 130])
+def test_many_rows_evicted_and_excluded(kvq, T):
+    """Evicted slots, a request with every slot evicted, slots excluded for one kv head, a list."""
+    rng = np.random.default_rng(T)
+    dead = [np.sort(rng.choice(1260, 160, replace=False)), np.arange(64), []]
+    P = Pool(kvq, 2, [mixed(1260, 7, (2, 3, 4, 0xF4)), mixed(64, 8), mixed(90, 9)], seed=1, dead=dead)
+    rows = [0, 1, 63, 64, T - 1]
+    check(P, MMA, [0, 1, 2], [T, T, T], 8, rows=rows)
+    ex = {0: {(1, int(p)) for p in rng.choice(1260, 400, replace=False)}, 2: {(0, p) for p in range(90)}}
+    for r, s in ex.items():
+        s = sorted(s)
+        P.pool.evict_head([P.ids[r]] * len(s), [p for _, p in s], [h for h, _ in s])
+    check(P, MMA, [0, 1, 2], [T, T, T], 8, rows=rows, head_dead=ex)
+    out = check(P, MMA, [2, 1], [T, T], 8, rows=[0], head_dead=ex, with_kv=False)
+    assert (out[:T, :4] == 0).all() and (out[T:] == 0).all()
+    P.pool.fp_configure(200)
+    fp = {}
+    for r, n in ((1, 131), (2, 3)):
+        k, v = rand((n, 2, 128), P.gen), rand((n, 2, 128), P.gen)
+        P.pool.fp_append(P.ids[r], k, v)
+        fp[r] = (k.double().cpu().numpy(), v.double().cpu().numpy())
+    check(P, MMA, [0, 1, 2], [T, T, T], 8, rows=rows, head_dead=ex, fp=fp)
+
+
+@pytest.mark.parametrize("choice", [(2,), (3,), (4,), (0xF4,), (2, 3, 4, 0xF4)])
+def test_many_rows_every_width(kvq, choice):
+    P = Pool(kvq, 2, [mixed(450, 3, choice), mixed(70, 4, choice)], seed=len(choice) + choice[0], reorder=False)
+    check(P, MMA, [0, 1], [98, 110], 8, rows=[0, 33, 64, 97, 109])
+
+
+@pytest.mark.parametrize("T", [49, 64])
+@pytest.mark.parametrize("n", [0, 100, 5000])
+def test_many_rows_tree(kvq, T, n):
+    """392 to 512 rows of random masks: ancestors, later tokens, none at all, bits past the tokens."""
+    P = Pool(kvq, 1, [mixed(n, 1), mixed(0, 1)], seed=T, chunk=1000)
+    rng = np.random.default_rng(T + n)
+    tree = rng.integers(0, 1 << 63, 2 * T, dtype=np.uint64) * np.uint64(2) + rng.integers(0, 2, 2 * T).astype(np.uint64)
+    tree[0] = tree[T] = tree[T + 40] = 0
+    tree[T + 1] = np.uint64(1) << np.uint64(T - 1)
+    tree[-1] = np.uint64(0xFFFFFFFFFFFFFFFF)
+    out = check(P, MMA, [0, 1], [T, T], 8, tree=tree, rows=[0, 1, 31, 32, 40, T - 1])
+    assert (out[T] == 0).all() and (out[T + 40] == 0).all()
+
+
+@pytest.mark.parametrize("n", [140, 5000])
+def test_many_rows_unaligned_guards_and_out(kvq, n):
+    """Inputs and outputs one element past an aligned address, blocks whole and merged from pieces;
+    what lies around out stays."""
+    P = Pool(kvq, 2, [mixed(n, 1)], seed=8, chunk=1000)
+    hq, T = 8, 130
+    base = {name: torch.randn(T * h * 128 + 1, generator=P.gen, device="cuda").bfloat16()
+            for name, h in (("q", hq), ("k", 2), ("v", 2))}
+    view = {name: base[name][1:].view(T, h, 128) for name, h in (("q", hq), ("k", 2), ("v", 2))}
+    flat = torch.full((T * hq * 128 + 9,), 7.0, dtype=torch.bfloat16, device="cuda")
+    P.pool.set_decode_impl(MMA)
+    P.pool.attend(view["q"], P.ids, [T], SCALE, view["k"], view["v"], out=flat[1:1 + T * hq * 128].view(T, hq, 128))
+    out = P.pool.attend(view["q"].clone(), P.ids, [T], SCALE, view["k"].clone(), view["v"].clone())
+    P.pool.sync()
+    assert torch.equal(flat[1:1 + T * hq * 128].view(T, hq, 128), out)
+    assert flat[0] == 7.0 and (flat[1 + T * hq * 128:] == 7.0).all()
+    check(P, MMA, [0], [T], hq, rows=[0, 63, 64, 127, T - 1])
+
+
+def test_many_rows_values_out_of_range(kvq):
+    T = 130
+    P = Pool(kvq, 1, [mixed(50, 1)], seed=9)
+    q, k, v = (rand((T, h, 128), P.gen) for h in (4, 1, 1))
+    k[T - 1, 0, 5], v[T - 1, 0, 7], v[T - 1, 0, 8] = float("nan"), float("inf"), 1e38
+    P.pool.set_decode_impl(MMA)
+    out = P.pool.attend(q, P.ids, [T], SCALE, k, v)
+    range_error(kvq, P.pool)
+    k[T - 1, 0, 5] = v[T - 1, 0, 7] = v[T - 1, 0, 8] = 0
+    ref = P.pool.attend(q, P.ids, [T], SCALE, k, v)
+    P.pool.sync()
+    assert torch.isfinite(out.float()).all() and torch.equal(out, ref)
+
+
+def test_many_rows_other_stream_and_two_threads(kvq):
+    """On another stream, repeated, and on two pools at once: what one call alone gives."""
+    import threading
+    pools = [Pool(kvq, 2, [mixed(900, s), mixed(333, s + 1)], seed=s) for s in (31, 33)]
+    n_new = [110, 101]
+    q, k, v = (rand((sum(n_new), h, 128), pools[0].gen) for h in (8, 2, 2))
+    alone = [P.pool.attend(q, P.ids, n_new, SCALE, k, v) for P in pools]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(P, want):
+        s = torch.cuda.Stream()
+        out = torch.empty_like(want)
+        for _ in range(10):
+            P.pool.attend(q, P.ids, n_new, SCALE, k, v, out=out, stream=s)
+        s.synchronize()
+        P.pool.sync()
+        if not torch.equal(out, want):
+            wrong.append(P)
+
+    t = [threading.Thread(target=work, args=x) for x in zip(pools, alone)]
+    [x.start() for x in t]
+    [x.join() for x in t]
+    assert not wrong
+
+
+def test_many_rows_of_one_long_chunk(kvq):
+    """70,001 new tokens: 274 blocks of rows, 547 tiles of new keys."""
+    P = Pool(kvq, 1, [mixed(1000, 1)], seed=3, chunk=500)
+    check(P, MMA, [0], [70001], 1, rows=[0, 255, 256, 40000, 65535, 65536, 70000])
+
+
+@pytest.mark.parametrize("impl", IMPLS)
+def test_64_kv_heads(kvq, impl):
+    P = Pool(kvq, 64, [mixed(90, 1), mixed(33, 2)], seed=5)
+    check(P, impl, [0, 1], [2, 1], 64)
+    check(P, impl, [1], [400], 64, rows=[0, 399])

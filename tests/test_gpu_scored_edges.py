@@ -215,3 +215,172 @@ def test_outputs_are_blocks_of_the_stream_of_the_call(kvq):
         s.synchronize()
         assert torch.equal(out, want)
     pool.sync()
+
+
+@pytest.mark.parametrize("per_head", [False, True])
+def test_selection_of_rows_past_shared_memory(kvq, per_head):
+    """More than 393,216 positions: keys are read again for every digit."""
+    n, hkv = 400007, 2
+    pool = kvq.KVPool(hkv, n // 32 + 16, n // 32 + 16, 1, n // 32 + 32)
+    rid = pool.open()
+    gen = torch.Generator("cuda").manual_seed(5)
+    for a in range(0, n, 50000):
+        m = min(50000, n - a)
+        pool.append(rand((m, hkv, 128), gen), rand((m, hkv, 128), gen), np.full(m, rid, np.int32), np.full(m, 2, np.uint8))
+    dead = np.arange(1000, 390000, 7)
+    pool.evict(np.full(dead.size, rid, np.int32), dead)
+    x = torch.rand(1, hkv, n + 3, device="cuda", generator=gen)
+    x = torch.where(x < 0.2, torch.zeros_like(x), x)
+    live = np.setdiff1d(np.arange(n - 100), dead)
+    xs = x.cpu().numpy()[0]
+    keys = list(xs) if per_head else [summed_keys(xs)]
+    for m in (1, 1000, 200000, 399000):
+        got = pool.select_lowest(x, [rid], m, protect=100, per_head=per_head).cpu().numpy()[0]
+        for row, key in zip(got if per_head else got[None], keys):
+            want = np.sort(live[np.argsort(key[live], kind="stable")[:m]])
+            assert np.array_equal(row[:want.size], want) and (row[want.size:] == -1).all(), m
+
+
+def test_evict_lowest_of_every_head_its_own(kvq):
+    """The chosen positions are the least of each head and read as dead for that head only."""
+    P = Pool(kvq, 2, [mixed(500, 1), mixed(77, 2), mixed(0, 1)], seed=3)
+    P.pool.set_decode_impl(MMA)
+    x = torch.rand(3, 2, 500, device="cuda", generator=P.gen)
+    want = check_select(P, x, [60, 20, 4], 10, True)
+    pos = P.pool.evict_lowest(x, P.ids, [60, 20, 4], protect=10, per_head=True)
+    assert np.array_equal(pos, want)
+    ex = {r: {(h, int(p)) for h in range(2) for p in pos[r, h] if p >= 0} for r in range(2)}
+    assert [len(ex[r]) for r in range(2)] == [120, 40]
+    step(P, 8, torch.rand(3, 2, 520, device="cuda"), 1.0, head_dead=ex)
+    again = check_select(P, x, [60, 20, 4], 10, True, head_dead=ex)
+    for r in range(2):
+        for h in range(2):
+            assert not set(again[r, h].tolist()) & {p for y, p in ex[r] if y == h}
+    # everything, and once more with nothing left
+    P.pool.evict_lowest(x, P.ids, 500, per_head=True)
+    assert (P.pool.evict_lowest(x, P.ids, 500, per_head=True) == -1).all()
+    assert (P.pool.evict_lowest(x, P.ids, 500) == -1).all()
+
+
+def test_scored_decode_of_requests_without_tokens(kvq):
+    P = Pool(kvq, 2, [mixed(0, 1), mixed(0, 2)], seed=1)
+    scores = torch.rand(2, 2, 5, device="cuda", generator=P.gen)
+    kept = scores.clone()
+    out = P.pool.decode_scored(rand((2, 8, 128), P.gen), P.ids, SCALE, scores, decay=0.5)
+    assert (out == 0).all() and torch.equal(scores, kept)
+    assert (P.pool.evict_lowest(scores, P.ids, 3) == -1).all()
+
+
+class Live:
+    """A pool under random calls, and which positions of every request are live for every kv head."""
+
+    def __init__(self, kvq, seed):
+        self.rng = np.random.default_rng(seed)
+        self.gen = torch.Generator("cuda").manual_seed(seed)
+        self.hkv, self.kvq = 2, kvq
+        self.pool = kvq.KVPool(self.hkv, 90, 70, 3, 60, n_int3_pages=30, n_fp4_pages=30)
+        self.pool.fp_configure(32)
+        self.live, self.lists = {}, {}
+        for _ in range(3):
+            self.open()
+
+    def open(self):
+        r = self.pool.open()
+        self.live[r], self.lists[r] = np.zeros((self.hkv, 0), bool), 0
+
+    def some(self, r, share):
+        n = self.live[r].shape[1]
+        return self.rng.choice(n, int(n * share), replace=False) if n else np.zeros(0, np.int64)
+
+    def append(self):
+        reqs = [int(x) for x in self.rng.permutation(list(self.live))[:self.rng.integers(1, 4)]]
+        n = int(self.rng.choice([1, 3, 31, 33, 64, 130]))
+        ids = np.repeat(reqs, n)
+        if self.rng.random() < 0.4:
+            self.rng.shuffle(ids)
+        choice = [(2, 4), (2,), (4,), (2, 3, 4, 0xF4)][self.rng.integers(4)]
+        w = self.rng.choice(choice, ids.size).astype(np.uint8)
+        k, v = (rand((ids.size, self.hkv, 128), self.gen) for _ in range(2))
+        try:
+            self.pool.append(k, v, ids, w)
+        except self.kvq.KVError as e:
+            assert e.status == self.kvq.KV_ERR_OOM
+            return
+        for r in reqs:
+            self.live[r] = np.concatenate([self.live[r], np.ones((self.hkv, n), bool)], 1)
+
+    def evict(self):
+        r = int(self.rng.choice(list(self.live)))
+        n = self.live[r].shape[1]
+        at = self.some(r, 0.1) if self.rng.random() < 0.5 else np.arange(n // 4, n // 4 + min(90, n - n // 4))
+        self.pool.evict(np.full(at.size, r, np.int32), at)
+        self.live[r][:, at] = False
+
+    def evict_head(self):
+        r, h = int(self.rng.choice(list(self.live))), int(self.rng.integers(self.hkv))
+        at = self.some(r, 0.3)
+        self.pool.evict_head(np.full(at.size, r, np.int32), at, np.full(at.size, h, np.int32))
+        self.live[r][h, at] = False
+
+    def reorder(self):
+        self.pool.reorder(list(self.live))
+
+    def drop(self):
+        self.pool.drop_dead_pages(list(self.live))
+
+    def again(self):
+        r = int(self.rng.choice(list(self.live)))
+        self.pool.close_request(r)
+        del self.live[r], self.lists[r]
+        self.open()
+
+    def fp(self):
+        r = int(self.rng.choice(list(self.live)))
+        if self.lists[r]:
+            self.pool.fp_drop(r, 0, self.lists[r])
+            self.lists[r] = 0
+        else:
+            self.pool.fp_append(r, *(rand((5, self.hkv, 128), self.gen) for _ in range(2)))
+            self.lists[r] = 5
+
+    def check(self):
+        ids = [int(x) for x in self.rng.permutation(list(self.live))]
+        S = max(max(x.shape[1] for x in self.live.values()), 1)
+        g = int(self.rng.integers(1, 9))
+        scores = torch.rand(len(ids), self.hkv, S, device="cuda", generator=self.gen)
+        before = scores.cpu().numpy().astype(np.float64)
+        # softmax_scale 0: every key weighs the same
+        self.pool.decode_scored(rand((len(ids), g * self.hkv, 128), self.gen), ids, 0.0, scores, decay=0.5)
+        after = scores.cpu().numpy()
+        n_sel = [int(self.rng.integers(0, S + 1)) for _ in ids]
+        protect = int(self.rng.integers(0, 40))
+        shared = self.pool.select_lowest(scores, ids, n_sel, protect=protect).cpu().numpy()
+        own = self.pool.select_lowest(scores, ids, n_sel, protect=protect, per_head=True).cpu().numpy()
+        self.pool.sync()
+        for b, r in enumerate(ids):
+            L, limit = self.live[r], self.live[r].shape[1] - protect
+            for h in range(self.hkv):
+                n = int(L[h].sum()) + self.lists[r]
+                want = before[b, h].copy()
+                at = np.flatnonzero(L[h])
+                want[at] = 0.5 * want[at] + (g / n if n else 0.0)
+                # g weights of 1 / n and their sum, each rounded a few times
+                assert np.abs(after[b, h] - want).max() <= 2.0 ** -20 and (np.delete(after[b, h], at) == np.delete(before[b, h], at)).all()
+            rows = [(shared[b], L.any(0), summed_keys(after[b]))] + [(own[b, h], L[h], after[b, h]) for h in range(self.hkv)]
+            for got, live, key in rows:
+                at = np.flatnonzero(live)
+                at = at[at < limit]
+                pick = np.sort(at[np.argsort(key[at], kind="stable")[:n_sel[b]]])
+                assert np.array_equal(got[:pick.size], pick) and (got[pick.size:] == -1).all()
+
+
+@pytest.mark.parametrize("seed", [1, 2, 3])
+def test_positions_follow_tokens_through_random_calls(kvq, seed):
+    """Appends of every shape, repacks, evictions, exclusions, reorders, drops, pages and request ids that
+    change hands, lists: weights reach every live position's score and no other; selections match."""
+    L = Live(kvq, seed)
+    calls = [L.append] * 8 + [L.evict] * 2 + [L.evict_head, L.reorder, L.reorder, L.drop, L.drop, L.again, L.fp]
+    for step_no in range(150):
+        calls[L.rng.integers(len(calls))]()
+        if step_no % 3 == 0:
+            L.check()
