@@ -304,8 +304,9 @@ KVQ_API kv_status_t kv_decode_attn_groups(kv_pool_t* const* pools, int32_t n_poo
  * kv_decode_attn; n_req x num_kv_heads <= 65535.  K, V and the softmax weights
  * pass through binary16 (logits, sums and outputs are accumulated in fp32 and
  * rounded to bf16 once); with KV_DECODE_SIMT everything is fp32.  A list token
- * past binary16's range counts as above; a row of q that is not finite, or whose
- * sums are not, gives a row that is not finite, and KV_ERR_RANGE.  Workspace:
+ * past binary16's range counts as above.  A row of q that is not finite, or whose
+ * greatest logit passes fp32's range (KV_DECODE_SIMT: or whose q . k does), gives
+ * a row that is not finite, and KV_ERR_RANGE.  Workspace:
  * 64 KB per 128 keys and kv head of requests with more than 128 rows (n_new x q
  * heads per kv head), up to 4.3 GB or one kv head of the longest request, and
  * the rows' partial sums; it grows with cudaMalloc, and without memory for it

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) attend_merge_kernel(AttArgs A
   }
 #pragma unroll
   for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, x);
-  const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
+  const float inv = row_inverse(M, L);
   const float r[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
   bool bad = false;
   const int g = A.hq / A.hkv, row = D.row0 + i;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(32 * kTallWarps) attend_merge_tall_kernel(AttA
         }
       }
   }
-  const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);
+  const float inv = row_inverse(M, L);
   const float r[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
   bool bad = false;
   uint32_t h[4];

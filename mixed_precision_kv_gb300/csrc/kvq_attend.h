@@ -69,6 +69,13 @@ __device__ __forceinline__ int att_page(const AttArgs& A, int32_t id, int32_t kv
   blk = A.pool + A.fp4_off + ((size_t)(id - A.nfb) * A.hkv + kvh) * kFp4Block;
   return kClsFp4;
 }
+// 1 / l of a row with maximum m and sum l.  A row that saw nothing (m = -inf, l = 0)
+// is 0, a NaN stays one.  A maximum without a sum: the greatest logit is past
+// fp32's range (above: every weight is 2^(x - inf) = 0; below, where it is held at a
+// lowest value: every weight is 0 too), and the row is not a number.
+__device__ __forceinline__ float row_inverse(float m, float l) {
+  return l > 0.0f ? 1.0f / l : (l == 0.0f && m == -INFINITY ? 0.0f : __int_as_float(0x7FFFFFFF));
+}
 // Offset of channel c in list row t: the 8-channel pieces of a row are stored
 // in the order piece ^ (t & 7).
 __device__ __forceinline__ int att_list_at(int t, int c) { return (((c >> 3) ^ (t & 7)) << 3) | (c & 7); }

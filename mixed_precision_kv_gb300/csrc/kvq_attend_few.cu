@@ -342,9 +342,7 @@ __global__ void __launch_bounds__(kThreads<R>, 1) attend_few_kernel(
             const float mo = S.m[tid], mn = w > 0.95f * kNever ? fmaxf(mo, w) : mo;
             S.m[tid] = mn;
             S.fac[tid] = mo == -INFINITY ? 1.0f : ex2f(mo - mn);
-            // a logit above fp32's range, or all below it so far: the row's weights are not a number
-            const bool past = mn == INFINITY || mn == kLowest;
-            S.nm[tid] = mn == -INFINITY ? kUnseen : (past ? __int_as_float(0x7FFFFFFF) : kHead - mn);
+            S.nm[tid] = mn == -INFINITY ? kUnseen : kHead - mn;
             if (mn == -INFINITY && tid < T.rows) S.unseen = 1u;
           }
           group_stop(false);
@@ -397,16 +395,16 @@ __global__ void __launch_bounds__(kThreads<R>, 1) attend_few_kernel(
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
           if (c + n >= T.rows) break;
-          const float L = __uint_as_float(ls[n]);
-          if (!(L < INFINITY)) bad = 1u;
+          const float m = S.m[c + n], L = __uint_as_float(ls[n]);
+          if (whole && !(L < INFINITY)) bad = 1u;
           if (whole) {
-            const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);   // a NaN stays
+            const float inv = row_inverse(m, L);
             const float v = __uint_as_float(o[n]) * inv;
             if (!(fabsf(v) < INFINITY)) bad = 1u;
             A.out[rows.at(A, u, I.row0 + c + n) + key] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
           } else {
             pp[(size_t)(c + n) * kAttPart + key] = __uint_as_float(o[n]);
-            if (key == 0) *reinterpret_cast<float2*>(pp + (size_t)(c + n) * kAttPart + kHeadDim) = make_float2(S.m[c + n], L);
+            if (key == 0) *reinterpret_cast<float2*>(pp + (size_t)(c + n) * kAttPart + kHeadDim) = make_float2(m, L);
           }
         }
         __syncwarp();

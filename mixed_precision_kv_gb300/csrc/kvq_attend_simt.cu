@@ -75,10 +75,12 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttArgs A, const AttUn
     qs[x / kHeadDim][x % kHeadDim] = i < rows ? bf(A.q[row_at(i) + x % kHeadDim]) : 0.0f;
   }
   float m[kPer], l[kPer], o[kPer][4];
+  bool seen[kPer];   // this lane's keys so far: any that the row sees
 #pragma unroll
   for (int y = 0; y < kPer; ++y) {
     m[y] = -INFINITY;
     l[y] = 0.0f;
+    seen[y] = false;
     o[y][0] = o[y][1] = o[y][2] = o[y][3] = 0.0f;
   }
   // the 32 keys in shared memory; may(y): whether this lane's key is seen by row r0 + kPer w + y
@@ -92,11 +94,13 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttArgs A, const AttUn
         const float4 qv = *reinterpret_cast<const float4*>(&qr[c]);
         s = fmaf(qv.x, kv.x, s); s = fmaf(qv.y, kv.y, s); s = fmaf(qv.z, kv.z, s); s = fmaf(qv.w, kv.w, s);
       }
-      s *= A.scale_log2;
-      const bool see = may(y), odd = see && !(fabsf(s) < INFINITY);
-      // a logit that is not finite makes the row's sum, and so the row, not a number
-      if (__any_sync(0xFFFFFFFFu, odd)) l[y] = __int_as_float(0x7FFFFFFF);
-      s = see && !odd ? s : -INFINITY;
+      const bool see = may(y), whole = fabsf(s) < INFINITY;
+      s = see ? s * A.scale_log2 : -INFINITY;
+      // A row whose greatest logit is past fp32's range, above or below, is not a number, nor is one with a sum
+      // that is not finite.
+      if (__any_sync(0xFFFFFFFFu, see && !(whole && s < INFINITY))) l[y] = __int_as_float(0x7FFFFFFF);
+      if (see) seen[y] = true;
+      s = whole && s < INFINITY ? s : -INFINITY;
       float mx = s;
 #pragma unroll
       for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
@@ -173,7 +177,8 @@ __global__ void __launch_bounds__(256) attend_simt_kernel(AttArgs A, const AttUn
 #pragma unroll
   for (int y = 0; y < kPer; ++y) {
     const int i = r0 + kPer * w + y;
-    if (i >= rows) continue;
+    if (i >= rows) continue;   // (warp-uniform)
+    if (__any_sync(0xFFFFFFFFu, seen[y]) && m[y] == -INFINITY) l[y] = __int_as_float(0x7FFFFFFF);
     const float inv = l[y] > 0.0f ? 1.0f / l[y] : (l[y] == 0.0f ? 0.0f : l[y]);   // a NaN sum stays NaN
     uint16_t* op = A.out + row_at(i) + 4 * lane;
 #pragma unroll

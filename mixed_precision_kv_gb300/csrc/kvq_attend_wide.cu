@@ -398,8 +398,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
           const float corr = grow ? ex2f(m - mx) : 1.0f;   // m = -inf: 0
           if (grow) m = mx;
           l *= corr;
-          // a logit above fp32's range, or all below it so far: the row's sum is not a number
-          if (m == INFINITY || m == kLowest) l = __int_as_float(0x7FFFFFFF);
           if (any) {
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
@@ -449,9 +447,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
         tm_fence_after();
       }
       const bool whole = I.part < 0;
-      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // a NaN stays
+      const float inv = row_inverse(m, l);
       // an infinite sum or a NaN: a value of the cache past binary16 (or of q)
-      if (valid && !(l < INFINITY)) bad = 1u;
+      if (whole && valid && !(l < INFINITY)) bad = 1u;
       float4* const pp = reinterpret_cast<float4*>(part + (size_t)(whole ? 0 : I.part + x) * 128 * kAttPart) + rt;
       float check = 0.0f;   // becomes a NaN if any element is not finite
 #pragma unroll 1

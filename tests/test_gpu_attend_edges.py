@@ -81,6 +81,31 @@ def test_logits_past_fp32(kvq, impl, T, sign):
 
 
 @pytest.mark.parametrize("impl", IMPLS)
+@pytest.mark.parametrize("n,T", [(70, 3), (6000, 3), (70, 130), (6000, 130)])
+def test_logits_far_below_the_greatest(kvq, impl, n, T):
+    """Cached keys whose logits all pass fp32's range downwards weigh nothing beside a new token with a
+    logit of 0, whatever pieces the work is cut into; without it, the row is not finite."""
+    P = Pool(kvq, 1, [[]], seed=T, chunk=1000)
+    P.pool.destroy()
+    pages = n // 32 + 64
+    pool = kvq.KVPool(1, pages, pages, 1, pages)
+    rid = pool.open()
+    k = torch.full((n, 1, 128), -1.0, device="cuda").bfloat16()
+    pool.append(k, rand((n, 1, 128), P.gen), np.full(n, rid, np.int32), mixed(n, 1))
+    pool.set_decode_impl(impl)
+    q = torch.ones(T, 4, 128, device="cuda").bfloat16()
+    kn, vn = torch.zeros(T, 1, 128, device="cuda").bfloat16(), rand((T, 1, 128), P.gen)
+    kn[1:] = -1.0
+    out = pool.attend(q, [rid], [T], 2.0 ** 126, kn, vn)
+    pool.sync()
+    assert torch.equal(out, vn[:1].expand(T, 4, 128))
+    kn[0] = -1.0
+    out = pool.attend(q, [rid], [T], 2.0 ** 126, kn, vn)
+    range_error(kvq, pool)
+    assert not torch.isfinite(out.float()).any()
+
+
+@pytest.mark.parametrize("impl", IMPLS)
 @pytest.mark.parametrize("T", [2, 130])
 def test_list_tokens_out_of_range(kvq, impl, T):
     """A list token past binary16's range (or not a number) is used as 0 there and reported."""
