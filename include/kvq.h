@@ -396,7 +396,8 @@ KVQ_API kv_status_t kv_export_request(kv_pool_t* pool, int32_t req_id, int32_t* 
                               uint32_t* live, uint8_t* k_codes, uint8_t* v_codes, uint16_t* k_meta,
                               uint16_t* v_meta);
 
-/* Algorithmic bytes and split count of the most recent kv_decode_attn call:
+/* Algorithmic bytes and split count of the most recent kv_decode_attn or
+ * kv_decode_attn_scored call (without the scored call's logits and scores):
  * codes + scale/zero of every page block read (partial INT4, INT3 and FP4
  * pages count their filled prefix: 160, 128 and 144 bytes per token and kv
  * head), 8 bytes per table entry, q (bf16) and out (fp32), and the bf16 K and

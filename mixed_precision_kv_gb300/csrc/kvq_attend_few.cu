@@ -26,7 +26,7 @@
 // 52 % of the issue slots, against 520 (INT2) to 870 cycles (INT4) that its bytes take
 // from HBM and 600 of MMAs at R = 64; two stages of K and V are all that TMEM holds
 // beside S and O.  24 requests with 1 to 7 new tokens over 1K to 32K, 32 q on 8 kv
-// heads: 283 us, 1.4 TB/s; a tree of 31 for 8 requests over 32K: 381 us.  Slower: K
+// heads: 285 us, 1.4 TB/s; a tree of 31 for 8 requests over 32K: 381 us.  Slower: K
 // and V by the same sixteen warps in turn, one code path at a time (drafts + 10 %);
 // softmax warps that skip a half without rows (+ 4 %).
 #include <algorithm>

@@ -158,7 +158,7 @@ __device__ __forceinline__ void or_in_cluster(uint32_t* p, uint32_t rank, uint32
 //   two words); keys; radix selection by digits of 11 bits, the CTAs' histograms
 //   added up through distributed shared memory; an ordered listing.
 // Bound by the scores' bytes for long rows, by a dozen barriers for short ones.
-// 16 x 100K positions, 8 heads summed: 68 us, of which the eligible positions and the
+// 16 x 100K positions, 8 heads summed: 66 us, of which the eligible positions and the
 // keys take a third each; 380 with one CTA per row that reads its keys once per digit.
 constexpr int kSelThreads = 512;            // (1024, and no limit of two CTAs per SM below: 64 rows of 20K to 32K 73 us, 38 so)
 constexpr int kSelStored = 48 * 1024;      // positions per CTA whose keys fit its shared memory
