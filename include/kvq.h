@@ -62,7 +62,7 @@ typedef enum {
   KV_OK = 0,
   KV_ERR_INVALID_ARG = 1,     /* bad argument or size; nothing changed */
   KV_ERR_OOM = 2,             /* pool pages, table slots or request slots exhausted; nothing changed */
-  KV_ERR_RANGE = 3,           /* an appended K/V value was NaN, Inf or |x| > 65504 */
+  KV_ERR_RANGE = 3,           /* an appended K/V value was NaN, Inf or |x| > 65504, or a position not in its table */
   KV_ERR_CUDA = 4,            /* a CUDA runtime call failed */
   KV_ERR_DEVICE_TIMEOUT = 5,  /* a bounded device-side wait gave up */
   KV_ERR_STATE = 6            /* call not valid in the pool's current state */
@@ -132,6 +132,69 @@ KVQ_API kv_status_t kv_request_close(kv_pool_t* pool, int32_t req_id);
  * request's table entries returns KV_ERR_OOM, also with nothing changed. */
 KVQ_API kv_status_t kv_append_quant(kv_pool_t* pool, const void* k, const void* v, const int32_t* req_ids,
                             const uint8_t* bits, int64_t n_tok, void* stream);
+
+/* Rotary positions.  Frequency f of rot_dim / 2 turns one pair (a, b) of a
+ * head's channels, (f, f + rot_dim / 2) or, interleaved, (2 f, 2 f + 1), into
+ *     (a cos - b sin, b cos + a sin)
+ * with the cosine and sine of the table's row at the token's position on f's
+ * axis; channels from rot_dim on pass.  Several axes (time, height, width of an
+ * image or video) give a token one position each, and every frequency takes one
+ * of them.  Products and sums are rounded to fp32 one by one, the result once to
+ * bf16. */
+typedef struct {
+  const float* cos_sin;   /* device, fp32 [rows][rot_dim], 16-byte aligned: the frequencies' cosines, then their sines */
+  int64_t rows;           /* positions are [0, rows), rows <= 2^31 - 1 */
+  int32_t rot_dim;        /* a multiple of 16 in [16, 128] */
+  int32_t interleaved;    /* which channels pair */
+  int32_t n_axes;         /* 1 to 4 */
+  const uint8_t* axis;    /* host [rot_dim / 2]: each frequency's axis; NULL (one axis only): all 0 */
+} kv_rope_t;
+
+/* Rotate rows of q and of k in one launch.
+ *   pos      device, int32 [n_axes][pos_stride], pos_stride >= n_tok (any with
+ *            one axis): the tokens' positions.  One outside the table is taken as
+ *            0 and makes kv_pool_sync() return KV_ERR_RANGE.
+ *   q, k     device, bf16: token t's head h at t * stride + h * 128 (strides in
+ *            elements, so slices of a projection's output need no copy); k_heads
+ *            0 with NULL k: q alone.  q_heads and k_heads <= 65535.
+ *   q_out, k_out  device, bf16, laid out by their own strides (at least heads *
+ *            128); may be q and k themselves with their strides, and must not
+ *            overlap them otherwise
+ * 2-byte alignment suffices; pointers aligned to 16 bytes and strides that are
+ * multiples of 8 are faster.  The call reads nothing of the pool and is ordered by
+ * `stream` alone; it may be captured into a graph. */
+KVQ_API kv_status_t kv_rotate(kv_pool_t* pool, const kv_rope_t* rope, const int32_t* pos, int64_t pos_stride, int64_t n_tok,
+                              const void* q, int32_t q_heads, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                              const void* k, int32_t k_heads, int64_t k_stride, void* k_out, int64_t k_out_stride,
+                              void* stream);
+
+/* kv_append_quant with K rotated on its way into the pages: the same pages and
+ * codes as kv_append_quant of the keys that kv_rotate returns, without the rows
+ * written and read in between.
+ *   pos      as in kv_rotate, one column per token of the call; positions are the
+ *            caller's and need not be the tokens' places in the request
+ *   k, v     device, bf16: token t's kv head h at t * stride + h * 128 (elements);
+ *            8-byte aligned, strides multiples of 4 (16 bytes and 8: the faster
+ *            kernels of large calls)
+ * The other arguments and the rules are kv_append_quant's; values are checked
+ * after the rotation. */
+KVQ_API kv_status_t kv_append_rotated(kv_pool_t* pool, const kv_rope_t* rope, const int32_t* pos, int64_t pos_stride,
+                                      const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                      const int32_t* req_ids, const uint8_t* bits, int64_t n_tok, void* stream);
+
+/* Cached tokens' values by token position, dequantized: code * scale + zero in
+ * fp32, rounded once to bf16 (fp32 != 0: not rounded).
+ *   req_ids  host, int32 [n_req], n_req <= 65535; a request may be listed twice
+ *   first, n_tok  host, int64 [n_req]: positions [first, first + n_tok) of the request
+ *   k, v     device, [sum of n_tok][num_kv_heads][128], requests one after the
+ *            other; 16-byte aligned; either may be NULL
+ * Evicted tokens, tokens of dropped pages and, for the head, excluded ones are
+ * rows of zeros.  Full-precision list tokens have no position and are not read.
+ * The first call puts the slots' positions on the device (128 bytes per page of
+ * the pool; KV_ERR_OOM without memory for it); on a stream that is being captured
+ * it is KV_ERR_STATE. */
+KVQ_API kv_status_t kv_read_tokens(kv_pool_t* pool, const int32_t* req_ids, const int64_t* first, const int64_t* n_tok,
+                                   int32_t n_req, int32_t fp32, void* k, void* v, void* stream);
 
 /* Phase-1 reorder (TriAxialKV key design 4): stable partition of each listed
  * request's table so INT2 entries precede INT4 entries; with INT3 or FP4

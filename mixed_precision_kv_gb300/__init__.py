@@ -28,7 +28,8 @@ EXPORTED = ["kv_pool_create", "kv_pool_destroy", "kv_request_open", "kv_request_
             "kv_request_info", "kv_export_request", "kv_last_decode_stats", "kv_pool_launch_count", "kv_alloc_bits",
             "kv_last_error", "kv_decode_attn_noalloc", "kv_decode_timing", "kv_evict_slots_head", "kv_fp_configure",
             "kv_fp_append", "kv_fp_drop", "kv_fp_count", "kv_set_wait_limit", "kv_drop_dead_pages",
-            "kv_decode_attn_groups", "kv_alloc_bits3", "kv_attend", "kv_decode_attn_scored", "kv_select_lowest"]
+            "kv_decode_attn_groups", "kv_alloc_bits3", "kv_attend", "kv_decode_attn_scored", "kv_select_lowest",
+            "kv_rotate", "kv_append_rotated", "kv_read_tokens"]
 
 _P = ctypes.c_void_p
 _I32, _I64 = ctypes.c_int32, ctypes.c_int64
@@ -41,6 +42,11 @@ class KVConfig(ctypes.Structure):
                 ("group", ctypes.c_int32), ("n_int2_pages", ctypes.c_int64), ("n_int4_pages", ctypes.c_int64),
                 ("max_requests", ctypes.c_int32), ("max_pages_per_request", ctypes.c_int32),
                 ("device", ctypes.c_int32), ("n_int3_pages", ctypes.c_int64), ("n_fp4_pages", ctypes.c_int64)]
+
+
+class KVRope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("rows", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("axis", ctypes.c_void_p)]
 
 
 class KVError(RuntimeError):
@@ -78,6 +84,9 @@ def load_library(path: str = LIB_PATH):
             "kv_attend": [_P, _P, _P, _P, _P, _P, _P, _I32, _I32, ctypes.c_float, _P, _P],
             "kv_decode_attn_scored": [_P, _P, _P, _I32, _I32, ctypes.c_float, ctypes.c_float, _P, _I64, _P, _P],
             "kv_select_lowest": [_P, _P, _I64, _P, _P, _I32, _I64, _I32, _P, _I64, _P],
+            "kv_rotate": [_P, _P, _P, _I64, _I64, _P, _I32, _I64, _P, _I64, _P, _I32, _I64, _P, _I64, _P],
+            "kv_append_rotated": [_P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P],
+            "kv_read_tokens": [_P, _P, _P, _P, _I32, _I32, _P, _P, _P],
             "kv_set_decode_impl": [_P, _I32],
             "kv_set_wait_limit": [_P, _I64],
             "kv_pool_sync": [_P],
@@ -172,6 +181,28 @@ def alloc_bits3(N, D2, D3, D4, budget):
     return out
 
 
+class Rope:
+    """A rotation of q and k by position (kv_rope_t): cos_sin, fp32 CUDA [positions][R], the cosines of
+    R / 2 frequencies, then their sines; interleaved: channels (2 f, 2 f + 1) pair instead of
+    (f, f + R / 2); axis: host sequence [R / 2], each frequency's position axis (one axis: None)."""
+
+    def __init__(self, cos_sin, axis=None, interleaved=False):
+        torch = _torch_mod()
+        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_cuda or \
+                not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous fp32 CUDA tensor [positions][rot_dim]")
+        rows, rot = cos_sin.shape
+        if axis is not None:
+            axis = np.asarray(axis)
+            if axis.shape != (rot // 2,) or (axis.size and (axis.min() < 0 or axis.max() > 3)):
+                raise ValueError("axis must hold rot_dim / 2 values in [0, 3]")
+            axis = _np(axis, np.uint8)
+        self.cos_sin, self.axis = cos_sin, axis
+        self.n_axes = int(axis.max()) + 1 if axis is not None and axis.size else 1
+        self._c = KVRope(cos_sin.data_ptr(), rows, rot, int(bool(interleaved)), self.n_axes, _ptr(axis))
+        self._ref = ctypes.addressof(self._c)
+
+
 class KVPool:
     """A paged INT2/INT4 pool on one GPU (see include/kvq.h for every call's contract)."""
 
@@ -234,6 +265,102 @@ class KVPool:
                 t.shape != (n, self.num_kv_heads, HEAD_DIM) or not t.is_contiguous():
             raise ValueError(f"expected a contiguous bf16 tensor [{n}][{self.num_kv_heads}][128] on the pool's "
                              f"device")
+
+    def _positions(self, rope, positions, n):
+        torch = _torch_mod()
+        if not self._on_pool_device(rope.cos_sin):
+            raise ValueError("the rotation's table must be on the pool's device")
+        if positions.dtype is not torch.int32 or not self._on_pool_device(positions) or positions.dim() not in (1, 2) or \
+                positions.shape[-1] != n or (1 if positions.dim() == 1 else positions.shape[0]) < rope.n_axes or \
+                (n > 1 and positions.stride(-1) != 1):
+            raise ValueError(f"positions must be an int32 tensor [{n}], or [axes][{n}] with {rope.n_axes} axes, its rows "
+                             f"contiguous, on the pool's device")
+        if positions.dim() == 2 and rope.n_axes > 1 and positions.stride(0) < n:
+            raise ValueError("the axes' positions must not overlap")
+        return positions.stride(0) if positions.dim() == 2 else n
+
+    def _rows(self, t, what, heads=None):
+        """Checks rows [n][heads][128], a token's heads together; the stride between tokens."""
+        torch = _torch_mod()
+        if t.dtype is not torch.bfloat16 or not self._on_pool_device(t) or t.dim() != 3 or t.shape[2] != HEAD_DIM or \
+                (heads is not None and t.shape[1] != heads) or t.stride(2) != 1 or \
+                (t.shape[1] > 1 and t.stride(1) != HEAD_DIM):
+            raise ValueError(f"{what} must be a bf16 tensor [n][{'heads' if heads is None else heads}][128] on the pool's "
+                             f"device, each token's heads contiguous")
+        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * HEAD_DIM
+
+    def rotate(self, q, rope, positions, k=None, out=None, k_out=None, stream=None):
+        """kv_rotate: q (and k) bf16 CUDA [n][heads][128], turned by the tokens' positions (int32 CUDA
+        [n], or [axes][n]).  A token's heads lie together; tokens may be apart (slices of a
+        projection's output).  Returns the rotated rows (with k: both); out, k_out: where to (q and k
+        themselves: in place)."""
+        n = q.shape[0]
+        qs = self._rows(q, "q")
+        ks = 0
+        if k is not None:
+            ks = self._rows(k, "k")
+            if k.shape[0] != n:
+                raise ValueError("q and k differ in length")
+        elif k_out is not None:
+            raise ValueError("k_out comes with k")
+        ps = self._positions(rope, positions, n)
+        if out is None:
+            out = _empty(q.shape, q.dtype, q.device, stream)
+        if k is not None and k_out is None:
+            k_out = _empty(k.shape, k.dtype, k.device, stream)
+        os_, ko = self._rows(out, "out", q.shape[1]), self._rows(k_out, "k_out", k.shape[1]) if k is not None else 0
+        if out.shape != q.shape or (k is not None and k_out.shape != k.shape):
+            raise ValueError("out and k_out must be shaped like q and k")
+        hk = k.shape[1] if k is not None else 0
+        rc = self._L.kv_rotate(self._h, rope._ref, positions.data_ptr(), ps, n, q.data_ptr(), q.shape[1], qs,
+                               out.data_ptr(), os_, k.data_ptr() if hk else None, hk, ks,
+                               k_out.data_ptr() if hk else None, ko, _stream(stream, self.device))
+        if rc:
+            _check(rc, "kv_rotate")
+        return out if k is None else (out, k_out)
+
+    def append_rotated(self, k, v, req_ids, bits, rope, positions, stream=None):
+        """kv_append_rotated: append() with k turned by the tokens' positions on the way (see rotate();
+        k and v as its rows)."""
+        req_ids = _np(req_ids, np.int32)
+        bits = _np(bits, np.uint8)
+        n = req_ids.size
+        if bits.size != n:
+            raise ValueError("bits and req_ids differ in length")
+        ks, vs = self._rows(k, "k", self.num_kv_heads), self._rows(v, "v", self.num_kv_heads)
+        if k.shape[0] != n or v.shape[0] != n:
+            raise ValueError("k, v and req_ids differ in length")
+        ps = self._positions(rope, positions, n)
+        rc = self._L.kv_append_rotated(self._h, rope._ref, positions.data_ptr(), ps, k.data_ptr(), ks, v.data_ptr(), vs,
+                                       req_ids.ctypes.data, bits.ctypes.data, n, _stream(stream, self.device))
+        if rc:
+            _check(rc, "kv_append_rotated")
+
+    def read(self, req_ids, first=0, n=None, dtype=None, stream=None):
+        """kv_read_tokens: the values of positions [first, first + n) of each request (n None: to its
+        end), dequantized -> (k, v), CUDA [sum(n)][Hkv][128], bf16 or dtype=torch.float32; evicted
+        tokens are zeros.  first, n: ints or host sequences [requests]."""
+        torch = _torch_mod()
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("dtype must be torch.bfloat16 or torch.float32")
+        req_ids = np.atleast_1d(_np(req_ids, np.int32))
+        first = np.full(req_ids.size, int(first), np.int64) if np.ndim(first) == 0 else _np(first, np.int64)
+        if n is None:
+            n = np.array([self.info(r)[1] for r in req_ids], np.int64).reshape(req_ids.size) - first
+        else:
+            n = np.full(req_ids.size, int(n), np.int64) if np.ndim(n) == 0 else _np(n, np.int64)
+        if req_ids.ndim != 1 or first.shape != req_ids.shape or n.shape != req_ids.shape:
+            raise ValueError("req_ids, first and n must be sequences of one length")
+        if n.size and int(n.min()) < 0:
+            raise ValueError("n must not be negative")
+        device = torch.device("cuda", self.device)
+        k, v = (_empty((int(n.sum()), self.num_kv_heads, HEAD_DIM), dtype, device, stream) for _ in range(2))
+        rc = self._L.kv_read_tokens(self._h, req_ids.ctypes.data, first.ctypes.data, n.ctypes.data, req_ids.size,
+                                    int(dtype is torch.float32), k.data_ptr(), v.data_ptr(), _stream(stream, self.device))
+        if rc:
+            _check(rc, "kv_read_tokens")
+        return k, v
 
     def reorder(self, req_ids, stream=None):
         req_ids = _np(req_ids, np.int32)

@@ -72,6 +72,10 @@ kv_status_t refuse_capture(const char* what, cudaStream_t s);
 // Bring the slots' token positions on the device (P->d_pos) up to date.
 kv_status_t sync_positions(kv_pool* P, cudaStream_t s);
 
+// kv_append_quant, and with P->rope kv_append_rotated (`what`: the name in messages).
+kv_status_t append_tokens(kv_pool* P, const char* what, const void* k, const void* v, const int32_t* req_ids,
+                          const uint8_t* bits, int64_t n_tok, void* stream);
+
 // The split plan of a decode over a batch, on the device (kept while it fits).
 kv_status_t build_plan(kv_pool* P, const int32_t* req_ids, int32_t batch, int32_t hq, int32_t impl, cudaStream_t s);
 

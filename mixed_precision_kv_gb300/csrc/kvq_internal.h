@@ -12,6 +12,7 @@
 
 #include "../../include/kvq.h"
 #include "kvq_layout.cuh"
+#include "kvq_rope.h"
 
 namespace kvq {
 
@@ -224,6 +225,7 @@ struct NoFillAlloc : std::allocator<T> {
 
 struct Request {
   bool open = false;
+  bool dropped = false;             // some positions' pages have been dropped
   std::vector<int32_t> table;       // page ids in table order
   int32_t tail4 = -1, tail3 = -1, tailf = -1, staging = -1;
   std::vector<uint32_t, NoFillAlloc<uint32_t>> loc;   // token position -> page_id << 5 | slot
@@ -308,6 +310,7 @@ struct kv_pool {
   kvq::DevBuf partials;               // decode split partials
   kvq::DevBuf frags;                  // per-unit q operands of the tensor-core scan
   kvq::DevBuf logits;                 // scored decode: logits of the batch's pages, then each row's (maximum, 1 / sum)
+  kvq::DevBuf read;                   // reading tokens back: the requests of a call of many
   kvq::DevBuf select;                 // lowest-score selection: the rows of a call of many requests
   kvq::DevBuf attend;                 // attention of new tokens: plan, then partials
   kvq::DevBuf attend_tiles;           // ... many rows per unit: operand tiles, then their live words
@@ -374,6 +377,7 @@ struct kv_pool {
   int64_t timed_calls = 0;            // decode calls recorded since timing started
   std::vector<cudaEvent_t> tev;       // ring of [before scan, after scan, after merge] per call
   cudaEvent_t merge_event = nullptr;  // recorded by the launchers between scan and merge when timing
+  const kvq::RopeArgs* rope = nullptr;   // the running append rotates K by this (its launchers read it)
   int64_t first_wait_spins = -1;      // kv_set_wait_limit: bound of the scans' first copy wait (-1: normal)
 };
 

@@ -505,6 +505,7 @@ kv_status_t kv_pool_destroy(kv_pool_t* P) {
   cudaFree(P->fp_scratch.ptr);
   cudaFree(P->logits.ptr);
   cudaFree(P->select.ptr);
+  cudaFree(P->read.ptr);
   cudaFree(P->attend.ptr);
   cudaFree(P->attend_tiles.ptr);
   cudaFree(P->d_pos);
@@ -589,20 +590,19 @@ kv_status_t kv_pool_sync(kv_pool_t* P) {
   KV_CUDA(cudaMemcpy(&st, P->d_status, 4, cudaMemcpyDeviceToHost));
   if (st) KV_CUDA(cudaMemset(P->d_status, 0, 4));
   if (st & kStatusTimeout) return fail(KV_ERR_DEVICE_TIMEOUT, "kv_pool_sync: a bounded device wait expired");
-  if (st & kStatusRange) return fail(KV_ERR_RANGE, "kv_pool_sync: an appended value was NaN, Inf or |x| > 65504");
+  if (st & kStatusRange)
+    return fail(KV_ERR_RANGE, "kv_pool_sync: an appended value was NaN, Inf or |x| > 65504, or a position is not in its table");
   return KV_OK;
 }
 
 }  // extern "C"
 
-extern "C" {
-
-kv_status_t kv_append_quant(kv_pool_t* P, const void* k, const void* v, const int32_t* req_ids,
-                            const uint8_t* bits, int64_t n_tok, void* stream) {
-  if (!P) return fail(KV_ERR_INVALID_ARG, "kv_append_quant: null pool");
-  if (n_tok < 0 || n_tok > INT32_MAX) return fail(KV_ERR_INVALID_ARG, "kv_append_quant: bad n_tok %lld", (long long)n_tok);
+kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, const void* v, const int32_t* req_ids,
+                               const uint8_t* bits, int64_t n_tok, void* stream) {
+  if (!P) return fail(KV_ERR_INVALID_ARG, "%s: null pool", what);
+  if (n_tok < 0 || n_tok > INT32_MAX) return fail(KV_ERR_INVALID_ARG, "%s: bad n_tok %lld", what, (long long)n_tok);
   if (n_tok == 0) return KV_OK;
-  if (!k || !v || !req_ids || !bits) return fail(KV_ERR_INVALID_ARG, "kv_append_quant: null pointer");
+  if (!k || !v || !req_ids || !bits) return fail(KV_ERR_INVALID_ARG, "%s: null pointer", what);
   // Per-request state of this call, found through a pool-wide slot index.
   struct CallReq {
     int32_t r;
@@ -744,14 +744,14 @@ kv_status_t kv_append_quant(kv_pool_t* P, const void* k, const void* v, const in
       need4 += opens;
       need2 += u.ndirect + (u.repack ? 1 : 0);
       if ((int64_t)R.table.size() + opens > P->cfg.max_pages_per_request)
-        return fail(KV_ERR_OOM, "kv_append_quant: request %d would exceed %d table entries", u.r,
+        return fail(KV_ERR_OOM, "%s: request %d would exceed %d table entries", what, u.r,
                     P->cfg.max_pages_per_request);
       if ((int64_t)R.loc.size() + u.n > kMaxPositions)
-        return fail(KV_ERR_INVALID_ARG, "kv_append_quant: request %d would exceed %lld token positions", u.r,
+        return fail(KV_ERR_INVALID_ARG, "%s: request %d would exceed %lld token positions", what, u.r,
                     (long long)kMaxPositions);
     }
     if (need4 > (int64_t)P->free4.size() || need2 > (int64_t)P->free2.size())
-      return fail(KV_ERR_OOM, "kv_append_quant: needs %lld INT4 + %lld INT2 pages, %zu + %zu free", (long long)need4,
+      return fail(KV_ERR_OOM, "%s: needs %lld INT4 + %lld INT2 pages, %zu + %zu free", what, (long long)need4,
                   (long long)need2, P->free4.size(), P->free2.size());
   }
   // Dry run: pages taken and table growth, so that OOM changes nothing.
@@ -759,10 +759,9 @@ kv_status_t kv_append_quant(kv_pool_t* P, const void* k, const void* v, const in
     int64_t need4 = 0, need3 = 0, needf = 0, need2 = 0;
     for (int64_t t = 0; t < n_tok; ++t) {
       if (!req_ok(P, req_ids[t]))
-        return fail(KV_ERR_INVALID_ARG, "kv_append_quant: token %lld: request %d not open", (long long)t, req_ids[t]);
+        return fail(KV_ERR_INVALID_ARG, "%s: token %lld: request %d not open", what, (long long)t, req_ids[t]);
       if ((bits[t] < 2 || bits[t] > 4) && bits[t] != KV_WIDTH_FP4)
-        return fail(KV_ERR_INVALID_ARG, "kv_append_quant: token %lld: bits must be 2, 3, 4 or KV_WIDTH_FP4",
-                    (long long)t);
+        return fail(KV_ERR_INVALID_ARG, "%s: token %lld: bits must be 2, 3, 4 or KV_WIDTH_FP4", what, (long long)t);
       CallReq& c = slot_of(req_ids[t]);
       if (bits[t] == 4) {
         if (!c.tail || c.tailfill == kPage) { ++need4; ++c.tablen; c.tail = true; c.tailfill = 0; }
@@ -779,18 +778,18 @@ kv_status_t kv_append_quant(kv_pool_t* P, const void* k, const void* v, const in
         if (++c.stagfill == kPage) { ++need2; c.stag = false; }
       }
       if (c.tablen > P->cfg.max_pages_per_request)
-        return fail(KV_ERR_OOM, "kv_append_quant: request %d would exceed %d table entries", req_ids[t], P->cfg.max_pages_per_request);
+        return fail(KV_ERR_OOM, "%s: request %d would exceed %d table entries", what, req_ids[t], P->cfg.max_pages_per_request);
       if (++c.npos > kMaxPositions)
-        return fail(KV_ERR_INVALID_ARG, "kv_append_quant: request %d would exceed %lld token positions", req_ids[t],
+        return fail(KV_ERR_INVALID_ARG, "%s: request %d would exceed %lld token positions", what, req_ids[t],
                     (long long)kMaxPositions);
     }
     if (need4 > (int64_t)P->free4.size() || need2 > (int64_t)P->free2.size())
-      return fail(KV_ERR_OOM, "kv_append_quant: needs %lld INT4 + %lld INT2 pages, %zu + %zu free", (long long)need4,
+      return fail(KV_ERR_OOM, "%s: needs %lld INT4 + %lld INT2 pages, %zu + %zu free", what, (long long)need4,
                   (long long)need2, P->free4.size(), P->free2.size());
     if (need3 > (int64_t)P->free3.size())
-      return fail(KV_ERR_OOM, "kv_append_quant: needs %lld INT3 pages, %zu free", (long long)need3, P->free3.size());
+      return fail(KV_ERR_OOM, "%s: needs %lld INT3 pages, %zu free", what, (long long)need3, P->free3.size());
     if (needf > (int64_t)P->freef.size())
-      return fail(KV_ERR_OOM, "kv_append_quant: needs %lld FP4 pages, %zu free", (long long)needf, P->freef.size());
+      return fail(KV_ERR_OOM, "%s: needs %lld FP4 pages, %zu free", what, (long long)needf, P->freef.size());
   }
   // room for this call's tokens in each position map; growth is geometric
   // (reserving just the new size on every call would copy the whole map)
@@ -1097,7 +1096,8 @@ kv_status_t kv_append_quant(kv_pool_t* P, const void* k, const void* v, const in
   const bool small = n_i3 + n_f4 == 0 && jobs.size() <= (size_t)SmallAppend::kMaxJobs && off <= SmallAppend::kMaxToks;
   // Large calls with 16-byte aligned K/V rows: fresh pages filled with 32
   // tokens go to the bulk INT4 kernel, direct groups to the bulk INT2 kernel.
-  const bool aligned = ((uintptr_t)k % 16 == 0) && ((uintptr_t)v % 16 == 0);
+  const bool aligned = (uintptr_t)k % 16 == 0 && (uintptr_t)v % 16 == 0 &&
+                       (!P->rope || (P->rope->k_stride % 8 == 0 && P->rope->v_stride % 8 == 0));
   const bool use_bulk = !small && aligned;
   size_t n_full = 0;
   const auto jobs4_end = jobs.end() - (ptrdiff_t)(n_i3 + n_f4);
@@ -1164,6 +1164,13 @@ kv_status_t kv_append_quant(kv_pool_t* P, const void* k, const void* v, const in
   KV_CUDA(launch_repack(P, (const RepackJob*)(base + o_rep), (int)repacks.size(), s));
   KV_CUDA(launch_scatter(P, (const TableUpd*)(base + o_upd), (int)upd.size(), s));
   return KV_OK;
+}
+
+extern "C" {
+
+kv_status_t kv_append_quant(kv_pool_t* P, const void* k, const void* v, const int32_t* req_ids,
+                            const uint8_t* bits, int64_t n_tok, void* stream) {
+  return append_tokens(P, "kv_append_quant", k, v, req_ids, bits, n_tok, stream);
 }
 
 kv_status_t kv_reorder_pages(kv_pool_t* P, const int32_t* req_ids, int32_t n_req, void* stream) {
@@ -1329,6 +1336,7 @@ kv_status_t kv_drop_dead_pages(kv_pool_t* P, const int32_t* req_ids, int32_t n_r
         const int32_t pp = P->pos[(size_t)id * kPage + sl];
         if (pp >= 0 && (size_t)pp < R.loc.size()) R.loc[(size_t)pp] = kDroppedLoc;
       }
+      R.dropped = true;
       if (R.tail4 == id) R.tail4 = -1;
       if (R.tail3 == id) R.tail3 = -1;
       if (R.tailf == id) R.tailf = -1;

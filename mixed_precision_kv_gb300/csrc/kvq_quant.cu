@@ -13,12 +13,31 @@
 #include <cuda_fp16.h>
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "kvq_internal.h"
 
 namespace kvq {
 namespace {
 
 constexpr int kThreads = 128;
+
+// Every kernel that reads K rows comes in two forms: as they are, or rotated on the
+// way (kRope: RopeArgs, which also gives the distance between tokens' rows).
+struct NoRope {};
+template <bool kRope>
+using RopeParam = std::conditional_t<kRope, RopeArgs, NoRope>;
+// elements from a token's K (V) rows to the next token's
+template <bool kRope>
+__device__ __forceinline__ size_t k_step(const RopeParam<kRope>& R, int hkv) {
+  if constexpr (kRope) return (size_t)R.k_stride;
+  else return (size_t)hkv * kHeadDim;
+}
+template <bool kRope>
+__device__ __forceinline__ size_t v_step(const RopeParam<kRope>& R, int hkv) {
+  if constexpr (kRope) return (size_t)R.v_stride;
+  else return (size_t)hkv * kHeadDim;
+}
 
 __device__ __forceinline__ bool out_of_range(float x) { return !(fabsf(x) <= 65504.0f); }
 
@@ -89,10 +108,27 @@ __device__ __forceinline__ void or_bits(uint8_t* img, int byte_off, int shift, u
 struct RawRows {
   uint2 kr, vr;
 };
-__device__ __forceinline__ RawRows load_rows(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
-                                             int t, int h, int hkv) {
-  const size_t row = ((size_t)t * hkv + h) * kHeadDim + 4 * (threadIdx.x & 31);
-  return RawRows{*reinterpret_cast<const uint2*>(k + row), *reinterpret_cast<const uint2*>(v + row)};
+// With kRope they come with the lane's factors, and turned() gives K rotated (rounded
+// to bf16, as a key that came rotated would be).
+template <bool kRope>
+struct Rows {
+  RawRows raw;
+  std::conditional_t<kRope, RopeLane, NoRope> lane;
+};
+template <bool kRope>
+__device__ __forceinline__ Rows<kRope> load_rows(const RopeParam<kRope>& R, const __nv_bfloat16* __restrict__ k,
+                                                 const __nv_bfloat16* __restrict__ v, int t, int h, int hkv, bool& bad) {
+  const size_t at = (size_t)h * kHeadDim + 4 * (threadIdx.x & 31);
+  Rows<kRope> r;
+  r.raw = RawRows{*reinterpret_cast<const uint2*>(k + (size_t)t * k_step<kRope>(R, hkv) + at),
+                  *reinterpret_cast<const uint2*>(v + (size_t)t * v_step<kRope>(R, hkv) + at)};
+  if constexpr (kRope) r.lane = rope_lane(R, t, bad);
+  return r;
+}
+template <bool kRope>
+__device__ __forceinline__ RawRows turned(const RopeParam<kRope>& R, const Rows<kRope>& r) {
+  if constexpr (kRope) return RawRows{rope_lane_turn(R, r.raw.kr, r.lane), r.raw.vr};
+  else return r.raw;
 }
 
 __device__ __forceinline__ bool quantize_rows(uint8_t* img, const RawRows& rr, int slot, float& vmax,
@@ -149,8 +185,8 @@ __device__ __forceinline__ bool quantize_rows(uint8_t* img, const RawRows& rr, i
 // The tokens j = warp, warp + W, ... < n of a job (W = warps per CTA), each
 // into slot first + j: their indices are read at once (lane q holds the q-th)
 // and the next token's rows are loaded while the current one is quantized.
-template <int W>
-__device__ __forceinline__ bool quantize_tokens(uint8_t* img, const __nv_bfloat16* __restrict__ k,
+template <int W, bool kRope>
+__device__ __forceinline__ bool quantize_tokens(const RopeParam<kRope>& R, uint8_t* img, const __nv_bfloat16* __restrict__ k,
                                                 const __nv_bfloat16* __restrict__ v,
                                                 const int32_t* __restrict__ tk, int n, int first, int h, int hkv,
                                                 float& vmax, uint8_t* vcodes) {
@@ -159,11 +195,11 @@ __device__ __forceinline__ bool quantize_tokens(uint8_t* img, const __nv_bfloat1
   const int t_l = lane < mine ? tk[warp + W * lane] : 0;
   bool bad = false;
   if (mine == 0) return bad;
-  RawRows cur = load_rows(k, v, __shfl_sync(0xFFFFFFFFu, t_l, 0), h, hkv);
+  Rows<kRope> cur = load_rows<kRope>(R, k, v, __shfl_sync(0xFFFFFFFFu, t_l, 0), h, hkv, bad);
   for (int q = 0; q < mine; ++q) {
-    RawRows nxt = cur;
-    if (q + 1 < mine) nxt = load_rows(k, v, __shfl_sync(0xFFFFFFFFu, t_l, q + 1), h, hkv);
-    bad |= quantize_rows(img, cur, first + warp + W * q, vmax, vcodes);
+    Rows<kRope> nxt = cur;
+    if (q + 1 < mine) nxt = load_rows<kRope>(R, k, v, __shfl_sync(0xFFFFFFFFu, t_l, q + 1), h, hkv, bad);
+    bad |= quantize_rows(img, turned<kRope>(R, cur), first + warp + W * q, vmax, vcodes);
     cur = nxt;
   }
   return bad;
@@ -196,12 +232,12 @@ __device__ __forceinline__ void pack_i4v(uint8_t* __restrict__ img, const uint8_
 // atomic OR).  The kv-head-0 CTA also writes the page's table entry and the
 // request's table length, so an append that only fills or adds tail pages
 // needs no separate table update.
-template <bool kByValue>
+template <bool kByValue, bool kRope>
 __global__ void __launch_bounds__(kThreads) append_int4_kernel(
     uint8_t* __restrict__ pool, size_t int4_off, int64_t n2, int hkv, const __nv_bfloat16* __restrict__ k,
     const __nv_bfloat16* __restrict__ v, const AppendJob* __restrict__ jobs, const int32_t* __restrict__ toks,
     Entry* __restrict__ table, int32_t* __restrict__ ntab, uint32_t* __restrict__ status,
-    const __grid_constant__ SmallAppend small) {
+    const __grid_constant__ SmallAppend small, const __grid_constant__ RopeParam<kRope> rope) {
   __shared__ __align__(16) uint8_t img[kInt4Block];
   __shared__ __align__(16) uint8_t vcodes[kPage * kHeadDim];   // V codes of a new page, packed after
   asm volatile("griddepcontrol.wait;" ::: "memory");   // earlier work on the stream (the previous decode) is done
@@ -219,16 +255,16 @@ __global__ void __launch_bounds__(kThreads) append_int4_kernel(
     for (int i = threadIdx.x; i < kPage * kHeadDim / 16; i += kThreads)
       reinterpret_cast<uint4*>(vcodes)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    bad |= quantize_tokens<kThreads / 32>(img, k, v, tk + job.tok_off, job.n_slots, job.first_slot, h, hkv, vmax,
-                                          vcodes);
+    bad |= quantize_tokens<kThreads / 32, kRope>(rope, img, k, v, tk + job.tok_off, job.n_slots, job.first_slot, h, hkv,
+                                                 vmax, vcodes);
     __syncthreads();
     pack_i4v(img, vcodes);
     __syncthreads();
     uint4* out4 = reinterpret_cast<uint4*>(blk);
     for (int i = threadIdx.x; i < kInt4Block / 16; i += kThreads) out4[i] = img4[i];
   } else {
-    bad |= quantize_tokens<kThreads / 32>(blk, k, v, tk + job.tok_off, job.n_slots, job.first_slot, h, hkv, vmax,
-                                          nullptr);
+    bad |= quantize_tokens<kThreads / 32, kRope>(rope, blk, k, v, tk + job.tok_off, job.n_slots, job.first_slot, h, hkv,
+                                                 vmax, nullptr);
   }
   flush_vmax(vmax, status);
   if (bad) atomicOr(status, kStatusRange);
@@ -332,10 +368,12 @@ __device__ __forceinline__ void pack_i3v(uint8_t* __restrict__ img, const uint8_
 // is built in shared memory from zeros and written whole, a page that
 // already holds tokens gets its new slots in place (V bits by atomic OR).
 // Table entry and length as in append_int4_kernel.
+template <bool kRope>
 __global__ void __launch_bounds__(kThreads) append_int3_kernel(
     uint8_t* __restrict__ pool, size_t int3_off, int64_t n3b, int hkv, const __nv_bfloat16* __restrict__ k,
     const __nv_bfloat16* __restrict__ v, const AppendJob* __restrict__ jobs, const int32_t* __restrict__ toks,
-    Entry* __restrict__ table, int32_t* __restrict__ ntab, uint32_t* __restrict__ status) {
+    Entry* __restrict__ table, int32_t* __restrict__ ntab, uint32_t* __restrict__ status,
+    const __grid_constant__ RopeParam<kRope> rope) {
   __shared__ __align__(16) uint8_t img[kInt3Block];
   __shared__ __align__(16) uint8_t vcodes[kPage * kHeadDim];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -356,7 +394,8 @@ __global__ void __launch_bounds__(kThreads) append_int3_kernel(
   bool bad = false;
   float vmax = 0.0f;
   for (int q = warp; q < job.n_slots; q += kThreads / 32)
-    bad |= quantize_rows3(dst, load_rows(k, v, tk[q], h, hkv), job.first_slot + q, vmax, fresh ? vcodes : nullptr);
+    bad |= quantize_rows3(dst, turned<kRope>(rope, load_rows<kRope>(rope, k, v, tk[q], h, hkv, bad)), job.first_slot + q,
+                         vmax, fresh ? vcodes : nullptr);
   if (fresh) {
     __syncthreads();
     pack_i3v(img, vcodes);
@@ -453,10 +492,12 @@ __device__ __forceinline__ void pack_f4v(uint8_t* __restrict__ img, const uint8_
 
 // One CTA per (job, kv head) of FP4 tail pages, a warp per token (as
 // append_int3_kernel).
+template <bool kRope>
 __global__ void __launch_bounds__(kThreads) append_fp4_kernel(
     uint8_t* __restrict__ pool, size_t fp4_off, int64_t nfb, int hkv, const __nv_bfloat16* __restrict__ k,
     const __nv_bfloat16* __restrict__ v, const AppendJob* __restrict__ jobs, const int32_t* __restrict__ toks,
-    Entry* __restrict__ table, int32_t* __restrict__ ntab, uint32_t* __restrict__ status) {
+    Entry* __restrict__ table, int32_t* __restrict__ ntab, uint32_t* __restrict__ status,
+    const __grid_constant__ RopeParam<kRope> rope) {
   __shared__ __align__(16) uint8_t img[kFp4Block];
   __shared__ __align__(16) uint8_t vcodes[kPage * kHeadDim];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -477,7 +518,8 @@ __global__ void __launch_bounds__(kThreads) append_fp4_kernel(
   bool bad = false;
   float vmax = 0.0f;
   for (int q = warp; q < job.n_slots; q += kThreads / 32)
-    bad |= quantize_rows_fp4(dst, load_rows(k, v, tk[q], h, hkv), job.first_slot + q, vmax, fresh ? vcodes : nullptr);
+    bad |= quantize_rows_fp4(dst, turned<kRope>(rope, load_rows<kRope>(rope, k, v, tk[q], h, hkv, bad)), job.first_slot + q,
+                            vmax, fresh ? vcodes : nullptr);
   if (fresh) {
     __syncthreads();
     pack_f4v(img, vcodes);
@@ -620,9 +662,11 @@ __global__ void __launch_bounds__(kThreads) repack_int2_kernel(uint8_t* __restri
 // Every thread waits for the append grid before it exits, so the kernels
 // that follow in stream order (the repack reads staging pages the append
 // kernel fills) see both.
+template <bool kRope>
 __global__ void __launch_bounds__(kThreads) direct_int2_kernel(
     uint8_t* __restrict__ pool, int hkv, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
-    const DirectJob* __restrict__ jobs, const int32_t* __restrict__ toks, uint32_t* __restrict__ status) {
+    const DirectJob* __restrict__ jobs, const int32_t* __restrict__ toks, uint32_t* __restrict__ status,
+    const __grid_constant__ RopeParam<kRope> rope) {
   __shared__ __align__(16) uint8_t img[kInt4Block];
   __shared__ __align__(16) uint8_t dst[kInt2Block];
   __shared__ __align__(16) uint8_t codes[kPage * kHeadDim];
@@ -631,7 +675,7 @@ __global__ void __launch_bounds__(kThreads) direct_int2_kernel(
   bool bad = false;
   float vmax = 0.0f;
   // every slot is written: no zeroing
-  bad |= quantize_tokens<kThreads / 32>(img, k, v, toks + job.tok_off, kPage, 0, h, hkv, vmax, codes);
+  bad |= quantize_tokens<kThreads / 32, kRope>(rope, img, k, v, toks + job.tok_off, kPage, 0, h, hkv, vmax, codes);
   flush_vmax(vmax, status);
   if (bad) atomicOr(status, kStatusRange);
   __syncthreads();
@@ -677,14 +721,65 @@ __device__ __forceinline__ float redux_max(float x) {
   return d;
 }
 
-// The 32 bf16 channels 32gr .. 32gr + 31 of token T, kv head h (16 words).
-__device__ __forceinline__ void load_group(const __nv_bfloat16* __restrict__ src, int T, int h, int hkv, int gr,
+// The 32 bf16 channels 32gr .. 32gr + 31 of token T, kv head h (16 words); step:
+// elements from a token's rows to the next token's.
+__device__ __forceinline__ void load_group(const __nv_bfloat16* __restrict__ src, int T, int h, size_t step, int gr,
                                            uint32_t (&w)[16]) {
-  const uint4* p = reinterpret_cast<const uint4*>(src + ((size_t)T * hkv + h) * kHeadDim + 32 * gr);
+  const uint4* p = reinterpret_cast<const uint4*>(src + (size_t)T * step + (size_t)h * kHeadDim + 32 * gr);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const uint4 v = __ldg(p + q);
     w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
+  }
+}
+
+// A page's 32 K rows, rotated, in shared memory (rows 272 bytes apart, so that the
+// reads of a group by 32 lanes hit distinct banks).  The channels that a rotation
+// pairs lie in two groups, so the rows are rotated before a lane takes its token's
+// group: an item of a row (8 pairs) per thread at a time, loads by whole rows.
+struct RopeTile {
+  uint4 row[kPage][17];
+};
+__device__ __forceinline__ void rotate_page(RopeTile& K, const RopeArgs& R, const __nv_bfloat16* __restrict__ k,
+                                            const int32_t* __restrict__ toks, int h, bool& bad) {
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const int t = (int)(threadIdx.x >> 3) + 16 * y, i = threadIdx.x & 7;
+    const int T = __ldg(toks + t);
+    const uint4* p = reinterpret_cast<const uint4*>(k + (size_t)T * (size_t)R.k_stride + (size_t)h * kHeadDim);
+    int a, b;
+    rope_item(R, i, a, b);
+    uint4 x = __ldg(p + a), z = __ldg(p + b);
+    if (8 * i < R.half) {
+      float c[8], s[8];
+      rope_factors<8>(R, T, 8 * i, c, s, bad);
+      rope_turn(R, x, z, c, s);
+    }
+    K.row[t][a] = x;
+    K.row[t][b] = z;
+  }
+}
+// K of the warp's group of slot t: rotated in shared memory or as it is.
+template <bool kRope>
+struct KSource {
+  RopeTile tile;
+};
+template <>
+struct KSource<false> {};
+template <bool kRope>
+__device__ __forceinline__ void load_k_group(KSource<kRope>& S, const RopeParam<kRope>& R, const __nv_bfloat16* __restrict__ k,
+                                             const int32_t* __restrict__ toks, int T, int t, int h, int hkv, int gr,
+                                             uint32_t (&w)[16], bool& bad) {
+  if constexpr (kRope) {
+    rotate_page(S.tile, R, k, toks, h, bad);
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint4 v = S.tile.row[t][4 * gr + q];
+      w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
+    }
+  } else {
+    load_group(k, T, h, k_step<kRope>(R, hkv), gr, w);
   }
 }
 
@@ -828,12 +923,15 @@ __device__ __forceinline__ void deq8(uint32_t cw, const GroupMeta& m, float (&y)
 }
 
 // Fresh INT4 pages filled with 32 tokens within one call.  Grid (jobs, kv heads).
+template <bool kRope>
 __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int4_kernel(
     uint8_t* __restrict__ pool, size_t int4_off, int64_t n2, int hkv, const __nv_bfloat16* __restrict__ k,
     const __nv_bfloat16* __restrict__ v, const AppendJob* __restrict__ jobs, const int32_t* __restrict__ toks,
-    Entry* __restrict__ table, int32_t* __restrict__ ntab, uint32_t* __restrict__ status) {
+    Entry* __restrict__ table, int32_t* __restrict__ ntab, uint32_t* __restrict__ status,
+    const __grid_constant__ RopeParam<kRope> rope) {
   __shared__ __align__(16) uint8_t img[kInt4Block];
   __shared__ __align__(16) uint32_t wbuf[4][128];
+  __shared__ KSource<kRope> ksrc;
   asm volatile("griddepcontrol.wait;" ::: "memory");   // token lists and earlier stream work are done
   asm volatile("griddepcontrol.launch_dependents;");
   const AppendJob job = jobs[blockIdx.x];
@@ -843,7 +941,7 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int4_kernel(
   {
     // K: slot t's row, words (i, gr) i = 0..3 hold channels 32gr + 8i + n in nibble n
     uint32_t w[16], cw[4];
-    load_group(k, T, h, hkv, gr, w);
+    load_k_group<kRope>(ksrc, rope, k, toks + job.tok_off, T, t, h, hkv, gr, w, bad);
     const GroupMeta m = quant_i4_words(w, cw, bad);
 #pragma unroll
     for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(img + kI4KCodes + 64 * t + 16 * i + 4 * gr) = cw[i];
@@ -852,7 +950,7 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int4_kernel(
   }
   {
     uint32_t w[16], cw[4];
-    load_group(v, T, h, hkv, gr, w);
+    load_group(v, T, h, v_step<kRope>(rope, hkv), gr, w);
     const GroupMeta m = quant_i4_words(w, cw, bad);
     store_i4v_group(img, cw, gr, wbuf[gr]);
     st_half(img, kI4VMeta + 2 * v_meta_index(t, gr), m.s);
@@ -876,9 +974,12 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int4_kernel(
 // token and group.  Only the INT2 block is written.  Grid (jobs, kv heads).
 // Launched as a programmatic dependent of the INT4 kernels, as the
 // warp-per-token direct kernel is (it touches nothing they write).
+template <bool kRope>
 __global__ void __launch_bounds__(kBulkThreads, 6) bulk_int2_kernel(
     uint8_t* __restrict__ pool, int hkv, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
-    const DirectJob* __restrict__ jobs, const int32_t* __restrict__ toks, uint32_t* __restrict__ status) {
+    const DirectJob* __restrict__ jobs, const int32_t* __restrict__ toks, uint32_t* __restrict__ status,
+    const __grid_constant__ RopeParam<kRope> rope) {
+  __shared__ KSource<kRope> ksrc;
   __shared__ __align__(16) uint8_t img[kInt2Block];
   __shared__ __align__(16) float4 kmeta[4][32];          // per channel of the warp's group: zero, 1/scale, scale, nz
   __shared__ __align__(16) uint32_t vbuf[4][32][3];      // INT2 V codes [slot][channels 0..15, 16..31] (padded)
@@ -891,7 +992,7 @@ __global__ void __launch_bounds__(kBulkThreads, 6) bulk_int2_kernel(
     float xq[32];   // INT4-dequantized K of slot t's group
     {
       uint32_t w[16], cw[4];
-      load_group(k, T, h, hkv, gr, w);
+      load_k_group<kRope>(ksrc, rope, k, toks + job.tok_off, T, t, h, hkv, gr, w, bad);
       const GroupMeta m = quant_i4_words(w, cw, bad);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -955,7 +1056,7 @@ __global__ void __launch_bounds__(kBulkThreads, 6) bulk_int2_kernel(
     GroupMeta m;
     {
       uint32_t w[16];
-      load_group(v, T, h, hkv, gr, w);
+      load_group(v, T, h, v_step<kRope>(rope, hkv), gr, w);
       m = quant_i4_words(w, cw, bad);
     }
     flush_vmax(m.sf, status);   // the INT4 V scales count toward the pool's V-scale maximum too
@@ -1031,60 +1132,78 @@ __global__ void scatter_kernel(Entry* __restrict__ table, int32_t* __restrict__ 
 
 }  // namespace
 
+// with(std::bool_constant<kRope>, RopeParam<kRope>): the form of the running append
+template <class F>
+static cudaError_t with_rope(const kv_pool* P, F&& with) {
+  return P->rope ? with(std::true_type{}, *P->rope) : with(std::false_type{}, NoRope{});
+}
+
 cudaError_t launch_append(kv_pool* P, const void* k, const void* v, const AppendJob* d_jobs, int n_jobs,
                           const int32_t* d_toks, const SmallAppend* small, cudaStream_t s) {
   if (n_jobs <= 0) return cudaSuccess;
   dim3 grid((unsigned)n_jobs, (unsigned)P->cfg.num_kv_heads);
   ++P->launches;
-  const AppendJob* no_jobs = nullptr;
-  const int32_t* no_toks = nullptr;
-  if (small)
-    return launch_pdl(append_int4_kernel<true>, grid, dim3(kThreads), 0, s, P->d_pool, P->int4_offset,
+  return with_rope(P, [&](auto is, const auto& rope) {
+    constexpr bool kRope = decltype(is)::value;
+    const AppendJob* no_jobs = nullptr;
+    const int32_t* no_toks = nullptr;
+    if (small)
+      return launch_pdl(append_int4_kernel<true, kRope>, grid, dim3(kThreads), 0, s, P->d_pool, P->int4_offset,
+                        P->cfg.n_int2_pages, P->cfg.num_kv_heads, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v,
+                        no_jobs, no_toks, P->d_table, P->d_ntab, P->d_status, *small, rope);
+    static const SmallAppend none{};
+    return launch_pdl(append_int4_kernel<false, kRope>, grid, dim3(kThreads), 0, s, P->d_pool, P->int4_offset,
                       P->cfg.n_int2_pages, P->cfg.num_kv_heads, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v,
-                      no_jobs, no_toks, P->d_table, P->d_ntab, P->d_status, *small);
-  static const SmallAppend none{};
-  return launch_pdl(append_int4_kernel<false>, grid, dim3(kThreads), 0, s, P->d_pool, P->int4_offset,
-                    P->cfg.n_int2_pages, P->cfg.num_kv_heads, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v,
-                    d_jobs, d_toks, P->d_table, P->d_ntab, P->d_status, none);
+                      d_jobs, d_toks, P->d_table, P->d_ntab, P->d_status, none, rope);
+  });
 }
 
 cudaError_t launch_append_int3(kv_pool* P, const void* k, const void* v, const AppendJob* d_jobs, int n_jobs,
                                const int32_t* d_toks, cudaStream_t s) {
   if (n_jobs <= 0) return cudaSuccess;
   ++P->launches;
-  return launch_pdl(append_int3_kernel, dim3((unsigned)n_jobs, (unsigned)P->cfg.num_kv_heads), dim3(kThreads), 0, s,
-                    P->d_pool, P->int3_offset, (int64_t)(P->cfg.n_int2_pages + P->cfg.n_int4_pages),
-                    P->cfg.num_kv_heads, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, d_jobs, d_toks,
-                    P->d_table, P->d_ntab, P->d_status);
+  return with_rope(P, [&](auto is, const auto& rope) {
+    return launch_pdl(append_int3_kernel<decltype(is)::value>, dim3((unsigned)n_jobs, (unsigned)P->cfg.num_kv_heads),
+                      dim3(kThreads), 0, s, P->d_pool, P->int3_offset,
+                      (int64_t)(P->cfg.n_int2_pages + P->cfg.n_int4_pages), P->cfg.num_kv_heads, (const __nv_bfloat16*)k,
+                      (const __nv_bfloat16*)v, d_jobs, d_toks, P->d_table, P->d_ntab, P->d_status, rope);
+  });
 }
 
 cudaError_t launch_append_fp4(kv_pool* P, const void* k, const void* v, const AppendJob* d_jobs, int n_jobs,
                               const int32_t* d_toks, cudaStream_t s) {
   if (n_jobs <= 0) return cudaSuccess;
   ++P->launches;
-  return launch_pdl(append_fp4_kernel, dim3((unsigned)n_jobs, (unsigned)P->cfg.num_kv_heads), dim3(kThreads), 0, s,
-                    P->d_pool, P->fp4_offset,
-                    (int64_t)(P->cfg.n_int2_pages + P->cfg.n_int4_pages + P->cfg.n_int3_pages), P->cfg.num_kv_heads,
-                    (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, d_jobs, d_toks, P->d_table, P->d_ntab,
-                    P->d_status);
+  return with_rope(P, [&](auto is, const auto& rope) {
+    return launch_pdl(append_fp4_kernel<decltype(is)::value>, dim3((unsigned)n_jobs, (unsigned)P->cfg.num_kv_heads),
+                      dim3(kThreads), 0, s, P->d_pool, P->fp4_offset,
+                      (int64_t)(P->cfg.n_int2_pages + P->cfg.n_int4_pages + P->cfg.n_int3_pages), P->cfg.num_kv_heads,
+                      (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, d_jobs, d_toks, P->d_table, P->d_ntab,
+                      P->d_status, rope);
+  });
 }
 
 cudaError_t launch_bulk_int4(kv_pool* P, const void* k, const void* v, const AppendJob* d_jobs, int n_jobs,
                              const int32_t* d_toks, cudaStream_t s) {
   if (n_jobs <= 0) return cudaSuccess;
   ++P->launches;
-  return launch_pdl(bulk_int4_kernel, dim3((unsigned)n_jobs, (unsigned)P->cfg.num_kv_heads), dim3(kBulkThreads), 0,
-                    s, P->d_pool, P->int4_offset, P->cfg.n_int2_pages, P->cfg.num_kv_heads, (const __nv_bfloat16*)k,
-                    (const __nv_bfloat16*)v, d_jobs, d_toks, P->d_table, P->d_ntab, P->d_status);
+  return with_rope(P, [&](auto is, const auto& rope) {
+    return launch_pdl(bulk_int4_kernel<decltype(is)::value>, dim3((unsigned)n_jobs, (unsigned)P->cfg.num_kv_heads),
+                      dim3(kBulkThreads), 0, s, P->d_pool, P->int4_offset, P->cfg.n_int2_pages, P->cfg.num_kv_heads,
+                      (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, d_jobs, d_toks, P->d_table, P->d_ntab,
+                      P->d_status, rope);
+  });
 }
 
 cudaError_t launch_bulk_int2(kv_pool* P, const void* k, const void* v, const DirectJob* d_jobs, int n_jobs,
                              const int32_t* d_toks, cudaStream_t s) {
   if (n_jobs <= 0) return cudaSuccess;
   ++P->launches;
-  return launch_pdl(bulk_int2_kernel, dim3((unsigned)n_jobs, (unsigned)P->cfg.num_kv_heads), dim3(kBulkThreads), 0,
-                    s, P->d_pool, P->cfg.num_kv_heads, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, d_jobs, d_toks,
-                    P->d_status);
+  return with_rope(P, [&](auto is, const auto& rope) {
+    return launch_pdl(bulk_int2_kernel<decltype(is)::value>, dim3((unsigned)n_jobs, (unsigned)P->cfg.num_kv_heads),
+                      dim3(kBulkThreads), 0, s, P->d_pool, P->cfg.num_kv_heads, (const __nv_bfloat16*)k,
+                      (const __nv_bfloat16*)v, d_jobs, d_toks, P->d_status, rope);
+  });
 }
 
 cudaError_t launch_repack(kv_pool* P, const RepackJob* d_jobs, int n_jobs, cudaStream_t s) {
@@ -1101,8 +1220,11 @@ cudaError_t launch_direct_int2(kv_pool* P, const void* k, const void* v, const D
   if (n_jobs <= 0) return cudaSuccess;
   dim3 grid((unsigned)n_jobs, (unsigned)P->cfg.num_kv_heads);
   ++P->launches;
-  return launch_pdl(direct_int2_kernel, grid, dim3(kThreads), 0, s, P->d_pool, P->cfg.num_kv_heads,
-                    (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, d_jobs, d_toks, P->d_status);
+  return with_rope(P, [&](auto is, const auto& rope) {
+    return launch_pdl(direct_int2_kernel<decltype(is)::value>, grid, dim3(kThreads), 0, s, P->d_pool,
+                      P->cfg.num_kv_heads, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, d_jobs, d_toks,
+                      P->d_status, rope);
+  });
 }
 
 cudaError_t launch_scatter(kv_pool* P, const TableUpd* d_upd, int n, cudaStream_t s) {

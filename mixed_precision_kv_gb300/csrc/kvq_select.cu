@@ -388,8 +388,11 @@ kv_status_t sync_positions(kv_pool* P, cudaStream_t s) {
   for (size_t a = 0; a < ids.size(); a += kPosChunk) {
     const size_t n = std::min(kPosChunk, ids.size() - a);
     rows.resize(n);
-    for (size_t x = 0; x < n; ++x)
-      std::copy_n(&P->pos[(size_t)ids[a + x] * kPage], kPage, rows[x].pos);
+    for (size_t x = 0; x < n; ++x) {   // slots that hold no token: -1
+      const int fill = P->fill[ids[a + x]];
+      std::copy_n(&P->pos[(size_t)ids[a + x] * kPage], fill, rows[x].pos);
+      std::fill(rows[x].pos + fill, rows[x].pos + kPage, -1);
+    }
     Upload u;
     const size_t oi = u.add(ids.data() + a, n * sizeof(int32_t)), orow = u.add(rows.data(), n * sizeof(PosRow));
     const kv_status_t st = upload(P, u, s);
