@@ -380,6 +380,23 @@ KVQ_API kv_status_t kv_attend(kv_pool_t* pool, const void* q, const void* k, con
                               const int32_t* req_ids, const int32_t* n_new, int32_t n_req, int32_t num_q_heads,
                               float softmax_scale, void* out, void* stream);
 
+/* kv_attend for requests that share a cached prefix (samples of one prompt, a
+ * system prompt or a document under many questions): the tokens of req_ids[b]
+ * see the cache of request prefix_ids[b] first, then what they see in kv_attend.
+ * The prefix is a request of its own, filled once with kv_append_quant or
+ * kv_append_rotated; its pages are read once for all rows of all the requests of
+ * the call that have it, wherever they stand in the batch.
+ *   prefix_ids  host, int32 [n_req]: an open request other than req_ids[b], or -1:
+ *               none.  Its live slots and its full-precision list are seen by
+ *               every new token, whatever tree says.
+ *   k, v        NULL (both): rows see the caches only, e.g. one token per request
+ *               (n_new 1) that has been appended: the decode step of such a batch
+ * The other arguments and the rules are kv_attend's (out is bf16); at most 2^20
+ * new tokens over one prefix; always the tensor-core kernels. */
+KVQ_API kv_status_t kv_attend_shared(kv_pool_t* pool, const void* q, const void* k, const void* v, const uint64_t* tree,
+                                     const int32_t* req_ids, const int32_t* prefix_ids, const int32_t* n_new,
+                                     int32_t n_req, int32_t num_q_heads, float softmax_scale, void* out, void* stream);
+
 /* kv_decode_attn that also accumulates attention weight per cached token, the
  * ranking of eviction policies that keep heavy hitters.  For batch row b, kv
  * head h and every slot of the request that is live for h, with p_jt the

@@ -29,7 +29,7 @@ EXPORTED = ["kv_pool_create", "kv_pool_destroy", "kv_request_open", "kv_request_
             "kv_last_error", "kv_decode_attn_noalloc", "kv_decode_timing", "kv_evict_slots_head", "kv_fp_configure",
             "kv_fp_append", "kv_fp_drop", "kv_fp_count", "kv_set_wait_limit", "kv_drop_dead_pages",
             "kv_decode_attn_groups", "kv_alloc_bits3", "kv_attend", "kv_decode_attn_scored", "kv_select_lowest",
-            "kv_rotate", "kv_append_rotated", "kv_read_tokens"]
+            "kv_rotate", "kv_append_rotated", "kv_read_tokens", "kv_attend_shared"]
 
 _P = ctypes.c_void_p
 _I32, _I64 = ctypes.c_int32, ctypes.c_int64
@@ -82,6 +82,7 @@ def load_library(path: str = LIB_PATH):
             "kv_decode_attn": [_P, _P, _P, _I32, _I32, ctypes.c_float, _P, _P],
             "kv_decode_attn_noalloc": [_P, _P, _P, _I32, _I32, ctypes.c_float, _P, _P],
             "kv_attend": [_P, _P, _P, _P, _P, _P, _P, _I32, _I32, ctypes.c_float, _P, _P],
+            "kv_attend_shared": [_P, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, ctypes.c_float, _P, _P],
             "kv_decode_attn_scored": [_P, _P, _P, _I32, _I32, ctypes.c_float, ctypes.c_float, _P, _I64, _P, _P],
             "kv_select_lowest": [_P, _P, _I64, _P, _P, _I32, _I64, _I32, _P, _I64, _P],
             "kv_rotate": [_P, _P, _P, _I64, _I64, _P, _I32, _I64, _P, _I64, _P, _I32, _I64, _P, _I64, _P],
@@ -489,11 +490,8 @@ class KVPool:
                "kv_decode_attn_groups")
         return out
 
-    def attend(self, q, req_ids, n_new, softmax_scale, k=None, v=None, tree=None, out=None, stream=None):
-        """kv_attend: n_new[b] new tokens of each request attend to the request's cache and to
-        each other (causally, or as tree says).  q: torch bf16 CUDA [N][Hq][128], N = sum(n_new);
-        k, v: the new tokens' own rows, bf16 [N][Hkv][128] (None: the cache only); tree: int64
-        (or uint64) CUDA [N], bit j = may see new token j of its request -> out bf16 like q."""
+    def _attend_args(self, q, req_ids, n_new, k, v, tree, out, stream):
+        """The arguments of attend() and attend_shared(), checked."""
         torch = _torch_mod()
         req_ids = _np(req_ids, np.int32)
         n_new = _np(n_new, np.int32)
@@ -516,12 +514,38 @@ class KVPool:
         elif out.dtype is not torch.bfloat16 or out.shape != q.shape or not self._on_pool_device(out) or \
                 not out.is_contiguous():
             raise ValueError("out must be a contiguous bf16 tensor shaped like q on the pool's device")
+        return req_ids, n_new, out
+
+    def attend(self, q, req_ids, n_new, softmax_scale, k=None, v=None, tree=None, out=None, stream=None):
+        """kv_attend: n_new[b] new tokens of each request attend to the request's cache and to
+        each other (causally, or as tree says).  q: torch bf16 CUDA [N][Hq][128], N = sum(n_new);
+        k, v: the new tokens' own rows, bf16 [N][Hkv][128] (None: the cache only); tree: int64
+        (or uint64) CUDA [N], bit j = may see new token j of its request -> out bf16 like q."""
+        req_ids, n_new, out = self._attend_args(q, req_ids, n_new, k, v, tree, out, stream)
         rc = self._L.kv_attend(self._h, q.data_ptr(), k.data_ptr() if k is not None else None,
                                v.data_ptr() if v is not None else None, tree.data_ptr() if tree is not None else None,
                                req_ids.ctypes.data, n_new.ctypes.data, req_ids.size, q.shape[1], softmax_scale,
                                out.data_ptr(), _stream(stream, self.device))
         if rc:
             _check(rc, "kv_attend")
+        return out
+
+    def attend_shared(self, q, req_ids, prefix_ids, n_new, softmax_scale, k=None, v=None, tree=None, out=None,
+                      stream=None):
+        """kv_attend_shared: attend() for requests that share cached prefixes.  prefix_ids: host
+        sequence like req_ids, the request whose cache each one's tokens see before its own (-1: none),
+        read once for all that have it.  n_new all 1 without k and v: a decode step."""
+        req_ids, n_new, out = self._attend_args(q, req_ids, n_new, k, v, tree, out, stream)
+        prefix_ids = _np(prefix_ids, np.int32)
+        if prefix_ids.shape != req_ids.shape:
+            raise ValueError("req_ids and prefix_ids must be sequences of one length")
+        rc = self._L.kv_attend_shared(self._h, q.data_ptr(), k.data_ptr() if k is not None else None,
+                                      v.data_ptr() if v is not None else None,
+                                      tree.data_ptr() if tree is not None else None, req_ids.ctypes.data,
+                                      prefix_ids.ctypes.data, n_new.ctypes.data, req_ids.size, q.shape[1], softmax_scale,
+                                      out.data_ptr(), _stream(stream, self.device))
+        if rc:
+            _check(rc, "kv_attend_shared")
         return out
 
     def _check_scores(self, scores, n):

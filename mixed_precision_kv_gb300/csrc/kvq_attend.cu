@@ -164,6 +164,100 @@ cudaError_t launch_attend_merge(kv_pool* P, const AttArgs& A, const AttUnit* d_u
   return cudaSuccess;
 }
 
+// Rows with a shared prefix: the parts of the request's own unit and those of the
+// prefix unit, each in the layout of the kernel that made it, as in
+// attend_merge_kernel: a warp per row.  Bound by the partials' bytes, which are
+// still in L2 (parts by channel: 16 of every 32 bytes read are used).
+struct PartRow {
+  const float *o, *ml;   // this lane's four channels of part 0, its m and l
+  size_t step;
+  int n;
+};
+__device__ __forceinline__ PartRow part_row(const AttSrc& S, const float* part, int r, int lane, bool tall) {
+  const float* p = part + S.off;
+  return tall ? PartRow{p + (size_t)lane * (4 * kTallRows) + 4 * r, p + kTallRows * kHeadDim + 2 * r, (size_t)S.step, S.n_parts}
+              : PartRow{p + (size_t)r * kAttPart + 4 * lane, p + (size_t)r * kAttPart + kHeadDim, (size_t)S.step, S.n_parts};
+}
+__global__ void __launch_bounds__(32 * kMergeRows) attend_join_kernel(AttArgs A, const AttUnit* __restrict__ units,
+                                                                      const AttJoin* __restrict__ joins,
+                                                                      const AttSrc* __restrict__ srcs,
+                                                                      const float* __restrict__ part) {
+  const AttJoin J = joins[blockIdx.y];
+  const int i = blockIdx.x * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (i >= J.rows) return;
+  const int ip = J.pre_row + i;
+  const PartRow two[2] = {
+      part_row(srcs[J.own0 + (i >> J.own_shift)], part, i & ((1 << J.own_shift) - 1), lane, J.tall & 1),
+      part_row(srcs[J.pre0 + (ip >> J.pre_shift)], part, ip & ((1 << J.pre_shift) - 1), lane, (J.tall & 2) != 0)};
+  float M = -INFINITY;
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    for (int p = lane; p < two[x].n; p += 32) M = fmaxf(M, two[x].ml[(size_t)p * two[x].step]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  float L = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const PartRow& R = two[x];
+    for (int p0 = 0; p0 < R.n; p0 += 32) {
+      float f = 0.0f;
+      if (p0 + lane < R.n) {
+        const float2 ml = *reinterpret_cast<const float2*>(R.ml + (size_t)(p0 + lane) * R.step);
+        // a part that saw nothing (m = -inf, l = 0) adds nothing; one with a NaN sum keeps it
+        f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2f(ml.x - M);
+        L = fmaf(ml.y, f, L);
+      }
+      const int n = min(32, R.n - p0);
+      for (int p = 0; p < n; p += 8) {
+        float4 a[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) a[y] = *reinterpret_cast<const float4*>(R.o + (size_t)(p0 + min(p + y, n - 1)) * R.step);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const float w = __shfl_sync(0xFFFFFFFFu, f, (p + y) & 31);
+          if (p + y < n && w != 0.0f) {
+            o.x = fmaf(a[y].x, w, o.x); o.y = fmaf(a[y].y, w, o.y); o.z = fmaf(a[y].z, w, o.z); o.w = fmaf(a[y].w, w, o.w);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, x);
+  const float inv = row_inverse(M, L);
+  const float r[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+  const AttUnit u = units[J.unit];
+  const int g = A.hq / A.hkv;
+  uint16_t* op = A.out + ((size_t)(u.tok0 + i / g) * A.hq + (size_t)u.kvh * g + i % g) * kHeadDim + 4 * lane;
+  bool bad = false;
+  uint32_t h[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (!(fabsf(r[k]) < INFINITY)) bad = true;
+    h[k] = __bfloat16_as_ushort(__float2bfloat16_rn(r[k]));
+  }
+  if (((uintptr_t)A.out & 7) == 0) {
+    *reinterpret_cast<uint2*>(op) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) op[k] = (uint16_t)h[k];
+  }
+  if (bad) atomicOr(A.status, kStatusRange);
+}
+
+cudaError_t launch_attend_join(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const AttJoin* d_joins, int n_joins,
+                               int max_rows, const AttSrc* d_srcs, const float* d_part, cudaStream_t s) {
+  for (int a = 0; a < n_joins; a += 65535) {
+    ++P->launches;
+    attend_join_kernel<<<dim3((unsigned)((max_rows + kMergeRows - 1) / kMergeRows), (unsigned)std::min(65535, n_joins - a)),
+                         32 * kMergeRows, 0, s>>>(A, d_units, d_joins + a, d_srcs, d_part);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
 // ---- work plan ---------------------------------------------------------
 struct AttPlan {
   std::vector<AttItem> items;
@@ -171,12 +265,23 @@ struct AttPlan {
   std::vector<AttMerge> merges;
   int64_t n_parts = 0;
   int merge_rows = 0;
+  std::vector<AttSrc> srcs;        // joined units: the blocks' parts (off, step: parts), and a unit's first block
+  std::vector<int32_t> src0;
 };
 
 // Key tiles of the block of rows [row0, row0 + rows) of a unit.
-int block_tiles(const AttUnit& u, int g, int row0, int rows, bool kv, bool tree) {
+int block_tiles(const AttUnit& u, int g, int row0, int rows, bool tree) {
   const int t_last = (row0 + rows - 1) / g;
-  return (u.n_pages + 3) / 4 + (u.n_fp + 127) / 128 + (kv ? (tree ? u.T - 1 : t_last) / 128 + 1 : 0);
+  return (u.n_pages + 3) / 4 + (u.n_fp + 127) / 128 + (u.n_own ? (tree ? u.T - 1 : t_last) / 128 + 1 : 0);
+}
+// Room for the blocks of joined units [u0, u1), blocks of `rows` rows.
+void make_srcs(const std::vector<AttUnit>& units, int u0, int u1, int g, int rows, AttPlan& out) {
+  out.src0.resize(units.size(), -1);
+  for (int x = u0; x < u1; ++x) {
+    if (!units[(size_t)x].joined) continue;
+    out.src0[(size_t)x] = (int32_t)out.srcs.size();
+    out.srcs.resize(out.srcs.size() + (size_t)((units[(size_t)x].T * g + rows - 1) / rows));
+  }
 }
 
 // Blocks of kWideRows rows of units [u0, u1).  An item costs its tiles (3700 cycles
@@ -190,18 +295,19 @@ int block_tiles(const AttUnit& u, int g, int row0, int rows, bool kv, bool tree)
 // by_cta[c] gets the items of CTA c.
 constexpr int kWideRows = 256;
 constexpr double kWideItem = 5.4;
-void plan_wide(const std::vector<AttUnit>& units, int u0, int u1, int g, bool kv, bool tree, int ctas,
+void plan_wide(const std::vector<AttUnit>& units, int u0, int u1, int g, bool tree, int ctas,
                std::vector<std::vector<AttItem>>& by_cta, AttPlan& out) {
   struct Block {
     int unit, row0, rows, tiles;
   };
   std::vector<Block> blocks, rest;
   double total = kWideItem * ctas;   // about one cut per CTA
+  make_srcs(units, u0, u1, g, 128, out);
   for (int x = u0; x < u1; ++x) {
     const int rows = units[(size_t)x].T * g;
     for (int r = 0; r < rows; r += kWideRows) {
       const int n = std::min(kWideRows, rows - r);
-      const Block b{x, r, n, block_tiles(units[(size_t)x], g, r, n, kv, tree)};
+      const Block b{x, r, n, block_tiles(units[(size_t)x], g, r, n, tree)};
       blocks.push_back(b);
       total += b.tiles + kWideItem;
     }
@@ -216,10 +322,17 @@ void plan_wide(const std::vector<AttUnit>& units, int u0, int u1, int g, bool kv
   };
   auto join = [&](const Block& b) {   // partials of a block, if it needs any
     const int n = (int)pieces.size();
-    if (n == 1) return;
+    const bool joined = units[(size_t)b.unit].joined;
+    if (n == 1 && !joined) return;
     const int32_t p0 = (int32_t)out.n_parts;
     for (int y = 0; y < n; ++y) by_cta[(size_t)pieces[(size_t)y].first][pieces[(size_t)y].second].part = p0 + 2 * y;
     out.n_parts += 2 * n;
+    if (joined) {
+      AttSrc* s = &out.srcs[(size_t)(out.src0[(size_t)b.unit] + b.row0 / 128)];
+      s[0] = AttSrc{p0, n, 2};
+      if (b.rows > 128) s[1] = AttSrc{p0 + 1, n, 2};
+      return;
+    }
     out.merges.push_back(AttMerge{b.unit, b.row0, std::min(128, b.rows), p0, n, 2});
     if (b.rows > 128) out.merges.push_back(AttMerge{b.unit, b.row0 + 128, b.rows - 128, p0 + 1, n, 2});
     out.merge_rows = std::max(out.merge_rows, std::min(128, b.rows));
@@ -279,12 +392,13 @@ int64_t wide_gain(int rows, int64_t tiles) {
 // Few rows per unit: blocks of R rows, all key tiles of all blocks in one line, cut
 // into equal runs.  A tile costs 1 (its unpacking, whatever R), an item 3 more (its
 // rows, the first and last steps).
-void plan_few(const std::vector<AttUnit>& units, int g, int R, bool kv, bool tree, int sms, AttPlan& out) {
+void plan_few(const std::vector<AttUnit>& units, int g, int R, bool tree, int sms, AttPlan& out) {
   double total = 0.0;
+  make_srcs(units, 0, (int)units.size(), g, R, out);
   int64_t tiles = 0;
   for (const AttUnit& u : units)
     for (int r = 0; r < u.T * g; r += R) {
-      const int t = block_tiles(u, g, r, std::min(R, u.T * g - r), kv, tree);
+      const int t = block_tiles(u, g, r, std::min(R, u.T * g - r), tree);
       tiles += t;
       total += t + 3.0;
     }
@@ -296,7 +410,7 @@ void plan_few(const std::vector<AttUnit>& units, int g, int R, bool kv, bool tre
   for (int x = 0; x < (int)units.size(); ++x) {
     const AttUnit& u = units[(size_t)x];
     for (int r = 0; r < u.T * g; r += R) {
-      const int rows = std::min(R, u.T * g - r), n = block_tiles(u, g, r, rows, kv, tree);
+      const int rows = std::min(R, u.T * g - r), n = block_tiles(u, g, r, rows, tree);
       const size_t first = out.items.size();
       int t = 0;
       do {
@@ -315,11 +429,15 @@ void plan_few(const std::vector<AttUnit>& units, int g, int R, bool kv, bool tre
         t += take;
       } while (t < n);
       const int pieces = (int)(out.items.size() - first);
-      if (pieces == 1) continue;
+      if (pieces == 1 && !u.joined) continue;
       for (int y = 0; y < pieces; ++y) out.items[first + (size_t)y].part = (int32_t)out.n_parts + y;
-      out.merges.push_back(AttMerge{x, r, rows, (int32_t)out.n_parts, pieces, 1});
+      if (u.joined) {
+        out.srcs[(size_t)(out.src0[(size_t)x] + r / R)] = AttSrc{out.n_parts, pieces, 1};
+      } else {
+        out.merges.push_back(AttMerge{x, r, rows, (int32_t)out.n_parts, pieces, 1});
+        out.merge_rows = std::max(out.merge_rows, rows);
+      }
       out.n_parts += pieces;
-      out.merge_rows = std::max(out.merge_rows, rows);
     }
   }
   out.cta_item.push_back((int32_t)out.items.size());
@@ -328,44 +446,170 @@ void plan_few(const std::vector<AttUnit>& units, int g, int R, bool kv, bool tre
 // A pass holds the operand tiles of as many units as fit into this many.
 constexpr int64_t kTilesPerPass = 1 << 16;   // 4.3 GB
 
-}  // namespace
-}  // namespace kvq
+// The units of a call that run one after the other in the same way, shared out to the two kernels and planned.
+struct AttSet {
+  std::vector<AttUnit> few, wide;   // few and many rows per unit
+  struct Where {
+    int32_t wide, index;
+  };
+  std::vector<Where> where;         // of every unit that plan() was given
+  AttPlan pf, pl;
+  int R = 16;                       // rows of the first kernel's blocks
+  struct Pass {
+    int u0, u1, max_tiles, cta0;
+  };
+  std::vector<Pass> passes;         // of the second kernel
+  int64_t most = 0;                 // operand tiles of a pass
+  struct Placed {                   // a plan's arrays in the upload, its partials behind
+    size_t units, items, ctas, merges, parts;
+  } xf, xl;
 
-using namespace kvq;
+  // units: hkv of every request (or prefix), kv head by kv head
+  void plan(const std::vector<AttUnit>& units, int g, int hkv, bool tree, int sms) {
+    int few_most = kFewMost;        // rows of a unit that the few-row kernel takes
+    int64_t gain = -kWideStart * sms;
+    for (size_t x = 0; x < units.size(); x += (size_t)hkv) {
+      const int rows = units[x].T * g;
+      if (rows > kFewMost) gain += kWideStart * sms;   // the other kernel runs anyway
+      if (rows > kFewRows && rows <= kFewMost) gain += hkv * wide_gain(rows, block_tiles(units[x], g, 0, rows, tree));
+    }
+    if (gain > 0) few_most = kFewRows;
+    int few_rows = 0;
+    for (const AttUnit& u : units) {
+      const bool many = u.T * g > few_most;
+      where.push_back(Where{many, (int32_t)(many ? wide : few).size()});
+      if (many) {
+        wide.push_back(u);
+      } else {
+        few.push_back(u);
+        few_rows = std::max(few_rows, u.T * g);
+      }
+    }
+    R = few_rows <= 16 ? 16 : (few_rows <= 32 ? 32 : 64);
+    if (!few.empty()) plan_few(few, g, R, tree, sms, pf);
+    std::vector<std::vector<AttItem>> by_cta((size_t)sms);
+    int64_t n = 0;
+    int u0 = 0, max_tiles = 0;
+    auto end_pass = [&](int x) {
+      passes.push_back(Pass{u0, x, max_tiles, (int)pl.cta_item.size()});
+      plan_wide(wide, u0, x, g, tree, sms, by_cta, pl);
+      for (auto& c : by_cta) {
+        pl.cta_item.push_back((int32_t)pl.items.size());
+        pl.items.insert(pl.items.end(), c.begin(), c.end());
+        c.clear();
+      }
+      pl.cta_item.push_back((int32_t)pl.items.size());
+      most = std::max(most, n);
+      u0 = x;
+      n = 0;
+      max_tiles = 0;
+    };
+    for (int x = 0; x < (int)wide.size(); ++x) {
+      const int t = block_tiles(wide[(size_t)x], g, 0, wide[(size_t)x].T * g, tree);
+      if (x > u0 && n + t > kTilesPerPass) end_pass(x);
+      wide[(size_t)x].tile_base = (int32_t)n;
+      n += t;
+      max_tiles = std::max(max_tiles, t);
+    }
+    if (!wide.empty()) end_pass((int)wide.size());
+  }
+  void place(Upload& u) {
+    auto one = [&](const std::vector<AttUnit>& un, const AttPlan& p, Placed& x) {
+      x.units = u.add(un.data(), un.size() * sizeof(AttUnit));
+      x.items = u.add(p.items.data(), p.items.size() * sizeof(AttItem));
+      x.ctas = u.add(p.cta_item.data(), p.cta_item.size() * sizeof(int32_t));
+      x.merges = u.add(p.merges.data(), p.merges.size() * sizeof(AttMerge));
+    };
+    if (!few.empty()) one(few, pf, xf);
+    if (!wide.empty()) one(wide, pl, xl);
+  }
+  // partials from byte `at` on; returns the end
+  size_t place_parts(size_t at) {
+    xf.parts = at;
+    xl.parts = at + (size_t)pf.n_parts * R * kAttPart * sizeof(float);
+    return xl.parts + (size_t)pl.n_parts * 128 * kAttPart * sizeof(float);
+  }
+  // the joined units' blocks, in floats from byte `from` of the workspace; the first block of a unit of
+  // each kind is src0[unit] + the index that comes back
+  std::pair<int32_t, int32_t> add_srcs(size_t from, std::vector<AttSrc>& out) const {
+    std::pair<int32_t, int32_t> at;
+    auto add = [&](const AttPlan& p, size_t parts, int rows) {
+      const int32_t first = (int32_t)out.size();
+      for (AttSrc s : p.srcs) {
+        s.off = (int64_t)((parts - from) / sizeof(float)) + s.off * rows * kAttPart;
+        s.step *= rows * kAttPart;
+        out.push_back(s);
+      }
+      return first;
+    };
+    at.first = add(pf, xf.parts, R);
+    at.second = add(pl, xl.parts, 128);
+    return at;
+  }
+  kv_status_t launch(kv_pool* P, const AttArgs& A, int64_t tiles, cudaStream_t s) const {
+    uint8_t* base = (uint8_t*)P->attend.ptr;
+    auto merge = [&](const Placed& x, const AttPlan& p, int part_rows) -> cudaError_t {
+      if (p.merges.empty()) return cudaSuccess;
+      return launch_attend_merge(P, A, (const AttUnit*)(base + x.units), (const AttMerge*)(base + x.merges),
+                                 (int)p.merges.size(), p.merge_rows, (const float*)(base + x.parts), part_rows, s);
+    };
+    if (!few.empty()) {
+      KV_CUDA(launch_attend_few(P, R, A, (const AttUnit*)(base + xf.units), (const AttItem*)(base + xf.items),
+                                (const int32_t*)(base + xf.ctas), (int)pf.cta_item.size() - 1, (float*)(base + xf.parts), s));
+      KV_CUDA(merge(xf, pf, R));
+    }
+    if (wide.empty()) return KV_OK;
+    const AttUnit* du = (const AttUnit*)(base + xl.units);
+    uint32_t* d_live = (uint32_t*)((uint8_t*)P->attend_tiles.ptr + (size_t)tiles * kAttTileBytes);
+    for (const Pass& G : passes) {
+      KV_CUDA(launch_attend_tiles(P, A, du + G.u0, G.u1 - G.u0, G.max_tiles, P->attend_tiles.ptr, d_live, s));
+      KV_CUDA(launch_attend_wide(P, A, du, (const AttItem*)(base + xl.items), (const int32_t*)(base + xl.ctas) + G.cta0,
+                                 P->sm_count, P->attend_tiles.ptr, d_live, (float*)(base + xl.parts), s));
+    }
+    KV_CUDA(merge(xl, pl, 128));
+    return KV_OK;
+  }
+};
 
-extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, const void* v, const uint64_t* tree,
-                                 const int32_t* req_ids, const int32_t* n_new, int32_t n_req, int32_t hq,
-                                 float softmax_scale, void* out, void* stream) try {
-  if (!P) return fail(KV_ERR_INVALID_ARG, "kv_attend: null pool");
-  if (!req_ids || !n_new || n_req < 1) return fail(KV_ERR_INVALID_ARG, "kv_attend: null pointer or n_req < 1");
-  if ((k == nullptr) != (v == nullptr)) return fail(KV_ERR_INVALID_ARG, "kv_attend: k and v come together");
-  if (tree && !k) return fail(KV_ERR_INVALID_ARG, "kv_attend: a tree needs k and v");
+// Workspaces of a call, grown: `bytes` of plan and partials, `tiles` operand tiles.
+kv_status_t attend_room(kv_pool* P, size_t bytes, int64_t tiles) {
+  const kv_status_t st = ensure(P->attend, bytes);
+  if (st != KV_OK) return st;
+  return ensure(P->attend_tiles, (size_t)tiles * (kAttTileBytes + 16), (size_t)kTilesPerPass * (kAttTileBytes + 16));
+}
+
+// The checks that both entries make; total: new tokens.
+kv_status_t attend_check(const char* what, kv_pool* P, const void* q, const void* k, const void* v, const uint64_t* tree,
+                         const int32_t* req_ids, const int32_t* n_new, int32_t n_req, int32_t hq, float softmax_scale,
+                         const void* out, int64_t& total, int32_t& max_new) {
+  if (!P) return fail(KV_ERR_INVALID_ARG, "%s: null pool", what);
+  if (!req_ids || !n_new || n_req < 1) return fail(KV_ERR_INVALID_ARG, "%s: null pointer or n_req < 1", what);
+  if ((k == nullptr) != (v == nullptr)) return fail(KV_ERR_INVALID_ARG, "%s: k and v come together", what);
+  if (tree && !k) return fail(KV_ERR_INVALID_ARG, "%s: a tree needs k and v", what);
   const int hkv = P->cfg.num_kv_heads;
   if (hq < hkv || hq % hkv != 0 || hq / hkv > 8)
-    return fail(KV_ERR_INVALID_ARG, "kv_attend: num_q_heads %d must be a multiple of %d with ratio <= 8", hq, hkv);
-  if (!std::isfinite(softmax_scale)) return fail(KV_ERR_INVALID_ARG, "kv_attend: softmax_scale must be finite");
-  if ((int64_t)n_req * hkv > 65535) return fail(KV_ERR_INVALID_ARG, "kv_attend: n_req x num_kv_heads must be <= 65535");
-  const int g = hq / hkv;
-  int64_t total = 0;
-  int32_t max_new = 0;
+    return fail(KV_ERR_INVALID_ARG, "%s: num_q_heads %d must be a multiple of %d with ratio <= 8", what, hq, hkv);
+  if (!std::isfinite(softmax_scale)) return fail(KV_ERR_INVALID_ARG, "%s: softmax_scale must be finite", what);
+  if ((int64_t)n_req * hkv > 65535) return fail(KV_ERR_INVALID_ARG, "%s: n_req x num_kv_heads must be <= 65535", what);
+  total = 0;
+  max_new = 0;
   for (int32_t b = 0; b < n_req; ++b) {
-    if (!req_ok(P, req_ids[b])) return fail(KV_ERR_INVALID_ARG, "kv_attend: request %d not open", req_ids[b]);
+    if (!req_ok(P, req_ids[b])) return fail(KV_ERR_INVALID_ARG, "%s: request %d not open", what, req_ids[b]);
     if (n_new[b] < 0 || n_new[b] > kMaxNewTokens)
-      return fail(KV_ERR_INVALID_ARG, "kv_attend: n_new[%d] = %d is not in [0, %d]", b, n_new[b], kMaxNewTokens);
-    if (tree && n_new[b] > 64) return fail(KV_ERR_INVALID_ARG, "kv_attend: a tree holds at most 64 tokens of a request");
+      return fail(KV_ERR_INVALID_ARG, "%s: n_new[%d] = %d is not in [0, %d]", what, b, n_new[b], kMaxNewTokens);
+    if (tree && n_new[b] > 64) return fail(KV_ERR_INVALID_ARG, "%s: a tree holds at most 64 tokens of a request", what);
     total += n_new[b];
     max_new = std::max(max_new, n_new[b]);
   }
   if (total == 0) return KV_OK;
   if (total > kMaxRows / hq)
-    return fail(KV_ERR_INVALID_ARG, "kv_attend: more than %lld rows (tokens x num_q_heads)", (long long)kMaxRows);
-  if (!q || !out) return fail(KV_ERR_INVALID_ARG, "kv_attend: null pointer");
-  DeviceGuard dg(P->cfg.device);
-  cudaStream_t s = (cudaStream_t)stream;
-  kv_status_t st = refuse_capture("kv_attend", s);
-  if (st != KV_OK) return st;
-  if ((st = order_after_previous(P, s)) != KV_OK) return st;
+    return fail(KV_ERR_INVALID_ARG, "%s: more than %lld rows (tokens x num_q_heads)", what, (long long)kMaxRows);
+  if (!q || !out) return fail(KV_ERR_INVALID_ARG, "%s: null pointer", what);
+  return KV_OK;
+}
 
+AttArgs attend_args(const kv_pool* P, const void* q, const void* k, const void* v, const uint64_t* tree, int32_t hq,
+                    float softmax_scale, void* out) {
   AttArgs A;
   A.pool = P->d_pool;
   A.int4_off = P->int4_offset;
@@ -382,120 +626,210 @@ extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, con
   A.k = (const uint16_t*)k;
   A.v = (const uint16_t*)v;
   A.tree = tree;
+  A.tok_map = nullptr;
   A.out = (uint16_t*)out;
   A.status = P->d_status;
   A.scale_log2 = softmax_scale * 1.4426950408889634f;
   A.max_pages = P->cfg.max_pages_per_request;
-  A.hkv = hkv;
+  A.hkv = P->cfg.num_kv_heads;
   A.hq = hq;
   A.fp_cap = P->fp_cap;
+  return A;
+}
 
-  const bool simt = P->decode_impl == KV_DECODE_SIMT;
-  std::vector<AttUnit> units, few;   // many rows (or all, on the CUDA cores) and few rows per unit
-  const bool kv = k != nullptr, tr = tree != nullptr;
-  auto unit = [&](int32_t b, int h, int64_t tok0) {
-    const int32_t r = req_ids[b];
-    return AttUnit{r, h, n_new[b], (int32_t)P->reqs[r].table.size(), P->n_fp.empty() ? 0 : P->n_fp[r], 0, tok0};
-  };
-  int few_most = kFewMost;   // rows of a unit that the few-row kernel takes
-  int64_t gain = -kWideStart * P->sm_count;
-  for (int32_t b = 0; b < n_req; ++b) {
-    const int rows = n_new[b] * g;
-    if (rows > kFewMost) gain += kWideStart * P->sm_count;   // the other kernel runs anyway
-    if (rows > kFewRows && rows <= kFewMost) gain += hkv * wide_gain(rows, block_tiles(unit(b, 0, 0), g, 0, rows, kv, tr));
-  }
-  if (gain > 0) few_most = kFewRows;
-  int few_rows = 0;
+AttUnit attend_unit(const kv_pool* P, int32_t r, int h, int32_t T, bool kv, int64_t tok0) {
+  return AttUnit{r, h, T, (int32_t)P->reqs[r].table.size(), P->n_fp.empty() ? 0 : P->n_fp[r], 0, tok0, -1, kv ? T : 0, 0, 0};
+}
+
+}  // namespace
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" kv_status_t kv_attend(kv_pool_t* P, const void* q, const void* k, const void* v, const uint64_t* tree,
+                                 const int32_t* req_ids, const int32_t* n_new, int32_t n_req, int32_t hq,
+                                 float softmax_scale, void* out, void* stream) try {
+  int64_t total;
+  int32_t max_new;
+  kv_status_t st = attend_check("kv_attend", P, q, k, v, tree, req_ids, n_new, n_req, hq, softmax_scale, out, total, max_new);
+  if (st != KV_OK || total == 0) return st;
+  DeviceGuard dg(P->cfg.device);
+  cudaStream_t s = (cudaStream_t)stream;
+  if ((st = refuse_capture("kv_attend", s)) != KV_OK) return st;
+  if ((st = order_after_previous(P, s)) != KV_OK) return st;
+  const AttArgs A = attend_args(P, q, k, v, tree, hq, softmax_scale, out);
+  const int hkv = A.hkv, g = hq / hkv;
+  std::vector<AttUnit> units;
   int64_t tok0 = 0;
   for (int32_t b = 0; b < n_req; ++b) {
-    const bool is_few = !simt && n_new[b] * g <= few_most;
     if (n_new[b] > 0)
-      for (int h = 0; h < hkv; ++h) (is_few ? few : units).push_back(unit(b, h, tok0));
-    if (is_few) few_rows = std::max(few_rows, n_new[b] * g);
+      for (int h = 0; h < hkv; ++h) units.push_back(attend_unit(P, req_ids[b], h, n_new[b], k != nullptr, tok0));
     tok0 += n_new[b];
   }
-  if (simt) {
-    Upload u;
+  Upload u;
+  if (P->decode_impl == KV_DECODE_SIMT) {
     u.add(units.data(), units.size() * sizeof(AttUnit));
     if ((st = ensure(P->attend, u.size)) != KV_OK) return st;
     if ((st = h2d(P, P->attend.ptr, u, s)) != KV_OK) return st;
     KV_CUDA(launch_attend_simt(P, A, (const AttUnit*)P->attend.ptr, (int)units.size(), max_new * g, s));
     return KV_OK;
   }
-  AttPlan pf, pl;
-  const int R = few_rows <= 16 ? 16 : (few_rows <= 32 ? 32 : 64);
-  if (!few.empty()) plan_few(few, g, R, kv, tr, P->sm_count, pf);
-  struct Pass {
-    int u0, u1, max_tiles, cta0;
-  };
-  std::vector<Pass> passes;
-  std::vector<std::vector<AttItem>> by_cta((size_t)P->sm_count);
-  int64_t most = 0, n = 0;
-  int u0 = 0, max_tiles = 0;
-  auto end_pass = [&](int x) {
-    passes.push_back(Pass{u0, x, max_tiles, (int)pl.cta_item.size()});
-    plan_wide(units, u0, x, g, kv, tr, P->sm_count, by_cta, pl);
-    for (auto& c : by_cta) {
-      pl.cta_item.push_back((int32_t)pl.items.size());
-      pl.items.insert(pl.items.end(), c.begin(), c.end());
-      c.clear();
-    }
-    pl.cta_item.push_back((int32_t)pl.items.size());
-    most = std::max(most, n);
-    u0 = x;
-    n = 0;
-    max_tiles = 0;
-  };
-  if (!units.empty()) {
-    for (int x = 0; x < (int)units.size(); ++x) {
-      const int t = block_tiles(units[(size_t)x], g, 0, units[(size_t)x].T * g, kv, tr);
-      if (x > u0 && n + t > kTilesPerPass) end_pass(x);
-      units[(size_t)x].tile_base = (int32_t)n;
-      n += t;
-      max_tiles = std::max(max_tiles, t);
-    }
-    end_pass((int)units.size());
-  }
-  struct Placed {   // a plan's arrays in the upload, its partials behind
-    size_t units, items, ctas, merges, parts;
-  };
-  Upload u;
-  auto place = [&](const std::vector<AttUnit>& un, const AttPlan& p) {
-    Placed x;
-    x.units = u.add(un.data(), un.size() * sizeof(AttUnit));
-    x.items = u.add(p.items.data(), p.items.size() * sizeof(AttItem));
-    x.ctas = u.add(p.cta_item.data(), p.cta_item.size() * sizeof(int32_t));
-    x.merges = u.add(p.merges.data(), p.merges.size() * sizeof(AttMerge));
-    return x;
-  };
-  Placed xf = place(few, pf), xl = place(units, pl);
-  xf.parts = (u.size + 255) & ~size_t(255);
-  xl.parts = xf.parts + (size_t)pf.n_parts * R * kAttPart * sizeof(float);
-  if ((st = ensure(P->attend, xl.parts + (size_t)pl.n_parts * 128 * kAttPart * sizeof(float))) != KV_OK) return st;
-  if ((st = ensure(P->attend_tiles, (size_t)most * (kAttTileBytes + 16), (size_t)kTilesPerPass * (kAttTileBytes + 16))) !=
-      KV_OK)
-    return st;
+  AttSet S;
+  S.plan(units, g, hkv, tree != nullptr, P->sm_count);
+  S.place(u);
+  const size_t end = S.place_parts((u.size + 255) & ~size_t(255));
+  if ((st = attend_room(P, end, S.most)) != KV_OK) return st;
   if ((st = h2d(P, P->attend.ptr, u, s)) != KV_OK) return st;
-  uint8_t* base = (uint8_t*)P->attend.ptr;
-  auto merge = [&](const Placed& x, const AttPlan& p, int part_rows) -> cudaError_t {
-    if (p.merges.empty()) return cudaSuccess;
-    return launch_attend_merge(P, A, (const AttUnit*)(base + x.units), (const AttMerge*)(base + x.merges),
-                               (int)p.merges.size(), p.merge_rows, (const float*)(base + x.parts), part_rows, s);
-  };
-  if (!few.empty()) {
-    KV_CUDA(launch_attend_few(P, R, A, (const AttUnit*)(base + xf.units), (const AttItem*)(base + xf.items),
-                              (const int32_t*)(base + xf.ctas), (int)pf.cta_item.size() - 1, (float*)(base + xf.parts), s));
-    KV_CUDA(merge(xf, pf, R));
-  }
-  const AttUnit* du = (const AttUnit*)(base + xl.units);
-  uint32_t* d_live = (uint32_t*)((uint8_t*)P->attend_tiles.ptr + (size_t)most * kAttTileBytes);
-  for (const Pass& G : passes) {
-    KV_CUDA(launch_attend_tiles(P, A, du + G.u0, G.u1 - G.u0, G.max_tiles, P->attend_tiles.ptr, d_live, s));
-    KV_CUDA(launch_attend_wide(P, A, du, (const AttItem*)(base + xl.items), (const int32_t*)(base + xl.ctas) + G.cta0,
-                               P->sm_count, P->attend_tiles.ptr, d_live, (float*)(base + xl.parts), s));
-  }
-  KV_CUDA(merge(xl, pl, 128));
-  return KV_OK;
+  return S.launch(P, A, S.most, s);
 } catch (const std::bad_alloc&) {
   return fail(KV_ERR_OOM, "kv_attend: host allocation failed");
+}
+
+// The rows of every request with a prefix are in two units: the prefix's, which reads its keys once for all of
+// them, and the request's own.  Both give partials, joined at the end.
+extern "C" kv_status_t kv_attend_shared(kv_pool_t* P, const void* q, const void* k, const void* v, const uint64_t* tree,
+                                        const int32_t* req_ids, const int32_t* prefix_ids, const int32_t* n_new,
+                                        int32_t n_req, int32_t hq, float softmax_scale, void* out, void* stream) try {
+  int64_t total;
+  int32_t max_new;
+  kv_status_t st =
+      attend_check("kv_attend_shared", P, q, k, v, tree, req_ids, n_new, n_req, hq, softmax_scale, out, total, max_new);
+  if (st != KV_OK) return st;
+  if (!prefix_ids) return fail(KV_ERR_INVALID_ARG, "kv_attend_shared: null prefix_ids");
+  // prefixes in the order of their first request, each with its requests
+  std::vector<int32_t> group_of((size_t)n_req, -1), pre_id;
+  std::vector<int64_t> pre_tok((size_t)n_req, 0), tok0((size_t)n_req, 0), group_T;
+  {
+    std::vector<int32_t> at((size_t)P->cfg.max_requests, -1);
+    int64_t t = 0;
+    for (int32_t b = 0; b < n_req; ++b) {
+      const int32_t p = prefix_ids[b];
+      tok0[(size_t)b] = t;
+      t += n_new[b];
+      if (p == -1) continue;
+      if (!req_ok(P, p)) return fail(KV_ERR_INVALID_ARG, "kv_attend_shared: prefix %d not open", p);
+      if (p == req_ids[b]) return fail(KV_ERR_INVALID_ARG, "kv_attend_shared: request %d is its own prefix", p);
+      if (n_new[b] == 0) continue;
+      int32_t& x = at[(size_t)p];
+      if (x < 0) {
+        x = (int32_t)pre_id.size();
+        pre_id.push_back(p);
+        group_T.push_back(0);
+      }
+      group_of[(size_t)b] = x;
+      pre_tok[(size_t)b] = group_T[(size_t)x];
+      if ((group_T[(size_t)x] += n_new[b]) > kMaxNewTokens)
+        return fail(KV_ERR_INVALID_ARG, "kv_attend_shared: more than %d new tokens share prefix %d", kMaxNewTokens, p);
+    }
+  }
+  if (total == 0) return KV_OK;
+  DeviceGuard dg(P->cfg.device);
+  cudaStream_t s = (cudaStream_t)stream;
+  if ((st = refuse_capture("kv_attend_shared", s)) != KV_OK) return st;
+  if ((st = order_after_previous(P, s)) != KV_OK) return st;
+  AttArgs A = attend_args(P, q, k, v, tree, hq, softmax_scale, out);
+  const int hkv = A.hkv, g = hq / hkv;
+
+  // ---- the prefixes' units: tokens that lie together by their first row, others by a list
+  std::vector<AttUnit> pre, own;
+  std::vector<int32_t> tok_map;
+  {
+    const size_t n = pre_id.size();
+    std::vector<int64_t> first(n, -1);
+    std::vector<uint8_t> apart(n, 0);
+    for (int32_t b = 0; b < n_req; ++b) {
+      const int32_t x = group_of[(size_t)b];
+      if (x < 0) continue;
+      if (first[(size_t)x] < 0) first[(size_t)x] = tok0[(size_t)b];
+      if (tok0[(size_t)b] != first[(size_t)x] + pre_tok[(size_t)b]) apart[(size_t)x] = 1;
+    }
+    std::vector<int32_t> map(n, -1);
+    for (size_t x = 0; x < n; ++x)
+      if (apart[x]) {
+        map[x] = (int32_t)tok_map.size();
+        tok_map.resize(tok_map.size() + (size_t)group_T[x]);
+      }
+    for (int32_t b = 0; b < n_req; ++b) {
+      const int32_t x = group_of[(size_t)b];
+      if (x < 0 || map[(size_t)x] < 0) continue;
+      for (int32_t t = 0; t < n_new[b]; ++t)
+        tok_map[(size_t)(map[(size_t)x] + pre_tok[(size_t)b] + t)] = (int32_t)(tok0[(size_t)b] + t);
+    }
+    for (size_t x = 0; x < n; ++x)
+      for (int h = 0; h < hkv; ++h) {
+        AttUnit w = attend_unit(P, pre_id[x], h, (int32_t)group_T[x], false, map[x] < 0 ? first[x] : 0);
+        w.map = map[x];
+        w.joined = 1;
+        pre.push_back(w);
+      }
+  }
+  for (int32_t b = 0; b < n_req; ++b)
+    for (int h = 0; h < hkv && n_new[b] > 0; ++h) {
+      AttUnit w = attend_unit(P, req_ids[b], h, n_new[b], k != nullptr, tok0[(size_t)b]);
+      w.joined = group_of[(size_t)b] >= 0;
+      own.push_back(w);
+    }
+  AttSet SP, SO;
+  SP.plan(pre, g, hkv, tree != nullptr, P->sm_count);
+  SO.plan(own, g, hkv, tree != nullptr, P->sm_count);
+
+  // ---- joins; where a unit's blocks are: units go to a set's two lists in order
+  std::vector<AttJoin> joins;   // of own units with few rows, then of those with many
+  std::vector<AttSrc> srcs;
+  int32_t join_rows = 0;
+  size_t n_few_joins = 0;
+  Upload u;
+  SP.place(u);
+  SO.place(u);
+  const size_t o_map = u.add(tok_map.data(), tok_map.size() * sizeof(int32_t));
+  size_t end = 0, o_joins = 0, o_srcs = 0;
+  {
+    // the partials lie behind everything that is uploaded: sizes first
+    const size_t n_src = SP.pf.srcs.size() + SP.pl.srcs.size() + SO.pf.srcs.size() + SO.pl.srcs.size();
+    size_t n_joins = 0;
+    for (const AttUnit& w : own) n_joins += w.joined ? 1 : 0;
+    joins.resize(n_joins);
+    srcs.reserve(n_src);
+    o_joins = u.add(joins.data(), n_joins * sizeof(AttJoin));
+    o_srcs = u.add(srcs.data(), n_src * sizeof(AttSrc));
+    end = SO.place_parts(SP.place_parts((u.size + 255) & ~size_t(255)));
+    const auto ps = SP.add_srcs(0, srcs), os = SO.add_srcs(0, srcs);
+    auto log2i = [](int x) { int n = 0; while ((1 << n) < x) ++n; return n; };
+    size_t at_few = 0, at_wide = 0;
+    for (size_t x = 0; x < own.size(); ++x) at_wide += own[x].joined && !SO.where[x].wide ? 1 : 0;
+    n_few_joins = at_wide;
+    size_t x = 0;
+    for (int32_t b = 0; b < n_req; ++b)
+      for (int h = 0; h < hkv && n_new[b] > 0; ++h, ++x) {
+        if (!own[x].joined) continue;
+        const AttSet::Where o = SO.where[x], p = SP.where[(size_t)group_of[(size_t)b] * hkv + h];
+        AttJoin J;
+        J.unit = o.index;
+        J.rows = n_new[b] * g;
+        J.own0 = o.wide ? os.second + SO.pl.src0[(size_t)o.index] : os.first + SO.pf.src0[(size_t)o.index];
+        J.own_shift = o.wide ? 7 : log2i(SO.R);
+        J.pre0 = p.wide ? ps.second + SP.pl.src0[(size_t)p.index] : ps.first + SP.pf.src0[(size_t)p.index];
+        J.pre_shift = p.wide ? 7 : log2i(SP.R);
+        J.pre_row = (int32_t)pre_tok[(size_t)b] * g;
+        J.tall = o.wide | (p.wide << 1);
+        joins[o.wide ? at_wide++ : at_few++] = J;
+        join_rows = std::max(join_rows, J.rows);
+      }
+  }
+  const int64_t tiles = std::max(SP.most, SO.most);
+  if ((st = attend_room(P, end, tiles)) != KV_OK) return st;
+  if ((st = h2d(P, P->attend.ptr, u, s)) != KV_OK) return st;
+  uint8_t* base = (uint8_t*)P->attend.ptr;
+  A.tok_map = (const int32_t*)(base + o_map);
+  if ((st = SP.launch(P, A, tiles, s)) != KV_OK) return st;
+  if ((st = SO.launch(P, A, tiles, s)) != KV_OK) return st;
+  const AttJoin* dj = (const AttJoin*)(base + o_joins);
+  const AttSrc* ds = (const AttSrc*)(base + o_srcs);
+  KV_CUDA(launch_attend_join(P, A, (const AttUnit*)(base + SO.xf.units), dj, (int)n_few_joins, join_rows, ds,
+                             (const float*)base, s));
+  KV_CUDA(launch_attend_join(P, A, (const AttUnit*)(base + SO.xl.units), dj + n_few_joins, (int)(joins.size() - n_few_joins),
+                             join_rows, ds, (const float*)base, s));
+  return KV_OK;
+} catch (const std::bad_alloc&) {
+  return fail(KV_ERR_OOM, "kv_attend_shared: host allocation failed");
 }

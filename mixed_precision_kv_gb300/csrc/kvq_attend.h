@@ -9,7 +9,8 @@ constexpr int kMaxNewTokens = 1 << 20;   // new tokens of one request in a call
 constexpr int64_t kMaxRows = int64_t(1) << 31;   // rows of q of a call (512 GB)
 
 // One (request of the call, kv head): T new tokens of g q heads each.  Row i
-// of a unit is (new token i / g, q head kvh * g + i % g).
+// of a unit is (new token i / g, q head kvh * g + i % g).  A shared prefix is a
+// unit too: its rows are the new tokens of every request that has it.
 struct AttUnit {
   int32_t req, kvh;
   int32_t T;          // new tokens
@@ -17,6 +18,10 @@ struct AttUnit {
   int32_t n_fp;       // full-precision list tokens
   int32_t tile_base;  // wide kernel: the unit's first operand tile pair
   int64_t tok0;       // the request's first row in q, k, v and out
+  int32_t map;        // -1: new token t is row tok0 + t of q; else row tok_map[map + t]
+  int32_t n_own;      // new tokens that are keys too: T, or 0 (none: no k and v, or a prefix)
+  int32_t joined;     // the rows' results are joined with another unit's: partials, whatever the plan
+  int32_t pad;
 };
 
 // A block of a unit's rows over a run of its key tiles, done by one CTA.
@@ -34,6 +39,22 @@ struct AttMerge {
 };
 constexpr int kAttPart = kHeadDim + 4;   // floats per row of a partial: O, then m and l
 
+// The partials of a block of rows of a joined unit.
+struct AttSrc {
+  int64_t off;       // first part (floats)
+  int32_t n_parts;
+  int32_t step;      // floats from a part to the next
+};
+// One unit's rows joined with those of the prefix unit that they are also in (no prefix: pre0 < 0).
+struct AttJoin {
+  int32_t unit;              // the request's own unit (in the array the join kernel gets)
+  int32_t rows;
+  int32_t own0, own_shift;   // its first block in the AttSrc array, log2 of a block's rows
+  int32_t pre0, pre_shift;   // the prefix unit's
+  int32_t pre_row;           // row 0 of the request among the prefix unit's rows
+  int32_t tall;              // bit 0: own parts are laid out as 128 rows by channel, bit 1: the prefix's
+};
+
 // Everything a kernel needs besides its plan.
 struct AttArgs {
   const uint8_t* pool;
@@ -44,6 +65,7 @@ struct AttArgs {
   const uint16_t *fpk, *fpv;     // full-precision lists [request][kv head][fp_cap][128], see att_list_at
   const uint16_t *q, *k, *v;     // new tokens, bf16; k and v null: the rows see the cache only
   const uint64_t* tree;          // null: causal
+  const int32_t* tok_map;        // rows of q of units whose tokens do not lie together (AttUnit::map)
   uint16_t* out;                 // bf16
   uint32_t* status;
   float scale_log2;

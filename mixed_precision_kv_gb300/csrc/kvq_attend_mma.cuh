@@ -404,7 +404,8 @@ struct RowMap {
   __device__ __forceinline__ int token(int row) const { return g == 1 ? row : (int)__umulhi((uint32_t)row, magic); }
   __device__ __forceinline__ size_t at(const AttArgs& A, const AttUnit& u, int row) const {
     const int t = token(row);
-    return ((size_t)(u.tok0 + t) * A.hq + (size_t)(u.kvh * g + row - t * g)) * kHeadDim;
+    const int64_t tok = u.map < 0 ? u.tok0 + t : (int64_t)__ldg(A.tok_map + u.map + t);
+    return ((size_t)tok * A.hq + (size_t)(u.kvh * g + row - t * g)) * kHeadDim;
   }
 };
 // 8 values in order8, scaled by 2^e exactly (mul), as binary16

@@ -69,7 +69,7 @@ __device__ __forceinline__ Tiles tiles_of(const AttArgs& A, const AttUnit& u, in
   t.rows = min(rows, u.T * g - row0);
   t.pages = (u.n_pages + 3) >> 2;
   t.lists = t.pages + ((u.n_fp + 127) >> 7);
-  t.all = t.lists + (!A.k ? 0 : (((A.tree ? u.T - 1 : (row0 + t.rows - 1) / g) >> 7) + 1));
+  t.all = t.lists + (u.n_own == 0 ? 0 : (((A.tree ? u.T - 1 : (row0 + t.rows - 1) / g) >> 7) + 1));
   return t;
 }
 

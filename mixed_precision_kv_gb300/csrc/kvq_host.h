@@ -45,7 +45,7 @@ struct Upload {
     const void* p;
     size_t n, off;
   };
-  static constexpr int kMaxPieces = 8;
+  static constexpr int kMaxPieces = 24;
   Piece pieces[kMaxPieces];
   int n_pieces = 0;
   size_t size = 0;

@@ -20,7 +20,8 @@ def test_null_pool(kvq):
     one = np.zeros(1, np.int64).ctypes.data
     for rc in (L.kv_rotate(None, one, one, 1, 1, one, 1, 128, one, 128, None, 0, 0, None, 0, None),
                L.kv_append_rotated(None, one, one, 1, one, 128, one, 128, one, one, 1, None),
-               L.kv_read_tokens(None, one, one, one, 1, 0, one, one, None)):
+               L.kv_read_tokens(None, one, one, one, 1, 0, one, one, None),
+               L.kv_attend_shared(None, one, one, one, None, one, one, one, 1, 8, 1.0, one, None)):
         assert rc == kvq.KV_ERR_INVALID_ARG
         assert b"null pool" in L.kv_last_error()
 
