@@ -459,6 +459,9 @@ KVQ_API kv_status_t kv_pool_sync(kv_pool_t* pool);
 /* Host outputs: number of table entries and of appended tokens of a request. */
 KVQ_API kv_status_t kv_request_info(kv_pool_t* pool, int32_t req_id, int32_t* n_pages, int64_t* n_tokens);
 
+/* The appended tokens of each listed request: n_tokens host int64 [n_req]. */
+KVQ_API kv_status_t kv_request_lengths(kv_pool_t* pool, const int32_t* req_ids, int32_t n_req, int64_t* n_tokens);
+
 /* Canonical, synchronous export of one request, pages in table order (host
  * buffers sized from kv_request_info):
  *   ids [n], is_int2 [n], fill [n] (tokens written), live [n] (bit t = slot t live)

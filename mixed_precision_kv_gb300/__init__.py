@@ -29,7 +29,8 @@ EXPORTED = ["kv_pool_create", "kv_pool_destroy", "kv_request_open", "kv_request_
             "kv_last_error", "kv_decode_attn_noalloc", "kv_decode_timing", "kv_evict_slots_head", "kv_fp_configure",
             "kv_fp_append", "kv_fp_drop", "kv_fp_count", "kv_set_wait_limit", "kv_drop_dead_pages",
             "kv_decode_attn_groups", "kv_alloc_bits3", "kv_attend", "kv_decode_attn_scored", "kv_select_lowest",
-            "kv_rotate", "kv_append_rotated", "kv_read_tokens", "kv_attend_shared"]
+            "kv_rotate", "kv_append_rotated", "kv_read_tokens", "kv_attend_shared",
+            "kv_request_lengths"]
 
 _P = ctypes.c_void_p
 _I32, _I64 = ctypes.c_int32, ctypes.c_int64
@@ -92,6 +93,7 @@ def load_library(path: str = LIB_PATH):
             "kv_set_wait_limit": [_P, _I64],
             "kv_pool_sync": [_P],
             "kv_request_info": [_P, _I32, _P, _P],
+            "kv_request_lengths": [_P, _P, _I32, _P],
             "kv_export_request": [_P, _I32, _P, _P, _P, _P, _P, _P, _P, _P],
             "kv_last_decode_stats": [_P, _P, _P, _P],
             "kv_pool_launch_count": [_P, _P],
@@ -198,7 +200,7 @@ class Rope:
             if axis.shape != (rot // 2,) or (axis.size and (axis.min() < 0 or axis.max() > 3)):
                 raise ValueError("axis must hold rot_dim / 2 values in [0, 3]")
             axis = _np(axis, np.uint8)
-        self.cos_sin, self.axis = cos_sin, axis
+        self.cos_sin, self.axis, self.device = cos_sin, axis, cos_sin.get_device()
         self.n_axes = int(axis.max()) + 1 if axis is not None and axis.size else 1
         self._c = KVRope(cos_sin.data_ptr(), rows, rot, int(bool(interleaved)), self.n_axes, _ptr(axis))
         self._ref = ctypes.addressof(self._c)
@@ -221,6 +223,7 @@ class KVPool:
         self.n_int3_pages = n_int3_pages
         self.n_fp4_pages = n_fp4_pages
         self.device = device
+        self._dev = f"cuda:{device}"
 
     @property
     def handle(self):
@@ -239,11 +242,15 @@ class KVPool:
 
     def open(self) -> int:
         r = ctypes.c_int32()
-        _check(load_library().kv_request_open(self._h, ctypes.byref(r)), "kv_request_open")
+        rc = self._L.kv_request_open(self._h, ctypes.byref(r))
+        if rc:
+            _check(rc, "kv_request_open")
         return r.value
 
     def close_request(self, rid):
-        _check(load_library().kv_request_close(self._h, int(rid)), "kv_request_close")
+        rc = self._L.kv_request_close(self._h, int(rid))
+        if rc:
+            _check(rc, "kv_request_close")
 
     def append(self, k, v, req_ids, bits, stream=None):
         """k, v: torch bf16 CUDA tensors [n][Hkv][128]; req_ids, bits: host sequences [n]."""
@@ -268,54 +275,61 @@ class KVPool:
                              f"device")
 
     def _positions(self, rope, positions, n):
-        torch = _torch_mod()
-        if not self._on_pool_device(rope.cos_sin):
+        """Checks a rotation and the positions of n tokens; the stride between axes."""
+        shape, axes = positions.shape, rope.n_axes
+        if rope.device != self.device:
             raise ValueError("the rotation's table must be on the pool's device")
-        if positions.dtype is not torch.int32 or not self._on_pool_device(positions) or positions.dim() not in (1, 2) or \
-                positions.shape[-1] != n or (1 if positions.dim() == 1 else positions.shape[0]) < rope.n_axes or \
-                (n > 1 and positions.stride(-1) != 1):
-            raise ValueError(f"positions must be an int32 tensor [{n}], or [axes][{n}] with {rope.n_axes} axes, its rows "
+        if positions.dtype is not _torch.int32 or positions.get_device() != self.device or len(shape) not in (1, 2) or \
+                shape[-1] != n or (shape[0] if len(shape) == 2 else 1) < axes or (n > 1 and positions.stride(-1) != 1):
+            raise ValueError(f"positions must be an int32 tensor [{n}], or [axes][{n}] with {axes} axes, its rows "
                              f"contiguous, on the pool's device")
-        if positions.dim() == 2 and rope.n_axes > 1 and positions.stride(0) < n:
+        if axes == 1:
+            return n
+        if positions.stride(0) < n:
             raise ValueError("the axes' positions must not overlap")
-        return positions.stride(0) if positions.dim() == 2 else n
+        return positions.stride(0)
 
     def _rows(self, t, what, heads=None):
         """Checks rows [n][heads][128], a token's heads together; the stride between tokens."""
-        torch = _torch_mod()
-        if t.dtype is not torch.bfloat16 or not self._on_pool_device(t) or t.dim() != 3 or t.shape[2] != HEAD_DIM or \
-                (heads is not None and t.shape[1] != heads) or t.stride(2) != 1 or \
-                (t.shape[1] > 1 and t.stride(1) != HEAD_DIM):
+        shape, stride = t.shape, t.stride()
+        if t.dtype is not _torch.bfloat16 or t.get_device() != self.device or len(shape) != 3 or \
+                shape[2] != HEAD_DIM or (heads is not None and shape[1] != heads) or stride[2] != 1 or \
+                (stride[1] != HEAD_DIM and shape[1] > 1):
             raise ValueError(f"{what} must be a bf16 tensor [n][{'heads' if heads is None else heads}][128] on the pool's "
                              f"device, each token's heads contiguous")
-        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * HEAD_DIM
+        return stride[0] if shape[0] > 1 else shape[1] * HEAD_DIM
 
     def rotate(self, q, rope, positions, k=None, out=None, k_out=None, stream=None):
         """kv_rotate: q (and k) bf16 CUDA [n][heads][128], turned by the tokens' positions (int32 CUDA
         [n], or [axes][n]).  A token's heads lie together; tokens may be apart (slices of a
         projection's output).  Returns the rotated rows (with k: both); out, k_out: where to (q and k
         themselves: in place)."""
-        n = q.shape[0]
         qs = self._rows(q, "q")
-        ks = 0
-        if k is not None:
-            ks = self._rows(k, "k")
-            if k.shape[0] != n:
-                raise ValueError("q and k differ in length")
-        elif k_out is not None:
-            raise ValueError("k_out comes with k")
+        n, hq, _ = q.shape
         ps = self._positions(rope, positions, n)
         if out is None:
-            out = _empty(q.shape, q.dtype, q.device, stream)
-        if k is not None and k_out is None:
-            k_out = _empty(k.shape, k.dtype, k.device, stream)
-        os_, ko = self._rows(out, "out", q.shape[1]), self._rows(k_out, "k_out", k.shape[1]) if k is not None else 0
-        if out.shape != q.shape or (k is not None and k_out.shape != k.shape):
-            raise ValueError("out and k_out must be shaped like q and k")
-        hk = k.shape[1] if k is not None else 0
-        rc = self._L.kv_rotate(self._h, rope._ref, positions.data_ptr(), ps, n, q.data_ptr(), q.shape[1], qs,
-                               out.data_ptr(), os_, k.data_ptr() if hk else None, hk, ks,
-                               k_out.data_ptr() if hk else None, ko, _stream(stream, self.device))
+            out, os_ = _empty(q.shape, q.dtype, q.device, stream), hq * HEAD_DIM
+        else:
+            os_ = self._rows(out, "out", hq)
+            if out.shape[0] != n:
+                raise ValueError("out must be shaped like q")
+        hk, ks, ko, kp, kop = 0, 0, 0, None, None
+        if k is not None:
+            ks, hk = self._rows(k, "k"), k.shape[1]
+            if k.shape[0] != n:
+                raise ValueError("q and k differ in length")
+            if k_out is None:
+                k_out, ko = _empty(k.shape, k.dtype, k.device, stream), hk * HEAD_DIM
+            else:
+                ko = self._rows(k_out, "k_out", hk)
+                if k_out.shape[0] != n:
+                    raise ValueError("k_out must be shaped like k")
+            if hk:
+                kp, kop = k.data_ptr(), k_out.data_ptr()
+        elif k_out is not None:
+            raise ValueError("k_out comes with k")
+        rc = self._L.kv_rotate(self._h, rope._ref, positions.data_ptr(), ps, n, q.data_ptr(), hq, qs, out.data_ptr(), os_,
+                               kp, hk, ks, kop, ko, _stream(stream, self.device))
         if rc:
             _check(rc, "kv_rotate")
         return out if k is None else (out, k_out)
@@ -348,15 +362,19 @@ class KVPool:
         req_ids = np.atleast_1d(_np(req_ids, np.int32))
         first = np.full(req_ids.size, int(first), np.int64) if np.ndim(first) == 0 else _np(first, np.int64)
         if n is None:
-            n = np.array([self.info(r)[1] for r in req_ids], np.int64).reshape(req_ids.size) - first
+            n = np.empty(req_ids.size, np.int64)
+            rc = self._L.kv_request_lengths(self._h, req_ids.ctypes.data, req_ids.size, n.ctypes.data)
+            if rc:
+                _check(rc, "kv_request_lengths")
+            n -= first
         else:
             n = np.full(req_ids.size, int(n), np.int64) if np.ndim(n) == 0 else _np(n, np.int64)
         if req_ids.ndim != 1 or first.shape != req_ids.shape or n.shape != req_ids.shape:
             raise ValueError("req_ids, first and n must be sequences of one length")
         if n.size and int(n.min()) < 0:
             raise ValueError("n must not be negative")
-        device = torch.device("cuda", self.device)
-        k, v = (_empty((int(n.sum()), self.num_kv_heads, HEAD_DIM), dtype, device, stream) for _ in range(2))
+        shape = (int(n.sum()), self.num_kv_heads, HEAD_DIM)
+        k, v = _empty(shape, dtype, self._dev, stream), _empty(shape, dtype, self._dev, stream)
         rc = self._L.kv_read_tokens(self._h, req_ids.ctypes.data, first.ctypes.data, n.ctypes.data, req_ids.size,
                                     int(dtype is torch.float32), k.data_ptr(), v.data_ptr(), _stream(stream, self.device))
         if rc:

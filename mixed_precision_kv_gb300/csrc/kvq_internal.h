@@ -44,6 +44,7 @@ struct AppendJob {
   uint32_t live;       // the page's live mask after the call
   int32_t ntab_req;    // request whose table length to set (-1: none)
   int32_t ntab_len;    // that length
+  int32_t pos0;        // calls of per-request runs: call token t has position pos0 + t
 };
 
 // The jobs of a small append call, passed to the kernel by value (no copy).
@@ -64,6 +65,7 @@ struct RepackJob {
 struct DirectJob {
   int32_t dst;      // INT2 page id
   int32_t tok_off;  // offset of its 32 token indices (slot order)
+  int32_t pos0;     // as AppendJob::pos0
 };
 
 // Work unit of the decode: one (batch row, kv head).  Its splits (page ranges,
@@ -378,6 +380,7 @@ struct kv_pool {
   std::vector<cudaEvent_t> tev;       // ring of [before scan, after scan, after merge] per call
   cudaEvent_t merge_event = nullptr;  // recorded by the launchers between scan and merge when timing
   const kvq::RopeArgs* rope = nullptr;   // the running append rotates K by this (its launchers read it)
+  int32_t* job_pos = nullptr;            // d_pos, if the running append's kernels write their slots' positions
   int64_t first_wait_spins = -1;      // kv_set_wait_limit: bound of the scans' first copy wait (-1: normal)
 };
 

@@ -524,7 +524,6 @@ kv_status_t kv_request_open(kv_pool_t* P, int32_t* req_id) {
   for (int32_t r = 0; r < P->cfg.max_requests; ++r)
     if (!P->reqs[r].open) {
       const uint64_t v = P->reqs[r].version;
-      P->reqs[r] = Request();
       P->reqs[r].open = true;
       P->reqs[r].shape = ++P->shape_clock;
       P->reqs[r].version = v + 1;
@@ -555,7 +554,10 @@ kv_status_t kv_request_close(kv_pool_t* P, int32_t r) {
   }
   if (!P->n_fp.empty()) P->n_fp[r] = 0;
   const uint64_t v = P->reqs[r].version;
+  auto loc = std::move(P->reqs[r].loc);   // its memory stays for the next request of this id
+  loc.clear();
   P->reqs[r] = Request();
+  P->reqs[r].loc = std::move(loc);
   P->reqs[r].version = v + 1;
   return KV_OK;
 }
@@ -564,6 +566,15 @@ kv_status_t kv_request_info(kv_pool_t* P, int32_t r, int32_t* n_pages, int64_t* 
   if (!P || !req_ok(P, r)) return fail(KV_ERR_INVALID_ARG, "kv_request_info: request %d is not open", r);
   if (n_pages) *n_pages = (int32_t)P->reqs[r].table.size();
   if (n_tokens) *n_tokens = (int64_t)P->reqs[r].loc.size();
+  return KV_OK;
+}
+
+kv_status_t kv_request_lengths(kv_pool_t* P, const int32_t* req_ids, int32_t n_req, int64_t* n_tokens) {
+  if (!P) return fail(KV_ERR_INVALID_ARG, "kv_request_lengths: null pool");
+  if (n_req < 0 || (n_req > 0 && (!req_ids || !n_tokens))) return fail(KV_ERR_INVALID_ARG, "kv_request_lengths: bad arguments");
+  for (int32_t i = 0; i < n_req; ++i)
+    if (!req_ok(P, req_ids[i])) return fail(KV_ERR_INVALID_ARG, "kv_request_lengths: request %d is not open", req_ids[i]);
+  for (int32_t i = 0; i < n_req; ++i) n_tokens[i] = (int64_t)P->reqs[req_ids[i]].loc.size();
   return KV_OK;
 }
 
@@ -701,17 +712,20 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
       runs.push_back(BulkRun{req_ids[0], 0, n_tok, 0, c4, 0, c2, 0, 0, 0, 0, 0, 0, 0, false});
     } else if (ok) {
       // several requests: a second pass finds the runs (this keeps the first
-      // pass free of branches and calls)
-      int64_t tb = 0, d4 = 0, d2 = 0, b4 = 0, b2 = 0;
-      for (int64_t t = 1; t <= n_tok; ++t) {
-        d4 += bits[t - 1] == 4u;
-        d2 += bits[t - 1] != 4u;
-        if (t == n_tok || req_ids[t] != req_ids[t - 1]) {
-          runs.push_back(BulkRun{req_ids[tb], tb, t - tb, b4, d4 - b4, b2, d2 - b2, 0, 0, 0, 0, 0, 0, 0, false});
-          tb = t;
-          b4 = d4;
-          b2 = d2;
+      // pass free of branches and calls), the INT4 list how many of a run are in it
+      int64_t b4 = 0;
+      for (int64_t tb = 0, t; tb < n_tok && ok; tb = t) {
+        const int32_t r = req_ids[tb];
+        for (t = tb + 1; t + 8 <= n_tok; t += 8) {
+          int32_t other = 0;
+          for (int y = 0; y < 8; ++y) other |= req_ids[t + y] ^ r;
+          if (other) break;
         }
+        while (t < n_tok && req_ids[t] == r) ++t;
+        const int64_t d4 = std::lower_bound(p4 + b4, p4 + c4, (int32_t)std::min<int64_t>(t, INT32_MAX)) - p4;
+        runs.push_back(BulkRun{r, tb, t - tb, b4, d4 - b4, tb - b4, (t - tb) - (d4 - b4), 0, 0, 0, 0, 0, 0, 0, false});
+        b4 = d4;
+        ok = t - tb >= kPage;   // a short run: the per-token path
       }
     }
     // each run an open request of its own, at least a page of tokens long
@@ -793,9 +807,9 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
   }
   // room for this call's tokens in each position map; growth is geometric
   // (reserving just the new size on every call would copy the whole map)
-  for (const auto& c : cr) {
-    Request& R = P->reqs[c.r];
-    const size_t need = R.loc.size() + (size_t)n_tok;
+  for (size_t x = 0; x < cr.size(); ++x) {
+    Request& R = P->reqs[cr[x].r];
+    const size_t need = R.loc.size() + (size_t)(bulk ? runs[x].n : n_tok);   // (runs: in the order of cr)
     if (R.loc.capacity() < need) R.loc.reserve(std::max(need, 2 * R.loc.capacity()));
   }
   DeviceGuard dg(P->cfg.device);
@@ -842,7 +856,7 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
     uint32_t* const loc = R.loc.data();
     auto add_job = [&](int32_t page, int first, bool int4_list, int64_t a, int64_t n) {
       const int64_t off = (int4_list ? u.o4 : n4 + u.o2) + a;
-      jobs.push_back(AppendJob{page, first, (int32_t)n, (int32_t)off, -1, 0u, -1, 0});
+      jobs.push_back(AppendJob{page, first, (int32_t)n, (int32_t)off, -1, 0u, -1, 0, (int32_t)P0});
       job_req.push_back(r);
       const int32_t* src = (int4_list ? l4 : l2) + a;
       int32_t* pp = pos + (size_t)page * kPage + first;
@@ -916,7 +930,7 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
       P->live[sg] = 0xFFFFFFFFu;
       P->fill[nid] = kPage;
       P->live[nid] = 0xFFFFFFFFu;
-      directs.push_back(DirectJob{nid, (int32_t)(u.o2 + a)});   // its tokens: the INT2 list, uploaded whole
+      directs.push_back(DirectJob{nid, (int32_t)(u.o2 + a), (int32_t)P0});   // its tokens: the INT2 list, uploaded whole
       deferred.push_back(sg);
       app.emplace_back(l2[(size_t)(a + kPage - 1)], nid);
     }
@@ -975,7 +989,7 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
       int32_t& jb = b4 ? c.tail_job : (b3 ? c.tail3_job : (bf ? c.tailf_job : c.stag_job));
       if (jb < 0) {
         jb = (int32_t)jobs.size();
-        jobs.push_back(AppendJob{cur, slot, 0, 0, -1, 0u, -1, 0});
+        jobs.push_back(AppendJob{cur, slot, 0, 0, -1, 0u, -1, 0, 0});
         job_req.push_back(r);
       }
       ++jobs[(size_t)jb].n_slots;
@@ -1000,7 +1014,7 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
       R.shape = ++P->shape_clock;
       R.table.push_back(nid);
       if (c.stag_direct) {
-        directs.push_back(DirectJob{nid, (int32_t)dtoks.size()});
+        directs.push_back(DirectJob{nid, (int32_t)dtoks.size(), 0});
         dtoks.insert(dtoks.end(), c.grp, c.grp + kPage);
         c.ngrp = 0;
       } else {
@@ -1023,7 +1037,18 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
   }
   }   // per-token path
   const int64_t off = bulk ? bulk_job_toks : (int64_t)toks.size();
-  if (P->d_pos) {   // the pages whose slots got other positions
+  // Positions on the device: the kernels of a call of runs write those of the slots they fill (a
+  // token's position is its index in the call plus a constant); other pages are refreshed from the
+  // host by the next call that reads positions.
+  const bool few_jobs = bulk && jobs.size() <= (size_t)SmallAppend::kMaxJobs && off <= SmallAppend::kMaxToks;
+  struct JobPos {
+    kv_pool* P;
+    ~JobPos() { P->job_pos = nullptr; }
+  } job_pos{P};
+  if (P->d_pos && bulk && !few_jobs) {
+    P->job_pos = P->d_pos;
+    for (const auto& j : repacks) P->pos_dirty.push_back(j.dst);
+  } else if (P->d_pos) {   // the pages whose slots got other positions
     for (const auto& j : jobs) P->pos_dirty.push_back(j.page);
     for (const auto& j : repacks) P->pos_dirty.push_back(j.dst);
     for (const auto& j : directs) P->pos_dirty.push_back(j.dst);

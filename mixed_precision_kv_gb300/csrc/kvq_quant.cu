@@ -225,6 +225,17 @@ __device__ __forceinline__ void pack_i4v(uint8_t* __restrict__ img, const uint8_
   }
 }
 
+// Positions of a page's slots first .. first + n - 1 (a new page's others: -1, no token), by one CTA.
+__device__ __forceinline__ void write_positions(int32_t* __restrict__ pos, int32_t page, const int32_t* __restrict__ tk,
+                                                int32_t pos0, int first, int n) {
+  const int t = threadIdx.x;
+  if (t >= kPage || t < first) return;
+  if (t < first + n)
+    pos[(size_t)page * kPage + t] = pos0 + tk[t - first];
+  else if (first == 0)
+    pos[(size_t)page * kPage + t] = -1;
+}
+
 // One CTA per (job, kv head), a warp per token.  A new page (job starting at
 // slot 0) is built as an image in shared memory from zeros and written whole,
 // so its unfilled slots read as code 0, scale 0, zero 0; a page that already
@@ -237,7 +248,7 @@ __global__ void __launch_bounds__(kThreads) append_int4_kernel(
     uint8_t* __restrict__ pool, size_t int4_off, int64_t n2, int hkv, const __nv_bfloat16* __restrict__ k,
     const __nv_bfloat16* __restrict__ v, const AppendJob* __restrict__ jobs, const int32_t* __restrict__ toks,
     Entry* __restrict__ table, int32_t* __restrict__ ntab, uint32_t* __restrict__ status,
-    const __grid_constant__ SmallAppend small, const __grid_constant__ RopeParam<kRope> rope) {
+    const __grid_constant__ SmallAppend small, int32_t* __restrict__ pos, const __grid_constant__ RopeParam<kRope> rope) {
   __shared__ __align__(16) uint8_t img[kInt4Block];
   __shared__ __align__(16) uint8_t vcodes[kPage * kHeadDim];   // V codes of a new page, packed after
   asm volatile("griddepcontrol.wait;" ::: "memory");   // earlier work on the stream (the previous decode) is done
@@ -266,6 +277,7 @@ __global__ void __launch_bounds__(kThreads) append_int4_kernel(
     bad |= quantize_tokens<kThreads / 32, kRope>(rope, blk, k, v, tk + job.tok_off, job.n_slots, job.first_slot, h, hkv,
                                                  vmax, nullptr);
   }
+  if (!kByValue && pos && h == 0) write_positions(pos, job.page, tk + job.tok_off, job.pos0, job.first_slot, job.n_slots);
   flush_vmax(vmax, status);
   if (bad) atomicOr(status, kStatusRange);
   if (h == 0 && threadIdx.x == 0) {
@@ -666,7 +678,7 @@ template <bool kRope>
 __global__ void __launch_bounds__(kThreads) direct_int2_kernel(
     uint8_t* __restrict__ pool, int hkv, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
     const DirectJob* __restrict__ jobs, const int32_t* __restrict__ toks, uint32_t* __restrict__ status,
-    const __grid_constant__ RopeParam<kRope> rope) {
+    int32_t* __restrict__ pos, const __grid_constant__ RopeParam<kRope> rope) {
   __shared__ __align__(16) uint8_t img[kInt4Block];
   __shared__ __align__(16) uint8_t dst[kInt2Block];
   __shared__ __align__(16) uint8_t codes[kPage * kHeadDim];
@@ -674,6 +686,7 @@ __global__ void __launch_bounds__(kThreads) direct_int2_kernel(
   const int h = blockIdx.y;
   bool bad = false;
   float vmax = 0.0f;
+  if (pos && h == 0) write_positions(pos, job.dst, toks + job.tok_off, job.pos0, 0, kPage);
   // every slot is written: no zeroing
   bad |= quantize_tokens<kThreads / 32, kRope>(rope, img, k, v, toks + job.tok_off, kPage, 0, h, hkv, vmax, codes);
   flush_vmax(vmax, status);
@@ -928,7 +941,7 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int4_kernel(
     uint8_t* __restrict__ pool, size_t int4_off, int64_t n2, int hkv, const __nv_bfloat16* __restrict__ k,
     const __nv_bfloat16* __restrict__ v, const AppendJob* __restrict__ jobs, const int32_t* __restrict__ toks,
     Entry* __restrict__ table, int32_t* __restrict__ ntab, uint32_t* __restrict__ status,
-    const __grid_constant__ RopeParam<kRope> rope) {
+    int32_t* __restrict__ pos, const __grid_constant__ RopeParam<kRope> rope) {
   __shared__ __align__(16) uint8_t img[kInt4Block];
   __shared__ __align__(16) uint32_t wbuf[4][128];
   __shared__ KSource<kRope> ksrc;
@@ -937,6 +950,7 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int4_kernel(
   const AppendJob job = jobs[blockIdx.x];
   const int h = blockIdx.y, gr = threadIdx.x >> 5, t = threadIdx.x & 31;
   const int T = toks[job.tok_off + t];
+  if (pos && h == 0 && gr == 0) pos[(size_t)job.page * kPage + t] = job.pos0 + T;
   bool bad = false;
   {
     // K: slot t's row, words (i, gr) i = 0..3 hold channels 32gr + 8i + n in nibble n
@@ -978,7 +992,7 @@ template <bool kRope>
 __global__ void __launch_bounds__(kBulkThreads, 6) bulk_int2_kernel(
     uint8_t* __restrict__ pool, int hkv, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
     const DirectJob* __restrict__ jobs, const int32_t* __restrict__ toks, uint32_t* __restrict__ status,
-    const __grid_constant__ RopeParam<kRope> rope) {
+    int32_t* __restrict__ pos, const __grid_constant__ RopeParam<kRope> rope) {
   __shared__ KSource<kRope> ksrc;
   __shared__ __align__(16) uint8_t img[kInt2Block];
   __shared__ __align__(16) float4 kmeta[4][32];          // per channel of the warp's group: zero, 1/scale, scale, nz
@@ -986,6 +1000,7 @@ __global__ void __launch_bounds__(kBulkThreads, 6) bulk_int2_kernel(
   const DirectJob job = jobs[blockIdx.x];
   const int h = blockIdx.y, gr = threadIdx.x >> 5, t = threadIdx.x & 31;
   const int T = toks[job.tok_off + t];
+  if (pos && h == 0 && gr == 0) pos[(size_t)job.dst * kPage + t] = job.pos0 + T;
   bool bad = false;
   // ---- K: INT4 per token, dequantized, then INT2 per channel across the 32 slots
   {
@@ -1150,11 +1165,11 @@ cudaError_t launch_append(kv_pool* P, const void* k, const void* v, const Append
     if (small)
       return launch_pdl(append_int4_kernel<true, kRope>, grid, dim3(kThreads), 0, s, P->d_pool, P->int4_offset,
                         P->cfg.n_int2_pages, P->cfg.num_kv_heads, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v,
-                        no_jobs, no_toks, P->d_table, P->d_ntab, P->d_status, *small, rope);
+                        no_jobs, no_toks, P->d_table, P->d_ntab, P->d_status, *small, P->job_pos, rope);
     static const SmallAppend none{};
     return launch_pdl(append_int4_kernel<false, kRope>, grid, dim3(kThreads), 0, s, P->d_pool, P->int4_offset,
                       P->cfg.n_int2_pages, P->cfg.num_kv_heads, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v,
-                      d_jobs, d_toks, P->d_table, P->d_ntab, P->d_status, none, rope);
+                      d_jobs, d_toks, P->d_table, P->d_ntab, P->d_status, none, P->job_pos, rope);
   });
 }
 
@@ -1191,7 +1206,7 @@ cudaError_t launch_bulk_int4(kv_pool* P, const void* k, const void* v, const App
     return launch_pdl(bulk_int4_kernel<decltype(is)::value>, dim3((unsigned)n_jobs, (unsigned)P->cfg.num_kv_heads),
                       dim3(kBulkThreads), 0, s, P->d_pool, P->int4_offset, P->cfg.n_int2_pages, P->cfg.num_kv_heads,
                       (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, d_jobs, d_toks, P->d_table, P->d_ntab,
-                      P->d_status, rope);
+                      P->d_status, P->job_pos, rope);
   });
 }
 
@@ -1202,7 +1217,7 @@ cudaError_t launch_bulk_int2(kv_pool* P, const void* k, const void* v, const Dir
   return with_rope(P, [&](auto is, const auto& rope) {
     return launch_pdl(bulk_int2_kernel<decltype(is)::value>, dim3((unsigned)n_jobs, (unsigned)P->cfg.num_kv_heads),
                       dim3(kBulkThreads), 0, s, P->d_pool, P->cfg.num_kv_heads, (const __nv_bfloat16*)k,
-                      (const __nv_bfloat16*)v, d_jobs, d_toks, P->d_status, rope);
+                      (const __nv_bfloat16*)v, d_jobs, d_toks, P->d_status, P->job_pos, rope);
   });
 }
 
@@ -1223,7 +1238,7 @@ cudaError_t launch_direct_int2(kv_pool* P, const void* k, const void* v, const D
   return with_rope(P, [&](auto is, const auto& rope) {
     return launch_pdl(direct_int2_kernel<decltype(is)::value>, grid, dim3(kThreads), 0, s, P->d_pool,
                       P->cfg.num_kv_heads, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, d_jobs, d_toks,
-                      P->d_status, rope);
+                      P->d_status, P->job_pos, rope);
   });
 }
 

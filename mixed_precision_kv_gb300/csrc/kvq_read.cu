@@ -35,11 +35,26 @@ struct ReadArgs {
   int32_t max_pages, hkv;
 };
 
-constexpr int kReadThreads = 128;
+constexpr int kReadThreads = 256;
 
 __device__ __forceinline__ float half_lo(uint32_t w) { return __half2float(__ushort_as_half((uint16_t)w)); }
 __device__ __forceinline__ float half_hi(uint32_t w) { return __half2float(__ushort_as_half((uint16_t)(w >> 16))); }
 __device__ __forceinline__ float half_of(const uint8_t* p) { return __half2float(*reinterpret_cast<const __half*>(p)); }
+
+// The code in the bits `mask` of w, at bit p, as the float code * 2^p (p <= 19), exactly: or-ed into the
+// mantissa of 2^23, and 2^23 taken off.  Conversions of integers run at a quarter of the rate.  With the
+// scale times 2^-p (exact) one fused multiply-add then gives code * scale + zero, rounded once.
+__device__ __forceinline__ float code_at(uint32_t w, uint32_t mask) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "n"(0x4B000000));
+  return __uint_as_float(d);
+}
+// (a0, a1) * (s0, s1) + (z0, z1) of two codes from code_at
+__device__ __forceinline__ void value2(float& x0, float& x1, float a0, float a1, float s0, float s1, float z0, float z1) {
+  asm("{.reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%8, %8};\n add.rn.f32x2 a, a, b;\n"
+      " mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;}"
+      : "=f"(x0), "=f"(x1) : "f"(a0), "f"(a1), "f"(s0), "f"(s1), "f"(z0), "f"(z1), "f"(-8388608.0f));
+}
 
 // 8 values of a row, rounded once to bf16 or kept
 template <bool kF32>
@@ -56,149 +71,164 @@ __device__ __forceinline__ void put8(void* out, size_t at, const float (&x)[8]) 
   }
 }
 
-// K: channels 8 c8 .. 8 c8 + 7 of slot t.
-__device__ __forceinline__ void k_values(const uint8_t* b, int cls, int t, int c8, float (&x)[8]) {
-  const int gr = c8 >> 2, i = c8 & 3;
-  if (cls == kClsInt2) {
-    const uint32_t w = __ldg(reinterpret_cast<const uint16_t*>(b + kI2KCodes + 32 * t + 2 * c8));
-    // channel 8 c8 + n is in pair (gr, i >> 1, 4 (n >> 2) + (n & 3)), the half by i & 1 (the first pair swapped)
-    const uint4* p = reinterpret_cast<const uint4*>(b + kI2KMeta + 4 * ((gr * 2 + (i >> 1)) * 8));
-    const uint4 s0 = __ldg(p), s1 = __ldg(p + 1), z0 = __ldg(p + 16), z1 = __ldg(p + 17);
-    const uint32_t s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-    const uint32_t z[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const bool hi = ((i & 1) != 0) != (n == 0);
-      x[n] = fmaf((float)((w >> (2 * n)) & 3u), hi ? half_hi(s[n]) : half_lo(s[n]), hi ? half_hi(z[n]) : half_lo(z[n]));
-    }
-  } else if (cls == kClsInt4) {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(b + kI4KCodes + 64 * t + 16 * i + 4 * gr));
-    const uint32_t m = __ldg(reinterpret_cast<const uint32_t*>(b + kI4KMeta + 16 * t + 4 * gr));
-    const float s = half_lo(m), z = half_hi(m);
-#pragma unroll
-    for (int n = 0; n < 8; ++n) x[n] = fmaf((float)((w >> (4 * n)) & 15u), s, z);
-  } else if (cls == kClsInt3) {
-    const uint32_t m = __ldg(reinterpret_cast<const uint32_t*>(b + kI3KMeta + 16 * t + 4 * gr));
-    const float s = half_lo(m), z = half_hi(m);
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      const int c = 8 * c8 + n;
-      const uint32_t code = (((uint32_t)b[i3k_lo_byte(t, c)] >> i3k_lo_shift(c)) & 3u) |
-                            ((((uint32_t)b[i3k_hi_byte(t, c)] >> i3k_hi_shift(c)) & 1u) << 2);
-      x[n] = fmaf((float)code, s, z);
-    }
-  } else {
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(b + kF4KCodes + 64 * t + 16 * i + 4 * gr));
-    const float s = half_of(b + kF4KScale + 8 * t + 2 * gr);
-#pragma unroll
-    for (int n = 0; n < 8; ++n) x[n] = e2m1_value((w >> (8 * (n & 3) + 4 * (n >> 2))) & 15u) * s;
-  }
-}
-
-// V: the code words of channels 8 o .. 8 o + 7, slots 8 j .. 8 j + 7, and the slots' scales and zeros.
-struct VBlock {
-  uint32_t w[8];
-  uint4 s, z;
+// INT3 and FP4 pages: channels c0 .. c0 + 7 of slot t of K or V, code by code.
+struct Eight {
+  float x[8];
 };
-__device__ __forceinline__ void v_load(const uint8_t* b, int cls, int j, int o, VBlock& B) {
-  const int m = o >> 1, e = o & 1, gr = o >> 2;
+__device__ __noinline__ Eight other_values(const uint8_t* b, int cls, bool is_k, int t, int c0) {
+  Eight r;
+  const int gr = c0 >> 5, mi = v_meta_index(t, gr);
+  if (cls == kClsInt3) {
+    const uint8_t* m = is_k ? b + kI3KMeta + 16 * t + 4 * gr : b + kI3VMeta + 2 * mi;
+    const float s = half_of(m), z = half_of(m + (is_k ? 2 : 256));
 #pragma unroll
-  for (int r = 0; r < 8; ++r)
-    B.w[r] = cls == kClsInt2 ? __ldg(reinterpret_cast<const uint32_t*>(b + kI2VCodes + 16 * (32 * (m >> 2) + 4 * r + j) + 4 * (m & 3)))
-             : cls == kClsInt3 ? 0u
-                               : __ldg(reinterpret_cast<const uint32_t*>(b + kI4VCodes + 16 * (32 * (m >> 1) + 4 * r + j) + 4 * (2 * (m & 1) + e)));
-  const int meta = cls == kClsInt2 ? kI2VMeta : (cls == kClsInt4 ? kI4VMeta : (cls == kClsInt3 ? kI3VMeta : kF4VScale));
-  B.s = __ldg(reinterpret_cast<const uint4*>(b + meta + 64 * gr + 16 * j));
-  B.z = cls == kClsFp4 ? make_uint4(0u, 0u, 0u, 0u) : __ldg(reinterpret_cast<const uint4*>(b + meta + 256 + 64 * gr + 16 * j));
-}
-// The row of slot 8 j + k.
-__device__ __forceinline__ void v_values(const VBlock& B, const uint8_t* b, int cls, int j, int o, int k, float (&x)[8]) {
-  // slots k and k + 4 share a word of scales
-  const uint32_t sw = (k & 3) == 0 ? B.s.x : ((k & 3) == 1 ? B.s.y : ((k & 3) == 2 ? B.s.z : B.s.w));
-  const uint32_t zw = (k & 3) == 0 ? B.z.x : ((k & 3) == 1 ? B.z.y : ((k & 3) == 2 ? B.z.z : B.z.w));
-  const float s = k < 4 ? half_lo(sw) : half_hi(sw), z = k < 4 ? half_lo(zw) : half_hi(zw);
-  const int e = o & 1;
-  if (cls == kClsInt2) {
-    const int half = (k >> 2) ^ ((e == 0 && (k & 3) == 0) ? 1 : 0), sh = 8 * e + 16 * half + 2 * (k & 3);
-#pragma unroll
-    for (int r = 0; r < 8; ++r) x[r] = fmaf((float)((B.w[r] >> sh) & 3u), s, z);
-  } else if (cls == kClsInt4) {
-#pragma unroll
-    for (int r = 0; r < 8; ++r) x[r] = fmaf((float)((B.w[r] >> (4 * k)) & 15u), s, z);
-  } else if (cls == kClsInt3) {
-    const int t = 8 * j + k;
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int c = 8 * o + r;
-      const uint32_t code = (((uint32_t)b[i3v_lo_byte(t, c)] >> i3v_lo_shift(t)) & 3u) |
-                            ((((uint32_t)b[i3v_hi_byte(t, c)] >> i3v_hi_shift(t, c)) & 1u) << 2);
-      x[r] = fmaf((float)code, s, z);
+    for (int n = 0; n < 8; ++n) {
+      const int c = c0 + n;
+      const uint32_t code = is_k ? (((uint32_t)b[i3k_lo_byte(t, c)] >> i3k_lo_shift(c)) & 3u) |
+                                       ((((uint32_t)b[i3k_hi_byte(t, c)] >> i3k_hi_shift(c)) & 1u) << 2)
+                                 : (((uint32_t)b[i3v_lo_byte(t, c)] >> i3v_lo_shift(t)) & 3u) |
+                                       ((((uint32_t)b[i3v_hi_byte(t, c)] >> i3v_hi_shift(t, c)) & 1u) << 2);
+      r.x[n] = fmaf((float)code, s, z);
     }
   } else {
+    const float s = half_of(is_k ? b + kF4KScale + 8 * t + 2 * gr : b + kF4VScale + 2 * mi);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) x[r] = e2m1_value((B.w[r] >> (8 * (k & 3) + 4 * (k >> 2))) & 15u) * s;
+    for (int n = 0; n < 8; ++n) {
+      const int c = c0 + n;
+      const uint32_t code = is_k ? (uint32_t)b[f4k_byte(t, c)] >> f4k_shift(c) : (uint32_t)b[f4v_byte(t, c)] >> f4v_shift(t);
+      r.x[n] = e2m1_value(code & 15u) * s;
+    }
   }
+  return r;
 }
 
-// A CTA per (page, request, kv head): warps 0 and 1 take K, a run of 8 channels of a
-// slot per lane at a time (16 lanes write a row); warps 2 and 3 V, whose codes lie by
-// channel: a lane takes 8 channels x 8 slots, a code word per channel, and gives 8
-// rows 16 bytes each.  Bound by the rows written.
+// A CTA per (page, request): warps 2 x and 2 x + 1 take K and V of heads x, x + 4, ..  K: a lane takes a run
+// of 8 channels of a slot at a time, 16 lanes a row, so an INT2 page's scales, which go by channel, stay in
+// registers over the page.  V, whose codes lie by channel: 8 channels x 8 slots at a time, a code word per
+// channel, which give 8 rows 16 bytes each (8 lanes: 128 bytes of a row).
 template <bool kF32>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadArgs A,
                                                             const __grid_constant__ ReadRows by_value,
                                                             const ReadRow* __restrict__ d_rows) {
   const ReadRow R = d_rows ? d_rows[blockIdx.y] : by_value.r[blockIdx.y];
   if ((int)blockIdx.x >= R.n_pages) return;
-  const int h = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool is_k = (warp & 1) == 0;
+  void* const out = is_k ? A.k : A.v;
+  if (!out) return;
   const Entry e = A.table[(size_t)R.req * A.max_pages + blockIdx.x];
   // this lane's slot: its place in the range (-1: none, or outside)
   const int p = A.pos[(size_t)e.id * kPage + lane];
   const int mine = p >= R.first && p - R.first < R.n ? p - R.first : -1;
   if (!__any_sync(0xFFFFFFFFu, mine >= 0)) return;
-  const uint32_t live = A.hdead ? e.live & ~A.hdead[(size_t)e.id * A.hkv + h] : e.live;
   AttArgs T;
   T.pool = A.pool; T.int4_off = A.int4_off; T.int3_off = A.int3_off; T.fp4_off = A.fp4_off;
   T.n2 = A.n2; T.n3b = A.n3b; T.nfb = A.nfb; T.hkv = A.hkv;
-  const uint8_t* b;
-  const int cls = att_page(T, e.id, h, b);
-  const size_t step = (size_t)A.hkv * kHeadDim, base = (size_t)R.row0 * step + (size_t)h * kHeadDim;
-  if (warp < 2) {
-    if (!A.k) return;
-    const int c8 = lane & 15;
-#pragma unroll 4
-    for (int y = 0; y < 8; ++y) {
-      const int t = 4 * y + 2 * warp + (lane >> 4);
+  const size_t step = (size_t)A.hkv * kHeadDim;
+#pragma unroll 1
+  for (int h = warp >> 1; h < A.hkv; h += kReadThreads / 64) {
+    const uint32_t live = A.hdead ? e.live & ~A.hdead[(size_t)e.id * A.hkv + h] : e.live;
+    const uint8_t* b;
+    const int cls = att_page(T, e.id, h, b);
+    const size_t base = (size_t)R.row0 * step + (size_t)h * kHeadDim;
+    // row of slot t: values x, or zeros where the slot is dead; rows outside the range are left
+    auto store = [&](int t, int c0, float (&x)[8]) {
       const int row = __shfl_sync(0xFFFFFFFFu, mine, t);
-      float x[8];
-      if (row >= 0) {
-        if ((live >> t) & 1u) {
-          k_values(b, cls, t, c8, x);
-        } else {
+      if (!((live >> t) & 1u)) {
 #pragma unroll
-          for (int n = 0; n < 8; ++n) x[n] = 0.0f;
-        }
-        put8<kF32>(A.k, base + (size_t)row * step + 8 * c8, x);
+        for (int n = 0; n < 8; ++n) x[n] = 0.0f;
       }
-    }
-  } else {
-    if (!A.v) return;
-    const int o = (lane & 7) + 8 * (warp & 1), j = lane >> 3;   // 8 lanes: half a row
-    VBlock B;
-    v_load(b, cls, j, o, B);
+      if (row >= 0) put8<kF32>(out, base + (size_t)row * step + c0, x);
+    };
+    if (cls > kClsInt4) {
+#pragma unroll 1
+      for (int y = 0; y < 16; ++y) {
+        const int t = 2 * y + (lane >> 4), c0 = 8 * (lane & 15);
+        Eight v = other_values(b, cls, is_k, t, c0);
+        store(t, c0, v.x);
+      }
+    } else if (is_k) {
+      const int c8 = lane & 15, hi = lane >> 4, gr = c8 >> 2, i = c8 & 3;
+      if (cls == kClsInt2) {
+        // channel 8 c8 + n is in pair (gr, i >> 1, n), the half by i & 1 (the first pair swapped)
+        float s[8], z[8];
+        {
+          const uint4* m = reinterpret_cast<const uint4*>(b + kI2KMeta + 4 * ((gr * 2 + (i >> 1)) * 8));
+          const uint4 s0 = __ldg(m), s1 = __ldg(m + 1), z0 = __ldg(m + 16), z1 = __ldg(m + 17);
+          const uint32_t sw[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+          const uint32_t zw[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int t = 8 * j + k;
-      const int row = __shfl_sync(0xFFFFFFFFu, mine, t);
-      float x[8];
-      if (row >= 0) {
-        if ((live >> t) & 1u) {
-          v_values(B, b, cls, j, o, k, x);
-        } else {
-#pragma unroll
-          for (int n = 0; n < 8; ++n) x[n] = 0.0f;
+          for (int n = 0; n < 8; ++n) {
+            const uint32_t sh = ((i & 1) != 0) != (n == 0) ? 16u : 0u;
+            s[n] = half_lo(sw[n] >> sh) * (1.0f / (float)(1 << (2 * n)));
+            z[n] = half_lo(zw[n] >> sh);
+          }
         }
-        put8<kF32>(A.v, base + (size_t)row * step + 8 * o, x);
+#pragma unroll 1
+        for (int y0 = 0; y0 < 16; y0 += 8) {
+          uint32_t w[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            w[y] = __ldg(reinterpret_cast<const uint16_t*>(b + kI2KCodes + 32 * (2 * (y0 + y) + hi) + 2 * c8));
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            float x[8];
+#pragma unroll
+            for (int n = 0; n < 8; n += 2)
+              value2(x[n], x[n + 1], code_at(w[y], 3u << (2 * n)), code_at(w[y], 12u << (2 * n)), s[n], s[n + 1], z[n], z[n + 1]);
+            store(2 * (y0 + y) + hi, 8 * c8, x);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int y0 = 0; y0 < 16; y0 += 8) {
+          uint32_t w[8], m[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const int t = 2 * (y0 + y) + hi;
+            w[y] = __ldg(reinterpret_cast<const uint32_t*>(b + kI4KCodes + 64 * t + 16 * i + 4 * gr));
+            m[y] = __ldg(reinterpret_cast<const uint32_t*>(b + kI4KMeta + 16 * t + 4 * gr));
+          }
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const float s = half_lo(m[y]), z = half_hi(m[y]);
+            float x[8];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const float sp = s * (1.0f / (float)(1 << (4 * n)));
+              value2(x[n], x[n + 4], code_at(w[y], 15u << (4 * n)), code_at(w[y] >> 16, 15u << (4 * n)), sp, sp, z, z);
+            }
+            store(2 * (y0 + y) + hi, 8 * c8, x);
+          }
+        }
+      }
+    } else {
+      const int j = lane >> 3;
+#pragma unroll 1
+      for (int o = lane & 7; o < 16; o += 8) {   // channels 8 o .. 8 o + 7
+        const int mt = o >> 1, ev = o & 1, gr = o >> 2;
+        const int meta = cls == kClsInt2 ? kI2VMeta : kI4VMeta;
+        const uint8_t* cw = cls == kClsInt2 ? b + kI2VCodes + 16 * (32 * (mt >> 2) + j) + 4 * (mt & 3)
+                                            : b + kI4VCodes + 16 * (32 * (mt >> 1) + j) + 4 * (2 * (mt & 1) + ev);
+        uint32_t w[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) w[r] = __ldg(reinterpret_cast<const uint32_t*>(cw + 64 * r));
+        const uint4 s4 = __ldg(reinterpret_cast<const uint4*>(b + meta + 64 * gr + 16 * j));
+        const uint4 z4 = __ldg(reinterpret_cast<const uint4*>(b + meta + 256 + 64 * gr + 16 * j));
+        const uint32_t sw[4] = {s4.x, s4.y, s4.z, s4.w}, zw[4] = {z4.x, z4.y, z4.z, z4.w};   // slots k and k + 4
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float s = half_lo(sw[k & 3] >> (k < 4 ? 0 : 16)), z = half_lo(zw[k & 3] >> (k < 4 ? 0 : 16));
+          // INT2: byte ev (slots 0..3) or ev + 2 (4..7) of a word, slot 8 j and 8 j + 4 the other way round for ev 0
+          const uint32_t sh = cls == kClsInt2 ? 8u * ev + 2u * (k & 3) + (((k >> 2) != 0) != (ev == 0 && (k & 3) == 0) ? 16u : 0u)
+                                              : 4u * k;
+          const uint32_t mask = cls == kClsInt2 ? 3u : 15u;
+          float x[8];
+#pragma unroll
+          for (int r = 0; r < 8; r += 2)
+            value2(x[r], x[r + 1], code_at(w[r] >> sh, mask), code_at(w[r + 1] >> sh, mask), s, s, z, z);
+          store(8 * j + k, 8 * o, x);
+        }
       }
     }
   }
@@ -273,7 +303,7 @@ extern "C" kv_status_t kv_read_tokens(kv_pool_t* P, const int32_t* req_ids, cons
   A.v = v;
   A.max_pages = P->cfg.max_pages_per_request;
   A.hkv = hkv;
-  const dim3 grid((unsigned)max_pages, (unsigned)rows.size(), (unsigned)hkv);
+  const dim3 grid((unsigned)max_pages, (unsigned)rows.size());
   ++P->launches;
   if (fp32)
     read_kernel<true><<<grid, kReadThreads, 0, s>>>(A, by_value, d_rows);

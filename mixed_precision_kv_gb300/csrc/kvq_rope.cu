@@ -43,7 +43,7 @@ __device__ __forceinline__ void row_store(uint16_t* p, const uint4& v, bool alig
 // A thread takes item i of a row (kvq_rope.h) of one token, its factors once and
 // then every `lines`-th head of q and k together; 256 / (8 lines) tokens a CTA.
 template <bool kAligned>
-__global__ void __launch_bounds__(kRotThreads) rotate_kernel(const __grid_constant__ RopeArgs R,
+__global__ void __launch_bounds__(kRotThreads, 5) rotate_kernel(const __grid_constant__ RopeArgs R,
                                                              const __grid_constant__ RotTensor Q,
                                                              const __grid_constant__ RotTensor K, int64_t n, int lines,
                                                              uint32_t* __restrict__ status) {
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kRotThreads) rotate_kernel(const __grid_consta
   uint16_t* qy = Q.y + (size_t)t * (size_t)Q.ys;
   uint16_t* ky = K.y + (size_t)t * (size_t)K.ys;
   const int all = Q.heads + K.heads;
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 2;
   for (int h0 = line; h0 < all; h0 += kAhead * lines) {
     uint4 x[kAhead], z[kAhead];
 #pragma unroll
