@@ -703,13 +703,20 @@ __global__ void __launch_bounds__(kThreads) direct_int2_kernel(
 }
 
 // ---- bulk kernels: a CTA of 4 warps per (page, kv head), warp gr = the
-// 32-channel group gr, lane t = slot t (its token's 32 channels of the group
-// held in registers).  A token's group is quantized without any cross-lane
-// step; INT4 metadata comes from packed bf16 min/max, per-channel INT2 K
-// statistics from warp reductions across the 32 tokens.  The arithmetic of
-// every code, scale and zero is the one qcode_fast / make_meta apply (same
-// operations, same order), so the results are bit-identical.
+// 32-channel group gr, lane t = slot t.  The page's K and V rows come to shared
+// memory first (V while K is worked on; K rotated on the way where the call asks
+// for it), and a lane reads its token's 32 channels of the group from there, 8 at a
+// time.  A token's group is quantized without any cross-lane step; INT4 metadata
+// comes from packed bf16 min / max, per-channel INT2 K statistics from warp
+// reductions across the 32 tokens.  The results are those of make_meta and
+// qcode_fast, bit for bit.
+//
+// What bounds them: instruction issue.  The loops over the 8-channel pieces are kept
+// as loops and the rare exact divisions out of line: with everything unrolled the
+// INT2 kernel was 105 KB of code, and a third of its stalls were waits for
+// instructions.
 constexpr int kBulkThreads = 128;
+constexpr float kRound = 12582912.0f;    // 1.5 * 2^23: x + kRound - kRound is x rounded to an integer, ties to even
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -734,17 +741,66 @@ __device__ __forceinline__ float redux_max(float x) {
   return d;
 }
 
-// The 32 bf16 channels 32gr .. 32gr + 31 of token T, kv head h (16 words); step:
-// elements from a token's rows to the next token's.
-__device__ __forceinline__ void load_group(const __nv_bfloat16* __restrict__ src, int T, int h, size_t step, int gr,
-                                           uint32_t (&w)[16]) {
-  const uint4* p = reinterpret_cast<const uint4*>(src + (size_t)T * step + (size_t)h * kHeadDim + 32 * gr);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint4 v = __ldg(p + q);
-    w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
-  }
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 d;
+  asm("{.reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) { return add2(a, F2{-b.x, -b.y}); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("{.reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("{.reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// Codes of two values: rint((x - z) rs) clamped to [0, QMAX], negz = -z, rs the approximate
+// reciprocal of the scale (0 where the scale is: code 0).  far: the largest distance of a quotient from
+// its integer so far; past kTie the exact quotient could round the other way (qcode_fast), and the
+// caller takes the 8 codes again, divided.
+constexpr float kTie = 0.49999f;
+template <int QMAX>
+__device__ __forceinline__ F2 codes2(F2 x, F2 negz, F2 rs, float& far) {
+  const F2 q = mul2(add2(x, negz), rs);
+  const F2 c = add2(add2(q, F2{kRound, kRound}), F2{-kRound, -kRound});
+  const F2 d = sub2(q, c);
+  far = fmaxf(fmaxf(far, fabsf(d.x)), fabsf(d.y));
+  return F2{fminf(fmaxf(c.x, 0.0f), (float)QMAX), fminf(fmaxf(c.y, 0.0f), (float)QMAX)};
+}
+__device__ __forceinline__ float code_divided(float x, float z, float s, float qmax) {
+  return s == 0.0f ? 0.0f : fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x, z), s)), 0.0f), qmax);
+}
+// 8 codes, divided: of bf16 values, and (INT2 K) of the INT4 values of a code word, channel by channel
+__device__ __noinline__ uint32_t divided_nib8(uint4 v, float z, float s) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t d = 0u;
+#pragma unroll 1
+  for (int n = 0; n < 4; ++n) {
+    const uint32_t x = n == 0 ? w[0] : (n == 1 ? w[1] : (n == 2 ? w[2] : w[3]));
+    d |= (uint32_t)code_divided(bf_lo(x), z, s, 15.0f) << (8 * n);
+    d |= (uint32_t)code_divided(bf_hi(x), z, s, 15.0f) << (8 * n + 4);
+  }
+  return d;
+}
+__device__ __noinline__ uint32_t divided_crumb8(uint32_t cw, float s4, float z4, const float* z, const float* s) {
+  uint32_t d = 0u;
+#pragma unroll 1
+  for (int n = 0; n < 8; ++n)
+    d |= (uint32_t)code_divided(__fmaf_rn((float)((cw >> (4 * n)) & 15u), s4, z4), z[n], s[n], 3.0f) << (2 * n);
+  return d;
+}
+__device__ __noinline__ float divided_one(float x, float z, float s, float qmax) { return code_divided(x, z, s, qmax); }
 
 // A page's 32 K rows, rotated, in shared memory (rows 272 bytes apart, so that the
 // reads of a group by 32 lanes hit distinct banks).  The channels that a rotation
@@ -772,100 +828,78 @@ __device__ __forceinline__ void rotate_page(RopeTile& K, const RopeArgs& R, cons
     K.row[t][b] = z;
   }
 }
-// K of the warp's group of slot t: rotated in shared memory or as it is.
-template <bool kRope>
-struct KSource {
-  RopeTile tile;
-};
-template <>
-struct KSource<false> {};
-template <bool kRope>
-__device__ __forceinline__ void load_k_group(KSource<kRope>& S, const RopeParam<kRope>& R, const __nv_bfloat16* __restrict__ k,
-                                             const int32_t* __restrict__ toks, int T, int t, int h, int hkv, int gr,
-                                             uint32_t (&w)[16], bool& bad) {
-  if constexpr (kRope) {
-    rotate_page(S.tile, R, k, toks, h, bad);
-    __syncthreads();
+// K or V rows of a page as they are, asynchronously.
+__device__ __forceinline__ void fetch_page(RopeTile& X, const __nv_bfloat16* __restrict__ src, const int32_t* __restrict__ toks,
+                                           int h, size_t step) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint4 v = S.tile.row[t][4 * gr + q];
-      w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
-    }
-  } else {
-    load_group(k, T, h, k_step<kRope>(R, hkv), gr, w);
+  for (int y = 0; y < 4; ++y) {
+    const int t = (int)(threadIdx.x >> 4) + 8 * y, c = threadIdx.x & 15;
+    const __nv_bfloat16* p = src + (size_t)__ldg(toks + t) * step + (size_t)h * kHeadDim + 8 * c;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(&X.row[t][c])), "l"(p)
+                 : "memory");
   }
 }
-
-// Group metadata of 32 bf16 values (INT4): min / max exactly, NaN carried so
-// that the range check sees it (NaN, Inf or |x| > 65504 sets `bad`).
-__device__ __forceinline__ GroupMeta meta_i4(const uint32_t (&w)[16], bool& bad) {
-  uint32_t mn2 = w[0], mx2 = w[0];
-#pragma unroll
-  for (int j = 1; j < 16; ++j) {
-    mn2 = bf2_min(mn2, w[j]);
-    mx2 = bf2_max(mx2, w[j]);
+// The rows of a page: V's on their way, K's in shared memory.
+template <bool kRope>
+__device__ __forceinline__ void start_page(RopeTile& K, RopeTile& V, const RopeParam<kRope>& R,
+                                           const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
+                                           const int32_t* __restrict__ toks, int h, int hkv, bool& bad) {
+  if constexpr (!kRope) {
+    fetch_page(K, k, toks, h, k_step<kRope>(R, hkv));
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  const float a = bf_lo(mn2), b = bf_hi(mn2), c = bf_lo(mx2), d = bf_hi(mx2);
+  fetch_page(V, v, toks, h, v_step<kRope>(R, hkv));
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  if constexpr (kRope) rotate_page(K, R, k, toks, h, bad);
+  else asm volatile("cp.async.wait_group 1;" ::: "memory");
+  __syncthreads();
+}
+__device__ __forceinline__ void v_ready() {
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+}
+
+// Metadata of a token's group at row (4 pieces of 8 bf16 channels): min / max exactly, NaN
+// carried so that the range check sees it (NaN, Inf or |x| > 65504 sets `bad`).
+__device__ __forceinline__ GroupMeta meta_i4(const uint4* row, bool& bad, float& mn, float& mx) {
+  uint32_t lo = 0u, hi = 0u;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint4 v = row[q];
+    const uint32_t a = bf2_min(bf2_min(v.x, v.y), bf2_min(v.z, v.w)), b = bf2_max(bf2_max(v.x, v.y), bf2_max(v.z, v.w));
+    lo = q ? bf2_min(lo, a) : a;
+    hi = q ? bf2_max(hi, b) : b;
+  }
+  const float a = bf_lo(lo), b = bf_hi(lo), c = bf_lo(hi), d = bf_hi(hi);
   bad |= out_of_range(a) | out_of_range(b) | out_of_range(c) | out_of_range(d);
-  return make_meta(fminf(a, b), fmaxf(c, d), 15.0f);
+  mn = fminf(a, b);
+  mx = fmaxf(c, d);
+  return make_meta(mn, mx, 15.0f);
 }
+__device__ __forceinline__ float rcp_of(const GroupMeta& m) { return m.nz ? approx_rcp(m.sf) : 0.0f; }
 
-// Codes of 8 values of one group: qcode_fast for each (same operations), the
-// exact division redone for the whole chunk when any of its quotients lies
-// near a rounding tie (rare).
-template <int QMAX>
-__device__ __forceinline__ void codes8(const float (&x)[8], const GroupMeta& m, float rs, float (&c)[8]) {
-  bool tie = false;
+// INT4 codes of 8 channels as nibbles; c: the codes as floats, pairs (2 j, 2 j + 1) (after a tie: read off the word).
+__device__ __forceinline__ uint32_t quant_i4_8(uint4 v, const GroupMeta& m, float rs, F2 (&c)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float far = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float u = __fsub_rn(x[j], m.zf);
-    const float q0 = u * rs;
-    const float r = rintf(q0);
-    tie |= !(fabsf(fabsf(q0 - r) - 0.5f) > 1e-5f);
-    c[j] = fminf(fmaxf(r, 0.0f), (float)QMAX);
-  }
-  if (tie) {
+  for (int j = 0; j < 4; ++j) c[j] = codes2<15>(F2{bf_lo(w[j]), bf_hi(w[j])}, F2{-m.zf, -m.zf}, F2{rs, rs}, far);
+  if (far > kTie) {
+    const uint32_t d = divided_nib8(v, m.zf, m.sf);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float u = __fsub_rn(x[j], m.zf);
-      const float q0 = u * rs;
-      float r = rintf(q0);
-      if (!(fabsf(fabsf(q0 - r) - 0.5f) > 1e-5f)) r = rintf(__fdiv_rn(u, m.sf));
-      c[j] = fminf(fmaxf(r, 0.0f), (float)QMAX);
-    }
+    for (int j = 0; j < 4; ++j) c[j] = F2{(float)((d >> (8 * j)) & 15u), (float)((d >> (8 * j + 4)) & 15u)};
   }
-  if (!m.nz) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = 0.0f;
-  }
+  // exact: integers below 2^16, read off after adding 2^23
+  const F2 a = fma2(c[1], F2{256.0f, 256.0f}, c[0]), b = fma2(c[3], F2{256.0f, 256.0f}, c[2]);
+  const uint32_t l = __float_as_uint(fmaf(a.y, 16.0f, a.x) + 8388608.0f), h = __float_as_uint(fmaf(b.y, 16.0f, b.x) + 8388608.0f);
+  return __byte_perm(l, h, 0x5410u);
 }
-// 8 bf16 values of words w[4q .. 4q + 3] as floats
-__device__ __forceinline__ void bf8(const uint32_t (&w)[16], int q, float (&x)[8]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x[2 * j] = bf_lo(w[4 * q + j]);
-    x[2 * j + 1] = bf_hi(w[4 * q + j]);
-  }
-}
-
-// Pack 8 integer-valued floats (0..15) as nibbles 0..7 of a word (exact:
-// the two halves are integers below 2^16, read off after adding 2^23).
-__device__ __forceinline__ uint32_t pack_nib8(const float (&c)[8]) {
-  float lo = c[0], hi = c[4];
-#pragma unroll
-  for (int n = 1; n < 4; ++n) {
-    lo = fmaf(c[n], (float)(1 << (4 * n)), lo);
-    hi = fmaf(c[4 + n], (float)(1 << (4 * n)), hi);
-  }
-  const uint32_t l = __float_as_uint(lo + 8388608.0f) & 0xFFFFu, h = __float_as_uint(hi + 8388608.0f) & 0xFFFFu;
-  return l | (h << 16);
-}
-// Pack 8 integer-valued floats (0..3) as 2-bit fields 0..7 (16 bits).
-__device__ __forceinline__ uint32_t pack_crumb8(const float (&c)[8]) {
-  float a = c[0];
-#pragma unroll
-  for (int n = 1; n < 8; ++n) a = fmaf(c[n], (float)(1 << (2 * n)), a);
-  return __float_as_uint(a + 8388608.0f) & 0xFFFFu;
+// 8 codes 0..3, pairs (2 j, 2 j + 1), as 2-bit fields
+__device__ __forceinline__ uint32_t pack_crumb8(const F2 (&c)[4]) {
+  F2 a = fma2(c[1], F2{16.0f, 16.0f}, c[0]);
+  a = fma2(c[2], F2{256.0f, 256.0f}, a);
+  a = fma2(c[3], F2{4096.0f, 4096.0f}, a);
+  return __float_as_uint(fmaf(a.y, 4.0f, a.x) + 8388608.0f) & 0xFFFFu;
 }
 
 // Transpose of an 8 x 8 matrix of nibbles held in 8 words (word k = row k,
@@ -893,14 +927,11 @@ __device__ __forceinline__ void transpose_nib8x8(uint32_t (&r)[8]) {
   }
 }
 
-// INT4 V codes of one group into the block image: lane t holds its slot's
-// codes as nibbles of cw[o] (channels 32gr + 8o + n); word (channel, slot chunk j) gets
-// slots 8j .. 8j + 7 in nibbles 0..7.  `wbuf`: 128 words of the warp's own
-// shared memory.
-__device__ __forceinline__ void store_i4v_group(uint8_t* img, const uint32_t (&cw)[4], int gr, uint32_t* wbuf) {
+// INT4 V codes of one group into the block image: word (channel, slot chunk j) gets
+// slots 8j .. 8j + 7 in nibbles 0..7.  `wbuf`: 128 words of the warp's own shared
+// memory, [o][slot] the codes of channels 32gr + 8o + n as nibbles.
+__device__ __forceinline__ void store_i4v_group(uint8_t* img, int gr, const uint32_t* wbuf) {
   const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 0; o < 4; ++o) wbuf[32 * o + lane] = cw[o];   // channels 8o .. 8o+7 of slot lane, as nibbles
   __syncwarp();
   if (lane < 16) {
     const int o = lane >> 2, j = lane & 3;
@@ -915,26 +946,6 @@ __device__ __forceinline__ void store_i4v_group(uint8_t* img, const uint32_t (&c
   __syncwarp();
 }
 
-// INT4 quantization of one token's group (K or V): the metadata and the codes
-// as nibble words cw[q] (channels 8q .. 8q + 7 of the group in nibbles 0..7).
-__device__ __forceinline__ GroupMeta quant_i4_words(const uint32_t (&w)[16], uint32_t (&cw)[4], bool& bad) {
-  const GroupMeta m = meta_i4(w, bad);
-  const float rs = approx_rcp(m.sf);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    float x[8], c[8];
-    bf8(w, q, x);
-    codes8<15>(x, m, rs, c);
-    cw[q] = pack_nib8(c);
-  }
-  return m;
-}
-// fmaf(code, scale, zero) of the 8 nibbles of a code word
-__device__ __forceinline__ void deq8(uint32_t cw, const GroupMeta& m, float (&y)[8]) {
-#pragma unroll
-  for (int n = 0; n < 8; ++n) y[n] = __fmaf_rn((float)((cw >> (4 * n)) & 15u), m.sf, m.zf);
-}
-
 // Fresh INT4 pages filled with 32 tokens within one call.  Grid (jobs, kv heads).
 template <bool kRope>
 __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int4_kernel(
@@ -944,34 +955,42 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int4_kernel(
     int32_t* __restrict__ pos, const __grid_constant__ RopeParam<kRope> rope) {
   __shared__ __align__(16) uint8_t img[kInt4Block];
   __shared__ __align__(16) uint32_t wbuf[4][128];
-  __shared__ KSource<kRope> ksrc;
+  __shared__ RopeTile kt, vt;
   asm volatile("griddepcontrol.wait;" ::: "memory");   // token lists and earlier stream work are done
   asm volatile("griddepcontrol.launch_dependents;");
   const AppendJob job = jobs[blockIdx.x];
   const int h = blockIdx.y, gr = threadIdx.x >> 5, t = threadIdx.x & 31;
-  const int T = toks[job.tok_off + t];
-  if (pos && h == 0 && gr == 0) pos[(size_t)job.page * kPage + t] = job.pos0 + T;
   bool bad = false;
-  {
-    // K: slot t's row, words (i, gr) i = 0..3 hold channels 32gr + 8i + n in nibble n
-    uint32_t w[16], cw[4];
-    load_k_group<kRope>(ksrc, rope, k, toks + job.tok_off, T, t, h, hkv, gr, w, bad);
-    const GroupMeta m = quant_i4_words(w, cw, bad);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(img + kI4KCodes + 64 * t + 16 * i + 4 * gr) = cw[i];
-    *reinterpret_cast<uint32_t*>(img + kI4KMeta + 16 * t + 4 * gr) =
-        (uint32_t)__half_as_ushort(m.s) | ((uint32_t)__half_as_ushort(m.z) << 16);
+  start_page<kRope>(kt, vt, rope, k, v, toks + job.tok_off, h, hkv, bad);
+  float vmax = 0.0f;
+#pragma unroll 1
+  for (int kv = 0; kv < 2; ++kv) {   // K, then V: the same code
+    if (kv) v_ready();
+    const uint4* row = &(kv ? vt : kt).row[t][4 * gr];
+    float mn, mx;
+    const GroupMeta m = meta_i4(row, bad, mn, mx);
+    const float rs = rcp_of(m);
+    // K: words (i, gr), i = 0..3, hold channels 32gr + 8i + n of slot t in nibble n; V: to be transposed
+    uint32_t* to = kv ? wbuf[gr] + t : reinterpret_cast<uint32_t*>(img + kI4KCodes + 64 * t + 4 * gr);
+    const int by = kv ? 32 : 4;
+#pragma unroll 2
+    for (int q = 0; q < 4; ++q) {
+      F2 c[4];
+      to[by * q] = quant_i4_8(row[q], m, rs, c);
+    }
+    if (!kv) {
+      *reinterpret_cast<uint32_t*>(img + kI4KMeta + 16 * t + 4 * gr) =
+          (uint32_t)__half_as_ushort(m.s) | ((uint32_t)__half_as_ushort(m.z) << 16);
+    } else {
+      store_i4v_group(img, gr, wbuf[gr]);
+      st_half(img, kI4VMeta + 2 * v_meta_index(t, gr), m.s);
+      st_half(img, kI4VMeta + 256 + 2 * v_meta_index(t, gr), m.z);
+      vmax = m.sf;
+    }
   }
-  {
-    uint32_t w[16], cw[4];
-    load_group(v, T, h, v_step<kRope>(rope, hkv), gr, w);
-    const GroupMeta m = quant_i4_words(w, cw, bad);
-    store_i4v_group(img, cw, gr, wbuf[gr]);
-    st_half(img, kI4VMeta + 2 * v_meta_index(t, gr), m.s);
-    st_half(img, kI4VMeta + 256 + 2 * v_meta_index(t, gr), m.z);
-    flush_vmax(m.sf, status);
-  }
+  flush_vmax(vmax, status);
   if (__any_sync(0xFFFFFFFFu, bad) && t == 0) atomicOr(status, kStatusRange);
+  if (pos && h == 0) write_positions(pos, job.page, toks + job.tok_off, job.pos0, 0, kPage);
   __syncthreads();
   uint4* out4 = reinterpret_cast<uint4*>(pool + int4_off + ((size_t)(job.page - n2) * hkv + h) * kInt4Block);
   const uint4* img4 = reinterpret_cast<const uint4*>(img);
@@ -988,146 +1007,154 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int4_kernel(
 // token and group.  Only the INT2 block is written.  Grid (jobs, kv heads).
 // Launched as a programmatic dependent of the INT4 kernels, as the
 // warp-per-token direct kernel is (it touches nothing they write).
+//
+// V: both quantizations go by (token, group), so the INT2 code of a value is a
+// function of its INT4 code alone, 16 entries per lane, looked up by byte permutes.
+// The least and greatest INT4 value are those of the codes of the least and
+// greatest channel, since every step is monotone.
 template <bool kRope>
-__global__ void __launch_bounds__(kBulkThreads, 6) bulk_int2_kernel(
+__global__ void __launch_bounds__(kBulkThreads, 8) bulk_int2_kernel(
     uint8_t* __restrict__ pool, int hkv, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
     const DirectJob* __restrict__ jobs, const int32_t* __restrict__ toks, uint32_t* __restrict__ status,
     int32_t* __restrict__ pos, const __grid_constant__ RopeParam<kRope> rope) {
-  __shared__ KSource<kRope> ksrc;
   __shared__ __align__(16) uint8_t img[kInt2Block];
-  __shared__ __align__(16) float4 kmeta[4][32];          // per channel of the warp's group: zero, 1/scale, scale, nz
-  __shared__ __align__(16) uint32_t vbuf[4][32][3];      // INT2 V codes [slot][channels 0..15, 16..31] (padded)
+  __shared__ RopeTile kt, vt;
+  __shared__ uint32_t kcw[4][4][32];                     // INT4 K codes [group][8-channel piece][slot]
+  __shared__ __align__(16) float kz[4][32], kr[4][32], ks[4][32];   // per channel of the warp's group: -zero, 1 / scale, scale
+  __shared__ uint32_t vbuf[4][2][33];                    // INT2 V codes [group][channels 0..15, 16..31][slot]
   const DirectJob job = jobs[blockIdx.x];
   const int h = blockIdx.y, gr = threadIdx.x >> 5, t = threadIdx.x & 31;
-  const int T = toks[job.tok_off + t];
-  if (pos && h == 0 && gr == 0) pos[(size_t)job.dst * kPage + t] = job.pos0 + T;
   bool bad = false;
+  start_page<kRope>(kt, vt, rope, k, v, toks + job.tok_off, h, hkv, bad);
   // ---- K: INT4 per token, dequantized, then INT2 per channel across the 32 slots
   {
-    float xq[32];   // INT4-dequantized K of slot t's group
-    {
-      uint32_t w[16], cw[4];
-      load_k_group<kRope>(ksrc, rope, k, toks + job.tok_off, T, t, h, hkv, gr, w, bad);
-      const GroupMeta m = quant_i4_words(w, cw, bad);
+    const uint4* row = &kt.row[t][4 * gr];
+    float mn, mx;
+    const GroupMeta m = meta_i4(row, bad, mn, mx);
+    const float rs = rcp_of(m);
+    float my_mn = 0.0f, my_mx = 0.0f;   // channel t of the group: min / max over the 32 slots
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+      F2 c[4];
+      kcw[gr][q][t] = quant_i4_8(row[q], m, rs, c);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float y[8];
-        deq8(cw[q], m, y);
-#pragma unroll
-        for (int n = 0; n < 8; ++n) xq[8 * q + n] = y[n];
+      for (int j = 0; j < 4; ++j) {
+        const F2 y = fma2(c[j], F2{m.sf, m.sf}, F2{m.zf, m.zf});
+        const float a0 = redux_min(y.x), b0 = redux_max(y.x), a1 = redux_min(y.y), b1 = redux_max(y.y);
+        if (t == 8 * q + 2 * j) my_mn = a0, my_mx = b0;
+        if (t == 8 * q + 2 * j + 1) my_mn = a1, my_mx = b1;
       }
     }
-    float my_mn = 0.0f, my_mx = 0.0f;   // channel t of the group: min / max over the 32 slots
-#pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      const float a = redux_min(xq[c]), b = redux_max(xq[c]);
-      my_mn = t == c ? a : my_mn;
-      my_mx = t == c ? b : my_mx;
-    }
     const GroupMeta m2 = make_meta(my_mn, my_mx, 3.0f);
-    kmeta[gr][t] = make_float4(m2.zf, approx_rcp(m2.sf), m2.sf, m2.nz ? 1.0f : 0.0f);
+    kz[gr][t] = -m2.zf;
+    kr[gr][t] = rcp_of(m2);
+    ks[gr][t] = m2.sf;
     const int ch = 32 * gr + t;
     st_half(img, kI2KMeta + 2 * i2k_meta_index(ch), m2.s);
     st_half(img, kI2KMeta + 256 + 2 * i2k_meta_index(ch), m2.z);
-    float smx = m2.sf;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) smx = fmaxf(smx, __shfl_xor_sync(0xFFFFFFFFu, smx, o));
+    const float smx = redux_max(m2.sf);   // running maximum of INT2 K scales
     if (t == 0) atomicMax(status + 1, __float_as_uint(smx));
     __syncwarp();
-    // slot t's codes, channel c with channel c's metadata (the repack's rule per element)
-    uint32_t row[2] = {0u, 0u};
-#pragma unroll
+    // slot t's codes, channel c with channel c's metadata: channel c at byte c >> 2, bits 2 (c & 3) of its row
+#pragma unroll 1
     for (int q = 0; q < 4; ++q) {
-      float c2[8];
-      bool tie = false;
+      const uint32_t cw = kcw[gr][q][t];
+      F2 c2[4];
+      float far = 0.0f;
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const float4 mm = kmeta[gr][8 * q + n];
-        const float u = __fsub_rn(xq[8 * q + n], mm.x);
-        const float q0 = u * mm.y;
-        const float r = rintf(q0);
-        tie |= mm.w != 0.0f && !(fabsf(fabsf(q0 - r) - 0.5f) > 1e-5f);
-        c2[n] = mm.w != 0.0f ? fminf(fmaxf(r, 0.0f), 3.0f) : 0.0f;
+      for (int j = 0; j < 4; ++j) {
+        const F2 c = add2(F2{__uint_as_float(((cw >> (8 * j)) & 15u) | 0x4B000000u),
+                             __uint_as_float(((cw >> (8 * j + 4)) & 15u) | 0x4B000000u)}, F2{-8388608.0f, -8388608.0f});
+        const F2 y = fma2(c, F2{m.sf, m.sf}, F2{m.zf, m.zf});
+        const float2 z = *reinterpret_cast<const float2*>(&kz[gr][8 * q + 2 * j]), r = *reinterpret_cast<const float2*>(&kr[gr][8 * q + 2 * j]);
+        c2[j] = codes2<3>(y, F2{z.x, z.y}, F2{r.x, r.y}, far);
       }
-      if (tie) {
+      uint32_t d = pack_crumb8(c2);
+      if (far > kTie) {
+        float z[8];
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          const float4 mm = kmeta[gr][8 * q + n];
-          const float u = __fsub_rn(xq[8 * q + n], mm.x);
-          const float q0 = u * mm.y;
-          float r = rintf(q0);
-          if (!(fabsf(fabsf(q0 - r) - 0.5f) > 1e-5f)) r = rintf(__fdiv_rn(u, mm.z));
-          c2[n] = mm.w != 0.0f ? fminf(fmaxf(r, 0.0f), 3.0f) : 0.0f;
-        }
+        for (int n = 0; n < 8; ++n) z[n] = -kz[gr][8 * q + n];
+        d = divided_crumb8(cw, m.sf, m.zf, z, &ks[gr][8 * q]);
       }
-      row[q >> 1] |= pack_crumb8(c2) << (16 * (q & 1));
+      *reinterpret_cast<uint16_t*>(img + kI2KCodes + 32 * t + 8 * gr + 2 * q) = (uint16_t)d;
     }
-    // slot t's row: channel c at byte c >> 2, bits 2 (c & 3): the group's 8 bytes
-    *reinterpret_cast<uint2*>(img + kI2KCodes + 32 * t + 8 * gr) = make_uint2(row[0], row[1]);
   }
   // ---- V: INT4 per token, then INT2 per token on the dequantized values
+  v_ready();
   {
-    uint32_t cw[4];
-    GroupMeta m;
-    {
-      uint32_t w[16];
-      load_group(v, T, h, v_step<kRope>(rope, hkv), gr, w);
-      m = quant_i4_words(w, cw, bad);
-    }
+    const uint4* row = &vt.row[t][4 * gr];
+    float mn, mx;
+    const GroupMeta m = meta_i4(row, bad, mn, mx);
+    const float rs = rcp_of(m);
     flush_vmax(m.sf, status);   // the INT4 V scales count toward the pool's V-scale maximum too
-    float mn = 0.0f, mx = 0.0f;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float y[8];
-      deq8(cw[q], m, y);
-#pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        mn = (q == 0 && n == 0) ? y[0] : fminf(mn, y[n]);
-        mx = (q == 0 && n == 0) ? y[0] : fmaxf(mx, y[n]);
-      }
-    }
-    const GroupMeta m2 = make_meta(mn, mx, 3.0f);
-    const float rs2 = approx_rcp(m2.sf);
-    uint32_t row[2] = {0u, 0u};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float y[8], c2[8];
-      deq8(cw[q], m, y);
-      codes8<3>(y, m2, rs2, c2);
-      row[q >> 1] |= pack_crumb8(c2) << (16 * (q & 1));
-    }
+    const float c_lo = divided_one(mn, m.zf, m.sf, 15.0f), c_hi = divided_one(mx, m.zf, m.sf, 15.0f);
+    const GroupMeta m2 = make_meta(__fmaf_rn(c_lo, m.sf, m.zf), __fmaf_rn(c_hi, m.sf, m.zf), 3.0f);
+    const float rs2 = rcp_of(m2);
     st_half(img, kI2VMeta + 2 * v_meta_index(t, gr), m2.s);
     st_half(img, kI2VMeta + 256 + 2 * v_meta_index(t, gr), m2.z);
-    float vmx = m2.sf;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) vmx = fmaxf(vmx, __shfl_xor_sync(0xFFFFFFFFu, vmx, o));
+    const float vmx = redux_max(m2.sf);
     if (t == 0) atomicMax(status + 2, __float_as_uint(vmx));
-    // codes [slot][channels 0..15, 16..31] as 2-bit fields
-    vbuf[gr][t][0] = row[0];
-    vbuf[gr][t][1] = row[1];
+    // the INT2 code of every INT4 code, a byte each
+    uint32_t tab[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      float far = 0.0f;
+      F2 c[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float n = (float)(4 * y + 2 * j);
+        c[j] = codes2<3>(fma2(F2{n, n + 1.0f}, F2{m.sf, m.sf}, F2{m.zf, m.zf}), F2{-m2.zf, -m2.zf}, F2{rs2, rs2}, far);
+      }
+      if (far > kTie) {
+#pragma unroll 1
+        for (int n = 0; n < 4; ++n) {
+          const float x = divided_one(__fmaf_rn((float)(4 * y + n), m.sf, m.zf), m2.zf, m2.sf, 3.0f);
+          if (n == 0) c[0].x = x;
+          else if (n == 1) c[0].y = x;
+          else if (n == 2) c[1].x = x;
+          else c[1].y = x;
+        }
+      }
+      // below 2^24: two bytes at a time
+      const uint32_t l = __float_as_uint(fmaf(c[0].y, 256.0f, c[0].x) + 8388608.0f), u = __float_as_uint(fmaf(c[1].y, 256.0f, c[1].x) + 8388608.0f);
+      tab[y] = __byte_perm(l, u, 0x5410u);
+    }
+    uint32_t half[2] = {0u, 0u};   // channels 0..15 and 16..31 as 2-bit fields
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      F2 c[4];
+      const uint32_t cw = quant_i4_8(row[q], m, rs, c);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const uint32_t sel = cw >> (16 * y);
+        const uint32_t lo = __byte_perm(tab[0], tab[1], sel & 0x7777u), hi = __byte_perm(tab[2], tab[3], sel & 0x7777u);
+        const uint32_t up = __byte_perm(0x0000FF00u, 0u, (sel >> 3) & 0x1111u);   // bytes whose code is 8 or more
+        const uint32_t b = (lo & ~up) | (hi & up);
+        // bytes of 2 bits -> the top byte of the product (no carries)
+        half[q >> 1] |= ((b * 0x01041040u) >> 24) << (16 * (q & 1) + 8 * y);
+      }
+    }
+    vbuf[gr][0][t] = half[0];
+    vbuf[gr][1][t] = half[1];
   }
   __syncwarp();
-  // INT2 V bytes: lane = channel cc of the group; the 4 slot chunks i
+  // INT2 V words: lane = (r, i); word (r, m, i) of m = 2 gr and 2 gr + 1 (channels 16 m + r and 16 m + r + 8, slots 8 i .. + 7)
   {
-    const int c = 32 * gr + t;
-    const int wsel = t >> 4, sh = 2 * (t & 15);
+    const int r = t >> 2, i = t & 3;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int b0 = i2v_byte(8 * i, c);
-      int b1 = b0;
-      uint32_t v0 = 0u, v1 = 0u;
+    for (int y = 0; y < 2; ++y) {
+      uint32_t p[2] = {0u, 0u};   // slots 0..3 and 4..7: channel r in the low half, r + 8 in the high one
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const int tt = 8 * i + kk, b = i2v_byte(tt, c);
-        const uint32_t code = ((vbuf[gr][tt][wsel] >> sh) & 3u) << i2v_shift(tt);
-        if (b == b0) v0 |= code;
-        else { v1 |= code; b1 = b; }
-      }
-      img[b0] = (uint8_t)v0;
-      img[b1] = (uint8_t)v1;
+      for (int kk = 0; kk < 8; ++kk) p[kk >> 2] |= ((vbuf[gr][y][8 * i + kk] >> (2 * r)) & 0x00030003u) << (2 * (kk & 3));
+      uint32_t w = __byte_perm(p[0], p[1], 0x6420u);
+      const uint32_t x = (w ^ (w >> 16)) & 3u;   // channel r: slots 8 i and 8 i + 4 the other way round
+      w ^= x | (x << 16);
+      const int mm = 2 * gr + y;
+      *reinterpret_cast<uint32_t*>(img + kI2VCodes + 16 * (32 * (mm >> 2) + 4 * r + i) + 4 * (mm & 3)) = w;
     }
   }
   if (__any_sync(0xFFFFFFFFu, bad) && t == 0) atomicOr(status, kStatusRange);
+  if (pos && h == 0) write_positions(pos, job.dst, toks + job.tok_off, job.pos0, 0, kPage);
   __syncthreads();
   uint4* out4 = reinterpret_cast<uint4*>(pool + ((size_t)job.dst * hkv + h) * kInt2Block);
   const uint4* img4 = reinterpret_cast<const uint4*>(img);
