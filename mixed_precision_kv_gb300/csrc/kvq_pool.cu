@@ -688,23 +688,39 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
   std::vector<int32_t>& i2 = P->scr_i2;
   int64_t n4 = 0, n2 = 0;
   if (bulk) {
-    // one pass: bits valid, run boundaries; raw pointers and local counts
-    // (stores through vectors next to uint8_t loads defeat registers)
+    // one pass: bits valid, the two lists; raw pointers and local counts (stores
+    // through vectors next to uint8_t loads defeat registers).  Widths come in runs:
+    // eight tokens of one width are listed at once.
     if (i4.size() < (size_t)n_tok) i4.resize((size_t)n_tok);
     if (i2.size() < (size_t)n_tok) i2.resize((size_t)n_tok);
     int32_t* p4 = i4.data();
     int32_t* p2 = i2.data();
     int64_t c4 = 0, c2 = 0, changes = 0;
-    int32_t rp = req_ids[0];
     bool ok = true;
-    for (int64_t t = 0; t < n_tok; ++t) {
+    for (int64_t t = 1; t < n_tok; ++t) changes += req_ids[t] != req_ids[t - 1];
+    int64_t t = 0;
+    for (; t + 8 <= n_tok; t += 8) {
+      uint64_t w;
+      std::memcpy(&w, bits + t, 8);
+      if (w == 0x0404040404040404ull || w == 0x0202020202020202ull) {
+        const bool four = (w & 4u) != 0;
+        int32_t* to = four ? p4 + c4 : p2 + c2;
+        for (int y = 0; y < 8; ++y) to[y] = (int32_t)t + y;
+        (four ? c4 : c2) += 8;
+        continue;
+      }
+      for (int y = 0; y < 8; ++y) {
+        const uint32_t b = bits[t + y];
+        ok &= (b == 2u) | (b == 4u);
+        p4[c4] = p2[c2] = (int32_t)t + y;
+        c4 += b == 4u;
+        c2 += b != 4u;
+      }
+    }
+    for (; t < n_tok; ++t) {
       const uint32_t b = bits[t];
-      const int32_t rt = req_ids[t];
       ok &= (b == 2u) | (b == 4u);
-      changes += rt != rp;
-      rp = rt;
-      p4[c4] = (int32_t)t;
-      p2[c2] = (int32_t)t;
+      p4[c4] = p2[c2] = (int32_t)t;
       c4 += b == 4u;
       c2 += b != 4u;
     }
@@ -843,10 +859,6 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
     const int64_t T0 = (int64_t)R.loc.size();
     const int64_t P0 = T0 - u.t0;                 // the request's position of call token t: P0 + t
     R.loc.resize((size_t)(T0 + u.n));   // every new entry is written below
-    auto put = [&](int32_t page, int slot, int32_t t) {
-      P->pos[(size_t)page * kPage + slot] = (int32_t)(P0 + t);
-      R.loc[(size_t)(P0 + t)] = ((uint32_t)page << 5) | (uint32_t)slot;
-    };
     auto slots = [](int first, int64_t n) { return (uint32_t)((n >= kPage ? 0xFFFFFFFFull : ((1ull << n) - 1)) << first); };
     // An append job over the run's INT4 (int4_list) or INT2 tokens
     // [a, a + n) into slots first .. of page.  Its tok_off indexes the call's
@@ -854,18 +866,29 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
     // below places the lists and adjusts the offsets into the INT2 list.
     int32_t* const pos = P->pos.data();
     uint32_t* const loc = R.loc.data();
+    // the positions of slots first .. of page, and where these positions are: tokens src[0 .. n)
+    auto place = [=](int32_t page, int first, const int32_t* src, int64_t n) {
+      int32_t* __restrict pp = pos + (size_t)page * kPage + first;
+      const uint32_t base = ((uint32_t)page << 5) | (uint32_t)first;
+      if (src[n - 1] - src[0] == n - 1) {   // tokens that follow one another, as in a run of one width
+        const int64_t p = P0 + src[0];
+        uint32_t* __restrict lp = loc + p;
+        for (int64_t q = 0; q < n; ++q) pp[q] = (int32_t)(p + q);
+        for (int64_t q = 0; q < n; ++q) lp[q] = base + (uint32_t)q;
+        return;
+      }
+      uint32_t* __restrict lp = loc + P0;
+      for (int64_t q = 0; q < n; ++q) {
+        const int32_t t = src[q];
+        pp[q] = (int32_t)(P0 + t);
+        lp[t] = base + (uint32_t)q;
+      }
+    };
     auto add_job = [&](int32_t page, int first, bool int4_list, int64_t a, int64_t n) {
       const int64_t off = (int4_list ? u.o4 : n4 + u.o2) + a;
       jobs.push_back(AppendJob{page, first, (int32_t)n, (int32_t)off, -1, 0u, -1, 0, (int32_t)P0});
       job_req.push_back(r);
-      const int32_t* src = (int4_list ? l4 : l2) + a;
-      int32_t* pp = pos + (size_t)page * kPage + first;
-      const uint32_t base = ((uint32_t)page << 5) | (uint32_t)first;
-      for (int64_t q = 0; q < n; ++q) {
-        const int32_t t = src[q];
-        pp[q] = (int32_t)(P0 + t);
-        loc[P0 + t] = base + (uint32_t)q;
-      }
+      place(page, first, (int4_list ? l4 : l2) + a, n);
       bulk_job_toks += n;
       P->fill[page] = (uint8_t)(first + n);
       P->live[page] |= slots(first, n);
@@ -925,7 +948,7 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
     for (int64_t g = 0; g < u.ndirect; ++g) {
       const int64_t a = u.e + kPage * g;
       const int32_t sg = idS[(size_t)g], nid = idD[(size_t)g];
-      for (int sl = 0; sl < kPage; ++sl) put(nid, sl, l2[(size_t)(a + sl)]);
+      place(nid, 0, l2 + a, kPage);
       P->fill[sg] = kPage;
       P->live[sg] = 0xFFFFFFFFu;
       P->fill[nid] = kPage;
@@ -1127,8 +1150,19 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
   size_t n_full = 0;
   const auto jobs4_end = jobs.end() - (ptrdiff_t)(n_i3 + n_f4);
   if (use_bulk) {
-    std::stable_partition(jobs.begin(), jobs4_end, [](const AppendJob& j) { return !(j.first_slot == 0 && j.n_slots == kPage); });
-    for (auto it = jobs.begin(); it != jobs4_end; ++it) n_full += (it->first_slot == 0 && it->n_slots == kPage) ? 1 : 0;
+    // the full ones go last, in order (few are not)
+    std::vector<AppendJob> part;
+    auto to = jobs4_end;
+    for (auto it = jobs4_end; it != jobs.begin();) {
+      --it;
+      if (it->first_slot == 0 && it->n_slots == kPage) {
+        if (--to != it) *to = *it;
+      } else {
+        part.push_back(*it);
+      }
+    }
+    std::reverse_copy(part.begin(), part.end(), jobs.begin());
+    n_full = (size_t)(jobs4_end - to);
   }
   if (bulk && small) {
     // the small launch carries its token lists by value: gather each job's tokens
