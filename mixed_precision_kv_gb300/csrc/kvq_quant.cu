@@ -750,7 +750,6 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
       : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-__device__ __forceinline__ F2 sub2(F2 a, F2 b) { return add2(a, F2{-b.x, -b.y}); }
 __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
   F2 d;
   asm("{.reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;}"
@@ -765,18 +764,27 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   return d;
 }
 
-// Codes of two values: rint((x - z) rs) clamped to [0, QMAX], negz = -z, rs the approximate
-// reciprocal of the scale (0 where the scale is: code 0).  far: the largest distance of a quotient from
-// its integer so far; past kTie the exact quotient could round the other way (qcode_fast), and the
-// caller takes the 8 codes again, divided.
+// Codes of two values, negated (the steps then need no sign changes): with f = 1 / (QMAX s), approximately,
+//     q = sat((x - z) f),   code = rint(QMAX q),
+// so the clamp to [0, QMAX] costs nothing.  negz = -z, f = 0 where the scale is 0: code 0.  f is off by
+// less than 2^-21.2 of itself and QMAX q by less than 1e-5 from the exact quotient's value; far: the
+// largest distance of QMAX q from its integer so far.  Past kTie the exact quotient could round the
+// other way, and the caller takes the 8 codes again, divided.
 constexpr float kTie = 0.49999f;
+__device__ __forceinline__ float mul_sat(float a, float b) {
+  float d;
+  asm("mul.rn.sat.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 template <int QMAX>
-__device__ __forceinline__ F2 codes2(F2 x, F2 negz, F2 rs, float& far) {
-  const F2 q = mul2(add2(x, negz), rs);
-  const F2 c = add2(add2(q, F2{kRound, kRound}), F2{-kRound, -kRound});
-  const F2 d = sub2(q, c);
+__device__ __forceinline__ F2 codes2(F2 x, F2 negz, F2 f, float& far) {
+  constexpr float Q = (float)QMAX;
+  const F2 u = add2(x, negz);
+  const F2 q{mul_sat(u.x, f.x), mul_sat(u.y, f.y)};
+  const F2 c = add2(fma2(q, F2{-Q, -Q}, F2{-kRound, -kRound}), F2{kRound, kRound});
+  const F2 d = fma2(q, F2{Q, Q}, c);
   far = fmaxf(fmaxf(far, fabsf(d.x)), fabsf(d.y));
-  return F2{fminf(fmaxf(c.x, 0.0f), (float)QMAX), fminf(fmaxf(c.y, 0.0f), (float)QMAX)};
+  return c;
 }
 __device__ __forceinline__ float code_divided(float x, float z, float s, float qmax) {
   return s == 0.0f ? 0.0f : fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x, z), s)), 0.0f), qmax);
@@ -828,36 +836,32 @@ __device__ __forceinline__ void rotate_page(RopeTile& K, const RopeArgs& R, cons
     K.row[t][b] = z;
   }
 }
-// K or V rows of a page as they are, asynchronously.
-__device__ __forceinline__ void fetch_page(RopeTile& X, const __nv_bfloat16* __restrict__ src, const int32_t* __restrict__ toks,
-                                           int h, size_t step) {
+// This lane's pieces of K or V as they are, asynchronously: the lane that reads them fetches them, so they
+// need no barrier.
+__device__ __forceinline__ void fetch_group(RopeTile& X, const __nv_bfloat16* __restrict__ src, int T, int t, int h, size_t step,
+                                            int gr) {
+  const __nv_bfloat16* p = src + (size_t)T * step + (size_t)h * kHeadDim + 32 * gr;
 #pragma unroll
-  for (int y = 0; y < 4; ++y) {
-    const int t = (int)(threadIdx.x >> 4) + 8 * y, c = threadIdx.x & 15;
-    const __nv_bfloat16* p = src + (size_t)__ldg(toks + t) * step + (size_t)h * kHeadDim + 8 * c;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(&X.row[t][c])), "l"(p)
-                 : "memory");
-  }
+  for (int q = 0; q < 4; ++q)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(&X.row[t][4 * gr + q])),
+                 "l"(p + 8 * q) : "memory");
+  asm volatile("cp.async.commit_group;" ::: "memory");
 }
-// The rows of a page: V's on their way, K's in shared memory.
+// The rows of a page: K's in shared memory, V's on their way.
 template <bool kRope>
 __device__ __forceinline__ void start_page(RopeTile& K, RopeTile& V, const RopeParam<kRope>& R,
                                            const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
-                                           const int32_t* __restrict__ toks, int h, int hkv, bool& bad) {
-  if constexpr (!kRope) {
-    fetch_page(K, k, toks, h, k_step<kRope>(R, hkv));
-    asm volatile("cp.async.commit_group;" ::: "memory");
+                                           const int32_t* __restrict__ toks, int T, int t, int h, int hkv, int gr, bool& bad) {
+  if constexpr (!kRope) fetch_group(K, k, T, t, h, k_step<kRope>(R, hkv), gr);
+  fetch_group(V, v, T, t, h, v_step<kRope>(R, hkv), gr);
+  if constexpr (kRope) {
+    rotate_page(K, R, k, toks, h, bad);
+    __syncthreads();
+  } else {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
   }
-  fetch_page(V, v, toks, h, v_step<kRope>(R, hkv));
-  asm volatile("cp.async.commit_group;" ::: "memory");
-  if constexpr (kRope) rotate_page(K, R, k, toks, h, bad);
-  else asm volatile("cp.async.wait_group 1;" ::: "memory");
-  __syncthreads();
 }
-__device__ __forceinline__ void v_ready() {
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  __syncthreads();
-}
+__device__ __forceinline__ void v_ready() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 // Metadata of a token's group at row (4 pieces of 8 bf16 channels): min / max exactly, NaN
 // carried so that the range check sees it (NaN, Inf or |x| > 65504 sets `bad`).
@@ -876,30 +880,31 @@ __device__ __forceinline__ GroupMeta meta_i4(const uint4* row, bool& bad, float&
   mx = fmaxf(c, d);
   return make_meta(mn, mx, 15.0f);
 }
-__device__ __forceinline__ float rcp_of(const GroupMeta& m) { return m.nz ? approx_rcp(m.sf) : 0.0f; }
+template <int QMAX>
+__device__ __forceinline__ float factor_of(const GroupMeta& m) { return m.nz ? approx_rcp(m.sf) * (1.0f / QMAX) : 0.0f; }
 
-// INT4 codes of 8 channels as nibbles; c: the codes as floats, pairs (2 j, 2 j + 1) (after a tie: read off the word).
-__device__ __forceinline__ uint32_t quant_i4_8(uint4 v, const GroupMeta& m, float rs, F2 (&c)[4]) {
+// INT4 codes of 8 channels as nibbles; c: the codes as floats, negated, pairs (2 j, 2 j + 1).
+__device__ __forceinline__ uint32_t quant_i4_8(uint4 v, const GroupMeta& m, float f, F2 (&c)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   float far = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) c[j] = codes2<15>(F2{bf_lo(w[j]), bf_hi(w[j])}, F2{-m.zf, -m.zf}, F2{rs, rs}, far);
+  for (int j = 0; j < 4; ++j) c[j] = codes2<15>(F2{bf_lo(w[j]), bf_hi(w[j])}, F2{-m.zf, -m.zf}, F2{f, f}, far);
   if (far > kTie) {
     const uint32_t d = divided_nib8(v, m.zf, m.sf);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] = F2{(float)((d >> (8 * j)) & 15u), (float)((d >> (8 * j + 4)) & 15u)};
+    for (int j = 0; j < 4; ++j) c[j] = F2{-(float)((d >> (8 * j)) & 15u), -(float)((d >> (8 * j + 4)) & 15u)};
   }
   // exact: integers below 2^16, read off after adding 2^23
   const F2 a = fma2(c[1], F2{256.0f, 256.0f}, c[0]), b = fma2(c[3], F2{256.0f, 256.0f}, c[2]);
-  const uint32_t l = __float_as_uint(fmaf(a.y, 16.0f, a.x) + 8388608.0f), h = __float_as_uint(fmaf(b.y, 16.0f, b.x) + 8388608.0f);
+  const uint32_t l = __float_as_uint(8388608.0f - fmaf(a.y, 16.0f, a.x)), h = __float_as_uint(8388608.0f - fmaf(b.y, 16.0f, b.x));
   return __byte_perm(l, h, 0x5410u);
 }
-// 8 codes 0..3, pairs (2 j, 2 j + 1), as 2-bit fields
+// 8 codes 0..3, negated, pairs (2 j, 2 j + 1), as 2-bit fields
 __device__ __forceinline__ uint32_t pack_crumb8(const F2 (&c)[4]) {
   F2 a = fma2(c[1], F2{16.0f, 16.0f}, c[0]);
   a = fma2(c[2], F2{256.0f, 256.0f}, a);
   a = fma2(c[3], F2{4096.0f, 4096.0f}, a);
-  return __float_as_uint(fmaf(a.y, 4.0f, a.x) + 8388608.0f) & 0xFFFFu;
+  return __float_as_uint(8388608.0f - fmaf(a.y, 4.0f, a.x)) & 0xFFFFu;
 }
 
 // Transpose of an 8 x 8 matrix of nibbles held in 8 words (word k = row k,
@@ -915,15 +920,15 @@ __device__ __forceinline__ void transpose_nib8x8(uint32_t (&r)[8]) {
   for (int k = 0; k < 8; k += 4)
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const uint32_t t = ((r[k + q] >> 8) ^ r[k + q + 2]) & 0x00FF00FFu;
-      r[k + q + 2] ^= t;
-      r[k + q] ^= t << 8;
+      const uint32_t x = r[k + q], y = r[k + q + 2];
+      r[k + q] = __byte_perm(x, y, 0x6240u);
+      r[k + q + 2] = __byte_perm(x, y, 0x7351u);
     }
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const uint32_t t = ((r[q] >> 16) ^ r[q + 4]) & 0x0000FFFFu;
-    r[q + 4] ^= t;
-    r[q] ^= t << 16;
+    const uint32_t x = r[q], y = r[q + 4];
+    r[q] = __byte_perm(x, y, 0x5410u);
+    r[q + 4] = __byte_perm(x, y, 0x7632u);
   }
 }
 
@@ -960,8 +965,9 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int4_kernel(
   asm volatile("griddepcontrol.launch_dependents;");
   const AppendJob job = jobs[blockIdx.x];
   const int h = blockIdx.y, gr = threadIdx.x >> 5, t = threadIdx.x & 31;
+  const int T = toks[job.tok_off + t];
   bool bad = false;
-  start_page<kRope>(kt, vt, rope, k, v, toks + job.tok_off, h, hkv, bad);
+  start_page<kRope>(kt, vt, rope, k, v, toks + job.tok_off, T, t, h, hkv, gr, bad);
   float vmax = 0.0f;
 #pragma unroll 1
   for (int kv = 0; kv < 2; ++kv) {   // K, then V: the same code
@@ -969,14 +975,14 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int4_kernel(
     const uint4* row = &(kv ? vt : kt).row[t][4 * gr];
     float mn, mx;
     const GroupMeta m = meta_i4(row, bad, mn, mx);
-    const float rs = rcp_of(m);
+    const float f = factor_of<15>(m);
     // K: words (i, gr), i = 0..3, hold channels 32gr + 8i + n of slot t in nibble n; V: to be transposed
     uint32_t* to = kv ? wbuf[gr] + t : reinterpret_cast<uint32_t*>(img + kI4KCodes + 64 * t + 4 * gr);
     const int by = kv ? 32 : 4;
 #pragma unroll 2
     for (int q = 0; q < 4; ++q) {
       F2 c[4];
-      to[by * q] = quant_i4_8(row[q], m, rs, c);
+      to[by * q] = quant_i4_8(row[q], m, f, c);
     }
     if (!kv) {
       *reinterpret_cast<uint32_t*>(img + kI4KMeta + 16 * t + 4 * gr) =
@@ -990,7 +996,7 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int4_kernel(
   }
   flush_vmax(vmax, status);
   if (__any_sync(0xFFFFFFFFu, bad) && t == 0) atomicOr(status, kStatusRange);
-  if (pos && h == 0) write_positions(pos, job.page, toks + job.tok_off, job.pos0, 0, kPage);
+  if (pos && h == 0 && gr == 0) pos[(size_t)job.page * kPage + t] = job.pos0 + T;
   __syncthreads();
   uint4* out4 = reinterpret_cast<uint4*>(pool + int4_off + ((size_t)(job.page - n2) * hkv + h) * kInt4Block);
   const uint4* img4 = reinterpret_cast<const uint4*>(img);
@@ -1020,26 +1026,27 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int2_kernel(
   __shared__ __align__(16) uint8_t img[kInt2Block];
   __shared__ RopeTile kt, vt;
   __shared__ uint32_t kcw[4][4][32];                     // INT4 K codes [group][8-channel piece][slot]
-  __shared__ __align__(16) float kz[4][32], kr[4][32], ks[4][32];   // per channel of the warp's group: -zero, 1 / scale, scale
+  __shared__ __align__(16) float kz[4][32], kr[4][32], ks[4][32];   // per channel of the warp's group: -zero, 1 / (3 scale), scale
   __shared__ uint32_t vbuf[4][2][33];                    // INT2 V codes [group][channels 0..15, 16..31][slot]
   const DirectJob job = jobs[blockIdx.x];
   const int h = blockIdx.y, gr = threadIdx.x >> 5, t = threadIdx.x & 31;
+  const int T = toks[job.tok_off + t];
   bool bad = false;
-  start_page<kRope>(kt, vt, rope, k, v, toks + job.tok_off, h, hkv, bad);
+  start_page<kRope>(kt, vt, rope, k, v, toks + job.tok_off, T, t, h, hkv, gr, bad);
   // ---- K: INT4 per token, dequantized, then INT2 per channel across the 32 slots
   {
     const uint4* row = &kt.row[t][4 * gr];
     float mn, mx;
     const GroupMeta m = meta_i4(row, bad, mn, mx);
-    const float rs = rcp_of(m);
+    const float f = factor_of<15>(m);
     float my_mn = 0.0f, my_mx = 0.0f;   // channel t of the group: min / max over the 32 slots
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       F2 c[4];
-      kcw[gr][q][t] = quant_i4_8(row[q], m, rs, c);
+      kcw[gr][q][t] = quant_i4_8(row[q], m, f, c);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const F2 y = fma2(c[j], F2{m.sf, m.sf}, F2{m.zf, m.zf});
+        const F2 y = fma2(c[j], F2{-m.sf, -m.sf}, F2{m.zf, m.zf});
         const float a0 = redux_min(y.x), b0 = redux_max(y.x), a1 = redux_min(y.y), b1 = redux_max(y.y);
         if (t == 8 * q + 2 * j) my_mn = a0, my_mx = b0;
         if (t == 8 * q + 2 * j + 1) my_mn = a1, my_mx = b1;
@@ -1047,7 +1054,7 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int2_kernel(
     }
     const GroupMeta m2 = make_meta(my_mn, my_mx, 3.0f);
     kz[gr][t] = -m2.zf;
-    kr[gr][t] = rcp_of(m2);
+    kr[gr][t] = factor_of<3>(m2);
     ks[gr][t] = m2.sf;
     const int ch = 32 * gr + t;
     st_half(img, kI2KMeta + 2 * i2k_meta_index(ch), m2.s);
@@ -1063,9 +1070,12 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int2_kernel(
       float far = 0.0f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const F2 c = add2(F2{__uint_as_float(((cw >> (8 * j)) & 15u) | 0x4B000000u),
-                             __uint_as_float(((cw >> (8 * j + 4)) & 15u) | 0x4B000000u)}, F2{-8388608.0f, -8388608.0f});
-        const F2 y = fma2(c, F2{m.sf, m.sf}, F2{m.zf, m.zf});
+        // codes 2 j and 2 j + 1 times 16^(2 (j & 1)) and 16 times that, in the mantissa of 2^23 (exact)
+        const uint32_t w = j < 2 ? cw : cw >> 16;
+        const int p = 8 * (j & 1);
+        const F2 c = add2(F2{__uint_as_float((w & (15u << p)) | 0x4B000000u), __uint_as_float((w & (240u << p)) | 0x4B000000u)},
+                          F2{-8388608.0f, -8388608.0f});
+        const F2 y = fma2(c, F2{m.sf * (1.0f / (1 << p)), m.sf * (1.0f / (16 << p))}, F2{m.zf, m.zf});
         const float2 z = *reinterpret_cast<const float2*>(&kz[gr][8 * q + 2 * j]), r = *reinterpret_cast<const float2*>(&kr[gr][8 * q + 2 * j]);
         c2[j] = codes2<3>(y, F2{z.x, z.y}, F2{r.x, r.y}, far);
       }
@@ -1085,11 +1095,11 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int2_kernel(
     const uint4* row = &vt.row[t][4 * gr];
     float mn, mx;
     const GroupMeta m = meta_i4(row, bad, mn, mx);
-    const float rs = rcp_of(m);
+    const float f = factor_of<15>(m);
     flush_vmax(m.sf, status);   // the INT4 V scales count toward the pool's V-scale maximum too
     const float c_lo = divided_one(mn, m.zf, m.sf, 15.0f), c_hi = divided_one(mx, m.zf, m.sf, 15.0f);
     const GroupMeta m2 = make_meta(__fmaf_rn(c_lo, m.sf, m.zf), __fmaf_rn(c_hi, m.sf, m.zf), 3.0f);
-    const float rs2 = rcp_of(m2);
+    const float f2 = factor_of<3>(m2);
     st_half(img, kI2VMeta + 2 * v_meta_index(t, gr), m2.s);
     st_half(img, kI2VMeta + 256 + 2 * v_meta_index(t, gr), m2.z);
     const float vmx = redux_max(m2.sf);
@@ -1103,12 +1113,12 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int2_kernel(
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float n = (float)(4 * y + 2 * j);
-        c[j] = codes2<3>(fma2(F2{n, n + 1.0f}, F2{m.sf, m.sf}, F2{m.zf, m.zf}), F2{-m2.zf, -m2.zf}, F2{rs2, rs2}, far);
+        c[j] = codes2<3>(fma2(F2{n, n + 1.0f}, F2{m.sf, m.sf}, F2{m.zf, m.zf}), F2{-m2.zf, -m2.zf}, F2{f2, f2}, far);
       }
       if (far > kTie) {
 #pragma unroll 1
         for (int n = 0; n < 4; ++n) {
-          const float x = divided_one(__fmaf_rn((float)(4 * y + n), m.sf, m.zf), m2.zf, m2.sf, 3.0f);
+          const float x = -divided_one(__fmaf_rn((float)(4 * y + n), m.sf, m.zf), m2.zf, m2.sf, 3.0f);
           if (n == 0) c[0].x = x;
           else if (n == 1) c[0].y = x;
           else if (n == 2) c[1].x = x;
@@ -1116,14 +1126,14 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int2_kernel(
         }
       }
       // below 2^24: two bytes at a time
-      const uint32_t l = __float_as_uint(fmaf(c[0].y, 256.0f, c[0].x) + 8388608.0f), u = __float_as_uint(fmaf(c[1].y, 256.0f, c[1].x) + 8388608.0f);
+      const uint32_t l = __float_as_uint(8388608.0f - fmaf(c[0].y, 256.0f, c[0].x)), u = __float_as_uint(8388608.0f - fmaf(c[1].y, 256.0f, c[1].x));
       tab[y] = __byte_perm(l, u, 0x5410u);
     }
     uint32_t half[2] = {0u, 0u};   // channels 0..15 and 16..31 as 2-bit fields
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       F2 c[4];
-      const uint32_t cw = quant_i4_8(row[q], m, rs, c);
+      const uint32_t cw = quant_i4_8(row[q], m, f, c);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const uint32_t sel = cw >> (16 * y);
@@ -1154,7 +1164,7 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int2_kernel(
     }
   }
   if (__any_sync(0xFFFFFFFFu, bad) && t == 0) atomicOr(status, kStatusRange);
-  if (pos && h == 0) write_positions(pos, job.dst, toks + job.tok_off, job.pos0, 0, kPage);
+  if (pos && h == 0 && gr == 0) pos[(size_t)job.dst * kPage + t] = job.pos0 + T;
   __syncthreads();
   uint4* out4 = reinterpret_cast<uint4*>(pool + ((size_t)job.dst * hkv + h) * kInt2Block);
   const uint4* img4 = reinterpret_cast<const uint4*>(img);

@@ -115,6 +115,7 @@ kv_status_t rope_args(const char* what, const kv_rope_t* rope, const int32_t* po
   R.half = rope->rot_dim / 2;
   R.pairs = rope->interleaved ? 1 : 0;
   R.n_axes = rope->n_axes;
+  R.minus0 = -0.0f;
   for (int f = 0; rope->axis && f < R.half; ++f) {
     if (rope->axis[f] >= rope->n_axes)
       return fail(KV_ERR_INVALID_ARG, "%s: frequency %d has axis %d of %d", what, f, rope->axis[f], rope->n_axes);

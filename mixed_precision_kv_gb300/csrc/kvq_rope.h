@@ -23,6 +23,7 @@ struct RopeArgs {
   int32_t rows, half;
   int32_t pairs;         // 1: neighbouring channels
   int32_t n_axes;
+  float minus0;          // -0: see rope_uv2
   uint32_t axis[4];      // axis of frequency f: 2 bits at 2 (f & 15) of word f >> 4
   int64_t k_stride, v_stride;   // appends: elements from a token's rows to the next token's
 };
@@ -75,6 +76,18 @@ __device__ __forceinline__ uint32_t rope_bf2(float lo, float hi) {
 __device__ __forceinline__ float rope_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float rope_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// The same of two pairs at once: (u, v) = (a c - b s, b c + a s), each step rounded as above.  The products
+// are multiply-adds of R.minus0, which the compiler does not know: it merges a packed product and a sum into
+// one rounding, whatever their modifiers.
+__device__ __forceinline__ void rope_uv2(const RopeArgs& R, float2 a, float2 b, float2 c, float2 s, float2& u, float2& v) {
+  asm("{.reg .b64 a, b, c, s, n, x, y, o;\n mov.b64 a, {%4, %5};\n mov.b64 b, {%6, %7};\n mov.b64 c, {%8, %9};\n"
+      " mov.b64 s, {%10, %11};\n mov.b64 n, {%12, %13};\n mov.b64 o, {%14, %14};\n"
+      " fma.rn.f32x2 x, a, c, o;\n fma.rn.f32x2 y, b, n, o;\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n"
+      " fma.rn.f32x2 x, b, c, o;\n fma.rn.f32x2 y, a, s, o;\n add.rn.f32x2 x, x, y;\n mov.b64 {%2, %3}, x;}"
+      : "=f"(u.x), "=f"(u.y), "=f"(v.x), "=f"(v.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(s.x), "f"(s.y), "f"(-s.x), "f"(-s.y), "f"(R.minus0));
+}
+
 // A row of 128 channels is 16 chunks of 8; item i of a row takes two of them: for i < rot_dim / 16 those of
 // frequencies 8 i .. 8 i + 7, else two that pass.
 __device__ __forceinline__ void rope_item(const RopeArgs& R, int i, int& a, int& b) {
@@ -85,19 +98,26 @@ __device__ __forceinline__ void rope_item(const RopeArgs& R, int i, int& a, int&
 // Rotates an item's chunks.
 __device__ __forceinline__ void rope_turn(const RopeArgs& R, uint4& x, uint4& y, const float (&c)[8], const float (&s)[8]) {
   uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+  float2 u, v;
   if (!R.pairs) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float a0 = rope_lo(a[k]), a1 = rope_hi(a[k]), b0 = rope_lo(b[k]), b1 = rope_hi(b[k]);
-      a[k] = rope_bf2(rope_u(a0, b0, c[2 * k], s[2 * k]), rope_u(a1, b1, c[2 * k + 1], s[2 * k + 1]));
-      b[k] = rope_bf2(rope_v(a0, b0, c[2 * k], s[2 * k]), rope_v(a1, b1, c[2 * k + 1], s[2 * k + 1]));
+      rope_uv2(R, make_float2(rope_lo(a[k]), rope_hi(a[k])), make_float2(rope_lo(b[k]), rope_hi(b[k])),
+               make_float2(c[2 * k], c[2 * k + 1]), make_float2(s[2 * k], s[2 * k + 1]), u, v);
+      a[k] = rope_bf2(u.x, u.y);
+      b[k] = rope_bf2(v.x, v.y);
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float a0 = rope_lo(a[k]), a1 = rope_hi(a[k]), b0 = rope_lo(b[k]), b1 = rope_hi(b[k]);
-      a[k] = rope_bf2(rope_u(a0, a1, c[k], s[k]), rope_v(a0, a1, c[k], s[k]));
-      b[k] = rope_bf2(rope_u(b0, b1, c[4 + k], s[4 + k]), rope_v(b0, b1, c[4 + k], s[4 + k]));
+    for (int k = 0; k < 4; k += 2) {
+      rope_uv2(R, make_float2(rope_lo(a[k]), rope_lo(a[k + 1])), make_float2(rope_hi(a[k]), rope_hi(a[k + 1])),
+               make_float2(c[k], c[k + 1]), make_float2(s[k], s[k + 1]), u, v);
+      a[k] = rope_bf2(u.x, v.x);
+      a[k + 1] = rope_bf2(u.y, v.y);
+      rope_uv2(R, make_float2(rope_lo(b[k]), rope_lo(b[k + 1])), make_float2(rope_hi(b[k]), rope_hi(b[k + 1])),
+               make_float2(c[4 + k], c[5 + k]), make_float2(s[4 + k], s[5 + k]), u, v);
+      b[k] = rope_bf2(u.x, v.x);
+      b[k + 1] = rope_bf2(u.y, v.y);
     }
   }
   x = make_uint4(a[0], a[1], a[2], a[3]);
