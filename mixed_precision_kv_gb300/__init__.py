@@ -223,7 +223,7 @@ class KVPool:
         self.n_int3_pages = n_int3_pages
         self.n_fp4_pages = n_fp4_pages
         self.device = device
-        self._dev = f"cuda:{device}"
+        self._dev = None   # torch.device, made when it is first needed
 
     @property
     def handle(self):
@@ -356,23 +356,27 @@ class KVPool:
         end), dequantized -> (k, v), CUDA [sum(n)][Hkv][128], bf16 or dtype=torch.float32; evicted
         tokens are zeros.  first, n: ints or host sequences [requests]."""
         torch = _torch_mod()
-        dtype = torch.bfloat16 if dtype is None else dtype
-        if dtype not in (torch.bfloat16, torch.float32):
+        if dtype is None:
+            dtype = torch.bfloat16
+        elif dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("dtype must be torch.bfloat16 or torch.float32")
-        req_ids = np.atleast_1d(_np(req_ids, np.int32))
-        first = np.full(req_ids.size, int(first), np.int64) if np.ndim(first) == 0 else _np(first, np.int64)
+        req_ids = _np(req_ids, np.int32).reshape(-1)
+        first = np.full(req_ids.size, first, np.int64) if isinstance(first, int) else _np(first, np.int64)
         if n is None:
             n = np.empty(req_ids.size, np.int64)
             rc = self._L.kv_request_lengths(self._h, req_ids.ctypes.data, req_ids.size, n.ctypes.data)
             if rc:
                 _check(rc, "kv_request_lengths")
-            n -= first
+            if first.shape == n.shape:
+                n -= first
         else:
-            n = np.full(req_ids.size, int(n), np.int64) if np.ndim(n) == 0 else _np(n, np.int64)
-        if req_ids.ndim != 1 or first.shape != req_ids.shape or n.shape != req_ids.shape:
+            n = np.full(req_ids.size, n, np.int64) if isinstance(n, int) else _np(n, np.int64)
+        if first.shape != req_ids.shape or n.shape != req_ids.shape:
             raise ValueError("req_ids, first and n must be sequences of one length")
-        if n.size and int(n.min()) < 0:
+        if n.size and n.min() < 0:
             raise ValueError("n must not be negative")
+        if self._dev is None:
+            self._dev = torch.device("cuda", self.device)
         shape = (int(n.sum()), self.num_kv_heads, HEAD_DIM)
         k, v = _empty(shape, dtype, self._dev, stream), _empty(shape, dtype, self._dev, stream)
         rc = self._L.kv_read_tokens(self._h, req_ids.ctypes.data, first.ctypes.data, n.ctypes.data, req_ids.size,

@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) attend_join_kernel(AttArgs A,
                                                                       const AttSrc* __restrict__ srcs,
                                                                       const float* __restrict__ part) {
   const AttJoin J = joins[blockIdx.y];
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // (the plan was there before the kernels that this one follows)
   const int i = blockIdx.x * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (i >= J.rows) return;
   const int ip = J.pre_row + i;
@@ -250,9 +251,9 @@ cudaError_t launch_attend_join(kv_pool* P, const AttArgs& A, const AttUnit* d_un
                                int max_rows, const AttSrc* d_srcs, const float* d_part, cudaStream_t s) {
   for (int a = 0; a < n_joins; a += 65535) {
     ++P->launches;
-    attend_join_kernel<<<dim3((unsigned)((max_rows + kMergeRows - 1) / kMergeRows), (unsigned)std::min(65535, n_joins - a)),
-                         32 * kMergeRows, 0, s>>>(A, d_units, d_joins + a, d_srcs, d_part);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        launch_pdl(attend_join_kernel, dim3((unsigned)((max_rows + kMergeRows - 1) / kMergeRows), (unsigned)std::min(65535, n_joins - a)),
+                   dim3(32 * kMergeRows), 0, s, A, d_units, d_joins + a, d_srcs, d_part);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -546,7 +547,9 @@ struct AttSet {
     at.second = add(pl, xl.parts, 128);
     return at;
   }
-  kv_status_t launch(kv_pool* P, const AttArgs& A, int64_t tiles, cudaStream_t s) const {
+  // chain: as launch_attend_few, where the set is one launch of that kernel
+  bool one_launch() const { return wide.empty() && !few.empty() && pf.merges.empty(); }
+  kv_status_t launch(kv_pool* P, const AttArgs& A, int64_t tiles, cudaStream_t s, int chain = 0) const {
     uint8_t* base = (uint8_t*)P->attend.ptr;
     auto merge = [&](const Placed& x, const AttPlan& p, int part_rows) -> cudaError_t {
       if (p.merges.empty()) return cudaSuccess;
@@ -555,7 +558,8 @@ struct AttSet {
     };
     if (!few.empty()) {
       KV_CUDA(launch_attend_few(P, R, A, (const AttUnit*)(base + xf.units), (const AttItem*)(base + xf.items),
-                                (const int32_t*)(base + xf.ctas), (int)pf.cta_item.size() - 1, (float*)(base + xf.parts), s));
+                                (const int32_t*)(base + xf.ctas), (int)pf.cta_item.size() - 1, (float*)(base + xf.parts), s,
+                                chain));
       KV_CUDA(merge(xf, pf, R));
     }
     if (wide.empty()) return KV_OK;
@@ -769,9 +773,32 @@ extern "C" kv_status_t kv_attend_shared(kv_pool_t* P, const void* q, const void*
       w.joined = group_of[(size_t)b] >= 0;
       own.push_back(w);
     }
-  AttSet SP, SO;
-  SP.plan(pre, g, hkv, tree != nullptr, P->sm_count);
-  SO.plan(own, g, hkv, tree != nullptr, P->sm_count);
+  // One launch for both kinds where their rows go by blocks of one size, or where there is so little
+  // work that a launch more counts for more than the larger blocks: 4 x 2K tokens of 2 kv heads.
+  auto few_size = [&](const std::vector<AttUnit>& units, int64_t& tiles) {
+    int rows = 0;
+    for (const AttUnit& w : units) {
+      rows = std::max(rows, w.T * g);
+      tiles += block_tiles(w, g, 0, w.T * g, tree != nullptr);
+    }
+    return rows;
+  };
+  int64_t tiles_in_all = 0;
+  const int pre_rows = few_size(pre, tiles_in_all), own_rows = few_size(own, tiles_in_all);
+  auto size_of = [](int rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); };
+  const bool together = !pre.empty() && std::max(pre_rows, own_rows) <= kFewRows &&
+                        (size_of(pre_rows) == size_of(own_rows) || tiles_in_all <= 2 * (int64_t)P->sm_count);
+  const size_t n_pre = pre.size();
+  AttSet SP, SO;   // together: SO holds the prefixes' units too, first
+  if (together) {
+    std::vector<AttUnit> all(pre);
+    all.insert(all.end(), own.begin(), own.end());
+    SO.plan(all, g, hkv, tree != nullptr, P->sm_count);
+  } else {
+    SP.plan(pre, g, hkv, tree != nullptr, P->sm_count);
+    SO.plan(own, g, hkv, tree != nullptr, P->sm_count);
+  }
+  const size_t o0 = together ? n_pre : 0;   // the first own unit of SO
 
   // ---- joins; where a unit's blocks are: units go to a set's two lists in order
   std::vector<AttJoin> joins;   // of own units with few rows, then of those with many
@@ -793,23 +820,25 @@ extern "C" kv_status_t kv_attend_shared(kv_pool_t* P, const void* q, const void*
     o_joins = u.add(joins.data(), n_joins * sizeof(AttJoin));
     o_srcs = u.add(srcs.data(), n_src * sizeof(AttSrc));
     end = SO.place_parts(SP.place_parts((u.size + 255) & ~size_t(255)));
-    const auto ps = SP.add_srcs(0, srcs), os = SO.add_srcs(0, srcs);
+    const auto ps0 = SP.add_srcs(0, srcs), os = SO.add_srcs(0, srcs);
+    const auto ps = together ? os : ps0;
+    const AttSet& PS = together ? SO : SP;   // where the prefixes' units are
     auto log2i = [](int x) { int n = 0; while ((1 << n) < x) ++n; return n; };
     size_t at_few = 0, at_wide = 0;
-    for (size_t x = 0; x < own.size(); ++x) at_wide += own[x].joined && !SO.where[x].wide ? 1 : 0;
+    for (size_t x = 0; x < own.size(); ++x) at_wide += own[x].joined && !SO.where[o0 + x].wide ? 1 : 0;
     n_few_joins = at_wide;
     size_t x = 0;
     for (int32_t b = 0; b < n_req; ++b)
       for (int h = 0; h < hkv && n_new[b] > 0; ++h, ++x) {
         if (!own[x].joined) continue;
-        const AttSet::Where o = SO.where[x], p = SP.where[(size_t)group_of[(size_t)b] * hkv + h];
+        const AttSet::Where o = SO.where[o0 + x], p = PS.where[(size_t)group_of[(size_t)b] * hkv + h];
         AttJoin J;
         J.unit = o.index;
         J.rows = n_new[b] * g;
         J.own0 = o.wide ? os.second + SO.pl.src0[(size_t)o.index] : os.first + SO.pf.src0[(size_t)o.index];
         J.own_shift = o.wide ? 7 : log2i(SO.R);
-        J.pre0 = p.wide ? ps.second + SP.pl.src0[(size_t)p.index] : ps.first + SP.pf.src0[(size_t)p.index];
-        J.pre_shift = p.wide ? 7 : log2i(SP.R);
+        J.pre0 = p.wide ? ps.second + PS.pl.src0[(size_t)p.index] : ps.first + PS.pf.src0[(size_t)p.index];
+        J.pre_shift = p.wide ? 7 : log2i(PS.R);
         J.pre_row = (int32_t)pre_tok[(size_t)b] * g;
         J.tall = o.wide | (p.wide << 1);
         joins[o.wide ? at_wide++ : at_few++] = J;
@@ -821,8 +850,10 @@ extern "C" kv_status_t kv_attend_shared(kv_pool_t* P, const void* q, const void*
   if ((st = h2d(P, P->attend.ptr, u, s)) != KV_OK) return st;
   uint8_t* base = (uint8_t*)P->attend.ptr;
   A.tok_map = (const int32_t*)(base + o_map);
-  if ((st = SP.launch(P, A, tiles, s)) != KV_OK) return st;
-  if ((st = SO.launch(P, A, tiles, s)) != KV_OK) return st;
+  // the second launch starts as CTAs of the first leave, the joins as those of the second do
+  const bool chained = SP.one_launch() && SO.one_launch();
+  if ((st = SP.launch(P, A, tiles, s, chained ? kChainNext : 0)) != KV_OK) return st;
+  if ((st = SO.launch(P, A, tiles, s, SO.one_launch() ? kChainNext | (chained ? kChainPrev : 0) : 0)) != KV_OK) return st;
   const AttJoin* dj = (const AttJoin*)(base + o_joins);
   const AttSrc* ds = (const AttSrc*)(base + o_srcs);
   KV_CUDA(launch_attend_join(P, A, (const AttUnit*)(base + SO.xf.units), dj, (int)n_few_joins, join_rows, ds,

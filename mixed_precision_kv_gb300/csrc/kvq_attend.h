@@ -108,9 +108,13 @@ cudaError_t launch_attend_simt(kv_pool* P, const AttArgs& A, const AttUnit* d_un
                                cudaStream_t s);
 
 // Tensor-core kernel for few rows per unit (kvq_attend_few.cu): blocks of `rows`
-// (16, 32 or 64) rows, one partial of that many rows per item.
+// (16, 32 or 64) rows, one partial of that many rows per item.  chain: launched so that the stream's next
+// kernel may start as this one's CTAs leave (kChainNext), or as the one before it does so (kChainPrev: this
+// launch must not read what that kernel writes); a kernel that follows either with griddepcontrol.wait, or
+// plainly, starts when both are done.
+enum : int { kChainNext = 1, kChainPrev = 2 };
 cudaError_t launch_attend_few(kv_pool* P, int rows, const AttArgs& A, const AttUnit* d_units, const AttItem* d_items,
-                              const int32_t* d_cta_item, int n_ctas, float* d_part, cudaStream_t s);
+                              const int32_t* d_cta_item, int n_ctas, float* d_part, cudaStream_t s, int chain = 0);
 
 // Tensor-core kernels for many rows per unit (kvq_attend_wide.cu): the units' keys
 // as operand tiles (64 KB and four live words per 128 keys), then blocks of 256

@@ -138,7 +138,8 @@ __device__ __forceinline__ bool elect_one() {
 template <int R>
 __global__ void __launch_bounds__(kThreads<R>, 1) attend_few_kernel(
     AttArgs A, const AttUnit* __restrict__ units, const AttItem* __restrict__ items, const int32_t* __restrict__ cta_item,
-    float* __restrict__ part, uint32_t first_spins) {
+    float* __restrict__ part, uint32_t first_spins, int chain) {
+  if (chain & kChainNext) asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   FewSmem<R>& S = *reinterpret_cast<FewSmem<R>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -681,11 +682,12 @@ __global__ void __launch_bounds__(kThreads<R>, 1) attend_few_kernel(
     tm_fence_after();
     tm_free(tmem, 512);
   }
+  if (chain & kChainPrev) asm volatile("griddepcontrol.wait;" ::: "memory");   // what waits for this grid waits for that one too
 }
 
 template <int R>
 cudaError_t launch_r(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const AttItem* d_items,
-                     const int32_t* d_cta_item, int n_ctas, float* d_part, cudaStream_t s) {
+                     const int32_t* d_cta_item, int n_ctas, float* d_part, cudaStream_t s, int chain) {
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -696,20 +698,24 @@ cudaError_t launch_r(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const
     attr_set.fetch_or(uint64_t(1) << dev);
   }
   ++P->launches;
-  attend_few_kernel<R><<<(unsigned)n_ctas, kThreads<R>, sizeof(FewSmem<R>), s>>>(
-      A, d_units, d_items, d_cta_item, d_part, P->first_wait_spins < 0 ? kAttSpin : (uint32_t)P->first_wait_spins);
+  const uint32_t spins = P->first_wait_spins < 0 ? kAttSpin : (uint32_t)P->first_wait_spins;
+  if (chain & kChainPrev)
+    return launch_pdl(attend_few_kernel<R>, dim3((unsigned)n_ctas), dim3(kThreads<R>), sizeof(FewSmem<R>), s, A, d_units,
+                      d_items, d_cta_item, d_part, spins, chain);
+  attend_few_kernel<R><<<(unsigned)n_ctas, kThreads<R>, sizeof(FewSmem<R>), s>>>(A, d_units, d_items, d_cta_item, d_part,
+                                                                                 spins, chain);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_attend_few(kv_pool* P, int rows, const AttArgs& A, const AttUnit* d_units, const AttItem* d_items,
-                              const int32_t* d_cta_item, int n_ctas, float* d_part, cudaStream_t s) {
+                              const int32_t* d_cta_item, int n_ctas, float* d_part, cudaStream_t s, int chain) {
   if (n_ctas <= 0) return cudaSuccess;
   switch (rows) {
-    case 16: return launch_r<16>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s);
-    case 32: return launch_r<32>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s);
-    case 64: return launch_r<64>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s);
+    case 16: return launch_r<16>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s, chain);
+    case 32: return launch_r<32>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s, chain);
+    case 64: return launch_r<64>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s, chain);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -172,7 +172,17 @@ def test_not_finite_rows(kvq):
     assert e.value.status == kvq.KV_ERR_RANGE
     fin = torch.isfinite(out).all(-1)
     assert not bool(fin[1, 2]) and not bool(fin[3, 0]) and int(fin.sum()) == 14
-    assert torch.equal(out[fin], good[fin])
+    # The rows of a block refresh their maxima together, and a row without one asks for it at every key tile, so the
+    # others' weights 2^(x - m + 7) may be scaled by another power of two: exact in x, each weight is still rounded by
+    # 2^-11 of itself.  Both results are therefore within the operator's own tolerance of the 64-bit one.
+    C = [P.content(r) for r in range(3)]
+    for t, r in enumerate((1, 1, 2, 2)):
+        K, V = (np.concatenate([getattr(C[0], m)[0], getattr(C[r], m)[0]]) for m in "KV")
+        for j in range(4):
+            if bool(fin[t, j]):
+                o, tol = attend_row(q[t, j].double().cpu().numpy(), K, V, SCALE, U)
+                for x in (out, good):
+                    assert np.all(np.abs(x[t, j].double().cpu().numpy() - o) <= tol)
     pool.sync()
     pool.destroy()
 
