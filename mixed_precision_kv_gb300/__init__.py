@@ -117,8 +117,11 @@ def _check(rc, what):
         raise KVError(rc, f"{what}: {msg}")
 
 
+_dtypes = {t: np.dtype(t) for t in (np.int32, np.int64, np.uint8, np.float64)}
+
+
 def _np(a, dtype):
-    if type(a) is np.ndarray and a.dtype == dtype and a.flags.c_contiguous:
+    if type(a) is np.ndarray and a.dtype is _dtypes[dtype] and a.flags.c_contiguous:
         return a
     return np.ascontiguousarray(np.asarray(a), dtype=dtype)
 
@@ -373,11 +376,12 @@ class KVPool:
             n = np.full(req_ids.size, n, np.int64) if isinstance(n, int) else _np(n, np.int64)
         if first.shape != req_ids.shape or n.shape != req_ids.shape:
             raise ValueError("req_ids, first and n must be sequences of one length")
-        if n.size and n.min() < 0:
+        rows = n.tolist()
+        if rows and min(rows) < 0:
             raise ValueError("n must not be negative")
         if self._dev is None:
             self._dev = torch.device("cuda", self.device)
-        shape = (int(n.sum()), self.num_kv_heads, HEAD_DIM)
+        shape = (sum(rows), self.num_kv_heads, HEAD_DIM)
         k, v = _empty(shape, dtype, self._dev, stream), _empty(shape, dtype, self._dev, stream)
         rc = self._L.kv_read_tokens(self._h, req_ids.ctypes.data, first.ctypes.data, n.ctypes.data, req_ids.size,
                                     int(dtype is torch.float32), k.data_ptr(), v.data_ptr(), _stream(stream, self.device))
@@ -442,7 +446,7 @@ class KVPool:
         return int(n.value)
 
     def _on_pool_device(self, t):
-        return t.is_cuda and t.device.index == self.device
+        return t.get_device() == self.device   # (-1: not on a GPU)
 
     def decode(self, q, req_ids, softmax_scale, out=None, stream=None):
         """q: torch bf16 CUDA [B][Hq][128] -> out fp32 [B][Hq][128], both on the pool's device."""
@@ -519,8 +523,9 @@ class KVPool:
         n_new = _np(n_new, np.int32)
         if req_ids.ndim != 1 or n_new.shape != req_ids.shape:
             raise ValueError("req_ids and n_new must be sequences of one length")
-        n = int(n_new.sum(dtype=np.int64))
-        if q.dim() != 3 or q.shape[0] != n or q.shape[2] != HEAD_DIM or q.dtype is not torch.bfloat16 or \
+        n = sum(n_new.tolist())
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != n or shape[2] != HEAD_DIM or q.dtype is not torch.bfloat16 or \
                 not self._on_pool_device(q) or not q.is_contiguous():
             raise ValueError("q must be a contiguous bf16 tensor [sum(n_new)][Hq][128] on the pool's device")
         if (k is None) != (v is None):
@@ -532,8 +537,8 @@ class KVPool:
                                  not self._on_pool_device(tree) or not tree.is_contiguous()):
             raise ValueError("tree must be a contiguous int64 tensor [sum(n_new)] on the pool's device")
         if out is None:
-            out = _empty(q.shape, q.dtype, q.device, stream)
-        elif out.dtype is not torch.bfloat16 or out.shape != q.shape or not self._on_pool_device(out) or \
+            out = _empty(shape, torch.bfloat16, q.device, stream)
+        elif out.dtype is not torch.bfloat16 or out.shape != shape or not self._on_pool_device(out) or \
                 not out.is_contiguous():
             raise ValueError("out must be a contiguous bf16 tensor shaped like q on the pool's device")
         return req_ids, n_new, out
