@@ -13,7 +13,7 @@ SOURCES = ["kvq_pool.cu", "kvq_quant.cu", "kvq_decode_simt.cu", "kvq_decode_mma.
            "kvq_decode_score.cu", "kvq_select.cu", "kvq_attend.cu", "kvq_attend_simt.cu", "kvq_attend_wide.cu", "kvq_attend_few.cu",
            "kvq_rope.cu", "kvq_read.cu"]
 HEADERS = ["kvq_internal.h", "kvq_host.h", "kvq_grow.h", "kvq_layout.cuh", "kvq_scan_mma.cuh", "kvq_attend.h",
-           "kvq_attend_mma.cuh", "kvq_rope.h"]
+           "kvq_attend_mma.cuh", "kvq_rope.h", "kvq_values.cuh"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
 

@@ -11,8 +11,8 @@
 #include <new>
 #include <vector>
 
-#include "kvq_attend.h"
 #include "kvq_host.h"
+#include "kvq_values.cuh"
 
 namespace kvq {
 namespace {
@@ -172,65 +172,146 @@ struct PartRow {
   const float *o, *ml;   // this lane's four channels of part 0, its m and l
   size_t step;
   int n;
+  float head;            // what its maxima lack of the attention kernels' (kAttHead or 0)
 };
 __device__ __forceinline__ PartRow part_row(const AttSrc& S, const float* part, int r, int lane, bool tall) {
   const float* p = part + S.off;
-  return tall ? PartRow{p + (size_t)lane * (4 * kTallRows) + 4 * r, p + kTallRows * kHeadDim + 2 * r, (size_t)S.step, S.n_parts}
-              : PartRow{p + (size_t)r * kAttPart + 4 * lane, p + (size_t)r * kAttPart + kHeadDim, (size_t)S.step, S.n_parts};
+  return tall ? PartRow{p + (size_t)lane * (4 * kTallRows) + 4 * r, p + kTallRows * kHeadDim + 2 * r, (size_t)S.step, S.n_parts, 0.0f}
+              : PartRow{p + (size_t)r * kAttPart + 4 * lane, p + (size_t)r * kAttPart + kHeadDim, (size_t)S.step, S.n_parts, 0.0f};
 }
-__global__ void __launch_bounds__(32 * kMergeRows) attend_join_kernel(AttArgs A, const AttUnit* __restrict__ units,
-                                                                      const AttJoin* __restrict__ joins,
-                                                                      const AttSrc* __restrict__ srcs,
-                                                                      const float* __restrict__ part) {
-  const AttJoin J = joins[blockIdx.y];
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // (the plan was there before the kernels that this one follows)
-  const int i = blockIdx.x * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (i >= J.rows) return;
-  const int ip = J.pre_row + i;
-  const PartRow two[2] = {
-      part_row(srcs[J.own0 + (i >> J.own_shift)], part, i & ((1 << J.own_shift) - 1), lane, J.tall & 1),
-      part_row(srcs[J.pre0 + (ip >> J.pre_shift)], part, ip & ((1 << J.pre_shift) - 1), lane, (J.tall & 2) != 0)};
+// The largest maximum of a row's parts.
+__device__ __forceinline__ float part_max(const PartRow& R, int lane) {
   float M = -INFINITY;
-#pragma unroll
-  for (int x = 0; x < 2; ++x)
-    for (int p = lane; p < two[x].n; p += 32) M = fmaxf(M, two[x].ml[(size_t)p * two[x].step]);
+  for (int p = lane; p < R.n; p += 32) M = fmaxf(M, R.ml[(size_t)p * R.step]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-  float L = 0.0f;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  return M + R.head;
+}
+// Adds a row's parts, relative to the maximum M: L per lane (to be summed), o.
+__device__ __forceinline__ void part_add(const PartRow& R, int lane, float M, float& L, float4& o) {
+  for (int p0 = 0; p0 < R.n; p0 += 32) {
+    float f = 0.0f;
+    if (p0 + lane < R.n) {
+      const float2 ml = *reinterpret_cast<const float2*>(R.ml + (size_t)(p0 + lane) * R.step);
+      // a part that saw nothing (m = -inf, l = 0) adds nothing; one with a NaN sum keeps it
+      f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2f(ml.x + R.head - M);
+      L = fmaf(ml.y, f, L);
+    }
+    const int n = min(32, R.n - p0);
+    for (int p = 0; p < n; p += 8) {
+      float4 a[8];
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const PartRow& R = two[x];
-    for (int p0 = 0; p0 < R.n; p0 += 32) {
-      float f = 0.0f;
-      if (p0 + lane < R.n) {
-        const float2 ml = *reinterpret_cast<const float2*>(R.ml + (size_t)(p0 + lane) * R.step);
-        // a part that saw nothing (m = -inf, l = 0) adds nothing; one with a NaN sum keeps it
-        f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2f(ml.x - M);
-        L = fmaf(ml.y, f, L);
-      }
-      const int n = min(32, R.n - p0);
-      for (int p = 0; p < n; p += 8) {
-        float4 a[8];
+      for (int y = 0; y < 8; ++y) a[y] = *reinterpret_cast<const float4*>(R.o + (size_t)(p0 + min(p + y, n - 1)) * R.step);
 #pragma unroll
-        for (int y = 0; y < 8; ++y) a[y] = *reinterpret_cast<const float4*>(R.o + (size_t)(p0 + min(p + y, n - 1)) * R.step);
-#pragma unroll
-        for (int y = 0; y < 8; ++y) {
-          const float w = __shfl_sync(0xFFFFFFFFu, f, (p + y) & 31);
-          if (p + y < n && w != 0.0f) {
-            o.x = fmaf(a[y].x, w, o.x); o.y = fmaf(a[y].y, w, o.y); o.z = fmaf(a[y].z, w, o.z); o.w = fmaf(a[y].w, w, o.w);
-          }
+      for (int y = 0; y < 8; ++y) {
+        const float w = __shfl_sync(0xFFFFFFFFu, f, (p + y) & 31);
+        if (p + y < n && w != 0.0f) {
+          o.x = fmaf(a[y].x, w, o.x); o.y = fmaf(a[y].y, w, o.y); o.z = fmaf(a[y].z, w, o.z); o.w = fmaf(a[y].w, w, o.w);
         }
       }
     }
   }
+}
+__device__ __forceinline__ bool finite4(const float4& o) {
+  return fabsf(o.x) < INFINITY && fabsf(o.y) < INFINITY && fabsf(o.z) < INFINITY && fabsf(o.w) < INFINITY;
+}
+
+// A row over its request's pages, plainly (as the CUDA-core kernel): where the scan's parts do not say it.  A
+// warp: a slot per lane for the logits, four channels for the sums.
+struct PlainRow {
+  float m, l;
+  float4 o;
+};
+__device__ __noinline__ PlainRow plain_row(const AttArgs& A, const uint16_t* q, int req, int kvh, int n_pages) {
+  const int lane = threadIdx.x & 31;
+  PlainRow R{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  bool seen = false, wild = false;
+  for (int p = 0; p < n_pages; ++p) {
+    const Entry e = A.table[(size_t)req * A.max_pages + p];
+    const uint32_t live = A.hdead ? e.live & ~A.hdead[(size_t)e.id * A.hkv + kvh] : e.live;
+    if (live == 0u) continue;
+    seen = true;
+    const uint8_t* b;
+    const int cls = att_page(A, e.id, kvh, b);
+    const bool on = (live >> lane) & 1u;
+    float s = 0.0f;
+    for (int c = 0; on && c < kHeadDim; ++c) s = fmaf(__uint_as_float((uint32_t)q[c] << 16), k_value(b, cls, lane, c), s);
+    const bool whole = fabsf(s) < INFINITY;
+    s *= A.scale_log2;
+    // past fp32's range, above or below: the row is not a number
+    if (__any_sync(0xFFFFFFFFu, on && !(whole && s < INFINITY))) wild = true;
+    s = on && whole && s < INFINITY ? s : -INFINITY;
+    float mx = s;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+    const float mn = fmaxf(R.m, mx);
+    if (mn == -INFINITY) continue;
+    const float corr = exp2f(R.m - mn), w = exp2f(s - mn);
+    float ws = w;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ws += __shfl_xor_sync(0xFFFFFFFFu, ws, o);
+    R.l = R.l * corr + ws;
+    R.m = mn;
+    R.o.x *= corr; R.o.y *= corr; R.o.z *= corr; R.o.w *= corr;
+    for (int t = 0; t < kPage; ++t) {
+      const float wt = __shfl_sync(0xFFFFFFFFu, w, t);
+      if (!((live >> t) & 1u)) continue;   // slots never written hold no values
+      R.o.x = fmaf(wt, v_value(b, cls, t, 4 * lane), R.o.x);
+      R.o.y = fmaf(wt, v_value(b, cls, t, 4 * lane + 1), R.o.y);
+      R.o.z = fmaf(wt, v_value(b, cls, t, 4 * lane + 2), R.o.z);
+      R.o.w = fmaf(wt, v_value(b, cls, t, 4 * lane + 3), R.o.w);
+    }
+  }
+  if (wild || (seen && R.m == -INFINITY)) R.l = __int_as_float(0x7FFFFFFF);
+  return R;
+}
+
+// The decode scan gives a dead slot the logit kSentinel and the value 0.  Above kSentinel + 160 a maximum leaves it
+// no weight (2^-160 is 0), as here; a row below that, or one that is not finite, is taken plainly.
+constexpr float kSentinel = -1.0e4f * 1.4426950408889634f + kAttHead;
+
+__global__ void __launch_bounds__(32 * kMergeRows) attend_join_kernel(AttArgs A, const AttJoin* __restrict__ joins,
+                                                                      const AttSrc* __restrict__ srcs,
+                                                                      const float* __restrict__ part,
+                                                                      const Unit* __restrict__ scan_units,
+                                                                      const float* __restrict__ scan_part) {
+  const AttJoin J = joins[blockIdx.y];
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // (the plans were there before the kernels that this one follows)
+  const int i = blockIdx.x * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (i >= J.rows) return;
+  const int g = A.hq / A.hkv;
+  const size_t at = ((size_t)(J.tok0 + i / g) * A.hq + (size_t)J.kvh * g + i % g) * kHeadDim;
+  const bool scan = (J.flags & kJoinScan) != 0;
+  PartRow own, pre{nullptr, nullptr, 0, 0, 0.0f};
+  if (scan) {
+    const Unit u = scan_units[J.own0];
+    const float* p = scan_part + ((size_t)u.split_begin * g + i) * kAttPart;
+    own = PartRow{p + 4 * lane, p + kHeadDim, (size_t)g * kAttPart, u.n_splits, kAttHead};
+  } else {
+    own = part_row(srcs[J.own0 + (i >> J.own_shift)], part, i & ((1 << J.own_shift) - 1), lane, (J.flags & kJoinOwnTall) != 0);
+  }
+  if (J.pre0 >= 0) {
+    const int ip = J.pre_row + i;
+    pre = part_row(srcs[J.pre0 + (ip >> J.pre_shift)], part, ip & ((1 << J.pre_shift) - 1), lane, (J.flags & kJoinPreTall) != 0);
+  }
+  const float mo = part_max(own, lane), mp = part_max(pre, lane);
+  float L = 0.0f, M = fmaxf(mo, mp);
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  part_add(own, lane, M, L, o);
+  if (scan && J.n_pages > 0 && !(mo > kSentinel + 160.0f && __all_sync(0xFFFFFFFFu, finite4(o) && L < INFINITY))) {
+    PlainRow R = plain_row(A, A.q + at, J.req, J.kvh, J.n_pages);
+    R.m += kAttHead;
+    M = fmaxf(R.m, mp);
+    const float f = R.m == -INFINITY ? (R.l == 0.0f ? 0.0f : 1.0f) : exp2f(R.m - M);
+    L = lane == 0 ? R.l * f : 0.0f;
+    o = make_float4(R.o.x * f, R.o.y * f, R.o.z * f, R.o.w * f);
+  }
+  part_add(pre, lane, M, L, o);
 #pragma unroll
   for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, x);
   const float inv = row_inverse(M, L);
   const float r[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-  const AttUnit u = units[J.unit];
-  const int g = A.hq / A.hkv;
-  uint16_t* op = A.out + ((size_t)(u.tok0 + i / g) * A.hq + (size_t)u.kvh * g + i % g) * kHeadDim + 4 * lane;
+  uint16_t* op = A.out + at + 4 * lane;
   bool bad = false;
   uint32_t h[4];
 #pragma unroll
@@ -247,13 +328,14 @@ __global__ void __launch_bounds__(32 * kMergeRows) attend_join_kernel(AttArgs A,
   if (bad) atomicOr(A.status, kStatusRange);
 }
 
-cudaError_t launch_attend_join(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const AttJoin* d_joins, int n_joins,
-                               int max_rows, const AttSrc* d_srcs, const float* d_part, cudaStream_t s) {
+cudaError_t launch_attend_join(kv_pool* P, const AttArgs& A, const AttJoin* d_joins, int n_joins, int max_rows,
+                               const AttSrc* d_srcs, const float* d_part, const Unit* scan_units, const float* scan_part,
+                               cudaStream_t s) {
   for (int a = 0; a < n_joins; a += 65535) {
     ++P->launches;
-    const cudaError_t e =
-        launch_pdl(attend_join_kernel, dim3((unsigned)((max_rows + kMergeRows - 1) / kMergeRows), (unsigned)std::min(65535, n_joins - a)),
-                   dim3(32 * kMergeRows), 0, s, A, d_units, d_joins + a, d_srcs, d_part);
+    const cudaError_t e = launch_pdl(
+        attend_join_kernel, dim3((unsigned)((max_rows + kMergeRows - 1) / kMergeRows), (unsigned)std::min(65535, n_joins - a)),
+        dim3(32 * kMergeRows), 0, s, A, d_joins + a, d_srcs, d_part, scan_units, scan_part);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -775,19 +857,26 @@ extern "C" kv_status_t kv_attend_shared(kv_pool_t* P, const void* q, const void*
     }
   // One launch for both kinds where their rows go by blocks of one size, or where there is so little
   // work that a launch more counts for more than the larger blocks: 4 x 2K tokens of 2 kv heads.
-  auto few_size = [&](const std::vector<AttUnit>& units, int64_t& tiles) {
+  auto size_of = [&](const std::vector<AttUnit>& units, int64_t& tiles) {
     int rows = 0;
+    tiles = 0;
     for (const AttUnit& w : units) {
       rows = std::max(rows, w.T * g);
       tiles += block_tiles(w, g, 0, w.T * g, tree != nullptr);
     }
     return rows;
   };
-  int64_t tiles_in_all = 0;
-  const int pre_rows = few_size(pre, tiles_in_all), own_rows = few_size(own, tiles_in_all);
-  auto size_of = [](int rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); };
-  const bool together = !pre.empty() && std::max(pre_rows, own_rows) <= kFewRows &&
-                        (size_of(pre_rows) == size_of(own_rows) || tiles_in_all <= 2 * (int64_t)P->sm_count);
+  int64_t pre_tiles, own_tiles;
+  const int pre_rows = size_of(pre, pre_tiles), own_rows = size_of(own, own_tiles);
+  auto block_of = [](int rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); };
+  const bool little = pre_tiles + own_tiles <= 2 * (int64_t)P->sm_count;
+  // A decode step (a token per request, nothing but caches): the decode's scan reads the own caches at 2.2 to 2.6 us
+  // per 1000 tiles; the few-row kernel takes 8 for rows that fill a quarter or half of its blocks.
+  bool scan = !k && !little && own_tiles > 4 * (int64_t)P->sm_count;
+  for (int32_t b = 0; b < n_req && scan; ++b)
+    scan = n_new[b] == 1 && (P->n_fp.empty() || P->n_fp[req_ids[b]] == 0);
+  const bool together = !scan && !pre.empty() && std::max(pre_rows, own_rows) <= kFewRows &&
+                        (block_of(pre_rows) == block_of(own_rows) || little);
   const size_t n_pre = pre.size();
   AttSet SP, SO;   // together: SO holds the prefixes' units too, first
   if (together) {
@@ -796,70 +885,83 @@ extern "C" kv_status_t kv_attend_shared(kv_pool_t* P, const void* q, const void*
     SO.plan(all, g, hkv, tree != nullptr, P->sm_count);
   } else {
     SP.plan(pre, g, hkv, tree != nullptr, P->sm_count);
-    SO.plan(own, g, hkv, tree != nullptr, P->sm_count);
+    if (!scan) SO.plan(own, g, hkv, tree != nullptr, P->sm_count);
   }
   const size_t o0 = together ? n_pre : 0;   // the first own unit of SO
 
   // ---- joins; where a unit's blocks are: units go to a set's two lists in order
-  std::vector<AttJoin> joins;   // of own units with few rows, then of those with many
+  std::vector<AttJoin> joins;
   std::vector<AttSrc> srcs;
   int32_t join_rows = 0;
-  size_t n_few_joins = 0;
   Upload u;
   SP.place(u);
   SO.place(u);
   const size_t o_map = u.add(tok_map.data(), tok_map.size() * sizeof(int32_t));
-  size_t end = 0, o_joins = 0, o_srcs = 0;
-  {
-    // the partials lie behind everything that is uploaded: sizes first
-    const size_t n_src = SP.pf.srcs.size() + SP.pl.srcs.size() + SO.pf.srcs.size() + SO.pl.srcs.size();
-    size_t n_joins = 0;
-    for (const AttUnit& w : own) n_joins += w.joined ? 1 : 0;
-    joins.resize(n_joins);
-    srcs.reserve(n_src);
-    o_joins = u.add(joins.data(), n_joins * sizeof(AttJoin));
-    o_srcs = u.add(srcs.data(), n_src * sizeof(AttSrc));
-    end = SO.place_parts(SP.place_parts((u.size + 255) & ~size_t(255)));
-    const auto ps0 = SP.add_srcs(0, srcs), os = SO.add_srcs(0, srcs);
-    const auto ps = together ? os : ps0;
-    const AttSet& PS = together ? SO : SP;   // where the prefixes' units are
-    auto log2i = [](int x) { int n = 0; while ((1 << n) < x) ++n; return n; };
-    size_t at_few = 0, at_wide = 0;
-    for (size_t x = 0; x < own.size(); ++x) at_wide += own[x].joined && !SO.where[o0 + x].wide ? 1 : 0;
-    n_few_joins = at_wide;
-    size_t x = 0;
-    for (int32_t b = 0; b < n_req; ++b)
-      for (int h = 0; h < hkv && n_new[b] > 0; ++h, ++x) {
-        if (!own[x].joined) continue;
-        const AttSet::Where o = SO.where[o0 + x], p = PS.where[(size_t)group_of[(size_t)b] * hkv + h];
-        AttJoin J;
-        J.unit = o.index;
-        J.rows = n_new[b] * g;
+  // the partials lie behind everything that is uploaded: sizes first
+  const size_t n_src = SP.pf.srcs.size() + SP.pl.srcs.size() + SO.pf.srcs.size() + SO.pl.srcs.size();
+  size_t n_joins = 0;
+  for (const AttUnit& w : own) n_joins += scan || w.joined ? 1 : 0;
+  joins.reserve(n_joins);
+  srcs.reserve(n_src);
+  const size_t o_joins = u.add(joins.data(), n_joins * sizeof(AttJoin));
+  const size_t o_srcs = u.add(srcs.data(), n_src * sizeof(AttSrc));
+  const size_t end = SO.place_parts(SP.place_parts((u.size + 255) & ~size_t(255)));
+  const auto ps0 = SP.add_srcs(0, srcs), os = SO.add_srcs(0, srcs);
+  const auto ps = together ? os : ps0;
+  const AttSet& PS = together ? SO : SP;   // where the prefixes' units are
+  auto log2i = [](int x) { int n = 0; while ((1 << n) < x) ++n; return n; };
+  size_t x = 0;
+  for (int32_t b = 0; b < n_req; ++b)
+    for (int h = 0; h < hkv && n_new[b] > 0; ++h, ++x) {
+      if (!scan && !own[x].joined) continue;
+      AttJoin J{};
+      J.tok0 = own[x].tok0;
+      J.kvh = h;
+      J.rows = n_new[b] * g;
+      J.req = own[x].req;
+      J.n_pages = own[x].n_pages;
+      if (scan) {
+        J.own0 = (int32_t)x;   // the decode plan's units are in this order
+        J.flags = kJoinScan;
+      } else {
+        const AttSet::Where o = SO.where[o0 + x];
         J.own0 = o.wide ? os.second + SO.pl.src0[(size_t)o.index] : os.first + SO.pf.src0[(size_t)o.index];
         J.own_shift = o.wide ? 7 : log2i(SO.R);
+        J.flags = o.wide ? kJoinOwnTall : 0;
+      }
+      J.pre0 = -1;
+      if (own[x].joined) {
+        const AttSet::Where p = PS.where[(size_t)group_of[(size_t)b] * hkv + h];
         J.pre0 = p.wide ? ps.second + PS.pl.src0[(size_t)p.index] : ps.first + PS.pf.src0[(size_t)p.index];
         J.pre_shift = p.wide ? 7 : log2i(PS.R);
         J.pre_row = (int32_t)pre_tok[(size_t)b] * g;
-        J.tall = o.wide | (p.wide << 1);
-        joins[o.wide ? at_wide++ : at_few++] = J;
-        join_rows = std::max(join_rows, J.rows);
+        J.flags |= p.wide ? kJoinPreTall : 0;
       }
-  }
+      joins.push_back(J);
+      join_rows = std::max(join_rows, J.rows);
+    }
   const int64_t tiles = std::max(SP.most, SO.most);
   if ((st = attend_room(P, end, tiles)) != KV_OK) return st;
+  if (scan) {
+    if ((st = build_plan(P, req_ids, n_req, hq, KV_DECODE_MMA, s)) != KV_OK) return st;
+    if ((st = ensure(P->partials, (size_t)std::max(P->n_splits, 1) * g * kAttPart * sizeof(float))) != KV_OK) return st;
+    if ((st = ensure(P->frags, (size_t)std::max(P->n_units, 1) * decode_mma_frag_bytes())) != KV_OK) return st;
+  }
   if ((st = h2d(P, P->attend.ptr, u, s)) != KV_OK) return st;
   uint8_t* base = (uint8_t*)P->attend.ptr;
   A.tok_map = (const int32_t*)(base + o_map);
   // the second launch starts as CTAs of the first leave, the joins as those of the second do
-  const bool chained = SP.one_launch() && SO.one_launch();
+  const bool chained = SP.one_launch() && (scan || SO.one_launch());
   if ((st = SP.launch(P, A, tiles, s, chained ? kChainNext : 0)) != KV_OK) return st;
-  if ((st = SO.launch(P, A, tiles, s, SO.one_launch() ? kChainNext | (chained ? kChainPrev : 0) : 0)) != KV_OK) return st;
-  const AttJoin* dj = (const AttJoin*)(base + o_joins);
-  const AttSrc* ds = (const AttSrc*)(base + o_srcs);
-  KV_CUDA(launch_attend_join(P, A, (const AttUnit*)(base + SO.xf.units), dj, (int)n_few_joins, join_rows, ds,
-                             (const float*)base, s));
-  KV_CUDA(launch_attend_join(P, A, (const AttUnit*)(base + SO.xl.units), dj + n_few_joins, (int)(joins.size() - n_few_joins),
-                             join_rows, ds, (const float*)base, s));
+  const uint8_t* plan = (const uint8_t*)P->plan.ptr;
+  const Unit* scan_units = scan ? (const Unit*)(plan + P->plan_units_off) : nullptr;
+  if (scan)
+    KV_CUDA(launch_scan_mma(P, q, hq, A.scale_log2, scan_units, P->n_units, (const Split*)(plan + P->plan_splits_off),
+                            (const int32_t*)(plan + P->plan_cta_off), P->n_ctas, P->frags.ptr, (float*)P->partials.ptr, s));
+  else if ((st = SO.launch(P, A, tiles, s, SO.one_launch() ? kChainNext | (chained ? kChainPrev : 0) : 0)) != KV_OK)
+    return st;
+  KV_CUDA(launch_attend_join(P, A, (const AttJoin*)(base + o_joins), (int)joins.size(), join_rows,
+                             (const AttSrc*)(base + o_srcs), (const float*)base, scan_units, (const float*)P->partials.ptr, s));
   return KV_OK;
 } catch (const std::bad_alloc&) {
   return fail(KV_ERR_OOM, "kv_attend_shared: host allocation failed");

@@ -38,6 +38,7 @@ struct AttMerge {
   int32_t part0, n_parts, stride;
 };
 constexpr int kAttPart = kHeadDim + 4;   // floats per row of a partial: O, then m and l
+constexpr float kAttHead = 7.0f;         // weights (and O and l of the partials) are 2^(x - m + kAttHead): headroom of binary16
 
 // The partials of a block of rows of a joined unit.
 struct AttSrc {
@@ -45,14 +46,20 @@ struct AttSrc {
   int32_t n_parts;
   int32_t step;      // floats from a part to the next
 };
-// One unit's rows joined with those of the prefix unit that they are also in (no prefix: pre0 < 0).
+// The rows of a request (and kv head) with a prefix, or of a decode step: the parts of its own unit and those
+// of the prefix unit that the rows are also in.
+enum : int {
+  kJoinOwnTall = 1, kJoinPreTall = 2,   // parts laid out as 128 rows by channel
+  kJoinScan = 4                         // own parts are the decode scan's: own0 is a unit of its plan
+};
 struct AttJoin {
-  int32_t unit;              // the request's own unit (in the array the join kernel gets)
-  int32_t rows;
-  int32_t own0, own_shift;   // its first block in the AttSrc array, log2 of a block's rows
-  int32_t pre0, pre_shift;   // the prefix unit's
+  int64_t tok0;              // the request's first row in q and out
+  int32_t kvh, rows;
+  int32_t own0, own_shift;   // the own unit's first block in the AttSrc array, log2 of a block's rows
+  int32_t pre0, pre_shift;   // the prefix unit's (no prefix: pre0 < 0)
   int32_t pre_row;           // row 0 of the request among the prefix unit's rows
-  int32_t tall;              // bit 0: own parts are laid out as 128 rows by channel, bit 1: the prefix's
+  int32_t flags;
+  int32_t req, n_pages;      // the request's own cache
 };
 
 // Everything a kernel needs besides its plan.

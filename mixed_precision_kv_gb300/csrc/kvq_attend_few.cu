@@ -47,7 +47,7 @@ constexpr int kMma = 8 + 2 * kSide<R>;          // first MMA warp
 template <int R>
 constexpr int kThreads = 32 * (kMma<R> + 3);
 constexpr int kMaskRing = 16;                   // tiles whose live words are kept
-constexpr float kHead = 7.0f;                   // P = 2^(x - m + 7)
+constexpr float kHead = kAttHead;               // P = 2^(x - m + 7)
 constexpr float kGrow = 8.0f;                   // a maximum may be stale by this much (base 2)
 constexpr float kNever = -3.0e38f;              // S of a key that is not seen
 constexpr float kLowest = 0.9f * kNever;        // logits below it count as it

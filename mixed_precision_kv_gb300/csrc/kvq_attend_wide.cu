@@ -47,7 +47,7 @@ constexpr int kRing = 5;                        // K and V tiles in flight
 constexpr int kWarps = 12;                      // the last one idle
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTileBytes = 128 * 128 * 2;
-constexpr float kHead = 7.0f;                   // P = 2^(x - m + 7)
+constexpr float kHead = kAttHead;               // P = 2^(x - m + 7)
 constexpr float kGrow = 8.0f;                   // a maximum may be stale by this much (base 2)
 constexpr float kNever = -3.0e38f;              // S of a key that is not seen
 constexpr float kLowest = 0.9f * kNever;        // logits below it count as it

@@ -62,17 +62,13 @@ int mma_occupancy() {
 
 size_t decode_mma_frag_bytes() { return sizeof(UnitFrag); }
 
-cudaError_t launch_decode_mma(kv_pool* P, const void* q, int32_t hq, float scale_log2, const Unit* d_units, int n_units,
-                              const Split* d_splits, const int32_t* d_wsplit, int n_workers, void* d_frags,
-                              float* d_part, float* out, cudaStream_t s, const GroupPool* d_gpools,
-                              int32_t total_kv_heads, bool groups_extra) {
-  cudaError_t e;
-  const int g = hq / (total_kv_heads > 0 ? total_kv_heads : P->cfg.num_kv_heads);
-#define KVQ_MMA_CASE(gg)                                                                                          \
-  case gg:                                                                                                        \
-    e = launch_mma_g<gg>(P, q, hq, scale_log2, d_units, n_units, d_splits, d_wsplit, n_workers, d_frags, d_part, s, \
-                         d_gpools, groups_extra);                                                                 \
-    break;
+static cudaError_t launch_scan(kv_pool* P, int g, const void* q, int32_t hq, float scale_log2, const Unit* d_units, int n_units,
+                               const Split* d_splits, const int32_t* d_wsplit, int n_workers, void* d_frags, float* d_part,
+                               cudaStream_t s, const GroupPool* d_gpools, bool groups_extra) {
+#define KVQ_MMA_CASE(gg)                                                                                              \
+  case gg:                                                                                                            \
+    return launch_mma_g<gg>(P, q, hq, scale_log2, d_units, n_units, d_splits, d_wsplit, n_workers, d_frags, d_part, s, \
+                            d_gpools, groups_extra);
   switch (g) {
     KVQ_MMA_CASE(1)
     KVQ_MMA_CASE(2)
@@ -85,6 +81,22 @@ cudaError_t launch_decode_mma(kv_pool* P, const void* q, int32_t hq, float scale
     default: return cudaErrorInvalidValue;
   }
 #undef KVQ_MMA_CASE
+}
+
+cudaError_t launch_scan_mma(kv_pool* P, const void* q, int32_t hq, float scale_log2, const Unit* d_units, int n_units,
+                            const Split* d_splits, const int32_t* d_wsplit, int n_workers, void* d_frags, float* d_part,
+                            cudaStream_t s) {
+  return launch_scan(P, hq / P->cfg.num_kv_heads, q, hq, scale_log2, d_units, n_units, d_splits, d_wsplit, n_workers, d_frags,
+                     d_part, s, nullptr, false);
+}
+
+cudaError_t launch_decode_mma(kv_pool* P, const void* q, int32_t hq, float scale_log2, const Unit* d_units, int n_units,
+                              const Split* d_splits, const int32_t* d_wsplit, int n_workers, void* d_frags,
+                              float* d_part, float* out, cudaStream_t s, const GroupPool* d_gpools,
+                              int32_t total_kv_heads, bool groups_extra) {
+  const int g = hq / (total_kv_heads > 0 ? total_kv_heads : P->cfg.num_kv_heads);
+  cudaError_t e = launch_scan(P, g, q, hq, scale_log2, d_units, n_units, d_splits, d_wsplit, n_workers, d_frags, d_part, s,
+                              d_gpools, groups_extra);
   if (e != cudaSuccess) return e;
   if ((e = launch_fp_pending(P, q, hq, scale_log2, d_units, d_part, s)) != cudaSuccess) return e;
   if (P->merge_event && (e = cudaEventRecord(P->merge_event, s)) != cudaSuccess) return e;

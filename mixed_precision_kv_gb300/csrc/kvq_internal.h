@@ -472,6 +472,10 @@ cudaError_t launch_decode_mma(kv_pool* P, const void* q, int32_t hq, float scale
                               float* d_part, float* out, cudaStream_t s, const GroupPool* d_gpools = nullptr,
                               int32_t total_kv_heads = 0, bool groups_extra = false);
 int decode_mma_workers_per_sm(int g);
+// The scan alone: partials [split][g][kHeadDim + 4], O, then the maximum (base 2) and the sum.
+cudaError_t launch_scan_mma(kv_pool* P, const void* q, int32_t hq, float scale_log2, const Unit* d_units, int n_units,
+                            const Split* d_splits, const int32_t* d_wsplit, int n_workers, void* d_frags, float* d_part,
+                            cudaStream_t s);
 constexpr int kMmaWarpsPerCta = 16;
 size_t decode_mma_frag_bytes();
 // The same scan, keeping every page's logits (base 2): logits[row][head][slot], row = Split::pad[0] + table

@@ -80,6 +80,74 @@ def test_shared(kvq, hkv, hq, pre, own, n_new, prefix, with_kv):
     P.pool.destroy()
 
 
+@pytest.mark.parametrize("g", [1, 4, 7])
+def test_decode_step(kvq, g):
+    """A token per request and no new keys, enough tiles for the decode's scan: ragged own caches (one empty), a request
+    without a prefix, evicted slots and slots excluded for a head, a second prefix with one request."""
+    rng = np.random.default_rng(g)
+    lens = [260, 33] + [0] + [int(x) for x in rng.integers(300, 600, 21)]
+    dead = [list(rng.choice(n, n // 8, replace=False)) if n else [] for n in lens]
+    P = Pool(kvq, 8, [mixed(n, i) for i, n in enumerate(lens)], seed=g, dead=dead, slack=200)
+    P.pool.evict_head([P.ids[5]] * 2 + [P.ids[0]], [7, 200, 3], [0, 7, 2])
+    head_dead = {5: {(0, 7), (7, 200)}, 0: {(2, 3)}}
+    which = list(range(2, 24))
+    prefix = [0] * 22
+    prefix[4], prefix[9] = -1, 1
+    for _ in range(2):   # the second call finds the plan in place
+        check(P, which, prefix, [1] * 22, 8 * g, with_kv=False, head_dead=head_dead)
+    assert sum((n + 127) // 128 * 8 for n in lens[2:]) > 4 * torch.cuda.get_device_properties(0).multi_processor_count
+    P.pool.destroy()
+
+
+def test_decode_step_far_below(kvq):
+    """Rows of a decode step whose logits lie below the logit that the scan gives a dead slot, that are not finite, or
+    whose own cache holds nothing live: as in the other kernels.  With an empty prefix, so that the weights go by the own
+    caches, whose values are taken in fp32."""
+    hkv, n = 8, 24
+    P = Pool(kvq, hkv, [mixed(0, 0)] + [mixed(410, i) for i in range(n)], seed=3, slack=200,
+             dead=[[]] + [list(range(410)) if i == 4 else [1, 40] for i in range(n)])
+    pool = P.pool
+    q = rand((n, hkv, 128), P.gen)
+    q[1, 0] *= 3000.0            # logits of either sign beyond 1e4
+    q[2] = -q[2].abs() * 4000.0
+    q[3, 1, 9] = float("nan")
+    q[5, 2, 8] = float("inf")
+    ids, pre = P.ids[1:], [P.ids[0]] * (n // 2) + [-1] * (n // 2)
+    out = pool.attend_shared(q, ids, pre, [1] * n, SCALE)
+    with pytest.raises(kvq.KVError) as e:
+        pool.sync()
+    assert e.value.status == kvq.KV_ERR_RANGE
+    got = out.double().cpu().numpy()
+    for b in (0, 1, 2, 4, n - 1):
+        C = P.content(b + 1)
+        for h in range(hkv):
+            o, tol = attend_row(q[b, h].double().cpu().numpy(), C.K[h], C.V[h], SCALE, 2.0 ** -17)
+            assert np.all(np.abs(got[b, h] - o) <= tol), (b, h)
+    assert np.all(got[4] == 0)
+    assert not np.isfinite(got[3, 1]).all() and np.isfinite(got[3, 0]).all() and np.isfinite(got[3, 2]).all()
+    assert not np.isfinite(got[5, 2]).all() and np.isfinite(got[5, 3]).all()
+    # keys that all point one way: every logit far below -1e4, the softmax among them unchanged by a common offset
+    pool2 = kvq.KVPool(hkv, 8, 400, n, 20)
+    ids = [pool2.open() for _ in range(n)]
+    x = rand((n * 410, hkv, 128), P.gen)
+    x[..., 32:64] = 0
+    x[..., 40] = 16.0            # exact in the page: its group holds 0 and 16 alone
+    v = rand((n * 410, hkv, 128), P.gen)
+    pool2.append(x, v, np.repeat(ids, 410), np.full(n * 410, 4, np.uint8))
+    q = rand((n, hkv, 128), P.gen)
+    near = pool2.attend_shared(q * (torch.arange(128, device="cuda") != 40), ids, [-1] * n, [1] * n, SCALE)
+    q[..., 40] = -16384.0        # logit -16 * 16384 / sqrt(128) = -23170, plus those of the other channels
+    far = pool2.attend_shared(q, ids, [-1] * n, [1] * n, SCALE)
+    pool2.sync()
+    # the other channels' sum, of up to some tens, is rounded to fp32 beside 262144: 2^-6 at most each way before the
+    # scale, so a logit moves by 2^-6 / 11.3 * 128 at the very most in a sum of 128 terms; bf16 rounds both results
+    lim = 2 * (np.exp(2 * 128 * 2.0 ** -6 / 11.3) - 1) * float(v.float().abs().max())
+    assert (near.float() - far.float()).abs().max() <= lim
+    assert bool((far.float().abs().amax(-1) > 0).all())
+    pool2.destroy()
+    pool.destroy()
+
+
 @pytest.mark.parametrize("rows_each,batch", [(25, 6), (70, 8), (40, 2)])
 def test_shared_many_rows(kvq, rows_each, batch):
     """The prefix's rows go to the kernel for many rows (600 and 2,240 of them), the requests' own to either."""
