@@ -49,9 +49,10 @@ struct AppendJob {
 
 // The jobs of a small append call, passed to the kernel by value (no copy).
 struct SmallAppend {
-  static constexpr int kMaxJobs = 32, kMaxToks = 128;
+  static constexpr int kMaxJobs = 64, kMaxToks = 128;
   AppendJob jobs[kMaxJobs];
   int32_t toks[kMaxToks];
+  int32_t pos[kMaxToks];   // the tokens' positions
 };
 
 struct RepackJob {
@@ -65,8 +66,9 @@ struct RepackJob {
 struct DirectJob {
   int32_t dst;      // INT2 page id
   int32_t tok_off;  // offset of its 32 token indices (slot order)
-  int32_t pos0;     // as AppendJob::pos0
+  int32_t pos0;     // as AppendJob::pos0; kNoPos: positions come from the host later
 };
+constexpr int32_t kNoPos = INT32_MIN;
 
 // Work unit of the decode: one (batch row, kv head).  Its splits (page ranges,
 // one partial each) are contiguous in the split list, and so are the splits
@@ -381,6 +383,7 @@ struct kv_pool {
   cudaEvent_t merge_event = nullptr;  // recorded by the launchers between scan and merge when timing
   const kvq::RopeArgs* rope = nullptr;   // the running append rotates K by this (its launchers read it)
   int32_t* job_pos = nullptr;            // d_pos, if the running append's kernels write their slots' positions
+  const int32_t* tok_pos = nullptr;      // ... the positions of its token list (device), else AppendJob::pos0 + token
   int64_t first_wait_spins = -1;      // kv_set_wait_limit: bound of the scans' first copy wait (-1: normal)
 };
 

@@ -1037,7 +1037,7 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
       R.shape = ++P->shape_clock;
       R.table.push_back(nid);
       if (c.stag_direct) {
-        directs.push_back(DirectJob{nid, (int32_t)dtoks.size(), 0});
+        directs.push_back(DirectJob{nid, (int32_t)dtoks.size(), kNoPos});
         dtoks.insert(dtoks.end(), c.grp, c.grp + kPage);
         c.ngrp = 0;
       } else {
@@ -1060,21 +1060,23 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
   }
   }   // per-token path
   const int64_t off = bulk ? bulk_job_toks : (int64_t)toks.size();
-  // Positions on the device: the kernels of a call of runs write those of the slots they fill (a
-  // token's position is its index in the call plus a constant); other pages are refreshed from the
-  // host by the next call that reads positions.
-  const bool few_jobs = bulk && jobs.size() <= (size_t)SmallAppend::kMaxJobs && off <= SmallAppend::kMaxToks;
+  // Positions on the device: the INT4 and INT2 kernels write those of the slots they fill (in a call of
+  // runs a token's position is its index in the call plus a constant, else it comes with the token
+  // list); other pages are refreshed from the host by the next call that reads positions.
   struct JobPos {
     kv_pool* P;
-    ~JobPos() { P->job_pos = nullptr; }
+    ~JobPos() {
+      P->job_pos = nullptr;
+      P->tok_pos = nullptr;
+    }
   } job_pos{P};
-  if (P->d_pos && bulk && !few_jobs) {
+  if (P->d_pos) {
     P->job_pos = P->d_pos;
+    for (const auto& j : jobs)
+      if (is_int3(P, j.page) || is_fp4(P, j.page)) P->pos_dirty.push_back(j.page);
     for (const auto& j : repacks) P->pos_dirty.push_back(j.dst);
-  } else if (P->d_pos) {   // the pages whose slots got other positions
-    for (const auto& j : jobs) P->pos_dirty.push_back(j.page);
-    for (const auto& j : repacks) P->pos_dirty.push_back(j.dst);
-    for (const auto& j : directs) P->pos_dirty.push_back(j.dst);
+    if (!bulk)
+      for (const auto& j : directs) P->pos_dirty.push_back(j.dst);
     if (P->pos_dirty.size() > 2 * P->fill.size() + 4096) {   // no reader for long: each page once
       std::sort(P->pos_dirty.begin(), P->pos_dirty.end());
       P->pos_dirty.erase(std::unique(P->pos_dirty.begin(), P->pos_dirty.end()), P->pos_dirty.end());
@@ -1173,6 +1175,14 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
       toks.insert(toks.end(), src, src + j.n_slots);
     }
   }
+  std::vector<int32_t> tpos;   // positions of the token list (calls that are not of runs, and small ones)
+  if (P->job_pos && (small || !bulk)) {
+    tpos.resize(toks.size());
+    for (const auto& j : jobs) {
+      const int32_t* src = &P->pos[(size_t)j.page * kPage + j.first_slot];
+      std::copy(src, src + j.n_slots, tpos.begin() + j.tok_off);
+    }
+  }
   Upload u;
   const size_t o_jobs = small ? 0 : u.add(jobs.data(), jobs.size() * sizeof(AppendJob));
   size_t o_toks = 0, o_dtok = 0;
@@ -1190,6 +1200,7 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
     o_toks = small ? 0 : u.add(toks.data(), toks.size() * sizeof(int32_t));
     o_dtok = u.add(dtoks.data(), dtoks.size() * sizeof(int32_t));
   }
+  const size_t o_tpos = small ? 0 : u.add(tpos.data(), tpos.size() * sizeof(int32_t));
   const size_t o_rep = u.add(repacks.data(), repacks.size() * sizeof(RepackJob));
   const size_t o_dir = u.add(directs.data(), directs.size() * sizeof(DirectJob));
   const size_t o_upd = u.add(upd.data(), upd.size() * sizeof(TableUpd));
@@ -1199,8 +1210,10 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
     SmallAppend sa;
     std::copy(jobs.begin(), jobs.end(), sa.jobs);
     std::copy(toks.begin(), toks.end(), sa.toks);
+    std::copy(tpos.begin(), tpos.end(), sa.pos);
     KV_CUDA(launch_append(P, k, v, nullptr, (int)jobs.size(), nullptr, &sa, s));
   } else {
+    if (!tpos.empty()) P->tok_pos = (const int32_t*)(base + o_tpos);
     const int n_part = (int)(jobs.size() - n_i3 - n_f4 - n_full);
     KV_CUDA(launch_append(P, k, v, (const AppendJob*)(base + o_jobs), n_part, (const int32_t*)(base + o_toks),
                           nullptr, s));

@@ -225,13 +225,14 @@ __device__ __forceinline__ void pack_i4v(uint8_t* __restrict__ img, const uint8_
   }
 }
 
-// Positions of a page's slots first .. first + n - 1 (a new page's others: -1, no token), by one CTA.
-__device__ __forceinline__ void write_positions(int32_t* __restrict__ pos, int32_t page, const int32_t* __restrict__ tk,
-                                                int32_t pos0, int first, int n) {
+// Positions of a page's slots first .. first + n - 1 (a new page's others: -1, no token), by one CTA: tp, or
+// the tokens' indices and a constant.
+__device__ __forceinline__ void write_positions(int32_t* __restrict__ pos, int32_t page, const int32_t* tp,
+                                                const int32_t* __restrict__ tk, int32_t pos0, int first, int n) {
   const int t = threadIdx.x;
   if (t >= kPage || t < first) return;
   if (t < first + n)
-    pos[(size_t)page * kPage + t] = pos0 + tk[t - first];
+    pos[(size_t)page * kPage + t] = tp ? tp[t - first] : pos0 + tk[t - first];
   else if (first == 0)
     pos[(size_t)page * kPage + t] = -1;
 }
@@ -248,7 +249,8 @@ __global__ void __launch_bounds__(kThreads) append_int4_kernel(
     uint8_t* __restrict__ pool, size_t int4_off, int64_t n2, int hkv, const __nv_bfloat16* __restrict__ k,
     const __nv_bfloat16* __restrict__ v, const AppendJob* __restrict__ jobs, const int32_t* __restrict__ toks,
     Entry* __restrict__ table, int32_t* __restrict__ ntab, uint32_t* __restrict__ status,
-    const __grid_constant__ SmallAppend small, int32_t* __restrict__ pos, const __grid_constant__ RopeParam<kRope> rope) {
+    const __grid_constant__ SmallAppend small, int32_t* __restrict__ pos, const int32_t* __restrict__ tok_pos,
+    const __grid_constant__ RopeParam<kRope> rope) {
   __shared__ __align__(16) uint8_t img[kInt4Block];
   __shared__ __align__(16) uint8_t vcodes[kPage * kHeadDim];   // V codes of a new page, packed after
   asm volatile("griddepcontrol.wait;" ::: "memory");   // earlier work on the stream (the previous decode) is done
@@ -277,7 +279,10 @@ __global__ void __launch_bounds__(kThreads) append_int4_kernel(
     bad |= quantize_tokens<kThreads / 32, kRope>(rope, blk, k, v, tk + job.tok_off, job.n_slots, job.first_slot, h, hkv,
                                                  vmax, nullptr);
   }
-  if (!kByValue && pos && h == 0) write_positions(pos, job.page, tk + job.tok_off, job.pos0, job.first_slot, job.n_slots);
+  if (pos && h == 0) {
+    const int32_t* tp = kByValue ? small.pos : tok_pos;
+    write_positions(pos, job.page, tp ? tp + job.tok_off : nullptr, tk + job.tok_off, job.pos0, job.first_slot, job.n_slots);
+  }
   flush_vmax(vmax, status);
   if (bad) atomicOr(status, kStatusRange);
   if (h == 0 && threadIdx.x == 0) {
@@ -686,7 +691,7 @@ __global__ void __launch_bounds__(kThreads) direct_int2_kernel(
   const int h = blockIdx.y;
   bool bad = false;
   float vmax = 0.0f;
-  if (pos && h == 0) write_positions(pos, job.dst, toks + job.tok_off, job.pos0, 0, kPage);
+  if (pos && h == 0 && job.pos0 != kNoPos) write_positions(pos, job.dst, nullptr, toks + job.tok_off, job.pos0, 0, kPage);
   // every slot is written: no zeroing
   bad |= quantize_tokens<kThreads / 32, kRope>(rope, img, k, v, toks + job.tok_off, kPage, 0, h, hkv, vmax, codes);
   flush_vmax(vmax, status);
@@ -957,7 +962,7 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int4_kernel(
     uint8_t* __restrict__ pool, size_t int4_off, int64_t n2, int hkv, const __nv_bfloat16* __restrict__ k,
     const __nv_bfloat16* __restrict__ v, const AppendJob* __restrict__ jobs, const int32_t* __restrict__ toks,
     Entry* __restrict__ table, int32_t* __restrict__ ntab, uint32_t* __restrict__ status,
-    int32_t* __restrict__ pos, const __grid_constant__ RopeParam<kRope> rope) {
+    int32_t* __restrict__ pos, const int32_t* __restrict__ tok_pos, const __grid_constant__ RopeParam<kRope> rope) {
   __shared__ __align__(16) uint8_t img[kInt4Block];
   __shared__ __align__(16) uint32_t wbuf[4][128];
   __shared__ RopeTile kt, vt;
@@ -996,7 +1001,7 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int4_kernel(
   }
   flush_vmax(vmax, status);
   if (__any_sync(0xFFFFFFFFu, bad) && t == 0) atomicOr(status, kStatusRange);
-  if (pos && h == 0 && gr == 0) pos[(size_t)job.page * kPage + t] = job.pos0 + T;
+  if (pos && h == 0 && gr == 0) pos[(size_t)job.page * kPage + t] = tok_pos ? tok_pos[job.tok_off + t] : job.pos0 + T;
   __syncthreads();
   uint4* out4 = reinterpret_cast<uint4*>(pool + int4_off + ((size_t)(job.page - n2) * hkv + h) * kInt4Block);
   const uint4* img4 = reinterpret_cast<const uint4*>(img);
@@ -1164,7 +1169,7 @@ __global__ void __launch_bounds__(kBulkThreads, 8) bulk_int2_kernel(
     }
   }
   if (__any_sync(0xFFFFFFFFu, bad) && t == 0) atomicOr(status, kStatusRange);
-  if (pos && h == 0 && gr == 0) pos[(size_t)job.dst * kPage + t] = job.pos0 + T;
+  if (pos && h == 0 && gr == 0 && job.pos0 != kNoPos) pos[(size_t)job.dst * kPage + t] = job.pos0 + T;
   __syncthreads();
   uint4* out4 = reinterpret_cast<uint4*>(pool + ((size_t)job.dst * hkv + h) * kInt2Block);
   const uint4* img4 = reinterpret_cast<const uint4*>(img);
@@ -1202,11 +1207,11 @@ cudaError_t launch_append(kv_pool* P, const void* k, const void* v, const Append
     if (small)
       return launch_pdl(append_int4_kernel<true, kRope>, grid, dim3(kThreads), 0, s, P->d_pool, P->int4_offset,
                         P->cfg.n_int2_pages, P->cfg.num_kv_heads, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v,
-                        no_jobs, no_toks, P->d_table, P->d_ntab, P->d_status, *small, P->job_pos, rope);
+                        no_jobs, no_toks, P->d_table, P->d_ntab, P->d_status, *small, P->job_pos, P->tok_pos, rope);
     static const SmallAppend none{};
     return launch_pdl(append_int4_kernel<false, kRope>, grid, dim3(kThreads), 0, s, P->d_pool, P->int4_offset,
                       P->cfg.n_int2_pages, P->cfg.num_kv_heads, (const __nv_bfloat16*)k, (const __nv_bfloat16*)v,
-                      d_jobs, d_toks, P->d_table, P->d_ntab, P->d_status, none, P->job_pos, rope);
+                      d_jobs, d_toks, P->d_table, P->d_ntab, P->d_status, none, P->job_pos, P->tok_pos, rope);
   });
 }
 
@@ -1243,7 +1248,7 @@ cudaError_t launch_bulk_int4(kv_pool* P, const void* k, const void* v, const App
     return launch_pdl(bulk_int4_kernel<decltype(is)::value>, dim3((unsigned)n_jobs, (unsigned)P->cfg.num_kv_heads),
                       dim3(kBulkThreads), 0, s, P->d_pool, P->int4_offset, P->cfg.n_int2_pages, P->cfg.num_kv_heads,
                       (const __nv_bfloat16*)k, (const __nv_bfloat16*)v, d_jobs, d_toks, P->d_table, P->d_ntab,
-                      P->d_status, P->job_pos, rope);
+                      P->d_status, P->job_pos, P->tok_pos, rope);
   });
 }
 
