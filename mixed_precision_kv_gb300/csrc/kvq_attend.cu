@@ -165,49 +165,69 @@ cudaError_t launch_attend_merge(kv_pool* P, const AttArgs& A, const AttUnit* d_u
 }
 
 // Rows with a shared prefix: the parts of the request's own unit and those of the
-// prefix unit, each in the layout of the kernel that made it, as in
-// attend_merge_kernel: a warp per row.  Bound by the partials' bytes, which are
-// still in L2 (parts by channel: 16 of every 32 bytes read are used).
+// prefix unit, each in the layout of the kernel that made it.  A warp takes two
+// rows, a lane 4 channels of each half of one: parts by channel hold neighbouring
+// rows side by side, so whole sectors are read.  Bound by the partials' bytes,
+// which are still in L2.
 struct PartRow {
-  const float *o, *ml;   // this lane's four channels of part 0, its m and l
+  const float *o, *ml;   // this lane's first channels of part 0, the row's m and l
   size_t step;
+  int half;              // from channel 0 to channel 64
   int n;
   float head;            // what its maxima lack of the attention kernels' (kAttHead or 0)
 };
-__device__ __forceinline__ PartRow part_row(const AttSrc& S, const float* part, int r, int lane, bool tall) {
+__device__ __forceinline__ PartRow part_row(const AttSrc& S, const float* part, int r, int c, bool tall) {
   const float* p = part + S.off;
-  return tall ? PartRow{p + (size_t)lane * (4 * kTallRows) + 4 * r, p + kTallRows * kHeadDim + 2 * r, (size_t)S.step, S.n_parts, 0.0f}
-              : PartRow{p + (size_t)r * kAttPart + 4 * lane, p + (size_t)r * kAttPart + kHeadDim, (size_t)S.step, S.n_parts, 0.0f};
+  return tall ? PartRow{p + (size_t)c * (4 * kTallRows) + 4 * r, p + kTallRows * kHeadDim + 2 * r, (size_t)S.step,
+                        64 * kTallRows, S.n_parts, 0.0f}
+              : PartRow{p + (size_t)r * kAttPart + 4 * c, p + (size_t)r * kAttPart + kHeadDim, (size_t)S.step, 64, S.n_parts, 0.0f};
 }
-// The largest maximum of a row's parts.
-__device__ __forceinline__ float part_max(const PartRow& R, int lane) {
-  float M = -INFINITY;
-  for (int p = lane; p < R.n; p += 32) M = fmaxf(M, R.ml[(size_t)p * R.step]);
+// Reductions over the 16 lanes of a row.
+__device__ __forceinline__ float row_max(float x) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-  return M + R.head;
+  for (int o = 16; o > 1; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+  return x;
 }
-// Adds a row's parts, relative to the maximum M: L per lane (to be summed), o.
-__device__ __forceinline__ void part_add(const PartRow& R, int lane, float M, float& L, float4& o) {
-  for (int p0 = 0; p0 < R.n; p0 += 32) {
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 1; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+  return x;
+}
+__device__ __forceinline__ float part_max(const PartRow& R, int c) {
+  float M = -INFINITY;
+  for (int p = c; p < R.n; p += 16) M = fmaxf(M, R.ml[(size_t)p * R.step]);
+  return row_max(M) + R.head;
+}
+// Adds a row's parts, relative to the maximum M: L per lane (to be summed), o: 4 channels of each half.
+__device__ __forceinline__ void part_add(const PartRow& R, int lane, float M, float& L, float4 (&o)[2]) {
+  const int c = lane >> 1, rr = lane & 1;
+  const int most = max(R.n, __shfl_xor_sync(0xFFFFFFFFu, R.n, 1));
+  for (int p0 = 0; p0 < most; p0 += 16) {
     float f = 0.0f;
-    if (p0 + lane < R.n) {
-      const float2 ml = *reinterpret_cast<const float2*>(R.ml + (size_t)(p0 + lane) * R.step);
+    if (p0 + c < R.n) {
+      const float2 ml = *reinterpret_cast<const float2*>(R.ml + (size_t)(p0 + c) * R.step);
       // a part that saw nothing (m = -inf, l = 0) adds nothing; one with a NaN sum keeps it
       f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2f(ml.x + R.head - M);
       L = fmaf(ml.y, f, L);
     }
-    const int n = min(32, R.n - p0);
-    for (int p = 0; p < n; p += 8) {
-      float4 a[8];
+    for (int p = 0; p < min(16, most - p0); p += 4) {
+      float4 a[4][2];
 #pragma unroll
-      for (int y = 0; y < 8; ++y) a[y] = *reinterpret_cast<const float4*>(R.o + (size_t)(p0 + min(p + y, n - 1)) * R.step);
+      for (int y = 0; y < 4; ++y) {
+        const float* q = R.o + (size_t)(p0 + p + y) * R.step;
+        const bool is = p0 + p + y < R.n;
+        a[y][0] = is ? *reinterpret_cast<const float4*>(q) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        a[y][1] = is ? *reinterpret_cast<const float4*>(q + R.half) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
 #pragma unroll
-      for (int y = 0; y < 8; ++y) {
-        const float w = __shfl_sync(0xFFFFFFFFu, f, (p + y) & 31);
-        if (p + y < n && w != 0.0f) {
-          o.x = fmaf(a[y].x, w, o.x); o.y = fmaf(a[y].y, w, o.y); o.z = fmaf(a[y].z, w, o.z); o.w = fmaf(a[y].w, w, o.w);
-        }
+      for (int y = 0; y < 4; ++y) {
+        const float w = __shfl_sync(0xFFFFFFFFu, f, 2 * (p + y) + rr);
+        if (w != 0.0f)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            o[x].x = fmaf(a[y][x].x, w, o[x].x); o[x].y = fmaf(a[y][x].y, w, o[x].y);
+            o[x].z = fmaf(a[y][x].z, w, o[x].z); o[x].w = fmaf(a[y][x].w, w, o[x].w);
+          }
       }
     }
   }
@@ -277,53 +297,74 @@ __global__ void __launch_bounds__(32 * kMergeRows) attend_join_kernel(AttArgs A,
                                                                       const float* __restrict__ scan_part) {
   const AttJoin J = joins[blockIdx.y];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // (the plans were there before the kernels that this one follows)
-  const int i = blockIdx.x * kMergeRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (i >= J.rows) return;
+  const int lane = threadIdx.x & 31, c = lane >> 1;
+  const int i0 = 2 * (blockIdx.x * kMergeRows + (int)(threadIdx.x >> 5));
+  if (i0 >= J.rows) return;
+  const bool mine = i0 + (lane & 1) < J.rows;   // (an odd last row: both halves of the warp take it)
+  const int i = mine ? i0 + (lane & 1) : i0;
   const int g = A.hq / A.hkv;
   const size_t at = ((size_t)(J.tok0 + i / g) * A.hq + (size_t)J.kvh * g + i % g) * kHeadDim;
   const bool scan = (J.flags & kJoinScan) != 0;
-  PartRow own, pre{nullptr, nullptr, 0, 0, 0.0f};
+  PartRow own, pre{nullptr, nullptr, 0, 0, 0, 0.0f};
   if (scan) {
     const Unit u = scan_units[J.own0];
     const float* p = scan_part + ((size_t)u.split_begin * g + i) * kAttPart;
-    own = PartRow{p + 4 * lane, p + kHeadDim, (size_t)g * kAttPart, u.n_splits, kAttHead};
+    own = PartRow{p + 4 * c, p + kHeadDim, (size_t)g * kAttPart, 64, u.n_splits, kAttHead};
   } else {
-    own = part_row(srcs[J.own0 + (i >> J.own_shift)], part, i & ((1 << J.own_shift) - 1), lane, (J.flags & kJoinOwnTall) != 0);
+    own = part_row(srcs[J.own0 + (i >> J.own_shift)], part, i & ((1 << J.own_shift) - 1), c, (J.flags & kJoinOwnTall) != 0);
   }
   if (J.pre0 >= 0) {
     const int ip = J.pre_row + i;
-    pre = part_row(srcs[J.pre0 + (ip >> J.pre_shift)], part, ip & ((1 << J.pre_shift) - 1), lane, (J.flags & kJoinPreTall) != 0);
+    pre = part_row(srcs[J.pre0 + (ip >> J.pre_shift)], part, ip & ((1 << J.pre_shift) - 1), c, (J.flags & kJoinPreTall) != 0);
   }
-  const float mo = part_max(own, lane), mp = part_max(pre, lane);
+  const float mo = part_max(own, c), mp = part_max(pre, c);
   float L = 0.0f, M = fmaxf(mo, mp);
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float4 o[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
   part_add(own, lane, M, L, o);
-  if (scan && J.n_pages > 0 && !(mo > kSentinel + 160.0f && __all_sync(0xFFFFFFFFu, finite4(o) && L < INFINITY))) {
-    PlainRow R = plain_row(A, A.q + at, J.req, J.kvh, J.n_pages);
-    R.m += kAttHead;
-    M = fmaxf(R.m, mp);
-    const float f = R.m == -INFINITY ? (R.l == 0.0f ? 0.0f : 1.0f) : exp2f(R.m - M);
-    L = lane == 0 ? R.l * f : 0.0f;
-    o = make_float4(R.o.x * f, R.o.y * f, R.o.z * f, R.o.w * f);
+  if (scan && J.n_pages > 0) {
+    const uint32_t unsure = __ballot_sync(0xFFFFFFFFu, !(mo > kSentinel + 160.0f && finite4(o[0]) && finite4(o[1]) && L < INFINITY));
+#pragma unroll 1
+    for (int y = 0; y < 2; ++y) {
+      if (!(unsure & (0x55555555u << y))) continue;
+      const PlainRow R = plain_row(A, A.q + __shfl_sync(0xFFFFFFFFu, (unsigned long long)at, y), J.req, J.kvh, J.n_pages);
+      const float x[4] = {R.o.x, R.o.y, R.o.z, R.o.w};
+      float lo[4], hi[4];   // channels 4 c .. and 64 + 4 c ..
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        lo[k] = __shfl_sync(0xFFFFFFFFu, x[k], c);
+        hi[k] = __shfl_sync(0xFFFFFFFFu, x[k], 16 + c);
+      }
+      if ((lane & 1) != y) continue;
+      const float m = R.m + kAttHead;
+      M = fmaxf(m, mp);
+      const float f = R.m == -INFINITY ? (R.l == 0.0f ? 0.0f : 1.0f) : exp2f(m - M);
+      L = c == 0 ? R.l * f : 0.0f;
+      o[0] = make_float4(lo[0] * f, lo[1] * f, lo[2] * f, lo[3] * f);
+      o[1] = make_float4(hi[0] * f, hi[1] * f, hi[2] * f, hi[3] * f);
+    }
+    __syncwarp();
   }
   part_add(pre, lane, M, L, o);
-#pragma unroll
-  for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, x);
+  L = row_sum(L);
   const float inv = row_inverse(M, L);
-  const float r[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-  uint16_t* op = A.out + at + 4 * lane;
   bool bad = false;
-  uint32_t h[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (!(fabsf(r[k]) < INFINITY)) bad = true;
-    h[k] = __bfloat16_as_ushort(__float2bfloat16_rn(r[k]));
-  }
-  if (((uintptr_t)A.out & 7) == 0) {
-    *reinterpret_cast<uint2*>(op) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-  } else {
+  for (int x = 0; x < 2; ++x) {
+    const float r[4] = {o[x].x * inv, o[x].y * inv, o[x].z * inv, o[x].w * inv};
+    uint16_t* op = A.out + at + 64 * x + 4 * c;
+    uint32_t h[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) op[k] = (uint16_t)h[k];
+    for (int k = 0; k < 4; ++k) {
+      if (!(fabsf(r[k]) < INFINITY)) bad = true;
+      h[k] = __bfloat16_as_ushort(__float2bfloat16_rn(r[k]));
+    }
+    if (!mine) continue;
+    if (((uintptr_t)A.out & 7) == 0) {
+      *reinterpret_cast<uint2*>(op) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) op[k] = (uint16_t)h[k];
+    }
   }
   if (bad) atomicOr(A.status, kStatusRange);
 }
@@ -334,7 +375,7 @@ cudaError_t launch_attend_join(kv_pool* P, const AttArgs& A, const AttJoin* d_jo
   for (int a = 0; a < n_joins; a += 65535) {
     ++P->launches;
     const cudaError_t e = launch_pdl(
-        attend_join_kernel, dim3((unsigned)((max_rows + kMergeRows - 1) / kMergeRows), (unsigned)std::min(65535, n_joins - a)),
+        attend_join_kernel, dim3((unsigned)((max_rows + 2 * kMergeRows - 1) / (2 * kMergeRows)), (unsigned)std::min(65535, n_joins - a)),
         dim3(32 * kMergeRows), 0, s, A, d_joins + a, d_srcs, d_part, scan_units, scan_part);
     if (e != cudaSuccess) return e;
   }

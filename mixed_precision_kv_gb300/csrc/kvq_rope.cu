@@ -43,7 +43,7 @@ __device__ __forceinline__ void row_store(uint16_t* p, const uint4& v, bool alig
 // A thread takes item i of a row (kvq_rope.h) of one token, its factors once and
 // then every `lines`-th head of q and k together; 256 / (8 lines) tokens a CTA.
 template <bool kAligned>
-__global__ void __launch_bounds__(kRotThreads, 5) rotate_kernel(const __grid_constant__ RopeArgs R,
+__global__ void __launch_bounds__(kRotThreads, 4) rotate_kernel(const __grid_constant__ RopeArgs R,
                                                              const __grid_constant__ RotTensor Q,
                                                              const __grid_constant__ RotTensor K, int64_t n, int lines,
                                                              uint32_t* __restrict__ status) {
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kRotThreads, 5) rotate_kernel(const __grid_con
   uint16_t* qy = Q.y + (size_t)t * (size_t)Q.ys;
   uint16_t* ky = K.y + (size_t)t * (size_t)K.ys;
   const int all = Q.heads + K.heads;
-  constexpr int kAhead = 2;
+  constexpr int kAhead = 3;
   for (int h0 = line; h0 < all; h0 += kAhead * lines) {
     uint4 x[kAhead], z[kAhead];
 #pragma unroll
@@ -156,9 +156,9 @@ extern "C" kv_status_t kv_rotate(kv_pool_t* P, const kv_rope_t* rope, const int3
   const kv_status_t st = rope_args("kv_rotate", rope, pos, pos_stride, n_tok, R);
   if (st != KV_OK) return st;
   DeviceGuard dg(P->cfg.device);
-  // Lines of heads side by side: about four heads a thread, fewer while the call's tokens do not fill the SMs.
+  // Lines of heads side by side: about five heads a thread, fewer while the call's tokens do not fill the SMs.
   int lines = 1;
-  while (lines < kRotThreads / 8 && (lines * 4 < q_heads + k_heads || n_tok * lines * 8 < (int64_t)P->sm_count * 512)) lines *= 2;
+  while (lines < kRotThreads / 8 && (lines * 6 < q_heads + k_heads || n_tok * lines * 8 < (int64_t)P->sm_count * 512)) lines *= 2;
   const int per = kRotThreads / 8 / lines;
   const unsigned grid = (unsigned)((n_tok + per - 1) / per);
   ++P->launches;
