@@ -80,6 +80,23 @@ def test_shared(kvq, hkv, hq, pre, own, n_new, prefix, with_kv):
     P.pool.destroy()
 
 
+@pytest.mark.parametrize("rows", [65, 100, 127, 128, 129, 200])
+def test_rows_of_a_prefix(kvq, rows):
+    """Blocks of 128 rows of a prefix, full and not: every width, list tokens, evicted slots, few keys and many."""
+    rng = np.random.default_rng(rows)
+    w = (2, 3, 4, 0xF4)
+    P = Pool(kvq, 1, [rng.choice(w, 900).astype(np.uint8), rng.choice(w, 20).astype(np.uint8), mixed(70, 2), mixed(40, 3)],
+             seed=rows, dead=[list(range(250, 420)), [], [], []], slack=128)
+    P.pool.fp_configure(140)
+    k, v = rand((130, 1, 128), P.gen), rand((130, 1, 128), P.gen)
+    P.pool.fp_append(P.ids[0], k, v)
+    fp = {0: (k.double().cpu().numpy(), v.double().cpu().numpy())}
+    some = sorted({0, 1, rows // 3 - 1, rows // 3, rows // 2, rows - rows // 3 - 1})
+    check(P, [2, 3], [0, 0], [rows // 3, rows - rows // 3], 1, fp=fp, rows=some)
+    check(P, [2, 3], [1, 1], [rows // 3, rows - rows // 3], 1, rows=some)
+    P.pool.destroy()
+
+
 @pytest.mark.parametrize("g", [1, 4, 7])
 def test_decode_step(kvq, g):
     """A token per request and no new keys, enough tiles for the decode's scan: ragged own caches (one empty), a request
