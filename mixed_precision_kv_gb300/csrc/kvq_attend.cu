@@ -893,7 +893,7 @@ extern "C" kv_status_t kv_attend_shared(kv_pool_t* P, const void* q, const void*
   for (int32_t b = 0; b < n_req; ++b)
     for (int h = 0; h < hkv && n_new[b] > 0; ++h) {
       AttUnit w = attend_unit(P, req_ids[b], h, n_new[b], k != nullptr, tok0[(size_t)b]);
-      w.joined = group_of[(size_t)b] >= 0;
+      w.joined = !pre.empty();   // (those without a prefix too: one kernel then ends the call)
       own.push_back(w);
     }
   // One launch for both kinds where their rows go by blocks of one size, or where there is so little
@@ -971,7 +971,7 @@ extern "C" kv_status_t kv_attend_shared(kv_pool_t* P, const void* q, const void*
         J.flags = o.wide ? kJoinOwnTall : 0;
       }
       J.pre0 = -1;
-      if (own[x].joined) {
+      if (group_of[(size_t)b] >= 0) {
         const AttSet::Where p = PS.where[(size_t)group_of[(size_t)b] * hkv + h];
         J.pre0 = p.wide ? ps.second + PS.pl.src0[(size_t)p.index] : ps.first + PS.pf.src0[(size_t)p.index];
         J.pre_shift = p.wide ? 7 : log2i(PS.R);
