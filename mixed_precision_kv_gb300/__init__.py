@@ -364,7 +364,7 @@ class KVPool:
         elif dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("dtype must be torch.bfloat16 or torch.float32")
         req_ids = _np(req_ids, np.int32).reshape(-1)
-        first = np.full(req_ids.size, first, np.int64) if isinstance(first, int) else _np(first, np.int64)
+        first = np.full(req_ids.size, first, np.int64) if isinstance(first, (int, np.integer)) else _np(first, np.int64)
         if n is None:
             n = np.empty(req_ids.size, np.int64)
             rc = self._L.kv_request_lengths(self._h, req_ids.ctypes.data, req_ids.size, n.ctypes.data)
@@ -373,7 +373,7 @@ class KVPool:
             if first.shape == n.shape:
                 n -= first
         else:
-            n = np.full(req_ids.size, n, np.int64) if isinstance(n, int) else _np(n, np.int64)
+            n = np.full(req_ids.size, n, np.int64) if isinstance(n, (int, np.integer)) else _np(n, np.int64)
         if first.shape != req_ids.shape or n.shape != req_ids.shape:
             raise ValueError("req_ids, first and n must be sequences of one length")
         rows = n.tolist()

@@ -167,8 +167,9 @@ cudaError_t launch_attend_merge(kv_pool* P, const AttArgs& A, const AttUnit* d_u
 // Rows with a shared prefix: the parts of the request's own unit and those of the
 // prefix unit, each in the layout of the kernel that made it.  A warp takes two
 // rows, a lane 4 channels of each half of one: parts by channel hold neighbouring
-// rows side by side, so whole sectors are read.  Bound by the partials' bytes,
-// which are still in L2.
+// rows side by side, so whole sectors are read (64 requests over 100K with 64 q
+// heads: the call 317 us, 326 with a row per warp).  Bound by the partials' latency:
+// they are still in L2, and a row has few of them.
 struct PartRow {
   const float *o, *ml;   // this lane's first channels of part 0, the row's m and l
   size_t step;
@@ -372,14 +373,10 @@ __global__ void __launch_bounds__(32 * kMergeRows) attend_join_kernel(AttArgs A,
 cudaError_t launch_attend_join(kv_pool* P, const AttArgs& A, const AttJoin* d_joins, int n_joins, int max_rows,
                                const AttSrc* d_srcs, const float* d_part, const Unit* scan_units, const float* scan_part,
                                cudaStream_t s) {
-  for (int a = 0; a < n_joins; a += 65535) {
-    ++P->launches;
-    const cudaError_t e = launch_pdl(
-        attend_join_kernel, dim3((unsigned)((max_rows + 2 * kMergeRows - 1) / (2 * kMergeRows)), (unsigned)std::min(65535, n_joins - a)),
-        dim3(32 * kMergeRows), 0, s, A, d_joins + a, d_srcs, d_part, scan_units, scan_part);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  if (n_joins == 0) return cudaSuccess;
+  ++P->launches;   // (a join per request and kv head: at most 65535)
+  return launch_pdl(attend_join_kernel, dim3((unsigned)((max_rows + 2 * kMergeRows - 1) / (2 * kMergeRows)), (unsigned)n_joins),
+                    dim3(32 * kMergeRows), 0, s, A, d_joins, d_srcs, d_part, scan_units, scan_part);
 }
 
 // ---- work plan ---------------------------------------------------------
@@ -897,7 +894,8 @@ extern "C" kv_status_t kv_attend_shared(kv_pool_t* P, const void* q, const void*
       own.push_back(w);
     }
   // One launch for both kinds where their rows go by blocks of one size, or where there is so little
-  // work that a launch more counts for more than the larger blocks: 4 x 2K tokens of 2 kv heads.
+  // work that a launch and a plan more count for more than the larger blocks (4 requests over 2K tokens of
+  // 2 kv heads: 20 us of the host's time a call, 34 apart).
   auto size_of = [&](const std::vector<AttUnit>& units, int64_t& tiles) {
     int rows = 0;
     tiles = 0;
@@ -911,8 +909,9 @@ extern "C" kv_status_t kv_attend_shared(kv_pool_t* P, const void* q, const void*
   const int pre_rows = size_of(pre, pre_tiles), own_rows = size_of(own, own_tiles);
   auto block_of = [](int rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); };
   const bool little = pre_tiles + own_tiles <= 2 * (int64_t)P->sm_count;
-  // A decode step (a token per request, nothing but caches): the decode's scan reads the own caches at 2.2 to 2.6 us
-  // per 1000 tiles; the few-row kernel takes 8 for rows that fill a quarter or half of its blocks.
+  // A decode step (a token per request, nothing but caches): the decode's scan reads the own caches faster than the
+  // few-row kernel, whose blocks such rows fill to a quarter or half: 32 x 1050 tokens, 32 q and 8 kv heads, 19 us
+  // against 32; 64 x 1000, 64 and 8 heads, 29 against 58.  It costs two launches and a plan more, so not for few tiles.
   bool scan = !k && !little && own_tiles > 4 * (int64_t)P->sm_count;
   for (int32_t b = 0; b < n_req && scan; ++b)
     scan = n_new[b] == 1 && (P->n_fp.empty() || P->n_fp[req_ids[b]] == 0);
