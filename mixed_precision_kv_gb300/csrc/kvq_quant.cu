@@ -843,15 +843,18 @@ __device__ __forceinline__ void rotate_page(RopeTile& K, const RopeArgs& R, cons
     K.row[t][b] = z;
   }
 }
-// This lane's pieces of K or V as they are, asynchronously: the lane that reads them fetches them, so they
-// need no barrier.
+// The warp's group of K or V as it is, asynchronously: 4 lanes take a token's 64 bytes, whole sectors, so that
+// the warp that reads them fetches them and needs no CTA-wide barrier.  T: token of slot t, this lane.
 __device__ __forceinline__ void fetch_group(RopeTile& X, const __nv_bfloat16* __restrict__ src, int T, int t, int h, size_t step,
                                             int gr) {
-  const __nv_bfloat16* p = src + (size_t)T * step + (size_t)h * kHeadDim + 32 * gr;
+  const __nv_bfloat16* p = src + (size_t)h * kHeadDim + 32 * gr + 8 * (t & 3);
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(&X.row[t][4 * gr + q])),
-                 "l"(p + 8 * q) : "memory");
+  for (int q = 0; q < 4; ++q) {
+    const int y = 8 * q + (t >> 2);
+    const int Ty = __shfl_sync(0xFFFFFFFFu, T, y);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(&X.row[y][4 * gr + (t & 3)])), "l"(p + (size_t)Ty * step) : "memory");
+  }
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 // The rows of a page: K's in shared memory, V's on their way.
@@ -866,9 +869,13 @@ __device__ __forceinline__ void start_page(RopeTile& K, RopeTile& V, const RopeP
     __syncthreads();
   } else {
     asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
   }
 }
-__device__ __forceinline__ void v_ready() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void v_ready() {
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncwarp();
+}
 
 // Metadata of a token's group at row (4 pieces of 8 bf16 channels): min / max exactly, NaN
 // carried so that the range check sees it (NaN, Inf or |x| > 65504 sets `bad`).
