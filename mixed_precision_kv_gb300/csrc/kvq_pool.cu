@@ -1144,8 +1144,8 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
                           [&](const AppendJob& j) { return is_int3(P, j.page); });
   }
   const bool small = n_i3 + n_f4 == 0 && jobs.size() <= (size_t)SmallAppend::kMaxJobs && off <= SmallAppend::kMaxToks;
-  // Large calls with 16-byte aligned K/V rows: fresh pages filled with 32
-  // tokens go to the bulk INT4 kernel, direct groups to the bulk INT2 kernel.
+  // 16-byte aligned K/V rows: direct groups go to the bulk INT2 kernel and, in large
+  // calls, fresh pages filled with 32 tokens to the bulk INT4 kernel.
   const bool aligned = (uintptr_t)k % 16 == 0 && (uintptr_t)v % 16 == 0 &&
                        (!P->rope || (P->rope->k_stride % 8 == 0 && P->rope->v_stride % 8 == 0));
   const bool use_bulk = !small && aligned;
@@ -1227,7 +1227,7 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
       KV_CUDA(launch_append_fp4(P, k, v, (const AppendJob*)(base + o_jobs) + (jobs.size() - n_f4), (int)n_f4,
                                 (const int32_t*)(base + o_toks), s));
   }
-  if (use_bulk)
+  if (aligned)
     KV_CUDA(launch_bulk_int2(P, k, v, (const DirectJob*)(base + o_dir), (int)directs.size(),
                              (const int32_t*)(base + o_dtok), s));
   else
