@@ -716,9 +716,11 @@ __global__ void __launch_bounds__(kThreads) direct_int2_kernel(
 // reductions across the 32 tokens.  The results are those of make_meta and
 // qcode_fast, bit for bit.
 //
-// What bounds them: instruction issue (105K INT4 tokens x 8 kv heads 170 us, rotated
-// 208 to 224; 157K INT2 tokens 422, rotated 441 to 455; rows through registers and
-// a step per value took 222 and 670, rotated).  The loops over the 8-channel pieces are kept
+// What bounds them: instruction issue (65K tokens of each width x 8 kv heads: INT4
+// pages 136 us, INT2 194; 106K and 156K tokens, rotated: 215 and 427).  Rows through
+// registers and a step per value took 145 and 277, rotated 222 and 670; rows fetched
+// by the lane that reads them, half sectors, 155 and 210.  A page's heads side by
+// side in the grid change nothing.  The loops over the 8-channel pieces are kept
 // as loops and the rare exact divisions out of line: with everything unrolled the
 // INT2 kernel was 105 KB of code, and a third of its stalls were waits for
 // instructions.
