@@ -1241,8 +1241,10 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
 extern "C" {
 
 kv_status_t kv_append_quant(kv_pool_t* P, const void* k, const void* v, const int32_t* req_ids,
-                            const uint8_t* bits, int64_t n_tok, void* stream) {
+                            const uint8_t* bits, int64_t n_tok, void* stream) try {
   return append_tokens(P, "kv_append_quant", k, v, req_ids, bits, n_tok, stream);
+} catch (const std::bad_alloc&) {
+  return fail(KV_ERR_OOM, "kv_append_quant: host allocation failed");
 }
 
 kv_status_t kv_reorder_pages(kv_pool_t* P, const int32_t* req_ids, int32_t n_req, void* stream) {
