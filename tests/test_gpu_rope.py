@@ -240,6 +240,44 @@ def test_append_rotated_alignment(kvq):
     b.destroy()
 
 
+def test_int2_groups_alone(kvq):
+    """Calls that are whole INT2 groups and nothing else: 16-byte aligned rows (the kernel of large calls) and rows at an
+    odd multiple of 8 bytes (a warp per token) give the same pages, positions and values."""
+    gen = torch.Generator("cuda").manual_seed(12)
+    a, b = small_pool(kvq, 3), small_pool(kvq, 3)
+    rope, _ = make_rope(kvq, 700, 128)
+    ra, rb = [[p.open() for _ in range(2)] for p in (a, b)]
+
+    def both(which, bits, rotated):
+        n = len(which)
+        flat = rand(gen, 2 * n * 3 * 128 + 8, scale=2.0)
+        off = flat[4:-4].view(2, n, 3, 128)
+        k, v = off.clone()
+        assert k.data_ptr() % 16 == 0 and off[0].data_ptr() % 16 == 8
+        if rotated:
+            pos = torch.randint(0, 700, (n,), generator=gen, device="cuda", dtype=torch.int32)
+            a.append_rotated(k, v, np.array(ra)[which], bits, rope, pos)
+            b.append_rotated(off[0], off[1], np.array(rb)[which], bits, rope, pos)
+        else:
+            a.append(k, v, np.array(ra)[which], bits)
+            b.append(off[0], off[1], np.array(rb)[which], bits)
+        for x, y in zip(ra, rb):
+            same_content(a, b, x, y)
+        for x, y in zip(a.read(ra, dtype=torch.float32), b.read(rb, dtype=torch.float32)):
+            assert torch.equal(x, y)
+
+    both([0] * 5 + [1] * 3, [4] * 8, False)   # (the read after it puts the positions on the device)
+    for rotated in (False, True):
+        for n in (32, 96, 64):
+            both([0] * n, [2] * n, rotated)
+        both([0] * 32 + [1] * 64, [2] * 96, rotated)    # runs
+        both([0, 1] * 64, [2] * 128, rotated)           # token by token
+    a.sync()
+    b.sync()
+    a.destroy()
+    b.destroy()
+
+
 def test_append_rotated_checks_values_after_the_rotation(kvq):
     pool = small_pool(kvq)
     rope, _ = make_rope(kvq, 10, 128)
