@@ -247,6 +247,15 @@ __device__ __noinline__ PlainRow plain_row(const AttArgs& A, const uint16_t* q, 
   const int lane = threadIdx.x & 31;
   PlainRow R{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
   bool seen = false, wild = false;
+  // rows past 2^60 are taken 2^64 smaller and their logits 2^64 larger, both exact, so that q . k stays in fp32
+  // where the logit does (the scale is within 2^40 of one here)
+  float mx_q = 0.0f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) mx_q = fmaxf(mx_q, fabsf(__uint_as_float((uint32_t)q[4 * lane + c] << 16)));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mx_q = fmaxf(mx_q, __shfl_xor_sync(0xFFFFFFFFu, mx_q, o));
+  const bool large = mx_q > 0x1p60f;
+  const float down = large ? 0x1p-64f : 1.0f, scale = large ? A.scale_log2 * 0x1p64f : A.scale_log2;
   for (int p = 0; p < n_pages; ++p) {
     const Entry e = A.table[(size_t)req * A.max_pages + p];
     const uint32_t live = A.hdead ? e.live & ~A.hdead[(size_t)e.id * A.hkv + kvh] : e.live;
@@ -256,9 +265,9 @@ __device__ __noinline__ PlainRow plain_row(const AttArgs& A, const uint16_t* q, 
     const int cls = att_page(A, e.id, kvh, b);
     const bool on = (live >> lane) & 1u;
     float s = 0.0f;
-    for (int c = 0; on && c < kHeadDim; ++c) s = fmaf(__uint_as_float((uint32_t)q[c] << 16), k_value(b, cls, lane, c), s);
+    for (int c = 0; on && c < kHeadDim; ++c) s = fmaf(__uint_as_float((uint32_t)q[c] << 16) * down, k_value(b, cls, lane, c), s);
     const bool whole = fabsf(s) < INFINITY;
-    s *= A.scale_log2;
+    s *= scale;
     // past fp32's range, above or below: the row is not a number
     if (__any_sync(0xFFFFFFFFu, on && !(whole && s < INFINITY))) wild = true;
     s = on && whole && s < INFINITY ? s : -INFINITY;
@@ -912,7 +921,10 @@ extern "C" kv_status_t kv_attend_shared(kv_pool_t* P, const void* q, const void*
   // A decode step (a token per request, nothing but caches): the decode's scan reads the own caches faster than the
   // few-row kernel, whose blocks such rows fill to a quarter or half: 32 x 1050 tokens, 32 q and 8 kv heads, 19 us
   // against 32; 64 x 1000, 64 and 8 heads, 29 against 58.  It costs two launches and a plan more, so not for few tiles.
-  bool scan = !k && !little && own_tiles > 4 * (int64_t)P->sm_count;
+  // The scan scales rows of q to binary16 by 2^-100 to 2^100: enough for every row whose logits are neither all
+  // near 0 nor past fp32, if the softmax's scale is within 2^40 of one.
+  const float abs_scale = std::fabs(softmax_scale);
+  bool scan = !k && !little && own_tiles > 4 * (int64_t)P->sm_count && abs_scale >= 0x1p-40f && abs_scale <= 0x1p40f;
   for (int32_t b = 0; b < n_req && scan; ++b)
     scan = n_new[b] == 1 && (P->n_fp.empty() || P->n_fp[req_ids[b]] == 0);
   const bool together = !scan && !pre.empty() && std::max(pre_rows, own_rows) <= kFewRows &&
