@@ -261,6 +261,15 @@ class FreeIds {
       if ((size_t)(x >> 6) < lo_) lo_ = (size_t)(x >> 6);
     }
   }
+  void remove(int32_t id) {   // (no-op if it is not free)
+    const int32_t x = id - first_;
+    uint64_t& wd = bits_[(size_t)(x >> 6)];
+    const uint64_t b = 1ull << (x & 63);
+    if (wd & b) {
+      wd &= ~b;
+      --count_;
+    }
+  }
   int32_t take_lowest() {   // caller ensures !empty()
     while (bits_[lo_] == 0) ++lo_;
     const int b = __builtin_ctzll(bits_[lo_]);

@@ -25,7 +25,7 @@ using namespace kvq;
 
 namespace {
 
-thread_local std::string g_err;
+thread_local char g_err[512];   // (no allocation: a message may be about memory)
 
 bool is_int2(const kv_pool* P, int32_t id) { return id < P->cfg.n_int2_pages; }
 // INT3 ids follow the INT2 and INT4 ids, FP4 ids the INT3 ids
@@ -109,15 +109,13 @@ void emit_updates(const kv_pool* P, const Dirty& d, std::vector<TableUpd>& out) 
 
 }  // namespace
 
-void kvq::set_last_error(const char* msg) { g_err = msg; }
+void kvq::set_last_error(const char* msg) { snprintf(g_err, sizeof(g_err), "%s", msg); }
 
 kv_status_t kvq::fail(kv_status_t st, const char* fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
   va_end(ap);
-  g_err = buf;
   return st;
 }
 
@@ -337,7 +335,7 @@ void kvq::plan_decode(const kv_pool* P, const int32_t* req_ids, int32_t batch, i
 
 extern "C" {
 
-const char* kv_last_error(void) { return g_err.c_str(); }
+const char* kv_last_error(void) { return g_err; }
 
 kv_status_t kv_alloc_bits(const int64_t* N, const double* D2, const double* D4, int32_t n_tags, int64_t B_num,
                           int64_t B_den, uint8_t* bits_out) {
@@ -630,6 +628,13 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
     bool tail; int tailfill; bool tail3; int tail3fill; bool tailf; int tailffill; bool stag; int stagfill;
     int64_t tablen;
     int64_t npos;          // the request's token positions after the call
+    // the request before the call, for Undo: its open pages (INT4, INT3, FP4 tails, staging), what they held
+    int32_t open[4];
+    uint8_t open_fill[4];
+    uint32_t open_live[4];
+    int64_t old_pos;
+    uint64_t old_version, old_shape;
+    int32_t erased;        // table index at which the staging page stood when it was requantized (-1: it stands)
   };
   std::vector<CallReq> cr;
   if (P->call_slot.size() != (size_t)P->cfg.max_requests) P->call_slot.assign((size_t)P->cfg.max_requests, -1);
@@ -637,7 +642,6 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
     int32_t& sl = P->call_slot[(size_t)r];
     if (sl < 0) {
       const Request& R = P->reqs[r];
-      sl = (int32_t)cr.size();
       CallReq c{};
       c.r = r;
       c.old_len = (int32_t)R.table.size();
@@ -652,7 +656,18 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
       c.stagfill = c.stag ? (int)P->fill[R.staging] : 0;
       c.tablen = (int64_t)R.table.size();
       c.npos = (int64_t)R.loc.size();
+      const int32_t open[4] = {R.tail4, R.tail3, R.tailf, R.staging};
+      for (int y = 0; y < 4; ++y) {
+        c.open[y] = open[y];
+        c.open_fill[y] = open[y] < 0 ? 0 : P->fill[open[y]];
+        c.open_live[y] = open[y] < 0 ? 0u : P->live[open[y]];
+      }
+      c.old_pos = c.npos;
+      c.old_version = R.version;
+      c.old_shape = R.shape;
+      c.erased = -1;
       cr.push_back(c);
+      sl = (int32_t)cr.size() - 1;
     }
     return cr[(size_t)sl];
   };
@@ -661,6 +676,58 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
     std::vector<CallReq>* cr;
     ~ResetSlots() { for (const auto& c : *cr) P->call_slot[(size_t)c.r] = -1; }
   } reset_slots{P, &cr};
+  // The host's memory can run out while the tokens are routed: the pool then goes back to what it was (KV_ERR_OOM).
+  // Nothing has been sent to the device by then, and nothing here allocates.
+  struct Undo {
+    kv_pool* P;
+    std::vector<CallReq>* cr;
+    std::vector<int32_t> taken;    // page ids that the call took
+    std::vector<uint32_t> hdead;   // exclusion words of each request's staging page
+    bool armed = false;
+    int32_t take(FreeIds& f) {
+      taken.push_back(f.take_lowest());   // (room for all of them is there)
+      return taken.back();
+    }
+    ~Undo() {
+      if (!armed) return;
+      const size_t hkv = (size_t)P->cfg.num_kv_heads;
+      for (int32_t id : taken) {
+        P->fill[id] = 0;
+        P->live[id] = 0u;
+        if (!P->hdead.empty()) std::fill_n(&P->hdead[(size_t)id * hkv], hkv, 0u);
+        free_list(P, id).insert(id);
+      }
+      for (size_t x = 0; x < cr->size(); ++x) {
+        const CallReq& c = (*cr)[x];
+        Request& R = P->reqs[c.r];
+        const int32_t sp = c.open[3];
+        if (c.erased < 0) {
+          R.table.resize((size_t)c.old_len);
+        } else {   // (the table has held old_len entries: no new memory)
+          R.table.resize((size_t)c.old_len - 1);
+          R.table.insert(R.table.begin() + c.erased, sp);
+          P->free4.remove(sp);
+        }
+        R.tail4 = c.open[0];
+        R.tail3 = c.open[1];
+        R.tailf = c.open[2];
+        R.staging = sp;
+        for (int y = 0; y < 4; ++y)
+          if (c.open[y] >= 0) {
+            P->fill[c.open[y]] = c.open_fill[y];
+            P->live[c.open[y]] = c.open_live[y];
+          }
+        if (sp >= 0) {
+          for (int sl = 0; sl < c.open_fill[3]; ++sl)
+            R.loc[(size_t)P->pos[(size_t)sp * kPage + sl]] = ((uint32_t)sp << 5) | (uint32_t)sl;
+          if (!P->hdead.empty()) std::copy_n(&hdead[x * hkv], hkv, &P->hdead[(size_t)sp * hkv]);
+        }
+        R.loc.resize((size_t)c.old_pos);
+        R.version = c.old_version;
+        R.shape = c.old_shape;
+      }
+    }
+  } undo{P, &cr, {}, {}};
 
   // Bulk path: the call's tokens come in runs, one per request (a prefill
   // chunk of one request, or one chunk of each of several requests): every
@@ -757,6 +824,7 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
     n4 = c4;
     n2 = c2;
   }
+  int64_t n_pages = 0;   // that the call takes
   if (bulk) {
     int64_t need4 = 0, need2 = 0;
     for (auto& u : runs) {
@@ -783,6 +851,7 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
     if (need4 > (int64_t)P->free4.size() || need2 > (int64_t)P->free2.size())
       return fail(KV_ERR_OOM, "%s: needs %lld INT4 + %lld INT2 pages, %zu + %zu free", what, (long long)need4,
                   (long long)need2, P->free4.size(), P->free2.size());
+    n_pages = need4 + need2;
   }
   // Dry run: pages taken and table growth, so that OOM changes nothing.
   if (!bulk) {
@@ -820,6 +889,7 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
       return fail(KV_ERR_OOM, "%s: needs %lld INT3 pages, %zu free", what, (long long)need3, P->free3.size());
     if (needf > (int64_t)P->freef.size())
       return fail(KV_ERR_OOM, "%s: needs %lld FP4 pages, %zu free", what, (long long)needf, P->freef.size());
+    n_pages = need4 + need3 + needf + need2;
   }
   // room for this call's tokens in each position map; growth is geometric
   // (reserving just the new size on every call would copy the whole map)
@@ -828,10 +898,18 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
     const size_t need = R.loc.size() + (size_t)(bulk ? runs[x].n : n_tok);   // (runs: in the order of cr)
     if (R.loc.capacity() < need) R.loc.reserve(std::max(need, 2 * R.loc.capacity()));
   }
+  undo.taken.reserve((size_t)n_pages);
+  if (!P->hdead.empty()) {
+    const size_t hkv = (size_t)P->cfg.num_kv_heads;
+    undo.hdead.resize(cr.size() * hkv);
+    for (size_t x = 0; x < cr.size(); ++x)
+      if (cr[x].open[3] >= 0) std::copy_n(&P->hdead[(size_t)cr[x].open[3] * hkv], hkv, &undo.hdead[x * hkv]);
+  }
   DeviceGuard dg(P->cfg.device);
   cudaStream_t s = (cudaStream_t)stream;
   kv_status_t st = order_after_previous(P, s);
   if (st != KV_OK) return st;
+  undo.armed = true;
 
   // Routing in token order (page ids are taken exactly as the per-token rules
   // dictate).  A staging page that starts empty and is filled within this
@@ -901,13 +979,13 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
       while (a < id4.size() || b < idS.size()) {
         const int32_t ta = a < id4.size() ? l4[(size_t)(u.cap4 + kPage * (int64_t)a)] : INT32_MAX;
         const int32_t tb = b < idS.size() ? l2[(size_t)(u.e + kPage * (int64_t)b)] : INT32_MAX;
-        if (ta < tb) id4[a++] = P->free4.take_lowest();
-        else idS[b++] = P->free4.take_lowest();
+        if (ta < tb) id4[a++] = undo.take(P->free4);
+        else idS[b++] = undo.take(P->free4);
       }
     }
-    const int32_t nid_rep = u.repack ? P->free2.take_lowest() : -1;
+    const int32_t nid_rep = u.repack ? undo.take(P->free2) : -1;
     std::vector<int32_t> idD((size_t)u.ndirect);
-    for (auto& x : idD) x = P->free2.take_lowest();
+    for (auto& x : idD) x = undo.take(P->free2);
     // table entries appended in this call, with the token that appends them
     std::vector<std::pair<int32_t, int32_t>> app;   // (token, page id)
     // INT4: the open tail page, then new pages
@@ -936,6 +1014,7 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
       const auto rit = std::find(R.table.rbegin(), R.table.rend(), sp);
       const auto it = std::next(rit).base();
       dirty.structural(r, (int32_t)(it - R.table.begin()));
+      cr[(size_t)P->call_slot[(size_t)r]].erased = (int32_t)(it - R.table.begin());
       R.table.erase(it);
       R.shape = ++P->shape_clock;
       repacks.push_back(RepackJob{sp, nid_rep});
@@ -983,7 +1062,7 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
     // INT4 tokens fill the INT4 tail, INT3 and FP4 tokens their own tails, INT2 tokens the (INT4) staging page
     int32_t& cur = b4 ? R.tail4 : (b3 ? R.tail3 : (bf ? R.tailf : R.staging));
     if (cur < 0 || P->fill[cur] == kPage) {
-      cur = (b3 ? P->free3 : (bf ? P->freef : P->free4)).take_lowest();
+      cur = undo.take(b3 ? P->free3 : (bf ? P->freef : P->free4));
       P->fill[cur] = 0;
       P->live[cur] = 0;
       R.table.push_back(cur);
@@ -1021,7 +1100,7 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
     }
     if (b2 && P->fill[cur] == kPage) {
       // 32 qualifying tokens: requantize the staging page into a new INT2 page.
-      const int32_t nid = P->free2.take_lowest();
+      const int32_t nid = undo.take(P->free2);
       P->fill[nid] = kPage;
       P->live[nid] = P->live[cur];
       hdead_copy(P, nid, cur, hupd);
@@ -1033,6 +1112,7 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
       const auto rit = std::find(R.table.rbegin(), R.table.rend(), cur);   // the staging page sits near the end
       const auto it = std::next(rit).base();
       dirty.structural(r, (int32_t)(it - R.table.begin()));
+      if (cur == c.open[3]) c.erased = (int32_t)(it - R.table.begin());
       R.table.erase(it);
       R.shape = ++P->shape_clock;
       R.table.push_back(nid);
@@ -1183,6 +1263,7 @@ kv_status_t kvq::append_tokens(kv_pool* P, const char* what, const void* k, cons
       std::copy(src, src + j.n_slots, tpos.begin() + j.tok_off);
     }
   }
+  undo.armed = false;   // from here on nothing allocates on the host
   Upload u;
   const size_t o_jobs = small ? 0 : u.add(jobs.data(), jobs.size() * sizeof(AppendJob));
   size_t o_toks = 0, o_dtok = 0;
