@@ -392,7 +392,9 @@ KVQ_API kv_status_t kv_attend(kv_pool_t* pool, const void* q, const void* k, con
  *   k, v        NULL (both): rows see the caches only, e.g. one token per request
  *               (n_new 1) that has been appended: the decode step of such a batch
  * The other arguments and the rules are kv_attend's (out is bf16); at most 2^20
- * new tokens over one prefix; always the tensor-core kernels. */
+ * new tokens over one prefix; always the tensor-core kernels.  The plan and the
+ * buffers are the call's own: a captured kv_decode_attn and kv_last_decode_stats
+ * stay as they are. */
 KVQ_API kv_status_t kv_attend_shared(kv_pool_t* pool, const void* q, const void* k, const void* v, const uint64_t* tree,
                                      const int32_t* req_ids, const int32_t* prefix_ids, const int32_t* n_new,
                                      int32_t n_req, int32_t num_q_heads, float softmax_scale, void* out, void* stream);

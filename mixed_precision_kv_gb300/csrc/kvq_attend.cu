@@ -994,10 +994,11 @@ extern "C" kv_status_t kv_attend_shared(kv_pool_t* P, const void* q, const void*
     }
   const int64_t tiles = std::max(SP.most, SO.most);
   if ((st = attend_room(P, end, tiles)) != KV_OK) return st;
+  DecodePlan& D = P->shared_plan;
   if (scan) {
-    if ((st = build_plan(P, req_ids, n_req, hq, KV_DECODE_MMA, s)) != KV_OK) return st;
-    if ((st = ensure(P->partials, (size_t)std::max(P->n_splits, 1) * g * kAttPart * sizeof(float))) != KV_OK) return st;
-    if ((st = ensure(P->frags, (size_t)std::max(P->n_units, 1) * decode_mma_frag_bytes())) != KV_OK) return st;
+    if ((st = build_plan(P, D, req_ids, n_req, hq, KV_DECODE_MMA, s)) != KV_OK) return st;
+    if ((st = ensure(P->shared_partials, (size_t)std::max(D.n_splits, 1) * g * kAttPart * sizeof(float))) != KV_OK) return st;
+    if ((st = ensure(P->shared_frags, (size_t)std::max(D.n_units, 1) * decode_mma_frag_bytes())) != KV_OK) return st;
   }
   if ((st = h2d(P, P->attend.ptr, u, s)) != KV_OK) return st;
   uint8_t* base = (uint8_t*)P->attend.ptr;
@@ -1005,15 +1006,15 @@ extern "C" kv_status_t kv_attend_shared(kv_pool_t* P, const void* q, const void*
   // the second launch starts as CTAs of the first leave, the joins as those of the second do
   const bool chained = SP.one_launch() && (scan || SO.one_launch());
   if ((st = SP.launch(P, A, tiles, s, chained ? kChainNext : 0)) != KV_OK) return st;
-  const uint8_t* plan = (const uint8_t*)P->plan.ptr;
-  const Unit* scan_units = scan ? (const Unit*)(plan + P->plan_units_off) : nullptr;
+  const uint8_t* plan = (const uint8_t*)D.buf.ptr;
+  const Unit* scan_units = scan ? (const Unit*)(plan + D.units_off) : nullptr;
   if (scan)
-    KV_CUDA(launch_scan_mma(P, q, hq, A.scale_log2, scan_units, P->n_units, (const Split*)(plan + P->plan_splits_off),
-                            (const int32_t*)(plan + P->plan_cta_off), P->n_ctas, P->frags.ptr, (float*)P->partials.ptr, s));
+    KV_CUDA(launch_scan_mma(P, q, hq, A.scale_log2, scan_units, D.n_units, (const Split*)(plan + D.splits_off),
+                            (const int32_t*)(plan + D.cta_off), D.n_ctas, P->shared_frags.ptr, (float*)P->shared_partials.ptr, s));
   else if ((st = SO.launch(P, A, tiles, s, SO.one_launch() ? kChainNext | (chained ? kChainPrev : 0) : 0)) != KV_OK)
     return st;
   KV_CUDA(launch_attend_join(P, A, (const AttJoin*)(base + o_joins), (int)joins.size(), join_rows,
-                             (const AttSrc*)(base + o_srcs), (const float*)base, scan_units, (const float*)P->partials.ptr, s));
+                             (const AttSrc*)(base + o_srcs), (const float*)base, scan_units, (const float*)P->shared_partials.ptr, s));
   return KV_OK;
 } catch (const std::bad_alloc&) {
   return fail(KV_ERR_OOM, "kv_attend_shared: host allocation failed");

@@ -201,28 +201,28 @@ extern "C" kv_status_t kv_decode_attn_scored(kv_pool_t* P, const void* q, const 
   kv_status_t st = refuse_capture("kv_decode_attn_scored", s);
   if (st != KV_OK) return st;
   if ((st = order_after_previous(P, s)) != KV_OK) return st;
-  if ((st = build_plan(P, req_ids, batch, hq, KV_DECODE_MMA, s)) != KV_OK) return st;
-  if (P->plan_rows > INT32_MAX)
+  if ((st = build_plan(P, P->plan, req_ids, batch, hq, KV_DECODE_MMA, s)) != KV_OK) return st;
+  if (P->plan.rows > INT32_MAX)
     return fail(KV_ERR_INVALID_ARG, "kv_decode_attn_scored: the batch holds more than 2^31 - 1 (page, kv head) pairs");
   if ((st = sync_positions(P, s)) != KV_OK) return st;
   const int g = hq / hkv;
-  const size_t ml_off = ((size_t)P->plan_rows * g * kPage * sizeof(float) + 255) & ~size_t(255);
-  if ((st = ensure(P->logits, ml_off + (size_t)P->n_units * g * sizeof(float2))) != KV_OK) return st;
-  if ((st = ensure(P->partials, (size_t)std::max(P->n_splits, 1) * g * (kHeadDim + 4) * sizeof(float))) != KV_OK)
+  const size_t ml_off = ((size_t)P->plan.rows * g * kPage * sizeof(float) + 255) & ~size_t(255);
+  if ((st = ensure(P->logits, ml_off + (size_t)P->plan.n_units * g * sizeof(float2))) != KV_OK) return st;
+  if ((st = ensure(P->partials, (size_t)std::max(P->plan.n_splits, 1) * g * (kHeadDim + 4) * sizeof(float))) != KV_OK)
     return st;
-  if ((st = ensure(P->frags, (size_t)std::max(P->n_units, 1) * decode_mma_frag_bytes())) != KV_OK) return st;
-  const uint8_t* base = (const uint8_t*)P->plan.ptr;
-  const Unit* du = (const Unit*)(base + P->plan_units_off);
-  const Split* dsp = (const Split*)(base + P->plan_splits_off);
+  if ((st = ensure(P->frags, (size_t)std::max(P->plan.n_units, 1) * decode_mma_frag_bytes())) != KV_OK) return st;
+  const uint8_t* base = (const uint8_t*)P->plan.buf.ptr;
+  const Unit* du = (const Unit*)(base + P->plan.units_off);
+  const Split* dsp = (const Split*)(base + P->plan.splits_off);
   float* logits = (float*)P->logits.ptr;
   float2* ml = (float2*)((uint8_t*)P->logits.ptr + ml_off);
   P->merge_event = nullptr;
-  P->fp_pending = FpLaunch{dsp + P->n_page_splits, (const int32_t*)(base + P->plan_fpw_off), P->n_fpw, P->n_page_splits};
-  KV_CUDA(launch_decode_mma_scored(P, q, hq, softmax_scale * 1.4426950408889634f, du, P->n_units, dsp,
-                                   (const int32_t*)(base + P->plan_cta_off), P->n_ctas, P->frags.ptr,
+  P->fp_pending = FpLaunch{dsp + P->plan.n_page_splits, (const int32_t*)(base + P->plan.fpw_off), P->plan.n_fpw, P->plan.n_page_splits};
+  KV_CUDA(launch_decode_mma_scored(P, q, hq, softmax_scale * 1.4426950408889634f, du, P->plan.n_units, dsp,
+                                   (const int32_t*)(base + P->plan.cta_off), P->plan.n_ctas, P->frags.ptr,
                                    (float*)P->partials.ptr, out, logits, ml, s));
   if (max_len > 0)
-    KV_CUDA(launch_score_add_any(g, P, du, P->n_units, max_len, ml, logits, decay, scores, score_stride, s));
+    KV_CUDA(launch_score_add_any(g, P, du, P->plan.n_units, max_len, ml, logits, decay, scores, score_stride, s));
   P->stat_req.assign(req_ids, req_ids + batch);
   P->stat_hq = hq;
   P->stat_skip_dead = true;   // as the scan does

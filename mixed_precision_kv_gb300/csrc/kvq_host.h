@@ -76,7 +76,7 @@ kv_status_t sync_positions(kv_pool* P, cudaStream_t s);
 kv_status_t append_tokens(kv_pool* P, const char* what, const void* k, const void* v, const int32_t* req_ids,
                           const uint8_t* bits, int64_t n_tok, void* stream);
 
-// The split plan of a decode over a batch, on the device (kept while it fits).
-kv_status_t build_plan(kv_pool* P, const int32_t* req_ids, int32_t batch, int32_t hq, int32_t impl, cudaStream_t s);
+// The split plan of a decode over a batch, on the device (kept in D while it fits).
+kv_status_t build_plan(kv_pool* P, DecodePlan& D, const int32_t* req_ids, int32_t batch, int32_t hq, int32_t impl, cudaStream_t s);
 
 }  // namespace kvq

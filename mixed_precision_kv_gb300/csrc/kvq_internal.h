@@ -290,6 +290,26 @@ struct DevBuf {
   size_t cap = 0;
 };
 
+// The split plan of a batch, on the device, kept while the batch is the same and its tables have grown by
+// little (build_plan).
+struct DecodePlan {
+  DevBuf buf;
+  std::vector<int32_t> req;
+  std::vector<int32_t> len;       // table lengths of req when the plan was built
+  std::vector<int32_t> nfp;       // full-precision list lengths when the plan was built
+  std::vector<uint64_t> ver;      // table shapes (Request::shape) when the plan was built
+  int32_t slack = 0;              // pages a table may grow before the plan is rebuilt
+  int32_t hq = 0;
+  int32_t impl = -1;              // -1: no plan stands
+  int32_t n_units = 0, n_splits = 0;
+  int32_t n_page_splits = 0;      // splits [0, n_page_splits) are page splits, the rest full-precision
+  int32_t n_fpw = 0;
+  int32_t n_ctas = 0;
+  size_t units_off = 0, splits_off = 0, cta_off = 0;
+  size_t fpw_off = 0;             // full-precision worker split ranges
+  int64_t rows = 0;               // rows of logits that the units reserve (table lengths and their slack)
+};
+
 }  // namespace kvq
 
 struct kv_pool {
@@ -319,7 +339,6 @@ struct kv_pool {
   // host scratch reused by every call (kept at capacity: fresh vectors cost
   // an allocation and first-touch page faults per call)
   std::vector<int32_t> scr_i4, scr_i2, scr_toks, scr_dtoks;
-  kvq::DevBuf plan;                   // decode plan (units, splits)
   kvq::DevBuf partials;               // decode split partials
   kvq::DevBuf frags;                  // per-unit q operands of the tensor-core scan
   kvq::DevBuf logits;                 // scored decode: logits of the batch's pages, then each row's (maximum, 1 / sum)
@@ -350,23 +369,13 @@ struct kv_pool {
   kvq::FreeIds free2, free3, free4, freef;
   std::vector<int32_t> call_slot;     // per request: index of its state inside the running append call (-1 outside)
   std::vector<int32_t> page_job;      // per page id: its append job inside the running call (-1 outside)
-  // decode plan cache
-  std::vector<int32_t> plan_req;
-  std::vector<int32_t> plan_len;      // table lengths of plan_req when the plan was built
-  std::vector<int32_t> plan_nfp;      // full-precision list lengths when the plan was built
-  std::vector<uint64_t> plan_ver;     // table shapes (Request::shape) when the plan was built
-  uint64_t shape_clock = 0;
-  int32_t plan_slack = 0;             // pages a table may grow before the plan is rebuilt
-  int32_t plan_hq = 0;
-  int32_t plan_impl = -1;
-  int32_t n_units = 0, n_splits = 0;
-  int32_t n_page_splits = 0;          // splits [0, n_page_splits) are page splits, the rest full-precision
-  size_t plan_fpw_off = 0;            // full-precision worker split ranges in the plan buffer
+  kvq::DecodePlan plan;               // of the decode calls
+  // decode steps over shared prefixes: a plan, partials and q operands of their own, so that a captured decode and
+  // what kv_last_decode_stats says stay as they are
+  kvq::DecodePlan shared_plan;
+  kvq::DevBuf shared_partials, shared_frags;
   kvq::FpLaunch fp_pending;           // launched by the next launch_decode_* between scan and merge
-  int32_t n_fpw = 0;
-  size_t plan_units_off = 0, plan_splits_off = 0, plan_cta_off = 0;
-  int64_t plan_rows = 0;              // rows of logits that the plan's units reserve (table lengths and their slack)
-  int32_t n_ctas = 0;
+  uint64_t shape_clock = 0;
   std::vector<int32_t> stat_req;      // request ids of the last decode (for kv_last_decode_stats)
   int32_t stat_hq = 0;
   bool stat_skip_dead = false;        // the last decode skipped pages with no live slot for a head

@@ -492,7 +492,10 @@ kv_status_t kv_pool_destroy(kv_pool_t* P) {
   cudaFree(P->d_ntab);
   cudaFree(P->d_status);
   cudaFree(P->upload.ptr);
-  cudaFree(P->plan.ptr);
+  cudaFree(P->plan.buf.ptr);
+  cudaFree(P->shared_plan.buf.ptr);
+  cudaFree(P->shared_partials.ptr);
+  cudaFree(P->shared_frags.ptr);
   cudaFree(P->partials.ptr);
   cudaFree(P->frags.ptr);
   cudaFree(P->gplan.ptr);
@@ -1451,7 +1454,7 @@ kv_status_t kv_evict_slots_head(kv_pool_t* P, const int32_t* req_ids, const int6
     hdead_set(P, id, kv_heads[i], P->hdead[(size_t)id * hkv + kv_heads[i]] | (1u << (l & 31u)), upd);
   }
   if (upd.empty()) return KV_OK;
-  P->plan_impl = -1;   // page costs per head changed: plan again at the next decode
+  P->plan.impl = P->shared_plan.impl = -1;   // page costs per head changed: plan again at the next decode
   hdead_final(P, upd);
   Upload u;
   const size_t o = u.add(upd.data(), upd.size() * sizeof(TableUpd));
@@ -1717,8 +1720,8 @@ kv_status_t kv_export_request(kv_pool_t* P, int32_t r, int32_t* ids, uint8_t* is
 // split per unit.  A page costs what the chosen scan kernel spends on a page
 // of its precision (PageCost), so INT2 and INT4 pages are weighed fairly.
 
-kv_status_t kvq::build_plan(kv_pool* P, const int32_t* req_ids, int32_t batch, int32_t hq, int32_t impl,
-                       cudaStream_t s) {
+kv_status_t kvq::build_plan(kv_pool* P, DecodePlan& D, const int32_t* req_ids, int32_t batch, int32_t hq, int32_t impl,
+                            cudaStream_t s) {
   const int hkv = P->cfg.num_kv_heads, g = hq / hkv;
   // A plan stays valid while the batch is the same and no table has shrunk:
   // splits are table index ranges and each unit's last one is open-ended.
@@ -1728,15 +1731,15 @@ kv_status_t kvq::build_plan(kv_pool* P, const int32_t* req_ids, int32_t batch, i
   // Full-precision splits follow the same rule: a unit's last one is
   // open-ended, and the plan is rebuilt once a list has grown by 64 tokens, has
   // shrunk, or was empty.
-  bool same = P->plan_impl == impl && P->plan_hq == hq && (int32_t)P->plan_req.size() == batch;
+  bool same = D.impl == impl && D.hq == hq && (int32_t)D.req.size() == batch;
   for (int32_t b = 0; same && b < batch; ++b) {
-    const int32_t len = (int32_t)P->reqs[req_ids[b]].table.size(), len0 = P->plan_len[b];
-    same = P->plan_req[b] == req_ids[b] && len >= len0 && len - len0 <= P->plan_slack && (len0 > 0 || len == 0);
-    const int32_t nf = P->n_fp.empty() ? 0 : P->n_fp[req_ids[b]], nf0 = P->plan_nfp[b];
+    const int32_t len = (int32_t)P->reqs[req_ids[b]].table.size(), len0 = D.len[b];
+    same = D.req[b] == req_ids[b] && len >= len0 && len - len0 <= D.slack && (len0 > 0 || len == 0);
+    const int32_t nf = P->n_fp.empty() ? 0 : P->n_fp[req_ids[b]], nf0 = D.nfp[b];
     same = same && nf >= nf0 && nf - nf0 < 2 * kFpMinTokens && (nf0 > 0 || nf == 0);
     // with per-head exclusion, splits may leave out positions found dead: an
     // entry erased or moved (not an append at the end) plans again
-    same = same && (P->hdead.empty() || P->plan_ver[b] == P->reqs[req_ids[b]].shape);
+    same = same && (P->hdead.empty() || D.ver[b] == P->reqs[req_ids[b]].shape);
   }
   if (same) return KV_OK;
 
@@ -1748,12 +1751,12 @@ kv_status_t kvq::build_plan(kv_pool* P, const int32_t* req_ids, int32_t batch, i
   int64_t total_pages = 0;
   for (int32_t b = 0; b < batch; ++b) total_pages += (int64_t)P->reqs[req_ids[b]].table.size() * hkv;
   // growth a tail worker absorbs before the plan is rebuilt: 5% of a worker's share
-  P->plan_slack = (int32_t)std::max<int64_t>(1, total_pages / std::max<int64_t>(1, hp.n_ctas()) / 20);
+  D.slack = (int32_t)std::max<int64_t>(1, total_pages / std::max<int64_t>(1, hp.n_ctas()) / 20);
   // rows of logits (scored decode): each unit reserves its table and the growth the plan allows
-  P->plan_rows = 0;
+  D.rows = 0;
   for (Unit& u : hp.units) {
-    u.pad = (int32_t)P->plan_rows;
-    P->plan_rows += (int64_t)P->reqs[u.req].table.size() + P->plan_slack;
+    u.pad = (int32_t)D.rows;
+    D.rows += (int64_t)P->reqs[u.req].table.size() + D.slack;
   }
   for (int32_t x = 0; x < hp.n_page_splits; ++x) hp.splits[(size_t)x].pad[0] = hp.units[(size_t)hp.splits[(size_t)x].unit].pad;
   Upload up;
@@ -1761,28 +1764,28 @@ kv_status_t kvq::build_plan(kv_pool* P, const int32_t* req_ids, int32_t batch, i
   const size_t os = up.add(hp.splits.data(), hp.splits.size() * sizeof(Split));
   const size_t oc = up.add(hp.cta_split.data(), hp.cta_split.size() * sizeof(int32_t));
   const size_t of = up.add(hp.fp_wsplit.data(), hp.fp_wsplit.size() * sizeof(int32_t));
-  P->plan_impl = -1;   // no plan stands until the new one is on the device
-  kv_status_t st = ensure(P->plan, up.size);
+  D.impl = -1;   // no plan stands until the new one is on the device
+  kv_status_t st = ensure(D.buf, up.size);
   if (st != KV_OK) return st;
-  if ((st = h2d(P, P->plan.ptr, up, s)) != KV_OK) return st;
-  P->plan_units_off = ou;
-  P->plan_splits_off = os;
-  P->plan_cta_off = oc;
-  P->n_units = (int32_t)hp.units.size();
-  P->n_splits = (int32_t)hp.splits.size();
-  P->n_page_splits = hp.n_page_splits;
-  P->plan_fpw_off = of;
-  P->n_fpw = (int32_t)hp.fp_wsplit.size() - 1;
-  P->n_ctas = (int32_t)hp.n_ctas();
-  P->plan_req.assign(req_ids, req_ids + batch);
-  P->plan_len.resize(batch);
-  P->plan_nfp.resize(batch);
-  P->plan_ver.resize(batch);
-  for (int32_t b = 0; b < batch; ++b) P->plan_ver[b] = P->reqs[req_ids[b]].shape;
-  for (int32_t b = 0; b < batch; ++b) P->plan_nfp[b] = P->n_fp.empty() ? 0 : P->n_fp[req_ids[b]];
-  for (int32_t b = 0; b < batch; ++b) P->plan_len[b] = (int32_t)P->reqs[req_ids[b]].table.size();
-  P->plan_hq = hq;
-  P->plan_impl = impl;
+  if ((st = h2d(P, D.buf.ptr, up, s)) != KV_OK) return st;
+  D.units_off = ou;
+  D.splits_off = os;
+  D.cta_off = oc;
+  D.n_units = (int32_t)hp.units.size();
+  D.n_splits = (int32_t)hp.splits.size();
+  D.n_page_splits = hp.n_page_splits;
+  D.fpw_off = of;
+  D.n_fpw = (int32_t)hp.fp_wsplit.size() - 1;
+  D.n_ctas = (int32_t)hp.n_ctas();
+  D.req.assign(req_ids, req_ids + batch);
+  D.len.resize(batch);
+  D.nfp.resize(batch);
+  D.ver.resize(batch);
+  for (int32_t b = 0; b < batch; ++b) D.ver[b] = P->reqs[req_ids[b]].shape;
+  for (int32_t b = 0; b < batch; ++b) D.nfp[b] = P->n_fp.empty() ? 0 : P->n_fp[req_ids[b]];
+  for (int32_t b = 0; b < batch; ++b) D.len[b] = (int32_t)P->reqs[req_ids[b]].table.size();
+  D.hq = hq;
+  D.impl = impl;
   return KV_OK;
 }
 
@@ -1803,28 +1806,28 @@ kv_status_t kv_decode_attn(kv_pool_t* P, const void* q, const int32_t* req_ids, 
   cudaStream_t s = (cudaStream_t)stream;
   kv_status_t st = order_after_previous(P, s);
   if (st != KV_OK) return st;
-  if ((st = build_plan(P, req_ids, batch, hq, impl, s)) != KV_OK) return st;
+  if ((st = build_plan(P, P->plan, req_ids, batch, hq, impl, s)) != KV_OK) return st;
   const int g = hq / hkv;
-  if ((st = ensure(P->partials, (size_t)std::max(P->n_splits, 1) * g * (kHeadDim + 4) * sizeof(float))) != KV_OK)
+  if ((st = ensure(P->partials, (size_t)std::max(P->plan.n_splits, 1) * g * (kHeadDim + 4) * sizeof(float))) != KV_OK)
     return st;
-  if (impl == KV_DECODE_MMA && (st = ensure(P->frags, (size_t)std::max(P->n_units, 1) * decode_mma_frag_bytes())) != KV_OK)
+  if (impl == KV_DECODE_MMA && (st = ensure(P->frags, (size_t)std::max(P->plan.n_units, 1) * decode_mma_frag_bytes())) != KV_OK)
     return st;
-  const uint8_t* base = (const uint8_t*)P->plan.ptr;
+  const uint8_t* base = (const uint8_t*)P->plan.buf.ptr;
   const float scale_log2 = softmax_scale * 1.4426950408889634f;
-  const Unit* du = (const Unit*)(base + P->plan_units_off);
-  const Split* dsp = (const Split*)(base + P->plan_splits_off);
-  const int32_t* dct = (const int32_t*)(base + P->plan_cta_off);
+  const Unit* du = (const Unit*)(base + P->plan.units_off);
+  const Split* dsp = (const Split*)(base + P->plan.splits_off);
+  const int32_t* dct = (const int32_t*)(base + P->plan.cta_off);
   const bool rec = P->timing && (P->timing_seen++ % P->timing_every) == 0;
   cudaEvent_t* tv = rec ? &P->tev[3 * (size_t)(P->timed_calls % kTimingRing)] : nullptr;
   if (tv) KV_CUDA(cudaEventRecord(tv[0], s));
   P->merge_event = tv ? tv[1] : nullptr;
-  P->fp_pending = FpLaunch{dsp + P->n_page_splits, (const int32_t*)(base + P->plan_fpw_off), P->n_fpw,
-                            P->n_page_splits};
+  P->fp_pending = FpLaunch{dsp + P->plan.n_page_splits, (const int32_t*)(base + P->plan.fpw_off), P->plan.n_fpw,
+                            P->plan.n_page_splits};
   if (impl == KV_DECODE_MMA)
-    KV_CUDA(launch_decode_mma(P, q, hq, scale_log2, du, P->n_units, dsp, dct, P->n_ctas, P->frags.ptr,
+    KV_CUDA(launch_decode_mma(P, q, hq, scale_log2, du, P->plan.n_units, dsp, dct, P->plan.n_ctas, P->frags.ptr,
                               (float*)P->partials.ptr, out, s));
   else
-    KV_CUDA(launch_decode_simt(P, q, hq, scale_log2, du, P->n_units, dsp, dct, P->n_ctas, (float*)P->partials.ptr, out, s));
+    KV_CUDA(launch_decode_simt(P, q, hq, scale_log2, du, P->plan.n_units, dsp, dct, P->plan.n_ctas, (float*)P->partials.ptr, out, s));
   if (tv) {
     KV_CUDA(cudaEventRecord(tv[2], s));
     ++P->timed_calls;
@@ -1901,7 +1904,7 @@ kv_status_t kv_last_decode_stats(kv_pool_t* P, int64_t* kv_bytes, int32_t* n_spl
     if (!P->n_fp.empty()) bytes += (int64_t)P->n_fp[r] * hkv * kHeadDim * 2 * 2;   // full-precision K and V
   }
   if (kv_bytes) *kv_bytes = bytes;
-  if (n_splits) *n_splits = P->n_splits;
+  if (n_splits) *n_splits = P->plan.n_splits;
   if (n_pages) *n_pages = pages * hkv;
   return KV_OK;
 }

@@ -55,3 +55,30 @@ def test_decode_step_large_logits(kvq):
             # its value, rounded to binary16 (2^-11) inside and to bf16 (2^-8) once
             assert np.all(np.abs(out[b, j].double().cpu().numpy() - o) <= np.abs(o) * (2.0 ** -8 + 2 * U) + 1e-30)
     P.pool.destroy()
+
+
+def test_decode_step_between_captured_decodes(kvq):
+    """A captured decode and the statistics of the last decode stay what they are over decode steps of larger and
+    smaller batches with shared prefixes, and the steps over decodes."""
+    P = step_pool(kvq, seed=3)
+    pool, n = P.pool, len(P.ids) - 1
+    q, out = rand((2, 16, 128), P.gen), torch.empty(2, 16, 128, device="cuda")
+    steps = [(rand((m, 16, 128), P.gen), P.ids[1:m + 1], [P.ids[0]] * m) for m in (n, n - 3)]
+    first = [pool.attend_shared(x, ids, pre, [1] * len(ids), SCALE) for x, ids, pre in steps]
+    want = pool.decode(q, P.ids[1:3], SCALE).clone()
+    stats = pool.last_decode_stats()
+    torch.cuda.synchronize()
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=s):
+        pool.decode(q, P.ids[1:3], SCALE, out=out)
+    for _ in range(2):
+        for (x, ids, pre), y in zip(steps, first):
+            assert torch.equal(pool.attend_shared(x, ids, pre, [1] * len(ids), SCALE), y)
+            assert pool.last_decode_stats() == stats
+            out.zero_()
+            torch.cuda.synchronize()
+            g.replay()
+            assert torch.equal(out, want)
+    assert torch.equal(pool.decode(q, P.ids[1:3], SCALE), want)
+    pool.sync()
+    pool.destroy()
