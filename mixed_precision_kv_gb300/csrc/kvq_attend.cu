@@ -256,13 +256,27 @@ __device__ __noinline__ PlainRow plain_row(const AttArgs& A, const uint16_t* q, 
   for (int o = 16; o; o >>= 1) mx_q = fmaxf(mx_q, __shfl_xor_sync(0xFFFFFFFFu, mx_q, o));
   const bool large = mx_q > 0x1p60f;
   const float down = large ? 0x1p-64f : 1.0f, scale = large ? A.scale_log2 * 0x1p64f : A.scale_log2;
-  for (int p = 0; p < n_pages; ++p) {
-    const Entry e = A.table[(size_t)req * A.max_pages + p];
-    const uint32_t live = A.hdead ? e.live & ~A.hdead[(size_t)e.id * A.hkv + kvh] : e.live;
-    if (live == 0u) continue;
+  // the next page with a live slot: the entries of 32 pages at a time.  A row that is not a number stays one.
+  int p0 = -32;
+  Entry e{0, 0u};        // lane's entry, its slots that are live for the head
+  uint32_t todo = 0u;    // pages of the 32 that are left
+  while (!wild) {
+    if (todo == 0u) {
+      p0 += 32;
+      if (p0 >= n_pages) break;
+      e = Entry{0, 0u};
+      if (p0 + lane < n_pages) e = A.table[(size_t)req * A.max_pages + p0 + lane];
+      if (A.hdead && e.live) e.live &= ~A.hdead[(size_t)e.id * A.hkv + kvh];
+      todo = __ballot_sync(0xFFFFFFFFu, e.live != 0u);
+      continue;
+    }
+    const int at = __ffs(todo) - 1;
+    todo &= todo - 1u;
+    const int32_t id = __shfl_sync(0xFFFFFFFFu, e.id, at);
+    const uint32_t live = __shfl_sync(0xFFFFFFFFu, e.live, at);
     seen = true;
     const uint8_t* b;
-    const int cls = att_page(A, e.id, kvh, b);
+    const int cls = att_page(A, id, kvh, b);
     const bool on = (live >> lane) & 1u;
     float s = 0.0f;
     for (int c = 0; on && c < kHeadDim; ++c) s = fmaf(__uint_as_float((uint32_t)q[c] << 16) * down, k_value(b, cls, lane, c), s);
