@@ -392,7 +392,12 @@ KVQ_API kv_status_t kv_attend(kv_pool_t* pool, const void* q, const void* k, con
  *   k, v        NULL (both): rows see the caches only, e.g. one token per request
  *               (n_new 1) that has been appended: the decode step of such a batch
  * The other arguments and the rules are kv_attend's (out is bf16); at most 2^20
- * new tokens over one prefix; always the tensor-core kernels.  The plan and the
+ * new tokens over one prefix; always the tensor-core kernels.  Workspace beyond
+ * kv_attend's: partial sums of every row of q (token and q head) with a prefix,
+ * 528 bytes for the prefix and 528 for the request's own keys, more where the
+ * work on a block of rows is shared out: 2.2 GB for 64 x 512 new tokens with 64
+ * q heads.  It is not bounded by passes; KV_ERR_OOM without memory for it, and
+ * calls with fewer new tokens need less.  The plan and the
  * buffers are the call's own: a captured kv_decode_attn and kv_last_decode_stats
  * stay as they are. */
 KVQ_API kv_status_t kv_attend_shared(kv_pool_t* pool, const void* q, const void* k, const void* v, const uint64_t* tree,

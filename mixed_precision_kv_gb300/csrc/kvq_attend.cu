@@ -913,7 +913,10 @@ extern "C" kv_status_t kv_attend_shared(kv_pool_t* P, const void* q, const void*
   for (int32_t b = 0; b < n_req; ++b)
     for (int h = 0; h < hkv && n_new[b] > 0; ++h) {
       AttUnit w = attend_unit(P, req_ids[b], h, n_new[b], k != nullptr, tok0[(size_t)b]);
-      w.joined = !pre.empty();   // (those without a prefix too: one kernel then ends the call)
+      // (few rows without a prefix too, so that one kernel ends the call; more of them would be partials of 528 bytes a
+      // row, written and read again: 4096 tokens x 64 q heads beside one token with a prefix took 561 us
+      // that way, 391 without)
+      w.joined = group_of[(size_t)b] >= 0 || (!pre.empty() && n_new[b] * g <= kFewRows);
       own.push_back(w);
     }
   // One launch for both kinds where their rows go by blocks of one size, or where there is so little

@@ -137,3 +137,44 @@ def test_decode_step_plain_rows_end(kvq):
     took = least_us(lambda: step(q))
     assert took < 2.5 * usual, (usual, took)       # an entry at a time: 4.7 times
     pool.destroy()
+
+
+def test_long_chunk_without_a_prefix(kvq):
+    """A long chunk of a request without a prefix beside one token of a request with one: no partial sums of its rows."""
+    P = Pool(kvq, 8, [mixed(256, i) for i in range(3)], seed=6)
+    pool, n, hq = P.pool, 4096, 64
+    q, k, v = (rand((n + 1, h, 128), P.gen) for h in (hq, 8, 8))
+    out = torch.empty_like(q)
+    want = pool.attend(q, P.ids[1:], [n, 1], SCALE, k, v)
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    pool.attend_shared(q, P.ids[1:], [-1, P.ids[0]], [n, 1], SCALE, k, v, out=out)
+    pool.sync()
+    grown = free - torch.cuda.mem_get_info()[0]
+    assert grown < 32 << 20, grown     # the chunk's rows would be 138 MB
+    # the chunk's blocks may be cut elsewhere than in kv_attend: other pieces of the same fp32 sums, each result rounded
+    # to bf16, by at most 2^-9 of itself
+    a, b = out[:n].double(), want[:n].double()
+    assert float((a - b).norm()) <= 1.1 * 2 * 2.0 ** -9 * float(b.norm())
+    P.pool.destroy()
+
+
+@pytest.mark.parametrize("n_new,prefix", [
+    ([1, 33, 97, 2], [-1, -1, -1, 0]), ([33, 1, 33], [-1, 0, 0]), ([40, 2, 40, 1], [-1, -1, 0, 1]),
+    ([300, 1, 1, 260], [-1, 0, -1, 0]), ([1, 100, 3], [1, -1, -1])])
+@pytest.mark.parametrize("with_kv", [True, False])
+def test_rows_with_and_without_a_prefix(kvq, n_new, prefix, with_kv):
+    """Few, middle and many rows of requests without a prefix beside few and many with one."""
+    P = Pool(kvq, 1, [mixed(300, 1), mixed(130, 2)] + [mixed(40 * i, i) for i in range(len(n_new))], seed=len(n_new))
+    check(P, range(2, 2 + len(n_new)), prefix, n_new, 4, with_kv, rows=[0, 1, 32, 39, 96, 99, 259, 299])
+    P.pool.destroy()
+
+
+def test_a_chunk_among_single_tokens(kvq):
+    """One long chunk and many single tokens over one prefix, in one call."""
+    n = 40
+    P = Pool(kvq, 2, [mixed(500, 1)] + [mixed(20 + i, i) for i in range(n)], seed=7)
+    n_new = [1] * n
+    n_new[17] = 700
+    check(P, range(1, n + 1), [0] * n, n_new, 8, rows=[0, 1, 350, 699])
+    P.pool.destroy()
