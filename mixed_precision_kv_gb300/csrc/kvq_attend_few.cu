@@ -135,11 +135,12 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-template <int R>
+// kShared: the call is kv_attend_shared's (units' tokens by a map, launches in a chain)
+template <int R, bool kShared>
 __global__ void __launch_bounds__(kThreads<R>, 1) attend_few_kernel(
     AttArgs A, const AttUnit* __restrict__ units, const AttItem* __restrict__ items, const int32_t* __restrict__ cta_item,
     float* __restrict__ part, uint32_t first_spins, int chain) {
-  if (chain & kChainNext) asm volatile("griddepcontrol.launch_dependents;");
+  if (kShared && (chain & kChainNext)) asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   FewSmem<R>& S = *reinterpret_cast<FewSmem<R>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(kThreads<R>, 1) attend_few_kernel(
         constexpr int kPer = R == 16 ? 16 : 256 / R, kRuns = 16 / kPer;
         const int n = tid / kPer, sub = tid % kPer;
         const bool valid = n < T.rows;
-        const uint16_t* qr = A.q + rows.at(A, u, I.row0 + (valid ? n : 0));
+        const uint16_t* qr = A.q + rows.q_at<kShared>(A, u, I.row0 + (valid ? n : 0));
         uint4 w[kRuns];
 #pragma unroll
         for (int y = 0; y < kRuns; ++y) w[y] = load8(qr + 8 * (sub + kPer * y), qal);
@@ -682,17 +683,17 @@ __global__ void __launch_bounds__(kThreads<R>, 1) attend_few_kernel(
     tm_fence_after();
     tm_free(tmem, 512);
   }
-  if (chain & kChainPrev) asm volatile("griddepcontrol.wait;" ::: "memory");   // what waits for this grid waits for that one too
+  if (kShared && (chain & kChainPrev)) asm volatile("griddepcontrol.wait;" ::: "memory");   // what waits for this grid waits for that one too
 }
 
-template <int R>
+template <int R, bool kShared>
 cudaError_t launch_r(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const AttItem* d_items,
                      const int32_t* d_cta_item, int n_ctas, float* d_part, cudaStream_t s, int chain) {
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!(attr_set.load() >> dev & 1u)) {
-    const cudaError_t e = cudaFuncSetAttribute(attend_few_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(attend_few_kernel<R, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)sizeof(FewSmem<R>));
     if (e != cudaSuccess) return e;
     attr_set.fetch_or(uint64_t(1) << dev);
@@ -700,11 +701,18 @@ cudaError_t launch_r(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const
   ++P->launches;
   const uint32_t spins = P->first_wait_spins < 0 ? kAttSpin : (uint32_t)P->first_wait_spins;
   if (chain & kChainPrev)
-    return launch_pdl(attend_few_kernel<R>, dim3((unsigned)n_ctas), dim3(kThreads<R>), sizeof(FewSmem<R>), s, A, d_units,
+    return launch_pdl(attend_few_kernel<R, kShared>, dim3((unsigned)n_ctas), dim3(kThreads<R>), sizeof(FewSmem<R>), s, A, d_units,
                       d_items, d_cta_item, d_part, spins, chain);
-  attend_few_kernel<R><<<(unsigned)n_ctas, kThreads<R>, sizeof(FewSmem<R>), s>>>(A, d_units, d_items, d_cta_item, d_part,
-                                                                                 spins, chain);
+  attend_few_kernel<R, kShared><<<(unsigned)n_ctas, kThreads<R>, sizeof(FewSmem<R>), s>>>(A, d_units, d_items, d_cta_item,
+                                                                                          d_part, spins, chain);
   return cudaGetLastError();
+}
+
+template <int R>
+cudaError_t launch_few(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const AttItem* d_items,
+                       const int32_t* d_cta_item, int n_ctas, float* d_part, cudaStream_t s, int chain) {
+  return A.tok_map ? launch_r<R, true>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s, chain)
+                   : launch_r<R, false>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s, 0);
 }
 
 }  // namespace
@@ -713,9 +721,9 @@ cudaError_t launch_attend_few(kv_pool* P, int rows, const AttArgs& A, const AttU
                               const int32_t* d_cta_item, int n_ctas, float* d_part, cudaStream_t s, int chain) {
   if (n_ctas <= 0) return cudaSuccess;
   switch (rows) {
-    case 16: return launch_r<16>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s, chain);
-    case 32: return launch_r<32>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s, chain);
-    case 64: return launch_r<64>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s, chain);
+    case 16: return launch_few<16>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s, chain);
+    case 32: return launch_few<32>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s, chain);
+    case 64: return launch_few<64>(P, A, d_units, d_items, d_cta_item, n_ctas, d_part, s, chain);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -404,6 +404,15 @@ struct RowMap {
   __device__ __forceinline__ int token(int row) const { return g == 1 ? row : (int)__umulhi((uint32_t)row, magic); }
   __device__ __forceinline__ size_t at(const AttArgs& A, const AttUnit& u, int row) const {
     const int t = token(row);
+    return ((size_t)(u.tok0 + t) * A.hq + (size_t)(u.kvh * g + row - t * g)) * kHeadDim;
+  }
+  // Of q, where the unit's tokens may lie apart (kShared; their results are partials, so only q is read by the
+  // map).  A form of its own: kv_attend's kernels lose 1 % (many
+  // rows: 1689 -> 1708 us) to 11 % (few: 284 -> 316) to the choice made in the kernel.
+  template <bool kShared>
+  __device__ __forceinline__ size_t q_at(const AttArgs& A, const AttUnit& u, int row) const {
+    if constexpr (!kShared) return at(A, u, row);
+    const int t = token(row);
     const int64_t tok = u.map < 0 ? u.tok0 + t : (int64_t)__ldg(A.tok_map + u.map + t);
     return ((size_t)tok * A.hq + (size_t)(u.kvh * g + row - t * g)) * kHeadDim;
   }

@@ -255,6 +255,8 @@ __global__ void __launch_bounds__(256) attend_tiles_kernel(AttArgs A, const AttU
   if (bad) atomicOr(A.status, kStatusRange);
 }
 
+// kShared: the call is kv_attend_shared's (units' tokens by a map)
+template <bool kShared>
 __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
     AttArgs A, const AttUnit* __restrict__ units, const AttItem* __restrict__ items, const int32_t* __restrict__ cta_item,
     const uint8_t* __restrict__ tiles, const uint32_t* __restrict__ live, float* __restrict__ part,
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(
           uint4 w[8];
 #pragma unroll
           for (int y = 0; y < 8; ++y)
-            w[y] = load8(A.q + rows.at(A, u, I.row0 + min(w32 + 2 * (y0 + y) + half, T.rows - 1)) + 8 * c, qal);
+            w[y] = load8(A.q + rows.q_at<kShared>(A, u, I.row0 + min(w32 + 2 * (y0 + y) + half, T.rows - 1)) + 8 * c, qal);
 #pragma unroll
           for (int y = 0; y < 8; ++y) {
             const uint32_t wd[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
@@ -617,24 +619,32 @@ cudaError_t launch_attend_tiles(kv_pool* P, const AttArgs& A, const AttUnit* d_u
   return cudaGetLastError();
 }
 
-cudaError_t launch_attend_wide(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const AttItem* d_items,
+template <bool kShared>
+static cudaError_t launch_wide(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const AttItem* d_items,
                                const int32_t* d_cta_item, int n_ctas, const void* d_tiles, const uint32_t* d_live,
                                float* d_part, cudaStream_t s) {
-  if (n_ctas <= 0) return cudaSuccess;
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!(attr_set.load() >> dev & 1u)) {
-    const cudaError_t e = cudaFuncSetAttribute(attend_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(attend_wide_kernel<kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)sizeof(WideSmem));
     if (e != cudaSuccess) return e;
     attr_set.fetch_or(uint64_t(1) << dev);
   }
   ++P->launches;
-  attend_wide_kernel<<<(unsigned)n_ctas, kThreads, sizeof(WideSmem), s>>>(
+  attend_wide_kernel<kShared><<<(unsigned)n_ctas, kThreads, sizeof(WideSmem), s>>>(
       A, d_units, d_items, d_cta_item, (const uint8_t*)d_tiles, d_live, d_part,
       P->first_wait_spins < 0 ? kAttSpin : (uint32_t)P->first_wait_spins);
   return cudaGetLastError();
+}
+
+cudaError_t launch_attend_wide(kv_pool* P, const AttArgs& A, const AttUnit* d_units, const AttItem* d_items,
+                               const int32_t* d_cta_item, int n_ctas, const void* d_tiles, const uint32_t* d_live,
+                               float* d_part, cudaStream_t s) {
+  if (n_ctas <= 0) return cudaSuccess;
+  return A.tok_map ? launch_wide<true>(P, A, d_units, d_items, d_cta_item, n_ctas, d_tiles, d_live, d_part, s)
+                   : launch_wide<false>(P, A, d_units, d_items, d_cta_item, n_ctas, d_tiles, d_live, d_part, s);
 }
 
 }  // namespace kvq
