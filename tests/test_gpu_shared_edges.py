@@ -178,3 +178,65 @@ def test_a_chunk_among_single_tokens(kvq):
     n_new[17] = 700
     check(P, range(1, n + 1), [0] * n, n_new, 8, rows=[0, 1, 350, 699])
     P.pool.destroy()
+
+
+def test_decode_step_expired_wait(kvq):
+    """A first wait of the own caches' scan that gives up is reported once, and the pool goes on."""
+    P = step_pool(kvq, seed=8)
+    n = len(P.ids) - 1
+    q = rand((n, 16, 128), P.gen)
+    step = lambda: P.pool.attend_shared(q, P.ids[1:], [P.ids[0]] * n, [1] * n, SCALE)
+    good = step()
+    P.pool.sync()
+    P.pool.set_wait_limit(0)
+    step()
+    with pytest.raises(kvq.KVError) as e:
+        P.pool.sync()
+    assert e.value.status == kvq.KV_ERR_DEVICE_TIMEOUT
+    P.pool.sync()
+    P.pool.set_wait_limit(-1)
+    assert torch.equal(step(), good)
+    P.pool.sync()
+    P.pool.destroy()
+
+
+def test_the_same_call_again(kvq):
+    """Equal bits from equal calls, whatever ran in between: a decode step, drafts, chunks."""
+    P = step_pool(kvq, seed=9)
+    n = len(P.ids) - 1
+    calls = []
+    for n_new, kv in (([1] * n, False), ([1 + i % 5 for i in range(n)], True), ([150, 2] + [0] * (n - 3) + [40], True)):
+        q = rand((sum(n_new), 16, 128), P.gen)
+        k, v = (rand((sum(n_new), 8, 128), P.gen) for _ in range(2)) if kv else (None, None)
+        prefix = [P.ids[0] if i % 4 else -1 for i in range(n)]
+        calls.append(lambda q=q, k=k, v=v, n_new=n_new, p=prefix: P.pool.attend_shared(q, P.ids[1:], p, n_new, SCALE, k, v))
+    first = [f() for f in calls]
+    for _ in range(3):
+        for f, y in zip(calls, first):
+            assert torch.equal(f(), y)
+    P.pool.sync()
+    P.pool.destroy()
+
+
+def test_decode_right_after_its_rotation(kvq):
+    """q rotated by the kernel before the decode (or the step over a prefix) on the same stream."""
+    P = step_pool(kvq, seed=10)
+    pool, n = P.pool, len(P.ids) - 1
+    rope = kvq.Rope(torch.randn(64, 128, generator=P.gen, device="cuda"))
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    x = [rand((n, 16, 128), P.gen) for _ in range(2)]
+    turned = [pool.rotate(y, rope, pos) for y in x]
+    torch.cuda.synchronize()
+    pre = [P.ids[0]] * n
+    want = [(pool.decode(y, P.ids[1:], SCALE).clone(), pool.attend_shared(y, P.ids[1:], pre, [1] * n, SCALE)) for y in turned]
+    torch.cuda.synchronize()
+    q, got = torch.empty_like(x[0]), []
+    for i in range(40):
+        pool.rotate(x[i & 1], rope, pos, out=q)
+        a = pool.decode(q, P.ids[1:], SCALE)
+        pool.rotate(x[i & 1], rope, pos, out=q)
+        got.append((a, pool.attend_shared(q, P.ids[1:], pre, [1] * n, SCALE)))
+    for i, y in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(y, want[i & 1])), i
+    pool.sync()
+    pool.destroy()
