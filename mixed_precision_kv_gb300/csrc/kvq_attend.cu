@@ -913,9 +913,9 @@ extern "C" kv_status_t kv_attend_shared(kv_pool_t* P, const void* q, const void*
   for (int32_t b = 0; b < n_req; ++b)
     for (int h = 0; h < hkv && n_new[b] > 0; ++h) {
       AttUnit w = attend_unit(P, req_ids[b], h, n_new[b], k != nullptr, tok0[(size_t)b]);
-      // (few rows without a prefix too, so that one kernel ends the call; more of them would be partials of 528 bytes a
-      // row, written and read again: 4096 tokens x 64 q heads beside one token with a prefix took 561 us
-      // that way, 391 without)
+      // (few rows without a prefix too, so that one kernel ends the call; more of them would be partials of 528 bytes
+      // a row, written and read again: 4096 tokens x 64 q heads beside one token with a prefix took 561 us that way,
+      // 391 without)
       w.joined = group_of[(size_t)b] >= 0 || (!pre.empty() && n_new[b] * g <= kFewRows);
       own.push_back(w);
     }
@@ -1020,7 +1020,8 @@ extern "C" kv_status_t kv_attend_shared(kv_pool_t* P, const void* q, const void*
   if ((st = h2d(P, P->attend.ptr, u, s)) != KV_OK) return st;
   uint8_t* base = (uint8_t*)P->attend.ptr;
   A.tok_map = (const int32_t*)(base + o_map);
-  // the second launch starts as CTAs of the first leave, the joins as those of the second do
+  // The second attention launch starts as CTAs of the first leave, the joins as those of the second do.  A scan of
+  // the own caches starts when the first launch is done: only its q operands are prepared meanwhile.
   const bool chained = SP.one_launch() && (scan || SO.one_launch());
   if ((st = SP.launch(P, A, tiles, s, chained ? kChainNext : 0)) != KV_OK) return st;
   const uint8_t* plan = (const uint8_t*)D.buf.ptr;

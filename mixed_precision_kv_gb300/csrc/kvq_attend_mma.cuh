@@ -407,8 +407,8 @@ struct RowMap {
     return ((size_t)(u.tok0 + t) * A.hq + (size_t)(u.kvh * g + row - t * g)) * kHeadDim;
   }
   // Of q, where the unit's tokens may lie apart (kShared; their results are partials, so only q is read by the
-  // map).  A form of its own: kv_attend's kernels lose 1 % (many
-  // rows: 1689 -> 1708 us) to 11 % (few: 284 -> 316) to the choice made in the kernel.
+  // map).  A form of its own: kv_attend's kernels lose 1 % (many rows: 1689 -> 1708 us) to 11 % (few: 284 -> 316) to
+  // the choice made in the kernel.
   template <bool kShared>
   __device__ __forceinline__ size_t q_at(const AttArgs& A, const AttUnit& u, int row) const {
     if constexpr (!kShared) return at(A, u, row);

@@ -716,8 +716,13 @@ __global__ void __launch_bounds__(kThreads) direct_int2_kernel(
 // reductions across the 32 tokens.  The results are those of make_meta and
 // qcode_fast, bit for bit.
 //
-// What bounds them: instruction issue (65K tokens of each width x 8 kv heads: INT4
-// pages 136 us, INT2 194; 106K and 156K tokens, rotated: 215 and 427).  Rows through
+// What bounds them: nothing alone.  65K tokens x 8 kv heads as they are: INT4 pages 97
+// us, INT2 171, issue active 72 and 70 % of the cycles; rotated 135 and 185, at 59 and
+// 70 %.  The first stalls are waits for memory (per issue 2.0 and 2.6, rotated 4.7 and
+// 2.6: job, token, position, table row and K row are loads that depend on one another
+// at the start of every CTA, and nothing of a next page is in flight), then the barrier
+// after the rotation (2.0).  In mixed calls, half and 0.6 of the tokens INT2: 65K of
+// each width 136 and 194 us; 106K and 156K, rotated, 215 and 427.  Rows through
 // registers and a step per value took 145 and 277, rotated 222 and 670; rows fetched
 // by the lane that reads them, half sectors, 155 and 210.  A page's heads side by
 // side in the grid change nothing.  The loops over the 8-channel pieces are kept

@@ -106,9 +106,11 @@ __device__ __noinline__ Eight other_values(const uint8_t* b, int cls, bool is_k,
 // of 8 channels of a slot at a time, 16 lanes a row, so an INT2 page's scales, which go by channel, stay in
 // registers over the page.  V, whose codes lie by channel: 8 channels x 8 slots at a time, a code word per
 // channel, which give 8 rows 16 bytes each (8 lanes: 128 bytes of a row).
-// Bound by the rows written, 3.9 to 5.8 bytes for each one read: 8 requests, 20K to
-// 32K tokens, 8 kv heads (1.0 GB) in 174 us, 0.90 of the copy rate.  With a
-// conversion per code and no values by pairs it was bound by issue: 291 us.
+// Bound by the rows written, 3.2 (INT4) to 5.3 (INT2) bytes of bf16 for each one read:
+// 8 requests, 20K to 32K tokens, 8 kv heads (1.0 GB) in 174 us, 0.90 of the copy rate.
+// With a conversion per code and no values by pairs it was bound by issue: 291 us.
+// INT3 and FP4 pages, code by code, take five times as long as INT2 pages (65K tokens x
+// 8 heads: 273 and 291 us against 58).
 template <bool kF32>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadArgs A,
                                                             const __grid_constant__ ReadRows by_value,
