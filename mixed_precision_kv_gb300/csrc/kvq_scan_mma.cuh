@@ -754,14 +754,12 @@ __global__ void __launch_bounds__(256) frag_kernel(const __nv_bfloat16* __restri
                                                    const GroupPool* __restrict__ gpools) {
   constexpr bool kPair = Cols<G>::kPair;
   __shared__ FragSmem S;
-  // Launched as a programmatic dependent of the last kernel before the decode
-  // (normally the append kernel, which signals after its own wait).  Nothing
-  // it reads is written by that kernel: q and the plan are in place before
-  // it, and the INT2 K scale maximum changes only in repacks, which finish
-  // before their dependents start.  It waits for that grid only before it
-  // exits, so the scan's wait (on this grid) covers the appends too.
+  // Launched as a programmatic dependent of the last kernel before the decode, which may be the caller's own that
+  // writes q, and may signal long before it has (matrix products of libraries do): only the plan is read before
+  // that grid is done.  The scan's wait (on this grid) covers everything before the decode.
   const Unit u = units[blockIdx.x];
   asm volatile("griddepcontrol.launch_dependents;");   // the scan may be staged
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   // a grouped decode: the unit's own pool bounds its INT2 K scales
   if (gpools) smax_bits = gpools[u.pad].smax;
@@ -844,7 +842,6 @@ __global__ void __launch_bounds__(256) frag_kernel(const __nv_bfloat16* __restri
   const uint4* src = reinterpret_cast<const uint4*>(&S.f);
   uint4* dst = reinterpret_cast<uint4*>(frags + blockIdx.x);
   for (int x = tid; x < (int)(sizeof(UnitFrag) / 16); x += 256) dst[x] = src[x];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---- persistent scan: warp gw = blockIdx.x * kWarps + w of the n_workers
