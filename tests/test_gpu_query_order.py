@@ -63,3 +63,58 @@ def test_projection_then_attention(kvq, call, batch, inner):
     for p in pools:
         p.sync()
         p.destroy()
+
+
+@pytest.mark.parametrize("batch,inner", [(16, 65536), (200, 16384)])
+@pytest.mark.parametrize("rotated", [False, True])
+def test_steps_without_a_wait(kvq, batch, inner, rotated):
+    """Projection, rotation, append, attention, output product, step after step on one stream with nothing waited for in
+    between: the bits of the same steps with a wait after every call.  Large batches append by the bulk kernels."""
+    hkv, hq, steps = 2, 8, 6
+    gen = torch.Generator("cuda").manual_seed(3)
+    W = rand((inner, (hq + 2 * hkv) * 128), gen, inner ** -0.5)
+    Wo = rand((hq * 128, inner), gen, (hq * 128) ** -0.5)
+    x0 = rand((batch, inner), gen)
+    rope = kvq.Rope(torch.randn(batch + steps, 128, generator=gen, device="cuda"))
+
+    def trip(wait):
+        pool = kvq.KVPool(hkv, 400, 400, 4, 300)
+        ids = [pool.open() for _ in range(4)]
+        req = np.repeat(ids, batch // 4)
+        x, outs = x0.clone(), []
+        settle = torch.cuda.synchronize if wait else (lambda: None)
+        for i in range(steps):
+            qkv = torch.matmul(x, W).view(batch, hq + 2 * hkv, 128)
+            settle()
+            pos = torch.arange(batch, dtype=torch.int32, device="cuda") + i
+            q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+            bits = np.where(np.arange(batch) % 7 < 3, 4, 2) if i % 2 else np.full(batch, 2)
+            if rotated:
+                pool.append_rotated(k, v, req, bits, rope, pos)
+                settle()
+                q = pool.rotate(q, rope, pos)
+            else:
+                k, v, q = k.contiguous(), v.contiguous(), q.contiguous()
+                pool.append(k, v, req, bits)
+            settle()
+            n = [batch // 4] * 4
+            if i % 3 == 2:
+                a = pool.attend_shared(q, ids, [-1, ids[0], ids[0], ids[1]], n, SCALE)
+            else:
+                a = pool.attend(q, ids, n, SCALE)
+            settle()
+            d = pool.decode(q[:4].contiguous(), ids, SCALE)
+            settle()
+            y = a.reshape(batch, hq * 128)
+            y[:4] += d.reshape(4, hq * 128).bfloat16()
+            x = torch.matmul(y, Wo)
+            settle()
+            outs += [a, d, x]
+        outs += list(pool.read(ids))
+        pool.sync()
+        pool.destroy()
+        return outs
+
+    want = trip(True)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(trip(False), want))
