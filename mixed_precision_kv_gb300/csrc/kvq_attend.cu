@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(32 * kMergeRows) attend_join_kernel(AttArgs A,
                                                                       const Unit* __restrict__ scan_units,
                                                                       const float* __restrict__ scan_part) {
   const AttJoin J = joins[blockIdx.y];
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // (the plans were there before the kernels that this one follows)
+  wait_for_grid(part, scan_part);   // (the plans were there before the kernels that this one follows)
   const int lane = threadIdx.x & 31, c = lane >> 1;
   const int i0 = 2 * (blockIdx.x * kMergeRows + (int)(threadIdx.x >> 5));
   if (i0 >= J.rows) return;

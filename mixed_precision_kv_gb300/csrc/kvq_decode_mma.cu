@@ -8,7 +8,7 @@ namespace {
 template <int G>
 cudaError_t launch_mma_g(kv_pool* P, const void* q, int32_t hq, float scale_log2, const Unit* d_units, int n_units,
                          const Split* d_splits, const int32_t* d_wsplit, int n_workers, void* d_frags, float* d_part,
-                         cudaStream_t s, const GroupPool* d_gpools, bool groups_extra) {
+                         cudaStream_t s, const GroupPool* d_gpools, bool groups_extra, bool in_place) {
   // function attributes are set once per device (bit = device ordinal)
   static std::atomic<uint64_t> attr_set{0};
   int dev = 0;
@@ -26,7 +26,7 @@ cudaError_t launch_mma_g(kv_pool* P, const void* q, int32_t hq, float scale_log2
   if (n_workers <= 0 || n_units <= 0) return cudaSuccess;
   const uint32_t* smax = P->d_status + 1;
   P->launches += 2;
-  cudaError_t e = launch_pdl(frag_kernel<G>, dim3((unsigned)n_units), dim3(256), 0, s, (const __nv_bfloat16*)q,
+  cudaError_t e = launch_pdl(in_place ? frag_kernel<G, true> : frag_kernel<G, false>, dim3((unsigned)n_units), dim3(256), 0, s, (const __nv_bfloat16*)q,
                              (int)hq, scale_log2, d_units, smax, (UnitFrag*)d_frags, d_gpools);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)((n_workers + kWarps - 1) / kWarps);
@@ -64,11 +64,11 @@ size_t decode_mma_frag_bytes() { return sizeof(UnitFrag); }
 
 static cudaError_t launch_scan(kv_pool* P, int g, const void* q, int32_t hq, float scale_log2, const Unit* d_units, int n_units,
                                const Split* d_splits, const int32_t* d_wsplit, int n_workers, void* d_frags, float* d_part,
-                               cudaStream_t s, const GroupPool* d_gpools, bool groups_extra) {
+                               cudaStream_t s, const GroupPool* d_gpools, bool groups_extra, bool in_place) {
 #define KVQ_MMA_CASE(gg)                                                                                              \
   case gg:                                                                                                            \
     return launch_mma_g<gg>(P, q, hq, scale_log2, d_units, n_units, d_splits, d_wsplit, n_workers, d_frags, d_part, s, \
-                            d_gpools, groups_extra);
+                            d_gpools, groups_extra, in_place);
   switch (g) {
     KVQ_MMA_CASE(1)
     KVQ_MMA_CASE(2)
@@ -87,7 +87,7 @@ cudaError_t launch_scan_mma(kv_pool* P, const void* q, int32_t hq, float scale_l
                             const Split* d_splits, const int32_t* d_wsplit, int n_workers, void* d_frags, float* d_part,
                             cudaStream_t s) {
   return launch_scan(P, hq / P->cfg.num_kv_heads, q, hq, scale_log2, d_units, n_units, d_splits, d_wsplit, n_workers, d_frags,
-                     d_part, s, nullptr, false);
+                     d_part, s, nullptr, false, true);
 }
 
 cudaError_t launch_decode_mma(kv_pool* P, const void* q, int32_t hq, float scale_log2, const Unit* d_units, int n_units,
@@ -96,7 +96,7 @@ cudaError_t launch_decode_mma(kv_pool* P, const void* q, int32_t hq, float scale
                               int32_t total_kv_heads, bool groups_extra) {
   const int g = hq / (total_kv_heads > 0 ? total_kv_heads : P->cfg.num_kv_heads);
   cudaError_t e = launch_scan(P, g, q, hq, scale_log2, d_units, n_units, d_splits, d_wsplit, n_workers, d_frags, d_part, s,
-                              d_gpools, groups_extra);
+                              d_gpools, groups_extra, false);
   if (e != cudaSuccess) return e;
   if ((e = launch_fp_pending(P, q, hq, scale_log2, d_units, d_part, s)) != cudaSuccess) return e;
   if (P->merge_event && (e = cudaEventRecord(P->merge_event, s)) != cudaSuccess) return e;

@@ -104,7 +104,7 @@ cudaError_t launch_scored_g(kv_pool* P, const void* q, int32_t hq, float scale_l
   if (n_workers <= 0 || n_units <= 0) return cudaSuccess;
   const uint32_t* smax = P->d_status + 1;
   P->launches += 2;
-  cudaError_t e = launch_pdl(frag_kernel<G>, dim3((unsigned)n_units), dim3(256), 0, s, (const __nv_bfloat16*)q,
+  cudaError_t e = launch_pdl(frag_kernel<G, false>, dim3((unsigned)n_units), dim3(256), 0, s, (const __nv_bfloat16*)q,
                              (int)hq, scale_log2, d_units, smax, (UnitFrag*)d_frags, (const GroupPool*)nullptr);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)((n_workers + kWarps - 1) / kWarps);

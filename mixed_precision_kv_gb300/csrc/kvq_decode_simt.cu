@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kThreads) decode_simt_kernel(
     const Unit* __restrict__ units, const Split* __restrict__ splits, const int32_t* __restrict__ cta_split,
     const int32_t* __restrict__ ntab, const uint32_t* __restrict__ hdead, float* __restrict__ part, size_t int3_off,
     int64_t n3b, size_t fp4_off, int64_t nfb) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the appends before this decode are done
+  wait_for_grid(q, table, ntab);   // the appends before this decode are done
   asm volatile("griddepcontrol.launch_dependents;");   // the merge may be scheduled as CTAs retire
   __shared__ float qs[G][kHeadDim];
   __shared__ __align__(16) uint8_t buf[kWarps][kInt4Block];
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const Unit* __restrict__ uni
   const Unit u = units[ui];   // the plan is copied in before the launch (not by a kernel): read it first
   // Launched as a programmatic dependent of the scan: wait until the scan grid
   // has completed and its partials are visible (immediate for a plain launch).
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_grid(part);
   asm volatile("griddepcontrol.launch_dependents;");   // the next call's kernels may be staged
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   const size_t rs = (size_t)G * kPartStride;          // stride between splits

@@ -410,7 +410,23 @@ namespace kvq {
 // Launch with programmatic stream serialization: the grid may be staged while
 // the previous kernel of the stream drains.  Every kernel launched this way
 // executes griddepcontrol.wait before it touches memory that earlier work in
-// the stream reads or writes.
+// the stream reads or writes (wait_for_grid).
+#ifdef __CUDACC__
+// p as the compiler knows nothing about: a load through a `const __restrict__` argument, which nothing is taken to
+// write, may be moved across a wait (it was, across one under a condition), one through p stays behind this.
+template <typename Ptr>
+__device__ __forceinline__ void fresh(Ptr& p) {
+  size_t a = __cvta_generic_to_global(p);
+  asm volatile("" : "+l"(a) : : "memory");
+  p = (Ptr)__cvta_global_to_generic(a);
+}
+// Waits for the grid before this one on the stream; what it may have written is then read through p.
+template <typename... Ptr>
+__device__ __forceinline__ void wait_for_grid(Ptr&... p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  (fresh(p), ...);
+}
+#endif
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                        Args&&... args) {
@@ -493,7 +509,8 @@ cudaError_t launch_decode_mma(kv_pool* P, const void* q, int32_t hq, float scale
                               float* d_part, float* out, cudaStream_t s, const GroupPool* d_gpools = nullptr,
                               int32_t total_kv_heads = 0, bool groups_extra = false);
 int decode_mma_workers_per_sm(int g);
-// The scan alone: partials [split][g][kHeadDim + 4], O, then the maximum (base 2) and the sum.
+// The scan alone: partials [split][g][kHeadDim + 4], O, then the maximum (base 2) and the sum.  After a copy or a
+// kernel of the library that started once q was written (its operands are prepared beside that kernel).
 cudaError_t launch_scan_mma(kv_pool* P, const void* q, int32_t hq, float scale_log2, const Unit* d_units, int n_units,
                             const Split* d_splits, const int32_t* d_wsplit, int n_workers, void* d_frags, float* d_part,
                             cudaStream_t s);

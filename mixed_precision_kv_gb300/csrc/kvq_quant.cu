@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) append_int4_kernel(
     const __grid_constant__ RopeParam<kRope> rope) {
   __shared__ __align__(16) uint8_t img[kInt4Block];
   __shared__ __align__(16) uint8_t vcodes[kPage * kHeadDim];   // V codes of a new page, packed after
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // earlier work on the stream (the previous decode) is done
+  wait_for_grid(k, v);   // earlier work on the stream (the previous decode) is done
   asm volatile("griddepcontrol.launch_dependents;");
   const AppendJob job = kByValue ? small.jobs[blockIdx.x] : jobs[blockIdx.x];
   const int32_t* tk = kByValue ? small.toks : toks;

@@ -746,7 +746,7 @@ __device__ __forceinline__ uint32_t frag_q3(const FragSmem& S, int L, int x) {
 // It computes what the scan needs on the q side of a unit: the per-head
 // power-of-two scales, the mma B fragments of both K formats, the INT2 K
 // zero-term pairs and the INT4 K zero-term fragments.
-template <int G>
+template <int G, bool kInPlace>
 __global__ void __launch_bounds__(256) frag_kernel(const __nv_bfloat16* __restrict__ q, int hq, float scale_log2,
                                                    const Unit* __restrict__ units,
                                                    const uint32_t* __restrict__ smax_bits,
@@ -756,10 +756,11 @@ __global__ void __launch_bounds__(256) frag_kernel(const __nv_bfloat16* __restri
   __shared__ FragSmem S;
   // Launched as a programmatic dependent of the last kernel before the decode, which may be the caller's own that
   // writes q, and may signal long before it has (matrix products of libraries do): only the plan is read before
-  // that grid is done.  The scan's wait (on this grid) covers everything before the decode.
+  // that grid is done.  kInPlace: that grid is the library's and started after all that is read here was there;
+  // it is waited for before this one ends.  Either way the scan's wait (on this grid) covers everything before it.
   const Unit u = units[blockIdx.x];
   asm volatile("griddepcontrol.launch_dependents;");   // the scan may be staged
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if constexpr (!kInPlace) wait_for_grid(q, smax_bits, gpools);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
   // a grouped decode: the unit's own pool bounds its INT2 K scales
   if (gpools) smax_bits = gpools[u.pad].smax;
@@ -842,6 +843,7 @@ __global__ void __launch_bounds__(256) frag_kernel(const __nv_bfloat16* __restri
   const uint4* src = reinterpret_cast<const uint4*>(&S.f);
   uint4* dst = reinterpret_cast<uint4*>(frags + blockIdx.x);
   for (int x = tid; x < (int)(sizeof(UnitFrag) / 16); x += 256) dst[x] = src[x];
+  if constexpr (kInPlace) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---- persistent scan: warp gw = blockIdx.x * kWarps + w of the n_workers
@@ -875,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_mma_kernel(
   const int gw = blockIdx.x * kWarps + w;
   // the plan is copied in before the launch (not by a kernel): read it first
   const int s_begin = gw < n_workers ? wsplit[gw] : 0, s_end = gw < n_workers ? wsplit[gw + 1] : 0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // fragments, and the appends before them, are done
+  wait_for_grid(smax_bits);   // fragments, and the appends before them, are done
   asm volatile("griddepcontrol.launch_dependents;");   // the merge may be staged
   if (s_begin >= s_end) return;   // no CTA-wide barrier below: idle warps may leave
   // P is carried as p * 2^sv in the fp16 folds so that p * scale stays clear

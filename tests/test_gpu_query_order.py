@@ -20,7 +20,7 @@ def kvq():
 
 
 @pytest.mark.parametrize("batch,inner", [(16, 65536), (256, 16384), (16, 4096)])
-@pytest.mark.parametrize("call", ["decode", "simt", "noalloc", "scored", "groups", "attend", "attend_shared"])
+@pytest.mark.parametrize("call", ["decode", "simt", "noalloc", "scored", "groups", "attend", "attend_shared", "prefix"])
 def test_projection_then_attention(kvq, call, batch, inner):
     hkv, hq, n, steps = 8, 32, 96, 12
     gen = torch.Generator("cuda").manual_seed(inner)
@@ -44,6 +44,8 @@ def test_projection_then_attention(kvq, call, batch, inner):
             return kvq.KVPool.decode_groups(pools, q, ids, SCALE)
         if call == "attend":
             return pool.attend(q, ids[0], [1] * batch, SCALE)
+        if call == "prefix":
+            return pool.attend_shared(q, ids[0], [-1] + ids[0][:1] * (batch - 1), [1] * batch, SCALE)
         return pool.attend_shared(q, ids[0], [-1] * batch, [1] * batch, SCALE)
 
     W = rand((inner, hq * 128), gen, inner ** -0.5)
